@@ -270,7 +270,8 @@ def _evict(s):
     out[:, :kept * g] = s["scores"][:, :tq].reshape(-1, nb, g).gather(1, at[..., None].expand(-1, -1, g)).flatten(1)
     out[:, kept * g:kept * g + nres] = s["scores"][:, tq:tq + nres]
     out[:, kept * g + nres:tq + nres] = 0.0
-    s["first_out"].copy_((s["first"].long()[:, None] - at * g).clamp(0, g).sum(1))
+    pad = s["first"].long()
+    s["first_out"].copy_((pad[:, None] - at * g).clamp(0, g).sum(1) + (pad - tq).clamp_min(0))
     return [keep, s["first_out"], out] + [s["dst"][k] for k in _STORE if s[k] is not None]
 
 
@@ -420,7 +421,7 @@ def _exact_evict(s):
         best = sorted(range(nb - recent), key=lambda i: (-sums[i], i))[:kept - recent]
         ids = sorted(best + list(range(nb - recent, nb)))
         keep[o] = torch.tensor(ids, dtype=torch.int32)
-        first[o] = sum(min(max(_first(c)[o] - i * g, 0), g) for i in ids)
+        first[o] = sum(min(max(_first(c)[o] - i * g, 0), g) for i in ids) + max(_first(c)[o] - c["tq"], 0)
         rows = torch.tensor([i * g + x for i in ids for x in range(g)])
         new[o, :kept * g] = sc[o, rows]
         new[o, kept * g:kept * g + c["nres"]] = sc[o, c["tq"]:c["tq"] + c["nres"]]
