@@ -1,4 +1,4 @@
-"""ctypes binding of libkvq.so (include/kvq.h).
+"""ctypes binding of libkvq.so (include/kvq.h, include/kvq_cache.h).
 
 Argument marshalling only: every step of the path runs in the library's CUDA
 kernels.  The functions named like the C entry points take device pointers
@@ -39,6 +39,12 @@ class kvq_err(ctypes.Structure):
     _fields_ = [("rmse", ctypes.c_double), ("max_abs", ctypes.c_double), ("mean_abs", ctypes.c_double)]
 
 
+class kvq_cache(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k_codes", "k_scale", "k_zero", "k_resid", "v_codes", "v_scale",
+                                               "v_zero", "v_resid")] + [
+        ("tq", ctypes.c_int64), ("nres", ctypes.c_int64), ("resid_rows", ctypes.c_int64), ("first", ctypes.c_void_p)]
+
+
 class KvqError(RuntimeError):
     def __init__(self, status: int, message: str):
         super().__init__(f"kvq status {status}: {message}")
@@ -52,6 +58,7 @@ def _load() -> ctypes.CDLL:
     lib = ctypes.CDLL(path)
     vp, i64, sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t
     S, P = ctypes.POINTER(kvq_shape), ctypes.POINTER(kvq_qparams)
+    K = ctypes.POINTER(kvq_cache)
     psz = ctypes.POINTER(ctypes.c_size_t)
     i32 = ctypes.c_int
     sig = {
@@ -81,6 +88,12 @@ def _load() -> ctypes.CDLL:
         "kvq_append_kv_workspace": [S, i32, P, P, i64, psz],
         "kvq_append_kv": [vp, vp, i64, i32, S, P, P, i64, vp, vp, vp, vp, vp, vp, vp, vp, ctypes.POINTER(i64),
                           ctypes.POINTER(i64), vp, sz, vp],
+        "kvq_attend_chunk_workspace": [S, i64, i64, i64, psz],
+        "kvq_attend_chunk": [vp, i64, i64, i64, K, P, P, S, vp, vp, vp, sz, vp],
+        "kvq_attend_weights_workspace": [S, i64, i64, i64, psz],
+        "kvq_attend_weights": [vp, vp, i64, i64, i64, K, P, S, vp, vp, i64, vp, sz, vp],
+        "kvq_evict_blocks_workspace": [S, i64, psz],
+        "kvq_evict_blocks": [K, K, P, P, S, i64, i64, i64, vp, vp, i64, vp, vp, sz, vp],
     }
     for name, args in sig.items():
         f = getattr(lib, name)
@@ -103,6 +116,10 @@ EXPORTS = ("kvq_quantized_sizes", "kvq_quantize", "kvq_dequantize", "kvq_error_s
            "kvq_rotate_quantize", "kvq_dequantize_rotate", "kvq_append_kv_workspace", "kvq_append_kv",
            "kvq_append_workspace", "kvq_append", "kvq_mixed_sizes", "kvq_mixed_quantize", "kvq_mixed_dequantize",
            "kvq_wait_timeouts")
+
+# every symbol include/kvq_cache.h declares
+CACHE_EXPORTS = ("kvq_attend_chunk_workspace", "kvq_attend_chunk", "kvq_attend_weights_workspace",
+                 "kvq_attend_weights", "kvq_evict_blocks_workspace", "kvq_evict_blocks")
 
 # size of the library's fixed scratch array behind kvq_error_stats_noalloc
 NOALLOC_SCRATCH_BYTES = 1 << 20
@@ -369,6 +386,50 @@ def kvq_mixed_dequantize(stream_buf, off, tags2, shape, out, stream=None):
                                     _stream(stream)))
 
 
+def kvq_attend_chunk_workspace(shape, resid_rows: int, n: int, group: int) -> int:
+    s, out = _shape(shape), ctypes.c_size_t()
+    _check(LIB.kvq_attend_chunk_workspace(ctypes.byref(s), int(resid_rows), int(n), int(group), ctypes.byref(out)))
+    return out.value
+
+
+def kvq_attend_chunk(q, n, group, kv_heads, cache: kvq_cache, kqp: QParams, vqp: QParams, shape, out, lse, workspace,
+                     workspace_B, stream=None):
+    s, pk, pv = _shape(shape), kqp.c(), vqp.c()
+    _check(LIB.kvq_attend_chunk(_ptr(q), int(n), int(group), int(kv_heads), ctypes.byref(cache), ctypes.byref(pk),
+                                ctypes.byref(pv), ctypes.byref(s), _ptr(out), _ptr(lse), _ptr(workspace),
+                                int(workspace_B), _stream(stream)))
+
+
+def kvq_attend_weights_workspace(shape, resid_rows: int, n: int, group: int) -> int:
+    s, out = _shape(shape), ctypes.c_size_t()
+    _check(LIB.kvq_attend_weights_workspace(ctypes.byref(s), int(resid_rows), int(n), int(group), ctypes.byref(out)))
+    return out.value
+
+
+def kvq_attend_weights(q, lse, n, group, kv_heads, cache: kvq_cache, kqp: QParams, shape, scores_in, scores_out,
+                       score_stride, workspace, workspace_B, stream=None):
+    s, pk = _shape(shape), kqp.c()
+    _check(LIB.kvq_attend_weights(_ptr(q), _ptr(lse), int(n), int(group), int(kv_heads), ctypes.byref(cache),
+                                  ctypes.byref(pk), ctypes.byref(s), _ptr(scores_in), _ptr(scores_out),
+                                  int(score_stride), _ptr(workspace), int(workspace_B), _stream(stream)))
+
+
+def kvq_evict_blocks_workspace(shape, block: int) -> int:
+    s, out = _shape(shape), ctypes.c_size_t()
+    _check(LIB.kvq_evict_blocks_workspace(ctypes.byref(s), int(block), ctypes.byref(out)))
+    return out.value
+
+
+def kvq_evict_blocks(src: kvq_cache, dst: kvq_cache, kqp: QParams, vqp: QParams, shape, block, budget, window,
+                     scores_in, scores_out, score_stride, keep, workspace, workspace_B, stream=None):
+    """dst.tq and dst.nres are updated."""
+    s, pk, pv = _shape(shape), kqp.c(), vqp.c()
+    _check(LIB.kvq_evict_blocks(ctypes.byref(src), ctypes.byref(dst), ctypes.byref(pk), ctypes.byref(pv),
+                                ctypes.byref(s), int(block), int(budget), int(window), _ptr(scores_in),
+                                _ptr(scores_out), int(score_stride), _ptr(keep), _ptr(workspace), int(workspace_B),
+                                _stream(stream)))
+
+
 def kvq_last_error() -> str:
     return LIB.kvq_last_error().decode(errors="replace")
 
@@ -537,3 +598,145 @@ def rotate(x, signs, inverse=False, out=None, out_dtype=None, stream=None):
     kvq_rotate(x, torch_dtype_code(x), shape, signs, inverse, out, od, stream)
     return out
 
+
+
+# ---- the streaming cache (torch tensors; calls run on the tensors' device) -----
+
+@dataclass
+class KVCache:
+    """One layer's streaming K and V caches: what kvq_append_kv fills, or what
+    one quantize() call per cache wrote (from_quantized).
+
+    k, v: (codes, scale, zero, resid) of each cache; shape: the stores'
+    (outer, T_cap, C), outer = batch * kv_heads; tq, nres: filled tokens of the
+    store and of the bf16 buffer of resid_rows rows; first: CUDA int32 [outer]
+    left padding, or None."""
+    k: tuple
+    v: tuple
+    shape: tuple
+    kqp: QParams
+    vqp: QParams
+    tq: int
+    nres: int
+    resid_rows: int
+    kv_heads: int = 1
+    first: "object" = None
+
+    @staticmethod
+    def from_quantized(qk: Quantized, qv: Quantized, kv_heads: int = 1, first=None) -> "KVCache":
+        outer, T, C = qk.shape
+        R = min(qk.qp.residual, T)
+        if tuple(qv.shape) != tuple(qk.shape) or min(qv.qp.residual, T) != R:
+            raise ValueError("the key and the value cache need the same shape and residual window")
+        return KVCache((qk.codes, qk.scale, qk.zero, qk.resid), (qv.codes, qv.scale, qv.zero, qv.resid),
+                       (outer, T - R, C), qk.qp, qv.qp, T - R, R, R, kv_heads, first)
+
+    @property
+    def T(self) -> int:
+        return self.tq + self.nres
+
+    def c(self) -> kvq_cache:
+        if self.first is not None and (str(self.first.dtype) != "torch.int32" or self.first.numel() != self.shape[0]):
+            raise ValueError("first must be int32 [outer]")
+        return kvq_cache(*[_ptr(x) for x in self.k], *[_ptr(x) for x in self.v], self.tq, self.nres, self.resid_rows,
+                         _ptr(self.first))
+
+
+def _on(t, stream):
+    """The context of a call on t's device: the current stream there, or the
+    given one (temporaries are then allocated on that stream)."""
+    import torch
+    if stream is None:
+        return torch.cuda.device(t.device)
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=t.device)
+    return torch.cuda.stream(stream)
+
+
+def _want(t, name, dtype, shape, device):
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous() or t.device != device:
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device} "
+                         f"(got {t.dtype} {tuple(t.shape)} on {t.device})")
+
+
+def _heads(q, cache: KVCache):
+    """(n, group) of q [batch, n, kv_heads * group, C] over the cache."""
+    import torch
+    outer, _, C = cache.shape
+    if q.dim() != 4 or cache.kv_heads < 1 or outer % cache.kv_heads or q.shape[2] % cache.kv_heads:
+        raise ValueError("q must be [batch, n, kv_heads * group, C] with batch * kv_heads = outer")
+    _want(q, "q", torch.bfloat16, (outer // cache.kv_heads, q.shape[1], q.shape[2], C), q.device)
+    return q.shape[1], q.shape[2] // cache.kv_heads
+
+
+def attend_chunk(q, cache: KVCache, out=None, lse=None, workspace=None, stream=None):
+    """q: CUDA bf16 [batch, n, kv_heads * group, C], the queries of the cache's
+    n newest tokens -> (out bf16 like q, lse float32 [batch, n, heads]): causal
+    attention over the streaming cache."""
+    import torch
+    n, group = _heads(q, cache)
+    if out is not None:
+        _want(out, "out", torch.bfloat16, q.shape, q.device)
+    if lse is not None:
+        _want(lse, "lse", torch.float32, q.shape[:3], q.device)
+    with _on(q, stream):
+        out = torch.empty_like(q) if out is None else out
+        lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device) if lse is None else lse
+        if workspace is None:
+            workspace = _empty(kvq_attend_chunk_workspace(cache.shape, cache.resid_rows, n, group), q.device)
+        kvq_attend_chunk(q, n, group, cache.kv_heads, cache.c(), cache.kqp, cache.vqp, cache.shape, out, lse,
+                         workspace, workspace.numel() * workspace.element_size())
+    return out, lse
+
+
+def attend_weights(q, lse, cache: KVCache, scores=None, out=None, workspace=None, stream=None):
+    """The attention weight that the queries of attend_chunk give every token of
+    the cache: scores (CUDA float32 [outer, S >= T], or None for zeros) plus the
+    weights, into out (scores itself to accumulate in place; a new tensor by
+    default, whose columns from T on are not written)."""
+    import torch
+    n, group = _heads(q, cache)
+    _want(lse, "lse", torch.float32, q.shape[:3], q.device)
+    outer = cache.shape[0]
+    for t, name in ((scores, "scores"), (out, "out")):
+        if t is not None:
+            _want(t, name, torch.float32, (outer, t.shape[-1]), q.device)
+    if scores is not None and out is not None and scores.shape != out.shape:
+        raise ValueError("scores and out must have the same shape")
+    with _on(q, stream):
+        if out is None:
+            out = torch.empty_like(scores) if scores is not None else torch.empty(
+                (outer, cache.T), dtype=torch.float32, device=q.device)
+        if workspace is None:
+            workspace = _empty(kvq_attend_weights_workspace(cache.shape, cache.resid_rows, n, group), q.device)
+        kvq_attend_weights(q, lse, n, group, cache.kv_heads, cache.c(), cache.kqp, cache.shape, scores, out,
+                           out.shape[1], workspace, workspace.numel() * workspace.element_size())
+    return out
+
+
+def evict_blocks(cache: KVCache, scores, budget: int, window: int, block: int, dst: Optional[KVCache] = None,
+                 scores_out=None, keep=None, workspace=None, stream=None):
+    """Keep `budget` blocks of `block` store tokens (the newest `window` and the
+    best scored others) -> (dst, scores_out, keep int32 [outer, kept]).  By
+    default the cache, its first and scores (CUDA float32 [outer, S >= T]) are
+    compacted in place; dst.tq and dst.nres are updated."""
+    import torch
+    dst = cache if dst is None else dst
+    scores_out = scores if scores_out is None else scores_out
+    outer = cache.shape[0]
+    _want(scores, "scores", torch.float32, (outer, scores.shape[-1]), scores.device)
+    _want(scores_out, "scores_out", torch.float32, scores.shape, scores.device)
+    if tuple(dst.shape) != tuple(cache.shape):
+        raise ValueError("dst must have the cache's shape")
+    kept = max(0, min(int(budget), cache.tq // max(int(block), 1)))
+    if keep is not None:
+        _want(keep, "keep", torch.int32, (outer, kept), scores.device)
+    with _on(scores, stream):
+        keep = torch.empty((outer, kept), dtype=torch.int32, device=scores.device) if keep is None else keep
+        if workspace is None:
+            workspace = _empty(kvq_evict_blocks_workspace(cache.shape, block), scores.device)
+        dst_c = dst.c()
+        kvq_evict_blocks(cache.c(), dst_c, cache.kqp, cache.vqp, cache.shape, block, budget, window, scores,
+                         scores_out, scores.shape[1], keep, workspace, workspace.numel() * workspace.element_size())
+    dst.tq, dst.nres = dst_c.tq, dst_c.nres
+    return dst, scores_out, keep

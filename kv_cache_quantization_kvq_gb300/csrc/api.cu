@@ -175,6 +175,11 @@ void set_last_error(const char* fmt, ...)
     g_last_error = buf;
 }
 
+kvq_status validate_format(const kvq_shape* shape, int x_dtype, const kvq_qparams* p, QSpec& q)
+{
+    return make_spec(shape, x_dtype, p, q);
+}
+
 int sm_count()
 {
     static std::atomic<int> cache[128];

@@ -1,0 +1,267 @@
+// evict.cu -- eviction from the streaming cache by accumulated score, in whole
+// blocks (kvq_evict_blocks).
+//
+// "KV Compression 公式到源码对照" §3.2: keep = TopK(score, B - W) union the recent
+// window; "KV cache 压缩：把历史装得更小" §"少存 token：合并，或淘汰": the dropped
+// entries' K and V are freed.
+//
+// select_blocks_kernel, a CTA per slice: block scores in binary64, an
+// order-preserving 64-bit key each, a radix search for the key of the last kept
+// block (8 bits a pass, until the remaining bin is taken whole), ties by index,
+// and an ordered scan that writes the ascending keep list; it also counts what
+// is left of the padding.
+//
+// move_blocks_kernel: kept block j goes to place j <= keep[j].  A thread owns
+// one piece (16 bytes where the alignment allows) at one place within the
+// block, of one buffer of one slice, and takes the kept blocks in ascending
+// order, a few loads ahead of their stores.  In place, a store to block j can
+// only hit a block that the same thread has loaded before (keep[j'] > j for
+// every later j'), and no other thread touches that piece: no barrier and no
+// second buffer are needed.
+#include <algorithm>
+
+#include "kvq_device.cuh"
+
+namespace kvq {
+
+namespace {
+
+constexpr int kSelThreads = 512;
+constexpr int kMoveThreads = 256;
+constexpr int kAhead = 8;                        // loads in flight per thread
+
+// ascending order of keys = ascending order of scores, NaN lowest, -0 = +0
+__device__ __forceinline__ unsigned long long key_of(double s) {
+    if (s != s) return 0ull;
+    const long long b = __double_as_longlong(s + 0.0);
+    return b < 0 ? ~(unsigned long long)b : (unsigned long long)b | 0x8000000000000000ull;
+}
+
+// exclusive prefix sum of one flag word per thread over the CTA; total in *sum
+__device__ __forceinline__ int cta_scan(int v, int* warp_sums, int* sum) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int x = v;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int y = __shfl_up_sync(0xFFFFFFFFu, x, d);
+        if (lane >= d) x += y;
+    }
+    if (lane == 31) warp_sums[warp] = x;
+    __syncthreads();
+    int before = 0, total = 0;
+#pragma unroll
+    for (int w = 0; w < kSelThreads / 32; ++w) {
+        const int s = warp_sums[w];
+        before += w < warp ? s : 0;
+        total += s;
+    }
+    __syncthreads();
+    *sum = total;
+    return before + x - v;
+}
+
+__global__ void __launch_bounds__(kSelThreads)
+select_blocks_kernel(const EvictArgs A)
+{
+    __shared__ int hist[256];
+    __shared__ int warp_sums[kSelThreads / 32];
+    __shared__ int s_digit, s_need, s_done;
+    __shared__ unsigned long long s_first;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int64_t o = blockIdx.x;
+    const int nb = (int)A.nb, kept = (int)A.kept;
+    const int recent = (int)min(A.window, A.nb);
+    const int cand = nb - recent;                // candidates [0, cand)
+    int need = kept - recent;                    // to be taken of them (kept >= recent)
+    unsigned long long* key = reinterpret_cast<unsigned long long*>(A.ws) + o * A.nb;
+    int32_t* keep = A.keep + o * kept;
+
+    unsigned long long prefix = 0;
+    int shift = 64;                              // key bits below `shift` are still open
+    if (need > 0 && need < cand) {
+        // ---- block scores: a warp per block, lanes' partial sums joined in lane order
+        for (int b = warp; b < cand; b += kSelThreads / 32) {
+            const float* p = A.scores_in + o * A.stride + (int64_t)b * A.block;
+            double s = 0.0;
+            for (int64_t t = lane; t < A.block; t += 32) s += (double)p[t];
+#pragma unroll
+            for (int x = 1; x < 32; x <<= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, x);
+            if (lane == 0) key[b] = key_of(s);
+        }
+        // ---- radix search, most significant digit first
+        for (bool done = false; !done && shift > 0;) {
+            for (int i = tid; i < 256; i += kSelThreads) hist[i] = 0;
+            __syncthreads();
+            const int lo = shift - 8;
+            for (int b = tid; b < cand; b += kSelThreads) {
+                const unsigned long long k = key[b];
+                if (shift == 64 || (k >> shift) == (prefix >> shift)) atomicAdd(&hist[(int)(k >> lo) & 255], 1);
+            }
+            __syncthreads();
+            if (tid < 32) {                      // the digit where the count from above reaches need
+                int c[8], sum = 0;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) { c[i] = hist[255 - (8 * tid + i)]; sum += c[i]; }
+                int x = sum;
+#pragma unroll
+                for (int d = 1; d < 32; d <<= 1) {
+                    const int y = __shfl_up_sync(0xFFFFFFFFu, x, d);
+                    if (lane >= d) x += y;
+                }
+                int above = x - sum;
+                if (above < need && need <= x) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        if (above < need && need <= above + c[i]) {
+                            s_digit = 255 - (8 * tid + i);
+                            s_need = need - above;
+                            s_done = c[i] == need - above;
+                        }
+                        above += c[i];
+                    }
+                }
+            }
+            __syncthreads();
+            prefix |= (unsigned long long)s_digit << lo;
+            need = s_need;
+            done = s_done;
+            shift = lo;
+            __syncthreads();
+        }
+    }
+    // a candidate stays if its open key is above the prefix, or equal to it and
+    // among the first `need` of those (all of them when the search ended early)
+    const bool all = kept - recent >= cand, none = kept - recent <= 0;
+    int base = 0, ties = 0;
+    unsigned long long left = 0;                 // tokens of the padding that stay
+    const long long pad = A.first_in ? max(A.first_in[o], 0) : 0;
+    if (tid == 0) s_first = 0;
+    __syncthreads();
+    for (int b0 = 0; b0 < nb; b0 += kSelThreads) {
+        const int b = b0 + tid;
+        int above = 0, equal = 0;
+        if (b < nb) {
+            if (b >= cand || all) above = 1;
+            else if (!none) {
+                const unsigned long long k = key[b];
+                const unsigned long long kh = shift == 64 ? 0ull : k >> shift, ph = shift == 64 ? 0ull : prefix >> shift;
+                above = kh > ph;
+                equal = kh == ph;
+            }
+        }
+        int total;
+        const int tie_rank = cta_scan(equal, warp_sums, &total);
+        const int flag = above || (equal && ties + tie_rank < need);
+        ties += total;
+        const int at = base + cta_scan(flag, warp_sums, &total);
+        base += total;
+        if (flag) {
+            keep[at] = b;
+            left += (unsigned long long)min(max(pad - (long long)b * A.block, 0ll), (long long)A.block);
+        }
+    }
+    if (A.first_out) {
+        if (left) atomicAdd(&s_first, left);     // integers: any order gives the same sum
+        __syncthreads();
+        // a padding that reaches past the store keeps its part of the buffer
+        const long long over = max(pad - (long long)nb * A.block, 0ll);
+        if (tid == 0) A.first_out[o] = (int32_t)((long long)s_first + over);
+    }
+}
+
+template <typename V>
+__device__ __forceinline__ void move_pieces(const char* src, char* dst, int64_t block_B, const int32_t* keep, int kept)
+{
+    const bool same = src == dst;
+    for (int j0 = 0; j0 < kept; j0 += kAhead) {
+        V x[kAhead];
+        int k[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const int j = j0 + i;
+            k[i] = j < kept ? keep[j] : -1;
+            if (k[i] >= 0 && !(same && k[i] == j)) x[i] = *reinterpret_cast<const V*>(src + k[i] * block_B);
+        }
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const int j = j0 + i;
+            if (k[i] >= 0 && !(same && k[i] == j)) *reinterpret_cast<V*>(dst + j * block_B) = x[i];
+        }
+    }
+}
+
+// threads of a slice: the pieces of every buffer's block, then one per score column of a block
+struct MovePlan {
+    int32_t first[kEvictBufs + 1];               // first thread of each buffer, and of the scores
+    int32_t width[kEvictBufs];                   // bytes of a piece
+    int32_t threads;                             // per slice
+};
+
+__global__ void __launch_bounds__(kMoveThreads)
+move_blocks_kernel(const EvictArgs A, const MovePlan P, int64_t total)
+{
+    const int64_t id = (int64_t)blockIdx.x * kMoveThreads + threadIdx.x;
+    if (id >= total) return;
+    const int64_t o = id / P.threads;
+    const int w = (int)(id - o * P.threads);
+    const int kept = (int)A.kept;
+    const int32_t* keep = A.keep + o * kept;
+    if (w >= P.first[kEvictBufs]) {
+        // scores: a column of the store's blocks, then of the buffered tokens, then zeros
+        const int64_t c = w - P.first[kEvictBufs];
+        const float* in = A.scores_in + o * A.stride;
+        float* out = A.scores_out + o * A.stride;
+        const int64_t tq = A.nb * A.block, tk = (int64_t)kept * A.block;
+        move_pieces<float>(reinterpret_cast<const char*>(in + c), reinterpret_cast<char*>(out + c), A.block * 4, keep, kept);
+        for (int64_t r = c; r < A.nres; r += A.block) out[tk + r] = in[tq + r];
+        // columns [tk + nres, tq + nres) that this thread owns: x = c (mod block)
+        const int64_t z0 = tk + A.nres;
+        for (int64_t x = z0 + ((c - z0) % A.block + A.block) % A.block; x < tq + A.nres; x += A.block) out[x] = 0.0f;
+        return;
+    }
+    int i = 0;
+#pragma unroll
+    for (int k = 1; k < kEvictBufs; ++k)
+        if (k < A.nbuf && w >= P.first[k]) i = k;
+    const EvictBuf& B = A.buf[i];
+    const int64_t at = o * B.slice_B + (int64_t)(w - P.first[i]) * P.width[i];
+    const char* src = B.src + at;
+    char* dst = B.dst + at;
+    switch (P.width[i]) {
+    case 16: move_pieces<uint4>(src, dst, B.block_B, keep, kept); break;
+    case 4: move_pieces<uint32_t>(src, dst, B.block_B, keep, kept); break;
+    case 2: move_pieces<uint16_t>(src, dst, B.block_B, keep, kept); break;
+    default: move_pieces<uint8_t>(src, dst, B.block_B, keep, kept); break;
+    }
+}
+
+}  // namespace
+
+size_t evict_workspace(int64_t outer, int64_t nb_max) { return (size_t)(outer * nb_max) * 8; }
+
+cudaError_t launch_evict(const EvictArgs& a, cudaStream_t st)
+{
+    if (a.outer == 0) return cudaSuccess;
+    select_blocks_kernel<<<(unsigned)a.outer, kSelThreads, 0, st>>>(a);
+    MovePlan P = {};
+    int64_t n = 0;
+    for (int i = 0; i < kEvictBufs; ++i) {
+        P.first[i] = (int32_t)n;
+        P.width[i] = 16;
+        if (i >= a.nbuf) continue;
+        const EvictBuf& b = a.buf[i];
+        const uint64_t bits = (uint64_t)(uintptr_t)b.src | (uint64_t)(uintptr_t)b.dst | (uint64_t)b.slice_B | (uint64_t)b.block_B;
+        P.width[i] = bits % 16 == 0 ? 16 : bits % 4 == 0 ? 4 : bits % 2 == 0 ? 2 : 1;
+        n += b.block_B / P.width[i];
+    }
+    P.first[kEvictBufs] = (int32_t)n;
+    n += a.block;
+    if (n > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+    P.threads = (int32_t)n;
+    const int64_t total = a.outer * n, grid = (total + kMoveThreads - 1) / kMoveThreads;
+    if (grid > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+    move_blocks_kernel<<<(unsigned)grid, kMoveThreads, 0, st>>>(a, P, total);
+    return cudaGetLastError();
+}
+
+}  // namespace kvq

@@ -142,6 +142,50 @@ cudaError_t launch_compact(const void* kv, size_t elem, int64_t heads, int64_t T
 cudaError_t launch_compact_pair(const void* k, const void* v, size_t elem, int64_t heads, int64_t T, int64_t D,
                                 const int32_t* keep, int64_t K, void* ok, void* ov, cudaStream_t st);
 
+// ---- the streaming cache (kvq_cache.h): attention, attention weights, eviction
+struct CacheArgs {
+    const void* q;                  // bf16 [outer / kv_heads][n][kv_heads * group][C]
+    const void *k_codes, *k_scale, *k_zero, *k_resid;
+    const void *v_codes, *v_scale, *v_zero, *v_resid;
+    const int32_t* first;           // [outer] or nullptr
+    int64_t outer, cap, C;          // the stores' [outer, cap, C]
+    int64_t tq, nres, rrows;        // filled store tokens, filled buffer rows, buffer rows
+    int64_t n, group, kv_heads;
+    int32_t bits, gk, gv;           // code bits; K group along T, V group along C
+    int32_t k_asym, v_asym;         // bf16 zero points present
+    int32_t k_signed, v_signed;     // two's complement codes
+};
+size_t chunk_workspace(int64_t outer, int64_t C, int64_t tmax, int64_t n, int64_t group);
+cudaError_t launch_attend_chunk(const CacheArgs& a, void* out, float* lse, void* ws, cudaStream_t st);
+size_t weights_workspace(int64_t outer, int64_t C, int64_t tmax, int64_t n, int64_t group);
+cudaError_t launch_attend_weights(const CacheArgs& a, const float* lse, const float* scores_in, float* scores_out,
+                                  int64_t stride, void* ws, cudaStream_t st);
+
+// One buffer of a store as eviction sees it: block b of slice o is the
+// `block_B` bytes at slice o * slice_B + b * block_B.
+struct EvictBuf {
+    const char* src;
+    char* dst;
+    int64_t slice_B, block_B;
+};
+constexpr int kEvictBufs = 6;
+struct EvictArgs {
+    EvictBuf buf[kEvictBufs];
+    int32_t nbuf;
+    int64_t outer, block, nb, kept, window, nres, stride;   // nb, kept, window in blocks
+    const float* scores_in;
+    float* scores_out;
+    const int32_t* first_in;
+    int32_t* first_out;
+    int32_t* keep;                  // [outer][kept]
+    void* ws;
+};
+size_t evict_workspace(int64_t outer, int64_t nb_max);
+cudaError_t launch_evict(const EvictArgs& a, cudaStream_t st);
+
+// make_spec of api.cu for the other API files: validates a format over a shape
+kvq_status validate_format(const kvq_shape* shape, int x_dtype, const kvq_qparams* p, QSpec& q);
+
 // number of SMs of the current device (cached per device)
 int sm_count();
 

@@ -1,0 +1,224 @@
+"""kvq_attend_chunk and kvq_attend_weights against the formulas in binary64.
+
+Both sides read the same quantized cache, whose rows are exactly those of
+kvq_dequantize, so only the attention's own arithmetic differs.  Tolerances
+(u = 2^-8, the largest relative error of a rounding to bf16; logit errors from
+stream_util.logit_error, e = twice that of the row: a probability is the
+exponential of a difference of two):
+  lse:     e + (T + 64) 2^-23 + 4 2^-23 (|lse| + 1)
+           (float32 sums of positive terms, at most one rounding a token and a
+           few a merge; the logarithm and its scaling);
+  out:     (u + e + (T + 64) 2^-23) sum_t p_t |v_t| + u |out|
+           (p rounded to bf16 for the value product, float32 sums, out rounded);
+  weights: (e + (rows + 64) 2^-23 + 8 2^-23 |lse|) sum w + 2^-23 |score|.
+"""
+import zlib
+
+import numpy as np
+import pytest
+
+import stream_util as S
+from gpu_util import Guarded, kb
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def b():
+    import torch
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    return kb()
+
+
+#   batch, kv_heads, group, n, C, tq, cap, nres, rows, formats, extras
+CASES = {
+    "one token alone": (1, 1, 1, 1, 128, 0, 64, 1, 64, {}, {}),
+    "buffer only": (2, 2, 4, 1, 128, 0, 0, 37, 64, {}, {}),
+    "store only, one block": (1, 2, 8, 1, 128, 64, 64, 0, 0, {}, {}),
+    "empty cache": (2, 1, 4, 3, 128, 0, 64, 0, 64, {}, {}),
+    "more queries than tokens": (1, 2, 3, 9, 64, 0, 64, 5, 64, {}, {}),
+    "ordinary step": (2, 2, 8, 1, 128, 960, 1024, 77, 192, {}, {}),
+    "step of 16 heads": (1, 2, 16, 1, 128, 512, 640, 130, 192, {}, {}),
+    "step of 64 heads": (1, 1, 64, 1, 64, 192, 192, 31, 64, {}, {}),
+    "ragged store end": (1, 2, 4, 2, 128, 333, 333, 19, 19, dict(gk=96), {}),
+    "two bits, symmetric": (1, 2, 4, 5, 128, 640, 704, 66, 192, dict(bits=2, kind="sym", gk=32, gv=128), {}),
+    "two bits, C 64": (1, 3, 5, 2, 64, 448, 448, 10, 64, dict(bits=2, gv=32), {}),
+    "symmetric, C 64": (2, 1, 7, 3, 64, 256, 320, 33, 64, dict(kind="sym", gk=128), {}),
+    "signed zero points": (1, 2, 4, 4, 128, 320, 320, 63, 64, dict(kind="signed", gk=32, gv=32), {}),
+    "far zero points": (1, 2, 4, 3, 128, 256, 256, 20, 64, {}, dict(shift=100.0)),
+    "far zero points, two bits": (1, 1, 2, 1, 64, 256, 256, 0, 64, dict(bits=2), dict(shift=-30.0)),
+    "far zero points, symmetric": (1, 1, 2, 2, 64, 128, 256, 40, 64, dict(kind="sym"), dict(shift=50.0)),
+    "padding": (4, 2, 4, 40, 128, 256, 320, 50, 64, {}, dict(first=[0, 0, -5, 1, 100, 290, 306, 999])),
+    "padding, step": (5, 1, 8, 1, 128, 256, 320, 50, 64, {}, dict(first=[0, 31, 32, 305, 400])),
+    "prompt from nothing": (1, 2, 2, 300, 64, 256, 256, 44, 64, {}, {}),
+    "prompt, odd group": (1, 1, 3, 517, 128, 448, 448, 69, 128, {}, {}),
+    "chunk": (1, 2, 4, 130, 128, 2048, 2112, 100, 192, {}, {}),
+    "chunk, padded": (2, 1, 5, 70, 128, 1024, 1024, 101, 192, {}, dict(first=[3, 700])),
+    "long, split": (1, 2, 4, 1, 128, 9024, 9088, 100, 192, {}, {}),
+    "long, split, padded": (1, 2, 1, 2, 64, 9024, 9088, 100, 192, {}, dict(first=[8000, 9100])),
+    "loud": (1, 1, 4, 6, 128, 512, 512, 64, 64, {}, dict(scale=6.0)),
+}
+
+
+def build(name):
+    rng = np.random.default_rng(zlib.crc32(name.encode()))
+    B, H, G, n, C, tq, cap, nres, rows, fm, ex = CASES[name]
+    kq, vq = S.formats(**{"gv": 64, **fm})
+    hc = S.HostCache(rng, B * H, C, tq, cap, nres, rows, kq, vq, ex.get("shift", 0.0), ex.get("scale", 1.0))
+    first = ex.get("first")
+    if first is not None:
+        # what lies wholly in the padding may be anything: NaN scales, NaN rows
+        for o, f in enumerate(first):
+            f = min(max(f, 0), hc.T)
+            hc.k[1][o, :min(f, tq) // kq.group] = 0x7FC0
+            hc.v[1][o, :min(f, tq)] = 0x7FC0
+            if f > tq:
+                hc.k[3][o, :f - tq] = hc.v[3][o, :f - tq] = 0x7FC0
+    q = S.W.to_bf16_bits(rng.standard_normal((B, n, H * G, C)).astype(np.float32))
+    return hc, q, first
+
+
+def upload_bf16(bits):
+    import torch
+    return torch.from_numpy(bits.view(np.int16).copy()).view(torch.bfloat16).cuda()
+
+
+def visible(hc, first):
+    """K and V with every hidden row zeroed (binary64 NaN would spread)."""
+    K, V = hc.K.copy(), hc.V.copy()
+    for o, f in enumerate(first if first is not None else []):
+        K[o, :max(f, 0)] = 0.0
+        V[o, :max(f, 0)] = 0.0
+    return K, V
+
+
+def reference(hc, q, first, kv_heads):
+    K, V = visible(hc, first)
+    x, mag = S.logits(S.bf16_to_f64(q), K, first, kv_heads)
+    p, lse = S.softmax(x)
+    out = np.einsum("oijt,otc->oijc", p, V)
+    absout = np.einsum("oijt,otc->oijc", p, np.abs(V))
+    return x, mag, p, lse, out, absout
+
+
+@pytest.mark.parametrize("name", CASES)
+def test_attend_chunk(b, name):
+    import torch
+    hc, q, first = build(name)
+    B, H, G, n, C = CASES[name][:5]
+    x, mag, p, lse, out, absout = reference(hc, q, first, H)
+    cache = hc.device(b, H, first)
+    g = Guarded()
+    do = g.alloc(max(q.size * 2, 16)).view(torch.bfloat16)[:q.size].view(q.shape)
+    dl = g.alloc(max(q.size // C * 4, 16)).view(torch.float32)[:q.size // C].view(q.shape[:3])
+    wB = b.kvq_attend_chunk_workspace(cache.shape, cache.resid_rows, n, G)
+    b.attend_chunk(upload_bf16(q), cache, do, dl, g.alloc(max(wB, 16)))
+    g.check("kvq_attend_chunk")
+    got, gl = do.float().cpu().numpy().astype(np.float64), dl.cpu().numpy().astype(np.float64)
+    e = 2 * S.logit_error(mag, x, C)
+    want, wl = S.to_rows(out, H), S.to_rows(lse, H)
+    none = np.isinf(wl)
+    assert np.array_equal(np.isneginf(gl), none)
+    assert np.all(got[none] == 0.0)
+    tl = S.to_rows(e, H) + (hc.T + 64) * 2.0 ** -23 + 4 * 2.0 ** -23 * (np.abs(wl) + 1)
+    assert np.all(np.abs(gl - wl)[~none] <= tl[~none]), np.max((np.abs(gl - wl) / tl)[~none])
+    u = 2.0 ** -8
+    to = S.to_rows((u + e[..., None] + (hc.T + 64) * 2.0 ** -23) * absout, H) + u * np.abs(want) + 1e-30
+    assert np.all(np.isfinite(got))
+    assert np.all(np.abs(got - want) <= to), np.max(np.abs(got - want) / to)
+    again = b.attend_chunk(upload_bf16(q), cache)           # equal calls give equal bits, lse optional
+    assert torch.equal(again[0].view(torch.int16), do.view(torch.int16)) and torch.equal(again[1], dl)
+
+
+@pytest.mark.parametrize("name", CASES)
+def test_attend_weights(b, name):
+    import torch
+    hc, q, first = build(name)
+    B, H, G, n, C = CASES[name][:5]
+    x, mag, p, lse, _, _ = reference(hc, q, first, H)
+    rng = np.random.default_rng(1)
+    stride = hc.T + 5
+    sc = rng.random((B * H, stride)).astype(np.float32)
+    l32 = lse.astype(np.float32)
+    with np.errstate(invalid="ignore"):
+        w = np.where(np.isinf(x), 0.0, np.exp(x - l32[..., None].astype(np.float64)))
+    w = np.where(np.isinf(l32)[..., None], 0.0, w)
+    e = 2 * S.logit_error(mag, x, C) + (n * G + 64) * 2.0 ** -23 + 8 * 2.0 ** -23 * np.where(np.isinf(lse), 0, np.abs(lse))
+    tol = np.einsum("oijt,oij->ot", w, e) + 2.0 ** -23 * (sc[:, :hc.T] + w.sum((1, 2))) + 1e-30
+    cache = hc.device(b, H, first)
+    dq, dl = upload_bf16(q), torch.from_numpy(S.to_rows(l32, H).copy()).cuda()
+    g = Guarded()
+    out = g.alloc(max(sc.size * 4, 16)).view(torch.float32)[:sc.size].view(sc.shape)
+    before = out.clone()
+    wB = b.kvq_attend_weights_workspace(cache.shape, cache.resid_rows, n, G)
+    ds = torch.from_numpy(sc).cuda()
+    b.attend_weights(dq, dl, cache, ds, out, g.alloc(max(wB, 16)))
+    g.check("kvq_attend_weights")
+    got = out.cpu().numpy()[:, :hc.T].astype(np.float64)
+    assert torch.equal(out[:, hc.T:].view(torch.int32), before[:, hc.T:].view(torch.int32))
+    want = sc[:, :hc.T].astype(np.float64) + w.sum((1, 2))
+    assert np.all(np.abs(got - want) <= tol), np.max(np.abs(got - want) / tol)
+    inplace = ds.clone()
+    b.attend_weights(dq, dl, cache, inplace, inplace)
+    assert torch.equal(inplace[:, :hc.T], out[:, :hc.T]) and torch.equal(inplace[:, hc.T:], ds[:, hc.T:])
+    bare = b.attend_weights(dq, dl, cache).cpu().numpy().astype(np.float64)
+    assert np.all(np.abs(bare - w.sum((1, 2))) <= tol)
+
+
+def test_a_captured_call_replays_on_new_data(b):
+    """attend_chunk and attend_weights in one graph: replay sees new queries."""
+    import torch
+    hc, q, first = build("ordinary step")
+    cache = hc.device(b, 2)
+    dq = upload_bf16(q)
+    out, lse = b.attend_chunk(dq, cache)
+    ws = torch.empty(max(b.kvq_attend_chunk_workspace(cache.shape, cache.resid_rows, 1, 8), 1), dtype=torch.uint8, device="cuda")
+    sc = torch.zeros((4, hc.T), device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        b.attend_chunk(dq, cache, out, lse, ws)
+        b.attend_weights(dq, lse, cache, sc, sc)
+    dq.copy_(torch.randn_like(dq.float()).bfloat16())
+    sc.zero_()
+    graph.replay()
+    graph.replay()
+    want, wl = b.attend_chunk(dq, cache)
+    one = b.attend_weights(dq, wl, cache)
+    torch.cuda.synchronize()
+    assert torch.equal(out.view(torch.int16), want.view(torch.int16)) and torch.equal(lse, wl)
+    assert torch.equal(sc, one + one)
+
+
+def test_other_streams(b):
+    """Two calls on two streams with their own workspaces and outputs."""
+    import torch
+    hc, q, first = build("long, split")
+    cache = hc.device(b, 2)
+    dq = upload_bf16(q)
+    want, wl = b.attend_chunk(dq, cache)
+    torch.cuda.synchronize()
+    st = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [b.attend_chunk(dq, cache, stream=s) for s in st for _ in range(4)]
+    torch.cuda.synchronize()
+    for o, l in got:
+        assert torch.equal(o.view(torch.int16), want.view(torch.int16)) and torch.equal(l, wl)
+
+
+def test_from_quantized_agrees_with_dequantize(b):
+    """A cache of two quantize() calls: the plain attention over dequantize()'s rows."""
+    import torch
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    k, v = (torch.randn((4, 700, 128), generator=gen, device="cuda").bfloat16() for _ in range(2))
+    kq = b.QParams.asym(4, 0, 15, axis=b.ALONG_T, group=64, residual=60, scale_dtype=b.BF16, zero_dtype=b.BF16)
+    vq = b.QParams.asym(4, 0, 15, axis=b.ALONG_C, group=64, residual=60, scale_dtype=b.BF16, zero_dtype=b.BF16)
+    qk, qv = b.quantize(k, kq), b.quantize(v, vq)
+    q = torch.randn((2, 1, 8, 128), generator=gen, device="cuda").bfloat16()
+    out, lse = b.attend_chunk(q, b.KVCache.from_quantized(qk, qv, kv_heads=2))
+    K, V = b.dequantize(qk).double(), b.dequantize(qv).double()
+    x = torch.einsum("ojc,otc->ojt", q.reshape(4, 4, 128).double(), K) / 128 ** 0.5
+    p = torch.softmax(x, -1)
+    want = p @ V
+    tol = 2.0 ** -8 * (want.abs() + p @ V.abs()) + 1e-4
+    assert bool(((out.reshape(4, 4, 128).double() - want).abs() <= tol).all())
+    assert bool(((lse.reshape(4, 4).double() - torch.logsumexp(x, -1)).abs() <= 1e-4).all())
