@@ -20,7 +20,7 @@
 // (m, l, y) in split order.
 #include <algorithm>
 
-#include "kvq_rows.cuh"
+#include "kvq_chunk.cuh"
 
 namespace kvq {
 
@@ -31,14 +31,6 @@ using namespace rows;
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kRowTile = 16;
-
-struct ChunkArgs {
-    View v;
-    __nv_bfloat16* out;
-    float* lse;
-    float* part;             // [outer][row][split][C + 2]: y, m, l
-    int32_t nsplit, ntiles;
-};
 
 // P.V of one 32-token batch of the store: this lane's code words of its eight
 // tokens (w[2 ks + e / 2][...], tokens 16 ks + {2 tig, 2 tig + 1, 8 + 2 tig,
@@ -413,19 +405,25 @@ cudaError_t launch_rows(const ChunkArgs& A, int64_t outer, cudaStream_t st)
     const int64_t grid = outer * A.ntiles * A.nsplit;
     if (grid > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
     attend_rows_kernel<BITS, C><<<(unsigned)grid, kThreads, 0, st>>>(A);
-    if (A.nsplit > 1) {
-        const int64_t total = outer * A.v.rows;
-        merge_rows_kernel<C><<<(unsigned)((total + kWarps - 1) / kWarps), kThreads, 0, st>>>(A, total);
-    }
+    if (A.nsplit > 1) launch_merge_rows(A, outer, C, st);
     return cudaGetLastError();
 }
 
 }  // namespace
 
+void launch_merge_rows(const ChunkArgs& A, int64_t outer, int64_t C, cudaStream_t st)
+{
+    const int64_t total = outer * A.v.rows;
+    const unsigned grid = (unsigned)((total + kWarps - 1) / kWarps);
+    if (C == 128) merge_rows_kernel<128><<<grid, kThreads, 0, st>>>(A, total);
+    else merge_rows_kernel<64><<<grid, kThreads, 0, st>>>(A, total);
+}
+
 size_t chunk_workspace(int64_t outer, int64_t C, int64_t tmax, int64_t n, int64_t group)
 {
     const int64_t rows = n * group;
     if (outer == 0 || rows == 0) return 0;
+    if (chunk_uses_tc(tmax, rows)) return chunk_tc_workspace(outer, C, tmax, rows);
     const int64_t ns = splits_of(outer, tmax, rows);
     return ns > 1 ? (size_t)(outer * rows * ns * (C + 4)) * sizeof(float) : 0;
 }
@@ -473,6 +471,7 @@ cudaError_t launch_attend_chunk(const CacheArgs& x, void* out, float* lse, void*
     A.out = static_cast<__nv_bfloat16*>(out);
     A.lse = lse;
     A.part = static_cast<float*>(ws);
+    if (chunk_uses_tc(A.v.T, A.v.rows)) return launch_attend_tc(A, x.bits, x.C, x.outer, ws, st);
     A.ntiles = (A.v.rows + kRowTile - 1) / kRowTile;
     A.nsplit = (int32_t)splits_of(x.outer, x.tq + x.nres, A.v.rows);
     if (x.bits == 4) return x.C == 128 ? launch_rows<4, 128>(A, x.outer, st) : launch_rows<4, 64>(A, x.outer, st);

@@ -1,0 +1,471 @@
+// prefill.cu -- causal attention of many query rows over the streaming
+// quantized cache, on tcgen05 tensor cores (kvq_attend_chunk with enough rows).
+//
+// Method as in chunk.cu.  With R query rows per slice the products cost 4 R C
+// operations a token while its codes are C bytes, so for hundreds of rows the
+// tensor cores bound it, and unpacking each key and value once per 256 rows
+// would compete with the softmax for issue slots.  So:
+//  1. expand_kernel writes the cache's bf16 rows, K^ and V^ [slice][Tp][C] (Tp =
+//     T rounded up to 128), once; hidden and missing tokens become zeros, so
+//     whatever lies there (NaN) never reaches a product;
+//  2. attend_tc_kernel, a CTA per (slice, 256 rows, split of the key tiles):
+//     two M = 128 tiles of query rows share every 128-token key and value tile.
+//     Warp 8 loads tiles by TMA into a ring; one thread of warp 9 issues the
+//     products; warps 0-3 and 4-7 are the softmax of the two row tiles, a
+//     thread per row: S (128 float32 columns of tensor memory) -> registers ->
+//     P in bf16 over the same columns, which the value product reads as its A
+//     operand from tensor memory.  While one tile is in its softmax the tensor
+//     cores work on the other.
+//     The running maximum is moved (and the output in tensor memory rescaled)
+//     only when it grows by more than 2^8: until then the weights are at most
+//     256, which costs float32 sums and bf16 weights no relative precision.
+#include <algorithm>
+
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include "kvq_chunk.cuh"
+#include "kvq_fast.cuh"
+#include "kvq_tc.cuh"
+
+namespace kvq {
+
+namespace {
+
+using namespace rows;
+
+constexpr int kTile = 128;                       // tokens of a key tile, rows of a query tile
+constexpr int kSlots = 4;                        // ring slots of one K or V tile
+constexpr int kThreadsTc = 384;                 // 12 warps, 168 registers each at launch (64512 in all):
+constexpr int kRegsSoftmax = 216;                // 8 softmax warps take 216 and the other four keep 56
+constexpr int kRegsOther = 56;                   // (62464), so a row of 128 scores stays in registers
+static_assert(256 * kRegsSoftmax + 128 * kRegsOther <= kThreadsTc * 168, "registers of the launch");
+constexpr float kSlack = 8.0f;                   // base-2 growth of the maximum that is let pass
+
+// ---------------------------------------------------------------- expansion
+// A thread takes one piece of 8 channels of 8 consecutive tokens: of K (its
+// group's scales and zero points read once) or of V.
+template <int BITS, int C>
+__global__ void __launch_bounds__(256)
+expand_kernel(const View a, int64_t o0, int64_t slices, int64_t Tp, __nv_bfloat16* kx, __nv_bfloat16* vx)
+{
+    using W = typename CodeWord<BITS>::T;
+    constexpr int P = C / 8;
+    const int64_t oct = Tp / 8, id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (id >= slices * oct * P) return;
+    const bool keys = blockIdx.y == 0;
+    const int p = (int)(id % P);
+    const int64_t so = id / P / oct;
+    const int t0 = (int)(id / P - so * oct) * 8;
+    const int64_t o = o0 + so;
+    const int first = a.first ? a.first[o] : 0;
+    const uint8_t* codes = keys ? a.kc : a.vc;
+    const __nv_bfloat16* sc = keys ? a.ks : a.vs;
+    const __nv_bfloat16* ze = keys ? a.kz : a.vz;
+    const float off = keys ? a.koff : a.voff;
+    const uint32_t flip = keys ? a.kflip : a.vflip;
+    __nv_bfloat16* dst = (keys ? kx : vx) + (so * Tp + t0) * C + p * 8;
+    float s[8], z[8];
+    if (keys && t0 < a.tq) {
+        const int64_t at = (o * a.ngk + t0 / a.gk) * C + p * 8;     // 8 tokens lie in one group
+        Raw8<__nv_bfloat16> r;
+        load_raw8(sc + at, r);
+        widen8(r, s);
+        if (ze) {
+            load_raw8(ze + at, r);
+            widen8(r, z);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int t = t0 + i;
+        uint4 x = make_uint4(0, 0, 0, 0);
+        if (t >= first && t < a.T) {
+            if (t >= a.tq) {
+                x = *reinterpret_cast<const uint4*>((keys ? a.kr : a.vr) + ((uint64_t)o * a.rrows + (t - a.tq)) * C + p * 8);
+            } else {
+                if (!keys) {
+                    const int64_t at = (o * a.cap + t) * a.ngv + p * 8 / a.gv;
+                    const float sv = __bfloat162float(sc[at]), zv = ze ? __bfloat162float(ze[at]) : 0.0f;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) { s[k] = sv; z[k] = zv; }
+                }
+                W w = *reinterpret_cast<const W*>(codes + ((uint64_t)o * a.cap + t) * (C * BITS / 8) + p * BITS);
+                w ^= (W)flip;
+                float v[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const float c = __fsub_rn((float)((w >> (BITS * k)) & ((1 << BITS) - 1)), off);
+                    v[k] = __fmul_rn(ze ? __fsub_rn(c, z[k]) : c, s[k]);
+                }
+                store8(reinterpret_cast<__nv_bfloat16*>(&x), v);
+            }
+        }
+        *reinterpret_cast<uint4*>(dst + (int64_t)i * C) = x;
+    }
+}
+
+// ---------------------------------------------------------------- attention
+template <int C>
+struct Smem {
+    static constexpr int kTileB = kTile * C * 2; // one Q, K or V tile
+    static constexpr int kQ = 0, kRing = 2 * kTileB, kBars = kRing + kSlots * kTileB;
+    static constexpr int kBytes = kBars + 256 + 1024;               // and room to align to 1024
+};
+
+struct TcArgs {
+    ChunkArgs A;
+    int64_t o0, slices, Tp;
+};
+
+template <int C>
+__global__ void __launch_bounds__(kThreadsTc, 1)
+attend_tc_kernel(const TcArgs X, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap)
+{
+    using S = Smem<C>;
+    constexpr int kHalves = C / 64;              // 64-channel halves of a tile, 16 KB each
+    extern __shared__ unsigned char raw[];
+    unsigned char* sm = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
+    uint64_t* full = reinterpret_cast<uint64_t*>(sm + S::kBars);
+    uint64_t* empty = full + kSlots;
+    uint64_t* sfull = empty + kSlots;            // [2] scores of a row tile are in tensor memory
+    uint64_t* pfull = sfull + 2;                 // [2] its weights are
+    uint64_t* odone = pfull + 2;                 // its output is complete
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(odone + 1);
+    volatile int* gone = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+    const ChunkArgs& A = X.A;
+    const View& a = A.v;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    int64_t blk = blockIdx.x;
+    const int split = (int)(blk % A.nsplit);
+    blk /= A.nsplit;
+    const int rt = A.ntiles - 1 - (int)(blk % A.ntiles);            // the longest first
+    const int64_t so = blk / A.ntiles, o = X.o0 + so;
+    const int r0 = rt * 2 * kTile;
+    const int nrows = min(2 * kTile, a.rows - r0);
+    const int nt = nrows > kTile ? 2 : 1;        // row tiles in use
+
+    // ---- the key tiles this CTA sees
+    const int base = a.T - a.n;
+    const int first = a.first ? max(a.first[o], 0) : 0;
+    const int last_hi = base + (r0 + nrows - 1) / a.group;
+    int j0 = 0, j1 = 0;
+    if (first <= last_hi) {
+        j0 = first / kTile;
+        j1 = last_hi / kTile + 1;
+    }
+    {
+        const int64_t len = j1 - j0;
+        const int e = j0 + (int)(len * (split + 1) / A.nsplit);
+        j0 += (int)(len * split / A.nsplit);
+        j1 = e;
+    }
+    const int n = j1 - j0;
+
+    // ---- setup: barriers, tensor memory, the query rows
+    if (tid == 0) {
+        for (int i = 0; i < kSlots; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sfull[i], 1);
+            mbar_init(&pfull[i], 4);
+        }
+        mbar_init(odone, 1);
+        *gone = 0;
+        mbar_init_fence();
+    }
+    if (warp == 9) tc::alloc(tmem_slot, 512);
+    for (int k = tid; k < nt * kTile * (C / 8); k += kThreadsTc) {
+        const int r = k / (C / 8), c = k % (C / 8);
+        uint4 x = make_uint4(0, 0, 0, 0);
+        if (r < nrows) x = *reinterpret_cast<const uint4*>(a.q + row_index(a, o, r0 + r) * C + c * 8);
+        *reinterpret_cast<uint4*>(sm + S::kQ + (r / kTile) * S::kTileB + (c / 8) * (kTile * 128) +
+                                  tc::swizzled(r % kTile, c % 8)) = x;
+    }
+    tc::async_fence();
+    tc::before_sync();
+    __syncthreads();
+    tc::after_sync();
+    const uint32_t tmem = *tmem_slot;
+
+    if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
+    if (warp == 8) {
+        // ---- tiles by TMA, in the order the products take them: K0, K1, V0, K2, V1, ...
+        if (lane == 0 && n > 0) {
+            int it = 0;
+            auto load = [&](const CUtensorMap* map, int j) {
+                const int s = it % kSlots;
+                if (it >= kSlots && !tc::wait(&empty[s], ((it / kSlots) - 1) & 1, gone)) return false;
+                mbar_expect_tx(&full[s], S::kTileB);
+                for (int h = 0; h < kHalves; ++h)
+                    tma_load_2d(sm + S::kRing + s * S::kTileB + h * (kTile * 128), map, h * 64,
+                                (int)(so * X.Tp) + j * kTile, &full[s]);
+                ++it;
+                return true;
+            };
+            bool ok = load(&kmap, j0);
+            for (int j = j0; ok && j < j1; ++j) {
+                if (j + 1 < j1) ok = load(&kmap, j + 1);
+                ok = ok && load(&vmap, j);
+            }
+            // every copy issued lands before the CTA's shared memory goes
+            for (int i = max(0, it - kSlots); i < it; ++i) tc::wait(&full[i % kSlots], (i / kSlots) & 1, gone);
+        }
+    } else if (warp == 9) {
+        // ---- products
+        if (lane == 0 && n > 0) {
+            constexpr uint32_t kScores = tc::instr_desc(kTile, kTile, false), kValues = tc::instr_desc(kTile, C, true);
+            const uint32_t q_at = smem_u32(sm + S::kQ), ring = smem_u32(sm + S::kRing);
+            auto scores = [&](int t, int s) {
+#pragma unroll
+                for (int k = 0; k < C / 16; ++k) {
+                    const uint32_t at = (k / 4) * (kTile * 128) + (k % 4) * 32;
+                    tc::mma_ss(tmem + t * kTile, tc::smem_desc(q_at + t * S::kTileB + at, 16),
+                               tc::smem_desc(ring + s * S::kTileB + at, 16), kScores, k > 0);
+                }
+                tc::commit(&sfull[t]);
+            };
+            int it = 0;
+            bool ok = tc::wait(&full[0], 0, gone);
+            if (ok) {
+                for (int t = 0; t < nt; ++t) scores(t, 0);
+                tc::commit(&empty[0]);
+            }
+            ++it;
+            for (int j = 0; ok && j < n; ++j) {
+                int ks = -1;
+                if (j + 1 < n) {
+                    ks = it % kSlots;
+                    ok = tc::wait(&full[ks], (it / kSlots) & 1, gone);
+                    ++it;
+                }
+                const int vs = it % kSlots;
+                ok = ok && tc::wait(&full[vs], (it / kSlots) & 1, gone);
+                ++it;
+                for (int t = 0; ok && t < nt; ++t) {
+                    ok = tc::wait(&pfull[t], j & 1, gone);
+                    if (!ok) break;
+                    tc::after_sync();
+#pragma unroll
+                    for (int k = 0; k < kTile / 16; ++k)
+                        tc::mma_ts(tmem + 256 + t * C, tmem + t * kTile + k * 8,
+                                   tc::smem_desc(ring + vs * S::kTileB + k * 2048, kTile * 128), kValues, j > 0 || k > 0);
+                    if (ks >= 0) scores(t, ks);
+                }
+                if (ok) {
+                    tc::commit(&empty[vs]);
+                    if (ks >= 0) tc::commit(&empty[ks]);
+                }
+            }
+            if (ok) tc::commit(odone);
+        }
+    }
+    } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    if (warp < 4 * nt) {
+        // ---- softmax of row tile t, a thread per row
+        const int t = warp / 4;
+        const int r = r0 + t * kTile + (warp & 3) * 32 + lane;
+        const int last = r < a.rows ? base + r / a.group : a.T;     // rows past the last are not written
+        const int tile_lo = base + (r0 + t * kTile) / a.group;      // the fewest tokens a row of the tile sees
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t s_at = tmem + lanes + t * kTile, o_at = tmem + lanes + 256 + t * C;
+        float m = -INFINITY;
+        u64 sum = 0;
+        bool ok = true;
+        for (int j = 0; ok && j < n; ++j) {
+            ok = tc::wait(&sfull[t], j & 1, gone);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (!ok) break;
+            tc::after_sync();
+            uint32_t s[kTile];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tc::ld32(s_at + 32 * c, s + 32 * c);
+            tc::wait_ld();
+            const int c0 = (j0 + j) * kTile;
+            if (c0 < first || c0 + kTile - 1 > tile_lo) {
+#pragma unroll
+                for (int c = 0; c < kTile; ++c)
+                    if (c0 + c < first || c0 + c > last) s[c] = 0xFF800000u;         // -inf
+            }
+            float x0 = -INFINITY, x1 = -INFINITY, x2 = -INFINITY, x3 = -INFINITY;
+#pragma unroll
+            for (int c = 0; c < kTile; c += 4) {
+                x0 = fmaxf(x0, __uint_as_float(s[c]));
+                x1 = fmaxf(x1, __uint_as_float(s[c + 1]));
+                x2 = fmaxf(x2, __uint_as_float(s[c + 2]));
+                x3 = fmaxf(x3, __uint_as_float(s[c + 3]));
+            }
+            const float top = __fmul_rn(fmaxf(fmaxf(x0, x1), fmaxf(x2, x3)), a.scale2);
+            const bool grow = top > __fadd_rn(m, kSlack);           // m = -inf: whenever anything is seen
+            if (__any_sync(0xFFFFFFFFu, grow)) {
+                const float f = grow ? ex2(__fsub_rn(m, top)) : 1.0f;
+                if (grow) m = top;
+                sum = mul2(sum, pk(f, f));
+                if (j > 0) {
+                    // the scores' arrival says that the products before them are done too
+#pragma unroll
+                    for (int c = 0; c < C / 32; ++c) {
+                        uint32_t y[32];
+                        tc::ld32(o_at + 32 * c, y);
+                        tc::wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) y[i] = __float_as_uint(__fmul_rn(__uint_as_float(y[i]), f));
+                        tc::st32(o_at + 32 * c, y);
+                    }
+                }
+            }
+            const float neg = m == -INFINITY ? 0.0f : -m;
+            const u64 sc2 = pk(a.scale2, a.scale2), ng2 = pk(neg, neg);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {        // 64 scores -> 32 columns of weight pairs
+                uint32_t p[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    const int c = 64 * h + 2 * i;
+                    const u64 e = fma2(pk(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), sc2, ng2);
+                    const float e0 = ex2(lo_of(e)), e1 = ex2(hi_of(e));
+                    sum = add2(sum, pk(e0, e1));
+                    p[i] = pack_bf16x2(e0, e1);
+                }
+                tc::st32(s_at + 32 * h, p);
+            }
+            tc::wait_st();
+            tc::before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&pfull[t]);
+        }
+        // ---- output
+        float l = 0.0f;
+        if (ok && n > 0) {
+            ok = __all_sync(0xFFFFFFFFu, tc::wait(odone, 0, gone));
+            tc::after_sync();
+            l = __fadd_rn(lo_of(sum), hi_of(sum));
+        }
+        const bool write = ok && r < a.rows;
+        const int64_t at = write ? row_index(a, o, r) : 0;
+        float* part = A.part + ((o * a.rows + r) * A.nsplit + split) * (C + 4);
+        const float inv = l > 0.0f ? __fdiv_rn(1.0f, l) : 0.0f;
+#pragma unroll
+        for (int c = 0; c < C / 32; ++c) {
+            uint32_t y[32];
+            if (ok && n > 0) {
+                tc::ld32(o_at + 32 * c, y);
+                tc::wait_ld();
+            } else {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) y[i] = 0u;
+            }
+            if (write && A.nsplit > 1) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    *reinterpret_cast<uint4*>(part + 32 * c + 4 * i) = make_uint4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+            } else if (write) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        w[k] = pack_bf16x2(__fmul_rn(__uint_as_float(y[8 * i + 2 * k]), inv),
+                                           __fmul_rn(__uint_as_float(y[8 * i + 2 * k + 1]), inv));
+                    *reinterpret_cast<uint4*>(A.out + at * C + 32 * c + 8 * i) = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+            }
+            __syncwarp();                        // the next load wants the whole warp
+        }
+        if (write && A.nsplit > 1) *reinterpret_cast<float2*>(part + C) = make_float2(m, l);
+        if (write && A.nsplit == 1 && A.lse)
+            A.lse[at] = l > 0.0f ? __fmul_rn(__fadd_rn(m, log2f(l)), 0.6931471805599453f) : -INFINITY;
+    }
+    }
+    __syncwarp();
+    tc::before_sync();
+    __syncthreads();
+    tc::after_sync();
+    if (warp == 9) tc::dealloc(tmem, 512);
+}
+
+// [rows, C] bf16 as boxes of 64 channels x 128 rows, 128-byte swizzle
+bool encode_map(const void* x, int64_t rows, int64_t C, CUtensorMap* map)
+{
+    auto enc = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(tensor_map_encode_fn());
+    if (!enc) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)C, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)C * 2};
+    const cuuint32_t box[2] = {64, kTile};
+    const cuuint32_t estr[2] = {1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(x), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+constexpr int64_t kExpandBytes = int64_t(1) << 30;                  // expanded K and V held at once
+
+struct TcPlan { int64_t Tp, slices, ntiles, nsplit; };
+
+TcPlan tc_plan(int64_t outer, int64_t C, int64_t T, int64_t rows)
+{
+    TcPlan p;
+    p.Tp = (T + kTile - 1) / kTile * kTile;
+    p.slices = std::max<int64_t>(1, std::min<int64_t>(outer, kExpandBytes / std::max<int64_t>(p.Tp * C * 4, 1)));
+    p.ntiles = (rows + 2 * kTile - 1) / (2 * kTile);
+    // few CTAs: split the key tiles, at least four a split
+    const int64_t ctas = p.slices * p.ntiles;
+    p.nsplit = std::max<int64_t>(1, std::min<int64_t>(152 / ctas, p.Tp / kTile / 4));
+    return p;
+}
+
+template <int BITS, int C>
+cudaError_t launch_tc(const ChunkArgs& A0, int64_t outer, void* ws, cudaStream_t st)
+{
+    const TcPlan p = tc_plan(outer, C, A0.v.T, A0.v.rows);
+    TcArgs X;
+    X.A = A0;
+    X.A.nsplit = (int32_t)p.nsplit;
+    X.A.ntiles = (int32_t)p.ntiles;
+    X.Tp = p.Tp;
+    __nv_bfloat16* kx = static_cast<__nv_bfloat16*>(ws);
+    __nv_bfloat16* vx = kx + p.slices * p.Tp * C;
+    X.A.part = reinterpret_cast<float*>(vx + p.slices * p.Tp * C);
+    if (p.slices * p.Tp > 0x7FFFFFFF || p.slices * p.ntiles * p.nsplit > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+    CUtensorMap km, vm;
+    if (!encode_map(kx, p.slices * p.Tp, C, &km) || !encode_map(vx, p.slices * p.Tp, C, &vm)) return cudaErrorNotSupported;
+    cudaError_t e = ensure_kernel_attrs(reinterpret_cast<const void*>(attend_tc_kernel<C>), Smem<C>::kBytes);
+    if (e != cudaSuccess) return e;
+    for (int64_t o0 = 0; o0 < outer; o0 += p.slices) {
+        X.o0 = o0;
+        X.slices = std::min(p.slices, outer - o0);
+        const int64_t items = X.slices * (p.Tp / 8) * (C / 8);
+        expand_kernel<BITS, C><<<dim3((unsigned)((items + 255) / 256), 2), 256, 0, st>>>(X.A.v, o0, X.slices, p.Tp, kx, vx);
+        attend_tc_kernel<C><<<(unsigned)(X.slices * p.ntiles * p.nsplit), kThreadsTc, Smem<C>::kBytes, st>>>(X, km, vm);
+    }
+    if (p.nsplit > 1) launch_merge_rows(X.A, outer, C, st);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+// Rows from which the tensor-core form is taken.
+bool chunk_uses_tc(int64_t T, int64_t rows) { return rows > 64 && T > 0; }
+
+// Enough for every T up to tmax: a shorter cache may take more slices at once,
+// but never more than the bound on expanded bytes.
+size_t chunk_tc_workspace(int64_t outer, int64_t C, int64_t tmax, int64_t rows)
+{
+    const TcPlan p = tc_plan(outer, C, tmax, rows);
+    size_t b = (size_t)std::min(outer * p.Tp * C * 4, std::max(kExpandBytes, p.Tp * C * 4));
+    if (p.nsplit > 1) b += (size_t)(outer * rows * p.nsplit * (C + 4)) * 4;
+    return b;
+}
+
+cudaError_t launch_attend_tc(const ChunkArgs& A, int bits, int64_t C, int64_t outer, void* ws, cudaStream_t st)
+{
+    if (bits == 4) return C == 128 ? launch_tc<4, 128>(A, outer, ws, st) : launch_tc<4, 64>(A, outer, ws, st);
+    return C == 128 ? launch_tc<2, 128>(A, outer, ws, st) : launch_tc<2, 64>(A, outer, ws, st);
+}
+
+}  // namespace kvq

@@ -13,11 +13,9 @@
 // sum needs an atomic and its order is fixed.
 #include <algorithm>
 
-#include "kvq_rows.cuh"
+#include "kvq_chunk.cuh"
 
 namespace kvq {
-
-rows::View cache_view(const CacheArgs& x);
 
 namespace {
 
