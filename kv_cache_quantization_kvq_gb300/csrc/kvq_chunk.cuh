@@ -2,6 +2,8 @@
 // rows; prefill.cu: many) share.
 #pragma once
 
+#include <cuda.h>
+
 #include "kvq_rows.cuh"
 
 namespace kvq {
@@ -22,5 +24,14 @@ void launch_merge_rows(const ChunkArgs& A, int64_t outer, int64_t C, cudaStream_
 bool chunk_uses_tc(int64_t T, int64_t rows);
 size_t chunk_tc_workspace(int64_t outer, int64_t C, int64_t tmax, int64_t rows);
 cudaError_t launch_attend_tc(const ChunkArgs& A, int bits, int64_t C, int64_t outer, void* ws, cudaStream_t st);
+
+// the same for kvq_attend_weights (weights_tc.cu)
+bool weights_use_tc(int64_t rows);
+size_t weights_tc_workspace(int64_t outer, int64_t C, int64_t tmax, int64_t rows);
+cudaError_t launch_weights_tc(const rows::View& v, const float* lse, const float* in, float* out, int64_t stride,
+                              int bits, int64_t C, int64_t outer, void* ws, cudaStream_t st);
+
+// [rows, C] bf16 as boxes of 64 channels x 128 rows, 128-byte swizzle (prefill.cu)
+bool encode_rows_tile_map(const void* x, int64_t rows, int64_t C, CUtensorMap* map);
 
 }  // namespace kvq

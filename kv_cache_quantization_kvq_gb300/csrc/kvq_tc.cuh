@@ -31,6 +31,13 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile in
     return false;
 }
 
+// The same for a copy already issued, which lands whatever else went wrong:
+// bounded, but not cut short.
+__device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity) {
+    volatile int never = 0;
+    wait(bar, parity, &never);
+}
+
 // ---- tensor memory
 __device__ __forceinline__ void alloc(uint32_t* slot, uint32_t cols) {           // one warp
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)), "r"(cols)

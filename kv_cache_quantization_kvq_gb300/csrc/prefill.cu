@@ -213,7 +213,7 @@ attend_tc_kernel(const TcArgs X, const __grid_constant__ CUtensorMap kmap, const
                 ok = ok && load(&vmap, j);
             }
             // every copy issued lands before the CTA's shared memory goes
-            for (int i = max(0, it - kSlots); i < it; ++i) tc::wait(&full[i % kSlots], (i / kSlots) & 1, gone);
+            for (int i = max(0, it - kSlots); i < it; ++i) tc::drain(&full[i % kSlots], (i / kSlots) & 1);
         }
     } else if (warp == 9) {
         // ---- products
@@ -389,20 +389,6 @@ attend_tc_kernel(const TcArgs X, const __grid_constant__ CUtensorMap kmap, const
     if (warp == 9) tc::dealloc(tmem, 512);
 }
 
-// [rows, C] bf16 as boxes of 64 channels x 128 rows, 128-byte swizzle
-bool encode_map(const void* x, int64_t rows, int64_t C, CUtensorMap* map)
-{
-    auto enc = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(tensor_map_encode_fn());
-    if (!enc) return false;
-    const cuuint64_t dims[2] = {(cuuint64_t)C, (cuuint64_t)rows};
-    const cuuint64_t strides[1] = {(cuuint64_t)C * 2};
-    const cuuint32_t box[2] = {64, kTile};
-    const cuuint32_t estr[2] = {1, 1};
-    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(x), dims, strides, box, estr,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 constexpr int64_t kExpandBytes = int64_t(1) << 30;                  // expanded K and V held at once
 
 struct TcPlan { int64_t Tp, slices, ntiles, nsplit; };
@@ -433,7 +419,7 @@ cudaError_t launch_tc(const ChunkArgs& A0, int64_t outer, void* ws, cudaStream_t
     X.A.part = reinterpret_cast<float*>(vx + p.slices * p.Tp * C);
     if (p.slices * p.Tp > 0x7FFFFFFF || p.slices * p.ntiles * p.nsplit > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
     CUtensorMap km, vm;
-    if (!encode_map(kx, p.slices * p.Tp, C, &km) || !encode_map(vx, p.slices * p.Tp, C, &vm)) return cudaErrorNotSupported;
+    if (!encode_rows_tile_map(kx, p.slices * p.Tp, C, &km) || !encode_rows_tile_map(vx, p.slices * p.Tp, C, &vm)) return cudaErrorNotSupported;
     cudaError_t e = ensure_kernel_attrs(reinterpret_cast<const void*>(attend_tc_kernel<C>), Smem<C>::kBytes);
     if (e != cudaSuccess) return e;
     for (int64_t o0 = 0; o0 < outer; o0 += p.slices) {
@@ -448,6 +434,20 @@ cudaError_t launch_tc(const ChunkArgs& A0, int64_t outer, void* ws, cudaStream_t
 }
 
 }  // namespace
+
+// [rows, C] bf16 as boxes of 64 channels x 128 rows, 128-byte swizzle
+bool encode_rows_tile_map(const void* x, int64_t rows, int64_t C, CUtensorMap* map)
+{
+    auto enc = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(tensor_map_encode_fn());
+    if (!enc) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)C, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)C * 2};
+    const cuuint32_t box[2] = {64, kTile};
+    const cuuint32_t estr[2] = {1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(x), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 // Rows from which the tensor-core form is taken.
 bool chunk_uses_tc(int64_t T, int64_t rows) { return rows > 64 && T > 0; }

@@ -178,10 +178,13 @@ cudaError_t launch_rows(const WeightArgs& A, int64_t outer, cudaStream_t st)
 
 }  // namespace
 
-size_t weights_workspace(int64_t, int64_t, int64_t, int64_t, int64_t) { return 0; }
+size_t weights_workspace(int64_t outer, int64_t C, int64_t tmax, int64_t n, int64_t group)
+{
+    return outer > 0 && weights_use_tc(n * group) ? weights_tc_workspace(outer, C, tmax, n * group) : 0;
+}
 
 cudaError_t launch_attend_weights(const CacheArgs& x, const float* lse, const float* scores_in, float* scores_out,
-                                  int64_t stride, void*, cudaStream_t st)
+                                  int64_t stride, void* ws, cudaStream_t st)
 {
     if (x.outer == 0 || x.tq + x.nres == 0) return cudaSuccess;
     WeightArgs A;
@@ -190,6 +193,8 @@ cudaError_t launch_attend_weights(const CacheArgs& x, const float* lse, const fl
     A.in = scores_in;
     A.out = scores_out;
     A.stride = stride;
+    if (weights_use_tc(A.v.rows))
+        return launch_weights_tc(A.v, lse, scores_in, scores_out, stride, x.bits, x.C, x.outer, ws, st);
     if (x.bits == 4) return x.C == 128 ? launch_rows<4, 128>(A, x.outer, st) : launch_rows<4, 64>(A, x.outer, st);
     return x.C == 128 ? launch_rows<2, 128>(A, x.outer, st) : launch_rows<2, 64>(A, x.outer, st);
 }
