@@ -198,7 +198,7 @@ kvq_status kvq_attend_weights_workspace(const kvq_shape* shape, int64_t resid_ro
 {
     kvq_status s = workspace_args(shape, resid_rows, n, group, workspace_B);
     if (s != KVQ_OK) return s;
-    *workspace_B = kvq::weights_workspace(shape->outer, shape->C, shape->T + resid_rows, n, group);
+    *workspace_B = kvq::weights_workspace(shape->outer, shape->C, n, group);
     return KVQ_OK;
 }
 
@@ -219,7 +219,7 @@ kvq_status kvq_attend_weights(const void* q, const float* lse, int64_t n, int64_
         return s;
     if (any && scores_in && partly_overlap(scores_in, scores_out, ((a.outer - 1) * score_stride + T) * sizeof(float)))
         KVQ_FAIL(KVQ_EINVAL, "scores_in and scores_out overlap without being the same buffer");
-    const size_t want = kvq::weights_workspace(a.outer, a.C, a.cap + a.rrows, n, group);
+    const size_t want = kvq::weights_workspace(a.outer, a.C, n, group);
     if ((s = check_workspace(workspace, workspace_B, want, 256, "kvq_attend_weights"))) return s;
     return cuda_result(kvq::launch_attend_weights(a, lse, scores_in, scores_out, score_stride, workspace,
                                                   (cudaStream_t)stream),

@@ -27,7 +27,7 @@ cudaError_t launch_attend_tc(const ChunkArgs& A, int bits, int64_t C, int64_t ou
 
 // the same for kvq_attend_weights (weights_tc.cu)
 bool weights_use_tc(int64_t rows);
-size_t weights_tc_workspace(int64_t outer, int64_t C, int64_t tmax, int64_t rows);
+size_t weights_tc_workspace(int64_t outer, int64_t C, int64_t rows);
 cudaError_t launch_weights_tc(const rows::View& v, const float* lse, const float* in, float* out, int64_t stride,
                               int bits, int64_t C, int64_t outer, void* ws, cudaStream_t st);
 

@@ -157,7 +157,7 @@ struct CacheArgs {
 };
 size_t chunk_workspace(int64_t outer, int64_t C, int64_t tmax, int64_t n, int64_t group);
 cudaError_t launch_attend_chunk(const CacheArgs& a, void* out, float* lse, void* ws, cudaStream_t st);
-size_t weights_workspace(int64_t outer, int64_t C, int64_t tmax, int64_t n, int64_t group);
+size_t weights_workspace(int64_t outer, int64_t C, int64_t n, int64_t group);
 cudaError_t launch_attend_weights(const CacheArgs& a, const float* lse, const float* scores_in, float* scores_out,
                                   int64_t stride, void* ws, cudaStream_t st);
 

@@ -178,9 +178,9 @@ cudaError_t launch_rows(const WeightArgs& A, int64_t outer, cudaStream_t st)
 
 }  // namespace
 
-size_t weights_workspace(int64_t outer, int64_t C, int64_t tmax, int64_t n, int64_t group)
+size_t weights_workspace(int64_t outer, int64_t C, int64_t n, int64_t group)
 {
-    return outer > 0 && weights_use_tc(n * group) ? weights_tc_workspace(outer, C, tmax, n * group) : 0;
+    return outer > 0 && weights_use_tc(n * group) ? weights_tc_workspace(outer, C, n * group) : 0;
 }
 
 cudaError_t launch_attend_weights(const CacheArgs& x, const float* lse, const float* scores_in, float* scores_out,

@@ -39,13 +39,13 @@ struct WtArgs {
     const float* in;
     float* out;
     int64_t stride, R;                           // R: rows padded to 128
-    const float* lse2;                           // [outer][R]
+    const float* row;                            // [outer][R / 128][2][128]: -lse in base 2; last token seen (int bits)
     float* part;                                 // [outer][split][Tp]
     int32_t nsplit, ntok;                        // row splits, 256-token CTAs of a slice
 };
 
 __global__ void __launch_bounds__(256)
-pack_rows_kernel(const View a, const float* lse, int64_t R, int C, int64_t total, __nv_bfloat16* qx, float* lse2)
+pack_rows_kernel(const View a, const float* lse, int64_t R, int C, int64_t total, __nv_bfloat16* qx, float* rows2)
 {
     const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (id >= total) return;
@@ -55,24 +55,30 @@ pack_rows_kernel(const View a, const float* lse, int64_t R, int C, int64_t total
     const int64_t o = row / R;
     const int r = (int)(row - o * R);
     uint4 x = make_uint4(0, 0, 0, 0);
-    float l = INFINITY;
+    float l = -INFINITY;                         // 2^(x - inf) = 0: no weight
+    int last = -1;
     if (r < a.rows) {
         const int64_t at = row_index(a, o, r);
         x = *reinterpret_cast<const uint4*>(a.q + at * C + p * 8);
         if (p == 0) {
             l = lse[at];
-            l = l == -INFINITY ? INFINITY : __fmul_rn(l, kLog2e);
+            l = l == -INFINITY ? -INFINITY : -__fmul_rn(l, kLog2e);
+            last = a.T - a.n + r / a.group;
         }
     }
     reinterpret_cast<uint4*>(qx)[id] = x;
-    if (p == 0) lse2[row] = l;
+    if (p == 0) {
+        float* at = rows2 + row / kTile * (2 * kTile) + row % kTile;
+        at[0] = l;
+        at[kTile] = __int_as_float(last);
+    }
 }
 
 template <int C>
 struct SmemW {
     static constexpr int kTileB = kTile * C * 2;
     static constexpr int kSlots = 4;
-    static constexpr int kK = 0, kRing = 2 * kTileB, kLse = kRing + kSlots * kTileB, kBars = kLse + kSlots * kTile * 4;
+    static constexpr int kK = 0, kRing = 2 * kTileB, kLse = kRing + kSlots * kTileB, kBars = kLse + kSlots * kTile * 8;
     static constexpr int kBytes = kBars + 256 + 1024;
 };
 
@@ -85,7 +91,7 @@ weights_tc_kernel(const WtArgs A, const __grid_constant__ CUtensorMap qmap)
     constexpr int kSlots = S::kSlots, kHalves = C / 64, P = C / 8;
     extern __shared__ unsigned char raw[];
     unsigned char* sm = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
-    float* slse = reinterpret_cast<float*>(sm + S::kLse);          // [slot][128]
+    float4* srow = reinterpret_cast<float4*>(sm + S::kLse);        // [slot][2][32]: four rows' -lse; their last tokens
     uint64_t* full = reinterpret_cast<uint64_t*>(sm + S::kBars);
     uint64_t* empty = full + kSlots;             // slot free: products done (1) and lse read (2 x 4 warps)
     uint64_t* dfull = empty + kSlots;            // [2 tiles][2 buffers]
@@ -132,6 +138,7 @@ weights_tc_kernel(const WtArgs A, const __grid_constant__ CUtensorMap qmap)
     if (warp == 9) tc::alloc(tmem_slot, 512);
     // ---- the keys: row = token, 16-byte pieces of 8 channels; hidden tokens are zeros
     if (n > 0) {
+#pragma unroll 4
         for (int k = tid; k < 2 * kTile * P; k += kThreadsW) {
             const int row = k / P, p = k % P, t = t0 + row;
             uint4 x = make_uint4(0, 0, 0, 0);
@@ -174,11 +181,11 @@ weights_tc_kernel(const WtArgs A, const __grid_constant__ CUtensorMap qmap)
             for (; it < n; ++it) {
                 const int s = it % kSlots;
                 if (it >= kSlots && !tc::wait(&empty[s], ((it / kSlots) - 1) & 1, gone)) break;
-                mbar_expect_tx(&full[s], S::kTileB + kTile * 4);
+                mbar_expect_tx(&full[s], S::kTileB + kTile * 8);
                 const int64_t row = o * A.R + (int64_t)(n0 + it) * kTile;
                 for (int h = 0; h < kHalves; ++h)
                     tma_load_2d(sm + S::kRing + s * S::kTileB + h * (kTile * 128), &qmap, h * 64, (int)row, &full[s]);
-                bulk_g2s(slse + s * kTile, A.lse2 + row, kTile * 4, &full[s]);
+                bulk_g2s(srow + s * (kTile / 2), A.row + row * 2, kTile * 8, &full[s]);
             }
             // every copy issued lands before the CTA's shared memory goes
             for (int i = max(0, it - kSlots); i < it; ++i) tc::drain(&full[i % kSlots], (i / kSlots) & 1);
@@ -224,26 +231,41 @@ weights_tc_kernel(const WtArgs A, const __grid_constant__ CUtensorMap qmap)
             const uint32_t d_at = tmem + lanes + (2 * t + b) * kTile;
             const int row0 = (n0 + it) * kTile;
             const bool cut = tile_hi > base + row0 / a.group;       // some row does not see some token
+            const float4* rp = srow + s * (kTile / 2);
             u64 acc0 = 0, acc1 = 0;
+            if (!cut) {
+                uint32_t x[2][32];               // the next 32 columns load while these are summed
+                tc::ld32(d_at, x[0]);
 #pragma unroll
-            for (int h = 0; h < 4; ++h) {
-                uint32_t x[32];
-                tc::ld32(d_at + 32 * h, x);
-                tc::wait_ld();
-                const float4* l4 = reinterpret_cast<const float4*>(slse + s * kTile + 32 * h);
+                for (int h = 0; h < 4; ++h) {
+                    tc::wait_ld();
+                    if (h < 3) tc::ld32(d_at + 32 * (h + 1), x[(h + 1) & 1]);
+                    const uint32_t* y = x[h & 1];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float4 l = l4[i];
-                    const u64 e0 = fma2(pk(__uint_as_float(x[4 * i]), __uint_as_float(x[4 * i + 1])), sc2, pk(-l.x, -l.y));
-                    const u64 e1 = fma2(pk(__uint_as_float(x[4 * i + 2]), __uint_as_float(x[4 * i + 3])), sc2, pk(-l.z, -l.w));
-                    float w[4] = {ex2(lo_of(e0)), ex2(hi_of(e0)), ex2(lo_of(e1)), ex2(hi_of(e1))};
-                    if (cut) {
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            if (tok > base + (row0 + 32 * h + 4 * i + k) / a.group) w[k] = 0.0f;
+                    for (int i = 0; i < 8; ++i) {
+                        const float4 l = rp[8 * h + i];
+                        const u64 e0 = fma2(pk(__uint_as_float(y[4 * i]), __uint_as_float(y[4 * i + 1])), sc2, pk(l.x, l.y));
+                        const u64 e1 = fma2(pk(__uint_as_float(y[4 * i + 2]), __uint_as_float(y[4 * i + 3])), sc2, pk(l.z, l.w));
+                        acc0 = add2(acc0, pk(ex2(lo_of(e0)), ex2(hi_of(e0))));
+                        acc1 = add2(acc1, pk(ex2(lo_of(e1)), ex2(hi_of(e1))));
                     }
-                    acc0 = add2(acc0, pk(w[0], w[1]));
-                    acc1 = add2(acc1, pk(w[2], w[3]));
+                }
+            } else {
+#pragma unroll 1
+                for (int h = 0; h < 4; ++h) {
+                    uint32_t y[32];
+                    tc::ld32(d_at + 32 * h, y);
+                    tc::wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float4 l = rp[8 * h + i], z = rp[kTile / 4 + 8 * h + i];
+                        const u64 e0 = fma2(pk(__uint_as_float(y[4 * i]), __uint_as_float(y[4 * i + 1])), sc2, pk(l.x, l.y));
+                        const u64 e1 = fma2(pk(__uint_as_float(y[4 * i + 2]), __uint_as_float(y[4 * i + 3])), sc2, pk(l.z, l.w));
+                        acc0 = add2(acc0, pk(tok <= __float_as_int(z.x) ? ex2(lo_of(e0)) : 0.0f,
+                                             tok <= __float_as_int(z.y) ? ex2(hi_of(e0)) : 0.0f));
+                        acc1 = add2(acc1, pk(tok <= __float_as_int(z.z) ? ex2(lo_of(e1)) : 0.0f,
+                                             tok <= __float_as_int(z.w) ? ex2(hi_of(e1)) : 0.0f));
+                    }
                 }
             }
             tc::before_sync();
@@ -284,6 +306,8 @@ join_kernel(const WtArgs A, int64_t total)
     A.out[at] = A.in ? __fadd_rn(A.in[at], s) : s;
 }
 
+constexpr int64_t kMaxCtas = 8 * 152;             // more CTAs than this are not split further
+
 struct WtPlan { int64_t R, ntok, nsplit; };
 
 WtPlan wt_plan(int64_t outer, int64_t T, int64_t rows)
@@ -291,8 +315,18 @@ WtPlan wt_plan(int64_t outer, int64_t T, int64_t rows)
     WtPlan p;
     p.R = (rows + kTile - 1) / kTile * kTile;
     p.ntok = (T + 2 * kTile - 1) / (2 * kTile);
-    // few CTAs: split the rows, at least four row tiles a split
-    p.nsplit = std::max<int64_t>(1, std::min<int64_t>(152 / std::max<int64_t>(outer * p.ntok, 1), p.R / kTile / 4));
+    // Splits of the rows that leave the least idle at the end: waves of 152 CTAs,
+    // each the row tiles of a split and the time of about three to lay out its keys.
+    const int64_t ctas = std::max<int64_t>(outer * p.ntok, 1), tiles = p.R / kTile;
+    p.nsplit = 1;
+    int64_t best = INT64_MAX;
+    for (int64_t s = 1; s == 1 || (s <= tiles && ctas * s <= kMaxCtas); ++s) {
+        const int64_t cost = ((ctas * s + 151) / 152) * ((tiles + s - 1) / s + 3);
+        if (cost < best) {
+            best = cost;
+            p.nsplit = s;
+        }
+    }
     return p;
 }
 
@@ -305,10 +339,10 @@ cudaError_t launch_wt(WtArgs A, int64_t outer, void* ws, cudaStream_t st)
     char* at = static_cast<char*>(ws);
     __nv_bfloat16* qx = reinterpret_cast<__nv_bfloat16*>(at);
     at += round256((size_t)(outer * p.R * C) * 2);
-    float* lse2 = reinterpret_cast<float*>(at);
-    at += round256((size_t)(outer * p.R) * 4);
+    float* rows2 = reinterpret_cast<float*>(at);
+    at += round256((size_t)(outer * p.R) * 8);
     A.R = p.R;
-    A.lse2 = lse2;
+    A.row = rows2;
     A.part = reinterpret_cast<float*>(at);
     A.nsplit = (int32_t)p.nsplit;
     A.ntok = (int32_t)p.ntok;
@@ -318,7 +352,7 @@ cudaError_t launch_wt(WtArgs A, int64_t outer, void* ws, cudaStream_t st)
     if (!encode_rows_tile_map(qx, outer * p.R, C, &qm)) return cudaErrorNotSupported;
     cudaError_t e = ensure_kernel_attrs(reinterpret_cast<const void*>(weights_tc_kernel<BITS, C>), SmemW<C>::kBytes);
     if (e != cudaSuccess) return e;
-    pack_rows_kernel<<<(unsigned)((packs + 255) / 256), 256, 0, st>>>(A.v, A.lse, p.R, C, packs, qx, lse2);
+    pack_rows_kernel<<<(unsigned)((packs + 255) / 256), 256, 0, st>>>(A.v, A.lse, p.R, C, packs, qx, rows2);
     weights_tc_kernel<BITS, C><<<(unsigned)grid, kThreadsW, SmemW<C>::kBytes, st>>>(A, qm);
     if (p.nsplit > 1) {
         const int64_t total = outer * A.v.T;
@@ -331,12 +365,11 @@ cudaError_t launch_wt(WtArgs A, int64_t outer, void* ws, cudaStream_t st)
 
 bool weights_use_tc(int64_t rows) { return rows > 64; }
 
-size_t weights_tc_workspace(int64_t outer, int64_t C, int64_t tmax, int64_t rows)
+size_t weights_tc_workspace(int64_t outer, int64_t C, int64_t rows)
 {
     const int64_t R = (rows + kTile - 1) / kTile * kTile;
-    size_t b = round256((size_t)(outer * R * C) * 2) + round256((size_t)(outer * R) * 4);
-    // the most splits times tokens of any T up to tmax: a split needs outer * ntok * nsplit <= 152 CTAs
-    if (R / kTile / 4 > 1) b += (size_t)std::min<int64_t>(152, outer * ((tmax + 255) / 256) * (R / kTile / 4)) * 256 * 4;
+    size_t b = round256((size_t)(outer * R * C) * 2) + round256((size_t)(outer * R) * 8);
+    if (R > kTile) b += (size_t)kMaxCtas * 2 * kTile * 4;
     return b;
 }
 
