@@ -195,73 +195,79 @@ attend_tc_kernel(const TcArgs X, const __grid_constant__ CUtensorMap kmap, const
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
     if (warp == 8) {
         // ---- tiles by TMA, in the order the products take them: K0, K1, V0, K2, V1, ...
-        if (lane == 0 && n > 0) {
-            int it = 0;
-            auto load = [&](const CUtensorMap* map, int j) {
-                const int s = it % kSlots;
-                if (it >= kSlots && !tc::wait(&empty[s], ((it / kSlots) - 1) & 1, gone)) return false;
+        int it = 0;
+        auto load = [&](const CUtensorMap* map, int j) {
+            const int s = it % kSlots;
+            if (it >= kSlots && !__all_sync(0xFFFFFFFFu, tc::wait(&empty[s], ((it / kSlots) - 1) & 1, gone))) return false;
+            if (tc::elect()) {
                 mbar_expect_tx(&full[s], S::kTileB);
                 for (int h = 0; h < kHalves; ++h)
                     tma_load_2d(sm + S::kRing + s * S::kTileB + h * (kTile * 128), map, h * 64,
                                 (int)(so * X.Tp) + j * kTile, &full[s]);
-                ++it;
-                return true;
-            };
+            }
+            __syncwarp();
+            ++it;
+            return true;
+        };
+        if (n > 0) {
             bool ok = load(&kmap, j0);
             for (int j = j0; ok && j < j1; ++j) {
                 if (j + 1 < j1) ok = load(&kmap, j + 1);
                 ok = ok && load(&vmap, j);
             }
-            // every copy issued lands before the CTA's shared memory goes
-            for (int i = max(0, it - kSlots); i < it; ++i) tc::drain(&full[i % kSlots], (i / kSlots) & 1);
         }
-    } else if (warp == 9) {
+        // every copy issued lands before the CTA's shared memory goes
+        for (int i = max(0, it - kSlots); i < it; ++i) tc::drain(&full[i % kSlots], (i / kSlots) & 1);
+    } else if (warp == 9 && n > 0) {
         // ---- products
-        if (lane == 0 && n > 0) {
-            constexpr uint32_t kScores = tc::instr_desc(kTile, kTile, false), kValues = tc::instr_desc(kTile, C, true);
-            const uint32_t q_at = smem_u32(sm + S::kQ), ring = smem_u32(sm + S::kRing);
-            auto scores = [&](int t, int s) {
+        constexpr uint32_t kScores = tc::instr_desc(kTile, kTile, false), kValues = tc::instr_desc(kTile, C, true);
+        const uint32_t q_at = smem_u32(sm + S::kQ), ring = smem_u32(sm + S::kRing);
+        auto scores = [&](int t, int s) {
 #pragma unroll
-                for (int k = 0; k < C / 16; ++k) {
-                    const uint32_t at = (k / 4) * (kTile * 128) + (k % 4) * 32;
-                    tc::mma_ss(tmem + t * kTile, tc::smem_desc(q_at + t * S::kTileB + at, 16),
-                               tc::smem_desc(ring + s * S::kTileB + at, 16), kScores, k > 0);
-                }
-                tc::commit(&sfull[t]);
-            };
-            int it = 0;
-            bool ok = tc::wait(&full[0], 0, gone);
-            if (ok) {
-                for (int t = 0; t < nt; ++t) scores(t, 0);
-                tc::commit(&empty[0]);
+            for (int k = 0; k < C / 16; ++k) {
+                const uint32_t at = (k / 4) * (kTile * 128) + (k % 4) * 32;
+                tc::mma_ss(tmem + t * kTile, tc::smem_desc(q_at + t * S::kTileB + at, 16),
+                           tc::smem_desc(ring + s * S::kTileB + at, 16), kScores, k > 0);
             }
-            ++it;
-            for (int j = 0; ok && j < n; ++j) {
-                int ks = -1;
-                if (j + 1 < n) {
-                    ks = it % kSlots;
-                    ok = tc::wait(&full[ks], (it / kSlots) & 1, gone);
-                    ++it;
-                }
-                const int vs = it % kSlots;
-                ok = ok && tc::wait(&full[vs], (it / kSlots) & 1, gone);
+            tc::commit(&sfull[t]);
+        };
+        auto ready = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xFFFFFFFFu, tc::wait(bar, parity, gone)) != 0; };
+        int it = 0;
+        bool ok = ready(&full[0], 0);
+        if (ok && tc::elect()) {
+            for (int t = 0; t < nt; ++t) scores(t, 0);
+            tc::commit(&empty[0]);
+        }
+        __syncwarp();
+        ++it;
+        for (int j = 0; ok && j < n; ++j) {
+            int ks = -1;
+            if (j + 1 < n) {
+                ks = it % kSlots;
+                ok = ready(&full[ks], (it / kSlots) & 1);
                 ++it;
-                for (int t = 0; ok && t < nt; ++t) {
-                    ok = tc::wait(&pfull[t], j & 1, gone);
-                    if (!ok) break;
-                    tc::after_sync();
+            }
+            const int vs = it % kSlots;
+            ok = ok && ready(&full[vs], (it / kSlots) & 1);
+            ++it;
+            for (int t = 0; ok && t < nt; ++t) {
+                ok = ready(&pfull[t], j & 1);
+                if (!ok) break;
+                tc::after_sync();
+                if (tc::elect()) {
 #pragma unroll
                     for (int k = 0; k < kTile / 16; ++k)
                         tc::mma_ts(tmem + 256 + t * C, tmem + t * kTile + k * 8,
                                    tc::smem_desc(ring + vs * S::kTileB + k * 2048, kTile * 128), kValues, j > 0 || k > 0);
                     if (ks >= 0) scores(t, ks);
+                    if (t == nt - 1) {
+                        tc::commit(&empty[vs]);
+                        if (ks >= 0) tc::commit(&empty[ks]);
+                        else tc::commit(odone);
+                    }
                 }
-                if (ok) {
-                    tc::commit(&empty[vs]);
-                    if (ks >= 0) tc::commit(&empty[ks]);
-                }
+                __syncwarp();
             }
-            if (ok) tc::commit(odone);
         }
     }
     } else {

@@ -176,32 +176,34 @@ weights_tc_kernel(const WtArgs A, const __grid_constant__ CUtensorMap qmap)
     const uint32_t tmem = *tmem_slot;
 
     if (warp == 8) {
-        if (lane == 0) {
-            int it = 0;
-            for (; it < n; ++it) {
-                const int s = it % kSlots;
-                if (it >= kSlots && !tc::wait(&empty[s], ((it / kSlots) - 1) & 1, gone)) break;
+        int it = 0;
+        for (; it < n; ++it) {
+            const int s = it % kSlots;
+            if (it >= kSlots && !__all_sync(0xFFFFFFFFu, tc::wait(&empty[s], ((it / kSlots) - 1) & 1, gone))) break;
+            if (tc::elect()) {
                 mbar_expect_tx(&full[s], S::kTileB + kTile * 8);
                 const int64_t row = o * A.R + (int64_t)(n0 + it) * kTile;
                 for (int h = 0; h < kHalves; ++h)
                     tma_load_2d(sm + S::kRing + s * S::kTileB + h * (kTile * 128), &qmap, h * 64, (int)row, &full[s]);
                 bulk_g2s(srow + s * (kTile / 2), A.row + row * 2, kTile * 8, &full[s]);
             }
-            // every copy issued lands before the CTA's shared memory goes
-            for (int i = max(0, it - kSlots); i < it; ++i) tc::drain(&full[i % kSlots], (i / kSlots) & 1);
+            __syncwarp();
         }
+        // every copy issued lands before the CTA's shared memory goes
+        for (int i = max(0, it - kSlots); i < it; ++i) tc::drain(&full[i % kSlots], (i / kSlots) & 1);
     } else if (warp == 9) {
-        if (lane == 0) {
-            constexpr uint32_t kDesc = tc::instr_desc(kTile, kTile, false);
-            const uint32_t k_at = smem_u32(sm + S::kK), ring = smem_u32(sm + S::kRing);
-            bool ok = true;
-            for (int it = 0; ok && it < n; ++it) {
-                const int s = it % kSlots, b = it & 1;
-                ok = tc::wait(&full[s], (it / kSlots) & 1, gone);
-                for (int t = 0; ok && t < 2; ++t) {
-                    if (it >= 2) ok = tc::wait(&dfree[2 * t + b], ((it >> 1) - 1) & 1, gone);
-                    if (!ok) break;
-                    tc::after_sync();
+        constexpr uint32_t kDesc = tc::instr_desc(kTile, kTile, false);
+        const uint32_t k_at = smem_u32(sm + S::kK), ring = smem_u32(sm + S::kRing);
+        auto ready = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xFFFFFFFFu, tc::wait(bar, parity, gone)) != 0; };
+        bool ok = true;
+        for (int it = 0; ok && it < n; ++it) {
+            const int s = it % kSlots, b = it & 1;
+            ok = ready(&full[s], (it / kSlots) & 1);
+            for (int t = 0; ok && t < 2; ++t) {
+                if (it >= 2) ok = ready(&dfree[2 * t + b], ((it >> 1) - 1) & 1);
+                if (!ok) break;
+                tc::after_sync();
+                if (tc::elect()) {
 #pragma unroll
                     for (int k = 0; k < C / 16; ++k) {
                         const uint32_t at = (k / 4) * (kTile * 128) + (k % 4) * 32;
@@ -209,8 +211,9 @@ weights_tc_kernel(const WtArgs A, const __grid_constant__ CUtensorMap qmap)
                                    tc::smem_desc(ring + s * S::kTileB + at, 16), kDesc, k > 0);
                     }
                     tc::commit(&dfull[2 * t + b]);
+                    if (t == 1) tc::commit(&empty[s]);
                 }
-                if (ok) tc::commit(&empty[s]);
+                __syncwarp();
             }
         }
     } else if (warp < 8) {
