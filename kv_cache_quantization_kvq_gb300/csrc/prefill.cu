@@ -10,8 +10,9 @@
 //     whatever lies there (NaN) never reaches a product;
 //  2. attend_tc_kernel, a CTA per (slice, 256 rows, split of the key tiles):
 //     two M = 128 tiles of query rows share every 128-token key and value tile.
-//     Warp 8 loads tiles by TMA into a ring; one thread of warp 9 issues the
-//     products; warps 0-3 and 4-7 are the softmax of the two row tiles, a
+//     Warp 8 loads tiles by TMA into a ring; warps 9 and 10 issue the products of
+//     a row tile each (one warp for both left the tensor cores idle at every
+//     wait: 1.85 ms for the chunk below); warps 0-3 and 4-7 are the softmax of the two row tiles, a
 //     thread per row: S (128 float32 columns of tensor memory) -> registers ->
 //     P in bf16 over the same columns, which the value product reads as its A
 //     operand from tensor memory.  While one tile is in its softmax the tensor
@@ -130,8 +131,8 @@ attend_tc_kernel(const TcArgs X, const __grid_constant__ CUtensorMap kmap, const
     uint64_t* empty = full + kSlots;
     uint64_t* sfull = empty + kSlots;            // [2] scores of a row tile are in tensor memory
     uint64_t* pfull = sfull + 2;                 // [2] its weights are
-    uint64_t* odone = pfull + 2;                 // its output is complete
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(odone + 1);
+    uint64_t* odone = pfull + 2;                 // [2] its output is complete
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(odone + 2);
     volatile int* gone = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
     const ChunkArgs& A = X.A;
@@ -167,13 +168,13 @@ attend_tc_kernel(const TcArgs X, const __grid_constant__ CUtensorMap kmap, const
     if (tid == 0) {
         for (int i = 0; i < kSlots; ++i) {
             mbar_init(&full[i], 1);
-            mbar_init(&empty[i], 1);
+            mbar_init(&empty[i], nt);            // every row tile is done with it
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sfull[i], 1);
             mbar_init(&pfull[i], 4);
+            mbar_init(&odone[i], 1);
         }
-        mbar_init(odone, 1);
         *gone = 0;
         mbar_init_fence();
     }
@@ -218,16 +219,17 @@ attend_tc_kernel(const TcArgs X, const __grid_constant__ CUtensorMap kmap, const
         }
         // every copy issued lands before the CTA's shared memory goes
         for (int i = max(0, it - kSlots); i < it; ++i) tc::drain(&full[i % kSlots], (i / kSlots) & 1);
-    } else if (warp == 9 && n > 0) {
-        // ---- products
+    } else if (warp <= 8 + nt && n > 0) {
+        // ---- products of row tile t
+        const int t = warp - 9;
         constexpr uint32_t kScores = tc::instr_desc(kTile, kTile, false), kValues = tc::instr_desc(kTile, C, true);
-        const uint32_t q_at = smem_u32(sm + S::kQ), ring = smem_u32(sm + S::kRing);
-        auto scores = [&](int t, int s) {
+        const uint32_t q_at = smem_u32(sm + S::kQ) + t * S::kTileB, ring = smem_u32(sm + S::kRing);
+        const uint32_t s_at = tmem + t * kTile, o_at = tmem + 256 + t * C;
+        auto scores = [&](int s) {
 #pragma unroll
             for (int k = 0; k < C / 16; ++k) {
                 const uint32_t at = (k / 4) * (kTile * 128) + (k % 4) * 32;
-                tc::mma_ss(tmem + t * kTile, tc::smem_desc(q_at + t * S::kTileB + at, 16),
-                           tc::smem_desc(ring + s * S::kTileB + at, 16), kScores, k > 0);
+                tc::mma_ss(s_at, tc::smem_desc(q_at + at, 16), tc::smem_desc(ring + s * S::kTileB + at, 16), kScores, k > 0);
             }
             tc::commit(&sfull[t]);
         };
@@ -235,7 +237,7 @@ attend_tc_kernel(const TcArgs X, const __grid_constant__ CUtensorMap kmap, const
         int it = 0;
         bool ok = ready(&full[0], 0);
         if (ok && tc::elect()) {
-            for (int t = 0; t < nt; ++t) scores(t, 0);
+            scores(0);
             tc::commit(&empty[0]);
         }
         __syncwarp();
@@ -248,26 +250,25 @@ attend_tc_kernel(const TcArgs X, const __grid_constant__ CUtensorMap kmap, const
                 ++it;
             }
             const int vs = it % kSlots;
-            ok = ok && ready(&full[vs], (it / kSlots) & 1);
+            ok = ok && ready(&full[vs], (it / kSlots) & 1) && ready(&pfull[t], j & 1);
             ++it;
-            for (int t = 0; ok && t < nt; ++t) {
-                ok = ready(&pfull[t], j & 1);
-                if (!ok) break;
-                tc::after_sync();
-                if (tc::elect()) {
+            if (!ok) break;
+            tc::after_sync();
+            if (tc::elect()) {
 #pragma unroll
-                    for (int k = 0; k < kTile / 16; ++k)
-                        tc::mma_ts(tmem + 256 + t * C, tmem + t * kTile + k * 8,
-                                   tc::smem_desc(ring + vs * S::kTileB + k * 2048, kTile * 128), kValues, j > 0 || k > 0);
-                    if (ks >= 0) scores(t, ks);
-                    if (t == nt - 1) {
-                        tc::commit(&empty[vs]);
-                        if (ks >= 0) tc::commit(&empty[ks]);
-                        else tc::commit(odone);
-                    }
+                for (int k = 0; k < kTile / 16; ++k)
+                    tc::mma_ts(o_at, s_at + k * 8, tc::smem_desc(ring + vs * S::kTileB + k * 2048, kTile * 128), kValues,
+                               j > 0 || k > 0);
+                if (ks >= 0) {
+                    scores(ks);
+                    tc::commit(&empty[vs]);
+                    tc::commit(&empty[ks]);
+                } else {
+                    tc::commit(&empty[vs]);
+                    tc::commit(&odone[t]);
                 }
-                __syncwarp();
             }
+            __syncwarp();
         }
     }
     } else {
@@ -348,7 +349,7 @@ attend_tc_kernel(const TcArgs X, const __grid_constant__ CUtensorMap kmap, const
         // ---- output
         float l = 0.0f;
         if (ok && n > 0) {
-            ok = __all_sync(0xFFFFFFFFu, tc::wait(odone, 0, gone));
+            ok = __all_sync(0xFFFFFFFFu, tc::wait(&odone[t], 0, gone));
             tc::after_sync();
             l = __fadd_rn(lo_of(sum), hi_of(sum));
         }

@@ -10,9 +10,9 @@
 //     gives nothing, so that 2^(x - inf) = 0);
 //  2. weights_tc_kernel, a CTA per (slice, 256 tokens, split of the rows): its
 //     keys are unpacked from the codes into two swizzled M = 128 tiles once;
-//     warp 8 loads tiles of 128 query rows by TMA into a ring, one thread of
-//     warp 9 issues the products into four tensor-memory buffers (two per key
-//     tile), warps 0-3 and 4-7 turn them into sums of 2^(x - lse), 128 columns
+//     warp 8 loads tiles of 128 query rows by TMA into a ring, warps 9
+//     and 10 issue the products of a key tile each into two tensor-memory
+//     buffers, warps 0-3 and 4-7 turn them into sums of 2^(x - lse), 128 columns
 //     a step and a thread.
 //  3. with several splits of the rows, join_kernel adds their sums in order.
 #include <algorithm>
@@ -93,7 +93,7 @@ weights_tc_kernel(const WtArgs A, const __grid_constant__ CUtensorMap qmap)
     unsigned char* sm = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
     float4* srow = reinterpret_cast<float4*>(sm + S::kLse);        // [slot][2][32]: four rows' -lse; their last tokens
     uint64_t* full = reinterpret_cast<uint64_t*>(sm + S::kBars);
-    uint64_t* empty = full + kSlots;             // slot free: products done (1) and lse read (2 x 4 warps)
+    uint64_t* empty = full + kSlots;             // slot free: products done (2) and row data read (2 x 4 warps)
     uint64_t* dfull = empty + kSlots;            // [2 tiles][2 buffers]
     uint64_t* dfree = dfull + 4;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(dfree + 4);
@@ -126,7 +126,7 @@ weights_tc_kernel(const WtArgs A, const __grid_constant__ CUtensorMap qmap)
     if (tid == 0) {
         for (int i = 0; i < kSlots; ++i) {
             mbar_init(&full[i], 1);
-            mbar_init(&empty[i], 9);
+            mbar_init(&empty[i], 10);
         }
         for (int i = 0; i < 4; ++i) {
             mbar_init(&dfull[i], 1);
@@ -191,30 +191,28 @@ weights_tc_kernel(const WtArgs A, const __grid_constant__ CUtensorMap qmap)
         }
         // every copy issued lands before the CTA's shared memory goes
         for (int i = max(0, it - kSlots); i < it; ++i) tc::drain(&full[i % kSlots], (i / kSlots) & 1);
-    } else if (warp == 9) {
+    } else if (warp == 9 || warp == 10) {
+        // ---- products of key tile t
+        const int t = warp - 9;
         constexpr uint32_t kDesc = tc::instr_desc(kTile, kTile, false);
-        const uint32_t k_at = smem_u32(sm + S::kK), ring = smem_u32(sm + S::kRing);
+        const uint32_t k_at = smem_u32(sm + S::kK) + t * S::kTileB, ring = smem_u32(sm + S::kRing);
         auto ready = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xFFFFFFFFu, tc::wait(bar, parity, gone)) != 0; };
-        bool ok = true;
-        for (int it = 0; ok && it < n; ++it) {
+        for (int it = 0; it < n; ++it) {
             const int s = it % kSlots, b = it & 1;
-            ok = ready(&full[s], (it / kSlots) & 1);
-            for (int t = 0; ok && t < 2; ++t) {
-                if (it >= 2) ok = ready(&dfree[2 * t + b], ((it >> 1) - 1) & 1);
-                if (!ok) break;
-                tc::after_sync();
-                if (tc::elect()) {
+            if (!ready(&full[s], (it / kSlots) & 1)) break;
+            if (it >= 2 && !ready(&dfree[2 * t + b], ((it >> 1) - 1) & 1)) break;
+            tc::after_sync();
+            if (tc::elect()) {
 #pragma unroll
-                    for (int k = 0; k < C / 16; ++k) {
-                        const uint32_t at = (k / 4) * (kTile * 128) + (k % 4) * 32;
-                        tc::mma_ss(tmem + (2 * t + b) * kTile, tc::smem_desc(k_at + t * S::kTileB + at, 16),
-                                   tc::smem_desc(ring + s * S::kTileB + at, 16), kDesc, k > 0);
-                    }
-                    tc::commit(&dfull[2 * t + b]);
-                    if (t == 1) tc::commit(&empty[s]);
+                for (int k = 0; k < C / 16; ++k) {
+                    const uint32_t at = (k / 4) * (kTile * 128) + (k % 4) * 32;
+                    tc::mma_ss(tmem + (2 * t + b) * kTile, tc::smem_desc(k_at + at, 16),
+                               tc::smem_desc(ring + s * S::kTileB + at, 16), kDesc, k > 0);
                 }
-                __syncwarp();
+                tc::commit(&dfull[2 * t + b]);
+                tc::commit(&empty[s]);
             }
+            __syncwarp();
         }
     } else if (warp < 8) {
         // ---- a thread per token: sum over the rows of 2^(x - lse)
