@@ -339,53 +339,14 @@ attend_rows_kernel(const ChunkArgs A)
     }
 }
 
-// One warp per query row joins its splits' (y, m, l) in split order.
 template <int C>
 __global__ void __launch_bounds__(kThreads)
 merge_rows_kernel(const ChunkArgs A, int64_t total)
 {
-    const View& a = A.v;
-    const int lane = threadIdx.x & 31;
     const int64_t row = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
     if (row >= total) return;
-    const float* p = A.part + row * A.nsplit * (C + 4);
-    float M = -INFINITY;
-    for (int s = lane; s < A.nsplit; s += 32) M = fmaxf(M, p[(int64_t)s * (C + 4) + C]);
-#pragma unroll
-    for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, x));
-    constexpr int N = C / 32;
-    float L = 0.0f, v[N];
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = 0.0f;
-    if (M != -INFINITY) {
-#pragma unroll 4
-        for (int s = 0; s < A.nsplit; ++s) {
-            const float* ps = p + (int64_t)s * (C + 4);
-            const float2 ml = *reinterpret_cast<const float2*>(ps + C);
-            const float f = ex2(__fsub_rn(ml.x, M));
-            L = __fmaf_rn(ml.y, f, L);
-            float x[N];
-            if constexpr (N == 4) {
-                const float4 t = *reinterpret_cast<const float4*>(ps + 4 * lane);
-                x[0] = t.x; x[1] = t.y; x[2] = t.z; x[3] = t.w;
-            } else {
-                const float2 t = *reinterpret_cast<const float2*>(ps + 2 * lane);
-                x[0] = t.x; x[1] = t.y;
-            }
-#pragma unroll
-            for (int i = 0; i < N; ++i) v[i] = __fmaf_rn(x[i], f, v[i]);
-        }
-    }
-    const int64_t o = row / a.rows;
-    const int64_t at = row_index(a, o, (int)(row - o * a.rows));
-    const float inv = L > 0.0f ? __fdiv_rn(1.0f, L) : 0.0f;
-    uint32_t w[N / 2];
-#pragma unroll
-    for (int i = 0; i < N / 2; ++i) w[i] = pack_bf16x2(__fmul_rn(v[2 * i], inv), __fmul_rn(v[2 * i + 1], inv));
-    if constexpr (N == 4) *reinterpret_cast<uint2*>(A.out + at * C + 4 * lane) = make_uint2(w[0], w[1]);
-    else *reinterpret_cast<uint32_t*>(A.out + at * C + 2 * lane) = w[0];
-    if (A.lse && lane == 0)
-        A.lse[at] = L > 0.0f ? __fmul_rn(__fadd_rn(M, log2f(L)), 0.6931471805599453f) : -INFINITY;
+    const int64_t o = row / A.v.rows;
+    merge_row<C>(A, o, (int)(row - o * A.v.rows), A.part + row * A.nsplit * (C + 4), threadIdx.x & 31);
 }
 
 constexpr int64_t kSlots = 152 * 2;              // resident CTAs (two per SM)
@@ -405,19 +366,14 @@ cudaError_t launch_rows(const ChunkArgs& A, int64_t outer, cudaStream_t st)
     const int64_t grid = outer * A.ntiles * A.nsplit;
     if (grid > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
     attend_rows_kernel<BITS, C><<<(unsigned)grid, kThreads, 0, st>>>(A);
-    if (A.nsplit > 1) launch_merge_rows(A, outer, C, st);
+    if (A.nsplit > 1) {
+        const int64_t total = outer * A.v.rows;
+        merge_rows_kernel<C><<<(unsigned)((total + kWarps - 1) / kWarps), kThreads, 0, st>>>(A, total);
+    }
     return cudaGetLastError();
 }
 
 }  // namespace
-
-void launch_merge_rows(const ChunkArgs& A, int64_t outer, int64_t C, cudaStream_t st)
-{
-    const int64_t total = outer * A.v.rows;
-    const unsigned grid = (unsigned)((total + kWarps - 1) / kWarps);
-    if (C == 128) merge_rows_kernel<128><<<grid, kThreads, 0, st>>>(A, total);
-    else merge_rows_kernel<64><<<grid, kThreads, 0, st>>>(A, total);
-}
 
 size_t chunk_workspace(int64_t outer, int64_t C, int64_t tmax, int64_t n, int64_t group)
 {
