@@ -12,8 +12,8 @@
 //     keys are unpacked from the codes into two swizzled M = 128 tiles once;
 //     warp 8 loads tiles of 128 query rows by TMA into a ring, warps 9
 //     and 10 issue the products of a key tile each into two tensor-memory
-//     buffers, warps 0-3 and 4-7 turn them into sums of 2^(x - lse), 128 columns
-//     a step and a thread.
+//     buffers, four groups of four warps, one per buffer, turn them into sums
+//     of 2^(x - lse), a token per thread.
 //  3. with several splits of the rows, join_kernel adds their sums in order.
 #include <algorithm>
 
@@ -31,7 +31,8 @@ namespace {
 using namespace rows;
 
 constexpr int kTile = 128;
-constexpr int kThreadsW = 384;
+constexpr int kSumWarps = 16;                    // four per scheduler: one warp's exponentials cover another's loads
+constexpr int kThreadsW = (kSumWarps + 4) * 32;
 
 struct WtArgs {
     View v;
@@ -89,6 +90,7 @@ weights_tc_kernel(const WtArgs A, const __grid_constant__ CUtensorMap qmap)
     using S = SmemW<C>;
     using W = typename CodeWord<BITS>::T;
     constexpr int kSlots = S::kSlots, kHalves = C / 64, P = C / 8;
+    __shared__ float half_sum[2][2 * kTile];
     extern __shared__ unsigned char raw[];
     unsigned char* sm = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
     float4* srow = reinterpret_cast<float4*>(sm + S::kLse);        // [slot][2][32]: four rows' -lse; their last tokens
@@ -135,7 +137,7 @@ weights_tc_kernel(const WtArgs A, const __grid_constant__ CUtensorMap qmap)
         *gone = 0;
         mbar_init_fence();
     }
-    if (warp == 9) tc::alloc(tmem_slot, 512);
+    if (warp == kSumWarps + 1) tc::alloc(tmem_slot, 512);
     // ---- the keys: row = token, 16-byte pieces of 8 channels; hidden tokens are zeros
     if (n > 0) {
 #pragma unroll 4
@@ -175,7 +177,7 @@ weights_tc_kernel(const WtArgs A, const __grid_constant__ CUtensorMap qmap)
     tc::after_sync();
     const uint32_t tmem = *tmem_slot;
 
-    if (warp == 8) {
+    if (warp == kSumWarps) {
         int it = 0;
         for (; it < n; ++it) {
             const int s = it % kSlots;
@@ -191,9 +193,9 @@ weights_tc_kernel(const WtArgs A, const __grid_constant__ CUtensorMap qmap)
         }
         // every copy issued lands before the CTA's shared memory goes
         for (int i = max(0, it - kSlots); i < it; ++i) tc::drain(&full[i % kSlots], (i / kSlots) & 1);
-    } else if (warp == 9 || warp == 10) {
+    } else if (warp == kSumWarps + 1 || warp == kSumWarps + 2) {
         // ---- products of key tile t
-        const int t = warp - 9;
+        const int t = warp - kSumWarps - 1;
         constexpr uint32_t kDesc = tc::instr_desc(kTile, kTile, false);
         const uint32_t k_at = smem_u32(sm + S::kK) + t * S::kTileB, ring = smem_u32(sm + S::kRing);
         auto ready = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xFFFFFFFFu, tc::wait(bar, parity, gone)) != 0; };
@@ -214,34 +216,29 @@ weights_tc_kernel(const WtArgs A, const __grid_constant__ CUtensorMap qmap)
             }
             __syncwarp();
         }
-    } else if (warp < 8) {
-        // ---- a thread per token: sum over the rows of 2^(x - lse)
-        const int t = warp / 4;
+    } else if (warp < kSumWarps) {
+        // ---- a thread per token of tile t and buffer b (every second row tile): sum of 2^(x - lse)
+        const int t = (warp >> 2) & 1, b = warp >> 3;
         const int tok = t0 + t * kTile + (warp & 3) * 32 + lane;
         const int tile_hi = t0 + t * kTile + kTile - 1;
-        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t d_at = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (2 * t + b) * kTile;
         const u64 sc2 = pk(a.scale2, a.scale2);
         float sum = 0.0f;
-        bool ok = true;
-        for (int it = 0; ok && it < n; ++it) {
-            const int s = it % kSlots, b = it & 1;
-            ok = tc::wait(&full[s], (it / kSlots) & 1, gone) && tc::wait(&dfull[2 * t + b], (it >> 1) & 1, gone);
-            ok = __all_sync(0xFFFFFFFFu, ok);
-            if (!ok) break;
+        for (int it = b; it < n; it += 2) {
+            const int s = it % kSlots;
+            bool ok = tc::wait(&full[s], (it / kSlots) & 1, gone) && tc::wait(&dfull[2 * t + b], (it >> 1) & 1, gone);
+            if (!__all_sync(0xFFFFFFFFu, ok)) break;
             tc::after_sync();
-            const uint32_t d_at = tmem + lanes + (2 * t + b) * kTile;
             const int row0 = (n0 + it) * kTile;
             const bool cut = tile_hi > base + row0 / a.group;       // some row does not see some token
             const float4* rp = srow + s * (kTile / 2);
             u64 acc0 = 0, acc1 = 0;
             if (!cut) {
-                uint32_t x[2][32];               // the next 32 columns load while these are summed
-                tc::ld32(d_at, x[0]);
 #pragma unroll
                 for (int h = 0; h < 4; ++h) {
+                    uint32_t y[32];
+                    tc::ld32(d_at + 32 * h, y);
                     tc::wait_ld();
-                    if (h < 3) tc::ld32(d_at + 32 * (h + 1), x[(h + 1) & 1]);
-                    const uint32_t* y = x[h & 1];
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         const float4 l = rp[8 * h + i];
@@ -278,21 +275,23 @@ weights_tc_kernel(const WtArgs A, const __grid_constant__ CUtensorMap qmap)
             const u64 acc = add2(acc0, acc1);
             sum = __fadd_rn(sum, __fadd_rn(lo_of(acc), hi_of(acc)));
         }
-        if (tok < a.T && ok) {
-            if (tok < first) sum = 0.0f;
-            if (A.nsplit > 1) {
-                A.part[(o * A.nsplit + split) * ((int64_t)A.ntok * 2 * kTile) + tok] = sum;
-            } else {
-                const int64_t at = o * A.stride + tok;
-                A.out[at] = A.in ? __fadd_rn(A.in[at], sum) : sum;
-            }
-        }
+        half_sum[b][t * kTile + (warp & 3) * 32 + lane] = sum;
     }
     __syncwarp();
     tc::before_sync();
     __syncthreads();
     tc::after_sync();
-    if (warp == 9) tc::dealloc(tmem, 512);
+    if (warp == kSumWarps + 1) tc::dealloc(tmem, 512);
+    if (tid < 2 * kTile && t0 + tid < a.T && !*gone) {
+        const int tok = t0 + tid;
+        const float sum = tok < first ? 0.0f : __fadd_rn(half_sum[0][tid], half_sum[1][tid]);
+        if (A.nsplit > 1) {
+            A.part[(o * A.nsplit + split) * ((int64_t)A.ntok * 2 * kTile) + tok] = sum;
+        } else {
+            const int64_t at = o * A.stride + tok;
+            A.out[at] = A.in ? __fadd_rn(A.in[at], sum) : sum;
+        }
+    }
 }
 
 __global__ void __launch_bounds__(256)
