@@ -13,10 +13,15 @@
 // probabilities never leave registers, and the keys and values go from packed
 // codes to B fragments in registers (kvq_rows.cuh).
 //
-// attend_rows_kernel: a CTA takes (slice, row tile, split of the visible
-// batches); its four warps walk the split's 32-token batches in turn, each with
-// its own m, l, y, merged through shared memory at the end.  With one split the
-// CTA writes out and lse; otherwise merge_rows_kernel joins the splits' partial
+// attend_rows_kernel: a CTA takes (slice, tile of 16 MT query rows, split of
+// the visible batches); each of its four warps walks its run of the split's
+// 32-token batches with its own m, l, y, merged through shared memory at the
+// end.  The query fragments and the key group's constants stay in shared memory
+// (12 warps a SM instead of 8), the next batch's codes are loaded as soon as the
+// current ones are used.  m is moved only when it grows by more than 2^8: until
+// then the weights are at most 256, which costs float32 sums and bf16 weights no
+// relative precision, and the output is seldom rescaled.  With one split the CTA
+// writes out and lse; otherwise merge_rows_kernel joins the splits' partial
 // (m, l, y) in split order.
 #include <algorithm>
 
@@ -30,19 +35,23 @@ using namespace rows;
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kRowTile = 16;
+constexpr float kSlack = 8.0f;                   // base-2 growth of the maximum that is let pass
 
 // P.V of one 32-token batch of the store: this lane's code words of its eight
-// tokens (w[2 ks + e / 2][...], tokens 16 ks + {2 tig, 2 tig + 1, 8 + 2 tig,
-// 9 + 2 tig}), their scale pairs and zero pairs.
-template <int BITS, int C, bool FAST>
-__device__ __forceinline__ void values_of(float (&y)[C / 8][4], const uint32_t (&p)[2][4],
-                                          const uint32_t (&w)[8][Geo<BITS, C>::kVW], const uint32_t (&s)[4],
-                                          const uint32_t (&z)[4], float off) {
+// tokens, 16 ks + {2 tig, 2 tig + 1, 8 + 2 tig, 9 + 2 tig}; vm: (scale, zero
+// point) of each token and V group.
+template <int BITS, int C, int MT, bool FAST>
+__device__ __forceinline__ void values_of(float (&y)[MT][C / 8][4], const uint4 (&p)[MT][2],
+                                          const uint32_t (&w)[8][Geo<BITS, C>::kVW], const uint32_t* vm, uint32_t mg,
+                                          float off, int tig) {
     using G = Geo<BITS, C>;
     constexpr int FH = 16 / BITS;                // fields of a half word: n-tiles per half
 #pragma unroll
-    for (int ks = 0; ks < 2; ++ks)
+    for (int ks = 0; ks < 2; ++ks) {
+        const uint2 m0 = *reinterpret_cast<const uint2*>(vm + 16 * ks + 2 * tig);
+        const uint2 m1 = *reinterpret_cast<const uint2*>(vm + 16 * ks + 8 + 2 * tig);
+        const uint32_t s0 = __byte_perm(m0.x, m0.y, 0x5410), z0 = __byte_perm(m0.x, m0.y, 0x7632);
+        const uint32_t s1 = __byte_perm(m1.x, m1.y, 0x5410), z1 = __byte_perm(m1.x, m1.y, 0x7632);
 #pragma unroll
         for (int h = 0; h < G::kVB / 2; ++h) {
             const uint32_t sel = (h & 1) ? 0x7632 : 0x5410;
@@ -50,291 +59,324 @@ __device__ __forceinline__ void values_of(float (&y)[C / 8][4], const uint32_t (
             const uint32_t x1 = __byte_perm(w[4 * ks + 2][h / 2], w[4 * ks + 3][h / 2], sel);
 #pragma unroll
             for (int i = 0; i < FH; ++i) {
-                const uint32_t b0 = value_pair<BITS, FAST>(x0, BITS * i, s[2 * ks], z[2 * ks], off);
-                const uint32_t b1 = value_pair<BITS, FAST>(x1, BITS * i, s[2 * ks + 1], z[2 * ks + 1], off);
-                mma16816(y[h * FH + i], p[ks], b0, b1);
+                const uint32_t b0 = value_pair<BITS, FAST>(x0, BITS * i, mg, s0, z0, off);
+                const uint32_t b1 = value_pair<BITS, FAST>(x1, BITS * i, mg, s1, z1, off);
+#pragma unroll
+                for (int m = 0; m < MT; ++m) mma16816(y[m][h * FH + i], p[m][ks], b0, b1);
             }
         }
+    }
 }
 
-template <int BITS, int C>
-__global__ void __launch_bounds__(kThreads, 2)
+// Softmax state of a lane's rows (g and g + 8 of each tile).
+template <int MT>
+struct Running { float m[MT][2], l[MT][2]; };
+
+// Masks (unless `whole`), moves the maximum if it must, and turns scores into
+// the weights' A fragments.
+template <int C, int MT>
+__device__ __forceinline__ void softmax_of(const View& a, float (&s)[MT][4][4], float (&y)[MT][C / 8][4], Running<MT>& st,
+                                           uint4 (&p)[MT][2], bool whole, int t0, int t1, int first,
+                                           const int (&last)[MT][2], int tig) {
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+        if (!whole) {
+            // selected, not multiplied: a hidden token's score may be NaN
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int t = t0 + 8 * j + 2 * tig + (e & 1);
+                    if (t < first || t >= t1 || t > last[m][e >> 1]) s[m][j][e] = -INFINITY;
+                }
+        }
+        float top[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            float x = fmaxf(fmaxf(fmaxf(s[m][0][2 * h], s[m][0][2 * h + 1]), fmaxf(s[m][1][2 * h], s[m][1][2 * h + 1])),
+                            fmaxf(fmaxf(s[m][2][2 * h], s[m][2][2 * h + 1]), fmaxf(s[m][3][2 * h], s[m][3][2 * h + 1])));
+            x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 1));
+            x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 2));
+            top[h] = __fmul_rn(x, a.scale2);
+        }
+        const bool grow[2] = {top[0] > __fadd_rn(st.m[m][0], kSlack), top[1] > __fadd_rn(st.m[m][1], kSlack)};
+        if (__any_sync(0xFFFFFFFFu, grow[0] || grow[1])) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float f = grow[h] ? ex2(__fsub_rn(st.m[m][h], top[h])) : 1.0f;
+                if (grow[h]) st.m[m][h] = top[h];
+                st.l[m][h] = __fmul_rn(st.l[m][h], f);
+#pragma unroll
+                for (int nt = 0; nt < C / 8; ++nt) {
+                    y[m][nt][2 * h] = __fmul_rn(y[m][nt][2 * h], f);
+                    y[m][nt][2 * h + 1] = __fmul_rn(y[m][nt][2 * h + 1], f);
+                }
+            }
+        }
+        const float neg[2] = {st.m[m][0] == -INFINITY ? 0.0f : -st.m[m][0], st.m[m][1] == -INFINITY ? 0.0f : -st.m[m][1]};
+        uint32_t w[4][2];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float e0 = ex2(__fmaf_rn(s[m][j][2 * h], a.scale2, neg[h]));
+                const float e1 = ex2(__fmaf_rn(s[m][j][2 * h + 1], a.scale2, neg[h]));
+                st.l[m][h] = __fadd_rn(st.l[m][h], __fadd_rn(e0, e1));
+                w[j][h] = pack_bf16x2(e0, e1);
+            }
+        p[m][0] = make_uint4(w[0][0], w[0][1], w[1][0], w[1][1]);
+        p[m][1] = make_uint4(w[2][0], w[2][1], w[3][0], w[3][1]);
+    }
+}
+
+template <int BITS, int C, int MT>
+__global__ void __launch_bounds__(kThreads, MT == 1 ? 3 : 2)
 attend_rows_kernel(const ChunkArgs A)
 {
     using G = Geo<BITS, C>;
+    constexpr int kRowTile = 16 * MT;
     const View& a = A.v;
-    __shared__ float sm[kWarps][kRowTile], sl[kWarps][kRowTile];
-    __shared__ __align__(16) float sy[kWarps][kRowTile][C];
+    __shared__ float sm[kWarps][16], sl[kWarps][16];
+    __shared__ __align__(16) float sy[kWarps][16][C];
+    __shared__ __align__(16) uint4 qf[MT * G::kSteps * 32];
+    __shared__ __align__(16) uint4 kcs[kWarps][C / 4];
+    __shared__ __align__(16) uint32_t vms[kWarps][4][kBatch];
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, tig = lane & 3;
-    int64_t blk = blockIdx.x;
-    const int split = (int)(blk % A.nsplit);
-    blk /= A.nsplit;
-    const int tile = (int)(blk % A.ntiles);
-    const int64_t o = blk / A.ntiles;
+    uint32_t blk = blockIdx.x;
+    const int split = (int)(blk % (uint32_t)A.nsplit);
+    blk /= (uint32_t)A.nsplit;
+    const int tile = (int)(blk % (uint32_t)A.ntiles);
+    const int64_t o = blk / (uint32_t)A.ntiles;
     const int r0 = tile * kRowTile;
+    stage_queries<BITS, C, MT>(a, o, r0, qf, tid, kThreads);
 
-    // ---- this lane's two query rows and the last token each sees
-    const int ra = r0 + g, rb = r0 + g + 8;
-    uint32_t qa[C / 8], qb[C / 8];
-#pragma unroll
-    for (int p = 0; p < C / 8; ++p) qa[p] = qb[p] = 0u;
-    if (ra < a.rows) load_pairs<BITS, C>(a.q + row_index(a, o, ra) * C + tig * (C / 4), qa);
-    if (rb < a.rows) load_pairs<BITS, C>(a.q + row_index(a, o, rb) * C + tig * (C / 4), qb);
+    // ---- the last token each of this lane's rows sees
     const int base = a.T - a.n;                  // token of query 0
-    const int last_a = base + ra / a.group, last_b = base + rb / a.group;      // rows past the last are not written
+    int last[MT][2];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {               // rows past the last are not written
+        last[m][0] = base + (r0 + 16 * m + g) / a.group;
+        last[m][1] = base + (r0 + 16 * m + g + 8) / a.group;
+    }
     const int last_hi = base + (min(r0 + kRowTile, a.rows) - 1) / a.group;     // of the tile's rows
     const int last_lo = base + r0 / a.group;
     const int first = a.first ? max(a.first[o], 0) : 0;
 
-    // ---- the visible batches, cut into splits
+    // ---- the visible batches, cut into splits, and a run of the split for each warp
     const Span sp = span_of(a);
     int b0 = 0, b1 = 0;
     if (first <= last_hi) {                      // first <= last_hi < T
         b0 = batch_of(a, sp, first);
         b1 = batch_of(a, sp, last_hi) + 1;
     }
-    const int64_t len = b1 - b0;
-    const int e1 = b0 + (int)(len * (split + 1) / A.nsplit);
-    b0 += (int)(len * split / A.nsplit);
-    b1 = e1;
+    {
+        const int64_t len = b1 - b0;
+        const int k = split * kWarps + warp, of = A.nsplit * kWarps;
+        b1 = b0 + (int)(len * (k + 1) / of);
+        b0 += (int)(len * k / of);
+    }
+    const int bs = min(b1, sp.nsb);              // the run's store batches: [b0, bs)
 
-    float y[C / 8][4];
+    float y[MT][C / 8][4];
+    Running<MT> st;
 #pragma unroll
-    for (int nt = 0; nt < C / 8; ++nt) y[nt][0] = y[nt][1] = y[nt][2] = y[nt][3] = 0.0f;
-    float ma = -INFINITY, mb = -INFINITY, la = 0.0f, lb = 0.0f;
-    uint32_t ks[C / 8], kz[C / 8];
-    int cur = -1;
-    bool kfast = true;
-
+    for (int m = 0; m < MT; ++m) {
+#pragma unroll
+        for (int nt = 0; nt < C / 8; ++nt) y[m][nt][0] = y[m][nt][1] = y[m][nt][2] = y[m][nt][3] = 0.0f;
+        st.m[m][0] = st.m[m][1] = -INFINITY;
+        st.l[m][0] = st.l[m][1] = 0.0f;
+    }
     const uint8_t* kc = a.kc + (uint64_t)o * a.cap * G::kRowB + tig * (G::kRowB / 4);
     const uint8_t* vc = a.vc + (uint64_t)o * a.cap * G::kRowB + g * G::kVB;
-    const int vg = g * (C / 8) / a.gv;           // this lane's V group (its C/8 channels lie in one)
+    const int64_t vmeta = o * a.cap * a.ngv;
+    const uint32_t kmg = magic<BITS>(a.kflip), vmg = magic<BITS>(a.vflip);
+    const uint32_t* vm = &vms[warp][g * (C / 8) / a.gv][0];         // this lane's V group (its C/8 channels lie in one)
 
-    for (int b = b0 + warp; b < b1; b += kWarps) {
+    // a batch's codes: whole batches at fixed offsets, the store's last one clamped to its tokens
+    uint32_t kw[4][G::kWpl], vw[8][G::kVW];
+    auto load_k = [&](int b) {
+        const uint8_t* p = kc + (int64_t)b * (kBatch * G::kRowB);
+        const int cnt = a.tq - b * kBatch - 1;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) load_words<G::kWpl>(p + min(8 * j + g, cnt) * G::kRowB, kw[j]);
+    };
+    auto load_v = [&](int b) {
+        const uint8_t* p = vc + (int64_t)b * (kBatch * G::kRowB);
+        const int cnt = a.tq - b * kBatch - 1;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const uint8_t* at = p + min(8 * (k >> 1) + 2 * tig + (k & 1), cnt) * G::kRowB;
+            if constexpr (G::kVB >= 4) load_words<G::kVW>(at, vw[k]);
+            else vw[k][0] = __ldcs(reinterpret_cast<const uint16_t*>(at));
+        }
+    };
+    // (scale, zero point) of token `lane` of a batch, a word per V group; hidden tokens get
+    // zeros, since theirs may be NaN
+    uint32_t vr[4];
+    auto load_vm = [&](int b) {
+        const int t = b * kBatch + lane;
+        const int64_t at = vmeta + (int64_t)t * a.ngv;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            vr[k] = 0u;
+            if (k < a.ngv && t >= first && t < a.tq)
+                vr[k] = bits_of(a.vs + at + k) | (a.vz ? bits_of(a.vz + at + k) << 16 : 0u);
+        }
+    };
+    KRaw kr = {0u, 0u, 0u, 0u};
+    int staged = -1, fetched = -1;
+    bool kfast = true;
+    if (b0 < bs) {
+        fetched = b0 * kBatch / a.gk;
+        load_k(b0);
+        kr = fetch_k_group<BITS, C>(a, o, fetched, lane);
+        load_vm(b0);
+        load_v(b0);
+    }
+    __syncthreads();                             // the queries are staged
+
+    for (int b = b0; b < bs; ++b) {
+        const int t0 = b * kBatch, t1 = min(t0 + kBatch, a.tq);
+        if (fetched != staged) {
+            kfast = stage_k_group(kr, a.koff, a.kz != nullptr, kcs[warp], lane, C / 4);
+            staged = fetched;
+        }
+        // the V constants of this batch
+        bool vfast = true;
+        if (a.vz) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) vfast = vfast && zero_exact(bf_hi(vr[k]));
+            vfast = __all_sync(0xFFFFFFFFu, vfast);
+        }
+        __syncwarp();                            // the batch before has been read
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (k < a.ngv) vms[warp][k][lane] = vfast ? (vr[k] & 0xFFFFu) | (biased(vr[k], 128.0f + a.voff) & 0xFFFF0000u) : vr[k];
+        __syncwarp();
+
+        float s[MT][4][4];
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s[m][j][0] = s[m][j][1] = s[m][j][2] = s[m][j][3] = 0.0f;
+        if (kfast) scores_of<BITS, C, MT, true>(s, kw, qf, kcs[warp], kmg, a.koff, lane);
+        else scores_of<BITS, C, MT, false>(s, kw, qf, kcs[warp], kmg, a.koff, lane);
+        if (b + 1 < bs) {
+            load_k(b + 1);
+            const int gk = (b + 1) * kBatch / a.gk;
+            if (gk != fetched) {
+                fetched = gk;
+                kr = fetch_k_group<BITS, C>(a, o, gk, lane);
+            }
+            load_vm(b + 1);
+        }
+        uint4 p[MT][2];
+        const bool whole = t0 >= first && t1 - t0 == kBatch && t1 - 1 <= last_lo;
+        softmax_of<C, MT>(a, s, y, st, p, whole, t0, t1, first, last, tig);
+        if (vfast) values_of<BITS, C, MT, true>(y, p, vw, vm, vmg, a.voff, tig);
+        else values_of<BITS, C, MT, false>(y, p, vw, vm, vmg, a.voff, tig);
+        if (b + 1 < bs) load_v(b + 1);
+    }
+
+    // ---- the run's buffer batches: bf16 rows
+    for (int b = max(b0, sp.nsb); b < b1; ++b) {
         int t0, t1;
         batch_at(a, sp, b, t0, t1);
-        const bool store = b < sp.nsb;
+        const __nv_bfloat16* krow[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            krow[j] = a.kr + ((uint64_t)o * a.rrows + (min(t0 + 8 * j + g, t1 - 1) - a.tq)) * C + tig * (C / 4);
+        float s[MT][4][4];
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s[m][j][0] = s[m][j][1] = s[m][j][2] = s[m][j][3] = 0.0f;
+        scores_of_rows<BITS, C, MT>(s, krow, qf, lane);
+        uint4 p[MT][2];
         const bool whole = t0 >= first && t1 - t0 == kBatch && t1 - 1 <= last_lo;
-
-        // ---- scores: n-tile j, token t0 + 8 j + {2 tig, 2 tig + 1}
-        float s[4][4];
-        if (store) {
-            uint32_t kw[4][G::kWpl];
+        softmax_of<C, MT>(a, s, y, st, p, whole, t0, t1, first, last, tig);
+        // this lane's C/8 channels of its tokens, paired by token
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int t = min(t0 + 8 * j + g, t1 - 1);
-                load_words<G::kWpl>(kc + (int64_t)t * G::kRowB, kw[j]);
+        for (int ks = 0; ks < 2; ++ks) {
+            uint32_t r[4][C / 16];
 #pragma unroll
-                for (int i = 0; i < G::kWpl; ++i) kw[j][i] ^= a.kflip;
-            }
-            const int gk = t0 / a.gk;
-            if (gk != cur) {
-                cur = gk;
-                kfast = load_k_group<BITS, C>(a, o, gk, tig, ks, kz);
-            }
+            for (int e = 0; e < 4; ++e) {
+                const int t = t0 + 16 * ks + 8 * (e >> 1) + 2 * tig + (e & 1);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                uint32_t kb[C / 8];
-                if (kfast) keys_of<BITS, C, true>(kw[j], ks, kz, a.koff, kb);
-                else keys_of<BITS, C, false>(kw[j], ks, kz, a.koff, kb);
-                s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.0f;
-#pragma unroll
-                for (int kk = 0; kk < G::kSteps; ++kk) {
-                    const uint32_t qf[4] = {qa[2 * kk], qb[2 * kk], qa[2 * kk + 1], qb[2 * kk + 1]};
-                    mma16816(s[j], qf, kb[2 * kk], kb[2 * kk + 1]);
+                for (int i = 0; i < C / 64; ++i) {
+                    uint4 x = make_uint4(0, 0, 0, 0);
+                    if (t >= first && t < t1)
+                        x = reinterpret_cast<const uint4*>(a.vr + ((uint64_t)o * a.rrows + (t - a.tq)) * C + g * (C / 8))[i];
+                    r[e][4 * i] = x.x; r[e][4 * i + 1] = x.y; r[e][4 * i + 2] = x.z; r[e][4 * i + 3] = x.w;
                 }
             }
-        } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int t = min(t0 + 8 * j + g, t1 - 1) - a.tq;
-                uint32_t kb[C / 8];
-                load_pairs<BITS, C>(a.kr + ((uint64_t)o * a.rrows + t) * C + tig * (C / 4), kb);
-                s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.0f;
-#pragma unroll
-                for (int kk = 0; kk < G::kSteps; ++kk) {
-                    const uint32_t qf[4] = {qa[2 * kk], qb[2 * kk], qa[2 * kk + 1], qb[2 * kk + 1]};
-                    mma16816(s[j], qf, kb[2 * kk], kb[2 * kk + 1]);
-                }
-            }
-        }
-        if (!whole) {
-            // selected, not multiplied: a hidden token's score may be NaN
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int t = t0 + 8 * j + 2 * tig + e;
-                    const bool live = t >= first && t < t1;
-                    if (!live || t > last_a) s[j][e] = -INFINITY;
-                    if (!live || t > last_b) s[j][2 + e] = -INFINITY;
-                }
-        }
-
-        // ---- running maximum and sum (the four lanes of a quad share a row)
-        float na = fmaxf(fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1])),
-                         fmaxf(fmaxf(s[2][0], s[2][1]), fmaxf(s[3][0], s[3][1])));
-        float nb = fmaxf(fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3])),
-                         fmaxf(fmaxf(s[2][2], s[2][3]), fmaxf(s[3][2], s[3][3])));
-        na = fmaxf(na, __shfl_xor_sync(0xFFFFFFFFu, na, 1));
-        nb = fmaxf(nb, __shfl_xor_sync(0xFFFFFFFFu, nb, 1));
-        na = fmaxf(na, __shfl_xor_sync(0xFFFFFFFFu, na, 2));
-        nb = fmaxf(nb, __shfl_xor_sync(0xFFFFFFFFu, nb, 2));
-        na = fmaxf(ma, __fmul_rn(na, a.scale2));
-        nb = fmaxf(mb, __fmul_rn(nb, a.scale2));
-        if (__any_sync(0xFFFFFFFFu, na != ma || nb != mb)) {
-            const float fa = na == -INFINITY ? 1.0f : ex2(__fsub_rn(ma, na));
-            const float fb = nb == -INFINITY ? 1.0f : ex2(__fsub_rn(mb, nb));
-            la = __fmul_rn(la, fa);
-            lb = __fmul_rn(lb, fb);
 #pragma unroll
             for (int nt = 0; nt < C / 8; ++nt) {
-                y[nt][0] = __fmul_rn(y[nt][0], fa);
-                y[nt][1] = __fmul_rn(y[nt][1], fa);
-                y[nt][2] = __fmul_rn(y[nt][2], fb);
-                y[nt][3] = __fmul_rn(y[nt][3], fb);
-            }
-            ma = na;
-            mb = nb;
-        }
-        const float xa = ma == -INFINITY ? 0.0f : -ma, xb = mb == -INFINITY ? 0.0f : -mb;
-        uint32_t p[2][4];
+                const uint32_t sel = (nt & 1) ? 0x7632 : 0x5410;
+                const uint32_t v0 = __byte_perm(r[0][nt / 2], r[1][nt / 2], sel);
+                const uint32_t v1 = __byte_perm(r[2][nt / 2], r[3][nt / 2], sel);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                s[j][e] = ex2(__fmaf_rn(s[j][e], a.scale2, xa));
-                s[j][2 + e] = ex2(__fmaf_rn(s[j][2 + e], a.scale2, xb));
-                la = __fadd_rn(la, s[j][e]);
-                lb = __fadd_rn(lb, s[j][2 + e]);
+                for (int m = 0; m < MT; ++m) mma16816(y[m][nt], p[m][ks], v0, v1);
             }
-            p[j / 2][2 * (j & 1)] = pack_bf16x2(s[j][0], s[j][1]);
-            p[j / 2][2 * (j & 1) + 1] = pack_bf16x2(s[j][2], s[j][3]);
         }
+    }
 
-        // ---- values: tokens t0 + 16 ks + {2 tig, 2 tig + 1, 8 + 2 tig, 9 + 2 tig}
-        if (store) {
-            uint32_t vw[8][G::kVW], vs[4], vz[4];
-            bool vfast = true;
+    // ---- merge the warps, a row tile at a time; channel of (nt, column e of lane tig) = (2 tig + e) C/8 + nt
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {        // pairs of tokens
-                const int tp = t0 + 8 * k + 2 * tig;
-                uint32_t sb[2], zb[2];
+    for (int m = 0; m < MT; ++m) {
+        if (m > 0) __syncthreads();
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int t = min(tp + e, t1 - 1);
-                    const bool dead = tp + e < first || tp + e >= t1;     // its scale may be NaN
-                    if constexpr (G::kVB >= 4) {
-                        load_words<G::kVW>(vc + (int64_t)t * G::kRowB, vw[2 * k + e]);
-                        vw[2 * k + e][0] ^= a.vflip;
-                        if constexpr (G::kVW == 2) vw[2 * k + e][1] ^= a.vflip;
-                    } else {
-                        vw[2 * k + e][0] = __ldcs(reinterpret_cast<const uint16_t*>(vc + (int64_t)t * G::kRowB)) ^
-                                           (a.vflip & 0xFFFFu);
-                    }
-                    const int64_t at = (o * a.cap + t) * a.ngv + vg;
-                    sb[e] = dead ? 0u : bits_of(a.vs + at);
-                    zb[e] = dead || !a.vz ? 0u : bits_of(a.vz + at);
-                }
-                vs[k] = sb[0] | (sb[1] << 16);
-                vz[k] = zb[0] | (zb[1] << 16);
-                vfast = vfast && zero_exact(bf_lo(vz[k])) && zero_exact(bf_hi(vz[k]));
+        for (int h = 0; h < 2; ++h) {
+            float l = st.l[m][h];
+            l = __fadd_rn(l, __shfl_xor_sync(0xFFFFFFFFu, l, 1));
+            l = __fadd_rn(l, __shfl_xor_sync(0xFFFFFFFFu, l, 2));
+            if (tig == 0) {
+                sm[warp][g + 8 * h] = st.m[m][h];
+                sl[warp][g + 8 * h] = l;
             }
-            vfast = __all_sync(0xFFFFFFFFu, vfast);
-            if (vfast) {
-                const float off = 128.0f + a.voff;
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    vz[k] = pack_bf16x2(__fadd_rn(off, bf_lo(vz[k])), __fadd_rn(off, bf_hi(vz[k])));
-                values_of<BITS, C, true>(y, p, vw, vs, vz, a.voff);
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int q4 = 0; q4 < C / 32; ++q4)
+                    *reinterpret_cast<float4*>(&sy[warp][g + 8 * h][(2 * tig + e) * (C / 8) + 4 * q4]) =
+                        make_float4(y[m][4 * q4][2 * h + e], y[m][4 * q4 + 1][2 * h + e], y[m][4 * q4 + 2][2 * h + e],
+                                    y[m][4 * q4 + 3][2 * h + e]);
+        }
+        __syncthreads();
+        for (int k = tid; k < 16 * (C / 4); k += kThreads) {
+            const int row = k / (C / 4), c4 = (k % (C / 4)) * 4, r = r0 + 16 * m + row;
+            if (r >= a.rows) break;
+            float M = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm[w][row]);
+            float L = 0.0f, v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            if (M != -INFINITY) {
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) {
+                    const float f = ex2(__fsub_rn(sm[w][row], M));
+                    L = __fmaf_rn(sl[w][row], f, L);
+                    const float4 x = *reinterpret_cast<const float4*>(&sy[w][row][c4]);
+                    v[0] = __fmaf_rn(x.x, f, v[0]);
+                    v[1] = __fmaf_rn(x.y, f, v[1]);
+                    v[2] = __fmaf_rn(x.z, f, v[2]);
+                    v[3] = __fmaf_rn(x.w, f, v[3]);
+                }
+            }
+            if (A.nsplit > 1) {
+                float* dst = A.part + ((o * a.rows + r) * A.nsplit + split) * (C + 4);
+                *reinterpret_cast<float4*>(dst + c4) = make_float4(v[0], v[1], v[2], v[3]);
+                if (c4 == 0) *reinterpret_cast<float2*>(dst + C) = make_float2(M, L);
             } else {
-                values_of<BITS, C, false>(y, p, vw, vs, vz, a.voff);
+                const int64_t at = row_index(a, o, r);
+                const float inv = L > 0.0f ? __fdiv_rn(1.0f, L) : 0.0f;
+                *reinterpret_cast<uint2*>(A.out + at * C + c4) =
+                    make_uint2(pack_bf16x2(__fmul_rn(v[0], inv), __fmul_rn(v[1], inv)),
+                               pack_bf16x2(__fmul_rn(v[2], inv), __fmul_rn(v[3], inv)));
+                if (A.lse && c4 == 0)
+                    A.lse[at] = L > 0.0f ? __fmul_rn(__fadd_rn(M, log2f(L)), 0.6931471805599453f) : -INFINITY;
             }
-        } else {
-            // bf16 rows: this lane's C/8 channels of its tokens, paired by token
-#pragma unroll
-            for (int ks2 = 0; ks2 < 2; ++ks2) {
-                uint32_t r[4][C / 16];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int t = t0 + 16 * ks2 + 8 * (e >> 1) + 2 * tig + (e & 1);
-                    if (t >= first && t < t1) {
-                        const uint4* src = reinterpret_cast<const uint4*>(
-                            a.vr + ((uint64_t)o * a.rrows + (t - a.tq)) * C + g * (C / 8));
-#pragma unroll
-                        for (int i = 0; i < C / 64; ++i) {
-                            const uint4 x = src[i];
-                            r[e][4 * i] = x.x; r[e][4 * i + 1] = x.y; r[e][4 * i + 2] = x.z; r[e][4 * i + 3] = x.w;
-                        }
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < C / 16; ++i) r[e][i] = 0u;
-                    }
-                }
-#pragma unroll
-                for (int nt = 0; nt < C / 8; ++nt) {
-                    const uint32_t sel = (nt & 1) ? 0x7632 : 0x5410;
-                    mma16816(y[nt], p[ks2], __byte_perm(r[0][nt / 2], r[1][nt / 2], sel),
-                             __byte_perm(r[2][nt / 2], r[3][nt / 2], sel));
-                }
-            }
-        }
-    }
-
-    // ---- merge the warps; channel of (nt, column e of lane tig) = (2 tig + e) C/8 + nt
-    la = __fadd_rn(la, __shfl_xor_sync(0xFFFFFFFFu, la, 1));
-    lb = __fadd_rn(lb, __shfl_xor_sync(0xFFFFFFFFu, lb, 1));
-    la = __fadd_rn(la, __shfl_xor_sync(0xFFFFFFFFu, la, 2));
-    lb = __fadd_rn(lb, __shfl_xor_sync(0xFFFFFFFFu, lb, 2));
-    if (tig == 0) {
-        sm[warp][g] = ma;
-        sm[warp][g + 8] = mb;
-        sl[warp][g] = la;
-        sl[warp][g + 8] = lb;
-    }
-#pragma unroll
-    for (int e = 0; e < 2; ++e)
-#pragma unroll
-        for (int q4 = 0; q4 < C / 32; ++q4) {
-            *reinterpret_cast<float4*>(&sy[warp][g][(2 * tig + e) * (C / 8) + 4 * q4]) =
-                make_float4(y[4 * q4][e], y[4 * q4 + 1][e], y[4 * q4 + 2][e], y[4 * q4 + 3][e]);
-            *reinterpret_cast<float4*>(&sy[warp][g + 8][(2 * tig + e) * (C / 8) + 4 * q4]) =
-                make_float4(y[4 * q4][2 + e], y[4 * q4 + 1][2 + e], y[4 * q4 + 2][2 + e], y[4 * q4 + 3][2 + e]);
-        }
-    __syncthreads();
-    for (int k = tid; k < kRowTile * (C / 4); k += kThreads) {
-        const int row = k / (C / 4), c4 = (k % (C / 4)) * 4, r = r0 + row;
-        if (r >= a.rows) break;
-        float M = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm[w][row]);
-        float L = 0.0f, v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        if (M != -INFINITY) {
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                const float f = ex2(__fsub_rn(sm[w][row], M));
-                L = __fmaf_rn(sl[w][row], f, L);
-                const float4 x = *reinterpret_cast<const float4*>(&sy[w][row][c4]);
-                v[0] = __fmaf_rn(x.x, f, v[0]);
-                v[1] = __fmaf_rn(x.y, f, v[1]);
-                v[2] = __fmaf_rn(x.z, f, v[2]);
-                v[3] = __fmaf_rn(x.w, f, v[3]);
-            }
-        }
-        if (A.nsplit > 1) {
-            float* dst = A.part + ((o * a.rows + r) * A.nsplit + split) * (C + 4);
-            *reinterpret_cast<float4*>(dst + c4) = make_float4(v[0], v[1], v[2], v[3]);
-            if (c4 == 0) *reinterpret_cast<float2*>(dst + C) = make_float2(M, L);
-        } else {
-            const int64_t at = row_index(a, o, r);
-            const float inv = L > 0.0f ? __fdiv_rn(1.0f, L) : 0.0f;
-            *reinterpret_cast<uint2*>(A.out + at * C + c4) =
-                make_uint2(pack_bf16x2(__fmul_rn(v[0], inv), __fmul_rn(v[1], inv)),
-                           pack_bf16x2(__fmul_rn(v[2], inv), __fmul_rn(v[3], inv)));
-            if (A.lse && c4 == 0)
-                A.lse[at] = L > 0.0f ? __fmul_rn(__fadd_rn(M, log2f(L)), 0.6931471805599453f) : -INFINITY;
         }
     }
 }
@@ -349,24 +391,46 @@ merge_rows_kernel(const ChunkArgs A, int64_t total)
     merge_row<C>(A, o, (int)(row - o * A.v.rows), A.part + row * A.nsplit * (C + 4), threadIdx.x & 31);
 }
 
-constexpr int64_t kSlots = 152 * 2;              // resident CTAs (two per SM)
+// Row tiles and splits.  Up to 16 rows take tiles of 16 (three CTAs a SM), more
+// take tiles of 32 (two), which unpack each key and value once for 32 rows.
+// Splits of the visible batches: the number that gives the shortest run through
+// all waves, counting about three batches for a CTA's start and end.
+struct RowsPlan { int64_t mt, ntiles, nsplit; };
 
-// Splits of the visible batches: enough CTAs for two waves of the GPU, at
-// least two batches per warp and split, and no more than the cache has.
-int64_t splits_of(int64_t outer, int64_t T, int64_t rows)
+constexpr int64_t kMaxWaves = 2;                 // more CTAs than this are not split further
+
+int64_t slots_of(int64_t mt) { return 152 * (mt == 1 ? 3 : 2); }
+
+RowsPlan rows_plan(int64_t outer, int64_t T, int64_t rows)
 {
-    const int64_t ctas = outer * ((rows + kRowTile - 1) / kRowTile);
-    const int64_t nb = (T + kBatch - 1) / kBatch;
-    return std::max<int64_t>(1, std::min<int64_t>((2 * kSlots + ctas - 1) / ctas, nb / (2 * kWarps)));
+    RowsPlan p;
+    p.mt = rows <= 16 ? 1 : 2;
+    p.ntiles = (rows + 16 * p.mt - 1) / (16 * p.mt);
+    const int64_t ctas = std::max<int64_t>(outer * p.ntiles, 1), slots = slots_of(p.mt);
+    const int64_t nb = (T + kBatch - 1) / kBatch + 1;
+    int64_t best = INT64_MAX;
+    p.nsplit = 1;
+    for (int64_t s = 1; s == 1 || (ctas * s <= kMaxWaves * slots && s * kWarps <= nb); ++s) {
+        const int64_t cost = ((ctas * s + slots - 1) / slots) * ((nb + s * kWarps - 1) / (s * kWarps) + 3);
+        if (cost < best) {
+            best = cost;
+            p.nsplit = s;
+        }
+    }
+    return p;
 }
 
 template <int BITS, int C>
-cudaError_t launch_rows(const ChunkArgs& A, int64_t outer, cudaStream_t st)
+cudaError_t launch_rows(ChunkArgs A, int64_t outer, cudaStream_t st)
 {
-    const int64_t grid = outer * A.ntiles * A.nsplit;
+    const RowsPlan p = rows_plan(outer, A.v.T, A.v.rows);
+    A.ntiles = (int32_t)p.ntiles;
+    A.nsplit = (int32_t)p.nsplit;
+    const int64_t grid = outer * p.ntiles * p.nsplit;
     if (grid > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
-    attend_rows_kernel<BITS, C><<<(unsigned)grid, kThreads, 0, st>>>(A);
-    if (A.nsplit > 1) {
+    if (p.mt == 1) attend_rows_kernel<BITS, C, 1><<<(unsigned)grid, kThreads, 0, st>>>(A);
+    else attend_rows_kernel<BITS, C, 2><<<(unsigned)grid, kThreads, 0, st>>>(A);
+    if (p.nsplit > 1) {
         const int64_t total = outer * A.v.rows;
         merge_rows_kernel<C><<<(unsigned)((total + kWarps - 1) / kWarps), kThreads, 0, st>>>(A, total);
     }
@@ -380,8 +444,10 @@ size_t chunk_workspace(int64_t outer, int64_t C, int64_t tmax, int64_t n, int64_
     const int64_t rows = n * group;
     if (outer == 0 || rows == 0) return 0;
     if (chunk_uses_tc(tmax, rows)) return chunk_tc_workspace(outer, C, tmax, rows);
-    const int64_t ns = splits_of(outer, tmax, rows);
-    return ns > 1 ? (size_t)(outer * rows * ns * (C + 4)) * sizeof(float) : 0;
+    // every T up to tmax may choose its splits: at most kMaxWaves of CTAs, or one per four batches
+    const int64_t mt = rows <= 16 ? 1 : 2, most = (tmax + kBatch - 1) / kBatch + 1;
+    const int64_t split_rows = std::min(kMaxWaves * slots_of(mt) * 16 * mt, outer * rows * (most / kWarps));
+    return most / kWarps > 1 ? (size_t)(split_rows * (C + 4)) * sizeof(float) : 0;
 }
 
 rows::View cache_view(const CacheArgs& x)
@@ -428,8 +494,6 @@ cudaError_t launch_attend_chunk(const CacheArgs& x, void* out, float* lse, void*
     A.lse = lse;
     A.part = static_cast<float*>(ws);
     if (chunk_uses_tc(A.v.T, A.v.rows)) return launch_attend_tc(A, x.bits, x.C, x.outer, ws, st);
-    A.ntiles = (A.v.rows + kRowTile - 1) / kRowTile;
-    A.nsplit = (int32_t)splits_of(x.outer, x.tq + x.nres, A.v.rows);
     if (x.bits == 4) return x.C == 128 ? launch_rows<4, 128>(A, x.outer, st) : launch_rows<4, 64>(A, x.outer, st);
     return x.C == 128 ? launch_rows<2, 128>(A, x.outer, st) : launch_rows<2, 64>(A, x.outer, st);
 }

@@ -1,24 +1,28 @@
-// kvq_rows.cuh -- K and V rows of the streaming cache as mma.sync fragments.
+// kvq_rows.cuh -- K and V rows of the streaming cache as mma.sync fragments,
+// for the kernels of few query rows (chunk.cu, weights.cu).
 //
 // A batch is 32 consecutive cache tokens, all of the store or all of the
 // buffer.  A warp turns a batch's packed codes into the B fragments of
-// mma.sync.m16n8k16 (bf16 x bf16 -> float32) without shared memory: the order
-// of the contracted index is free as long as both operands use the same, so
-// each is chosen such that a lane reads one contiguous piece of a code row.
+// mma.sync.m16n8k16 (bf16 x bf16 -> float32) in registers: the order of the
+// contracted index is free as long as both operands use the same, so each is
+// chosen such that a lane reads one contiguous piece of a code row.
 //  * scores, contraction over channels: lane (g, tig) = (lane / 4, lane % 4)
 //    reads its quarter of token g's row, channels [tig C/4, (tig+1) C/4).  A
 //    32-bit code word of F fields holds the channel pairs (i, i + F/2): fields
-//    BITS apart in its two halves, so one shift and one mask-and-or leave both
-//    as the bf16 values 128 + field;
+//    BITS apart in its two halves, so one shift and one mask-and-xor leave both
+//    as the bf16 values 128 + field (the xor also turns two's complement into
+//    offset binary);
 //  * values, contraction over tokens: lane (g, tig) reads channels
-//    [g C/8, (g+1) C/8) of the four tokens its score fragment covers; a byte
-//    permute pairs the words of two tokens, then the same shift and mask.
+//    [g C/8, (g+1) C/8) of the tokens its score fragment covers; a byte permute
+//    pairs the words of two tokens, then the same shift and mask.
 // One bf16x2 subtraction of 128 + off + zp is exact when |zp| <= 112 and an
 // integer (every operand and result is an integer of at most 256), and one
 // bf16x2 product with the bf16 scale rounds once: exactly RN_bf16(s (code -
 // zp)), what kvq_dequantize stores (its float32 product of an 8-bit and an
 // 8-bit significand is exact).  Groups with other zero points take the
 // float32 route: subtract, multiply and round as kvq_dequantize does.
+// Four instructions a pair make the unpacking half of these kernels' work:
+// they are bound by instruction issue, not by bytes.
 #pragma once
 
 #include "kvq_device.cuh"
@@ -63,11 +67,11 @@ __device__ __forceinline__ float ex2(float x) {  // 2^x, 2 ulp, 0 for -inf
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
-__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint4& a, uint32_t b0, uint32_t b1) {
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
                  "{%8, %9}, {%0, %1, %2, %3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+                 : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
 }
 
 // N 32-bit words (N = 1, 2, 4) from p, aligned to their size; read once.
@@ -88,28 +92,46 @@ __device__ __forceinline__ uint32_t bits_of(const __nv_bfloat16* p) {
     return *reinterpret_cast<const uint16_t*>(p);
 }
 
-// zero point of a pair as the fast route wants it, and whether it may take it
+// whether a zero point may take the bf16 route
 __device__ __forceinline__ bool zero_exact(float z) { return fabsf(z) <= 112.0f && z == rintf(z); }
+// a pair of zero points as that route wants them: 128 + off + zp
+__device__ __forceinline__ uint32_t biased(uint32_t z, float b) {
+    return pack_bf16x2(__fadd_rn(b, bf_lo(z)), __fadd_rn(b, bf_hi(z)));
+}
 
 template <int BITS, int C>
 struct Geo {
     static constexpr int kRowB = C * BITS / 8;   // packed bytes of a token row
     static constexpr int F = 32 / BITS;          // fields of a word
     static constexpr int kWpl = kRowB / 16;      // words of a row per lane, score side
-    static constexpr int kPairs = C / 8;         // channel pairs per lane, score side
     static constexpr int kSteps = C / 16;        // k-steps of a score product
     static constexpr int kVB = kRowB / 8;        // bytes of a row per lane, value side (2, 4 or 8)
     static constexpr int kVW = kVB >= 4 ? kVB / 4 : 1;
-    static constexpr int kTiles = C / 8;         // n-tiles of a value product
     static constexpr uint32_t kMask = BITS == 4 ? 0x000F000Fu : 0x00030003u;
+    // first channel, within its quarter, of pair p; the second is F/2 further
+    __host__ __device__ static constexpr int pair_channel(int p) { return p / (F / 2) * F + p % (F / 2); }
 };
 
 constexpr uint32_t kOne28 = 0x43004300u;         // bf16 128.0 in both halves
 
+// kOne28 with the sign fields' flip merged in (fields are the low BITS of each half)
+template <int BITS>
+__device__ __forceinline__ uint32_t magic(uint32_t flip) { return kOne28 | (flip & Geo<BITS, 64>::kMask); }
+
+// One pair of rows' values from two fields of w at bit `sh` of its halves.
+template <int BITS, bool FAST>
+__device__ __forceinline__ uint32_t value_pair(uint32_t w, int sh, uint32_t mg, uint32_t s, uint32_t z, float off) {
+    const uint32_t x = ((w >> sh) & Geo<BITS, 64>::kMask) ^ mg;
+    if constexpr (FAST) return mul_bf16x2(sub_bf16x2(x, z), s);
+    const float lo = __fsub_rn(__fsub_rn((float)(x & 0xFFu), off), bf_lo(z));
+    const float hi = __fsub_rn(__fsub_rn((float)((x >> 16) & 0xFFu), off), bf_hi(z));
+    return pack_bf16x2(__fmul_rn(lo, bf_lo(s)), __fmul_rn(hi, bf_hi(s)));
+}
+
 // Channel pairs (c, c + F/2) of this lane's quarter of a bf16 row, from the
 // quarter's first element: the order of the code words' fields.
 template <int BITS, int C>
-__device__ __forceinline__ void load_pairs(const __nv_bfloat16* quarter, uint32_t (&pr)[Geo<BITS, C>::kPairs]) {
+__device__ __forceinline__ void load_pairs(const __nv_bfloat16* quarter, uint32_t (&pr)[C / 8]) {
     using G = Geo<BITS, C>;
     constexpr int N = C / 8;                     // 32-bit words of the quarter
     uint32_t r[N];
@@ -119,61 +141,91 @@ __device__ __forceinline__ void load_pairs(const __nv_bfloat16* quarter, uint32_
         r[4 * i] = x.x; r[4 * i + 1] = x.y; r[4 * i + 2] = x.z; r[4 * i + 3] = x.w;
     }
 #pragma unroll
-    for (int p = 0; p < G::kPairs; ++p) {
-        const int c = p / (G::F / 2) * G::F + p % (G::F / 2);
+    for (int p = 0; p < N; ++p) {
+        const int c = G::pair_channel(p);
         pr[p] = __byte_perm(r[c / 2], r[(c + G::F / 2) / 2], (c & 1) ? 0x7632 : 0x5410);
     }
 }
 
-// K constants of one group for this lane's channels: scales and, in the fast
-// form, 128 + off + zp (else the raw zero points).  Returns whether the whole
-// warp may take the fast route.
+// ---- K constants of one group, staged in shared memory by the warp that uses
+// them: entry (kk, tig) = scale pairs 2 kk, 2 kk + 1 and zero pairs of lane
+// quarter tig.  Lane e < C/4 makes entry e.
+struct KRaw { uint32_t s0, s1, z0, z1; };
+
 template <int BITS, int C>
-__device__ __forceinline__ bool load_k_group(const View& a, int64_t o, int gk, int tig,
-                                             uint32_t (&s)[C / 8], uint32_t (&z)[C / 8]) {
-    const int64_t at = (o * a.ngk + gk) * C + tig * (C / 4);
-    load_pairs<BITS, C>(a.ks + at, s);
-    if (!a.kz) {
-        const uint32_t v = pack_bf16x2(128.0f + a.koff, 128.0f + a.koff);
-#pragma unroll
-        for (int p = 0; p < C / 8; ++p) z[p] = v;
-        return true;
+__device__ __forceinline__ KRaw fetch_k_group(const View& a, int64_t o, int gk, int lane) {
+    using G = Geo<BITS, C>;
+    KRaw r = {0u, 0u, 0u, 0u};
+    if (lane < C / 4) {
+        const int64_t at = (o * a.ngk + gk) * C + (lane & 3) * (C / 4) + G::pair_channel(2 * (lane >> 2));
+        r.s0 = *reinterpret_cast<const uint32_t*>(a.ks + at);       // channels c, c + 1
+        r.s1 = *reinterpret_cast<const uint32_t*>(a.ks + at + G::F / 2);
+        if (a.kz) {
+            r.z0 = *reinterpret_cast<const uint32_t*>(a.kz + at);
+            r.z1 = *reinterpret_cast<const uint32_t*>(a.kz + at + G::F / 2);
+        }
     }
-    load_pairs<BITS, C>(a.kz + at, z);
+    return r;
+}
+// Stages them; returns whether the warp may take the bf16 route (the zero
+// pairs are then 128 + off + zp, else as stored).
+__device__ __forceinline__ bool stage_k_group(const KRaw& r, float koff, bool asym, uint4* kc, int lane, int entries) {
+    const uint32_t s0 = __byte_perm(r.s0, r.s1, 0x5410), s1 = __byte_perm(r.s0, r.s1, 0x7632);
+    uint32_t z0 = __byte_perm(r.z0, r.z1, 0x5410), z1 = __byte_perm(r.z0, r.z1, 0x7632);
     bool ok = true;
-#pragma unroll
-    for (int p = 0; p < C / 8; ++p) ok = ok && zero_exact(bf_lo(z[p])) && zero_exact(bf_hi(z[p]));
-    ok = __all_sync(0xFFFFFFFFu, ok);
+    if (asym)
+        ok = __all_sync(0xFFFFFFFFu, zero_exact(bf_lo(z0)) && zero_exact(bf_hi(z0)) && zero_exact(bf_lo(z1)) &&
+                                         zero_exact(bf_hi(z1)));
     if (ok) {
-        const float b = 128.0f + a.koff;
-#pragma unroll
-        for (int p = 0; p < C / 8; ++p) z[p] = pack_bf16x2(__fadd_rn(b, bf_lo(z[p])), __fadd_rn(b, bf_hi(z[p])));
+        z0 = biased(z0, 128.0f + koff);
+        z1 = biased(z1, 128.0f + koff);
     }
+    __syncwarp();                                // the group before has been read
+    if (lane < entries) kc[lane] = make_uint4(s0, s1, z0, z1);
+    __syncwarp();
     return ok;
 }
 
-// One pair of rows' values from two fields of w at bit `sh` of its halves.
-template <int BITS, bool FAST>
-__device__ __forceinline__ uint32_t value_pair(uint32_t w, int sh, uint32_t s, uint32_t z, float off) {
-    const uint32_t x = (w >> sh) & Geo<BITS, 64>::kMask;
-    if constexpr (FAST) return mul_bf16x2(sub_bf16x2(x | kOne28, z), s);
-    const float lo = __fsub_rn(__fsub_rn((float)(x & 0xFFFFu), off), bf_lo(z));
-    const float hi = __fsub_rn(__fsub_rn((float)(x >> 16), off), bf_hi(z));
-    return pack_bf16x2(__fmul_rn(lo, bf_lo(s)), __fmul_rn(hi, bf_hi(s)));
-}
-
-// Scores of one n-tile (8 tokens) from a lane's code words of its token.
-template <int BITS, int C, bool FAST>
-__device__ __forceinline__ void keys_of(const uint32_t (&w)[Geo<BITS, C>::kWpl], const uint32_t (&s)[C / 8],
-                                        const uint32_t (&z)[C / 8], float off, uint32_t (&b)[C / 8]) {
+// ---- scores of a batch: s[mt][j] += Q(tile mt) . K(n-tile j, tokens 8 j + g)
+// from the lane's code words.  qf: [mt][kk][lane] A fragments.
+template <int BITS, int C, int MT, bool FAST>
+__device__ __forceinline__ void scores_of(float (&s)[MT][4][4], const uint32_t (&w)[4][Geo<BITS, C>::kWpl],
+                                          const uint4* qf, const uint4* kc, uint32_t mg, float off, int lane) {
     using G = Geo<BITS, C>;
 #pragma unroll
-    for (int p = 0; p < G::kPairs; ++p)
-        b[p] = value_pair<BITS, FAST>(w[p / (G::F / 2)], BITS * (p % (G::F / 2)), s[p], z[p], off);
+    for (int kk = 0; kk < G::kSteps; ++kk) {
+        const uint4 k = kc[kk * 4 + (lane & 3)];
+        uint4 q[MT];
+#pragma unroll
+        for (int m = 0; m < MT; ++m) q[m] = qf[(m * G::kSteps + kk) * 32 + lane];
+        const int wi = 2 * kk / (G::F / 2), sh = BITS * (2 * kk % (G::F / 2));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t b0 = value_pair<BITS, FAST>(w[j][wi], sh, mg, k.x, k.z, off);
+            const uint32_t b1 = value_pair<BITS, FAST>(w[j][wi], sh + BITS, mg, k.y, k.w, off);
+#pragma unroll
+            for (int m = 0; m < MT; ++m) mma16816(s[m][j], q[m], b0, b1);
+        }
+    }
+}
+// the same from bf16 rows of the buffer (row of token 8 j + g: krow[j], this lane's quarter)
+template <int BITS, int C, int MT>
+__device__ __forceinline__ void scores_of_rows(float (&s)[MT][4][4], const __nv_bfloat16* (&krow)[4], const uint4* qf,
+                                               int lane) {
+    using G = Geo<BITS, C>;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        uint32_t kb[C / 8];
+        load_pairs<BITS, C>(krow[j], kb);
+#pragma unroll
+        for (int kk = 0; kk < G::kSteps; ++kk)
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+                mma16816(s[m][j], qf[(m * G::kSteps + kk) * 32 + lane], kb[2 * kk], kb[2 * kk + 1]);
+    }
 }
 
-// Which batches of a slice a set of query rows can see: batches of the store
-// come first, then the buffer's.
+// Which batches of a slice exist: those of the store come first, then the buffer's.
 struct Span { int nsb, nb; };                    // store batches, all batches
 __device__ __forceinline__ Span span_of(const View& a) {
     Span s;
@@ -196,11 +248,36 @@ __device__ __forceinline__ int batch_of(const View& a, const Span& s, int t) {
     return t < a.tq ? t / kBatch : s.nsb + (t - a.tq) / kBatch;
 }
 
-// query row r of slice o: element offset of its q row / index of its lse
+// query row r of slice o: index of its q row (times C) and of its lse
 __device__ __forceinline__ int64_t row_index(const View& a, int64_t o, int r) {
     const int i = r / a.group, j = r - i * a.group;
-    const int64_t b = o / a.kv_heads, h = o - b * a.kv_heads;
-    return (b * a.n + i) * ((int64_t)a.kv_heads * a.group) + h * a.group + j;
+    const uint32_t b = (uint32_t)o / (uint32_t)a.kv_heads, h = (uint32_t)o - b * (uint32_t)a.kv_heads;
+    return ((int64_t)b * a.n + i) * ((int64_t)a.kv_heads * a.group) + (int64_t)h * a.group + j;
+}
+
+// A fragments of query rows [r0, r0 + 16 MT) of slice o, made by the whole CTA
+// (rows past the last are zeros): entry (mt, kk, lane) = rows g and g + 8 of
+// tile mt, channel pairs 2 kk and 2 kk + 1.
+template <int BITS, int C, int MT>
+__device__ __forceinline__ void stage_queries(const View& a, int64_t o, int r0, uint4* qf, int tid, int threads) {
+    using G = Geo<BITS, C>;
+    for (int e = tid; e < MT * G::kSteps * 32; e += threads) {
+        const int lane = e & 31, kk = (e >> 5) % G::kSteps, mt = (e >> 5) / G::kSteps;
+        const int c = (lane & 3) * (C / 4) + G::pair_channel(2 * kk);
+        uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int r = r0 + mt * 16 + (lane >> 2) + 8 * h;
+            if (r < a.rows) {
+                const __nv_bfloat16* p = a.q + row_index(a, o, r) * C + c;
+                const uint32_t x = *reinterpret_cast<const uint32_t*>(p);           // channels c, c + 1
+                const uint32_t y = *reinterpret_cast<const uint32_t*>(p + G::F / 2);
+                w[h] = __byte_perm(x, y, 0x5410);
+                w[2 + h] = __byte_perm(x, y, 0x7632);
+            }
+        }
+        qf[e] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
 }
 
 }  // namespace rows

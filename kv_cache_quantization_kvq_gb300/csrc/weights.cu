@@ -6,11 +6,11 @@
 // every query row at hand, w_t = sum_r exp(q_r.k_t / sqrt(C) - lse_r) needs one
 // pass over the keys and no history.
 //
-// The keys stay and the queries stream: a warp turns the keys of a 32-token
-// batch into B fragments of mma.sync.m16n8k16 once (kvq_rows.cuh), walks the
-// row tiles (16 query rows each) that see the batch, and keeps the running sum
-// of its columns' weights in registers.  Each token belongs to one warp, so no
-// sum needs an atomic and its order is fixed.
+// A CTA takes the query rows of a slice, 16 at a time, as A fragments in shared
+// memory; each of its warps walks a run of 32-token batches, turns their keys
+// into B fragments of mma.sync.m16n8k16 (kvq_rows.cuh) and sums the weights of
+// its columns over the rows.  Each token belongs to one warp, so no sum needs an
+// atomic and its order is fixed.  Up to 64 rows; more take weights_tc.cu.
 #include <algorithm>
 
 #include "kvq_chunk.cuh"
@@ -23,8 +23,7 @@ using namespace rows;
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kRowTile = 16;
-constexpr int kFold = 32;                        // row tiles summed before they join the total
+constexpr int kMaxTiles = 4;                     // row tiles of 16 held in shared memory
 
 struct WeightArgs {
     View v;
@@ -32,147 +31,152 @@ struct WeightArgs {
     const float* in;                             // nullptr: zeros
     float* out;
     int64_t stride;
+    int32_t ntiles, nrun;                        // row tiles; CTAs of a slice
 };
 
 template <int BITS, int C>
-__global__ void __launch_bounds__(kThreads, 2)
-weights_rows_kernel(const WeightArgs A, int nb, int64_t total)
+__global__ void __launch_bounds__(kThreads, 4)
+weights_rows_kernel(const WeightArgs A)
 {
     using G = Geo<BITS, C>;
     const View& a = A.v;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    __shared__ __align__(16) uint4 qf[kMaxTiles * G::kSteps * 32];
+    __shared__ float nlse[kMaxTiles * 16];       // -lse in base 2; -inf: no weight
+    __shared__ __align__(16) uint4 kcs[kWarps][C / 4];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, tig = lane & 3;
-    const int64_t job = (int64_t)blockIdx.x * kWarps + warp;
-    if (job >= total) return;
-    const int64_t o = job / nb;
-    const int b = (int)(job - o * nb);
+    const int64_t o = blockIdx.x / (uint32_t)A.nrun;
+    const int run = (int)(blockIdx.x - (uint32_t)o * (uint32_t)A.nrun);
     const Span sp = span_of(a);
-    int t0, t1;
-    batch_at(a, sp, b, t0, t1);
     const int first = a.first ? max(a.first[o], 0) : 0;
     const int base = a.T - a.n;                  // token of query 0
 
-    float sum[4][2];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) sum[j][0] = sum[j][1] = 0.0f;
-    if (t1 > first) {
-        // ---- the batch's keys
-        uint32_t kb[4][C / 8];
-        if (b < sp.nsb) {
-            const uint8_t* kc = a.kc + (uint64_t)o * a.cap * G::kRowB + tig * (G::kRowB / 4);
-            uint32_t kw[4][G::kWpl];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int t = min(t0 + 8 * j + g, t1 - 1);
-                load_words<G::kWpl>(kc + (int64_t)t * G::kRowB, kw[j]);
-#pragma unroll
-                for (int i = 0; i < G::kWpl; ++i) kw[j][i] ^= a.kflip;
-            }
-            uint32_t ks[C / 8], kz[C / 8];
-            const bool fast = load_k_group<BITS, C>(a, o, t0 / a.gk, tig, ks, kz);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                if (fast) keys_of<BITS, C, true>(kw[j], ks, kz, a.koff, kb[j]);
-                else keys_of<BITS, C, false>(kw[j], ks, kz, a.koff, kb[j]);
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int t = min(t0 + 8 * j + g, t1 - 1) - a.tq;
-                load_pairs<BITS, C>(a.kr + ((uint64_t)o * a.rrows + t) * C + tig * (C / 4), kb[j]);
-            }
+    for (int t = 0; t < A.ntiles; ++t) stage_queries<BITS, C, 1>(a, o, 16 * t, qf + t * G::kSteps * 32, tid, kThreads);
+    for (int r = tid; r < 16 * A.ntiles; r += kThreads) {
+        float l = -INFINITY;
+        if (r < a.rows) {
+            l = A.lse[row_index(a, o, r)];
+            l = l == -INFINITY ? -INFINITY : -__fmul_rn(l, kLog2e);
         }
+        nlse[r] = l;
+    }
+    // ---- this warp's run of batches
+    const int k = run * kWarps + warp, of = A.nrun * kWarps;
+    const int b0 = (int)((int64_t)sp.nb * k / of), b1 = (int)((int64_t)sp.nb * (k + 1) / of);
+    const int bs = min(b1, sp.nsb);
+    const uint8_t* kc = a.kc + (uint64_t)o * a.cap * G::kRowB + tig * (G::kRowB / 4);
+    const uint32_t kmg = magic<BITS>(a.kflip);
+    uint32_t kw[4][G::kWpl];
+    auto load_k = [&](int b) {
+        const uint8_t* p = kc + (int64_t)b * (kBatch * G::kRowB);
+        const int cnt = a.tq - b * kBatch - 1;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) load_words<G::kWpl>(p + min(8 * j + g, cnt) * G::kRowB, kw[j]);
+    };
+    KRaw kr = {0u, 0u, 0u, 0u};
+    int staged = -1, fetched = -1;
+    bool kfast = true;
+    if (b0 < bs) {
+        fetched = b0 * kBatch / a.gk;
+        load_k(b0);
+        kr = fetch_k_group<BITS, C>(a, o, fetched, lane);
+    }
+    __syncthreads();
 
-        // ---- the rows that see any of it: from query t0 - base on
-        const int i0 = max(0, max(t0, first) - base);
-        float part[4][2];
-        int fold = 0;
+    for (int b = b0; b < b1; ++b) {
+        int t0, t1;
+        batch_at(a, sp, b, t0, t1);
+        const bool seen = t1 > first;
+        const bool store = b < sp.nsb;
+        if (store && fetched != staged) {
+            kfast = stage_k_group(kr, a.koff, a.kz != nullptr, kcs[warp], lane, C / 4);
+            staged = fetched;
+        }
+        float sum[4][2];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) part[j][0] = part[j][1] = 0.0f;
-        for (int r0 = (int)((int64_t)i0 * a.group / kRowTile) * kRowTile; r0 < a.rows; r0 += kRowTile) {
-            const int ra = r0 + g, rb = ra + 8;
-            uint32_t qa[C / 8], qb[C / 8];
-            float xa = INFINITY, xb = INFINITY;  // a row past the last, or without weight, gives 2^-inf
-            int la = -1, lb = -1;
+        for (int j = 0; j < 4; ++j) sum[j][0] = sum[j][1] = 0.0f;
+        // the old scores, in flight meanwhile: lane (g, tig) writes n-tile g
+        const int wt = t0 + 8 * g + 2 * tig;
+        const int64_t at = o * A.stride + wt;
+        const float old0 = A.in && g < 4 && wt < t1 ? A.in[at] : 0.0f;
+        const float old1 = A.in && g < 4 && wt + 1 < t1 ? A.in[at + 1] : 0.0f;
+
+        auto add = [&](const float (&s)[1][4][4], int t) {
+            const float la = nlse[16 * t + g], lb = nlse[16 * t + g + 8];
+            const int ra = base + (16 * t + g) / a.group, rb = base + (16 * t + g + 8) / a.group;
+            const bool whole = t0 >= first && t1 - t0 == kBatch && t1 - 1 <= base + 16 * t / a.group;
 #pragma unroll
-            for (int p = 0; p < C / 8; ++p) qa[p] = qb[p] = 0u;
-            if (ra < a.rows) {
-                const int64_t at = row_index(a, o, ra);
-                load_pairs<BITS, C>(a.q + at * C + tig * (C / 4), qa);
-                const float l = A.lse[at];
-                if (l != -INFINITY) { xa = __fmul_rn(l, kLog2e); la = base + ra / a.group; }
-            }
-            if (rb < a.rows) {
-                const int64_t at = row_index(a, o, rb);
-                load_pairs<BITS, C>(a.q + at * C + tig * (C / 4), qb);
-                const float l = A.lse[at];
-                if (l != -INFINITY) { xb = __fmul_rn(l, kLog2e); lb = base + rb / a.group; }
-            }
-            const bool whole = t0 >= first && t1 - t0 == kBatch && t1 - 1 <= base + r0 / a.group;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                for (int kk = 0; kk < G::kSteps; ++kk) {
-                    const uint32_t qf[4] = {qa[2 * kk], qb[2 * kk], qa[2 * kk + 1], qb[2 * kk + 1]};
-                    mma16816(s, qf, kb[j][2 * kk], kb[j][2 * kk + 1]);
-                }
+            for (int j = 0; j < 4; ++j)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    float wa = ex2(__fmaf_rn(s[e], a.scale2, -xa)), wb = ex2(__fmaf_rn(s[2 + e], a.scale2, -xb));
+                    float wa = ex2(__fmaf_rn(s[0][j][e], a.scale2, la)), wb = ex2(__fmaf_rn(s[0][j][2 + e], a.scale2, lb));
                     if (!whole) {                // selected: a hidden token's score may be NaN
-                        const int t = t0 + 8 * j + 2 * tig + e;
-                        const bool live = t >= first && t < t1;
-                        wa = live && t <= la ? wa : 0.0f;
-                        wb = live && t <= lb ? wb : 0.0f;
+                        const int tok = t0 + 8 * j + 2 * tig + e;
+                        const bool live = tok >= first && tok < t1;
+                        wa = live && tok <= ra ? wa : 0.0f;
+                        wb = live && tok <= rb ? wb : 0.0f;
                     }
-                    part[j][e] = __fadd_rn(part[j][e], __fadd_rn(wa, wb));
+                    sum[j][e] = __fadd_rn(sum[j][e], __fadd_rn(wa, wb));
                 }
-            }
-            if (++fold == kFold) {
-                fold = 0;
+        };
+        if (seen) {
+            for (int t = 0; t < A.ntiles; ++t) {
+                if (base + (min(16 * t + 16, a.rows) - 1) / a.group < t0) continue;  // the tile sees none of the batch
+                float s[1][4][4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
+                for (int j = 0; j < 4; ++j) s[0][j][0] = s[0][j][1] = s[0][j][2] = s[0][j][3] = 0.0f;
+                const uint4* qt = qf + t * G::kSteps * 32;
+                if (!store) {
+                    const __nv_bfloat16* krow[4];
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        sum[j][e] = __fadd_rn(sum[j][e], part[j][e]);
-                        part[j][e] = 0.0f;
-                    }
+                    for (int j = 0; j < 4; ++j)
+                        krow[j] = a.kr + ((uint64_t)o * a.rrows + (min(t0 + 8 * j + g, t1 - 1) - a.tq)) * C + tig * (C / 4);
+                    scores_of_rows<BITS, C, 1>(s, krow, qt, lane);
+                } else if (kfast) {
+                    scores_of<BITS, C, 1, true>(s, kw, qt, kcs[warp], kmg, a.koff, lane);
+                } else {
+                    scores_of<BITS, C, 1, false>(s, kw, qt, kcs[warp], kmg, a.koff, lane);
+                }
+                add(s, t);
             }
         }
+        if (b + 1 < bs) {
+            load_k(b + 1);
+            const int gk = (b + 1) * kBatch / a.gk;
+            if (gk != fetched) {
+                fetched = gk;
+                kr = fetch_k_group<BITS, C>(a, o, gk, lane);
+            }
+        }
+        // ---- sum the lanes of a column (rows g, g + 8 of every tile), add the old score
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) sum[j][e] = __fadd_rn(sum[j][e], part[j][e]);
-    }
-    // ---- sum the lanes of a column (rows g, g + 8 of every tile), add the old score
+            for (int e = 0; e < 2; ++e)
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+                for (int x = 4; x < 32; x <<= 1)
+                    sum[j][e] = __fadd_rn(sum[j][e], __shfl_xor_sync(0xFFFFFFFFu, sum[j][e], x));
+        if (g < 4) {
+            float w0 = sum[0][0], w1 = sum[0][1];
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
-#pragma unroll
-            for (int x = 4; x < 32; x <<= 1)
-                sum[j][e] = __fadd_rn(sum[j][e], __shfl_xor_sync(0xFFFFFFFFu, sum[j][e], x));
-    if (g < 4) {
-        // lane (g, tig) writes n-tile j = g
-        float w0 = sum[0][0], w1 = sum[0][1];
-#pragma unroll
-        for (int j = 1; j < 4; ++j)
-            if (g == j) { w0 = sum[j][0]; w1 = sum[j][1]; }
-        const int t = t0 + 8 * g + 2 * tig;
-        const int64_t at = o * A.stride + t;
-        if (t < t1) A.out[at] = A.in ? __fadd_rn(A.in[at], w0) : w0;
-        if (t + 1 < t1) A.out[at + 1] = A.in ? __fadd_rn(A.in[at + 1], w1) : w1;
+            for (int j = 1; j < 4; ++j)
+                if (g == j) { w0 = sum[j][0]; w1 = sum[j][1]; }
+            if (wt < t1) A.out[at] = A.in ? __fadd_rn(old0, w0) : w0;
+            if (wt + 1 < t1) A.out[at + 1] = A.in ? __fadd_rn(old1, w1) : w1;
+        }
     }
 }
 
 template <int BITS, int C>
-cudaError_t launch_rows(const WeightArgs& A, int64_t outer, cudaStream_t st)
+cudaError_t launch_rows(WeightArgs A, int64_t outer, cudaStream_t st)
 {
-    const int nb = (A.v.tq + kBatch - 1) / kBatch + (A.v.nres + kBatch - 1) / kBatch;
-    const int64_t total = outer * nb, grid = (total + kWarps - 1) / kWarps;
+    // one wave of four CTAs a SM, or a CTA per four batches where there are fewer
+    const int64_t nb = (A.v.tq + kBatch - 1) / kBatch + (A.v.nres + kBatch - 1) / kBatch;
+    A.ntiles = (A.v.rows + 15) / 16;
+    A.nrun = (int32_t)std::max<int64_t>(1, std::min<int64_t>((152 * 4) / outer, (nb + kWarps - 1) / kWarps));
+    const int64_t grid = outer * A.nrun;
     if (grid > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
-    weights_rows_kernel<BITS, C><<<(unsigned)grid, kThreads, 0, st>>>(A, nb, total);
+    weights_rows_kernel<BITS, C><<<(unsigned)grid, kThreads, 0, st>>>(A);
     return cudaGetLastError();
 }
 
