@@ -11,6 +11,7 @@ there is no CPU fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 from typing import Optional
@@ -161,11 +162,13 @@ class QParams:
     zero_dtype: int = NONE
 
     @staticmethod
+    @functools.lru_cache(maxsize=256, typed=True)
     def sym(bits, axis=ALONG_T, group=0, residual=0, scale_dtype=F32, qmax=None):
         q = (1 << (bits - 1)) - 1 if qmax is None else qmax
         return QParams(bits, SYM, -q, q, axis, group, residual, scale_dtype, NONE)
 
     @staticmethod
+    @functools.lru_cache(maxsize=256, typed=True)
     def asym(bits, qmin, qmax, axis=ALONG_T, group=0, residual=0, scale_dtype=F32, zero_dtype=I8):
         return QParams(bits, ASYM, qmin, qmax, axis, group, residual, scale_dtype, zero_dtype)
 
@@ -602,6 +605,13 @@ def rotate(x, signs, inverse=False, out=None, out_dtype=None, stream=None):
 
 # ---- the streaming cache (torch tensors; calls run on the tensors' device) -----
 
+@functools.lru_cache(maxsize=1024)
+def _store_sizes(shape, qp: QParams, resid_rows: int):
+    """Bytes of (codes, scale, zero, resid) of one cache: a store without residual and the bf16 buffer."""
+    store = QParams(qp.bits, qp.mode, qp.qmin, qp.qmax, qp.axis, qp.group, 0, qp.scale_dtype, qp.zero_dtype)
+    return kvq_quantized_sizes(shape, BF16, store)[:3] + (shape[0] * resid_rows * shape[2] * 2,)
+
+
 @dataclass
 class KVCache:
     """One layer's streaming K and V caches: what kvq_append_kv fills, or what
@@ -610,7 +620,8 @@ class KVCache:
     k, v: (codes, scale, zero, resid) of each cache; shape: the stores'
     (outer, T_cap, C), outer = batch * kv_heads; tq, nres: filled tokens of the
     store and of the bf16 buffer of resid_rows rows; first: CUDA int32 [outer]
-    left padding, or None."""
+    left padding, or None.  The buffers are contiguous and on one device; their
+    sizes are checked against the shape and formats when the object is made."""
     k: tuple
     v: tuple
     shape: tuple
@@ -621,6 +632,15 @@ class KVCache:
     resid_rows: int
     kv_heads: int = 1
     first: "object" = None
+
+    def __post_init__(self):
+        self.shape = tuple(self.shape)
+        dev = self.k[0].device
+        for bufs, qp, who in ((self.k, self.kqp, "k"), (self.v, self.vqp, "v")):
+            for t, size in zip(bufs, _store_sizes(self.shape, qp, self.resid_rows)):
+                if size and (t is None or t.nbytes < size or t.device != dev or not t.is_contiguous()):
+                    raise ValueError(f"{who}: every buffer must be contiguous, on {dev} and hold its part of the cache "
+                                     f"(codes, scale, zero, resid: {_store_sizes(self.shape, qp, self.resid_rows)} bytes)")
 
     @staticmethod
     def from_quantized(qk: Quantized, qv: Quantized, kv_heads: int = 1, first=None) -> "KVCache":
@@ -638,35 +658,84 @@ class KVCache:
     def c(self) -> kvq_cache:
         if self.first is not None and (str(self.first.dtype) != "torch.int32" or self.first.numel() != self.shape[0]):
             raise ValueError("first must be int32 [outer]")
-        return kvq_cache(*[_ptr(x) for x in self.k], *[_ptr(x) for x in self.v], self.tq, self.nres, self.resid_rows,
-                         _ptr(self.first))
+        return kvq_cache(*[t if t is None else t.data_ptr() for t in (*self.k, *self.v)], self.tq, self.nres,
+                         self.resid_rows, self.first if self.first is None else self.first.data_ptr())
 
 
-def _on(t, stream):
+class _On:
     """The context of a call on t's device: the current stream there, or the
-    given one (temporaries are then allocated on that stream)."""
-    import torch
-    if stream is None:
-        return torch.cuda.device(t.device)
-    if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream), device=t.device)
-    return torch.cuda.stream(stream)
+    given one (temporaries are then allocated on that stream).  Entering returns
+    the stream's handle; a call on the current device and stream costs nothing
+    more."""
+    __slots__ = ("ctx", "device", "handle")
+
+    def __init__(self, t, stream):
+        import torch
+        self.ctx, self.device = None, t.device.index
+        if stream is not None:
+            if not hasattr(stream, "cuda_stream"):
+                stream = torch.cuda.ExternalStream(int(stream), device=t.device)
+            self.ctx = torch.cuda.stream(stream)
+        elif self.device != torch.cuda.current_device():
+            self.ctx = torch.cuda.device(t.device)
+
+    def __enter__(self):
+        import torch
+        if self.ctx is not None:
+            self.ctx.__enter__()
+        return torch._C._cuda_getCurrentRawStream(self.device)
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+
+
+# Sizes and ctypes forms that depend on plain numbers only.
+@functools.lru_cache(maxsize=1024)
+def _shape_of(shape) -> kvq_shape:
+    return _shape(shape)
+
+
+@functools.lru_cache(maxsize=256)
+def _params_of(qp: QParams) -> kvq_qparams:
+    return qp.c()
+
+
+_chunk_ws = functools.lru_cache(maxsize=1024)(kvq_attend_chunk_workspace)
+_weights_ws = functools.lru_cache(maxsize=1024)(kvq_attend_weights_workspace)
+_evict_ws = functools.lru_cache(maxsize=1024)(kvq_evict_blocks_workspace)
 
 
 def _want(t, name, dtype, shape, device):
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous() or t.device != device:
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device} "
+    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous() or t.device != device:
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape} on {device} "
                          f"(got {t.dtype} {tuple(t.shape)} on {t.device})")
+
+
+def _temporary(size, device):
+    import torch
+    return torch.empty(size, dtype=torch.uint8, device=device) if size else None
+
+
+def _scratch(t, device):
+    """(address, bytes) of a workspace, which may be None."""
+    if t is None:
+        return None, 0
+    if not t.is_contiguous() or t.device != device:
+        raise ValueError(f"workspace must be contiguous and on {device}")
+    return t.data_ptr(), t.nbytes
 
 
 def _heads(q, cache: KVCache):
     """(n, group) of q [batch, n, kv_heads * group, C] over the cache."""
     import torch
     outer, _, C = cache.shape
-    if q.dim() != 4 or cache.kv_heads < 1 or outer % cache.kv_heads or q.shape[2] % cache.kv_heads:
-        raise ValueError("q must be [batch, n, kv_heads * group, C] with batch * kv_heads = outer")
-    _want(q, "q", torch.bfloat16, (outer // cache.kv_heads, q.shape[1], q.shape[2], C), q.device)
-    return q.shape[1], q.shape[2] // cache.kv_heads
+    s = tuple(q.shape)
+    if len(s) != 4 or cache.kv_heads < 1 or s[0] * cache.kv_heads != outer or s[2] % cache.kv_heads or s[3] != C:
+        raise ValueError(f"q must be [batch, n, kv_heads * group, C] with batch * kv_heads = {outer}, C = {C} (got {s})")
+    if q.dtype != torch.bfloat16 or not q.is_contiguous() or not q.is_cuda or cache.k[0].device != q.device:
+        raise ValueError("q must be a contiguous bf16 CUDA tensor on the cache's device")
+    return s[1], s[2] // cache.kv_heads
 
 
 def attend_chunk(q, cache: KVCache, out=None, lse=None, workspace=None, stream=None):
@@ -675,17 +744,22 @@ def attend_chunk(q, cache: KVCache, out=None, lse=None, workspace=None, stream=N
     attention over the streaming cache."""
     import torch
     n, group = _heads(q, cache)
+    dev, ref = q.device, ctypes.byref
     if out is not None:
-        _want(out, "out", torch.bfloat16, q.shape, q.device)
+        _want(out, "out", torch.bfloat16, tuple(q.shape), dev)
     if lse is not None:
-        _want(lse, "lse", torch.float32, q.shape[:3], q.device)
-    with _on(q, stream):
-        out = torch.empty_like(q) if out is None else out
-        lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device) if lse is None else lse
+        _want(lse, "lse", torch.float32, tuple(q.shape[:3]), dev)
+    with _On(q, stream) as handle:
+        if out is None:
+            out = torch.empty_like(q)
+        if lse is None:
+            lse = torch.empty(q.shape[:3], dtype=torch.float32, device=dev)
         if workspace is None:
-            workspace = _empty(kvq_attend_chunk_workspace(cache.shape, cache.resid_rows, n, group), q.device)
-        kvq_attend_chunk(q, n, group, cache.kv_heads, cache.c(), cache.kqp, cache.vqp, cache.shape, out, lse,
-                         workspace, workspace.numel() * workspace.element_size())
+            workspace = _temporary(_chunk_ws(cache.shape, cache.resid_rows, n, group), dev)
+        ws, ws_B = _scratch(workspace, dev)
+        _check(LIB.kvq_attend_chunk(q.data_ptr(), n, group, cache.kv_heads, ref(cache.c()), ref(_params_of(cache.kqp)),
+                                    ref(_params_of(cache.vqp)), ref(_shape_of(cache.shape)), out.data_ptr(),
+                                    lse.data_ptr(), ws, ws_B, handle))
     return out, lse
 
 
@@ -696,21 +770,25 @@ def attend_weights(q, lse, cache: KVCache, scores=None, out=None, workspace=None
     default, whose columns from T on are not written)."""
     import torch
     n, group = _heads(q, cache)
-    _want(lse, "lse", torch.float32, q.shape[:3], q.device)
-    outer = cache.shape[0]
-    for t, name in ((scores, "scores"), (out, "out")):
-        if t is not None:
-            _want(t, name, torch.float32, (outer, t.shape[-1]), q.device)
-    if scores is not None and out is not None and scores.shape != out.shape:
-        raise ValueError("scores and out must have the same shape")
-    with _on(q, stream):
+    dev, ref, outer = q.device, ctypes.byref, cache.shape[0]
+    _want(lse, "lse", torch.float32, tuple(q.shape[:3]), dev)
+    if scores is not None:
+        _want(scores, "scores", torch.float32, (outer, scores.shape[-1]), dev)
+    if out is not None:
+        _want(out, "out", torch.float32, (outer, out.shape[-1]), dev)
+        if scores is not None and scores.shape != out.shape:
+            raise ValueError("scores and out must have the same shape")
+    with _On(q, stream) as handle:
         if out is None:
-            out = torch.empty_like(scores) if scores is not None else torch.empty(
-                (outer, cache.T), dtype=torch.float32, device=q.device)
+            out = torch.empty_like(scores) if scores is not None else torch.empty((outer, cache.T), dtype=torch.float32,
+                                                                                  device=dev)
         if workspace is None:
-            workspace = _empty(kvq_attend_weights_workspace(cache.shape, cache.resid_rows, n, group), q.device)
-        kvq_attend_weights(q, lse, n, group, cache.kv_heads, cache.c(), cache.kqp, cache.shape, scores, out,
-                           out.shape[1], workspace, workspace.numel() * workspace.element_size())
+            workspace = _temporary(_weights_ws(cache.shape, cache.resid_rows, n, group), dev)
+        ws, ws_B = _scratch(workspace, dev)
+        _check(LIB.kvq_attend_weights(q.data_ptr(), lse.data_ptr(), n, group, cache.kv_heads, ref(cache.c()),
+                                      ref(_params_of(cache.kqp)), ref(_shape_of(cache.shape)),
+                                      None if scores is None else scores.data_ptr(), out.data_ptr(), out.shape[1], ws, ws_B,
+                                      handle))
     return out
 
 
@@ -723,20 +801,27 @@ def evict_blocks(cache: KVCache, scores, budget: int, window: int, block: int, d
     import torch
     dst = cache if dst is None else dst
     scores_out = scores if scores_out is None else scores_out
-    outer = cache.shape[0]
-    _want(scores, "scores", torch.float32, (outer, scores.shape[-1]), scores.device)
-    _want(scores_out, "scores_out", torch.float32, scores.shape, scores.device)
-    if tuple(dst.shape) != tuple(cache.shape):
-        raise ValueError("dst must have the cache's shape")
+    dev, ref, outer = scores.device, ctypes.byref, cache.shape[0]
+    _want(scores, "scores", torch.float32, (outer, scores.shape[-1]), dev)
+    if scores_out is not scores:
+        _want(scores_out, "scores_out", torch.float32, tuple(scores.shape), dev)
+    if not scores.is_cuda or cache.k[0].device != dev:
+        raise ValueError("scores must be a CUDA tensor on the cache's device")
+    if dst is not cache and (dst.shape != cache.shape or dst.kqp != cache.kqp or dst.vqp != cache.vqp or
+                             dst.k[0].device != dev):
+        raise ValueError("dst must have the cache's shape, formats and device")
     kept = max(0, min(int(budget), cache.tq // max(int(block), 1)))
     if keep is not None:
-        _want(keep, "keep", torch.int32, (outer, kept), scores.device)
-    with _on(scores, stream):
-        keep = torch.empty((outer, kept), dtype=torch.int32, device=scores.device) if keep is None else keep
+        _want(keep, "keep", torch.int32, (outer, kept), dev)
+    with _On(scores, stream) as handle:
+        if keep is None:
+            keep = torch.empty((outer, kept), dtype=torch.int32, device=dev)
         if workspace is None:
-            workspace = _empty(kvq_evict_blocks_workspace(cache.shape, block), scores.device)
-        dst_c = dst.c()
-        kvq_evict_blocks(cache.c(), dst_c, cache.kqp, cache.vqp, cache.shape, block, budget, window, scores,
-                         scores_out, scores.shape[1], keep, workspace, workspace.numel() * workspace.element_size())
-    dst.tq, dst.nres = dst_c.tq, dst_c.nres
+            workspace = _temporary(_evict_ws(cache.shape, block), dev)
+        ws, ws_B = _scratch(workspace, dev)
+        to = dst.c()
+        _check(LIB.kvq_evict_blocks(ref(cache.c()), ref(to), ref(_params_of(cache.kqp)), ref(_params_of(cache.vqp)),
+                                    ref(_shape_of(cache.shape)), block, budget, window, scores.data_ptr(),
+                                    scores_out.data_ptr(), scores.shape[1], keep.data_ptr(), ws, ws_B, handle))
+    dst.tq, dst.nres = to.tq, to.nres
     return dst, scores_out, keep

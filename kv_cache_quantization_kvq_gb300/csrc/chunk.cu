@@ -21,11 +21,13 @@
 // current ones are used.  m is moved only when it grows by more than 2^8: until
 // then the weights are at most 256, which costs float32 sums and bf16 weights no
 // relative precision, and the output is seldom rescaled.  With one split the CTA
-// writes out and lse; otherwise merge_rows_kernel joins the splits' partial
-// (m, l, y) in split order.
+// writes out and lse; up to eight splits are a thread-block cluster that joins
+// its partial (m, l, y) through distributed shared memory (one launch); more go
+// through the workspace and merge_rows_kernel.  Both join in split order.
 #include <algorithm>
 
 #include "kvq_chunk.cuh"
+#include "kvq_bulk.cuh"
 
 namespace kvq {
 
@@ -35,6 +37,7 @@ using namespace rows;
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
+constexpr int kAhead = 3;                         // batches that the codes are fetched into L2 ahead
 constexpr float kSlack = 8.0f;                   // base-2 growth of the maximum that is let pass
 
 // P.V of one 32-token batch of the store: this lane's code words of its eight
@@ -66,6 +69,39 @@ __device__ __forceinline__ void values_of(float (&y)[MT][C / 8][4], const uint4 
             }
         }
     }
+}
+
+// ---- thread-block clusters
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t remote(const void* p, int rank) {
+    uint32_t a;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
+    return a;
+}
+__device__ __forceinline__ float remote_f(const void* p, int rank) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(remote(p, rank)) : "memory");
+    return v;
+}
+__device__ __forceinline__ float4 remote_f4(const void* p, int rank) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(remote(p, rank)) : "memory");
+    return v;
+}
+
+// out (4 channels) and, with the row's first channels, lse
+template <int C>
+__device__ __forceinline__ void write_row(const ChunkArgs& A, int64_t o, int r, int c4, float M, float L, const float (&v)[4]) {
+    const int64_t at = row_index(A.v, o, r);
+    const float inv = L > 0.0f ? __fdiv_rn(1.0f, L) : 0.0f;
+    *reinterpret_cast<uint2*>(A.out + at * C + c4) =
+        make_uint2(pack_bf16x2(__fmul_rn(v[0], inv), __fmul_rn(v[1], inv)),
+                   pack_bf16x2(__fmul_rn(v[2], inv), __fmul_rn(v[3], inv)));
+    if (A.lse && c4 == 0)
+        A.lse[at] = L > 0.0f ? __fmul_rn(__fadd_rn(M, log2f(L)), 0.6931471805599453f) : -INFINITY;
 }
 
 // Softmax state of a lane's rows (g and g + 8 of each tile).
@@ -136,7 +172,7 @@ attend_rows_kernel(const ChunkArgs A)
     using G = Geo<BITS, C>;
     constexpr int kRowTile = 16 * MT;
     const View& a = A.v;
-    __shared__ float sm[kWarps][16], sl[kWarps][16];
+    __shared__ float sm[kWarps][16], sl[kWarps][16], gm[16], gl[16];
     __shared__ __align__(16) float sy[kWarps][16][C];
     __shared__ __align__(16) uint4 qf[MT * G::kSteps * 32];
     __shared__ __align__(16) uint4 kcs[kWarps][C / 4];
@@ -188,8 +224,8 @@ attend_rows_kernel(const ChunkArgs A)
         st.m[m][0] = st.m[m][1] = -INFINITY;
         st.l[m][0] = st.l[m][1] = 0.0f;
     }
-    const uint8_t* kc = a.kc + (uint64_t)o * a.cap * G::kRowB + tig * (G::kRowB / 4);
-    const uint8_t* vc = a.vc + (uint64_t)o * a.cap * G::kRowB + g * G::kVB;
+    const uint8_t *kc0 = a.kc + (uint64_t)o * a.cap * G::kRowB, *vc0 = a.vc + (uint64_t)o * a.cap * G::kRowB;
+    const uint8_t *kc = kc0 + tig * (G::kRowB / 4), *vc = vc0 + g * G::kVB;
     const int64_t vmeta = o * a.cap * a.ngv;
     const uint32_t kmg = magic<BITS>(a.kflip), vmg = magic<BITS>(a.vflip);
     const uint32_t* vm = &vms[warp][g * (C / 8) / a.gv][0];         // this lane's V group (its C/8 channels lie in one)
@@ -264,6 +300,18 @@ attend_rows_kernel(const ChunkArgs A)
         if (kfast) scores_of<BITS, C, MT, true>(s, kw, qf, kcs[warp], kmg, a.koff, lane);
         else scores_of<BITS, C, MT, false>(s, kw, qf, kcs[warp], kmg, a.koff, lane);
         if (b + 1 < bs) {
+            const int ba = b + kAhead;           // into L2 a few batches ahead: codes, V constants, K group constants
+            if (lane < 8 && ba < bs && (ba + 1) * kBatch <= a.tq) {
+                if (lane < 2) {
+                    bulk_prefetch_l2((lane ? vc0 : kc0) + (int64_t)ba * (kBatch * G::kRowB), kBatch * G::kRowB);
+                } else {
+                    const bool key = lane >= 4;
+                    const __nv_bfloat16* at = (lane & 1) ? (key ? a.kz : a.vz) : (key ? a.ks : a.vs);
+                    const int64_t off = key ? (o * a.ngk + ba * kBatch / a.gk) * C + ((lane & 2) ? C / 2 : 0)
+                                            : vmeta + (int64_t)ba * kBatch * a.ngv;
+                    if (at) asm volatile("prefetch.global.L2 [%0];" ::"l"(at + off));
+                }
+            }
             load_k(b + 1);
             const int gk = (b + 1) * kBatch / a.gk;
             if (gk != fetched) {
@@ -364,19 +412,42 @@ attend_rows_kernel(const ChunkArgs A)
                     v[3] = __fmaf_rn(x.w, f, v[3]);
                 }
             }
-            if (A.nsplit > 1) {
+            if (A.cluster) {
+                *reinterpret_cast<float4*>(&sy[0][row][c4]) = make_float4(v[0], v[1], v[2], v[3]);   // read by this thread only
+                if (c4 == 0) {
+                    gm[row] = M;
+                    gl[row] = L;
+                }
+            } else if (A.nsplit > 1) {
                 float* dst = A.part + ((o * a.rows + r) * A.nsplit + split) * (C + 4);
                 *reinterpret_cast<float4*>(dst + c4) = make_float4(v[0], v[1], v[2], v[3]);
                 if (c4 == 0) *reinterpret_cast<float2*>(dst + C) = make_float2(M, L);
             } else {
-                const int64_t at = row_index(a, o, r);
-                const float inv = L > 0.0f ? __fdiv_rn(1.0f, L) : 0.0f;
-                *reinterpret_cast<uint2*>(A.out + at * C + c4) =
-                    make_uint2(pack_bf16x2(__fmul_rn(v[0], inv), __fmul_rn(v[1], inv)),
-                               pack_bf16x2(__fmul_rn(v[2], inv), __fmul_rn(v[3], inv)));
-                if (A.lse && c4 == 0)
-                    A.lse[at] = L > 0.0f ? __fmul_rn(__fadd_rn(M, log2f(L)), 0.6931471805599453f) : -INFINITY;
+                write_row<C>(A, o, r, c4, M, L, v);
             }
+        }
+        if (A.cluster) {                         // block rank = split; each takes its share of the rows' pieces
+            cluster_sync();
+            for (int k = split * kThreads + tid; k < 16 * (C / 4); k += A.nsplit * kThreads) {
+                const int row = k / (C / 4), c4 = (k % (C / 4)) * 4, r = r0 + 16 * m + row;
+                if (r >= a.rows) break;
+                float M = -INFINITY;
+                for (int s = 0; s < A.nsplit; ++s) M = fmaxf(M, remote_f(&gm[row], s));
+                float L = 0.0f, v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                if (M != -INFINITY) {
+                    for (int s = 0; s < A.nsplit; ++s) {
+                        const float f = ex2(__fsub_rn(remote_f(&gm[row], s), M));
+                        const float4 x = remote_f4(&sy[0][row][c4], s);
+                        L = __fmaf_rn(remote_f(&gl[row], s), f, L);
+                        v[0] = __fmaf_rn(x.x, f, v[0]);
+                        v[1] = __fmaf_rn(x.y, f, v[1]);
+                        v[2] = __fmaf_rn(x.z, f, v[2]);
+                        v[3] = __fmaf_rn(x.w, f, v[3]);
+                    }
+                }
+                write_row<C>(A, o, r, c4, M, L, v);
+            }
+            cluster_sync();                      // nobody leaves, or writes the next tile, before all have read
         }
     }
 }
@@ -395,8 +466,9 @@ merge_rows_kernel(const ChunkArgs A, int64_t total)
 // take tiles of 32 (two), which unpack each key and value once for 32 rows.
 // Splits of the visible batches: the number that gives the shortest run through
 // all waves, counting about three batches for a CTA's start and end.
-struct RowsPlan { int64_t mt, ntiles, nsplit; };
+struct RowsPlan { int64_t mt, ntiles, nsplit; bool cluster; };
 
+constexpr int64_t kCluster = 8;                   // most splits that a cluster joins
 constexpr int64_t kMaxWaves = 2;                 // more CTAs than this are not split further
 
 int64_t slots_of(int64_t mt) { return 152 * (mt == 1 ? 3 : 2); }
@@ -410,11 +482,17 @@ RowsPlan rows_plan(int64_t outer, int64_t T, int64_t rows)
     const int64_t nb = (T + kBatch - 1) / kBatch + 1;
     int64_t best = INT64_MAX;
     p.nsplit = 1;
+    p.cluster = false;
     for (int64_t s = 1; s == 1 || (ctas * s <= kMaxWaves * slots && s * kWarps <= nb); ++s) {
-        const int64_t cost = ((ctas * s + slots - 1) / slots) * ((nb + s * kWarps - 1) / (s * kWarps) + 3);
+        // clusters must find their SMs together: on a full GPU (448 CTAs in clusters of 7) they
+        // cost 73 us where two launches take 56, on 64 CTAs they save the second launch (5 us)
+        const bool cluster = s > 1 && s <= kCluster && 2 * ctas * s <= slots;
+        const int64_t cost = ((ctas * s + slots - 1) / slots) * ((nb + s * kWarps - 1) / (s * kWarps) + 3) +
+                             (s > 1 && !cluster ? 3 : 0);
         if (cost < best) {
             best = cost;
             p.nsplit = s;
+            p.cluster = cluster;
         }
     }
     return p;
@@ -428,9 +506,20 @@ cudaError_t launch_rows(ChunkArgs A, int64_t outer, cudaStream_t st)
     A.nsplit = (int32_t)p.nsplit;
     const int64_t grid = outer * p.ntiles * p.nsplit;
     if (grid > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
-    if (p.mt == 1) attend_rows_kernel<BITS, C, 1><<<(unsigned)grid, kThreads, 0, st>>>(A);
-    else attend_rows_kernel<BITS, C, 2><<<(unsigned)grid, kThreads, 0, st>>>(A);
-    if (p.nsplit > 1) {
+    A.cluster = p.cluster;
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim = {(unsigned)(A.cluster ? p.nsplit : 1), 1, 1};
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = st;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    const cudaError_t e = p.mt == 1 ? cudaLaunchKernelEx(&cfg, attend_rows_kernel<BITS, C, 1>, A)
+                                    : cudaLaunchKernelEx(&cfg, attend_rows_kernel<BITS, C, 2>, A);
+    if (e != cudaSuccess) return e;
+    if (p.nsplit > 1 && !p.cluster) {
         const int64_t total = outer * A.v.rows;
         merge_rows_kernel<C><<<(unsigned)((total + kWarps - 1) / kWarps), kThreads, 0, st>>>(A, total);
     }

@@ -5,7 +5,9 @@
 // window; "KV cache 压缩：把历史装得更小" §"少存 token：合并，或淘汰": the dropped
 // entries' K and V are freed.
 //
-// select_blocks_kernel, a CTA per slice: block scores in binary64, an
+// select_blocks_kernel, a CTA per slice: block scores as unevaluated sums of two
+// float32 (error-free additions: 46 bits or so; in binary64, whose units are
+// few here, the sums took 90 of 110 us for 128 slices of 32768 tokens), an
 // order-preserving 64-bit key each, a radix search for the key of the last kept
 // block (8 bits a pass, until the remaining bin is taken whole), ties by index,
 // and an ordered scan that writes the ascending keep list; it also counts what
@@ -26,15 +28,31 @@ namespace kvq {
 
 namespace {
 
-constexpr int kSelThreads = 512;
+constexpr int kSelThreads = 1024;
+constexpr int kSumAhead = 4;                     // blocks whose scores a warp has in flight
 constexpr int kMoveThreads = 256;
 constexpr int kAhead = 8;                        // loads in flight per thread
 
-// ascending order of keys = ascending order of scores, NaN lowest, -0 = +0
-__device__ __forceinline__ unsigned long long key_of(double s) {
-    if (s != s) return 0ull;
-    const long long b = __double_as_longlong(s + 0.0);
-    return b < 0 ? ~(unsigned long long)b : (unsigned long long)b | 0x8000000000000000ull;
+// ascending order of keys = ascending order of scores hi + lo (|lo| <= ulp(hi) / 2),
+// NaN lowest, -0 = +0
+__device__ __forceinline__ uint32_t order_of(float x) {
+    const int b = __float_as_int(__fadd_rn(x, 0.0f));
+    return b < 0 ? ~(uint32_t)b : (uint32_t)b | 0x80000000u;
+}
+__device__ __forceinline__ unsigned long long key_of(float hi, float lo) {
+    if (hi != hi) return 0ull;
+    // the sum of an infinite or overflowed block has no low part
+    return ((unsigned long long)order_of(hi) << 32) | order_of(fabsf(hi) == INFINITY ? 0.0f : lo);
+}
+// (hi, lo) += x, and (hi, lo) += (h, l): error-free sums (Knuth), the low parts rounded
+__device__ __forceinline__ void add_to(float& hi, float& lo, float x) {
+    const float s = __fadd_rn(hi, x), t = __fsub_rn(s, hi);
+    lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(hi, __fsub_rn(s, t)), __fsub_rn(x, t)));
+    hi = s;
+}
+__device__ __forceinline__ void join_to(float& hi, float& lo, float h, float l) {
+    add_to(hi, lo, h);
+    lo = __fadd_rn(lo, l);
 }
 
 // exclusive prefix sum of one flag word per thread over the CTA; total in *sum
@@ -79,14 +97,35 @@ select_blocks_kernel(const EvictArgs A)
     unsigned long long prefix = 0;
     int shift = 64;                              // key bits below `shift` are still open
     if (need > 0 && need < cand) {
-        // ---- block scores: a warp per block, lanes' partial sums joined in lane order
-        for (int b = warp; b < cand; b += kSelThreads / 32) {
-            const float* p = A.scores_in + o * A.stride + (int64_t)b * A.block;
-            double s = 0.0;
-            for (int64_t t = lane; t < A.block; t += 32) s += (double)p[t];
+        // ---- block scores: a warp takes kSumAhead blocks at a time, 32 tokens of each a step
+        for (int b0 = warp * kSumAhead; b0 < cand; b0 += kSelThreads / 32 * kSumAhead) {
+            const float* p = A.scores_in + o * A.stride + (int64_t)b0 * A.block;
+            float hi[kSumAhead], lo[kSumAhead];
 #pragma unroll
-            for (int x = 1; x < 32; x <<= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, x);
-            if (lane == 0) key[b] = key_of(s);
+            for (int i = 0; i < kSumAhead; ++i) hi[i] = lo[i] = 0.0f;
+            for (int64_t t = lane; t < A.block; t += 64) {
+                float x[kSumAhead][2];
+#pragma unroll
+                for (int i = 0; i < kSumAhead; ++i) {
+                    const float* at = p + i * A.block + t;
+                    x[i][0] = b0 + i < cand ? at[0] : 0.0f;
+                    x[i][1] = b0 + i < cand && t + 32 < A.block ? at[32] : 0.0f;
+                }
+#pragma unroll
+                for (int i = 0; i < kSumAhead; ++i) {
+                    add_to(hi[i], lo[i], x[i][0]);
+                    add_to(hi[i], lo[i], x[i][1]);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kSumAhead; ++i) {
+#pragma unroll
+                for (int x = 16; x > 0; x >>= 1)
+                    join_to(hi[i], lo[i], __shfl_down_sync(0xFFFFFFFFu, hi[i], x), __shfl_down_sync(0xFFFFFFFFu, lo[i], x));
+                const float s = __fadd_rn(hi[i], lo[i]);             // renormalised: lo is what hi misses
+                lo[i] = __fsub_rn(lo[i], __fsub_rn(s, hi[i]));
+                if (lane == 0 && b0 + i < cand) key[b0 + i] = key_of(fabsf(hi[i]) == INFINITY || hi[i] != hi[i] ? hi[i] : s, lo[i]);
+            }
         }
         // ---- radix search, most significant digit first
         for (bool done = false; !done && shift > 0;) {

@@ -13,7 +13,7 @@ struct ChunkArgs {
     __nv_bfloat16* out;
     float* lse;              // or nullptr
     float* part;             // [row][split][C + 4]: y, m, l
-    int32_t nsplit, ntiles;
+    int32_t nsplit, ntiles, cluster;
 };
 
 rows::View cache_view(const CacheArgs& x);

@@ -42,6 +42,7 @@ weights_rows_kernel(const WeightArgs A)
     const View& a = A.v;
     __shared__ __align__(16) uint4 qf[kMaxTiles * G::kSteps * 32];
     __shared__ float nlse[kMaxTiles * 16];       // -lse in base 2; -inf: no weight
+    __shared__ int lasts[kMaxTiles * 16];        // the last token a row sees
     __shared__ __align__(16) uint4 kcs[kWarps][C / 4];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, tig = lane & 3;
@@ -59,6 +60,7 @@ weights_rows_kernel(const WeightArgs A)
             l = l == -INFINITY ? -INFINITY : -__fmul_rn(l, kLog2e);
         }
         nlse[r] = l;
+        lasts[r] = base + r / a.group;
     }
     // ---- this warp's run of batches
     const int k = run * kWarps + warp, of = A.nrun * kWarps;
@@ -103,13 +105,14 @@ weights_rows_kernel(const WeightArgs A)
 
         auto add = [&](const float (&s)[1][4][4], int t) {
             const float la = nlse[16 * t + g], lb = nlse[16 * t + g + 8];
-            const int ra = base + (16 * t + g) / a.group, rb = base + (16 * t + g + 8) / a.group;
-            const bool whole = t0 >= first && t1 - t0 == kBatch && t1 - 1 <= base + 16 * t / a.group;
+            const int ra = lasts[16 * t + g], rb = lasts[16 * t + g + 8];
+            const bool whole = t0 >= first && t1 - t0 == kBatch && t1 - 1 <= lasts[16 * t];
+            const bool two = 16 * t + 8 < a.rows;                   // rows g + 8 exist
 #pragma unroll
             for (int j = 0; j < 4; ++j)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    float wa = ex2(__fmaf_rn(s[0][j][e], a.scale2, la)), wb = ex2(__fmaf_rn(s[0][j][2 + e], a.scale2, lb));
+                    float wa = ex2(__fmaf_rn(s[0][j][e], a.scale2, la)), wb = two ? ex2(__fmaf_rn(s[0][j][2 + e], a.scale2, lb)) : 0.0f;
                     if (!whole) {                // selected: a hidden token's score may be NaN
                         const int tok = t0 + 8 * j + 2 * tig + e;
                         const bool live = tok >= first && tok < t1;
@@ -121,7 +124,7 @@ weights_rows_kernel(const WeightArgs A)
         };
         if (seen) {
             for (int t = 0; t < A.ntiles; ++t) {
-                if (base + (min(16 * t + 16, a.rows) - 1) / a.group < t0) continue;  // the tile sees none of the batch
+                if (lasts[min(16 * t + 16, a.rows) - 1] < t0) continue;  // the tile sees none of the batch
                 float s[1][4][4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) s[0][j][0] = s[0][j][1] = s[0][j][2] = s[0][j][3] = 0.0f;
