@@ -118,6 +118,47 @@ struct TcArgs {
     ChunkArgs A;                                 // nsplit: of the split tiles
     int64_t o0, slices, Tp;
     int32_t nwhole;                              // query tiles taken whole; the others are split
+    int32_t trows;                               // rows of a tile that partial results are kept for
+};
+
+// The query tile and split of a CTA.
+struct TileOf {
+    int tile, split, nsplit, r0, nrows, nt;      // tile of up to 256 rows from r0; nt row tiles of 128 in use
+    int64_t so, o;                               // slice of this launch, slice
+    __device__ __forceinline__ explicit TileOf(const TcArgs& X) {
+        tile = blockIdx.x;                       // the longest of a slice first
+        split = 0;
+        nsplit = 1;
+        if (tile >= X.nwhole) {
+            nsplit = X.A.nsplit;
+            split = (tile - X.nwhole) % nsplit;
+            tile = X.nwhole + (tile - X.nwhole) / nsplit;
+        }
+        so = tile / X.A.ntiles;
+        o = X.o0 + so;
+        r0 = (X.A.ntiles - 1 - tile % X.A.ntiles) * 2 * kTile;
+        nrows = min(2 * kTile, X.A.v.rows - r0);
+        nt = nrows > kTile ? 2 : 1;
+    }
+    // the key tiles [j0, j0 + n) it sees; returns the first token that is not padding
+    __device__ __forceinline__ int keys(const TcArgs& X, int& j0, int& n) const {
+        const View& a = X.A.v;
+        const int first = a.first ? max(a.first[o], 0) : 0;
+        const int last_hi = a.T - a.n + (r0 + nrows - 1) / a.group;
+        int j1 = 0;
+        j0 = 0;
+        if (first <= last_hi) {
+            j0 = first / kTile;
+            j1 = last_hi / kTile + 1;
+        }
+        const int64_t len = j1 - j0;
+        n = (int)(len * (split + 1) / nsplit) - (int)(len * split / nsplit);
+        j0 += (int)(len * split / nsplit);
+        return first;
+    }
+    __device__ __forceinline__ float* part(const TcArgs& X, int r, int C) const {
+        return X.A.part + (((int64_t)(tile - X.nwhole) * X.trows + (r - r0)) * nsplit + split) * (C + 4);
+    }
 };
 
 template <int C>
@@ -139,34 +180,11 @@ attend_tc_kernel(const TcArgs X, const __grid_constant__ CUtensorMap kmap, const
     const ChunkArgs& A = X.A;
     const View& a = A.v;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    int tile = blockIdx.x, split = 0, nsplit = 1;                   // tiles of 256 rows, the longest of a slice first
-    if (tile >= X.nwhole) {
-        nsplit = A.nsplit;
-        split = (tile - X.nwhole) % nsplit;
-        tile = X.nwhole + (tile - X.nwhole) / nsplit;
-    }
-    const int rt = A.ntiles - 1 - tile % A.ntiles;
-    const int64_t so = tile / A.ntiles, o = X.o0 + so;
-    const int r0 = rt * 2 * kTile;
-    const int nrows = min(2 * kTile, a.rows - r0);
-    const int nt = nrows > kTile ? 2 : 1;        // row tiles in use
-
-    // ---- the key tiles this CTA sees
-    const int base = a.T - a.n;
-    const int first = a.first ? max(a.first[o], 0) : 0;
-    const int last_hi = base + (r0 + nrows - 1) / a.group;
-    int j0 = 0, j1 = 0;
-    if (first <= last_hi) {
-        j0 = first / kTile;
-        j1 = last_hi / kTile + 1;
-    }
-    {
-        const int64_t len = j1 - j0;
-        const int e = j0 + (int)(len * (split + 1) / nsplit);
-        j0 += (int)(len * split / nsplit);
-        j1 = e;
-    }
-    const int n = j1 - j0;
+    const TileOf w(X);
+    const int64_t so = w.so, o = w.o;
+    const int r0 = w.r0, nrows = w.nrows, nt = w.nt, nsplit = w.nsplit, base = a.T - a.n;
+    int j0, n;
+    const int first = w.keys(X, j0, n), j1 = j0 + n;
 
     // ---- setup: barriers, tensor memory, the query rows
     if (tid == 0) {
@@ -359,7 +377,7 @@ attend_tc_kernel(const TcArgs X, const __grid_constant__ CUtensorMap kmap, const
         }
         const bool write = ok && r < a.rows;
         const int64_t at = write ? row_index(a, o, r) : 0;
-        float* part = A.part + (((int64_t)(tile - X.nwhole) * 2 * kTile + (r - r0)) * nsplit + split) * (C + 4);
+        float* part = w.part(X, r, C);
         const float inv = l > 0.0f ? __fdiv_rn(1.0f, l) : 0.0f;
 #pragma unroll
         for (int c = 0; c < C / 32; ++c) {
@@ -400,20 +418,415 @@ attend_tc_kernel(const TcArgs X, const __grid_constant__ CUtensorMap kmap, const
     if (warp == 9) tc::dealloc(tmem, 512);
 }
 
+// ---------------------------------------------------------------- fused form
+// The same without the expansion, for fewer query rows: eight fill warps turn
+// the packed codes into the swizzled bf16 tiles themselves (warps 12-15 the
+// keys, 16-19 the values), so the cache is read once, as codes.  Per 128-token
+// tile that is 32768 values, four instructions a pair: about as long as the
+// products of 256 rows take, so more rows are better served by expanding once.
+// Within every 8 channels the tiles hold them in the order 0 4 1 5 2 6 3 7 in
+// which a code word gives them up; the query rows are staged, and the output is
+// written, accordingly.  With 640 threads a softmax thread has 96 registers and
+// reads its 128 scores twice, 32 at a time.
+constexpr int kFusedWarps = 20;
+constexpr int kFusedThreads = kFusedWarps * 32;
+
+template <int C>
+struct SmemF {
+    static constexpr int kTileB = kTile * C * 2;
+    static constexpr int kQ = 0, kK = 2 * kTileB, kV = kK + 2 * kTileB, kBars = kV + 2 * kTileB;    // two K, two V tiles
+    static constexpr int kBytes = kBars + 256 + 1024;
+};
+
+// 0 4 1 5 2 6 3 7 from eight bf16 in order
+__device__ __forceinline__ uint4 interleave(const uint4& x) {
+    return make_uint4(__byte_perm(x.x, x.z, 0x5410), __byte_perm(x.x, x.z, 0x7632), __byte_perm(x.y, x.w, 0x5410),
+                      __byte_perm(x.y, x.w, 0x7632));
+}
+
+// eight fields of a token's 8-channel piece, (i, i + 4) at bits BITS i of the halves
+template <int BITS>
+__device__ __forceinline__ uint32_t load_piece(const uint8_t* p) {
+    if constexpr (BITS == 4) return __ldcs(reinterpret_cast<const uint32_t*>(p));
+    else return __byte_perm((uint32_t)__ldcs(reinterpret_cast<const uint16_t*>(p)), 0u, 0x4140);
+}
+
+// one piece: values of fields (i, i + 4), i = 0 .. 3, with their scale and zero pairs
+template <int BITS>
+__device__ __forceinline__ uint4 unpack_piece(uint32_t w, bool fast, uint32_t mg, const uint32_t (&s)[4],
+                                              const uint32_t (&z)[4], float off) {
+    uint32_t r[4];
+    if (fast) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) r[i] = value_pair<BITS, true>(w, BITS * i, mg, s[i], z[i], off);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) r[i] = value_pair<BITS, false>(w, BITS * i, mg, s[i], z[i], off);
+    }
+    return make_uint4(r[0], r[1], r[2], r[3]);
+}
+
+// Tokens [t0, t0 + 128) of one cache as a swizzled tile, by 128 threads: a
+// thread takes 8-channel piece p of every (1024 / C)-th token, eight loads ahead.
+template <int BITS, int C, bool KEYS>
+__device__ __forceinline__ void fill_tile(const View& a, int64_t o, int t0, int first, unsigned char* tile, int tid) {
+    constexpr int P = C / 8, kStep = 128 / P, kAhead = 32 / kStep;  // rows a pass, passes of 32 tokens
+    const int p = tid % P, r0 = tid / P;
+    unsigned char* dst = tile + (p / 8) * (kTile * 128);
+    const uint8_t* codes = (KEYS ? a.kc : a.vc) + (uint64_t)o * a.cap * (C * BITS / 8) + p * BITS;
+    const uint32_t mg = magic<BITS>(KEYS ? a.kflip : a.vflip);
+    const float off = KEYS ? a.koff : a.voff;
+    const int vg = KEYS ? 0 : p * 8 / a.gv;
+    if (t0 >= first && t0 + kTile <= a.tq) {
+        // ---- wholly in the store: 32 tokens (of one key group) at a time, the next ones loading
+        uint32_t w[2][kAhead];
+        uint4 ks[2], kz[2];
+        uint32_t vm[2][kAhead];
+        auto fetch = [&](int q, int b) {
+            const int t = t0 + 32 * q + r0;
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                w[b][i] = load_piece<BITS>(codes + (int64_t)(t + i * kStep) * (C * BITS / 8));
+                if constexpr (!KEYS) {
+                    const int64_t at = (o * a.cap + t + i * kStep) * a.ngv + vg;
+                    vm[b][i] = bits_of(a.vs + at) | (a.vz ? bits_of(a.vz + at) << 16 : 0u);
+                }
+            }
+            if constexpr (KEYS) {
+                const int64_t at = (o * a.ngk + (t0 + 32 * q) / a.gk) * C + p * 8;
+                ks[b] = *reinterpret_cast<const uint4*>(a.ks + at);
+                kz[b] = a.kz ? *reinterpret_cast<const uint4*>(a.kz + at) : make_uint4(0, 0, 0, 0);
+            }
+        };
+        fetch(0, 0);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int b = q & 1;
+            if (q < 3) fetch(q + 1, b ^ 1);
+            if constexpr (KEYS) {
+                const uint4 s4 = interleave(ks[b]), z4 = interleave(kz[b]);
+                const uint32_t s[4] = {s4.x, s4.y, s4.z, s4.w};
+                uint32_t z[4] = {z4.x, z4.y, z4.z, z4.w};
+                bool fast = true;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) fast = fast && zero_exact(bf_lo(z[i])) && zero_exact(bf_hi(z[i]));
+                if (fast) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) z[i] = biased(z[i], 128.0f + off);
+                }
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i)
+                    *reinterpret_cast<uint4*>(dst + tc::swizzled(32 * q + r0 + i * kStep, p % 8)) =
+                        unpack_piece<BITS>(w[b][i], fast, mg, s, z, off);
+            } else {
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i) {
+                    const uint32_t s1 = __byte_perm(vm[b][i], 0u, 0x1010);
+                    uint32_t z1 = __byte_perm(vm[b][i], 0u, 0x3232);
+                    const bool fast = zero_exact(bf_lo(z1));
+                    if (fast) z1 = biased(z1, 128.0f + off);
+                    const uint32_t s[4] = {s1, s1, s1, s1}, z[4] = {z1, z1, z1, z1};
+                    *reinterpret_cast<uint4*>(dst + tc::swizzled(32 * q + r0 + i * kStep, p % 8)) =
+                        unpack_piece<BITS>(w[b][i], fast, mg, s, z, off);
+                }
+            }
+        }
+    } else {
+        // ---- at the padding, the store's end or in the buffer: token by token; hidden and missing ones are zeros
+#pragma unroll 1
+        for (int r = r0; r < kTile; r += kStep) {
+            const int t = t0 + r;
+            uint4 x = make_uint4(0, 0, 0, 0);
+            if (t >= first && t < a.T) {
+                if (t >= a.tq) {
+                    x = interleave(*reinterpret_cast<const uint4*>((KEYS ? a.kr : a.vr) +
+                                                                   ((uint64_t)o * a.rrows + (t - a.tq)) * C + p * 8));
+                } else {
+                    uint32_t s[4], z[4];
+                    bool fast = true;
+                    if constexpr (KEYS) {
+                        const int64_t at = (o * a.ngk + t / a.gk) * C + p * 8;
+                        const uint4 s4 = interleave(*reinterpret_cast<const uint4*>(a.ks + at));
+                        const uint4 z4 = interleave(a.kz ? *reinterpret_cast<const uint4*>(a.kz + at) : make_uint4(0, 0, 0, 0));
+                        s[0] = s4.x; s[1] = s4.y; s[2] = s4.z; s[3] = s4.w;
+                        z[0] = z4.x; z[1] = z4.y; z[2] = z4.z; z[3] = z4.w;
+                    } else {
+                        const int64_t at = (o * a.cap + t) * a.ngv + vg;
+                        s[0] = s[1] = s[2] = s[3] = bits_of(a.vs + at) * 0x10001u;
+                        z[0] = z[1] = z[2] = z[3] = a.vz ? bits_of(a.vz + at) * 0x10001u : 0u;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) fast = fast && zero_exact(bf_lo(z[i])) && zero_exact(bf_hi(z[i]));
+                    if (fast) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) z[i] = biased(z[i], 128.0f + off);
+                    }
+                    x = unpack_piece<BITS>(load_piece<BITS>(codes + (int64_t)t * (C * BITS / 8)), fast, mg, s, z, off);
+                }
+            }
+            *reinterpret_cast<uint4*>(dst + tc::swizzled(r, p % 8)) = x;
+        }
+    }
+}
+
+template <int BITS, int C>
+__global__ void __launch_bounds__(kFusedThreads, 1)
+attend_fused_kernel(const TcArgs X)
+{
+    using S = SmemF<C>;
+    extern __shared__ unsigned char raw[];
+    unsigned char* sm = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
+    uint64_t* kfull = reinterpret_cast<uint64_t*>(sm + S::kBars);  // [2] a key tile is in shared memory (4 warps)
+    uint64_t* kfree = kfull + 2;                 // [2] every row tile is done with it
+    uint64_t* vfull = kfree + 2;
+    uint64_t* vfree = vfull + 2;
+    uint64_t* sfull = vfree + 2;                 // [2] per row tile, as in attend_tc_kernel
+    uint64_t* pfull = sfull + 2;
+    uint64_t* odone = pfull + 2;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(odone + 2);
+    volatile int* gone = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+    const ChunkArgs& A = X.A;
+    const View& a = A.v;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const TileOf w(X);
+    const int64_t o = w.o;
+    const int r0 = w.r0, nrows = w.nrows, nt = w.nt, base = a.T - a.n;
+    int j0, n;
+    const int first = w.keys(X, j0, n);
+
+    if (tid == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&kfull[i], 4);
+            mbar_init(&kfree[i], nt);
+            mbar_init(&vfull[i], 4);
+            mbar_init(&vfree[i], nt);
+            mbar_init(&sfull[i], 1);
+            mbar_init(&pfull[i], 4);
+            mbar_init(&odone[i], 1);
+        }
+        *gone = 0;
+        mbar_init_fence();
+    }
+    if (warp == 8) tc::alloc(tmem_slot, 512);
+    if (warp < 12)
+        for (int k = tid; k < nt * kTile * (C / 8); k += 384) {
+            const int r = k / (C / 8), c = k % (C / 8);
+            uint4 x = make_uint4(0, 0, 0, 0);
+            if (r < nrows) x = interleave(*reinterpret_cast<const uint4*>(a.q + row_index(a, o, r0 + r) * C + c * 8));
+            *reinterpret_cast<uint4*>(sm + S::kQ + (r / kTile) * S::kTileB + (c / 8) * (kTile * 128) +
+                                      tc::swizzled(r % kTile, c % 8)) = x;
+        }
+    tc::async_fence();
+    tc::before_sync();
+    __syncthreads();
+    tc::after_sync();
+    const uint32_t tmem = *tmem_slot;
+    auto ready = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xFFFFFFFFu, tc::wait(bar, parity, gone)) != 0; };
+
+    if (warp >= 12) {
+        // ---- fill
+        const bool keys = warp < 16;
+        uint64_t* full = keys ? kfull : vfull;
+        uint64_t* free = keys ? kfree : vfree;
+        for (int j = 0; j < n; ++j) {
+            const int s = j & 1;
+            if (j >= 2 && !ready(&free[s], ((j >> 1) - 1) & 1)) break;
+            unsigned char* tile = sm + (keys ? S::kK : S::kV) + s * S::kTileB;
+            if (keys) fill_tile<BITS, C, true>(a, o, (j0 + j) * kTile, first, tile, tid & 127);
+            else fill_tile<BITS, C, false>(a, o, (j0 + j) * kTile, first, tile, tid & 127);
+            tc::async_fence();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&full[s]);
+        }
+    } else if (warp >= 8) {
+        // ---- products of row tile t (warps 8 and 9)
+        const int t = warp - 8;
+        if (t < nt && n > 0) {
+            constexpr uint32_t kScores = tc::instr_desc(kTile, kTile, false), kValues = tc::instr_desc(kTile, C, true);
+            const uint32_t q_at = smem_u32(sm + S::kQ) + t * S::kTileB, k_at = smem_u32(sm + S::kK), v_at = smem_u32(sm + S::kV);
+            const uint32_t s_at = tmem + t * kTile, o_at = tmem + 256 + t * C;
+            auto scores = [&](int s) {
+#pragma unroll
+                for (int k = 0; k < C / 16; ++k) {
+                    const uint32_t at = (k / 4) * (kTile * 128) + (k % 4) * 32;
+                    tc::mma_ss(s_at, tc::smem_desc(q_at + at, 16), tc::smem_desc(k_at + s * S::kTileB + at, 16), kScores, k > 0);
+                }
+                tc::commit(&sfull[t]);
+                tc::commit(&kfree[s]);
+            };
+            bool ok = ready(&kfull[0], 0);
+            tc::after_sync();
+            if (ok && tc::elect()) scores(0);
+            __syncwarp();
+            for (int j = 0; ok && j < n; ++j) {
+                const int s = j & 1;
+                if (j + 1 < n) ok = ready(&kfull[s ^ 1], ((j + 1) >> 1) & 1);
+                ok = ok && ready(&vfull[s], (j >> 1) & 1) && ready(&pfull[t], j & 1);
+                if (!ok) break;
+                tc::after_sync();
+                if (tc::elect()) {
+#pragma unroll
+                    for (int k = 0; k < kTile / 16; ++k)
+                        tc::mma_ts(o_at, s_at + k * 8, tc::smem_desc(v_at + s * S::kTileB + k * 2048, kTile * 128), kValues,
+                                   j > 0 || k > 0);
+                    tc::commit(&vfree[s]);
+                    if (j + 1 < n) scores(s ^ 1);
+                    else tc::commit(&odone[t]);
+                }
+                __syncwarp();
+            }
+        }
+    } else if (warp < 4 * nt) {
+        // ---- softmax of row tile t, a thread per row
+        const int t = warp / 4;
+        const int r = r0 + t * kTile + (warp & 3) * 32 + lane;
+        const int last = r < a.rows ? base + r / a.group : a.T;
+        const int tile_lo = base + (r0 + t * kTile) / a.group;
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t s_at = tmem + lanes + t * kTile, o_at = tmem + lanes + 256 + t * C;
+        float m = -INFINITY;
+        u64 sum = 0;
+        bool ok = true;
+        for (int j = 0; ok && j < n; ++j) {
+            ok = ready(&sfull[t], j & 1);
+            if (!ok) break;
+            tc::after_sync();
+            const int c0 = (j0 + j) * kTile;
+            const bool cut = c0 < first || c0 + kTile - 1 > tile_lo;
+            // tokens [lo, hi] of the tile are seen
+            const int lo = first - c0, hi = last - c0;
+            float x0 = -INFINITY, x1 = -INFINITY;
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+                uint32_t s[32];
+                tc::ld32(s_at + 32 * h, s);
+                tc::wait_ld();
+                if (cut) {
+#pragma unroll
+                    for (int c = 0; c < 32; ++c)
+                        if (32 * h + c < lo || 32 * h + c > hi) s[c] = 0xFF800000u;  // -inf
+                }
+#pragma unroll
+                for (int c = 0; c < 32; c += 2) {
+                    x0 = fmaxf(x0, __uint_as_float(s[c]));
+                    x1 = fmaxf(x1, __uint_as_float(s[c + 1]));
+                }
+            }
+            const float top = __fmul_rn(fmaxf(x0, x1), a.scale2);
+            const bool grow = top > __fadd_rn(m, kSlack);
+            if (__any_sync(0xFFFFFFFFu, grow)) {
+                const float f = grow ? ex2(__fsub_rn(m, top)) : 1.0f;
+                if (grow) m = top;
+                sum = mul2(sum, pk(f, f));
+                if (j > 0) {
+#pragma unroll
+                    for (int c = 0; c < C / 32; ++c) {
+                        uint32_t y[32];
+                        tc::ld32(o_at + 32 * c, y);
+                        tc::wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) y[i] = __float_as_uint(__fmul_rn(__uint_as_float(y[i]), f));
+                        tc::st32(o_at + 32 * c, y);
+                    }
+                }
+            }
+            const float neg = m == -INFINITY ? 0.0f : -m;
+            const u64 sc2 = pk(a.scale2, a.scale2), ng2 = pk(neg, neg);
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {        // 32 scores -> 16 columns of weight pairs, over scores read already
+                uint32_t s[32], p[16];
+                tc::ld32(s_at + 32 * h, s);
+                tc::wait_ld();
+                if (cut) {
+#pragma unroll
+                    for (int c = 0; c < 32; ++c)
+                        if (32 * h + c < lo || 32 * h + c > hi) s[c] = 0xFF800000u;
+                }
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const u64 e = fma2(pk(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), sc2, ng2);
+                    const float e0 = ex2(lo_of(e)), e1 = ex2(hi_of(e));
+                    sum = add2(sum, pk(e0, e1));
+                    p[i] = pack_bf16x2(e0, e1);
+                }
+                tc::st16(s_at + 16 * h, p);
+            }
+            tc::wait_st();
+            tc::before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&pfull[t]);
+        }
+        // ---- output
+        float l = 0.0f;
+        if (ok && n > 0) {
+            ok = ready(&odone[t], 0);
+            tc::after_sync();
+            l = __fadd_rn(lo_of(sum), hi_of(sum));
+        }
+        const bool write = ok && r < a.rows;
+        const int64_t at = write ? row_index(a, o, r) : 0;
+        float* part = w.part(X, r, C);
+        const float inv = l > 0.0f ? __fdiv_rn(1.0f, l) : 0.0f;
+#pragma unroll
+        for (int c = 0; c < C / 32; ++c) {
+            uint32_t y[32];
+            if (ok && n > 0) {
+                tc::ld32(o_at + 32 * c, y);
+                tc::wait_ld();
+            } else {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) y[i] = 0u;
+            }
+            if (write) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {    // channels 0 .. 7 sit in columns 0 2 4 6 1 3 5 7
+                    const uint32_t* z = y + 8 * i;
+                    if (w.nsplit > 1) {
+                        *reinterpret_cast<uint4*>(part + 32 * c + 8 * i) = make_uint4(z[0], z[2], z[4], z[6]);
+                        *reinterpret_cast<uint4*>(part + 32 * c + 8 * i + 4) = make_uint4(z[1], z[3], z[5], z[7]);
+                    } else {
+                        float v[8];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            v[k] = __fmul_rn(__uint_as_float(z[2 * k]), inv);
+                            v[4 + k] = __fmul_rn(__uint_as_float(z[2 * k + 1]), inv);
+                        }
+                        store8(A.out + at * C + 32 * c + 8 * i, v);
+                    }
+                }
+            }
+            __syncwarp();
+        }
+        if (write && w.nsplit > 1) *reinterpret_cast<float2*>(part + C) = make_float2(m, l);
+        if (write && w.nsplit == 1 && A.lse)
+            A.lse[at] = l > 0.0f ? __fmul_rn(__fadd_rn(m, log2f(l)), 0.6931471805599453f) : -INFINITY;
+    }
+    __syncwarp();
+    tc::before_sync();
+    __syncthreads();
+    tc::after_sync();
+    if (warp == 8) tc::dealloc(tmem, 512);
+}
+
 // One warp per row of the split query tiles joins their partial results.
 template <int C>
 __global__ void __launch_bounds__(256)
-merge_tiles_kernel(const TcArgs X)
+merge_tiles_kernel(const TcArgs X, int64_t total)
 {
     const ChunkArgs& A = X.A;
     const int64_t at = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-    const int tile = X.nwhole + (int)(at / (2 * kTile));
-    const int r = (A.ntiles - 1 - tile % A.ntiles) * 2 * kTile + (int)(at % (2 * kTile));
+    if (at >= total) return;
+    const int tile = X.nwhole + (int)(at / X.trows);
+    const int r = (A.ntiles - 1 - tile % A.ntiles) * 2 * kTile + (int)(at % X.trows);
     if (r < A.v.rows)
         merge_row<C>(A, X.o0 + tile / A.ntiles, r, A.part + at * A.nsplit * (C + 4), threadIdx.x & 31);
 }
 
 constexpr int64_t kExpandBytes = int64_t(1) << 30;                  // expanded K and V held at once
+
+// Rows up to which the fused form is taken.
+bool fused_form(int64_t rows) { return rows <= 512; }
 
 struct TcPlan { int64_t Tp, slices, ntiles; };
 
@@ -426,41 +839,55 @@ TcPlan tc_plan(int64_t outer, int64_t C, int64_t T, int64_t rows)
     return p;
 }
 
-// One CTA fits on an SM: full waves of 152 query tiles are taken whole, the
-// rest splits its key tiles over the 152 SMs, at least four key tiles a split
-// (512 tiles: 3.37 waves end after 3.5 instead of 4, 1.58 -> 1.40 ms).
+// One CTA fits on an SM.  Either every query tile is split into the same number
+// of key ranges, or full waves of 152 tiles are taken whole and the rest is split
+// over the 152 SMs (512 tiles: 3.37 waves end after 3.5 instead of 4, 1.58 -> 1.40
+// ms); the cheaper one, in key tiles through all waves with about six for a
+// CTA's start and end and eight for joining.
 constexpr int64_t kSms = 152;
+constexpr int64_t kMaxSplitCtas = 4 * kSms;      // CTAs of split tiles: bounds the partial results
 
 struct Waves { int64_t whole, tail, nsplit; };
 
 Waves waves_of(int64_t tiles, int64_t Tp)
 {
-    Waves w;
-    w.whole = tiles / kSms * kSms;
-    w.tail = tiles - w.whole;
-    w.nsplit = w.tail ? std::max<int64_t>(1, std::min<int64_t>(kSms / w.tail, Tp / kTile / 4)) : 1;
-    if (w.nsplit == 1) {
-        w.whole = tiles;
-        w.tail = 0;
+    const int64_t keys = Tp / kTile;
+    Waves w = {tiles, 0, 1};
+    int64_t best = (tiles + kSms - 1) / kSms * (keys + 6);
+    for (int64_t s = 2; s * 2 <= keys && tiles * s <= kMaxSplitCtas; ++s) {
+        const int64_t cost = (tiles * s + kSms - 1) / kSms * ((keys + s - 1) / s + 6) + 8;
+        if (cost < best) {
+            best = cost;
+            w = {0, tiles, s};
+        }
     }
+    const int64_t tail = tiles % kSms, s = tail ? std::min<int64_t>(kSms / tail, keys / 2) : 1;
+    if (tiles > kSms && s > 1 && tiles / kSms * (keys + 6) + (keys + s - 1) / s + 14 < best) w = {tiles - tail, tail, s};
     return w;
 }
 
 template <int BITS, int C>
 cudaError_t launch_tc(const ChunkArgs& A0, int64_t outer, void* ws, cudaStream_t st)
 {
-    const TcPlan p = tc_plan(outer, C, A0.v.T, A0.v.rows);
+    const bool fused = fused_form(A0.v.rows);
+    TcPlan p = tc_plan(outer, C, A0.v.T, A0.v.rows);
+    if (fused) p.slices = outer;
     TcArgs X;
     X.A = A0;
     X.A.ntiles = (int32_t)p.ntiles;
     X.Tp = p.Tp;
+    X.trows = (int32_t)std::min<int64_t>(A0.v.rows, 2 * kTile);
     __nv_bfloat16* kx = static_cast<__nv_bfloat16*>(ws);
     __nv_bfloat16* vx = kx + p.slices * p.Tp * C;
-    X.A.part = reinterpret_cast<float*>(vx + p.slices * p.Tp * C);
-    if (p.slices * p.Tp > 0x7FFFFFFF || p.slices * p.ntiles > 0x7FFFFFFF - kSms) return cudaErrorInvalidConfiguration;
+    X.A.part = fused ? static_cast<float*>(ws) : reinterpret_cast<float*>(vx + p.slices * p.Tp * C);
+    if ((!fused && p.slices * p.Tp > 0x7FFFFFFF) || p.slices * p.ntiles > 0x7FFFFFFF - kMaxSplitCtas)
+        return cudaErrorInvalidConfiguration;
     CUtensorMap km, vm;
-    if (!encode_rows_tile_map(kx, p.slices * p.Tp, C, &km) || !encode_rows_tile_map(vx, p.slices * p.Tp, C, &vm)) return cudaErrorNotSupported;
-    cudaError_t e = ensure_kernel_attrs(reinterpret_cast<const void*>(attend_tc_kernel<C>), Smem<C>::kBytes);
+    if (!fused && (!encode_rows_tile_map(kx, p.slices * p.Tp, C, &km) || !encode_rows_tile_map(vx, p.slices * p.Tp, C, &vm)))
+        return cudaErrorNotSupported;
+    const cudaError_t e = fused
+        ? ensure_kernel_attrs(reinterpret_cast<const void*>(attend_fused_kernel<BITS, C>), SmemF<C>::kBytes)
+        : ensure_kernel_attrs(reinterpret_cast<const void*>(attend_tc_kernel<C>), Smem<C>::kBytes);
     if (e != cudaSuccess) return e;
     for (int64_t o0 = 0; o0 < outer; o0 += p.slices) {
         X.o0 = o0;
@@ -468,10 +895,18 @@ cudaError_t launch_tc(const ChunkArgs& A0, int64_t outer, void* ws, cudaStream_t
         const Waves w = waves_of(X.slices * p.ntiles, p.Tp);
         X.nwhole = (int32_t)w.whole;
         X.A.nsplit = (int32_t)w.nsplit;
-        const int64_t items = X.slices * (p.Tp / 8) * (C / 8);
-        expand_kernel<BITS, C><<<dim3((unsigned)((items + 255) / 256), 2), 256, 0, st>>>(X.A.v, o0, X.slices, p.Tp, kx, vx);
-        attend_tc_kernel<C><<<(unsigned)(w.whole + w.tail * w.nsplit), kThreadsTc, Smem<C>::kBytes, st>>>(X, km, vm);
-        if (w.tail) merge_tiles_kernel<C><<<(unsigned)(w.tail * 2 * kTile / 8), 256, 0, st>>>(X);
+        const unsigned grid = (unsigned)(w.whole + w.tail * w.nsplit);
+        if (fused) {
+            attend_fused_kernel<BITS, C><<<grid, kFusedThreads, SmemF<C>::kBytes, st>>>(X);
+        } else {
+            const int64_t items = X.slices * (p.Tp / 8) * (C / 8);
+            expand_kernel<BITS, C><<<dim3((unsigned)((items + 255) / 256), 2), 256, 0, st>>>(X.A.v, o0, X.slices, p.Tp, kx, vx);
+            attend_tc_kernel<C><<<grid, kThreadsTc, Smem<C>::kBytes, st>>>(X, km, vm);
+        }
+        if (w.tail) {
+            const int64_t total = w.tail * X.trows;
+            merge_tiles_kernel<C><<<(unsigned)((total + 7) / 8), 256, 0, st>>>(X, total);
+        }
     }
     return cudaGetLastError();
 }
@@ -500,8 +935,9 @@ bool chunk_uses_tc(int64_t T, int64_t rows) { return rows > 64 && T > 0; }
 size_t chunk_tc_workspace(int64_t outer, int64_t C, int64_t tmax, int64_t rows)
 {
     const TcPlan p = tc_plan(outer, C, tmax, rows);
-    size_t b = (size_t)std::min(outer * p.Tp * C * 4, std::max(kExpandBytes, p.Tp * C * 4));
-    b += (size_t)(kSms * 2 * kTile * (C + 4)) * 4;                  // tail * nsplit <= 152
+    size_t b = fused_form(rows) ? 0 : (size_t)std::min(outer * p.Tp * C * 4, std::max(kExpandBytes, p.Tp * C * 4));
+    const int64_t trows = std::min<int64_t>(rows, 2 * kTile), tiles = outer * p.ntiles;
+    b += (size_t)(std::min(kMaxSplitCtas, tiles * std::max<int64_t>(p.Tp / kTile / 2, 1)) * trows * (C + 4)) * 4;
     return b;
 }
 

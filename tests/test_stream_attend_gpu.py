@@ -57,6 +57,18 @@ CASES = {
     "chunk, padded": (2, 1, 5, 70, 128, 1024, 1024, 101, 192, {}, dict(first=[3, 700])),
     "long, split": (1, 2, 4, 1, 128, 9024, 9088, 100, 192, {}, {}),
     "long, split, padded": (1, 2, 1, 2, 64, 9024, 9088, 100, 192, {}, dict(first=[8000, 9100])),
+    "many rows, two bits": (1, 2, 4, 40, 128, 640, 704, 66, 192, dict(bits=2, gk=32, gv=128), {}),
+    "many rows, two bits, C 64": (1, 2, 8, 20, 64, 448, 448, 10, 64, dict(bits=2, kind="sym", gv=32), {}),
+    "many rows, far zero points": (1, 1, 5, 30, 128, 512, 512, 40, 64, {}, dict(shift=100.0)),
+    "many rows, symmetric, C 64": (2, 1, 2, 50, 64, 512, 576, 33, 64, dict(kind="sym", gk=128), {}),
+    "many rows, ragged store": (1, 2, 7, 33, 128, 333, 333, 19, 19, dict(gk=96, gv=32), {}),
+    "many rows, signed, padded": (3, 1, 16, 9, 128, 480, 512, 64, 64, dict(kind="signed", gk=32), dict(first=[0, 200, 543])),
+    "many rows, split": (1, 1, 8, 40, 128, 4096, 4096, 100, 192, {}, dict(first=[1500])),
+    "more rows than tokens": (1, 2, 4, 70, 128, 0, 64, 50, 64, {}, {}),
+    "prompt, two bits": (1, 1, 4, 200, 128, 512, 576, 30, 64, dict(bits=2, gk=32, gv=32), {}),
+    "prompt, two bits, C 64": (1, 1, 4, 200, 64, 512, 576, 30, 64, dict(bits=2, kind="sym"), {}),
+    "prompt, far zero points": (1, 1, 3, 250, 128, 320, 320, 30, 64, {}, dict(shift=-60.0)),
+    "prompt, padded": (3, 1, 4, 150, 128, 333, 333, 60, 64, dict(gk=96), dict(first=[0, 130, 390])),
     "loud": (1, 1, 4, 6, 128, 512, 512, 64, 64, {}, dict(scale=6.0)),
 }
 
