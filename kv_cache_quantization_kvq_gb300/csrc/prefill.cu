@@ -452,126 +452,164 @@ __device__ __forceinline__ uint32_t load_piece(const uint8_t* p) {
 }
 
 // one piece: values of fields (i, i + 4), i = 0 .. 3, with their scale and zero pairs
-template <int BITS>
-__device__ __forceinline__ uint4 unpack_piece(uint32_t w, bool fast, uint32_t mg, const uint32_t (&s)[4],
-                                              const uint32_t (&z)[4], float off) {
+template <int BITS, bool FAST>
+__device__ __forceinline__ uint4 unpack_piece(uint32_t w, uint32_t mg, const uint32_t (&s)[4], const uint32_t (&z)[4],
+                                              float off) {
     uint32_t r[4];
-    if (fast) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) r[i] = value_pair<BITS, true>(w, BITS * i, mg, s[i], z[i], off);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) r[i] = value_pair<BITS, false>(w, BITS * i, mg, s[i], z[i], off);
-    }
+    for (int i = 0; i < 4; ++i) r[i] = value_pair<BITS, FAST>(w, BITS * i, mg, s[i], z[i], off);
     return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
-// Tokens [t0, t0 + 128) of one cache as a swizzled tile, by 128 threads: a
-// thread takes 8-channel piece p of every (1024 / C)-th token, eight loads ahead.
+// Rows [rb, re) of key tile j token by token: at the padding, the store's end, in
+// the buffer (hidden and missing tokens are zeros), or with far zero points.  Kept
+// out of line: inlined into the loops below it pushed them out of the instruction
+// cache (5.7 warps stalled on fetches per issue).
 template <int BITS, int C, bool KEYS>
-__device__ __forceinline__ void fill_tile(const View& a, int64_t o, int t0, int first, unsigned char* tile, int tid) {
-    constexpr int P = C / 8, kStep = 128 / P, kAhead = 32 / kStep;  // rows a pass, passes of 32 tokens
-    const int p = tid % P, r0 = tid / P;
-    unsigned char* dst = tile + (p / 8) * (kTile * 128);
-    const uint8_t* codes = (KEYS ? a.kc : a.vc) + (uint64_t)o * a.cap * (C * BITS / 8) + p * BITS;
-    const uint32_t mg = magic<BITS>(KEYS ? a.kflip : a.vflip);
+__device__ __noinline__ void fill_rows(const View& a, int64_t o, int first, int j, int rb, int re, unsigned char* tile,
+                                       int tid) {
+    constexpr int P = C / 8, kStep = 128 / P;
+    const int p = tid % P;
     const float off = KEYS ? a.koff : a.voff;
-    const int vg = KEYS ? 0 : p * 8 / a.gv;
-    if (t0 >= first && t0 + kTile <= a.tq) {
-        // ---- wholly in the store: 32 tokens (of one key group) at a time, the next ones loading
-        uint32_t w[2][kAhead];
-        uint4 ks[2], kz[2];
-        uint32_t vm[2][kAhead];
-        auto fetch = [&](int q, int b) {
-            const int t = t0 + 32 * q + r0;
-#pragma unroll
-            for (int i = 0; i < kAhead; ++i) {
-                w[b][i] = load_piece<BITS>(codes + (int64_t)(t + i * kStep) * (C * BITS / 8));
-                if constexpr (!KEYS) {
-                    const int64_t at = (o * a.cap + t + i * kStep) * a.ngv + vg;
-                    vm[b][i] = bits_of(a.vs + at) | (a.vz ? bits_of(a.vz + at) << 16 : 0u);
-                }
-            }
-            if constexpr (KEYS) {
-                const int64_t at = (o * a.ngk + (t0 + 32 * q) / a.gk) * C + p * 8;
-                ks[b] = *reinterpret_cast<const uint4*>(a.ks + at);
-                kz[b] = a.kz ? *reinterpret_cast<const uint4*>(a.kz + at) : make_uint4(0, 0, 0, 0);
-            }
-        };
-        fetch(0, 0);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const int b = q & 1;
-            if (q < 3) fetch(q + 1, b ^ 1);
-            if constexpr (KEYS) {
-                const uint4 s4 = interleave(ks[b]), z4 = interleave(kz[b]);
-                const uint32_t s[4] = {s4.x, s4.y, s4.z, s4.w};
-                uint32_t z[4] = {z4.x, z4.y, z4.z, z4.w};
-                bool fast = true;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) fast = fast && zero_exact(bf_lo(z[i])) && zero_exact(bf_hi(z[i]));
-                if (fast) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) z[i] = biased(z[i], 128.0f + off);
-                }
-#pragma unroll
-                for (int i = 0; i < kAhead; ++i)
-                    *reinterpret_cast<uint4*>(dst + tc::swizzled(32 * q + r0 + i * kStep, p % 8)) =
-                        unpack_piece<BITS>(w[b][i], fast, mg, s, z, off);
-            } else {
-#pragma unroll
-                for (int i = 0; i < kAhead; ++i) {
-                    const uint32_t s1 = __byte_perm(vm[b][i], 0u, 0x1010);
-                    uint32_t z1 = __byte_perm(vm[b][i], 0u, 0x3232);
-                    const bool fast = zero_exact(bf_lo(z1));
-                    if (fast) z1 = biased(z1, 128.0f + off);
-                    const uint32_t s[4] = {s1, s1, s1, s1}, z[4] = {z1, z1, z1, z1};
-                    *reinterpret_cast<uint4*>(dst + tc::swizzled(32 * q + r0 + i * kStep, p % 8)) =
-                        unpack_piece<BITS>(w[b][i], fast, mg, s, z, off);
-                }
-            }
-        }
-    } else {
-        // ---- at the padding, the store's end or in the buffer: token by token; hidden and missing ones are zeros
+    const uint32_t mg = magic<BITS>(KEYS ? a.kflip : a.vflip);
+    const uint8_t* codes = (KEYS ? a.kc : a.vc) + (uint64_t)o * a.cap * (C * BITS / 8) + p * BITS;
 #pragma unroll 1
-        for (int r = r0; r < kTile; r += kStep) {
-            const int t = t0 + r;
-            uint4 x = make_uint4(0, 0, 0, 0);
-            if (t >= first && t < a.T) {
-                if (t >= a.tq) {
-                    x = interleave(*reinterpret_cast<const uint4*>((KEYS ? a.kr : a.vr) +
-                                                                   ((uint64_t)o * a.rrows + (t - a.tq)) * C + p * 8));
+    for (int r = rb + tid / P; r < re; r += kStep) {
+        const int t = j * kTile + r;
+        uint4 x = make_uint4(0, 0, 0, 0);
+        if (t >= first && t < a.T) {
+            if (t >= a.tq) {
+                x = interleave(*reinterpret_cast<const uint4*>((KEYS ? a.kr : a.vr) +
+                                                               ((uint64_t)o * a.rrows + (t - a.tq)) * C + p * 8));
+            } else {
+                uint32_t s[4], z[4];
+                if constexpr (KEYS) {
+                    const int64_t at = (o * a.ngk + t / a.gk) * C + p * 8;
+                    const uint4 s4 = interleave(*reinterpret_cast<const uint4*>(a.ks + at));
+                    const uint4 z4 = interleave(a.kz ? *reinterpret_cast<const uint4*>(a.kz + at) : make_uint4(0, 0, 0, 0));
+                    s[0] = s4.x; s[1] = s4.y; s[2] = s4.z; s[3] = s4.w;
+                    z[0] = z4.x; z[1] = z4.y; z[2] = z4.z; z[3] = z4.w;
                 } else {
-                    uint32_t s[4], z[4];
-                    bool fast = true;
-                    if constexpr (KEYS) {
-                        const int64_t at = (o * a.ngk + t / a.gk) * C + p * 8;
-                        const uint4 s4 = interleave(*reinterpret_cast<const uint4*>(a.ks + at));
-                        const uint4 z4 = interleave(a.kz ? *reinterpret_cast<const uint4*>(a.kz + at) : make_uint4(0, 0, 0, 0));
-                        s[0] = s4.x; s[1] = s4.y; s[2] = s4.z; s[3] = s4.w;
-                        z[0] = z4.x; z[1] = z4.y; z[2] = z4.z; z[3] = z4.w;
-                    } else {
-                        const int64_t at = (o * a.cap + t) * a.ngv + vg;
-                        s[0] = s[1] = s[2] = s[3] = bits_of(a.vs + at) * 0x10001u;
-                        z[0] = z[1] = z[2] = z[3] = a.vz ? bits_of(a.vz + at) * 0x10001u : 0u;
-                    }
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) fast = fast && zero_exact(bf_lo(z[i])) && zero_exact(bf_hi(z[i]));
-                    if (fast) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) z[i] = biased(z[i], 128.0f + off);
-                    }
-                    x = unpack_piece<BITS>(load_piece<BITS>(codes + (int64_t)t * (C * BITS / 8)), fast, mg, s, z, off);
+                    const int64_t at = (o * a.cap + t) * a.ngv + p * 8 / a.gv;
+                    s[0] = s[1] = s[2] = s[3] = bits_of(a.vs + at) * 0x10001u;
+                    z[0] = z[1] = z[2] = z[3] = a.vz ? bits_of(a.vz + at) * 0x10001u : 0u;
                 }
+                x = unpack_piece<BITS, false>(load_piece<BITS>(codes + (int64_t)t * (C * BITS / 8)), mg, s, z, off);
             }
-            *reinterpret_cast<uint4*>(dst + tc::swizzled(r, p % 8)) = x;
         }
+        *reinterpret_cast<uint4*>(tile + p / 8 * (kTile * 128) + tc::swizzled(r, p % 8)) = x;
     }
 }
 
+// Tiles of 128 tokens of one cache, swizzled, by 128 threads: a thread takes
+// 8-channel piece p of every (1024 / C)-th token.  A tile wholly in the store is
+// held as code words a tile ahead (a quarter tile, 32 tokens of one key group, is
+// loaded for the next tile when its words are used); the codes come into L2 a few
+// tiles before.
+template <int BITS, int C, bool KEYS>
+struct Fill {
+    static constexpr int P = C / 8, kStep = 128 / P, kN = 32 / kStep;      // rows a pass, passes of a quarter
+    static constexpr int kRowB = C * BITS / 8, kAheadTiles = 4;
+    const View& a;
+    const int64_t o;
+    const int first, me, p, r0, vg;
+    const uint8_t* codes;
+    const uint32_t mg, place;
+    const float off;
+    int held = -1;                               // the tile whose words are held
+    uint32_t w[4][kN];
+    uint4 ks[KEYS ? 4 : 1], kz[KEYS ? 4 : 1];    // keys: the quarter's scales and zero points
+    uint32_t vm[KEYS ? 1 : 4][kN];               // values: (scale, zero point) of each token
+
+    __device__ __forceinline__ Fill(const View& v, int64_t slice, int hidden, int tid)
+        : a(v), o(slice), first(hidden), me(tid), p(tid % P), r0(tid / P), vg(KEYS ? 0 : tid % P * 8 / v.gv),
+          codes((KEYS ? v.kc : v.vc) + (uint64_t)slice * v.cap * kRowB + tid % P * BITS),
+          mg(magic<BITS>(KEYS ? v.kflip : v.vflip)),
+          place(tid % P / 8 * (kTile * 128) + tc::swizzled(tid / P, tid % P % 8)), off(KEYS ? v.koff : v.voff) {}
+
+    __device__ __forceinline__ bool whole(int j) const { return j * kTile >= first && (j + 1) * kTile <= a.tq; }
+
+    __device__ __forceinline__ void fetch(int j, int q) {
+        const int t = j * kTile + 32 * q;
+#pragma unroll
+        for (int i = 0; i < kN; ++i) w[q][i] = load_piece<BITS>(codes + (int64_t)(t + r0 + i * kStep) * kRowB);
+        if constexpr (KEYS) {
+            const int64_t at = (o * a.ngk + t / a.gk) * C + p * 8;
+            ks[q] = *reinterpret_cast<const uint4*>(a.ks + at);
+            kz[q] = a.kz ? *reinterpret_cast<const uint4*>(a.kz + at) : make_uint4(0, 0, 0, 0);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kN; ++i) {
+                const int64_t at = (o * a.cap + t + r0 + i * kStep) * a.ngv + vg;
+                vm[q][i] = bits_of(a.vs + at) | (a.vz ? bits_of(a.vz + at) << 16 : 0u);
+            }
+        }
+    }
+    // into L2: the codes, and the constants (lines of 128 bytes, one per thread)
+    __device__ __forceinline__ void prefetch(int j, int tid) const {
+        if (!whole(j)) return;
+        const int64_t t = (int64_t)j * kTile;
+        if (tid == 0) {
+            bulk_prefetch_l2(codes + t * kRowB, kTile * kRowB);     // thread 0's piece is the row's first
+        } else if (tid >= 32 && tid < 64) {
+            const __nv_bfloat16* m = (tid & 1) ? (KEYS ? a.kz : a.vz) : (KEYS ? a.ks : a.vs);
+            const int64_t line = (tid - 32) >> 1;
+            const int64_t from = KEYS ? (o * a.ngk + t / a.gk) * C : (o * a.cap + t) * a.ngv;
+            const int64_t to = KEYS ? (o * a.ngk + (t + kTile - 1) / a.gk + 1) * C : from + kTile * a.ngv;
+            if (m && from + line * 64 < to) asm volatile("prefetch.global.L2 [%0];" ::"l"(m + from + line * 64));
+        }
+    }
+
+    // the key tile j, then the words of tile jn (-1: none) in their place
+    __device__ __forceinline__ void run(int j, int jn, unsigned char* tile) {
+        if (whole(j)) {
+            if (held != j) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) fetch(j, q);
+            }
+            const bool next = jn >= 0 && whole(jn);
+            held = next ? jn : -1;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                unsigned char* dst = tile + place + 32 * q * 128;
+                bool fast = true;
+                if constexpr (KEYS) {
+                    const uint4 s4 = interleave(ks[q]), z4 = interleave(kz[q]);
+                    const uint32_t s[4] = {s4.x, s4.y, s4.z, s4.w};
+                    uint32_t z[4] = {z4.x, z4.y, z4.z, z4.w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        fast = fast && zero_exact(bf_lo(z[i])) && zero_exact(bf_hi(z[i]));
+                        z[i] = biased(z[i], 128.0f + off);
+                    }
+                    if (fast) {
+#pragma unroll
+                        for (int i = 0; i < kN; ++i)
+                            *reinterpret_cast<uint4*>(dst + i * kStep * 128) = unpack_piece<BITS, true>(w[q][i], mg, s, z, off);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < kN; ++i) {
+                        const uint32_t s1 = __byte_perm(vm[q][i], 0u, 0x1010);
+                        const float z0 = bf_hi(vm[q][i]);
+                        const uint32_t z1 = pack_bf16x2(__fadd_rn(z0, 128.0f + off), __fadd_rn(z0, 128.0f + off));
+                        fast = fast && zero_exact(z0);
+                        const uint32_t s[4] = {s1, s1, s1, s1}, z[4] = {z1, z1, z1, z1};
+                        *reinterpret_cast<uint4*>(dst + i * kStep * 128) = unpack_piece<BITS, true>(w[q][i], mg, s, z, off);
+                    }
+                }
+                if (!fast) fill_rows<BITS, C, KEYS>(a, o, first, j, 32 * q, 32 * q + 32, tile, me);
+                if (next) fetch(jn, q);
+            }
+        } else {
+            fill_rows<BITS, C, KEYS>(a, o, first, j, 0, kTile, tile, me);
+        }
+    }
+};
+
 template <int BITS, int C>
 __global__ void __launch_bounds__(kFusedThreads, 1)
-attend_fused_kernel(const TcArgs X)
+attend_fused_kernel(const __grid_constant__ TcArgs X)
 {
     using S = SmemF<C>;
     extern __shared__ unsigned char raw[];
@@ -626,19 +664,20 @@ attend_fused_kernel(const TcArgs X)
 
     if (warp >= 12) {
         // ---- fill
-        const bool keys = warp < 16;
-        uint64_t* full = keys ? kfull : vfull;
-        uint64_t* free = keys ? kfree : vfree;
-        for (int j = 0; j < n; ++j) {
-            const int s = j & 1;
-            if (j >= 2 && !ready(&free[s], ((j >> 1) - 1) & 1)) break;
-            unsigned char* tile = sm + (keys ? S::kK : S::kV) + s * S::kTileB;
-            if (keys) fill_tile<BITS, C, true>(a, o, (j0 + j) * kTile, first, tile, tid & 127);
-            else fill_tile<BITS, C, false>(a, o, (j0 + j) * kTile, first, tile, tid & 127);
-            tc::async_fence();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&full[s]);
-        }
+        auto fill = [&](auto f, uint64_t* full, uint64_t* free, unsigned char* tiles) {
+            for (int j = 1; j < min(n, f.kAheadTiles); ++j) f.prefetch(j0 + j, tid & 127);
+            for (int j = 0; j < n; ++j) {
+                const int s = j & 1;
+                if (j >= 2 && !ready(&free[s], ((j >> 1) - 1) & 1)) break;
+                if (j + f.kAheadTiles < n) f.prefetch(j0 + j + f.kAheadTiles, tid & 127);
+                f.run(j0 + j, j + 1 < n ? j0 + j + 1 : -1, tiles + s * S::kTileB);
+                tc::async_fence();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&full[s]);
+            }
+        };
+        if (warp < 16) fill(Fill<BITS, C, true>(a, o, first, tid & 127), kfull, kfree, sm + S::kK);
+        else fill(Fill<BITS, C, false>(a, o, first, tid & 127), vfull, vfree, sm + S::kV);
     } else if (warp >= 8) {
         // ---- products of row tile t (warps 8 and 9)
         const int t = warp - 8;
