@@ -502,107 +502,107 @@ __device__ __noinline__ void fill_rows(const View& a, int64_t o, int first, int 
 }
 
 // Tiles of 128 tokens of one cache, swizzled, by 128 threads: a thread takes
-// 8-channel piece p of every (1024 / C)-th token.  A tile wholly in the store is
-// held as code words a tile ahead (a quarter tile, 32 tokens of one key group, is
-// loaded for the next tile when its words are used); the codes come into L2 a few
-// tiles before.
+// 8-channel piece p of every (1024 / C)-th token, a quarter tile (32 tokens of
+// one key group) at a time, with the next two quarters' words loading and the
+// codes coming into L2 a few tiles before.  The loops stay rolled: unrolled over a
+// tile they miss the instruction cache.
 template <int BITS, int C, bool KEYS>
 struct Fill {
     static constexpr int P = C / 8, kStep = 128 / P, kN = 32 / kStep;      // rows a pass, passes of a quarter
     static constexpr int kRowB = C * BITS / 8, kAheadTiles = 4;
     const View& a;
     const int64_t o;
-    const int first, me, p, r0, vg;
+    const int first, me, end;                    // end: one past the last quarter wanted
     const uint8_t* codes;
+    const __nv_bfloat16 *sc, *ze;                // of this thread's channels / V group, its first row
     const uint32_t mg, place;
-    const float off;
-    int held = -1;                               // the tile whose words are held
-    uint32_t w[4][kN];
-    uint4 ks[KEYS ? 4 : 1], kz[KEYS ? 4 : 1];    // keys: the quarter's scales and zero points
-    uint32_t vm[KEYS ? 1 : 4][kN];               // values: (scale, zero point) of each token
+    const float bias;
+    uint32_t w[2][kN];
+    uint4 ks[KEYS ? 2 : 1], kz[KEYS ? 2 : 1];    // keys: the quarter's scales and zero points
+    uint32_t vs[KEYS ? 1 : 2][kN], vz[KEYS ? 1 : 2][kN];            // values: of each token
 
-    __device__ __forceinline__ Fill(const View& v, int64_t slice, int hidden, int tid)
-        : a(v), o(slice), first(hidden), me(tid), p(tid % P), r0(tid / P), vg(KEYS ? 0 : tid % P * 8 / v.gv),
-          codes((KEYS ? v.kc : v.vc) + (uint64_t)slice * v.cap * kRowB + tid % P * BITS),
+    __device__ __forceinline__ Fill(const View& v, int64_t slice, int hidden, int q0, int q1, int tid)
+        : a(v), o(slice), first(hidden), me(tid), end(q1),
+          codes((KEYS ? v.kc : v.vc) + ((uint64_t)slice * v.cap + tid / P) * kRowB + tid % P * BITS),
+          sc(KEYS ? v.ks + slice * v.ngk * C + tid % P * 8 : v.vs + (slice * v.cap + tid / P) * v.ngv + tid % P * 8 / v.gv),
+          ze(KEYS ? (v.kz ? v.kz + (sc - v.ks) : nullptr) : (v.vz ? v.vz + (sc - v.vs) : nullptr)),
           mg(magic<BITS>(KEYS ? v.kflip : v.vflip)),
-          place(tid % P / 8 * (kTile * 128) + tc::swizzled(tid / P, tid % P % 8)), off(KEYS ? v.koff : v.voff) {}
+          place(tid % P / 8 * (kTile * 128) + tc::swizzled(tid / P, tid % P % 8)),
+          bias(128.0f + (KEYS ? v.koff : v.voff)) {
+        if (whole(q0)) fetch(0, q0);
+        if (whole(q0 + 1)) fetch(1, q0 + 1);
+    }
 
-    __device__ __forceinline__ bool whole(int j) const { return j * kTile >= first && (j + 1) * kTile <= a.tq; }
+    __device__ __forceinline__ bool whole(int q) const { return q < end && q * 32 >= first && (q + 1) * 32 <= a.tq; }
 
-    __device__ __forceinline__ void fetch(int j, int q) {
-        const int t = j * kTile + 32 * q;
+    __device__ __forceinline__ void fetch(int b, int q) {
+        const uint8_t* c = codes + (int64_t)q * (32 * kRowB);
 #pragma unroll
-        for (int i = 0; i < kN; ++i) w[q][i] = load_piece<BITS>(codes + (int64_t)(t + r0 + i * kStep) * kRowB);
+        for (int i = 0; i < kN; ++i) w[b][i] = load_piece<BITS>(c + i * kStep * kRowB);
         if constexpr (KEYS) {
-            const int64_t at = (o * a.ngk + t / a.gk) * C + p * 8;
-            ks[q] = *reinterpret_cast<const uint4*>(a.ks + at);
-            kz[q] = a.kz ? *reinterpret_cast<const uint4*>(a.kz + at) : make_uint4(0, 0, 0, 0);
+            const int64_t at = (int64_t)(q * 32 / a.gk) * C;
+            ks[b] = *reinterpret_cast<const uint4*>(sc + at);
+            kz[b] = ze ? *reinterpret_cast<const uint4*>(ze + at) : make_uint4(0, 0, 0, 0);
         } else {
+            const int64_t at = (int64_t)q * 32 * a.ngv;
 #pragma unroll
             for (int i = 0; i < kN; ++i) {
-                const int64_t at = (o * a.cap + t + r0 + i * kStep) * a.ngv + vg;
-                vm[q][i] = bits_of(a.vs + at) | (a.vz ? bits_of(a.vz + at) << 16 : 0u);
+                vs[b][i] = bits_of(sc + at + i * kStep * a.ngv);
+                vz[b][i] = ze ? bits_of(ze + at + i * kStep * a.ngv) : 0u;
             }
         }
     }
     // into L2: the codes, and the constants (lines of 128 bytes, one per thread)
-    __device__ __forceinline__ void prefetch(int j, int tid) const {
-        if (!whole(j)) return;
+    __device__ __forceinline__ void prefetch(int j) const {
+        if (j * kTile < first || (j + 1) * kTile > a.tq) return;
         const int64_t t = (int64_t)j * kTile;
-        if (tid == 0) {
+        if (me == 0) {
             bulk_prefetch_l2(codes + t * kRowB, kTile * kRowB);     // thread 0's piece is the row's first
-        } else if (tid >= 32 && tid < 64) {
-            const __nv_bfloat16* m = (tid & 1) ? (KEYS ? a.kz : a.vz) : (KEYS ? a.ks : a.vs);
-            const int64_t line = (tid - 32) >> 1;
+        } else if (me >= 32 && me < 64) {
+            const __nv_bfloat16* m = (me & 1) ? (KEYS ? a.kz : a.vz) : (KEYS ? a.ks : a.vs);
+            const int64_t line = (me - 32) >> 1;
             const int64_t from = KEYS ? (o * a.ngk + t / a.gk) * C : (o * a.cap + t) * a.ngv;
             const int64_t to = KEYS ? (o * a.ngk + (t + kTile - 1) / a.gk + 1) * C : from + kTile * a.ngv;
             if (m && from + line * 64 < to) asm volatile("prefetch.global.L2 [%0];" ::"l"(m + from + line * 64));
         }
     }
 
-    // the key tile j, then the words of tile jn (-1: none) in their place
-    __device__ __forceinline__ void run(int j, int jn, unsigned char* tile) {
-        if (whole(j)) {
-            if (held != j) {
+    __device__ __forceinline__ void quarter(int b, int q, unsigned char* tile) {
+        bool fast = whole(q);
+        if (fast) {
+            unsigned char* dst = tile + place + (q & 3) * (32 * 128);
+            if constexpr (KEYS) {
+                const uint4 s4 = interleave(ks[b]), z4 = interleave(kz[b]);
+                const uint32_t s[4] = {s4.x, s4.y, s4.z, s4.w};
+                uint32_t z[4] = {z4.x, z4.y, z4.z, z4.w};
 #pragma unroll
-                for (int q = 0; q < 4; ++q) fetch(j, q);
-            }
-            const bool next = jn >= 0 && whole(jn);
-            held = next ? jn : -1;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                unsigned char* dst = tile + place + 32 * q * 128;
-                bool fast = true;
-                if constexpr (KEYS) {
-                    const uint4 s4 = interleave(ks[q]), z4 = interleave(kz[q]);
-                    const uint32_t s[4] = {s4.x, s4.y, s4.z, s4.w};
-                    uint32_t z[4] = {z4.x, z4.y, z4.z, z4.w};
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        fast = fast && zero_exact(bf_lo(z[i])) && zero_exact(bf_hi(z[i]));
-                        z[i] = biased(z[i], 128.0f + off);
-                    }
-                    if (fast) {
-#pragma unroll
-                        for (int i = 0; i < kN; ++i)
-                            *reinterpret_cast<uint4*>(dst + i * kStep * 128) = unpack_piece<BITS, true>(w[q][i], mg, s, z, off);
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < kN; ++i) {
-                        const uint32_t s1 = __byte_perm(vm[q][i], 0u, 0x1010);
-                        const float z0 = bf_hi(vm[q][i]);
-                        const uint32_t z1 = pack_bf16x2(__fadd_rn(z0, 128.0f + off), __fadd_rn(z0, 128.0f + off));
-                        fast = fast && zero_exact(z0);
-                        const uint32_t s[4] = {s1, s1, s1, s1}, z[4] = {z1, z1, z1, z1};
-                        *reinterpret_cast<uint4*>(dst + i * kStep * 128) = unpack_piece<BITS, true>(w[q][i], mg, s, z, off);
-                    }
+                for (int i = 0; i < 4; ++i) {
+                    fast = fast && zero_exact(bf_lo(z[i])) && zero_exact(bf_hi(z[i]));
+                    z[i] = biased(z[i], bias);
                 }
-                if (!fast) fill_rows<BITS, C, KEYS>(a, o, first, j, 32 * q, 32 * q + 32, tile, me);
-                if (next) fetch(jn, q);
+#pragma unroll
+                for (int i = 0; i < kN; ++i)
+                    *reinterpret_cast<uint4*>(dst + i * kStep * 128) = unpack_piece<BITS, true>(w[b][i], mg, s, z, 0.0f);
+            } else {
+#pragma unroll
+                for (int i = 0; i < kN; ++i) {
+                    const uint32_t s1 = vs[b][i] * 0x10001u;
+                    const float z0 = __uint_as_float(vz[b][i] << 16), zb = __fadd_rn(z0, bias);
+                    const uint32_t z1 = pack_bf16x2(zb, zb);
+                    fast = fast && zero_exact(z0);
+                    const uint32_t s[4] = {s1, s1, s1, s1}, z[4] = {z1, z1, z1, z1};
+                    *reinterpret_cast<uint4*>(dst + i * kStep * 128) = unpack_piece<BITS, true>(w[b][i], mg, s, z, 0.0f);
+                }
             }
-        } else {
-            fill_rows<BITS, C, KEYS>(a, o, first, j, 0, kTile, tile, me);
+        }
+        if (!fast) fill_rows<BITS, C, KEYS>(a, o, first, q >> 2, (q & 3) * 32, (q & 3) * 32 + 32, tile, me);
+        if (whole(q + 2)) fetch(b, q + 2);
+    }
+    __device__ __forceinline__ void run(int j, unsigned char* tile) {
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+            quarter(0, 4 * j + 2 * h, tile);
+            quarter(1, 4 * j + 2 * h + 1, tile);
         }
     }
 };
@@ -665,19 +665,19 @@ attend_fused_kernel(const __grid_constant__ TcArgs X)
     if (warp >= 12) {
         // ---- fill
         auto fill = [&](auto f, uint64_t* full, uint64_t* free, unsigned char* tiles) {
-            for (int j = 1; j < min(n, f.kAheadTiles); ++j) f.prefetch(j0 + j, tid & 127);
+            for (int j = 1; j < min(n, f.kAheadTiles); ++j) f.prefetch(j0 + j);
             for (int j = 0; j < n; ++j) {
                 const int s = j & 1;
                 if (j >= 2 && !ready(&free[s], ((j >> 1) - 1) & 1)) break;
-                if (j + f.kAheadTiles < n) f.prefetch(j0 + j + f.kAheadTiles, tid & 127);
-                f.run(j0 + j, j + 1 < n ? j0 + j + 1 : -1, tiles + s * S::kTileB);
+                if (j + f.kAheadTiles < n) f.prefetch(j0 + j + f.kAheadTiles);
+                f.run(j0 + j, tiles + s * S::kTileB);
                 tc::async_fence();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&full[s]);
             }
         };
-        if (warp < 16) fill(Fill<BITS, C, true>(a, o, first, tid & 127), kfull, kfree, sm + S::kK);
-        else fill(Fill<BITS, C, false>(a, o, first, tid & 127), vfull, vfree, sm + S::kV);
+        if (warp < 16) fill(Fill<BITS, C, true>(a, o, first, 4 * j0, 4 * (j0 + n), tid & 127), kfull, kfree, sm + S::kK);
+        else fill(Fill<BITS, C, false>(a, o, first, 4 * j0, 4 * (j0 + n), tid & 127), vfull, vfree, sm + S::kV);
     } else if (warp >= 8) {
         // ---- products of row tile t (warps 8 and 9)
         const int t = warp - 8;
@@ -736,7 +736,7 @@ attend_fused_kernel(const __grid_constant__ TcArgs X)
             // tokens [lo, hi] of the tile are seen
             const int lo = first - c0, hi = last - c0;
             float x0 = -INFINITY, x1 = -INFINITY;
-#pragma unroll
+#pragma unroll 1
             for (int h = 0; h < 4; ++h) {
                 uint32_t s[32];
                 tc::ld32(s_at + 32 * h, s);
@@ -759,7 +759,7 @@ attend_fused_kernel(const __grid_constant__ TcArgs X)
                 if (grow) m = top;
                 sum = mul2(sum, pk(f, f));
                 if (j > 0) {
-#pragma unroll
+#pragma unroll 1
                     for (int c = 0; c < C / 32; ++c) {
                         uint32_t y[32];
                         tc::ld32(o_at + 32 * c, y);
@@ -772,7 +772,7 @@ attend_fused_kernel(const __grid_constant__ TcArgs X)
             }
             const float neg = m == -INFINITY ? 0.0f : -m;
             const u64 sc2 = pk(a.scale2, a.scale2), ng2 = pk(neg, neg);
-#pragma unroll
+#pragma unroll 1
             for (int h = 0; h < 4; ++h) {        // 32 scores -> 16 columns of weight pairs, over scores read already
                 uint32_t s[32], p[16];
                 tc::ld32(s_at + 32 * h, s);
