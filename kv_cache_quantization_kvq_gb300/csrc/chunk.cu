@@ -13,8 +13,8 @@
 // probabilities never leave registers, and the keys and values go from packed
 // codes to B fragments in registers (kvq_rows.cuh).
 //
-// attend_rows_kernel: a CTA takes (slice, tile of 16 MT query rows, split of
-// the visible batches); each of its four warps walks its run of the split's
+// attend_rows_kernel: a CTA takes (slice, split of the visible batches) for
+// the slice's 16 MT query rows; each of its four warps walks its run of the split's
 // 32-token batches with its own m, l, y, merged through shared memory at the
 // end.  The query fragments and the key group's constants stay in shared memory
 // (12 warps a SM instead of 8), the next batch's codes are loaded as soon as the
@@ -170,7 +170,6 @@ __global__ void __launch_bounds__(kThreads, MT == 1 ? 3 : 2)
 attend_rows_kernel(const ChunkArgs A)
 {
     using G = Geo<BITS, C>;
-    constexpr int kRowTile = 16 * MT;
     const View& a = A.v;
     __shared__ float sm[kWarps][16], sl[kWarps][16], gm[16], gl[16];
     __shared__ __align__(16) float sy[kWarps][16][C];
@@ -180,24 +179,19 @@ attend_rows_kernel(const ChunkArgs A)
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, tig = lane & 3;
-    uint32_t blk = blockIdx.x;
-    const int split = (int)(blk % (uint32_t)A.nsplit);
-    blk /= (uint32_t)A.nsplit;
-    const int tile = (int)(blk % (uint32_t)A.ntiles);
-    const int64_t o = blk / (uint32_t)A.ntiles;
-    const int r0 = tile * kRowTile;
-    stage_queries<BITS, C, MT>(a, o, r0, qf, tid, kThreads);
+    const int split = (int)(blockIdx.x % (uint32_t)A.nsplit);
+    const int64_t o = blockIdx.x / (uint32_t)A.nsplit;
+    stage_queries<BITS, C, MT>(a, o, 0, qf, tid, kThreads);
 
     // ---- the last token each of this lane's rows sees
     const int base = a.T - a.n;                  // token of query 0
     int last[MT][2];
 #pragma unroll
     for (int m = 0; m < MT; ++m) {               // rows past the last are not written
-        last[m][0] = base + (r0 + 16 * m + g) / a.group;
-        last[m][1] = base + (r0 + 16 * m + g + 8) / a.group;
+        last[m][0] = base + (16 * m + g) / a.group;
+        last[m][1] = base + (16 * m + g + 8) / a.group;
     }
-    const int last_hi = base + (min(r0 + kRowTile, a.rows) - 1) / a.group;     // of the tile's rows
-    const int last_lo = base + r0 / a.group;
+    const int last_hi = a.T - 1, last_lo = base;                   // of the last and of the first row
     const int first = a.first ? max(a.first[o], 0) : 0;
 
     // ---- the visible batches, cut into splits, and a run of the split for each warp
@@ -394,7 +388,7 @@ attend_rows_kernel(const ChunkArgs A)
         }
         __syncthreads();
         for (int k = tid; k < 16 * (C / 4); k += kThreads) {
-            const int row = k / (C / 4), c4 = (k % (C / 4)) * 4, r = r0 + 16 * m + row;
+            const int row = k / (C / 4), c4 = (k % (C / 4)) * 4, r = 16 * m + row;
             if (r >= a.rows) break;
             float M = -INFINITY;
 #pragma unroll
@@ -429,7 +423,7 @@ attend_rows_kernel(const ChunkArgs A)
         if (A.cluster) {                         // block rank = split; each takes its share of the rows' pieces
             cluster_sync();
             for (int k = split * kThreads + tid; k < 16 * (C / 4); k += A.nsplit * kThreads) {
-                const int row = k / (C / 4), c4 = (k % (C / 4)) * 4, r = r0 + 16 * m + row;
+                const int row = k / (C / 4), c4 = (k % (C / 4)) * 4, r = 16 * m + row;
                 if (r >= a.rows) break;
                 float M = -INFINITY;
                 for (int s = 0; s < A.nsplit; ++s) M = fmaxf(M, remote_f(&gm[row], s));
@@ -462,11 +456,10 @@ merge_rows_kernel(const ChunkArgs A, int64_t total)
     merge_row<C>(A, o, (int)(row - o * A.v.rows), A.part + row * A.nsplit * (C + 4), threadIdx.x & 31);
 }
 
-// Row tiles and splits.  Up to 16 rows take tiles of 16 (three CTAs a SM), more
-// take tiles of 32 (two), which unpack each key and value once for 32 rows.
-// Splits of the visible batches: the number that gives the shortest run through
+// Up to 16 rows take a tile of 16 (three CTAs a SM), up to 32 one of 32 (two); more
+// rows take the tensor-core forms of prefill.cu.  Splits of the visible batches: the number that gives the shortest run through
 // all waves, counting about three batches for a CTA's start and end.
-struct RowsPlan { int64_t mt, ntiles, nsplit; bool cluster; };
+struct RowsPlan { int64_t mt, nsplit; bool cluster; };
 
 constexpr int64_t kCluster = 8;                   // most splits that a cluster joins
 constexpr int64_t kMaxWaves = 2;                 // more CTAs than this are not split further
@@ -477,8 +470,7 @@ RowsPlan rows_plan(int64_t outer, int64_t T, int64_t rows)
 {
     RowsPlan p;
     p.mt = rows <= 16 ? 1 : 2;
-    p.ntiles = (rows + 16 * p.mt - 1) / (16 * p.mt);
-    const int64_t ctas = std::max<int64_t>(outer * p.ntiles, 1), slots = slots_of(p.mt);
+    const int64_t ctas = std::max<int64_t>(outer, 1), slots = slots_of(p.mt);
     const int64_t nb = (T + kBatch - 1) / kBatch + 1;
     int64_t best = INT64_MAX;
     p.nsplit = 1;
@@ -502,9 +494,8 @@ template <int BITS, int C>
 cudaError_t launch_rows(ChunkArgs A, int64_t outer, cudaStream_t st)
 {
     const RowsPlan p = rows_plan(outer, A.v.T, A.v.rows);
-    A.ntiles = (int32_t)p.ntiles;
     A.nsplit = (int32_t)p.nsplit;
-    const int64_t grid = outer * p.ntiles * p.nsplit;
+    const int64_t grid = outer * p.nsplit;
     if (grid > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
     A.cluster = p.cluster;
     cudaLaunchAttribute at;

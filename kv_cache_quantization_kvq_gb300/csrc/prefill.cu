@@ -26,16 +26,17 @@
 #include <cudaTypedefs.h>
 
 #include "kvq_chunk.cuh"
-#include "kvq_fast.cuh"
-#include "kvq_tc.cuh"
+#include "kvq_fill.cuh"
 
 namespace kvq {
 
 namespace {
 
 using namespace rows;
+using fill::kTile;                               // 128 tokens of a key tile, 128 rows of a query tile
+using fill::Fill;
+using fill::interleave;
 
-constexpr int kTile = 128;                       // tokens of a key tile, rows of a query tile
 constexpr int kSlots = 4;                        // ring slots of one K or V tile
 constexpr int kThreadsTc = 384;                 // 12 warps, 168 registers each at launch (64512 in all):
 constexpr int kRegsSoftmax = 216;                // 8 softmax warps take 216 and the other four keep 56
@@ -438,175 +439,6 @@ struct SmemF {
     static constexpr int kBytes = kBars + 256 + 1024;
 };
 
-// 0 4 1 5 2 6 3 7 from eight bf16 in order
-__device__ __forceinline__ uint4 interleave(const uint4& x) {
-    return make_uint4(__byte_perm(x.x, x.z, 0x5410), __byte_perm(x.x, x.z, 0x7632), __byte_perm(x.y, x.w, 0x5410),
-                      __byte_perm(x.y, x.w, 0x7632));
-}
-
-// eight fields of a token's 8-channel piece, (i, i + 4) at bits BITS i of the halves
-template <int BITS>
-__device__ __forceinline__ uint32_t load_piece(const uint8_t* p) {
-    if constexpr (BITS == 4) return __ldcs(reinterpret_cast<const uint32_t*>(p));
-    else return __byte_perm((uint32_t)__ldcs(reinterpret_cast<const uint16_t*>(p)), 0u, 0x4140);
-}
-
-// one piece: values of fields (i, i + 4), i = 0 .. 3, with their scale and zero pairs
-template <int BITS, bool FAST>
-__device__ __forceinline__ uint4 unpack_piece(uint32_t w, uint32_t mg, const uint32_t (&s)[4], const uint32_t (&z)[4],
-                                              float off) {
-    uint32_t r[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) r[i] = value_pair<BITS, FAST>(w, BITS * i, mg, s[i], z[i], off);
-    return make_uint4(r[0], r[1], r[2], r[3]);
-}
-
-// Rows [rb, re) of key tile j token by token: at the padding, the store's end, in
-// the buffer (hidden and missing tokens are zeros), or with far zero points.  Kept
-// out of line: inlined into the loops below it pushed them out of the instruction
-// cache (5.7 warps stalled on fetches per issue).
-template <int BITS, int C, bool KEYS>
-__device__ __noinline__ void fill_rows(const View& a, int64_t o, int first, int j, int rb, int re, unsigned char* tile,
-                                       int tid) {
-    constexpr int P = C / 8, kStep = 128 / P;
-    const int p = tid % P;
-    const float off = KEYS ? a.koff : a.voff;
-    const uint32_t mg = magic<BITS>(KEYS ? a.kflip : a.vflip);
-    const uint8_t* codes = (KEYS ? a.kc : a.vc) + (uint64_t)o * a.cap * (C * BITS / 8) + p * BITS;
-#pragma unroll 1
-    for (int r = rb + tid / P; r < re; r += kStep) {
-        const int t = j * kTile + r;
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (t >= first && t < a.T) {
-            if (t >= a.tq) {
-                x = interleave(*reinterpret_cast<const uint4*>((KEYS ? a.kr : a.vr) +
-                                                               ((uint64_t)o * a.rrows + (t - a.tq)) * C + p * 8));
-            } else {
-                uint32_t s[4], z[4];
-                if constexpr (KEYS) {
-                    const int64_t at = (o * a.ngk + t / a.gk) * C + p * 8;
-                    const uint4 s4 = interleave(*reinterpret_cast<const uint4*>(a.ks + at));
-                    const uint4 z4 = interleave(a.kz ? *reinterpret_cast<const uint4*>(a.kz + at) : make_uint4(0, 0, 0, 0));
-                    s[0] = s4.x; s[1] = s4.y; s[2] = s4.z; s[3] = s4.w;
-                    z[0] = z4.x; z[1] = z4.y; z[2] = z4.z; z[3] = z4.w;
-                } else {
-                    const int64_t at = (o * a.cap + t) * a.ngv + p * 8 / a.gv;
-                    s[0] = s[1] = s[2] = s[3] = bits_of(a.vs + at) * 0x10001u;
-                    z[0] = z[1] = z[2] = z[3] = a.vz ? bits_of(a.vz + at) * 0x10001u : 0u;
-                }
-                x = unpack_piece<BITS, false>(load_piece<BITS>(codes + (int64_t)t * (C * BITS / 8)), mg, s, z, off);
-            }
-        }
-        *reinterpret_cast<uint4*>(tile + p / 8 * (kTile * 128) + tc::swizzled(r, p % 8)) = x;
-    }
-}
-
-// Tiles of 128 tokens of one cache, swizzled, by 128 threads: a thread takes
-// 8-channel piece p of every (1024 / C)-th token, a quarter tile (32 tokens of
-// one key group) at a time, with the next two quarters' words loading and the
-// codes coming into L2 a few tiles before.  The loops stay rolled: unrolled over a
-// tile they miss the instruction cache.
-template <int BITS, int C, bool KEYS>
-struct Fill {
-    static constexpr int P = C / 8, kStep = 128 / P, kN = 32 / kStep;      // rows a pass, passes of a quarter
-    static constexpr int kRowB = C * BITS / 8, kAheadTiles = 4;
-    const View& a;
-    const int64_t o;
-    const int first, me, end;                    // end: one past the last quarter wanted
-    const uint8_t* codes;
-    const __nv_bfloat16 *sc, *ze;                // of this thread's channels / V group, its first row
-    const uint32_t mg, place;
-    const float bias;
-    uint32_t w[2][kN];
-    uint4 ks[KEYS ? 2 : 1], kz[KEYS ? 2 : 1];    // keys: the quarter's scales and zero points
-    uint32_t vs[KEYS ? 1 : 2][kN], vz[KEYS ? 1 : 2][kN];            // values: of each token
-
-    __device__ __forceinline__ Fill(const View& v, int64_t slice, int hidden, int q0, int q1, int tid)
-        : a(v), o(slice), first(hidden), me(tid), end(q1),
-          codes((KEYS ? v.kc : v.vc) + ((uint64_t)slice * v.cap + tid / P) * kRowB + tid % P * BITS),
-          sc(KEYS ? v.ks + slice * v.ngk * C + tid % P * 8 : v.vs + (slice * v.cap + tid / P) * v.ngv + tid % P * 8 / v.gv),
-          ze(KEYS ? (v.kz ? v.kz + (sc - v.ks) : nullptr) : (v.vz ? v.vz + (sc - v.vs) : nullptr)),
-          mg(magic<BITS>(KEYS ? v.kflip : v.vflip)),
-          place(tid % P / 8 * (kTile * 128) + tc::swizzled(tid / P, tid % P % 8)),
-          bias(128.0f + (KEYS ? v.koff : v.voff)) {
-        if (whole(q0)) fetch(0, q0);
-        if (whole(q0 + 1)) fetch(1, q0 + 1);
-    }
-
-    __device__ __forceinline__ bool whole(int q) const { return q < end && q * 32 >= first && (q + 1) * 32 <= a.tq; }
-
-    __device__ __forceinline__ void fetch(int b, int q) {
-        const uint8_t* c = codes + (int64_t)q * (32 * kRowB);
-#pragma unroll
-        for (int i = 0; i < kN; ++i) w[b][i] = load_piece<BITS>(c + i * kStep * kRowB);
-        if constexpr (KEYS) {
-            const int64_t at = (int64_t)(q * 32 / a.gk) * C;
-            ks[b] = *reinterpret_cast<const uint4*>(sc + at);
-            kz[b] = ze ? *reinterpret_cast<const uint4*>(ze + at) : make_uint4(0, 0, 0, 0);
-        } else {
-            const int64_t at = (int64_t)q * 32 * a.ngv;
-#pragma unroll
-            for (int i = 0; i < kN; ++i) {
-                vs[b][i] = bits_of(sc + at + i * kStep * a.ngv);
-                vz[b][i] = ze ? bits_of(ze + at + i * kStep * a.ngv) : 0u;
-            }
-        }
-    }
-    // into L2: the codes, and the constants (lines of 128 bytes, one per thread)
-    __device__ __forceinline__ void prefetch(int j) const {
-        if (j * kTile < first || (j + 1) * kTile > a.tq) return;
-        const int64_t t = (int64_t)j * kTile;
-        if (me == 0) {
-            bulk_prefetch_l2(codes + t * kRowB, kTile * kRowB);     // thread 0's piece is the row's first
-        } else if (me >= 32 && me < 64) {
-            const __nv_bfloat16* m = (me & 1) ? (KEYS ? a.kz : a.vz) : (KEYS ? a.ks : a.vs);
-            const int64_t line = (me - 32) >> 1;
-            const int64_t from = KEYS ? (o * a.ngk + t / a.gk) * C : (o * a.cap + t) * a.ngv;
-            const int64_t to = KEYS ? (o * a.ngk + (t + kTile - 1) / a.gk + 1) * C : from + kTile * a.ngv;
-            if (m && from + line * 64 < to) asm volatile("prefetch.global.L2 [%0];" ::"l"(m + from + line * 64));
-        }
-    }
-
-    __device__ __forceinline__ void quarter(int b, int q, unsigned char* tile) {
-        bool fast = whole(q);
-        if (fast) {
-            unsigned char* dst = tile + place + (q & 3) * (32 * 128);
-            if constexpr (KEYS) {
-                const uint4 s4 = interleave(ks[b]), z4 = interleave(kz[b]);
-                const uint32_t s[4] = {s4.x, s4.y, s4.z, s4.w};
-                uint32_t z[4] = {z4.x, z4.y, z4.z, z4.w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    fast = fast && zero_exact(bf_lo(z[i])) && zero_exact(bf_hi(z[i]));
-                    z[i] = biased(z[i], bias);
-                }
-#pragma unroll
-                for (int i = 0; i < kN; ++i)
-                    *reinterpret_cast<uint4*>(dst + i * kStep * 128) = unpack_piece<BITS, true>(w[b][i], mg, s, z, 0.0f);
-            } else {
-#pragma unroll
-                for (int i = 0; i < kN; ++i) {
-                    const uint32_t s1 = vs[b][i] * 0x10001u;
-                    const float z0 = __uint_as_float(vz[b][i] << 16), zb = __fadd_rn(z0, bias);
-                    const uint32_t z1 = pack_bf16x2(zb, zb);
-                    fast = fast && zero_exact(z0);
-                    const uint32_t s[4] = {s1, s1, s1, s1}, z[4] = {z1, z1, z1, z1};
-                    *reinterpret_cast<uint4*>(dst + i * kStep * 128) = unpack_piece<BITS, true>(w[b][i], mg, s, z, 0.0f);
-                }
-            }
-        }
-        if (!fast) fill_rows<BITS, C, KEYS>(a, o, first, q >> 2, (q & 3) * 32, (q & 3) * 32 + 32, tile, me);
-        if (whole(q + 2)) fetch(b, q + 2);
-    }
-    __device__ __forceinline__ void run(int j, unsigned char* tile) {
-#pragma unroll 1
-        for (int h = 0; h < 2; ++h) {
-            quarter(0, 4 * j + 2 * h, tile);
-            quarter(1, 4 * j + 2 * h + 1, tile);
-        }
-    }
-};
-
 template <int BITS, int C>
 __global__ void __launch_bounds__(kFusedThreads, 1)
 attend_fused_kernel(const __grid_constant__ TcArgs X)
@@ -864,8 +696,10 @@ merge_tiles_kernel(const TcArgs X, int64_t total)
 
 constexpr int64_t kExpandBytes = int64_t(1) << 30;                  // expanded K and V held at once
 
-// Rows up to which the fused form is taken.
-bool fused_form(int64_t rows) { return rows <= 512; }
+// One query tile of up to 256 rows reads the codes itself; more rows share one
+// expansion (64 slices of 32768 tokens: 256 rows 413 us fused, 630 expanded; 512
+// rows 792 and 766).
+bool fused_form(int64_t rows) { return rows <= 2 * kTile; }
 
 struct TcPlan { int64_t Tp, slices, ntiles; };
 
@@ -966,8 +800,9 @@ bool encode_rows_tile_map(const void* x, int64_t rows, int64_t C, CUtensorMap* m
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Rows from which the tensor-core form is taken.
-bool chunk_uses_tc(int64_t T, int64_t rows) { return rows > 64 && T > 0; }
+// Rows from which the tensor-core forms are taken (64 slices of 32768 tokens: 32
+// rows 249 us on mma.sync and 349 here, 64 rows 506 and 351).
+bool chunk_uses_tc(int64_t T, int64_t rows) { return rows > 32 && T > 0; }
 
 // Enough for every T up to tmax: a shorter cache may take more slices at once,
 // but never more than the bound on expanded bytes.

@@ -6,23 +6,24 @@
 // query rows in its columns, so a token's sum over the rows is a sum over one
 // thread's registers: no shuffles, no atomics, a fixed order.
 //  1. pack_rows_kernel writes the query rows of every slice densely (rows
-//     padded to 128 with zeros) with their base-2 log-sum-exp (+inf where a row
-//     gives nothing, so that 2^(x - inf) = 0);
-//  2. weights_tc_kernel, a CTA per (slice, 256 tokens, split of the rows): its
-//     keys are unpacked from the codes into two swizzled M = 128 tiles once;
-//     warp 8 loads tiles of 128 query rows by TMA into a ring, warps 9
-//     and 10 issue the products of a key tile each into two tensor-memory
-//     buffers, four groups of four warps, one per buffer, turn them into sums
-//     of 2^(x - lse), a token per thread.
+//     padded to 128 with zeros), with -lse in base 2 (-inf where a row gives
+//     nothing, so that 2^(x - inf) = 0) and the last token a row sees;
+//  2. weights_tc_kernel, one CTA a SM, walks jobs of 256 tokens (and a split of
+//     the rows): eight fill warps unpack the next job's keys into two swizzled
+//     M = 128 tiles while the current ones are in use; one warp loads tiles of 128
+//     query rows by TMA into a ring, two issue the products of a key tile each
+//     into two tensor-memory buffers, four groups of four warps, one per buffer,
+//     turn them into sums of 2^(x - lse), a token per thread;
 //  3. with several splits of the rows, join_kernel adds their sums in order.
+// A CTA per job instead, its keys filled before its products, spent most of its
+// time there: 146 us for 63 queries x 4 heads over 32768 tokens and 16 slices.
 #include <algorithm>
 
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
 #include "kvq_chunk.cuh"
-#include "kvq_fast.cuh"
-#include "kvq_tc.cuh"
+#include "kvq_fill.cuh"
 
 namespace kvq {
 
@@ -30,9 +31,12 @@ namespace {
 
 using namespace rows;
 
-constexpr int kTile = 128;
+using fill::Fill;
+using fill::interleave;
+using fill::kTile;
 constexpr int kSumWarps = 16;                    // four per scheduler: one warp's exponentials cover another's loads
-constexpr int kThreadsW = (kSumWarps + 4) * 32;
+constexpr int kFillWarp = kSumWarps + 4;         // 16: copies, 17 and 18: products, 20-27: fill
+constexpr int kThreadsW = (kFillWarp + 8) * 32;
 
 struct WtArgs {
     View v;
@@ -42,7 +46,8 @@ struct WtArgs {
     int64_t stride, R;                           // R: rows padded to 128
     const float* row;                            // [outer][R / 128][2][128]: -lse in base 2; last token seen (int bits)
     float* part;                                 // [outer][split][Tp]
-    int32_t nsplit, ntok;                        // row splits, 256-token CTAs of a slice
+    int32_t nsplit, ntok;                        // row splits, 256-token jobs of a slice
+    int64_t jobs;                                // slices x splits x ntok
 };
 
 __global__ void __launch_bounds__(256)
@@ -60,7 +65,7 @@ pack_rows_kernel(const View a, const float* lse, int64_t R, int C, int64_t total
     int last = -1;
     if (r < a.rows) {
         const int64_t at = row_index(a, o, r);
-        x = *reinterpret_cast<const uint4*>(a.q + at * C + p * 8);
+        x = interleave(*reinterpret_cast<const uint4*>(a.q + at * C + p * 8));
         if (p == 0) {
             l = lse[at];
             l = l == -INFINITY ? -INFINITY : -__fmul_rn(l, kLog2e);
@@ -78,118 +83,121 @@ pack_rows_kernel(const View a, const float* lse, int64_t R, int C, int64_t total
 template <int C>
 struct SmemW {
     static constexpr int kTileB = kTile * C * 2;
-    static constexpr int kSlots = 4;
-    static constexpr int kK = 0, kRing = 2 * kTileB, kLse = kRing + kSlots * kTileB, kBars = kLse + kSlots * kTile * 8;
-    static constexpr int kBytes = kBars + 256 + 1024;
+    static constexpr int kSlots = 2;             // of the ring of query tiles
+    static constexpr int kK = 0, kRing = 4 * kTileB;                // two jobs' two key tiles
+    static constexpr int kRows = kRing + kSlots * kTileB, kHalf = kRows + kSlots * kTile * 8;
+    static constexpr int kBars = kHalf + 2 * 2 * kTile * 4, kBytes = kBars + 256 + 1024;
+};
+
+// A job: 256 tokens from t0 of slice o, row tiles [n0, n0 + n).
+struct Job {
+    int64_t o;
+    int t0, n0, n, split, first;
+    __device__ __forceinline__ Job(const WtArgs& A, int64_t job) {
+        const View& a = A.v;
+        const int tb = (int)(job % A.ntok);
+        job /= A.ntok;
+        split = (int)(job % A.nsplit);
+        o = job / A.nsplit;
+        t0 = tb * 2 * kTile;
+        first = a.first ? max(a.first[o], 0) : 0;
+        // the row tiles that see any of these tokens: from the first query that does
+        const int see = max(t0, first), i0 = max(0, see - (a.T - a.n));
+        int lo = (int)((int64_t)i0 * a.group / kTile), hi = (a.rows + kTile - 1) / kTile;
+        if (see >= min(t0 + 2 * kTile, a.T) || i0 >= a.n) hi = lo;
+        const int64_t len = max(hi - lo, 0);
+        n0 = lo + (int)(len * split / A.nsplit);
+        n = lo + (int)(len * (split + 1) / A.nsplit) - n0;
+    }
 };
 
 template <int BITS, int C>
 __global__ void __launch_bounds__(kThreadsW, 1)
-weights_tc_kernel(const WtArgs A, const __grid_constant__ CUtensorMap qmap)
+weights_tc_kernel(const __grid_constant__ WtArgs A, const __grid_constant__ CUtensorMap qmap)
 {
     using S = SmemW<C>;
-    using W = typename CodeWord<BITS>::T;
-    constexpr int kSlots = S::kSlots, kHalves = C / 64, P = C / 8;
-    __shared__ float half_sum[2][2 * kTile];
+    constexpr int kSlots = S::kSlots, kHalves = C / 64;
     extern __shared__ unsigned char raw[];
     unsigned char* sm = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
-    float4* srow = reinterpret_cast<float4*>(sm + S::kLse);        // [slot][2][32]: four rows' -lse; their last tokens
-    uint64_t* full = reinterpret_cast<uint64_t*>(sm + S::kBars);
-    uint64_t* empty = full + kSlots;             // slot free: products done (2) and row data read (2 x 4 warps)
-    uint64_t* dfull = empty + kSlots;            // [2 tiles][2 buffers]
+    float4* srow = reinterpret_cast<float4*>(sm + S::kRows);       // [slot][2][32]: four rows' -lse; their last tokens
+    float* half = reinterpret_cast<float*>(sm + S::kHalf);         // [job parity][2 tiles][128]: sums of odd row tiles
+    uint64_t* full = reinterpret_cast<uint64_t*>(sm + S::kBars);   // [slot] a query tile has landed
+    uint64_t* empty = full + kSlots;             // [slot] products (2) and row data (2 x 4 warps) are done with it
+    uint64_t* kfull = empty + kSlots;            // [job parity] both key tiles are filled (8 warps)
+    uint64_t* kfree = kfull + 2;                 // [job parity] both products are done with them
+    uint64_t* dfull = kfree + 2;                 // [2 tiles][2 buffers]
     uint64_t* dfree = dfull + 4;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(dfree + 4);
+    uint64_t* hfull = dfree + 4;                 // [2 tiles][job parity] the odd groups' sums are there
+    uint64_t* hfree = hfull + 4;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(hfree + 4);
     volatile int* gone = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
     const View& a = A.v;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    int64_t blk = blockIdx.x;
-    const int split = (int)(blk % A.nsplit);
-    blk /= A.nsplit;
-    const int tb = (int)(blk % A.ntok);
-    const int64_t o = blk / A.ntok;
-    const int t0 = tb * 2 * kTile;
-    const int first = a.first ? max(a.first[o], 0) : 0;
-    const int base = a.T - a.n;
-
-    // ---- the row tiles that see any of these tokens
-    const int see = max(t0, first);              // the first token that can be seen
-    const int i0 = max(0, see - base);           // by query i0 and later ones
-    int n0 = (int)((int64_t)i0 * a.group / kTile), n1 = (a.rows + kTile - 1) / kTile;
-    if (see >= min(t0 + 2 * kTile, a.T) || i0 >= a.n) n1 = n0;
-    {
-        const int64_t len = max(n1 - n0, 0);
-        const int e = n0 + (int)(len * (split + 1) / A.nsplit);
-        n0 += (int)(len * split / A.nsplit);
-        n1 = e;
-    }
-    const int n = n1 - n0;
+    const int64_t job0 = A.jobs * blockIdx.x / gridDim.x, job1 = A.jobs * (blockIdx.x + 1) / gridDim.x;
 
     if (tid == 0) {
         for (int i = 0; i < kSlots; ++i) {
             mbar_init(&full[i], 1);
             mbar_init(&empty[i], 10);
         }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&kfull[i], 8);
+            mbar_init(&kfree[i], 2);
+        }
         for (int i = 0; i < 4; ++i) {
             mbar_init(&dfull[i], 1);
             mbar_init(&dfree[i], 4);
+            mbar_init(&hfull[i], 4);
+            mbar_init(&hfree[i], 4);
         }
         *gone = 0;
         mbar_init_fence();
     }
     if (warp == kSumWarps + 1) tc::alloc(tmem_slot, 512);
-    // ---- the keys: row = token, 16-byte pieces of 8 channels; hidden tokens are zeros
-    if (n > 0) {
-#pragma unroll 4
-        for (int k = tid; k < 2 * kTile * P; k += kThreadsW) {
-            const int row = k / P, p = k % P, t = t0 + row;
-            uint4 x = make_uint4(0, 0, 0, 0);
-            if (t >= first && t < a.T) {
-                if (t >= a.tq) {
-                    x = *reinterpret_cast<const uint4*>(a.kr + ((uint64_t)o * a.rrows + (t - a.tq)) * C + p * 8);
-                } else {
-                    const int64_t at = (o * a.ngk + t / a.gk) * C + p * 8;
-                    Raw8<__nv_bfloat16> rs, rz;
-                    load_raw8(a.ks + at, rs);
-                    float s[8], z[8], v[8];
-                    widen8(rs, s);
-                    if (a.kz) {
-                        load_raw8(a.kz + at, rz);
-                        widen8(rz, z);
-                    }
-                    W w = *reinterpret_cast<const W*>(a.kc + ((uint64_t)o * a.cap + t) * (C * BITS / 8) + p * BITS);
-                    w ^= (W)a.kflip;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float c = __fsub_rn((float)((w >> (BITS * i)) & ((1 << BITS) - 1)), a.koff);
-                        v[i] = __fmul_rn(a.kz ? __fsub_rn(c, z[i]) : c, s[i]);
-                    }
-                    store8(reinterpret_cast<__nv_bfloat16*>(&x), v);
-                }
-            }
-            *reinterpret_cast<uint4*>(sm + S::kK + (row / kTile) * S::kTileB + (p / 8) * (kTile * 128) +
-                                      tc::swizzled(row % kTile, p % 8)) = x;
-        }
-        tc::async_fence();
-    }
     tc::before_sync();
     __syncthreads();
     tc::after_sync();
     const uint32_t tmem = *tmem_slot;
+    auto ready = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xFFFFFFFFu, tc::wait(bar, parity, gone)) != 0; };
+    // every role walks the jobs alike; `it` counts row tiles and `k` jobs with any, over the whole CTA
 
-    if (warp == kSumWarps) {
-        int it = 0;
-        for (; it < n; ++it) {
-            const int s = it % kSlots;
-            if (it >= kSlots && !__all_sync(0xFFFFFFFFu, tc::wait(&empty[s], ((it / kSlots) - 1) & 1, gone))) break;
-            if (tc::elect()) {
-                mbar_expect_tx(&full[s], S::kTileB + kTile * 8);
-                const int64_t row = o * A.R + (int64_t)(n0 + it) * kTile;
-                for (int h = 0; h < kHalves; ++h)
-                    tma_load_2d(sm + S::kRing + s * S::kTileB + h * (kTile * 128), &qmap, h * 64, (int)row, &full[s]);
-                bulk_g2s(srow + s * (kTile / 2), A.row + row * 2, kTile * 8, &full[s]);
-            }
+    if (warp >= kFillWarp) {
+        // ---- keys: four warps a tile
+        const int t = (warp - kFillWarp) >> 2, me = tid & 127;
+        int k = 0;
+        for (int64_t job = job0; job < job1; ++job) {
+            const Job J(A, job);
+            if (J.n == 0) continue;
+            if (k >= 2 && !ready(&kfree[k & 1], ((k >> 1) - 1) & 1)) break;
+            const int j = J.t0 / kTile + t;
+            Fill<BITS, C, true> f(a, J.o, J.first, 4 * j, 4 * j + 4, me);
+            if (job + 1 < job1) f.prefetch(j + 2);                  // the next job's tile, if the slice goes on
+            f.run(j, sm + S::kK + (2 * (k & 1) + t) * S::kTileB);
+            tc::async_fence();
             __syncwarp();
+            if (lane == 0) mbar_arrive(&kfull[k & 1]);
+            ++k;
+        }
+    } else if (warp == kSumWarps) {
+        // ---- query tiles
+        int it = 0;
+        bool ok = true;
+        for (int64_t job = job0; ok && job < job1; ++job) {
+            const Job J(A, job);
+            for (int i = 0; i < J.n; ++i, ++it) {
+                const int s = it % kSlots;
+                if (it >= kSlots) ok = ready(&empty[s], ((it / kSlots) - 1) & 1);
+                if (!ok) break;
+                if (tc::elect()) {
+                    mbar_expect_tx(&full[s], S::kTileB + kTile * 8);
+                    const int64_t row = J.o * A.R + (int64_t)(J.n0 + i) * kTile;
+                    for (int h = 0; h < kHalves; ++h)
+                        tma_load_2d(sm + S::kRing + s * S::kTileB + h * (kTile * 128), &qmap, h * 64, (int)row, &full[s]);
+                    bulk_g2s(srow + s * (kTile / 2), A.row + row * 2, kTile * 8, &full[s]);
+                }
+                __syncwarp();
+            }
         }
         // every copy issued lands before the CTA's shared memory goes
         for (int i = max(0, it - kSlots); i < it; ++i) tc::drain(&full[i % kSlots], (i / kSlots) & 1);
@@ -197,101 +205,129 @@ weights_tc_kernel(const WtArgs A, const __grid_constant__ CUtensorMap qmap)
         // ---- products of key tile t
         const int t = warp - kSumWarps - 1;
         constexpr uint32_t kDesc = tc::instr_desc(kTile, kTile, false);
-        const uint32_t k_at = smem_u32(sm + S::kK) + t * S::kTileB, ring = smem_u32(sm + S::kRing);
-        auto ready = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xFFFFFFFFu, tc::wait(bar, parity, gone)) != 0; };
-        for (int it = 0; it < n; ++it) {
-            const int s = it % kSlots, b = it & 1;
-            if (!ready(&full[s], (it / kSlots) & 1)) break;
-            if (it >= 2 && !ready(&dfree[2 * t + b], ((it >> 1) - 1) & 1)) break;
-            tc::after_sync();
-            if (tc::elect()) {
+        const uint32_t ring = smem_u32(sm + S::kRing);
+        int it = 0, k = 0;
+        bool ok = true;
+        for (int64_t job = job0; ok && job < job1; ++job) {
+            const Job J(A, job);
+            if (J.n == 0) continue;
+            const uint32_t k_at = smem_u32(sm + S::kK) + (2 * (k & 1) + t) * S::kTileB;
+            ok = ready(&kfull[k & 1], (k >> 1) & 1);
+            for (int i = 0; ok && i < J.n; ++i, ++it) {
+                const int s = it % kSlots, b = it & 1;
+                ok = ready(&full[s], (it / kSlots) & 1) && (it < 2 || ready(&dfree[2 * t + b], ((it >> 1) - 1) & 1));
+                if (!ok) break;
+                tc::after_sync();
+                if (tc::elect()) {
 #pragma unroll
-                for (int k = 0; k < C / 16; ++k) {
-                    const uint32_t at = (k / 4) * (kTile * 128) + (k % 4) * 32;
-                    tc::mma_ss(tmem + (2 * t + b) * kTile, tc::smem_desc(k_at + at, 16),
-                               tc::smem_desc(ring + s * S::kTileB + at, 16), kDesc, k > 0);
+                    for (int c = 0; c < C / 16; ++c) {
+                        const uint32_t at = (c / 4) * (kTile * 128) + (c % 4) * 32;
+                        tc::mma_ss(tmem + (2 * t + b) * kTile, tc::smem_desc(k_at + at, 16),
+                                   tc::smem_desc(ring + s * S::kTileB + at, 16), kDesc, c > 0);
+                    }
+                    tc::commit(&dfull[2 * t + b]);
+                    tc::commit(&empty[s]);
+                    if (i == J.n - 1) tc::commit(&kfree[k & 1]);
                 }
-                tc::commit(&dfull[2 * t + b]);
-                tc::commit(&empty[s]);
+                __syncwarp();
             }
-            __syncwarp();
+            ++k;
         }
     } else if (warp < kSumWarps) {
         // ---- a thread per token of tile t and buffer b (every second row tile): sum of 2^(x - lse)
-        const int t = (warp >> 2) & 1, b = warp >> 3;
-        const int tok = t0 + t * kTile + (warp & 3) * 32 + lane;
-        const int tile_hi = t0 + t * kTile + kTile - 1;
+        const int t = (warp >> 2) & 1, b = warp >> 3, me = (warp & 3) * 32 + lane;
         const uint32_t d_at = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (2 * t + b) * kTile;
         const u64 sc2 = pk(a.scale2, a.scale2);
-        float sum = 0.0f;
-        for (int it = b; it < n; it += 2) {
-            const int s = it % kSlots;
-            bool ok = tc::wait(&full[s], (it / kSlots) & 1, gone) && tc::wait(&dfull[2 * t + b], (it >> 1) & 1, gone);
-            if (!__all_sync(0xFFFFFFFFu, ok)) break;
-            tc::after_sync();
-            const int row0 = (n0 + it) * kTile;
-            const bool cut = tile_hi > base + row0 / a.group;       // some row does not see some token
-            const float4* rp = srow + s * (kTile / 2);
-            u64 acc0 = 0, acc1 = 0;
-            if (!cut) {
-#pragma unroll
-                for (int h = 0; h < 4; ++h) {
-                    uint32_t y[32];
-                    tc::ld32(d_at + 32 * h, y);
-                    tc::wait_ld();
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float4 l = rp[8 * h + i];
-                        const u64 e0 = fma2(pk(__uint_as_float(y[4 * i]), __uint_as_float(y[4 * i + 1])), sc2, pk(l.x, l.y));
-                        const u64 e1 = fma2(pk(__uint_as_float(y[4 * i + 2]), __uint_as_float(y[4 * i + 3])), sc2, pk(l.z, l.w));
-                        acc0 = add2(acc0, pk(ex2(lo_of(e0)), ex2(hi_of(e0))));
-                        acc1 = add2(acc1, pk(ex2(lo_of(e1)), ex2(hi_of(e1))));
-                    }
-                }
-            } else {
+        const int base = a.T - a.n;
+        int it = 0, k = 0;
+        bool ok = true;
+        for (int64_t job = job0; ok && job < job1; ++job) {
+            const Job J(A, job);
+            const int tok = J.t0 + t * kTile + me, tile_hi = J.t0 + t * kTile + kTile - 1;
+            float sum = 0.0f;
+            for (int i = 0; i < J.n; ++i, ++it) {
+                if ((it & 1) != b) continue;
+                const int s = it % kSlots;
+                ok = ready(&full[s], (it / kSlots) & 1) && ready(&dfull[2 * t + b], (it >> 1) & 1);
+                if (!ok) break;
+                tc::after_sync();
+                const int row0 = (J.n0 + i) * kTile;
+                const bool cut = tile_hi > base + row0 / a.group;   // some row does not see some token
+                const float4* rp = srow + s * (kTile / 2);
+                u64 acc0 = 0, acc1 = 0;
+                if (!cut) {
 #pragma unroll 1
-                for (int h = 0; h < 4; ++h) {
-                    uint32_t y[32];
-                    tc::ld32(d_at + 32 * h, y);
-                    tc::wait_ld();
+                    for (int h = 0; h < 4; ++h) {
+                        uint32_t y[32];
+                        tc::ld32(d_at + 32 * h, y);
+                        tc::wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float4 l = rp[8 * h + i], z = rp[kTile / 4 + 8 * h + i];
-                        const u64 e0 = fma2(pk(__uint_as_float(y[4 * i]), __uint_as_float(y[4 * i + 1])), sc2, pk(l.x, l.y));
-                        const u64 e1 = fma2(pk(__uint_as_float(y[4 * i + 2]), __uint_as_float(y[4 * i + 3])), sc2, pk(l.z, l.w));
-                        acc0 = add2(acc0, pk(tok <= __float_as_int(z.x) ? ex2(lo_of(e0)) : 0.0f,
-                                             tok <= __float_as_int(z.y) ? ex2(hi_of(e0)) : 0.0f));
-                        acc1 = add2(acc1, pk(tok <= __float_as_int(z.z) ? ex2(lo_of(e1)) : 0.0f,
-                                             tok <= __float_as_int(z.w) ? ex2(hi_of(e1)) : 0.0f));
+                        for (int c = 0; c < 8; ++c) {
+                            const float4 l = rp[8 * h + c];
+                            const u64 e0 = fma2(pk(__uint_as_float(y[4 * c]), __uint_as_float(y[4 * c + 1])), sc2, pk(l.x, l.y));
+                            const u64 e1 = fma2(pk(__uint_as_float(y[4 * c + 2]), __uint_as_float(y[4 * c + 3])), sc2, pk(l.z, l.w));
+                            acc0 = add2(acc0, pk(ex2(lo_of(e0)), ex2(hi_of(e0))));
+                            acc1 = add2(acc1, pk(ex2(lo_of(e1)), ex2(hi_of(e1))));
+                        }
+                    }
+                } else {
+#pragma unroll 1
+                    for (int h = 0; h < 4; ++h) {
+                        uint32_t y[32];
+                        tc::ld32(d_at + 32 * h, y);
+                        tc::wait_ld();
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) {
+                            const float4 l = rp[8 * h + c], z = rp[kTile / 4 + 8 * h + c];
+                            const u64 e0 = fma2(pk(__uint_as_float(y[4 * c]), __uint_as_float(y[4 * c + 1])), sc2, pk(l.x, l.y));
+                            const u64 e1 = fma2(pk(__uint_as_float(y[4 * c + 2]), __uint_as_float(y[4 * c + 3])), sc2, pk(l.z, l.w));
+                            acc0 = add2(acc0, pk(tok <= __float_as_int(z.x) ? ex2(lo_of(e0)) : 0.0f,
+                                                 tok <= __float_as_int(z.y) ? ex2(hi_of(e0)) : 0.0f));
+                            acc1 = add2(acc1, pk(tok <= __float_as_int(z.z) ? ex2(lo_of(e1)) : 0.0f,
+                                                 tok <= __float_as_int(z.w) ? ex2(hi_of(e1)) : 0.0f));
+                        }
+                    }
+                }
+                tc::before_sync();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&dfree[2 * t + b]);
+                    mbar_arrive(&empty[s]);
+                }
+                const u64 acc = add2(acc0, acc1);
+                sum = __fadd_rn(sum, __fadd_rn(lo_of(acc), hi_of(acc)));
+            }
+            if (!ok) break;
+            // the odd group hands its sums to the even one, which writes
+            const int hp = k & 1;
+            float* hs = half + (hp * 2 + t) * kTile + me;
+            if (b == 1) {
+                if (k >= 2 && !(ok = ready(&hfree[2 * t + hp], ((k >> 1) - 1) & 1))) break;
+                *hs = sum;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&hfull[2 * t + hp]);
+            } else {
+                if (!(ok = ready(&hfull[2 * t + hp], (k >> 1) & 1))) break;
+                sum = tok < J.first ? 0.0f : __fadd_rn(sum, *hs);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&hfree[2 * t + hp]);
+                if (tok < a.T) {
+                    if (A.nsplit > 1) {
+                        A.part[(J.o * A.nsplit + J.split) * ((int64_t)A.ntok * 2 * kTile) + tok] = sum;
+                    } else {
+                        const int64_t at = J.o * A.stride + tok;
+                        A.out[at] = A.in ? __fadd_rn(A.in[at], sum) : sum;
                     }
                 }
             }
-            tc::before_sync();
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(&dfree[2 * t + b]);
-                mbar_arrive(&empty[s]);
-            }
-            const u64 acc = add2(acc0, acc1);
-            sum = __fadd_rn(sum, __fadd_rn(lo_of(acc), hi_of(acc)));
+            ++k;                                 // counts every job here
         }
-        half_sum[b][t * kTile + (warp & 3) * 32 + lane] = sum;
     }
     __syncwarp();
     tc::before_sync();
     __syncthreads();
     tc::after_sync();
     if (warp == kSumWarps + 1) tc::dealloc(tmem, 512);
-    if (tid < 2 * kTile && t0 + tid < a.T && !*gone) {
-        const int tok = t0 + tid;
-        const float sum = tok < first ? 0.0f : __fadd_rn(half_sum[0][tid], half_sum[1][tid]);
-        if (A.nsplit > 1) {
-            A.part[(o * A.nsplit + split) * ((int64_t)A.ntok * 2 * kTile) + tok] = sum;
-        } else {
-            const int64_t at = o * A.stride + tok;
-            A.out[at] = A.in ? __fadd_rn(A.in[at], sum) : sum;
-        }
-    }
 }
 
 __global__ void __launch_bounds__(256)
@@ -306,7 +342,7 @@ join_kernel(const WtArgs A, int64_t total)
     A.out[at] = A.in ? __fadd_rn(A.in[at], s) : s;
 }
 
-constexpr int64_t kMaxCtas = 8 * 152;             // more CTAs than this are not split further
+constexpr int64_t kMaxCtas = 8 * 152;             // more jobs than this are not split further
 
 struct WtPlan { int64_t R, ntok, nsplit; };
 
@@ -315,13 +351,13 @@ WtPlan wt_plan(int64_t outer, int64_t T, int64_t rows)
     WtPlan p;
     p.R = (rows + kTile - 1) / kTile * kTile;
     p.ntok = (T + 2 * kTile - 1) / (2 * kTile);
-    // Splits of the rows that leave the least idle at the end: waves of 152 CTAs,
-    // each the row tiles of a split and the time of about three to lay out its keys.
-    const int64_t ctas = std::max<int64_t>(outer * p.ntok, 1), tiles = p.R / kTile;
+    // Splits of the rows that leave the least idle at the end: rounds of 152 jobs,
+    // each its row tiles, or the time of about three to unpack the next job's keys.
+    const int64_t jobs = std::max<int64_t>(outer * p.ntok, 1), tiles = p.R / kTile;
     p.nsplit = 1;
     int64_t best = INT64_MAX;
-    for (int64_t s = 1; s == 1 || (s <= tiles && ctas * s <= kMaxCtas); ++s) {
-        const int64_t cost = ((ctas * s + 151) / 152) * ((tiles + s - 1) / s + 3);
+    for (int64_t s = 1; s == 1 || (s <= tiles && jobs * s <= kMaxCtas); ++s) {
+        const int64_t cost = (jobs * s + 151) / 152 * std::max<int64_t>((tiles + s - 1) / s + 1, 3);
         if (cost < best) {
             best = cost;
             p.nsplit = s;
@@ -346,14 +382,15 @@ cudaError_t launch_wt(WtArgs A, int64_t outer, void* ws, cudaStream_t st)
     A.part = reinterpret_cast<float*>(at);
     A.nsplit = (int32_t)p.nsplit;
     A.ntok = (int32_t)p.ntok;
-    const int64_t packs = outer * p.R * (C / 8), grid = outer * p.ntok * p.nsplit;
-    if (outer * p.R > 0x7FFFFFFF || grid > 0x7FFFFFFF || packs / 256 >= 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+    const int64_t packs = outer * p.R * (C / 8);
+    A.jobs = outer * p.ntok * p.nsplit;
+    if (outer * p.R > 0x7FFFFFFF || packs / 256 >= 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
     CUtensorMap qm;
     if (!encode_rows_tile_map(qx, outer * p.R, C, &qm)) return cudaErrorNotSupported;
     cudaError_t e = ensure_kernel_attrs(reinterpret_cast<const void*>(weights_tc_kernel<BITS, C>), SmemW<C>::kBytes);
     if (e != cudaSuccess) return e;
     pack_rows_kernel<<<(unsigned)((packs + 255) / 256), 256, 0, st>>>(A.v, A.lse, p.R, C, packs, qx, rows2);
-    weights_tc_kernel<BITS, C><<<(unsigned)grid, kThreadsW, SmemW<C>::kBytes, st>>>(A, qm);
+    weights_tc_kernel<BITS, C><<<(unsigned)std::min<int64_t>(A.jobs, 152), kThreadsW, SmemW<C>::kBytes, st>>>(A, qm);
     if (p.nsplit > 1) {
         const int64_t total = outer * A.v.T;
         join_kernel<<<(unsigned)((total + 255) / 256), 256, 0, st>>>(A, total);
