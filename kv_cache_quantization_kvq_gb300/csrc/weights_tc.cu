@@ -83,9 +83,9 @@ pack_rows_kernel(const View a, const float* lse, int64_t R, int C, int64_t total
 template <int C>
 struct SmemW {
     static constexpr int kTileB = kTile * C * 2;
-    static constexpr int kSlots = 2;             // of the ring of query tiles
+    static constexpr int kSlots = 2, kRowSlots = 4;                 // rings of query tiles and of their rows' data
     static constexpr int kK = 0, kRing = 4 * kTileB;                // two jobs' two key tiles
-    static constexpr int kRows = kRing + kSlots * kTileB, kHalf = kRows + kSlots * kTile * 8;
+    static constexpr int kRows = kRing + kSlots * kTileB, kHalf = kRows + kRowSlots * kTile * 8;
     static constexpr int kBars = kHalf + 2 * 2 * kTile * 4, kBytes = kBars + 256 + 1024;
 };
 
@@ -122,8 +122,10 @@ weights_tc_kernel(const __grid_constant__ WtArgs A, const __grid_constant__ CUte
     float4* srow = reinterpret_cast<float4*>(sm + S::kRows);       // [slot][2][32]: four rows' -lse; their last tokens
     float* half = reinterpret_cast<float*>(sm + S::kHalf);         // [job parity][2 tiles][128]: sums of odd row tiles
     uint64_t* full = reinterpret_cast<uint64_t*>(sm + S::kBars);   // [slot] a query tile has landed
-    uint64_t* empty = full + kSlots;             // [slot] products (2) and row data (2 x 4 warps) are done with it
-    uint64_t* kfull = empty + kSlots;            // [job parity] both key tiles are filled (8 warps)
+    uint64_t* empty = full + kSlots;             // [slot] both products are done with it
+    uint64_t* rfull = empty + kSlots;            // [row slot] the same for -lse and last tokens (2 x 4 warps read them)
+    uint64_t* rempty = rfull + S::kRowSlots;
+    uint64_t* kfull = rempty + S::kRowSlots;            // [job parity] both key tiles are filled (8 warps)
     uint64_t* kfree = kfull + 2;                 // [job parity] both products are done with them
     uint64_t* dfull = kfree + 2;                 // [2 tiles][2 buffers]
     uint64_t* dfree = dfull + 4;
@@ -139,7 +141,11 @@ weights_tc_kernel(const __grid_constant__ WtArgs A, const __grid_constant__ CUte
     if (tid == 0) {
         for (int i = 0; i < kSlots; ++i) {
             mbar_init(&full[i], 1);
-            mbar_init(&empty[i], 10);
+            mbar_init(&empty[i], 2);
+        }
+        for (int i = 0; i < S::kRowSlots; ++i) {
+            mbar_init(&rfull[i], 1);
+            mbar_init(&rempty[i], 8);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&kfull[i], 8);
@@ -186,21 +192,24 @@ weights_tc_kernel(const __grid_constant__ WtArgs A, const __grid_constant__ CUte
         for (int64_t job = job0; ok && job < job1; ++job) {
             const Job J(A, job);
             for (int i = 0; i < J.n; ++i, ++it) {
-                const int s = it % kSlots;
+                const int s = it % kSlots, rs = it % S::kRowSlots;
                 if (it >= kSlots) ok = ready(&empty[s], ((it / kSlots) - 1) & 1);
+                if (ok && it >= S::kRowSlots) ok = ready(&rempty[rs], ((it / S::kRowSlots) - 1) & 1);
                 if (!ok) break;
                 if (tc::elect()) {
-                    mbar_expect_tx(&full[s], S::kTileB + kTile * 8);
                     const int64_t row = J.o * A.R + (int64_t)(J.n0 + i) * kTile;
+                    mbar_expect_tx(&rfull[rs], kTile * 8);
+                    bulk_g2s(srow + rs * (kTile / 2), A.row + row * 2, kTile * 8, &rfull[rs]);
+                    mbar_expect_tx(&full[s], S::kTileB);
                     for (int h = 0; h < kHalves; ++h)
                         tma_load_2d(sm + S::kRing + s * S::kTileB + h * (kTile * 128), &qmap, h * 64, (int)row, &full[s]);
-                    bulk_g2s(srow + s * (kTile / 2), A.row + row * 2, kTile * 8, &full[s]);
                 }
                 __syncwarp();
             }
         }
         // every copy issued lands before the CTA's shared memory goes
         for (int i = max(0, it - kSlots); i < it; ++i) tc::drain(&full[i % kSlots], (i / kSlots) & 1);
+        for (int i = max(0, it - S::kRowSlots); i < it; ++i) tc::drain(&rfull[i % S::kRowSlots], (i / S::kRowSlots) & 1);
     } else if (warp == kSumWarps + 1 || warp == kSumWarps + 2) {
         // ---- products of key tile t
         const int t = warp - kSumWarps - 1;
@@ -247,8 +256,8 @@ weights_tc_kernel(const __grid_constant__ WtArgs A, const __grid_constant__ CUte
             float sum = 0.0f;
             for (int i = 0; i < J.n; ++i, ++it) {
                 if ((it & 1) != b) continue;
-                const int s = it % kSlots;
-                ok = ready(&full[s], (it / kSlots) & 1) && ready(&dfull[2 * t + b], (it >> 1) & 1);
+                const int s = it % S::kRowSlots;
+                ok = ready(&rfull[s], (it / S::kRowSlots) & 1) && ready(&dfull[2 * t + b], (it >> 1) & 1);
                 if (!ok) break;
                 tc::after_sync();
                 const int row0 = (J.n0 + i) * kTile;
@@ -292,7 +301,7 @@ weights_tc_kernel(const __grid_constant__ WtArgs A, const __grid_constant__ CUte
                 __syncwarp();
                 if (lane == 0) {
                     mbar_arrive(&dfree[2 * t + b]);
-                    mbar_arrive(&empty[s]);
+                    mbar_arrive(&rempty[s]);
                 }
                 const u64 acc = add2(acc0, acc1);
                 sum = __fadd_rn(sum, __fadd_rn(lo_of(acc), hi_of(acc)));
