@@ -635,12 +635,16 @@ class KVCache:
 
     def __post_init__(self):
         self.shape = tuple(self.shape)
-        dev = self.k[0].device
+        dev = self.device
         for bufs, qp, who in ((self.k, self.kqp, "k"), (self.v, self.vqp, "v")):
             for t, size in zip(bufs, _store_sizes(self.shape, qp, self.resid_rows)):
                 if size and (t is None or t.nbytes < size or t.device != dev or not t.is_contiguous()):
                     raise ValueError(f"{who}: every buffer must be contiguous, on {dev} and hold its part of the cache "
                                      f"(codes, scale, zero, resid: {_store_sizes(self.shape, qp, self.resid_rows)} bytes)")
+
+    @property
+    def device(self):
+        return next(t for t in (*self.k, *self.v) if t is not None).device
 
     @staticmethod
     def from_quantized(qk: Quantized, qv: Quantized, kv_heads: int = 1, first=None) -> "KVCache":
@@ -656,10 +660,12 @@ class KVCache:
         return self.tq + self.nres
 
     def c(self) -> kvq_cache:
-        if self.first is not None and (str(self.first.dtype) != "torch.int32" or self.first.numel() != self.shape[0]):
-            raise ValueError("first must be int32 [outer]")
+        f = self.first
+        if f is not None and (str(f.dtype) != "torch.int32" or f.numel() != self.shape[0] or not f.is_contiguous() or
+                              f.device != self.device):
+            raise ValueError("first must be int32 [outer] on the cache's device")
         return kvq_cache(*[t if t is None else t.data_ptr() for t in (*self.k, *self.v)], self.tq, self.nres,
-                         self.resid_rows, self.first if self.first is None else self.first.data_ptr())
+                         self.resid_rows, f if f is None else f.data_ptr())
 
 
 class _On:
@@ -675,6 +681,8 @@ class _On:
         if stream is not None:
             if not hasattr(stream, "cuda_stream"):
                 stream = torch.cuda.ExternalStream(int(stream), device=t.device)
+            if stream.device != t.device:
+                raise ValueError(f"the stream is on {stream.device}, the tensors on {t.device}")
             self.ctx = torch.cuda.stream(stream)
         elif self.device != torch.cuda.current_device():
             self.ctx = torch.cuda.device(t.device)
@@ -733,7 +741,7 @@ def _heads(q, cache: KVCache):
     s = tuple(q.shape)
     if len(s) != 4 or cache.kv_heads < 1 or s[0] * cache.kv_heads != outer or s[2] % cache.kv_heads or s[3] != C:
         raise ValueError(f"q must be [batch, n, kv_heads * group, C] with batch * kv_heads = {outer}, C = {C} (got {s})")
-    if q.dtype != torch.bfloat16 or not q.is_contiguous() or not q.is_cuda or cache.k[0].device != q.device:
+    if q.dtype != torch.bfloat16 or not q.is_contiguous() or not q.is_cuda or cache.device != q.device:
         raise ValueError("q must be a contiguous bf16 CUDA tensor on the cache's device")
     return s[1], s[2] // cache.kv_heads
 
@@ -805,10 +813,10 @@ def evict_blocks(cache: KVCache, scores, budget: int, window: int, block: int, d
     _want(scores, "scores", torch.float32, (outer, scores.shape[-1]), dev)
     if scores_out is not scores:
         _want(scores_out, "scores_out", torch.float32, tuple(scores.shape), dev)
-    if not scores.is_cuda or cache.k[0].device != dev:
+    if not scores.is_cuda or cache.device != dev:
         raise ValueError("scores must be a CUDA tensor on the cache's device")
     if dst is not cache and (dst.shape != cache.shape or dst.kqp != cache.kqp or dst.vqp != cache.vqp or
-                             dst.k[0].device != dev):
+                             dst.device != dev):
         raise ValueError("dst must have the cache's shape, formats and device")
     kept = max(0, min(int(budget), cache.tq // max(int(block), 1)))
     if keep is not None:

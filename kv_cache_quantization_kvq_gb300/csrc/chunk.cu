@@ -523,7 +523,7 @@ size_t chunk_workspace(int64_t outer, int64_t C, int64_t tmax, int64_t n, int64_
 {
     const int64_t rows = n * group;
     if (outer == 0 || rows == 0) return 0;
-    if (chunk_uses_tc(tmax, rows)) return chunk_tc_workspace(outer, C, tmax, rows);
+    if (chunk_uses_tc(rows)) return chunk_tc_workspace(outer, C, tmax, rows);
     // every T up to tmax may choose its splits: at most kMaxWaves of CTAs, or one per four batches
     const int64_t mt = rows <= 16 ? 1 : 2, most = (tmax + kBatch - 1) / kBatch + 1;
     const int64_t split_rows = std::min(kMaxWaves * slots_of(mt) * 16 * mt, outer * rows * (most / kWarps));
@@ -573,7 +573,7 @@ cudaError_t launch_attend_chunk(const CacheArgs& x, void* out, float* lse, void*
     A.out = static_cast<__nv_bfloat16*>(out);
     A.lse = lse;
     A.part = static_cast<float*>(ws);
-    if (chunk_uses_tc(A.v.T, A.v.rows)) return launch_attend_tc(A, x.bits, x.C, x.outer, ws, st);
+    if (chunk_uses_tc(A.v.rows)) return launch_attend_tc(A, x.bits, x.C, x.outer, ws, st);
     if (x.bits == 4) return x.C == 128 ? launch_rows<4, 128>(A, x.outer, st) : launch_rows<4, 64>(A, x.outer, st);
     return x.C == 128 ? launch_rows<2, 128>(A, x.outer, st) : launch_rows<2, 64>(A, x.outer, st);
 }

@@ -60,7 +60,7 @@ __device__ __forceinline__ void merge_row(const ChunkArgs& A, int64_t o, int r, 
         A.lse[at] = L > 0.0f ? __fmul_rn(__fadd_rn(M, log2f(L)), 0.6931471805599453f) : -INFINITY;
 }
 
-bool chunk_uses_tc(int64_t T, int64_t rows);
+bool chunk_uses_tc(int64_t rows);
 size_t chunk_tc_workspace(int64_t outer, int64_t C, int64_t tmax, int64_t rows);
 cudaError_t launch_attend_tc(const ChunkArgs& A, int bits, int64_t C, int64_t outer, void* ws, cudaStream_t st);
 

@@ -742,7 +742,7 @@ Waves waves_of(int64_t tiles, int64_t Tp)
 template <int BITS, int C>
 cudaError_t launch_tc(const ChunkArgs& A0, int64_t outer, void* ws, cudaStream_t st)
 {
-    const bool fused = fused_form(A0.v.rows);
+    const bool fused = fused_form(A0.v.rows) || A0.v.T == 0;        // an empty cache has nothing to expand
     TcPlan p = tc_plan(outer, C, A0.v.T, A0.v.rows);
     if (fused) p.slices = outer;
     TcArgs X;
@@ -802,7 +802,7 @@ bool encode_rows_tile_map(const void* x, int64_t rows, int64_t C, CUtensorMap* m
 
 // Rows from which the tensor-core forms are taken (64 slices of 32768 tokens: 32
 // rows 249 us on mma.sync and 349 here, 64 rows 506 and 351).
-bool chunk_uses_tc(int64_t T, int64_t rows) { return rows > 32 && T > 0; }
+bool chunk_uses_tc(int64_t rows) { return rows > 32; }
 
 // Enough for every T up to tmax: a shorter cache may take more slices at once,
 // but never more than the bound on expanded bytes.

@@ -69,6 +69,13 @@ CASES = {
     "prompt, two bits, C 64": (1, 1, 4, 200, 64, 512, 576, 30, 64, dict(bits=2, kind="sym"), {}),
     "prompt, far zero points": (1, 1, 3, 250, 128, 320, 320, 30, 64, {}, dict(shift=-60.0)),
     "prompt, padded": (3, 1, 4, 150, 128, 333, 333, 60, 64, dict(gk=96), dict(first=[0, 130, 390])),
+    "many rows, empty cache": (2, 1, 4, 20, 128, 0, 64, 0, 64, {}, {}),
+    "prompt, empty cache": (1, 1, 4, 100, 64, 0, 64, 0, 64, {}, {}),
+    "rows of 24": (1, 2, 8, 3, 128, 512, 512, 40, 64, {}, {}),
+    "rows of 32, two bits": (2, 1, 16, 2, 64, 384, 384, 40, 64, dict(bits=2), dict(first=[0, 77])),
+    "rows of 33": (1, 1, 33, 1, 128, 256, 256, 40, 64, {}, {}),
+    "rows of 256": (1, 1, 64, 4, 128, 640, 640, 40, 64, {}, {}),
+    "rows of 257": (1, 1, 1, 257, 128, 640, 640, 40, 64, {}, {}),
     "loud": (1, 1, 4, 6, 128, 512, 512, 64, 64, {}, dict(scale=6.0)),
 }
 
@@ -134,7 +141,7 @@ def test_attend_chunk(b, name):
     assert np.array_equal(np.isneginf(gl), none)
     assert np.all(got[none] == 0.0)
     tl = S.to_rows(e, H) + (hc.T + 64) * 2.0 ** -23 + 4 * 2.0 ** -23 * (np.abs(wl) + 1)
-    assert np.all(np.abs(gl - wl)[~none] <= tl[~none]), np.max((np.abs(gl - wl) / tl)[~none])
+    assert np.all(np.abs(gl[~none] - wl[~none]) <= tl[~none]), np.max(np.abs(gl[~none] - wl[~none]) / tl[~none])
     u = 2.0 ** -8
     to = S.to_rows((u + e[..., None] + (hc.T + 64) * 2.0 ** -23) * absout, H) + u * np.abs(want) + 1e-30
     assert np.all(np.isfinite(got))
@@ -234,3 +241,102 @@ def test_from_quantized_agrees_with_dequantize(b):
     tol = 2.0 ** -8 * (want.abs() + p @ V.abs()) + 1e-4
     assert bool(((out.reshape(4, 4, 128).double() - want).abs() <= tol).all())
     assert bool(((lse.reshape(4, 4).double() - torch.logsumexp(x, -1)).abs() <= 1e-4).all())
+
+
+def test_more_slices_than_are_expanded_at_once(b):
+    """Over 1 GiB of expanded rows: several rounds of slices.  The last queries of
+    the chunk are also asked for alone, which takes the kernel of few rows."""
+    import torch
+    outer, T, C, n, G = 20, 112000, 128, 80, 4
+    assert outer * T * C * 4 > 1 << 30
+    gen = torch.Generator(device="cuda").manual_seed(7)
+    kq, vq = (b.QParams.asym(4, 0, 15, axis=a, group=64, scale_dtype=b.BF16, zero_dtype=b.BF16) for a in (b.ALONG_T, b.ALONG_C))
+    k, v = (b.quantize(torch.randn((outer, T, C), generator=gen, device="cuda").bfloat16(), qp) for qp in (kq, vq))
+    cache = b.KVCache.from_quantized(k, v, kv_heads=outer // 2)
+    q = torch.randn((2, n, outer // 2 * G, C), generator=gen, device="cuda").bfloat16()
+    out, lse = b.attend_chunk(q, cache)
+    few, fl = b.attend_chunk(q[:, -8:].contiguous(), cache)
+    # both are within u (sum p |v| + |out|) of the same value, u = 2^-8, and |v| <= 6 here
+    assert bool(((out[:, -8:].float() - few.float()).abs() <= 2 * 2.0 ** -8 * (6 + few.float().abs())).all())
+    assert bool((lse[:, -8:] - fl).abs().max() <= 1e-4)
+    assert bool(out.float().abs().sum(-1).gt(0).all())
+
+
+def test_serving_loop(b):
+    """append -> attend -> weights -> evict, as a decoder runs them, against the
+    formulas over the rows that the cache holds at each step."""
+    import torch
+    outer, kvh, G, C, block, budget, window = 4, 2, 4, 128, 64, 5, 2
+    cap, R = block * (budget + 2), 32
+    kqo, vqo = S.formats()
+    kqp, vqp = (b.QParams.asym(4, 0, 15, axis=a, group=64, residual=R, scale_dtype=b.BF16, zero_dtype=b.BF16)
+                for a in (b.ALONG_T, b.ALONG_C))
+    shape = (outer, cap, C)
+    bufs = []
+    for qp in (kqp, vqp):
+        sizes = b.kvq_quantized_sizes(shape, b.BF16, b.QParams.asym(4, 0, 15, axis=qp.axis, group=64, scale_dtype=b.BF16,
+                                                                      zero_dtype=b.BF16))
+        bufs.append([torch.zeros(s, dtype=torch.uint8, device="cuda") for s in sizes[:3]] +
+                    [torch.zeros((outer, R + block, C), dtype=torch.bfloat16, device="cuda")])
+    ws = torch.empty(b.kvq_append_kv_workspace(shape, b.BF16, kqp, vqp, block), dtype=torch.uint8, device="cuda")
+    app = b.KVAppender(shape, b.BF16, kqp, vqp, block, bufs[0], bufs[1], ws)
+    cache = b.KVCache(k=tuple(bufs[0]), v=tuple(bufs[1]), shape=shape, kqp=kqp, vqp=vqp, tq=0, nres=0,
+                      resid_rows=R + block, kv_heads=kvh)
+    scores = torch.zeros((outer, cap + R + block), device="cuda")
+    gen = torch.Generator(device="cuda").manual_seed(11)
+
+    def held():
+        torch.cuda.synchronize()
+        rows = []
+        for bf, qo, mr in ((bufs[0], kqo, cache.tq // 64), (bufs[1], vqo, cache.tq)):
+            x = np.zeros((outer, 0, C))
+            if cache.tq:
+                full = cap // 64 if qo is kqo else cap
+                width = C if qo is kqo else C // 64
+                codes = bf[0].cpu().numpy().reshape(outer, cap, C // 2)[:, :cache.tq]
+                sc, ze = (S.bf16_to_f64(t.cpu().numpy().view(np.uint16).reshape(outer, full, width)[:, :mr]) for t in bf[1:3])
+                c = np.stack([codes & 15, codes >> 4], -1).reshape(outer, cache.tq, C).astype(np.float64)
+                rep = (1, 64) if qo is kqo else (2, 64)
+                x = (c - np.repeat(ze, rep[1], rep[0])) * np.repeat(sc, rep[1], rep[0])
+                x = S.bf16_to_f64(S.W.to_bf16_bits(x.astype(np.float32)))
+            r = bf[3][:, :cache.nres].cpu().view(torch.int16).numpy().view(np.uint16)
+            rows.append(np.concatenate([x, S.bf16_to_f64(r)], 1))
+        return rows
+
+    evictions = 0
+    for step in range(150):
+        n = 200 if step == 0 else 1 if step % 9 else 37       # a prompt, then tokens and drafted runs
+        k, v = (torch.randn((outer, n, C), generator=gen, device="cuda").bfloat16() for _ in range(2))
+        app.append(k, v, n)
+        cache.tq, cache.nres = app.tq, app.nres
+        q = (2 * torch.randn((outer // kvh, n, kvh * G, C), generator=gen, device="cuda")).bfloat16()
+        out, lse = b.attend_chunk(q, cache)
+        before = scores.clone()
+        b.attend_weights(q, lse, cache, scores, scores)
+        K, V = held()
+        x, mag = S.logits(q.float().cpu().numpy().astype(np.float64), K, None, kvh)
+        p, wl = S.softmax(x)
+        e = 2 * S.logit_error(mag, x, C)
+        u = 2.0 ** -8
+        want, absout = np.einsum("oijt,otc->oijc", p, V), np.einsum("oijt,otc->oijc", p, np.abs(V))
+        to = S.to_rows((u + e[..., None] + (cache.T + 64) * 2.0 ** -23) * absout, kvh) + u * np.abs(S.to_rows(want, kvh)) + 1e-30
+        assert np.all(np.abs(out.float().cpu().numpy() - S.to_rows(want, kvh)) <= to), step
+        # the weights use the kernel's own lse, off by at most e more than its rounding
+        tw = np.einsum("oijt,oij->ot", p, 2 * e + (n * G + cache.T + 128) * 2.0 ** -23 + 16 * 2.0 ** -23 * (np.abs(wl) + 1))
+        old = before[:, :cache.T].cpu().numpy().astype(np.float64)
+        got = scores[:, :cache.T].cpu().numpy().astype(np.float64)
+        assert np.all(np.abs(got - old - p.sum((1, 2))) <= tw + 2.0 ** -23 * (old + 1)), step
+        if cache.tq > block * budget:
+            nb, sc = cache.tq // block, scores.cpu().numpy()
+            b.evict_blocks(cache, scores, budget, window, block)
+            app.set_counters(cache.tq, cache.nres)
+            K2, V2 = held()
+            for o in range(outer):
+                s = [sc[o, i * block:(i + 1) * block].astype(np.float64).sum() for i in range(nb - window)]
+                ids = sorted(sorted(range(nb - window), key=lambda i: (-s[i], i))[:budget - window] + list(range(nb - window, nb)))
+                tok = np.array([i * block + y for i in ids for y in range(block)] + list(range(nb * block, nb * block + cache.nres)))
+                assert np.array_equal(K2[o], K[o, tok]) and np.array_equal(V2[o], V[o, tok])
+                new = scores[o].cpu().numpy()
+                assert np.array_equal(new[:len(tok)], sc[o, tok]) and not new[len(tok):].any()
+            evictions += 1
+    assert evictions >= 2 and cache.tq <= block * (budget + 1)

@@ -141,3 +141,31 @@ def test_workspace_queries_refuse_bad_arguments(kb):
         assert e.value.status == kb.EUNSUPPORTED
     with pytest.raises(kb.KvqError):
         kb.kvq_evict_blocks_workspace((4, 64, 128), 0)
+
+
+def test_python_objects_refuse_what_does_not_fit(kb):
+    """KVCache and the helpers check sizes, types and devices before any call."""
+    import torch
+    shape, rows = (2, 128, 128), 64
+    ok = {w: tuple(torch.zeros(n, dtype=torch.uint8) for n in kb._store_sizes(shape, q, rows))
+          for w, q in (("k", kq(kb)), ("v", vq(kb)))}
+    make = dict(shape=shape, kqp=kq(kb), vqp=vq(kb), tq=64, nres=3, resid_rows=rows)
+    c = kb.KVCache(**ok, **make)
+    assert c.T == 67
+    for w in ("k", "v"):
+        for i in range(4):
+            for bad in (None, torch.zeros(ok[w][i].numel() - 1, dtype=torch.uint8)):
+                with pytest.raises(ValueError):
+                    kb.KVCache(**{**ok, w: ok[w][:i] + (bad,) + ok[w][i + 1:]}, **make)
+    with pytest.raises(ValueError):
+        kb.attend_chunk(torch.zeros((1, 1, 8, 128), dtype=torch.bfloat16), c)           # not a CUDA tensor
+    for q in (torch.zeros((1, 8, 128), dtype=torch.bfloat16), torch.zeros((3, 1, 8, 128), dtype=torch.bfloat16),
+              torch.zeros((2, 1, 8, 64), dtype=torch.bfloat16), torch.zeros((2, 1, 8, 128))):
+        with pytest.raises(ValueError):
+            kb.attend_chunk(q, c)
+    with pytest.raises(ValueError):
+        kb.evict_blocks(c, torch.zeros((2, 200)), 1, 0, 64)
+    with pytest.raises(ValueError):
+        kb.KVCache(**ok, **make, first=torch.zeros(2)).c()
+    with pytest.raises(ValueError):
+        kb.KVCache(**ok, **make, first=torch.zeros(3, dtype=torch.int32)).c()
