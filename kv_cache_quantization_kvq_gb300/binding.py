@@ -172,6 +172,10 @@ class QParams:
     def asym(bits, qmin, qmax, axis=ALONG_T, group=0, residual=0, scale_dtype=F32, zero_dtype=I8):
         return QParams(bits, ASYM, qmin, qmax, axis, group, residual, scale_dtype, zero_dtype)
 
+    @functools.cached_property
+    def _c(self) -> kvq_qparams:               # read by the library only, so one may serve every call
+        return self.c()
+
     def c(self) -> kvq_qparams:
         return kvq_qparams(self.bits, self.mode, self.qmin, self.qmax, self.axis, self.group,
                            self.residual, self.scale_dtype, self.zero_dtype)
@@ -605,9 +609,18 @@ def rotate(x, signs, inverse=False, out=None, out_dtype=None, stream=None):
 
 # ---- the streaming cache (torch tensors; calls run on the tensors' device) -----
 
-@functools.lru_cache(maxsize=1024)
 def _store_sizes(shape, qp: QParams, resid_rows: int):
     """Bytes of (codes, scale, zero, resid) of one cache: a store without residual and the bf16 buffer."""
+    known = qp.__dict__.setdefault("_sizes", {})
+    sizes = known.get((shape, resid_rows))
+    if sizes is None:
+        if len(known) > 64:
+            known.clear()
+        sizes = known[shape, resid_rows] = _sizes_of(shape, qp, resid_rows)
+    return sizes
+
+
+def _sizes_of(shape, qp: QParams, resid_rows: int):
     store = QParams(qp.bits, qp.mode, qp.qmin, qp.qmax, qp.axis, qp.group, 0, qp.scale_dtype, qp.zero_dtype)
     return kvq_quantized_sizes(shape, BF16, store)[:3] + (shape[0] * resid_rows * shape[2] * 2,)
 
@@ -644,7 +657,8 @@ class KVCache:
 
     @property
     def device(self):
-        return next(t for t in (*self.k, *self.v) if t is not None).device
+        t = self.k[0]
+        return (t if t is not None else next(x for x in (*self.k, *self.v) if x is not None)).device
 
     @staticmethod
     def from_quantized(qk: Quantized, qv: Quantized, kv_heads: int = 1, first=None) -> "KVCache":
@@ -704,11 +718,6 @@ def _shape_of(shape) -> kvq_shape:
     return _shape(shape)
 
 
-@functools.lru_cache(maxsize=256)
-def _params_of(qp: QParams) -> kvq_qparams:
-    return qp.c()
-
-
 _chunk_ws = functools.lru_cache(maxsize=1024)(kvq_attend_chunk_workspace)
 _weights_ws = functools.lru_cache(maxsize=1024)(kvq_attend_weights_workspace)
 _evict_ws = functools.lru_cache(maxsize=1024)(kvq_evict_blocks_workspace)
@@ -765,8 +774,8 @@ def attend_chunk(q, cache: KVCache, out=None, lse=None, workspace=None, stream=N
         if workspace is None:
             workspace = _temporary(_chunk_ws(cache.shape, cache.resid_rows, n, group), dev)
         ws, ws_B = _scratch(workspace, dev)
-        _check(LIB.kvq_attend_chunk(q.data_ptr(), n, group, cache.kv_heads, ref(cache.c()), ref(_params_of(cache.kqp)),
-                                    ref(_params_of(cache.vqp)), ref(_shape_of(cache.shape)), out.data_ptr(),
+        _check(LIB.kvq_attend_chunk(q.data_ptr(), n, group, cache.kv_heads, ref(cache.c()), ref(cache.kqp._c),
+                                    ref(cache.vqp._c), ref(_shape_of(cache.shape)), out.data_ptr(),
                                     lse.data_ptr(), ws, ws_B, handle))
     return out, lse
 
@@ -794,7 +803,7 @@ def attend_weights(q, lse, cache: KVCache, scores=None, out=None, workspace=None
             workspace = _temporary(_weights_ws(cache.shape, cache.resid_rows, n, group), dev)
         ws, ws_B = _scratch(workspace, dev)
         _check(LIB.kvq_attend_weights(q.data_ptr(), lse.data_ptr(), n, group, cache.kv_heads, ref(cache.c()),
-                                      ref(_params_of(cache.kqp)), ref(_shape_of(cache.shape)),
+                                      ref(cache.kqp._c), ref(_shape_of(cache.shape)),
                                       None if scores is None else scores.data_ptr(), out.data_ptr(), out.shape[1], ws, ws_B,
                                       handle))
     return out
@@ -828,7 +837,7 @@ def evict_blocks(cache: KVCache, scores, budget: int, window: int, block: int, d
             workspace = _temporary(_evict_ws(cache.shape, block), dev)
         ws, ws_B = _scratch(workspace, dev)
         to = dst.c()
-        _check(LIB.kvq_evict_blocks(ref(cache.c()), ref(to), ref(_params_of(cache.kqp)), ref(_params_of(cache.vqp)),
+        _check(LIB.kvq_evict_blocks(ref(cache.c()), ref(to), ref(cache.kqp._c), ref(cache.vqp._c),
                                     ref(_shape_of(cache.shape)), block, budget, window, scores.data_ptr(),
                                     scores_out.data_ptr(), scores.shape[1], keep.data_ptr(), ws, ws_B, handle))
     dst.tq, dst.nres = to.tq, to.nres

@@ -229,30 +229,48 @@ attend_rows_kernel(const ChunkArgs A)
     auto load_k = [&](int b) {
         const uint8_t* p = kc + (int64_t)b * (kBatch * G::kRowB);
         const int cnt = a.tq - b * kBatch - 1;
+        if (cnt >= kBatch - 1) {
+            p += g * G::kRowB;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) load_words<G::kWpl>(p + min(8 * j + g, cnt) * G::kRowB, kw[j]);
+            for (int j = 0; j < 4; ++j) load_words<G::kWpl>(p + 8 * j * G::kRowB, kw[j]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) load_words<G::kWpl>(p + min(8 * j + g, cnt) * G::kRowB, kw[j]);
+        }
     };
     auto load_v = [&](int b) {
         const uint8_t* p = vc + (int64_t)b * (kBatch * G::kRowB);
         const int cnt = a.tq - b * kBatch - 1;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const uint8_t* at = p + min(8 * (k >> 1) + 2 * tig + (k & 1), cnt) * G::kRowB;
+        auto one = [&](int k, const uint8_t* at) {
             if constexpr (G::kVB >= 4) load_words<G::kVW>(at, vw[k]);
             else vw[k][0] = __ldcs(reinterpret_cast<const uint16_t*>(at));
+        };
+        if (cnt >= kBatch - 1) {
+            p += 2 * tig * G::kRowB;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) one(k, p + (8 * (k >> 1) + (k & 1)) * G::kRowB);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) one(k, p + min(8 * (k >> 1) + 2 * tig + (k & 1), cnt) * G::kRowB);
         }
     };
     // (scale, zero point) of token `lane` of a batch, a word per V group; hidden tokens get
     // zeros, since theirs may be NaN
-    uint32_t vr[4];
+    uint32_t vr[4] = {0u, 0u, 0u, 0u};
     auto load_vm = [&](int b) {
         const int t = b * kBatch + lane;
-        const int64_t at = vmeta + (int64_t)t * a.ngv;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        const bool live = t >= first && t < a.tq;
+        const __nv_bfloat16* ps = a.vs + vmeta + (int64_t)t * a.ngv;
+        const __nv_bfloat16* pz = a.vz + vmeta + (int64_t)t * a.ngv;
+        auto one = [&](int k) {
             vr[k] = 0u;
-            if (k < a.ngv && t >= first && t < a.tq)
-                vr[k] = bits_of(a.vs + at + k) | (a.vz ? bits_of(a.vz + at + k) << 16 : 0u);
+            if (live) vr[k] = bits_of(ps + k) | (a.vz ? bits_of(pz + k) << 16 : 0u);
+        };
+        one(0);
+        if (a.ngv > 1) one(1);
+        if (a.ngv > 2) {
+            one(2);
+            one(3);
         }
     };
     KRaw kr = {0u, 0u, 0u, 0u};
@@ -276,14 +294,20 @@ attend_rows_kernel(const ChunkArgs A)
         // the V constants of this batch
         bool vfast = true;
         if (a.vz) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) vfast = vfast && zero_exact(bf_hi(vr[k]));
+            vfast = zero_exact(bf_hi(vr[0])) && zero_exact(bf_hi(vr[1]));
+            if (a.ngv > 2) vfast = vfast && zero_exact(bf_hi(vr[2])) && zero_exact(bf_hi(vr[3]));
             vfast = __all_sync(0xFFFFFFFFu, vfast);
         }
         __syncwarp();                            // the batch before has been read
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-            if (k < a.ngv) vms[warp][k][lane] = vfast ? (vr[k] & 0xFFFFu) | (biased(vr[k], 128.0f + a.voff) & 0xFFFF0000u) : vr[k];
+        auto stage = [&](int k) {
+            vms[warp][k][lane] = vfast ? (vr[k] & 0xFFFFu) | (biased(vr[k], 128.0f + a.voff) & 0xFFFF0000u) : vr[k];
+        };
+        stage(0);
+        if (a.ngv > 1) stage(1);
+        if (a.ngv > 2) {
+            stage(2);
+            stage(3);
+        }
         __syncwarp();
 
         float s[MT][4][4];
