@@ -14,7 +14,7 @@
 // codes to B fragments in registers (kvq_rows.cuh).
 //
 // attend_rows_kernel: a CTA takes (slice, split of the visible batches) for
-// the slice's 16 MT query rows; each of its four warps walks its run of the split's
+// the slice's up to 8, 16 or 32 query rows; each of its four warps walks its run of the split's
 // 32-token batches with its own m, l, y, merged through shared memory at the
 // end.  The query fragments and the key group's constants stay in shared memory
 // (12 warps a SM instead of 8), the next batch's codes are loaded as soon as the
@@ -40,11 +40,42 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kAhead = 3;                         // batches that the codes are fetched into L2 ahead
 constexpr float kSlack = 8.0f;                   // base-2 growth of the maximum that is let pass
 
+// What a number of query rows takes: MT tiles of 16 rows of the score product, H
+// halves of a tile in use.  Up to 8 rows the value product is transposed, Y^T[C x 8]
+// = V^T[C x tokens] P^T[tokens x 8]: a lane's score fragment of row g is just the B
+// fragment of P^T and two value B fragments are the A fragment of V^T, and the
+// output takes half the registers and half the products (16 warps a SM instead of
+// 12).
+template <int ROWS, int C>
+struct Rows {
+    static constexpr int MT = (ROWS + 15) / 16, H = ROWS == 8 ? 1 : 2;
+    static constexpr int NT = ROWS == 8 ? C / 16 : C / 8;          // output fragments of a tile
+    static constexpr int kCtas = ROWS == 8 ? 4 : ROWS == 16 ? 3 : 2;
+    static constexpr int kOut = ROWS == 8 ? 8 : 16;                // rows merged at a time
+};
+
+// y += P.V for 16 tokens: b0, b1: the value fragments of n-tiles nt and nt + 1 (tokens 2 tig + {0, 1} and + 8)
+template <int ROWS, int C>
+__device__ __forceinline__ void add_values(float (&y)[Rows<ROWS, C>::MT][Rows<ROWS, C>::NT][4], int nt,
+                                           const uint4 (&p)[Rows<ROWS, C>::MT], uint32_t b0, uint32_t b1, uint32_t c0,
+                                           uint32_t c1) {
+    if constexpr (ROWS == 8) {
+        mma16816(y[0][nt / 2], make_uint4(b0, c0, b1, c1), p[0].x, p[0].z);
+    } else {
+#pragma unroll
+        for (int m = 0; m < Rows<ROWS, C>::MT; ++m) {
+            mma16816(y[m][nt], p[m], b0, b1);
+            mma16816(y[m][nt + 1], p[m], c0, c1);
+        }
+    }
+}
+
 // P.V of one 32-token batch of the store: this lane's code words of its eight
 // tokens, 16 ks + {2 tig, 2 tig + 1, 8 + 2 tig, 9 + 2 tig}; vm: (scale, zero
 // point) of each token and V group.
-template <int BITS, int C, int MT, bool FAST>
-__device__ __forceinline__ void values_of(float (&y)[MT][C / 8][4], const uint4 (&p)[MT][2],
+template <int BITS, int C, int ROWS, bool FAST>
+__device__ __forceinline__ void values_of(float (&y)[Rows<ROWS, C>::MT][Rows<ROWS, C>::NT][4],
+                                          const uint4 (&p)[2][Rows<ROWS, C>::MT],
                                           const uint32_t (&w)[8][Geo<BITS, C>::kVW], const uint32_t* vm, uint32_t mg,
                                           float off, int tig) {
     using G = Geo<BITS, C>;
@@ -61,12 +92,11 @@ __device__ __forceinline__ void values_of(float (&y)[MT][C / 8][4], const uint4 
             const uint32_t x0 = __byte_perm(w[4 * ks][h / 2], w[4 * ks + 1][h / 2], sel);
             const uint32_t x1 = __byte_perm(w[4 * ks + 2][h / 2], w[4 * ks + 3][h / 2], sel);
 #pragma unroll
-            for (int i = 0; i < FH; ++i) {
-                const uint32_t b0 = value_pair<BITS, FAST>(x0, BITS * i, mg, s0, z0, off);
-                const uint32_t b1 = value_pair<BITS, FAST>(x1, BITS * i, mg, s1, z1, off);
-#pragma unroll
-                for (int m = 0; m < MT; ++m) mma16816(y[m][h * FH + i], p[m][ks], b0, b1);
-            }
+            for (int i = 0; i < FH; i += 2)
+                add_values<ROWS, C>(y, h * FH + i, p[ks], value_pair<BITS, FAST>(x0, BITS * i, mg, s0, z0, off),
+                                    value_pair<BITS, FAST>(x1, BITS * i, mg, s1, z1, off),
+                                    value_pair<BITS, FAST>(x0, BITS * (i + 1), mg, s0, z0, off),
+                                    value_pair<BITS, FAST>(x1, BITS * (i + 1), mg, s1, z1, off));
         }
     }
 }
@@ -104,75 +134,89 @@ __device__ __forceinline__ void write_row(const ChunkArgs& A, int64_t o, int r, 
         A.lse[at] = L > 0.0f ? __fmul_rn(__fadd_rn(M, log2f(L)), 0.6931471805599453f) : -INFINITY;
 }
 
-// Softmax state of a lane's rows (g and g + 8 of each tile).
-template <int MT>
-struct Running { float m[MT][2], l[MT][2]; };
+// Softmax state of a lane's rows (g, and g + 8 of each tile unless there are at most 8).
+template <int MT, int H>
+struct Running { float m[MT][H], l[MT][H]; };
 
 // Masks (unless `whole`), moves the maximum if it must, and turns scores into
-// the weights' A fragments.
-template <int C, int MT>
-__device__ __forceinline__ void softmax_of(const View& a, float (&s)[MT][4][4], float (&y)[MT][C / 8][4], Running<MT>& st,
-                                           uint4 (&p)[MT][2], bool whole, int t0, int t1, int first,
-                                           const int (&last)[MT][2], int tig) {
+// the weights' fragments.
+template <int C, int ROWS, class R = Rows<ROWS, C>>
+__device__ __forceinline__ void softmax_of(const View& a, float (&s)[R::MT][4][4], float (&y)[R::MT][R::NT][4],
+                                           Running<R::MT, R::H>& st, uint4 (&p)[2][R::MT], bool whole, int t0, int t1,
+                                           int first, const int (&last)[R::MT][R::H], int tig) {
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
+    for (int m = 0; m < R::MT; ++m) {
         if (!whole) {
             // selected, not multiplied: a hidden token's score may be NaN
 #pragma unroll
             for (int j = 0; j < 4; ++j)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
+                for (int e = 0; e < 2 * R::H; ++e) {
                     const int t = t0 + 8 * j + 2 * tig + (e & 1);
                     if (t < first || t >= t1 || t > last[m][e >> 1]) s[m][j][e] = -INFINITY;
                 }
         }
-        float top[2];
+        float top[R::H];
+        bool grow[R::H], any = false;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < R::H; ++h) {
             float x = fmaxf(fmaxf(fmaxf(s[m][0][2 * h], s[m][0][2 * h + 1]), fmaxf(s[m][1][2 * h], s[m][1][2 * h + 1])),
                             fmaxf(fmaxf(s[m][2][2 * h], s[m][2][2 * h + 1]), fmaxf(s[m][3][2 * h], s[m][3][2 * h + 1])));
             x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 1));
             x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 2));
             top[h] = __fmul_rn(x, a.scale2);
+            grow[h] = top[h] > __fadd_rn(st.m[m][h], kSlack);
+            any = any || grow[h];
         }
-        const bool grow[2] = {top[0] > __fadd_rn(st.m[m][0], kSlack), top[1] > __fadd_rn(st.m[m][1], kSlack)};
-        if (__any_sync(0xFFFFFFFFu, grow[0] || grow[1])) {
+        if (__any_sync(0xFFFFFFFFu, any)) {
+            float f[R::H];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const float f = grow[h] ? ex2(__fsub_rn(st.m[m][h], top[h])) : 1.0f;
+            for (int h = 0; h < R::H; ++h) {
+                f[h] = grow[h] ? ex2(__fsub_rn(st.m[m][h], top[h])) : 1.0f;
                 if (grow[h]) st.m[m][h] = top[h];
-                st.l[m][h] = __fmul_rn(st.l[m][h], f);
+                st.l[m][h] = __fmul_rn(st.l[m][h], f[h]);
+            }
+            // columns of a fragment: rows g and g + 8 of the tile, or (transposed) rows 2 tig and 2 tig + 1
+            float f0 = f[0], f1 = f[R::H - 1];
+            if constexpr (ROWS == 8) {
+                f0 = __shfl_sync(0xFFFFFFFFu, f[0], 8 * tig);
+                f1 = __shfl_sync(0xFFFFFFFFu, f[0], 8 * tig + 4);
+            }
 #pragma unroll
-                for (int nt = 0; nt < C / 8; ++nt) {
-                    y[m][nt][2 * h] = __fmul_rn(y[m][nt][2 * h], f);
-                    y[m][nt][2 * h + 1] = __fmul_rn(y[m][nt][2 * h + 1], f);
-                }
+            for (int nt = 0; nt < R::NT; ++nt) {
+                y[m][nt][0] = __fmul_rn(y[m][nt][0], f0);
+                y[m][nt][1] = __fmul_rn(y[m][nt][1], ROWS == 8 ? f1 : f0);
+                y[m][nt][2] = __fmul_rn(y[m][nt][2], ROWS == 8 ? f0 : f1);
+                y[m][nt][3] = __fmul_rn(y[m][nt][3], f1);
             }
         }
-        const float neg[2] = {st.m[m][0] == -INFINITY ? 0.0f : -st.m[m][0], st.m[m][1] == -INFINITY ? 0.0f : -st.m[m][1]};
-        uint32_t w[4][2];
+        uint32_t w[4][2] = {};
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int h = 0; h < R::H; ++h) {
+            const float neg = st.m[m][h] == -INFINITY ? 0.0f : -st.m[m][h];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const float e0 = ex2(__fmaf_rn(s[m][j][2 * h], a.scale2, neg[h]));
-                const float e1 = ex2(__fmaf_rn(s[m][j][2 * h + 1], a.scale2, neg[h]));
+            for (int j = 0; j < 4; ++j) {
+                const float e0 = ex2(__fmaf_rn(s[m][j][2 * h], a.scale2, neg));
+                const float e1 = ex2(__fmaf_rn(s[m][j][2 * h + 1], a.scale2, neg));
                 st.l[m][h] = __fadd_rn(st.l[m][h], __fadd_rn(e0, e1));
                 w[j][h] = pack_bf16x2(e0, e1);
             }
-        p[m][0] = make_uint4(w[0][0], w[0][1], w[1][0], w[1][1]);
-        p[m][1] = make_uint4(w[2][0], w[2][1], w[3][0], w[3][1]);
+        }
+        p[0][m] = make_uint4(w[0][0], w[0][1], w[1][0], w[1][1]);
+        p[1][m] = make_uint4(w[2][0], w[2][1], w[3][0], w[3][1]);
     }
 }
 
-template <int BITS, int C, int MT>
-__global__ void __launch_bounds__(kThreads, MT == 1 ? 3 : 2)
+template <int BITS, int C, int ROWS>
+__global__ void __launch_bounds__(kThreads, (Rows<ROWS, C>::kCtas))
 attend_rows_kernel(const ChunkArgs A)
 {
     using G = Geo<BITS, C>;
+    using R = Rows<ROWS, C>;
+    constexpr int MT = R::MT, H = R::H;
     const View& a = A.v;
     __shared__ float sm[kWarps][16], sl[kWarps][16], gm[16], gl[16];
-    __shared__ __align__(16) float sy[kWarps][16][C];
+    __shared__ __align__(16) float sy[kWarps][R::kOut][C];
     __shared__ __align__(16) uint4 qf[MT * G::kSteps * 32];
     __shared__ __align__(16) uint4 kcs[kWarps][C / 4];
     __shared__ __align__(16) uint32_t vms[kWarps][4][kBatch];
@@ -185,12 +229,11 @@ attend_rows_kernel(const ChunkArgs A)
 
     // ---- the last token each of this lane's rows sees
     const int base = a.T - a.n;                  // token of query 0
-    int last[MT][2];
+    int last[MT][H];
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {               // rows past the last are not written
-        last[m][0] = base + (16 * m + g) / a.group;
-        last[m][1] = base + (16 * m + g + 8) / a.group;
-    }
+    for (int m = 0; m < MT; ++m)                 // rows past the last are not written
+#pragma unroll
+        for (int h = 0; h < H; ++h) last[m][h] = base + (16 * m + g + 8 * h) / a.group;
     const int last_hi = a.T - 1, last_lo = base;                   // of the last and of the first row
     const int first = a.first ? max(a.first[o], 0) : 0;
 
@@ -209,14 +252,17 @@ attend_rows_kernel(const ChunkArgs A)
     }
     const int bs = min(b1, sp.nsb);              // the run's store batches: [b0, bs)
 
-    float y[MT][C / 8][4];
-    Running<MT> st;
+    float y[MT][R::NT][4];
+    Running<MT, H> st;
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
 #pragma unroll
-        for (int nt = 0; nt < C / 8; ++nt) y[m][nt][0] = y[m][nt][1] = y[m][nt][2] = y[m][nt][3] = 0.0f;
-        st.m[m][0] = st.m[m][1] = -INFINITY;
-        st.l[m][0] = st.l[m][1] = 0.0f;
+        for (int nt = 0; nt < R::NT; ++nt) y[m][nt][0] = y[m][nt][1] = y[m][nt][2] = y[m][nt][3] = 0.0f;
+#pragma unroll
+        for (int h = 0; h < H; ++h) {
+            st.m[m][h] = -INFINITY;
+            st.l[m][h] = 0.0f;
+        }
     }
     const uint8_t *kc0 = a.kc + (uint64_t)o * a.cap * G::kRowB, *vc0 = a.vc + (uint64_t)o * a.cap * G::kRowB;
     const uint8_t *kc = kc0 + tig * (G::kRowB / 4), *vc = vc0 + g * G::kVB;
@@ -338,11 +384,11 @@ attend_rows_kernel(const ChunkArgs A)
             }
             load_vm(b + 1);
         }
-        uint4 p[MT][2];
+        uint4 p[2][MT];
         const bool whole = t0 >= first && t1 - t0 == kBatch && t1 - 1 <= last_lo;
-        softmax_of<C, MT>(a, s, y, st, p, whole, t0, t1, first, last, tig);
-        if (vfast) values_of<BITS, C, MT, true>(y, p, vw, vm, vmg, a.voff, tig);
-        else values_of<BITS, C, MT, false>(y, p, vw, vm, vmg, a.voff, tig);
+        softmax_of<C, ROWS>(a, s, y, st, p, whole, t0, t1, first, last, tig);
+        if (vfast) values_of<BITS, C, ROWS, true>(y, p, vw, vm, vmg, a.voff, tig);
+        else values_of<BITS, C, ROWS, false>(y, p, vw, vm, vmg, a.voff, tig);
         if (b + 1 < bs) load_v(b + 1);
     }
 
@@ -360,9 +406,9 @@ attend_rows_kernel(const ChunkArgs A)
 #pragma unroll
             for (int j = 0; j < 4; ++j) s[m][j][0] = s[m][j][1] = s[m][j][2] = s[m][j][3] = 0.0f;
         scores_of_rows<BITS, C, MT>(s, krow, qf, lane);
-        uint4 p[MT][2];
+        uint4 p[2][MT];
         const bool whole = t0 >= first && t1 - t0 == kBatch && t1 - 1 <= last_lo;
-        softmax_of<C, MT>(a, s, y, st, p, whole, t0, t1, first, last, tig);
+        softmax_of<C, ROWS>(a, s, y, st, p, whole, t0, t1, first, last, tig);
         // this lane's C/8 channels of its tokens, paired by token
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks) {
@@ -379,22 +425,21 @@ attend_rows_kernel(const ChunkArgs A)
                 }
             }
 #pragma unroll
-            for (int nt = 0; nt < C / 8; ++nt) {
-                const uint32_t sel = (nt & 1) ? 0x7632 : 0x5410;
-                const uint32_t v0 = __byte_perm(r[0][nt / 2], r[1][nt / 2], sel);
-                const uint32_t v1 = __byte_perm(r[2][nt / 2], r[3][nt / 2], sel);
-#pragma unroll
-                for (int m = 0; m < MT; ++m) mma16816(y[m][nt], p[m][ks], v0, v1);
-            }
+            for (int nt = 0; nt < C / 8; nt += 2)
+                add_values<ROWS, C>(y, nt, p[ks], __byte_perm(r[0][nt / 2], r[1][nt / 2], 0x5410),
+                                    __byte_perm(r[2][nt / 2], r[3][nt / 2], 0x5410),
+                                    __byte_perm(r[0][nt / 2], r[1][nt / 2], 0x7632),
+                                    __byte_perm(r[2][nt / 2], r[3][nt / 2], 0x7632));
         }
     }
 
-    // ---- merge the warps, a row tile at a time; channel of (nt, column e of lane tig) = (2 tig + e) C/8 + nt
+    // ---- merge the warps, a row tile at a time; channel of (nt, column e of lane tig) = (2 tig + e) C/8 + nt,
+    // transposed: lane (g, tig) has channels g C/8 + i of rows 2 tig and 2 tig + 1
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
         if (m > 0) __syncthreads();
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < H; ++h) {
             float l = st.l[m][h];
             l = __fadd_rn(l, __shfl_xor_sync(0xFFFFFFFFu, l, 1));
             l = __fadd_rn(l, __shfl_xor_sync(0xFFFFFFFFu, l, 2));
@@ -402,16 +447,24 @@ attend_rows_kernel(const ChunkArgs A)
                 sm[warp][g + 8 * h] = st.m[m][h];
                 sl[warp][g + 8 * h] = l;
             }
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-#pragma unroll
-                for (int q4 = 0; q4 < C / 32; ++q4)
-                    *reinterpret_cast<float4*>(&sy[warp][g + 8 * h][(2 * tig + e) * (C / 8) + 4 * q4]) =
-                        make_float4(y[m][4 * q4][2 * h + e], y[m][4 * q4 + 1][2 * h + e], y[m][4 * q4 + 2][2 * h + e],
-                                    y[m][4 * q4 + 3][2 * h + e]);
         }
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int q4 = 0; q4 < C / 32; ++q4) {
+                if constexpr (ROWS == 8) {
+                    *reinterpret_cast<float4*>(&sy[warp][2 * tig + h][g * (C / 8) + 4 * q4]) =
+                        make_float4(y[0][2 * q4][h], y[0][2 * q4][2 + h], y[0][2 * q4 + 1][h], y[0][2 * q4 + 1][2 + h]);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        *reinterpret_cast<float4*>(&sy[warp][g + 8 * h][(2 * tig + e) * (C / 8) + 4 * q4]) =
+                            make_float4(y[m][4 * q4][2 * h + e], y[m][4 * q4 + 1][2 * h + e], y[m][4 * q4 + 2][2 * h + e],
+                                        y[m][4 * q4 + 3][2 * h + e]);
+                }
+            }
         __syncthreads();
-        for (int k = tid; k < 16 * (C / 4); k += kThreads) {
+        for (int k = tid; k < R::kOut * (C / 4); k += kThreads) {
             const int row = k / (C / 4), c4 = (k % (C / 4)) * 4, r = 16 * m + row;
             if (r >= a.rows) break;
             float M = -INFINITY;
@@ -446,7 +499,7 @@ attend_rows_kernel(const ChunkArgs A)
         }
         if (A.cluster) {                         // block rank = split; each takes its share of the rows' pieces
             cluster_sync();
-            for (int k = split * kThreads + tid; k < 16 * (C / 4); k += A.nsplit * kThreads) {
+            for (int k = split * kThreads + tid; k < R::kOut * (C / 4); k += A.nsplit * kThreads) {
                 const int row = k / (C / 4), c4 = (k % (C / 4)) * 4, r = 16 * m + row;
                 if (r >= a.rows) break;
                 float M = -INFINITY;
@@ -480,35 +533,38 @@ merge_rows_kernel(const ChunkArgs A, int64_t total)
     merge_row<C>(A, o, (int)(row - o * A.v.rows), A.part + row * A.nsplit * (C + 4), threadIdx.x & 31);
 }
 
-// Up to 16 rows take a tile of 16 (three CTAs a SM), up to 32 one of 32 (two); more
-// rows take the tensor-core forms of prefill.cu.  Splits of the visible batches: the number that gives the shortest run through
-// all waves, counting about three batches for a CTA's start and end.
-struct RowsPlan { int64_t mt, nsplit; bool cluster; };
+// Up to 8, 16 or 32 rows (four, three, two CTAs a SM); more rows take the
+// tensor-core forms of prefill.cu.  Splits of the visible batches: the number that
+// gives the shortest run through all waves, counting about three batches for a
+// CTA's start and end and three for a second launch.
+struct RowsPlan { int64_t nsplit; bool cluster; };
 
-constexpr int64_t kCluster = 8;                   // most splits that a cluster joins
+constexpr int64_t kCluster = 8;                  // most splits that a cluster joins
 constexpr int64_t kMaxWaves = 2;                 // more CTAs than this are not split further
 
-int64_t slots_of(int64_t mt) { return 152 * (mt == 1 ? 3 : 2); }
+int64_t slots_of(int64_t rows) { return 152 * (rows <= 8 ? 4 : rows <= 16 ? 3 : 2); }
+
+// Clusters must find their SMs together: on a full GPU (448 CTAs in clusters of 7)
+// they cost 73 us where two launches take 56; on 64 CTAs they save the second
+// launch (5 us).
+bool cluster_ok(int64_t outer, int64_t s, int64_t slots) { return s > 1 && s <= kCluster && 2 * outer * s <= slots; }
+
+// Up to 2048 tokens of few slices the splits stay within a cluster: no workspace.
+bool short_cache(int64_t outer, int64_t T, int64_t slots) { return T <= 2048 && cluster_ok(outer, kCluster, slots); }
 
 RowsPlan rows_plan(int64_t outer, int64_t T, int64_t rows)
 {
-    RowsPlan p;
-    p.mt = rows <= 16 ? 1 : 2;
-    const int64_t ctas = std::max<int64_t>(outer, 1), slots = slots_of(p.mt);
-    const int64_t nb = (T + kBatch - 1) / kBatch + 1;
+    const int64_t slots = slots_of(rows), nb = (T + kBatch - 1) / kBatch + 1;
+    const int64_t most = short_cache(outer, T, slots) ? kCluster : nb;
+    RowsPlan p = {1, false};
     int64_t best = INT64_MAX;
-    p.nsplit = 1;
-    p.cluster = false;
-    for (int64_t s = 1; s == 1 || (ctas * s <= kMaxWaves * slots && s * kWarps <= nb); ++s) {
-        // clusters must find their SMs together: on a full GPU (448 CTAs in clusters of 7) they
-        // cost 73 us where two launches take 56, on 64 CTAs they save the second launch (5 us)
-        const bool cluster = s > 1 && s <= kCluster && 2 * ctas * s <= slots;
-        const int64_t cost = ((ctas * s + slots - 1) / slots) * ((nb + s * kWarps - 1) / (s * kWarps) + 3) +
+    for (int64_t s = 1; s == 1 || (outer * s <= kMaxWaves * slots && s * kWarps <= nb && s <= most); ++s) {
+        const bool cluster = cluster_ok(outer, s, slots);
+        const int64_t cost = ((outer * s + slots - 1) / slots) * ((nb + s * kWarps - 1) / (s * kWarps) + 3) +
                              (s > 1 && !cluster ? 3 : 0);
         if (cost < best) {
             best = cost;
-            p.nsplit = s;
-            p.cluster = cluster;
+            p = {s, cluster};
         }
     }
     return p;
@@ -531,8 +587,9 @@ cudaError_t launch_rows(ChunkArgs A, int64_t outer, cudaStream_t st)
     cfg.stream = st;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
-    const cudaError_t e = p.mt == 1 ? cudaLaunchKernelEx(&cfg, attend_rows_kernel<BITS, C, 1>, A)
-                                    : cudaLaunchKernelEx(&cfg, attend_rows_kernel<BITS, C, 2>, A);
+    const cudaError_t e = A.v.rows <= 8 ? cudaLaunchKernelEx(&cfg, attend_rows_kernel<BITS, C, 8>, A)
+                          : A.v.rows <= 16 ? cudaLaunchKernelEx(&cfg, attend_rows_kernel<BITS, C, 16>, A)
+                                           : cudaLaunchKernelEx(&cfg, attend_rows_kernel<BITS, C, 32>, A);
     if (e != cudaSuccess) return e;
     if (p.nsplit > 1 && !p.cluster) {
         const int64_t total = outer * A.v.rows;
@@ -549,9 +606,9 @@ size_t chunk_workspace(int64_t outer, int64_t C, int64_t tmax, int64_t n, int64_
     if (outer == 0 || rows == 0) return 0;
     if (chunk_uses_tc(rows)) return chunk_tc_workspace(outer, C, tmax, rows);
     // every T up to tmax may choose its splits: at most kMaxWaves of CTAs, or one per four batches
-    const int64_t mt = rows <= 16 ? 1 : 2, most = (tmax + kBatch - 1) / kBatch + 1;
-    const int64_t split_rows = std::min(kMaxWaves * slots_of(mt) * 16 * mt, outer * rows * (most / kWarps));
-    return most / kWarps > 1 ? (size_t)(split_rows * (C + 4)) * sizeof(float) : 0;
+    const int64_t slots = slots_of(rows), most = (tmax + kBatch - 1) / kBatch + 1;
+    if (short_cache(outer, tmax, slots) || most / kWarps <= 1) return 0;
+    return (size_t)(std::min(kMaxWaves * slots, outer * (most / kWarps)) * rows * (C + 4)) * sizeof(float);
 }
 
 rows::View cache_view(const CacheArgs& x)
