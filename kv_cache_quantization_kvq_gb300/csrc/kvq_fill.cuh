@@ -185,5 +185,177 @@ struct Fill {
     }
 };
 
+// A run of consecutive tiles of one cache by two groups of 128 threads (four warps),
+// a half tile (64 tokens) each, their codes and the keys' constants staged in shared memory by another warp's bulk copies,
+// three halves deep.  With a warp or two per scheduler, what a half takes is the
+// latency of its chains: one group for both halves took 702 us where two take 584
+// (128 rows over 65536 tokens and 64 slices), and divisions stay out of it.
+template <int BITS, int C, bool KEYS>
+struct Staged {
+    static constexpr int P = C / 8, kStep = 128 / P, kN = 32 / kStep, kSub = 32 / P;   // as in Fill; rows of a warp's pass
+    static constexpr int kRowB = C * BITS / 8, kHalf = 64, kStages = 3, kAhead = 8;
+    static constexpr int kCodesB = kHalf * kRowB, kConstB = 2 * C * 2;                 // up to two key groups' scales
+    static constexpr int kStageB = kCodesB + 2 * (C == 128 ? kConstB : 2 * kConstB);   // V: 4 warps x 4 groups x 16 words
+    static constexpr int kBytes = kStages * kStageB;
+
+    const View& a;
+    const int64_t o;
+    const int first, me, sub, p, r0;             // sub: which half of every tile
+    unsigned char* stage;
+    uint64_t *rfull, *rfree;                     // [kStages]
+    const uint8_t* codes;                        // of the slice
+    const uint32_t mg, place;
+    const float bias;
+    int h0, h1;                                  // the half tiles that are staged: whole, in the store and seen
+    int rem;                                     // keys: tokens of the group before the next half
+    uint32_t vm[2];                              // values: (scale, zero point) of this lane's row and groups, next half
+
+    // tiles [j0, j0 + n)
+    __device__ __forceinline__ Staged(const View& v, int64_t slice, int hidden, int j0, int n, int tid, int part,
+                                      unsigned char* st, uint64_t* full, uint64_t* free)
+        : a(v), o(slice), first(hidden), me(tid), sub(part), p(tid % P), r0(tid / P), stage(st), rfull(full), rfree(free),
+          codes((KEYS ? v.kc : v.vc) + (uint64_t)slice * v.cap * kRowB), mg(magic<BITS>(KEYS ? v.kflip : v.vflip)),
+          place(tid % P / 8 * (kTile * 128) + tc::swizzled(tid / P, tid % P % 8)), bias(128.0f + (KEYS ? v.koff : v.voff)) {
+        h0 = max(2 * j0, (first + kHalf - 1) / kHalf);
+        h1 = max(h0, min(2 * (j0 + n), a.tq / kHalf));
+        rem = KEYS ? (int)((int64_t)mine() * kHalf % a.gk) : 0;
+    }
+
+    __device__ __forceinline__ int mine() const { return h0 + ((h0 ^ sub) & 1); }      // this group's first staged half
+    // stages half h (one lane); the stage's last readers are done
+    __device__ __forceinline__ void issue(int h) const {
+        const int s = (h - h0) % kStages;
+        unsigned char* dst = stage + s * kStageB;
+        uint32_t bytes = kCodesB;
+        const int64_t t = (int64_t)h * kHalf;
+        if constexpr (KEYS) {
+            const int g = (int)(t / a.gk), groups = (int)((t + kHalf - 1) / a.gk) - g + 1;
+            const uint32_t n = groups * C * 2;
+            bytes += a.kz ? 2 * n : n;
+            mbar_expect_tx(&rfull[s], bytes);
+            bulk_g2s(dst + kCodesB, a.ks + (o * a.ngk + g) * C, n, &rfull[s]);
+            if (a.kz) bulk_g2s(dst + kCodesB + kConstB, a.kz + (o * a.ngk + g) * C, n, &rfull[s]);
+        } else {
+            mbar_expect_tx(&rfull[s], bytes);
+        }
+        bulk_g2s(dst, codes + t * kRowB, kCodesB, &rfull[s]);
+    }
+    // values: the constants of half h, to registers: lane = row (l % 16) of the warp's 16, groups l / 16 and + 2
+    __device__ __forceinline__ void load_meta(int h) {
+        const int row = me & 15, lo = (me >> 4) & 1;
+        const int64_t t = (int64_t)h * kHalf + row / kSub * kStep + (me >> 5) * kSub + row % kSub;
+        const int64_t at = (o * a.cap + t) * a.ngv + lo;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            vm[k] = 0u;
+            if (lo + 2 * k < a.ngv) vm[k] = bits_of(a.vs + at + 2 * k) | (a.vz ? bits_of(a.vz + at + 2 * k) << 16 : 0u);
+        }
+    }
+
+    // half h of the tile; false: a wait gave up
+    template <class Ready>
+    __device__ __forceinline__ bool half(int h, unsigned char* tile, const Ready& ready) {
+        const int rb = (h & 1) * kHalf;
+        if (h < h0 || h >= h1) {
+            fill_rows<BITS, C, KEYS>(a, o, first, h >> 1, rb, rb + kHalf, tile, me);
+            return true;
+        }
+        const int k = h - h0, s = k % kStages;
+        unsigned char* st = stage + s * kStageB;
+        uint32_t* meta = reinterpret_cast<uint32_t*>(st + kCodesB) + (me >> 5) * 64;   // [4 groups][16 rows] of this warp
+        bool fast = true;
+        // the copy has landed, so the stage's last readers, the other group's among them, are done with it
+        if (!ready(&rfull[s], (k / kStages) & 1)) return false;
+        if constexpr (!KEYS) {
+            fast = __all_sync(0xFFFFFFFFu, zero_exact(bf_hi(vm[0])) && zero_exact(bf_hi(vm[1])));
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                meta[(((me >> 4) & 1) + 2 * i) * 16 + (me & 15)] = (vm[i] & 0xFFFFu) | (biased(vm[i], bias) & 0xFFFF0000u);
+            if (h + 2 < h1) load_meta(h + 2);
+            __syncwarp();
+        }
+        const int vg = KEYS ? 0 : p * 8 / a.gv * 16 + r0 % kSub;
+        uint32_t sk[4], zk[4];
+        bool okq[2] = {fast, fast};
+        int held = -1;                           // keys: the group in sk and zk, 0 or 1 of the stage's
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            unsigned char* dst = tile + place + (rb + 32 * q) * 128;
+            const unsigned char* src = st + (32 * q + r0) * kRowB + p * BITS;
+            if constexpr (KEYS) {
+                const int now = q && rem + 32 >= a.gk ? 1 : 0;
+                if (now != held) {
+                    const unsigned char* c = st + kCodesB + now * (C * 2) + p * 16;
+                    const uint4 s4 = interleave(*reinterpret_cast<const uint4*>(c));
+                    const uint4 z4 = a.kz ? interleave(*reinterpret_cast<const uint4*>(c + kConstB)) : make_uint4(0, 0, 0, 0);
+                    sk[0] = s4.x; sk[1] = s4.y; sk[2] = s4.z; sk[3] = s4.w;
+                    zk[0] = z4.x; zk[1] = z4.y; zk[2] = z4.z; zk[3] = z4.w;
+                    fast = true;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        fast = fast && zero_exact(bf_lo(zk[i])) && zero_exact(bf_hi(zk[i]));
+                        zk[i] = biased(zk[i], bias);
+                    }
+                    held = now;
+                }
+                okq[q] = fast;
+            }
+#pragma unroll
+            for (int i = 0; i < kN; ++i) {
+                uint32_t w;
+                if constexpr (BITS == 4) w = *reinterpret_cast<const uint32_t*>(src + i * kStep * kRowB);
+                else w = __byte_perm((uint32_t)*reinterpret_cast<const uint16_t*>(src + i * kStep * kRowB), 0u, 0x4140);
+                if constexpr (!KEYS) {
+                    const uint32_t x = meta[vg + (32 / kStep * q + i) * kSub];
+                    sk[0] = sk[1] = sk[2] = sk[3] = __byte_perm(x, 0u, 0x1010);
+                    zk[0] = zk[1] = zk[2] = zk[3] = __byte_perm(x, 0u, 0x3232);
+                }
+                *reinterpret_cast<uint4*>(dst + i * kStep * 128) = unpack_piece<BITS, true>(w, mg, sk, zk, 0.0f);
+            }
+        }
+        if (!okq[0] || !okq[1]) fill_rows<BITS, C, KEYS>(a, o, first, h >> 1, rb, rb + kHalf, tile, me);
+        if constexpr (KEYS) {
+            rem += 2 * kHalf;
+            while (rem >= a.gk) rem -= a.gk;
+        }
+        __syncwarp();
+        if ((me & 31) == 0) mbar_arrive(&rfree[s]);
+        return true;
+    }
+
+    // every tile, in order: `enter(j)` waits for tile buffer j's turn and returns it (nullptr: give up), `leave(j)` hands it on
+    template <class Ready, class Enter, class Leave>
+    __device__ __forceinline__ void run(int j0, int n, const Ready& ready, const Enter& enter, const Leave& leave) {
+        if (!KEYS && mine() < h1) load_meta(mine());
+        for (int j = 0; j < n; ++j) {
+            unsigned char* tile = enter(j);
+            if (!tile || !half(2 * (j0 + j) + sub, tile, ready)) break;
+            leave(j);
+        }
+    }
+    // the copies, by one warp: each stage again when its four readers are done; the codes come into L2 before that
+    template <class Ready>
+    __device__ __forceinline__ void produce(const Ready& ready) const {
+        int h = h0;
+        for (; h < h1; ++h) {
+            const int k = h - h0;
+            if (k >= kStages && !ready(&rfree[k % kStages], (k / kStages - 1) & 1)) break;
+            if (tc::elect()) {
+                if (h + kAhead < h1) bulk_prefetch_l2(codes + (int64_t)(h + kAhead) * kHalf * kRowB, kCodesB);
+                issue(h);
+            }
+            __syncwarp();
+            if constexpr (!KEYS) {               // and the values' constants: lines of 64 elements of scales, zero points
+                const int lane = me & 31, at = (lane >> 1) * 64;
+                const __nv_bfloat16* m = (lane & 1) ? a.vz : a.vs;
+                if (m && h + kAhead < h1 && at < kHalf * a.ngv)
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(m + (o * a.cap + (int64_t)(h + kAhead) * kHalf) * a.ngv + at));
+            }
+        }
+        // before the shared memory goes: every copy issued has landed
+        for (int k = max(0, h - h0 - kStages); k < h - h0; ++k) tc::drain(&rfull[k % kStages], (k / kStages) & 1);
+    }
+};
+
 }  // namespace fill
 }  // namespace kvq

@@ -34,7 +34,7 @@ namespace {
 
 using namespace rows;
 using fill::kTile;                               // 128 tokens of a key tile, 128 rows of a query tile
-using fill::Fill;
+using fill::Staged;
 using fill::interleave;
 
 constexpr int kSlots = 4;                        // ring slots of one K or V tile
@@ -420,40 +420,42 @@ attend_tc_kernel(const TcArgs X, const __grid_constant__ CUtensorMap kmap, const
 }
 
 // ---------------------------------------------------------------- fused form
-// The same without the expansion, for fewer query rows: eight fill warps turn
-// the packed codes into the swizzled bf16 tiles themselves (warps 12-15 the
-// keys, 16-19 the values), so the cache is read once, as codes.  Per 128-token
+// The same without the expansion, for fewer query rows: sixteen fill warps turn
+// the packed codes into the swizzled bf16 tiles themselves (warps 12-19 the
+// keys, 20-27 the values), so the cache is read once, as codes.  Per 128-token
 // tile that is 32768 values, four instructions a pair: about as long as the
 // products of 256 rows take, so more rows are better served by expanding once.
 // Within every 8 channels the tiles hold them in the order 0 4 1 5 2 6 3 7 in
 // which a code word gives them up; the query rows are staged, and the output is
-// written, accordingly.  With 640 threads a softmax thread has 96 registers and
+// written, accordingly.  With 896 threads a softmax thread has 72 registers and
 // reads its 128 scores twice, 32 at a time.
-constexpr int kFusedWarps = 20;
+constexpr int kFusedWarps = 28;
 constexpr int kFusedThreads = kFusedWarps * 32;
 
-template <int C>
+template <int BITS, int C>
 struct SmemF {
     static constexpr int kTileB = kTile * C * 2;
-    static constexpr int kQ = 0, kK = 2 * kTileB, kV = kK + 2 * kTileB, kBars = kV + 2 * kTileB;    // two K, two V tiles
-    static constexpr int kBytes = kBars + 256 + 1024;
+    static constexpr int kQ = 0, kK = 2 * kTileB, kV = kK + 2 * kTileB, kRawK = kV + 2 * kTileB;    // two K, two V tiles,
+    static constexpr int kRawV = kRawK + Staged<BITS, C, true>::kBytes;                 // and their staged codes
+    static constexpr int kBars = kRawV + Staged<BITS, C, false>::kBytes, kBytes = kBars + 256 + 1024;
 };
 
 template <int BITS, int C>
 __global__ void __launch_bounds__(kFusedThreads, 1)
 attend_fused_kernel(const __grid_constant__ TcArgs X)
 {
-    using S = SmemF<C>;
+    using S = SmemF<BITS, C>;
     extern __shared__ unsigned char raw[];
     unsigned char* sm = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
-    uint64_t* kfull = reinterpret_cast<uint64_t*>(sm + S::kBars);  // [2] a key tile is in shared memory (4 warps)
+    uint64_t* kfull = reinterpret_cast<uint64_t*>(sm + S::kBars);  // [2] a key tile is in shared memory (8 warps)
     uint64_t* kfree = kfull + 2;                 // [2] every row tile is done with it
     uint64_t* vfull = kfree + 2;
     uint64_t* vfree = vfull + 2;
     uint64_t* sfull = vfree + 2;                 // [2] per row tile, as in attend_tc_kernel
     uint64_t* pfull = sfull + 2;
     uint64_t* odone = pfull + 2;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(odone + 2);
+    uint64_t* raw_bars = odone + 2;              // [K full, K free, V full, V free][3]
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(raw_bars + 12);
     volatile int* gone = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
     const ChunkArgs& A = X.A;
@@ -467,14 +469,15 @@ attend_fused_kernel(const __grid_constant__ TcArgs X)
 
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&kfull[i], 4);
+            mbar_init(&kfull[i], 8);
             mbar_init(&kfree[i], nt);
-            mbar_init(&vfull[i], 4);
+            mbar_init(&vfull[i], 8);
             mbar_init(&vfree[i], nt);
             mbar_init(&sfull[i], 1);
             mbar_init(&pfull[i], 4);
             mbar_init(&odone[i], 1);
         }
+        for (int i = 0; i < 12; ++i) mbar_init(&raw_bars[i], i / 3 % 2 ? 4 : 1);
         *gone = 0;
         mbar_init_fence();
     }
@@ -494,22 +497,27 @@ attend_fused_kernel(const __grid_constant__ TcArgs X)
     const uint32_t tmem = *tmem_slot;
     auto ready = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xFFFFFFFFu, tc::wait(bar, parity, gone)) != 0; };
 
-    if (warp >= 12) {
-        // ---- fill
-        auto fill = [&](auto f, uint64_t* full, uint64_t* free, unsigned char* tiles) {
-            for (int j = 1; j < min(n, f.kAheadTiles); ++j) f.prefetch(j0 + j);
-            for (int j = 0; j < n; ++j) {
-                const int s = j & 1;
-                if (j >= 2 && !ready(&free[s], ((j >> 1) - 1) & 1)) break;
-                if (j + f.kAheadTiles < n) f.prefetch(j0 + j + f.kAheadTiles);
-                f.run(j0 + j, tiles + s * S::kTileB);
-                tc::async_fence();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&full[s]);
+    if (warp >= 10) {
+        // ---- fill: warps 12-19 the keys, 20-27 the values; warps 10 and 11 copy their codes
+        const int me = tid & 127, sub = ((warp - 12) >> 2) & 1;      // two groups of four warps each
+        const bool keys = warp < 12 ? warp == 10 : warp < 20;
+        auto role = [&](auto f, uint64_t* full, uint64_t* free, unsigned char* tiles) {
+            if (warp < 12) {
+                f.produce(ready);
+                return;
             }
+            f.run(j0, n, ready,
+                  [&](int j) -> unsigned char* {
+                      return j >= 2 && !ready(&free[j & 1], ((j >> 1) - 1) & 1) ? nullptr : tiles + (j & 1) * S::kTileB;
+                  },
+                  [&](int j) {
+                      tc::async_fence();
+                      __syncwarp();
+                      if (lane == 0) mbar_arrive(&full[j & 1]);
+                  });
         };
-        if (warp < 16) fill(Fill<BITS, C, true>(a, o, first, 4 * j0, 4 * (j0 + n), tid & 127), kfull, kfree, sm + S::kK);
-        else fill(Fill<BITS, C, false>(a, o, first, 4 * j0, 4 * (j0 + n), tid & 127), vfull, vfree, sm + S::kV);
+        if (keys) role(Staged<BITS, C, true>(a, o, first, j0, n, me, sub, sm + S::kRawK, raw_bars, raw_bars + 3), kfull, kfree, sm + S::kK);
+        else role(Staged<BITS, C, false>(a, o, first, j0, n, me, sub, sm + S::kRawV, raw_bars + 6, raw_bars + 9), vfull, vfree, sm + S::kV);
     } else if (warp >= 8) {
         // ---- products of row tile t (warps 8 and 9)
         const int t = warp - 8;
@@ -759,7 +767,7 @@ cudaError_t launch_tc(const ChunkArgs& A0, int64_t outer, void* ws, cudaStream_t
     if (!fused && (!encode_rows_tile_map(kx, p.slices * p.Tp, C, &km) || !encode_rows_tile_map(vx, p.slices * p.Tp, C, &vm)))
         return cudaErrorNotSupported;
     const cudaError_t e = fused
-        ? ensure_kernel_attrs(reinterpret_cast<const void*>(attend_fused_kernel<BITS, C>), SmemF<C>::kBytes)
+        ? ensure_kernel_attrs(reinterpret_cast<const void*>(attend_fused_kernel<BITS, C>), (SmemF<BITS, C>::kBytes))
         : ensure_kernel_attrs(reinterpret_cast<const void*>(attend_tc_kernel<C>), Smem<C>::kBytes);
     if (e != cudaSuccess) return e;
     for (int64_t o0 = 0; o0 < outer; o0 += p.slices) {
@@ -770,7 +778,7 @@ cudaError_t launch_tc(const ChunkArgs& A0, int64_t outer, void* ws, cudaStream_t
         X.A.nsplit = (int32_t)w.nsplit;
         const unsigned grid = (unsigned)(w.whole + w.tail * w.nsplit);
         if (fused) {
-            attend_fused_kernel<BITS, C><<<grid, kFusedThreads, SmemF<C>::kBytes, st>>>(X);
+            attend_fused_kernel<BITS, C><<<grid, kFusedThreads, (SmemF<BITS, C>::kBytes), st>>>(X);
         } else {
             const int64_t items = X.slices * (p.Tp / 8) * (C / 8);
             expand_kernel<BITS, C><<<dim3((unsigned)((items + 255) / 256), 2), 256, 0, st>>>(X.A.v, o0, X.slices, p.Tp, kx, vx);
