@@ -51,15 +51,25 @@ __device__ __noinline__ void fill_rows(const View& a, int64_t o, int first, int 
     const float off = KEYS ? a.koff : a.voff;
     const uint32_t mg = magic<BITS>(KEYS ? a.kflip : a.vflip);
     const uint8_t* codes = (KEYS ? a.kc : a.vc) + (uint64_t)o * a.cap * (C * BITS / 8) + p * BITS;
+    constexpr int kAhead = 4;                    // buffer rows in flight
 #pragma unroll 1
-    for (int r = rb + tid / P; r < re; r += kStep) {
-        const int t = j * kTile + r;
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (t >= first && t < a.T) {
+    for (int r = rb + tid / P; r < re; r += kAhead * kStep) {
+        uint4 x[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const int t = j * kTile + r + i * kStep;
+            x[i] = make_uint4(0, 0, 0, 0);
+            if (r + i * kStep < re && t >= max(first, a.tq) && t < a.T)
+                x[i] = *reinterpret_cast<const uint4*>((KEYS ? a.kr : a.vr) + ((uint64_t)o * a.rrows + (t - a.tq)) * C + p * 8);
+        }
+#pragma unroll 1
+        for (int i = 0; i < kAhead; ++i) {
+            const int row = r + i * kStep, t = j * kTile + row;
+            if (row >= re) break;
+            uint4 y = i == 0 ? x[0] : i == 1 ? x[1] : i == 2 ? x[2] : x[3];
             if (t >= a.tq) {
-                x = interleave(*reinterpret_cast<const uint4*>((KEYS ? a.kr : a.vr) +
-                                                               ((uint64_t)o * a.rrows + (t - a.tq)) * C + p * 8));
-            } else {
+                y = interleave(y);
+            } else if (t >= first) {
                 uint32_t s[4], z[4];
                 if constexpr (KEYS) {
                     const int64_t at = (o * a.ngk + t / a.gk) * C + p * 8;
@@ -72,10 +82,10 @@ __device__ __noinline__ void fill_rows(const View& a, int64_t o, int first, int 
                     s[0] = s[1] = s[2] = s[3] = bits_of(a.vs + at) * 0x10001u;
                     z[0] = z[1] = z[2] = z[3] = a.vz ? bits_of(a.vz + at) * 0x10001u : 0u;
                 }
-                x = unpack_piece<BITS, false>(load_piece<BITS>(codes + (int64_t)t * (C * BITS / 8)), mg, s, z, off);
+                y = unpack_piece<BITS, false>(load_piece<BITS>(codes + (int64_t)t * (C * BITS / 8)), mg, s, z, off);
             }
+            *reinterpret_cast<uint4*>(tile + p / 8 * (kTile * 128) + tc::swizzled(row, p % 8)) = y;
         }
-        *reinterpret_cast<uint4*>(tile + p / 8 * (kTile * 128) + tc::swizzled(r, p % 8)) = x;
     }
 }
 

@@ -705,8 +705,8 @@ merge_tiles_kernel(const TcArgs X, int64_t total)
 constexpr int64_t kExpandBytes = int64_t(1) << 30;                  // expanded K and V held at once
 
 // One query tile of up to 256 rows reads the codes itself; more rows share one
-// expansion (64 slices of 32768 tokens: 256 rows 413 us fused, 630 expanded; 512
-// rows 792 and 766).
+// expansion (64 slices of 32768 tokens: 256 rows 421 us fused, 630 expanded; 512
+// rows 815 and 766).
 bool fused_form(int64_t rows) { return rows <= 2 * kTile; }
 
 struct TcPlan { int64_t Tp, slices, ntiles; };
@@ -809,7 +809,7 @@ bool encode_rows_tile_map(const void* x, int64_t rows, int64_t C, CUtensorMap* m
 }
 
 // Rows from which the tensor-core forms are taken (64 slices of 32768 tokens: 32
-// rows 249 us on mma.sync and 349 here, 64 rows 506 and 351).
+// rows 249 us on mma.sync and 311 here, 64 rows 506 and 313).
 bool chunk_uses_tc(int64_t rows) { return rows > 32; }
 
 // Enough for every T up to tmax: a shorter cache may take more slices at once,

@@ -409,6 +409,8 @@ cudaError_t launch_wt(WtArgs A, int64_t outer, void* ws, cudaStream_t st)
 
 }  // namespace
 
+// Rows from which this form is taken (64 slices of 32768 tokens: 64 rows 205 us on
+// mma.sync and 268 here, where the time hardly moves up to 256 rows).
 bool weights_use_tc(int64_t rows) { return rows > 64; }
 
 size_t weights_tc_workspace(int64_t outer, int64_t C, int64_t rows)
