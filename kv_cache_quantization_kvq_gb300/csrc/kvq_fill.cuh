@@ -89,120 +89,17 @@ __device__ __noinline__ void fill_rows(const View& a, int64_t o, int first, int 
     }
 }
 
-// Tiles of 128 tokens of one cache, swizzled, by 128 threads: a thread takes
-// 8-channel piece p of every (1024 / C)-th token, a quarter tile (32 tokens of
-// one key group) at a time, with the next two quarters' words loading and the
-// codes coming into L2 a few tiles before.  The loops stay rolled: unrolled over a
-// tile they miss the instruction cache.
-template <int BITS, int C, bool KEYS>
-struct Fill {
-    static constexpr int P = C / 8, kStep = 128 / P, kN = 32 / kStep;      // rows a pass, passes of a quarter
-    static constexpr int kRowB = C * BITS / 8, kAheadTiles = 4;
-    const View& a;
-    const int64_t o;
-    const int first, me, end;                    // end: one past the last quarter wanted
-    const uint8_t* codes;
-    const __nv_bfloat16 *sc, *ze;                // of this thread's channels / V group, its first row
-    const uint32_t mg, place;
-    const float bias;
-    uint32_t w[2][kN];
-    uint4 ks[KEYS ? 2 : 1], kz[KEYS ? 2 : 1];    // keys: the quarter's scales and zero points
-    uint32_t vs[KEYS ? 1 : 2][kN], vz[KEYS ? 1 : 2][kN];            // values: of each token
-
-    __device__ __forceinline__ Fill(const View& v, int64_t slice, int hidden, int q0, int q1, int tid)
-        : a(v), o(slice), first(hidden), me(tid), end(q1),
-          codes((KEYS ? v.kc : v.vc) + ((uint64_t)slice * v.cap + tid / P) * kRowB + tid % P * BITS),
-          sc(KEYS ? v.ks + slice * v.ngk * C + tid % P * 8 : v.vs + (slice * v.cap + tid / P) * v.ngv + tid % P * 8 / v.gv),
-          ze(KEYS ? (v.kz ? v.kz + (sc - v.ks) : nullptr) : (v.vz ? v.vz + (sc - v.vs) : nullptr)),
-          mg(magic<BITS>(KEYS ? v.kflip : v.vflip)),
-          place(tid % P / 8 * (kTile * 128) + tc::swizzled(tid / P, tid % P % 8)),
-          bias(128.0f + (KEYS ? v.koff : v.voff)) {
-        if (whole(q0)) fetch(0, q0);
-        if (whole(q0 + 1)) fetch(1, q0 + 1);
-    }
-
-    __device__ __forceinline__ bool whole(int q) const { return q < end && q * 32 >= first && (q + 1) * 32 <= a.tq; }
-
-    __device__ __forceinline__ void fetch(int b, int q) {
-        const uint8_t* c = codes + (int64_t)q * (32 * kRowB);
-#pragma unroll
-        for (int i = 0; i < kN; ++i) w[b][i] = load_piece<BITS>(c + i * kStep * kRowB);
-        if constexpr (KEYS) {
-            const int64_t at = (int64_t)(q * 32 / a.gk) * C;
-            ks[b] = *reinterpret_cast<const uint4*>(sc + at);
-            kz[b] = ze ? *reinterpret_cast<const uint4*>(ze + at) : make_uint4(0, 0, 0, 0);
-        } else {
-            const int64_t at = (int64_t)q * 32 * a.ngv;
-#pragma unroll
-            for (int i = 0; i < kN; ++i) {
-                vs[b][i] = bits_of(sc + at + i * kStep * a.ngv);
-                vz[b][i] = ze ? bits_of(ze + at + i * kStep * a.ngv) : 0u;
-            }
-        }
-    }
-    // into L2: the codes, and the constants (lines of 128 bytes, one per thread)
-    __device__ __forceinline__ void prefetch(int j) const {
-        if (j * kTile < first || (j + 1) * kTile > a.tq) return;
-        const int64_t t = (int64_t)j * kTile;
-        if (me == 0) {
-            bulk_prefetch_l2(codes + t * kRowB, kTile * kRowB);     // thread 0's piece is the row's first
-        } else if (me >= 32 && me < 64) {
-            const __nv_bfloat16* m = (me & 1) ? (KEYS ? a.kz : a.vz) : (KEYS ? a.ks : a.vs);
-            const int64_t line = (me - 32) >> 1;
-            const int64_t from = KEYS ? (o * a.ngk + t / a.gk) * C : (o * a.cap + t) * a.ngv;
-            const int64_t to = KEYS ? (o * a.ngk + (t + kTile - 1) / a.gk + 1) * C : from + kTile * a.ngv;
-            if (m && from + line * 64 < to) asm volatile("prefetch.global.L2 [%0];" ::"l"(m + from + line * 64));
-        }
-    }
-
-    __device__ __forceinline__ void quarter(int b, int q, unsigned char* tile) {
-        bool fast = whole(q);
-        if (fast) {
-            unsigned char* dst = tile + place + (q & 3) * (32 * 128);
-            if constexpr (KEYS) {
-                const uint4 s4 = interleave(ks[b]), z4 = interleave(kz[b]);
-                const uint32_t s[4] = {s4.x, s4.y, s4.z, s4.w};
-                uint32_t z[4] = {z4.x, z4.y, z4.z, z4.w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    fast = fast && zero_exact(bf_lo(z[i])) && zero_exact(bf_hi(z[i]));
-                    z[i] = biased(z[i], bias);
-                }
-#pragma unroll
-                for (int i = 0; i < kN; ++i)
-                    *reinterpret_cast<uint4*>(dst + i * kStep * 128) = unpack_piece<BITS, true>(w[b][i], mg, s, z, 0.0f);
-            } else {
-#pragma unroll
-                for (int i = 0; i < kN; ++i) {
-                    const uint32_t s1 = vs[b][i] * 0x10001u;
-                    const float z0 = __uint_as_float(vz[b][i] << 16), zb = __fadd_rn(z0, bias);
-                    const uint32_t z1 = pack_bf16x2(zb, zb);
-                    fast = fast && zero_exact(z0);
-                    const uint32_t s[4] = {s1, s1, s1, s1}, z[4] = {z1, z1, z1, z1};
-                    *reinterpret_cast<uint4*>(dst + i * kStep * 128) = unpack_piece<BITS, true>(w[b][i], mg, s, z, 0.0f);
-                }
-            }
-        }
-        if (!fast) fill_rows<BITS, C, KEYS>(a, o, first, q >> 2, (q & 3) * 32, (q & 3) * 32 + 32, tile, me);
-        if (whole(q + 2)) fetch(b, q + 2);
-    }
-    __device__ __forceinline__ void run(int j, unsigned char* tile) {
-#pragma unroll 1
-        for (int h = 0; h < 2; ++h) {
-            quarter(0, 4 * j + 2 * h, tile);
-            quarter(1, 4 * j + 2 * h + 1, tile);
-        }
-    }
-};
-
 // A run of consecutive tiles of one cache by two groups of 128 threads (four warps),
-// a half tile (64 tokens) each, their codes and the keys' constants staged in shared memory by another warp's bulk copies,
-// three halves deep.  With a warp or two per scheduler, what a half takes is the
-// latency of its chains: one group for both halves took 702 us where two take 584
-// (128 rows over 65536 tokens and 64 slices), and divisions stay out of it.
+// a half tile (64 tokens) each, their codes and the keys' constants staged in
+// shared memory by another warp's bulk copies, three halves deep.  A thread takes
+// 8-channel piece p of every (1024 / C)-th token.  With a warp or two per scheduler,
+// what a half takes is the latency of its chains: one group for both halves took
+// 702 us where two take 584 (128 rows over 65536 tokens and 64 slices), and
+// divisions stay out of it.  Loops over a whole tile stay rolled: unrolled, with
+// four quarters' words in registers, they missed the instruction cache (893 us).
 template <int BITS, int C, bool KEYS>
 struct Staged {
-    static constexpr int P = C / 8, kStep = 128 / P, kN = 32 / kStep, kSub = 32 / P;   // as in Fill; rows of a warp's pass
+    static constexpr int P = C / 8, kStep = 128 / P, kN = 32 / kStep, kSub = 32 / P;   // rows a pass, passes of 32 tokens, rows of a warp's pass
     static constexpr int kRowB = C * BITS / 8, kHalf = 64, kStages = 3, kAhead = 8;
     static constexpr int kCodesB = kHalf * kRowB, kConstB = 2 * C * 2;                 // up to two key groups' scales
     static constexpr int kStageB = kCodesB + 2 * (C == 128 ? kConstB : 2 * kConstB);   // V: 4 warps x 4 groups x 16 words
@@ -216,25 +113,27 @@ struct Staged {
     const uint8_t* codes;                        // of the slice
     const uint32_t mg, place;
     const float bias;
+    const int k0;                                // halves staged before this run, in the same stages
     int h0, h1;                                  // the half tiles that are staged: whole, in the store and seen
     int rem;                                     // keys: tokens of the group before the next half
     uint32_t vm[2];                              // values: (scale, zero point) of this lane's row and groups, next half
 
     // tiles [j0, j0 + n)
     __device__ __forceinline__ Staged(const View& v, int64_t slice, int hidden, int j0, int n, int tid, int part,
-                                      unsigned char* st, uint64_t* full, uint64_t* free)
+                                      unsigned char* st, uint64_t* full, uint64_t* free, int before = 0)
         : a(v), o(slice), first(hidden), me(tid), sub(part), p(tid % P), r0(tid / P), stage(st), rfull(full), rfree(free),
           codes((KEYS ? v.kc : v.vc) + (uint64_t)slice * v.cap * kRowB), mg(magic<BITS>(KEYS ? v.kflip : v.vflip)),
-          place(tid % P / 8 * (kTile * 128) + tc::swizzled(tid / P, tid % P % 8)), bias(128.0f + (KEYS ? v.koff : v.voff)) {
+          place(tid % P / 8 * (kTile * 128) + tc::swizzled(tid / P, tid % P % 8)), bias(128.0f + (KEYS ? v.koff : v.voff)), k0(before) {
         h0 = max(2 * j0, (first + kHalf - 1) / kHalf);
         h1 = max(h0, min(2 * (j0 + n), a.tq / kHalf));
         rem = KEYS ? (int)((int64_t)mine() * kHalf % a.gk) : 0;
     }
 
+    __device__ __forceinline__ int staged() const { return h1 - h0; }
     __device__ __forceinline__ int mine() const { return h0 + ((h0 ^ sub) & 1); }      // this group's first staged half
     // stages half h (one lane); the stage's last readers are done
     __device__ __forceinline__ void issue(int h) const {
-        const int s = (h - h0) % kStages;
+        const int s = (k0 + h - h0) % kStages;
         unsigned char* dst = stage + s * kStageB;
         uint32_t bytes = kCodesB;
         const int64_t t = (int64_t)h * kHalf;
@@ -270,7 +169,7 @@ struct Staged {
             fill_rows<BITS, C, KEYS>(a, o, first, h >> 1, rb, rb + kHalf, tile, me);
             return true;
         }
-        const int k = h - h0, s = k % kStages;
+        const int k = k0 + h - h0, s = k % kStages;
         unsigned char* st = stage + s * kStageB;
         uint32_t* meta = reinterpret_cast<uint32_t*>(st + kCodesB) + (me >> 5) * 64;   // [4 groups][16 rows] of this warp
         bool fast = true;
@@ -335,20 +234,21 @@ struct Staged {
 
     // every tile, in order: `enter(j)` waits for tile buffer j's turn and returns it (nullptr: give up), `leave(j)` hands it on
     template <class Ready, class Enter, class Leave>
-    __device__ __forceinline__ void run(int j0, int n, const Ready& ready, const Enter& enter, const Leave& leave) {
+    __device__ __forceinline__ bool run(int j0, int n, const Ready& ready, const Enter& enter, const Leave& leave) {
         if (!KEYS && mine() < h1) load_meta(mine());
         for (int j = 0; j < n; ++j) {
             unsigned char* tile = enter(j);
-            if (!tile || !half(2 * (j0 + j) + sub, tile, ready)) break;
+            if (!tile || !half(2 * (j0 + j) + sub, tile, ready)) return false;
             leave(j);
         }
+        return true;
     }
     // the copies, by one warp: each stage again when its four readers are done; the codes come into L2 before that
     template <class Ready>
-    __device__ __forceinline__ void produce(const Ready& ready) const {
+    __device__ __forceinline__ bool produce(const Ready& ready) const {
         int h = h0;
         for (; h < h1; ++h) {
-            const int k = h - h0;
+            const int k = k0 + h - h0;
             if (k >= kStages && !ready(&rfree[k % kStages], (k / kStages - 1) & 1)) break;
             if (tc::elect()) {
                 if (h + kAhead < h1) bulk_prefetch_l2(codes + (int64_t)(h + kAhead) * kHalf * kRowB, kCodesB);
@@ -363,7 +263,8 @@ struct Staged {
             }
         }
         // before the shared memory goes: every copy issued has landed
-        for (int k = max(0, h - h0 - kStages); k < h - h0; ++k) tc::drain(&rfull[k % kStages], (k / kStages) & 1);
+        for (int k = k0 + max(0, h - h0 - kStages); k < k0 + h - h0; ++k) tc::drain(&rfull[k % kStages], (k / kStages) & 1);
+        return h == h1;
     }
 };
 

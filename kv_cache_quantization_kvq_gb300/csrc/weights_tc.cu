@@ -10,7 +10,7 @@
 //     nothing, so that 2^(x - inf) = 0) and the last token a row sees;
 //  2. weights_tc_kernel, one CTA a SM, walks jobs of 256 tokens (and a split of
 //     the rows): eight fill warps unpack the next job's keys into two swizzled
-//     M = 128 tiles while the current ones are in use; one warp loads tiles of 128
+//     M = 128 tiles (kvq_fill.cuh) while the current ones are in use; one warp loads tiles of 128
 //     query rows by TMA into a ring, two issue the products of a key tile each
 //     into two tensor-memory buffers, four groups of four warps, one per buffer,
 //     turn them into sums of 2^(x - lse), a token per thread;
@@ -31,11 +31,11 @@ namespace {
 
 using namespace rows;
 
-using fill::Fill;
 using fill::interleave;
 using fill::kTile;
+using fill::Staged;
 constexpr int kSumWarps = 16;                    // four per scheduler: one warp's exponentials cover another's loads
-constexpr int kFillWarp = kSumWarps + 4;         // 16: copies, 17 and 18: products, 20-27: fill
+constexpr int kFillWarp = kSumWarps + 4;         // 16: query tiles, 17 and 18: products, 19: codes, 20-27: fill
 constexpr int kThreadsW = (kFillWarp + 8) * 32;
 
 struct WtArgs {
@@ -80,13 +80,14 @@ pack_rows_kernel(const View a, const float* lse, int64_t R, int C, int64_t total
     }
 }
 
-template <int C>
+template <int BITS, int C>
 struct SmemW {
     static constexpr int kTileB = kTile * C * 2;
     static constexpr int kSlots = 2, kRowSlots = 4;                 // rings of query tiles and of their rows' data
     static constexpr int kK = 0, kRing = 4 * kTileB;                // two jobs' two key tiles
     static constexpr int kRows = kRing + kSlots * kTileB, kHalf = kRows + kRowSlots * kTile * 8;
-    static constexpr int kBars = kHalf + 2 * 2 * kTile * 4, kBytes = kBars + 256 + 1024;
+    static constexpr int kRaw = kHalf + 2 * 2 * kTile * 4, kBars = kRaw + Staged<BITS, C, true>::kBytes;
+    static constexpr int kBytes = kBars + 512 + 1024;
 };
 
 // A job: 256 tokens from t0 of slice o, row tiles [n0, n0 + n).
@@ -115,7 +116,7 @@ template <int BITS, int C>
 __global__ void __launch_bounds__(kThreadsW, 1)
 weights_tc_kernel(const __grid_constant__ WtArgs A, const __grid_constant__ CUtensorMap qmap)
 {
-    using S = SmemW<C>;
+    using S = SmemW<BITS, C>;
     constexpr int kSlots = S::kSlots, kHalves = C / 64;
     extern __shared__ unsigned char raw[];
     unsigned char* sm = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
@@ -125,13 +126,14 @@ weights_tc_kernel(const __grid_constant__ WtArgs A, const __grid_constant__ CUte
     uint64_t* empty = full + kSlots;             // [slot] both products are done with it
     uint64_t* rfull = empty + kSlots;            // [row slot] the same for -lse and last tokens (2 x 4 warps read them)
     uint64_t* rempty = rfull + S::kRowSlots;
-    uint64_t* kfull = rempty + S::kRowSlots;            // [job parity] both key tiles are filled (8 warps)
-    uint64_t* kfree = kfull + 2;                 // [job parity] both products are done with them
+    uint64_t* kfull = rempty + S::kRowSlots;     // [job parity][2] a key tile is filled (8 warps)
+    uint64_t* kfree = kfull + 4;                 // [job parity] both products are done with them
     uint64_t* dfull = kfree + 2;                 // [2 tiles][2 buffers]
     uint64_t* dfree = dfull + 4;
     uint64_t* hfull = dfree + 4;                 // [2 tiles][job parity] the odd groups' sums are there
     uint64_t* hfree = hfull + 4;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(hfree + 4);
+    uint64_t* raw_bars = hfree + 4;              // [full, free][3] of the staged codes
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(raw_bars + 6);
     volatile int* gone = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
     const View& a = A.v;
@@ -147,11 +149,10 @@ weights_tc_kernel(const __grid_constant__ WtArgs A, const __grid_constant__ CUte
             mbar_init(&rfull[i], 1);
             mbar_init(&rempty[i], 8);
         }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&kfull[i], 8);
-            mbar_init(&kfree[i], 2);
-        }
+        for (int i = 0; i < 2; ++i) mbar_init(&kfree[i], 2);
+        for (int i = 0; i < 6; ++i) mbar_init(&raw_bars[i], i < 3 ? 1 : 4);
         for (int i = 0; i < 4; ++i) {
+            mbar_init(&kfull[i], 8);
             mbar_init(&dfull[i], 1);
             mbar_init(&dfree[i], 4);
             mbar_init(&hfull[i], 4);
@@ -168,22 +169,39 @@ weights_tc_kernel(const __grid_constant__ WtArgs A, const __grid_constant__ CUte
     auto ready = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xFFFFFFFFu, tc::wait(bar, parity, gone)) != 0; };
     // every role walks the jobs alike; `it` counts row tiles and `k` jobs with any, over the whole CTA
 
-    if (warp >= kFillWarp) {
-        // ---- keys: four warps a tile
-        const int t = (warp - kFillWarp) >> 2, me = tid & 127;
-        int k = 0;
-        for (int64_t job = job0; job < job1; ++job) {
+    if (warp >= kFillWarp - 1) {
+        // ---- keys, and (warp 19) the copies of their codes: runs of jobs that go on in the same slice
+        int k = 0, staged = 0;
+        bool ok = true;
+        for (int64_t job = job0; ok && job < job1;) {
             const Job J(A, job);
+            int64_t end = job + 1;
+            for (; end < job1; ++end) {
+                const Job E(A, end);
+                if (E.o != J.o || E.split != J.split || (E.n > 0) != (J.n > 0)) break;
+            }
+            const int j0 = J.t0 / kTile, tiles = 2 * (int)(end - job);
+            job = end;
             if (J.n == 0) continue;
-            if (k >= 2 && !ready(&kfree[k & 1], ((k >> 1) - 1) & 1)) break;
-            const int j = J.t0 / kTile + t;
-            Fill<BITS, C, true> f(a, J.o, J.first, 4 * j, 4 * j + 4, me);
-            if (job + 1 < job1) f.prefetch(j + 2);                  // the next job's tile, if the slice goes on
-            f.run(j, sm + S::kK + (2 * (k & 1) + t) * S::kTileB);
-            tc::async_fence();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&kfull[k & 1]);
-            ++k;
+            Staged<BITS, C, true> f(a, J.o, J.first, j0, tiles, tid & 127, (warp - kFillWarp) >> 2 & 1, sm + S::kRaw, raw_bars,
+                                    raw_bars + 3, staged);
+            staged += f.staged();
+            if (warp < kFillWarp) {
+                ok = f.produce(ready);
+                continue;
+            }
+            ok = f.run(j0, tiles, ready,
+                       [&](int j) -> unsigned char* {
+                           const int c = k + (j >> 1);              // the job's number among those with any row
+                           if (!(j & 1) && c >= 2 && !ready(&kfree[c & 1], ((c >> 1) - 1) & 1)) return nullptr;
+                           return sm + S::kK + (2 * (c & 1) + (j & 1)) * S::kTileB;
+                       },
+                       [&](int j) {
+                           tc::async_fence();
+                           __syncwarp();
+                           if (lane == 0) mbar_arrive(&kfull[2 * ((k + (j >> 1)) & 1) + (j & 1)]);
+                       });
+            k += tiles >> 1;
         }
     } else if (warp == kSumWarps) {
         // ---- query tiles
@@ -221,7 +239,7 @@ weights_tc_kernel(const __grid_constant__ WtArgs A, const __grid_constant__ CUte
             const Job J(A, job);
             if (J.n == 0) continue;
             const uint32_t k_at = smem_u32(sm + S::kK) + (2 * (k & 1) + t) * S::kTileB;
-            ok = ready(&kfull[k & 1], (k >> 1) & 1);
+            ok = ready(&kfull[2 * (k & 1) + t], (k >> 1) & 1);
             for (int i = 0; ok && i < J.n; ++i, ++it) {
                 const int s = it % kSlots, b = it & 1;
                 ok = ready(&full[s], (it / kSlots) & 1) && (it < 2 || ready(&dfree[2 * t + b], ((it >> 1) - 1) & 1));
@@ -396,10 +414,10 @@ cudaError_t launch_wt(WtArgs A, int64_t outer, void* ws, cudaStream_t st)
     if (outer * p.R > 0x7FFFFFFF || packs / 256 >= 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
     CUtensorMap qm;
     if (!encode_rows_tile_map(qx, outer * p.R, C, &qm)) return cudaErrorNotSupported;
-    cudaError_t e = ensure_kernel_attrs(reinterpret_cast<const void*>(weights_tc_kernel<BITS, C>), SmemW<C>::kBytes);
+    cudaError_t e = ensure_kernel_attrs(reinterpret_cast<const void*>(weights_tc_kernel<BITS, C>), (SmemW<BITS, C>::kBytes));
     if (e != cudaSuccess) return e;
     pack_rows_kernel<<<(unsigned)((packs + 255) / 256), 256, 0, st>>>(A.v, A.lse, p.R, C, packs, qx, rows2);
-    weights_tc_kernel<BITS, C><<<(unsigned)std::min<int64_t>(A.jobs, 152), kThreadsW, SmemW<C>::kBytes, st>>>(A, qm);
+    weights_tc_kernel<BITS, C><<<(unsigned)std::min<int64_t>(A.jobs, 152), kThreadsW, (SmemW<BITS, C>::kBytes), st>>>(A, qm);
     if (p.nsplit > 1) {
         const int64_t total = outer * A.v.T;
         join_kernel<<<(unsigned)((total + 255) / 256), 256, 0, st>>>(A, total);
