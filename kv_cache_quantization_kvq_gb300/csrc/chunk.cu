@@ -24,6 +24,10 @@
 // writes out and lse; up to eight splits are a thread-block cluster that joins
 // its partial (m, l, y) through distributed shared memory (one launch); more go
 // through the workspace and merge_rows_kernel.  Both join in split order.
+//
+// Measured on one GB300, 4-bit codes: 64 slices x 8 heads over 8192 tokens 37 us
+// (79 MB: 2.1 TB/s), 8 x 4 over 131263 tokens 75 us; bound by the issue of the
+// unpacking (half of the slots busy), not by bytes.
 #include <algorithm>
 
 #include "kvq_chunk.cuh"

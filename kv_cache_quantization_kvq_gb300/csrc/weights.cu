@@ -11,6 +11,9 @@
 // into B fragments of mma.sync.m16n8k16 (kvq_rows.cuh) and sums the weights of
 // its columns over the rows.  Each token belongs to one warp, so no sum needs an
 // atomic and its order is fixed.  Up to 64 rows; more take weights_tc.cu.
+//
+// Measured on one GB300: 64 slices x 8 heads over 8192 tokens 26 us (42 MB: 1.6
+// TB/s), bound like chunk.cu by the issue of the unpacking.
 #include <algorithm>
 
 #include "kvq_chunk.cuh"

@@ -185,19 +185,27 @@ def test_attend_weights(b, name):
     assert np.all(np.abs(bare - w.sum((1, 2))) <= tol)
 
 
-def test_a_captured_call_replays_on_new_data(b):
+# one case for each form: few rows in a cluster and through the workspace, up to 256 rows, more
+FORMS = ["ordinary step", "long, split", "many rows, split", "chunk"]
+
+
+@pytest.mark.parametrize("name", FORMS)
+def test_a_captured_call_replays_on_new_data(b, name):
     """attend_chunk and attend_weights in one graph: replay sees new queries."""
     import torch
-    hc, q, first = build("ordinary step")
-    cache = hc.device(b, 2)
+    hc, q, first = build(name)
+    B, H, G, n = CASES[name][:4]
+    cache = hc.device(b, H, first)
     dq = upload_bf16(q)
     out, lse = b.attend_chunk(dq, cache)
-    ws = torch.empty(max(b.kvq_attend_chunk_workspace(cache.shape, cache.resid_rows, 1, 8), 1), dtype=torch.uint8, device="cuda")
-    sc = torch.zeros((4, hc.T), device="cuda")
+    wa, ww = (torch.empty(max(f(cache.shape, cache.resid_rows, n, G), 1), dtype=torch.uint8, device="cuda")
+              for f in (b.kvq_attend_chunk_workspace, b.kvq_attend_weights_workspace))
+    sc = torch.zeros((B * H, hc.T), device="cuda")
+    b.attend_weights(dq, lse, cache, sc, sc, ww)
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
-        b.attend_chunk(dq, cache, out, lse, ws)
-        b.attend_weights(dq, lse, cache, sc, sc)
+        b.attend_chunk(dq, cache, out, lse, wa)
+        b.attend_weights(dq, lse, cache, sc, sc, ww)
     dq.copy_(torch.randn_like(dq.float()).bfloat16())
     sc.zero_()
     graph.replay()
@@ -209,19 +217,21 @@ def test_a_captured_call_replays_on_new_data(b):
     assert torch.equal(sc, one + one)
 
 
-def test_other_streams(b):
-    """Two calls on two streams with their own workspaces and outputs."""
+@pytest.mark.parametrize("name", FORMS)
+def test_other_streams(b, name):
+    """Calls that may overlap on two streams, each with its own workspace and outputs."""
     import torch
-    hc, q, first = build("long, split")
-    cache = hc.device(b, 2)
+    hc, q, first = build(name)
+    cache = hc.device(b, CASES[name][1], first)
     dq = upload_bf16(q)
     want, wl = b.attend_chunk(dq, cache)
+    ww = b.attend_weights(dq, wl, cache)
     torch.cuda.synchronize()
     st = [torch.cuda.Stream(), torch.cuda.Stream()]
-    got = [b.attend_chunk(dq, cache, stream=s) for s in st for _ in range(4)]
+    got = [(b.attend_chunk(dq, cache, stream=s), b.attend_weights(dq, wl, cache, stream=s)) for _ in range(4) for s in st]
     torch.cuda.synchronize()
-    for o, l in got:
-        assert torch.equal(o.view(torch.int16), want.view(torch.int16)) and torch.equal(l, wl)
+    for (o, l), w in got:
+        assert torch.equal(o.view(torch.int16), want.view(torch.int16)) and torch.equal(l, wl) and torch.equal(w, ww)
 
 
 def test_from_quantized_agrees_with_dequantize(b):
