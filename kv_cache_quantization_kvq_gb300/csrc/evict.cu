@@ -33,6 +33,7 @@ namespace {
 
 constexpr int kSelThreads = 1024;
 constexpr int kSumAhead = 4;                     // blocks whose scores a warp has in flight
+constexpr int kSharedKeys = 2048;                // block keys held in shared memory; more go through the workspace
 constexpr int kMoveThreads = 256;
 constexpr int kAhead = 8;                        // loads in flight per thread
 
@@ -84,6 +85,7 @@ __device__ __forceinline__ int cta_scan(int v, int* warp_sums, int* sum) {
 __global__ void __launch_bounds__(kSelThreads)
 select_blocks_kernel(const EvictArgs A)
 {
+    __shared__ unsigned long long near[kSharedKeys];
     __shared__ int hist[256];
     __shared__ int warp_sums[kSelThreads / 32];
     __shared__ int s_digit, s_need, s_done;
@@ -94,7 +96,7 @@ select_blocks_kernel(const EvictArgs A)
     const int recent = (int)min(A.window, A.nb);
     const int cand = nb - recent;                // candidates [0, cand)
     int need = kept - recent;                    // to be taken of them (kept >= recent)
-    unsigned long long* key = reinterpret_cast<unsigned long long*>(A.ws) + o * A.nb;
+    unsigned long long* key = nb <= kSharedKeys ? near : reinterpret_cast<unsigned long long*>(A.ws) + o * A.nb;
     int32_t* keep = A.keep + o * kept;
 
     unsigned long long prefix = 0;
@@ -279,7 +281,7 @@ move_blocks_kernel(const EvictArgs A, const MovePlan P, int64_t total)
 
 }  // namespace
 
-size_t evict_workspace(int64_t outer, int64_t nb_max) { return (size_t)(outer * nb_max) * 8; }
+size_t evict_workspace(int64_t outer, int64_t nb_max) { return nb_max > kSharedKeys ? (size_t)(outer * nb_max) * 8 : 0; }
 
 cudaError_t launch_evict(const EvictArgs& a, cudaStream_t st)
 {

@@ -50,7 +50,7 @@ struct WtArgs {
     const float* row;                            // [outer][R / 128][2][128]: -lse in base 2; last token seen (int bits)
     float* part;                                 // [outer][split][Tp]
     int32_t nsplit, ntok;                        // row splits, 256-token jobs of a slice
-    int64_t jobs;                                // slices x splits x ntok
+    int64_t jobs, outer;                         // slices x splits x ntok; slices
 };
 
 __global__ void __launch_bounds__(256)
@@ -93,25 +93,45 @@ struct SmemW {
     static constexpr int kBytes = kBars + 512 + 1024;
 };
 
-// A job: 256 tokens from t0 of slice o, row tiles [n0, n0 + n).
+// A job: 256 tokens from t0 of slice o, row tiles [n0, n0 + n).  Each role walks
+// its CTA's jobs by next(): worked out from the job's number every time, the
+// divisions took longer than a row tile.
 struct Job {
     int64_t o;
-    int t0, n0, n, split, first;
+    int tb, t0, n0, n, split, first;
     __device__ __forceinline__ Job(const WtArgs& A, int64_t job) {
-        const View& a = A.v;
-        const int tb = (int)(job % A.ntok);
+        tb = (int)(job % A.ntok);
         job /= A.ntok;
         split = (int)(job % A.nsplit);
         o = job / A.nsplit;
+        slice(A);
+        rows(A);
+    }
+    __device__ __forceinline__ void next(const WtArgs& A) {
+        if (++tb == A.ntok) {
+            tb = 0;
+            if (++split == A.nsplit) {
+                split = 0;
+                if (++o < A.outer) slice(A);
+            }
+        }
+        rows(A);
+    }
+    __device__ __forceinline__ void slice(const WtArgs& A) { first = A.v.first ? max(A.v.first[o], 0) : 0; }
+    __device__ __forceinline__ void rows(const WtArgs& A) {
+        const View& a = A.v;
         t0 = tb * 2 * kTile;
-        first = a.first ? max(a.first[o], 0) : 0;
         // the row tiles that see any of these tokens: from the first query that does
         const int see = max(t0, first), i0 = max(0, see - (a.T - a.n));
         int lo = (int)((int64_t)i0 * a.group / kTile), hi = (a.rows + kTile - 1) / kTile;
         if (see >= min(t0 + 2 * kTile, a.T) || i0 >= a.n) hi = lo;
-        const int64_t len = max(hi - lo, 0);
-        n0 = lo + (int)(len * split / A.nsplit);
-        n = lo + (int)(len * (split + 1) / A.nsplit) - n0;
+        const int len = max(hi - lo, 0);
+        n0 = lo;
+        n = len;
+        if (A.nsplit > 1) {
+            n0 = lo + (int)((int64_t)len * split / A.nsplit);
+            n = lo + (int)((int64_t)len * (split + 1) / A.nsplit) - n0;
+        }
     }
 };
 
@@ -176,17 +196,19 @@ weights_tc_kernel(const __grid_constant__ WtArgs A, const __grid_constant__ CUte
         // ---- keys, and (warp 19) the copies of their codes: runs of jobs that go on in the same slice
         int k = 0, staged = 0;
         bool ok = true;
+        Job J(A, job0);
         for (int64_t job = job0; ok && job < job1;) {
-            const Job J(A, job);
-            int64_t end = job + 1;
-            for (; end < job1; ++end) {
-                const Job E(A, end);
-                if (E.o != J.o || E.split != J.split || (E.n > 0) != (J.n > 0)) break;
-            }
-            const int j0 = J.t0 / kTile, tiles = 2 * (int)(end - job);
-            job = end;
-            if (J.n == 0) continue;
-            Staged<BITS, C, true> f(a, J.o, J.first, j0, tiles, tid & 127, (warp - kFillWarp) >> 2 & 1, sm + S::kRaw, raw_bars,
+            const int64_t o = J.o;
+            const int split = J.split, first = J.first, j0 = J.t0 / kTile;
+            const bool any = J.n > 0;
+            int tiles = 0;
+            do {
+                ++job;
+                tiles += 2;
+                J.next(A);
+            } while (job < job1 && J.o == o && J.split == split && (J.n > 0) == any);
+            if (!any) continue;
+            Staged<BITS, C, true> f(a, o, first, j0, tiles, tid & 127, (warp - kFillWarp) >> 2 & 1, sm + S::kRaw, raw_bars,
                                     raw_bars + 3, staged);
             staged += f.staged();
             if (warp < kFillWarp) {
@@ -210,8 +232,8 @@ weights_tc_kernel(const __grid_constant__ WtArgs A, const __grid_constant__ CUte
         // ---- query tiles
         int it = 0;
         bool ok = true;
-        for (int64_t job = job0; ok && job < job1; ++job) {
-            const Job J(A, job);
+        Job J(A, job0);
+        for (int64_t job = job0; ok && job < job1; ++job, J.next(A)) {
             for (int i = 0; i < J.n; ++i, ++it) {
                 const int s = it % kSlots, rs = it % S::kRowSlots;
                 if (it >= kSlots) ok = ready(&empty[s], ((it / kSlots) - 1) & 1);
@@ -238,8 +260,8 @@ weights_tc_kernel(const __grid_constant__ WtArgs A, const __grid_constant__ CUte
         const uint32_t ring = smem_u32(sm + S::kRing);
         int it = 0, k = 0;
         bool ok = true;
-        for (int64_t job = job0; ok && job < job1; ++job) {
-            const Job J(A, job);
+        Job J(A, job0);
+        for (int64_t job = job0; ok && job < job1; ++job, J.next(A)) {
             if (J.n == 0) continue;
             const uint32_t k_at = smem_u32(sm + S::kK) + (2 * (k & 1) + t) * S::kTileB;
             ok = ready(&kfull[2 * (k & 1) + t], (k >> 1) & 1);
@@ -271,8 +293,8 @@ weights_tc_kernel(const __grid_constant__ WtArgs A, const __grid_constant__ CUte
         const int base = a.T - a.n;
         int it = 0, k = 0;
         bool ok = true;
-        for (int64_t job = job0; ok && job < job1; ++job) {
-            const Job J(A, job);
+        Job J(A, job0);
+        for (int64_t job = job0; ok && job < job1; ++job, J.next(A)) {
             const int tok = J.t0 + t * kTile + me, tile_hi = J.t0 + t * kTile + kTile - 1;
             float sum = 0.0f;
             for (int i = 0; i < J.n; ++i, ++it) {
@@ -414,6 +436,7 @@ cudaError_t launch_wt(WtArgs A, int64_t outer, void* ws, cudaStream_t st)
     A.ntok = (int32_t)p.ntok;
     const int64_t packs = outer * p.R * (C / 8);
     A.jobs = outer * p.ntok * p.nsplit;
+    A.outer = outer;
     if (outer * p.R > 0x7FFFFFFF || packs / 256 >= 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
     CUtensorMap qm;
     if (!encode_rows_tile_map(qx, outer * p.R, C, &qm)) return cudaErrorNotSupported;

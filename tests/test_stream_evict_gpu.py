@@ -65,6 +65,7 @@ CASES = [
     ("kivi", (2, 64, 128 * 6, 128 * 6, 33, 40, 128, 2, 2, None)),         # the newest only
     ("kivi", (1, 128, 0, 128, 5, 64, 64, 4, 1, None)),                    # no block at all
     ("kivi", (1, 128, 64 * 1300, 64 * 1300, 5, 64, 64, 700, 10, None)),   # more blocks than threads
+    ("kivi", (2, 64, 64 * 2300, 64 * 2304, 5, 64, 64, 1200, 10, [0, 7000])),   # more than are held in shared memory
     ("two bits", (3, 128, 32 * 21, 32 * 21 + 7, 50, 64, 32, 5, 1, None)),
     ("two bits", (2, 64, 96 * 5, 96 * 5, 3, 64, 96, 3, 1, [10, 200])),
     ("eight bits, per token, int8 zeros", (2, 48, 7 * 11, 80, 9, 16, 7, 4, 1, [9, 0])),

@@ -109,10 +109,13 @@ def test_evict_blocks_refusals(kb):
                dict(sin=None), dict(sout=None), dict(sin=FAKE + 2), dict(sout=FAKE + 4), dict(stride=137), dict(keep=None),
                dict(keep=FAKE + 2), dict(k=kq(kb, group=0)), dict(v=kq(kb, group=48)), dict(shape=(-1, 128, 128))):
         refused(kb, kb.EINVAL, evict, **kw)
-    refused(kb, kb.EWORKSPACE, evict, ws=None)
-    refused(kb, kb.EWORKSPACE, evict, ws_B=63)
-    refused(kb, kb.EINVAL, evict, ws=FAKE + 8)
-    assert kb.kvq_evict_blocks_workspace((4, 128, 128), 64) <= 64
+    big = dict(shape=(4, 1 << 18, 128), src=cache(kb, tq=1 << 18, nres=0), dst=cache(kb, tq=1 << 18, nres=0), stride=1 << 18,
+               sin=FAKE << 4, sout=FAKE << 4)
+    want = kb.kvq_evict_blocks_workspace((4, 1 << 18, 128), 64)
+    assert want > 0 and kb.kvq_evict_blocks_workspace((4, 128, 128), 64) == 0
+    refused(kb, kb.EWORKSPACE, evict, ws=None, **big)
+    refused(kb, kb.EWORKSPACE, evict, ws_B=want - 1, **big)
+    refused(kb, kb.EINVAL, evict, ws=FAKE + 8, **big)
 
 
 def test_a_refused_call_leaves_the_counters(kb):
