@@ -18,7 +18,7 @@
 // Measured on one GB300: 2048 queries x 4 heads over 16384 tokens and 8 slices 240
 // us (1.07 PFLOP/s; tensor cores half busy, issue slots 61 %: a value costs one
 // exponential and two packed operations).  63 queries x 4 heads over 32774 tokens
-// and 16 slices 96 us, bound by the fill; a CTA per job, its keys filled before its
+// and 16 slices 86 us, bound by the fill; a CTA per job, its keys filled before its
 // products, took 146.
 #include <algorithm>
 
