@@ -239,7 +239,7 @@ attend_rows_kernel(const ChunkArgs A)
 #pragma unroll
         for (int h = 0; h < H; ++h) last[m][h] = base + (16 * m + g + 8 * h) / a.group;
     const int last_hi = a.T - 1, last_lo = base;                   // of the last and of the first row
-    const int first = a.first ? max(a.first[o], 0) : 0;
+    const int first = padding(a, o);
 
     // ---- the visible batches, cut into splits, and a run of the split for each warp
     const Span sp = span_of(a);

@@ -225,6 +225,9 @@ __device__ __forceinline__ void scores_of_rows(float (&s)[MT][4][4], const __nv_
     }
 }
 
+// the first token of slice o that is not padding, 0 .. T
+__device__ __forceinline__ int padding(const View& a, int64_t o) { return a.first ? min(max(a.first[o], 0), a.T) : 0; }
+
 // Which batches of a slice exist: those of the store come first, then the buffer's.
 struct Span { int nsb, nb; };                    // store batches, all batches
 __device__ __forceinline__ Span span_of(const View& a) {

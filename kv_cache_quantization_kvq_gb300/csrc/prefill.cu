@@ -148,7 +148,7 @@ struct TileOf {
     // the key tiles [j0, j0 + n) it sees; returns the first token that is not padding
     __device__ __forceinline__ int keys(const TcArgs& X, int& j0, int& n) const {
         const View& a = X.A.v;
-        const int first = a.first ? max(a.first[o], 0) : 0;
+        const int first = padding(a, o);
         const int last_hi = a.T - a.n + (r0 + nrows - 1) / a.group;
         int j1 = 0;
         j0 = 0;

@@ -52,7 +52,7 @@ weights_rows_kernel(const WeightArgs A)
     const int64_t o = blockIdx.x / (uint32_t)A.nrun;
     const int run = (int)(blockIdx.x - (uint32_t)o * (uint32_t)A.nrun);
     const Span sp = span_of(a);
-    const int first = a.first ? max(a.first[o], 0) : 0;
+    const int first = padding(a, o);
     const int base = a.T - a.n;                  // token of query 0
 
     for (int t = 0; t < A.ntiles; ++t) stage_queries<BITS, C, 1>(a, o, 16 * t, qf + t * G::kSteps * 32, tid, kThreads);

@@ -117,7 +117,7 @@ struct Job {
         }
         rows(A);
     }
-    __device__ __forceinline__ void slice(const WtArgs& A) { first = A.v.first ? max(A.v.first[o], 0) : 0; }
+    __device__ __forceinline__ void slice(const WtArgs& A) { first = padding(A.v, o); }
     __device__ __forceinline__ void rows(const WtArgs& A) {
         const View& a = A.v;
         t0 = tb * 2 * kTile;

@@ -51,6 +51,9 @@ CASES = {
     "far zero points, symmetric": (1, 1, 2, 2, 64, 128, 256, 40, 64, dict(kind="sym"), dict(shift=50.0)),
     "padding": (4, 2, 4, 40, 128, 256, 320, 50, 64, {}, dict(first=[0, 0, -5, 1, 100, 290, 306, 999])),
     "padding, step": (5, 1, 8, 1, 128, 256, 320, 50, 64, {}, dict(first=[0, 31, 32, 305, 400])),
+    "padding, extreme": (3, 1, 4, 2, 128, 256, 256, 50, 64, {}, dict(first=[2**31 - 1, -2**31, 306])),
+    "padding, extreme, many rows": (3, 1, 8, 40, 64, 256, 256, 50, 64, dict(gv=32), dict(first=[2**31 - 1, -2**31, 305])),
+    "padding, extreme, prompt": (3, 1, 8, 50, 128, 256, 256, 50, 64, {}, dict(first=[2**31 - 1, -2**31, 200])),
     "prompt from nothing": (1, 2, 2, 300, 64, 256, 256, 44, 64, {}, {}),
     "prompt, odd group": (1, 1, 3, 517, 128, 448, 448, 69, 128, {}, {}),
     "chunk": (1, 2, 4, 130, 128, 2048, 2112, 100, 192, {}, {}),
