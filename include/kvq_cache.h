@@ -68,7 +68,8 @@ typedef struct {
  * with q = q[b][i][h*group+j][:] and k_t, v_t the bf16 rows that
  * kvq_dequantize returns, s * (code - zero_point) rounded once to bf16, and
  * the buffer's rows as they are.  A query that sees nothing (T = 0, n > T, or
- * padding) gets out = 0 and lse = -inf.  n = 0 does nothing.
+ * padding), or only logits of -inf, gets out = 0 and lse = -inf; one that sees
+ * a logit of NaN or +inf gets NaN in all of out and in lse.  n = 0 does nothing.
  *  - q: bf16 [outer/kv_heads][n][kv_heads*group][C]; out: bf16, same shape;
  *    lse: float32 [outer/kv_heads][n][kv_heads*group], or NULL.
  *  - Logits, softmax statistics and sums are float32; the probabilities enter

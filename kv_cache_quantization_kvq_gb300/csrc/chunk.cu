@@ -130,12 +130,12 @@ __device__ __forceinline__ float4 remote_f4(const void* p, int rank) {
 template <int C>
 __device__ __forceinline__ void write_row(const ChunkArgs& A, int64_t o, int r, int c4, float M, float L, const float (&v)[4]) {
     const int64_t at = row_index(A.v, o, r);
-    const float inv = L > 0.0f ? __fdiv_rn(1.0f, L) : 0.0f;
+    const float inv = row_scale(L);
     *reinterpret_cast<uint2*>(A.out + at * C + c4) =
-        make_uint2(pack_bf16x2(__fmul_rn(v[0], inv), __fmul_rn(v[1], inv)),
-                   pack_bf16x2(__fmul_rn(v[2], inv), __fmul_rn(v[3], inv)));
+        make_uint2(pack_bf16x2(row_value(v[0], inv), row_value(v[1], inv)),
+                   pack_bf16x2(row_value(v[2], inv), row_value(v[3], inv)));
     if (A.lse && c4 == 0)
-        A.lse[at] = L > 0.0f ? __fmul_rn(__fadd_rn(M, log2f(L)), 0.6931471805599453f) : -INFINITY;
+        A.lse[at] = row_lse(M, L);
 }
 
 // Softmax state of a lane's rows (g, and g + 8 of each tile unless there are at most 8).
@@ -268,16 +268,14 @@ attend_rows_kernel(const ChunkArgs A)
             st.l[m][h] = 0.0f;
         }
     }
-    const uint8_t *kc0 = a.kc + (uint64_t)o * a.cap * G::kRowB, *vc0 = a.vc + (uint64_t)o * a.cap * G::kRowB;
-    const uint8_t *kc = kc0 + tig * (G::kRowB / 4), *vc = vc0 + g * G::kVB;
-    const int64_t vmeta = o * a.cap * a.ngv;
+    const int64_t row0 = o * a.cap;              // the slice's first row: one register pair, not a pointer for each buffer
     const uint32_t kmg = magic<BITS>(a.kflip), vmg = magic<BITS>(a.vflip);
     const uint32_t* vm = &vms[warp][g * (C / 8) / a.gv][0];         // this lane's V group (its C/8 channels lie in one)
 
     // a batch's codes: whole batches at fixed offsets, the store's last one clamped to its tokens
     uint32_t kw[4][G::kWpl], vw[8][G::kVW];
     auto load_k = [&](int b) {
-        const uint8_t* p = kc + (int64_t)b * (kBatch * G::kRowB);
+        const uint8_t* p = a.kc + ((row0 + (int64_t)b * kBatch) * G::kRowB + tig * (G::kRowB / 4));
         const int cnt = a.tq - b * kBatch - 1;
         if (cnt >= kBatch - 1) {
             p += g * G::kRowB;
@@ -289,7 +287,7 @@ attend_rows_kernel(const ChunkArgs A)
         }
     };
     auto load_v = [&](int b) {
-        const uint8_t* p = vc + (int64_t)b * (kBatch * G::kRowB);
+        const uint8_t* p = a.vc + ((row0 + (int64_t)b * kBatch) * G::kRowB + g * G::kVB);
         const int cnt = a.tq - b * kBatch - 1;
         auto one = [&](int k, const uint8_t* at) {
             if constexpr (G::kVB >= 4) load_words<G::kVW>(at, vw[k]);
@@ -310,8 +308,8 @@ attend_rows_kernel(const ChunkArgs A)
     auto load_vm = [&](int b) {
         const int t = b * kBatch + lane;
         const bool live = t >= first && t < a.tq;
-        const __nv_bfloat16* ps = a.vs + vmeta + (int64_t)t * a.ngv;
-        const __nv_bfloat16* pz = a.vz + vmeta + (int64_t)t * a.ngv;
+        const __nv_bfloat16* ps = a.vs + (row0 + t) * a.ngv;
+        const __nv_bfloat16* pz = a.vz + (row0 + t) * a.ngv;
         auto one = [&](int k) {
             vr[k] = 0u;
             if (live) vr[k] = bits_of(ps + k) | (a.vz ? bits_of(pz + k) << 16 : 0u);
@@ -371,12 +369,12 @@ attend_rows_kernel(const ChunkArgs A)
             const int ba = b + kAhead;           // into L2 a few batches ahead: codes, V constants, K group constants
             if (lane < 8 && ba < bs && (ba + 1) * kBatch <= a.tq) {
                 if (lane < 2) {
-                    bulk_prefetch_l2((lane ? vc0 : kc0) + (int64_t)ba * (kBatch * G::kRowB), kBatch * G::kRowB);
+                    bulk_prefetch_l2((lane ? a.vc : a.kc) + (row0 + (int64_t)ba * kBatch) * G::kRowB, kBatch * G::kRowB);
                 } else {
                     const bool key = lane >= 4;
                     const __nv_bfloat16* at = (lane & 1) ? (key ? a.kz : a.vz) : (key ? a.ks : a.vs);
                     const int64_t off = key ? (o * a.ngk + ba * kBatch / a.gk) * C + ((lane & 2) ? C / 2 : 0)
-                                            : vmeta + (int64_t)ba * kBatch * a.ngv;
+                                            : (row0 + (int64_t)ba * kBatch) * a.ngv;
                     if (at) asm volatile("prefetch.global.L2 [%0];" ::"l"(at + off));
                 }
             }
@@ -475,17 +473,15 @@ attend_rows_kernel(const ChunkArgs A)
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm[w][row]);
             float L = 0.0f, v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            if (M != -INFINITY) {
 #pragma unroll
-                for (int w = 0; w < kWarps; ++w) {
-                    const float f = ex2(__fsub_rn(sm[w][row], M));
-                    L = __fmaf_rn(sl[w][row], f, L);
-                    const float4 x = *reinterpret_cast<const float4*>(&sy[w][row][c4]);
-                    v[0] = __fmaf_rn(x.x, f, v[0]);
-                    v[1] = __fmaf_rn(x.y, f, v[1]);
-                    v[2] = __fmaf_rn(x.z, f, v[2]);
-                    v[3] = __fmaf_rn(x.w, f, v[3]);
-                }
+            for (int w = 0; w < kWarps; ++w) {
+                const float f = part_scale(sm[w][row], M);
+                L = __fmaf_rn(sl[w][row], f, L);
+                const float4 x = *reinterpret_cast<const float4*>(&sy[w][row][c4]);
+                v[0] = __fmaf_rn(x.x, f, v[0]);
+                v[1] = __fmaf_rn(x.y, f, v[1]);
+                v[2] = __fmaf_rn(x.z, f, v[2]);
+                v[3] = __fmaf_rn(x.w, f, v[3]);
             }
             if (A.cluster) {
                 *reinterpret_cast<float4*>(&sy[0][row][c4]) = make_float4(v[0], v[1], v[2], v[3]);   // read by this thread only
@@ -509,16 +505,14 @@ attend_rows_kernel(const ChunkArgs A)
                 float M = -INFINITY;
                 for (int s = 0; s < A.nsplit; ++s) M = fmaxf(M, remote_f(&gm[row], s));
                 float L = 0.0f, v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                if (M != -INFINITY) {
-                    for (int s = 0; s < A.nsplit; ++s) {
-                        const float f = ex2(__fsub_rn(remote_f(&gm[row], s), M));
-                        const float4 x = remote_f4(&sy[0][row][c4], s);
-                        L = __fmaf_rn(remote_f(&gl[row], s), f, L);
-                        v[0] = __fmaf_rn(x.x, f, v[0]);
-                        v[1] = __fmaf_rn(x.y, f, v[1]);
-                        v[2] = __fmaf_rn(x.z, f, v[2]);
-                        v[3] = __fmaf_rn(x.w, f, v[3]);
-                    }
+                for (int s = 0; s < A.nsplit; ++s) {
+                    const float f = part_scale(remote_f(&gm[row], s), M);
+                    const float4 x = remote_f4(&sy[0][row][c4], s);
+                    L = __fmaf_rn(remote_f(&gl[row], s), f, L);
+                    v[0] = __fmaf_rn(x.x, f, v[0]);
+                    v[1] = __fmaf_rn(x.y, f, v[1]);
+                    v[2] = __fmaf_rn(x.z, f, v[2]);
+                    v[3] = __fmaf_rn(x.w, f, v[3]);
                 }
                 write_row<C>(A, o, r, c4, M, L, v);
             }

@@ -30,34 +30,53 @@ __device__ __forceinline__ void merge_row(const ChunkArgs& A, int64_t o, int r, 
     float L = 0.0f, v[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] = 0.0f;
-    if (M != -INFINITY) {
-#pragma unroll 4
-        for (int s = 0; s < A.nsplit; ++s) {
-            const float* ps = p + (int64_t)s * (C + 4);
-            const float2 ml = *reinterpret_cast<const float2*>(ps + C);
-            const float f = ex2(__fsub_rn(ml.x, M));
-            L = __fmaf_rn(ml.y, f, L);
-            float x[N];
-            if constexpr (N == 4) {
-                const float4 t = *reinterpret_cast<const float4*>(ps + 4 * lane);
-                x[0] = t.x; x[1] = t.y; x[2] = t.z; x[3] = t.w;
-            } else {
-                const float2 t = *reinterpret_cast<const float2*>(ps + 2 * lane);
-                x[0] = t.x; x[1] = t.y;
+    // What each split counts is worked out a split per lane, and the outputs are loaded kJoin splits at a time: as a
+    // plain loop over the splits the loads wait for one another (one token of 8 slices x 4 heads over 131263 tokens:
+    // 73.3 us with it, 66.6 so).
+    constexpr int kJoin = 8;
+    for (int s0 = 0; s0 < A.nsplit; s0 += 32) {
+        const int n = min(32, A.nsplit - s0);
+        const float* ps = p + (int64_t)s0 * (C + 4);
+        float l = 0.0f, f = 0.0f;
+        if (lane < n) {
+            const float2 ml = *reinterpret_cast<const float2*>(ps + (int64_t)lane * (C + 4) + C);
+            l = ml.y;
+            f = part_scale(ml.x, M);
+        }
+        for (int i0 = 0; i0 < n; i0 += kJoin) {
+            float x[kJoin][N];
+#pragma unroll
+            for (int i = 0; i < kJoin; ++i) {
+#pragma unroll
+                for (int k = 0; k < N; ++k) x[i][k] = 0.0f;
+                if (i0 + i >= n) continue;
+                const float* py = ps + (int64_t)(i0 + i) * (C + 4) + N * lane;
+                if constexpr (N == 4) {
+                    const float4 t = *reinterpret_cast<const float4*>(py);
+                    x[i][0] = t.x; x[i][1] = t.y; x[i][2] = t.z; x[i][3] = t.w;
+                } else {
+                    const float2 t = *reinterpret_cast<const float2*>(py);
+                    x[i][0] = t.x; x[i][1] = t.y;
+                }
             }
 #pragma unroll
-            for (int i = 0; i < N; ++i) v[i] = __fmaf_rn(x[i], f, v[i]);
+            for (int i = 0; i < kJoin; ++i) {    // splits past the last: all zeros
+                const float fi = __shfl_sync(0xFFFFFFFFu, f, i0 + i);
+                L = __fmaf_rn(__shfl_sync(0xFFFFFFFFu, l, i0 + i), fi, L);
+#pragma unroll
+                for (int k = 0; k < N; ++k) v[k] = __fmaf_rn(x[i][k], fi, v[k]);
+            }
         }
     }
     const int64_t at = row_index(A.v, o, r);
-    const float inv = L > 0.0f ? __fdiv_rn(1.0f, L) : 0.0f;
+    const float inv = row_scale(L);
     uint32_t w[N / 2];
 #pragma unroll
-    for (int i = 0; i < N / 2; ++i) w[i] = pack_bf16x2(__fmul_rn(v[2 * i], inv), __fmul_rn(v[2 * i + 1], inv));
+    for (int i = 0; i < N / 2; ++i) w[i] = pack_bf16x2(row_value(v[2 * i], inv), row_value(v[2 * i + 1], inv));
     if constexpr (N == 4) *reinterpret_cast<uint2*>(A.out + at * C + 4 * lane) = make_uint2(w[0], w[1]);
     else *reinterpret_cast<uint32_t*>(A.out + at * C + 2 * lane) = w[0];
     if (A.lse && lane == 0)
-        A.lse[at] = L > 0.0f ? __fmul_rn(__fadd_rn(M, log2f(L)), 0.6931471805599453f) : -INFINITY;
+        A.lse[at] = row_lse(M, L);
 }
 
 bool chunk_uses_tc(int64_t rows);

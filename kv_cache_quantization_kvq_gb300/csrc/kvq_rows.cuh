@@ -64,6 +64,18 @@ __device__ __forceinline__ float ex2(float x) {  // 2^x, 2 ulp, 0 for -inf
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// ---- the end of a softmax row: maximum m (base 2) and sum l of its weights.
+// A NaN among the row's logits never moves m (fmaxf passes over it) and +inf
+// makes 2^(inf - inf), so it is l that carries them: NaN, and so are out and lse.
+// l = 0 is a row that saw nothing, or logits of -inf only: out 0, lse -inf.
+__device__ __forceinline__ float row_scale(float l) { return l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l); }
+__device__ __forceinline__ float row_value(float y, float scale) { return scale == 0.0f ? 0.0f : __fmul_rn(y, scale); }
+__device__ __forceinline__ float row_lse(float m, float l) {
+    return l == 0.0f ? -INFINITY : __fmul_rn(__fadd_rn(m, log2f(l)), 0.6931471805599453f);
+}
+// what a part's sums count in the whole: 2^(part's maximum - the whole's), 1 where both are -inf (or +inf),
+// so that a part's NaN stays
+__device__ __forceinline__ float part_scale(float m, float M) { return m == M ? 1.0f : ex2(__fsub_rn(m, M)); }
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 

@@ -383,7 +383,7 @@ attend_tc_kernel(const TcArgs X, const __grid_constant__ CUtensorMap kmap, const
         const bool write = ok && r < a.rows;
         const int64_t at = write ? row_index(a, o, r) : 0;
         float* part = w.part(X, r, C);
-        const float inv = l > 0.0f ? __fdiv_rn(1.0f, l) : 0.0f;
+        const float inv = row_scale(l);
 #pragma unroll
         for (int c = 0; c < C / 32; ++c) {
             uint32_t y[32];
@@ -404,8 +404,8 @@ attend_tc_kernel(const TcArgs X, const __grid_constant__ CUtensorMap kmap, const
                     uint32_t w[4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        w[k] = pack_bf16x2(__fmul_rn(__uint_as_float(y[8 * i + 2 * k]), inv),
-                                           __fmul_rn(__uint_as_float(y[8 * i + 2 * k + 1]), inv));
+                        w[k] = pack_bf16x2(row_value(__uint_as_float(y[8 * i + 2 * k]), inv),
+                                           row_value(__uint_as_float(y[8 * i + 2 * k + 1]), inv));
                     *reinterpret_cast<uint4*>(A.out + at * C + 32 * c + 8 * i) = make_uint4(w[0], w[1], w[2], w[3]);
                 }
             }
@@ -413,7 +413,7 @@ attend_tc_kernel(const TcArgs X, const __grid_constant__ CUtensorMap kmap, const
         }
         if (write && nsplit > 1) *reinterpret_cast<float2*>(part + C) = make_float2(m, l);
         if (write && nsplit == 1 && A.lse)
-            A.lse[at] = l > 0.0f ? __fmul_rn(__fadd_rn(m, log2f(l)), 0.6931471805599453f) : -INFINITY;
+            A.lse[at] = row_lse(m, l);
     }
     }
     __syncwarp();
@@ -650,7 +650,7 @@ attend_fused_kernel(const __grid_constant__ TcArgs X)
         const bool write = ok && r < a.rows;
         const int64_t at = write ? row_index(a, o, r) : 0;
         float* part = w.part(X, r, C);
-        const float inv = l > 0.0f ? __fdiv_rn(1.0f, l) : 0.0f;
+        const float inv = row_scale(l);
 #pragma unroll
         for (int c = 0; c < C / 32; ++c) {
             uint32_t y[32];
@@ -672,8 +672,8 @@ attend_fused_kernel(const __grid_constant__ TcArgs X)
                         float v[8];
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
-                            v[k] = __fmul_rn(__uint_as_float(z[2 * k]), inv);
-                            v[4 + k] = __fmul_rn(__uint_as_float(z[2 * k + 1]), inv);
+                            v[k] = row_value(__uint_as_float(z[2 * k]), inv);
+                            v[4 + k] = row_value(__uint_as_float(z[2 * k + 1]), inv);
                         }
                         store8(A.out + at * C + 32 * c + 8 * i, v);
                     }
@@ -683,7 +683,7 @@ attend_fused_kernel(const __grid_constant__ TcArgs X)
         }
         if (write && w.nsplit > 1) *reinterpret_cast<float2*>(part + C) = make_float2(m, l);
         if (write && w.nsplit == 1 && A.lse)
-            A.lse[at] = l > 0.0f ? __fmul_rn(__fadd_rn(m, log2f(l)), 0.6931471805599453f) : -INFINITY;
+            A.lse[at] = row_lse(m, l);
     }
     __syncwarp();
     tc::before_sync();

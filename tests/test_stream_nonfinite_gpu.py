@@ -1,0 +1,172 @@
+"""kvq_attend_chunk where tokens hold NaN or infinities.
+
+The definition sums over the tokens a query sees, so:
+  * a logit that is NaN or +inf, seen, makes the row's out and lse NaN; a logit
+    of -inf is a weight of 0.
+Whether a number is finite, and which infinity it is, is compared exactly; the
+finite ones with the tolerances of test_stream_attend_gpu.py (u = 2^-8, the
+largest relative error of a rounding to bf16; e twice the logits' error):
+  lse: e + (T + 64) 2^-23 + 4 2^-23 (|lse| + 1)
+  out: (u + e + (T + 64) 2^-23) sum_t p_t |v_t| + u |out|
+"""
+import zlib
+
+import numpy as np
+import pytest
+
+import oracle as O
+import stream_util as S
+from gpu_util import kb
+
+pytestmark = pytest.mark.gpu
+NAN, INF = np.uint16(0x7FC0), np.uint16(0x7F80)
+NEG = np.uint16(0xFF80)
+
+
+@pytest.fixture(scope="module")
+def b():
+    import torch
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    return kb()
+
+
+# one case for each way through the kernels: batch, kv_heads, group, n, C, tq, cap, nres, rows, formats, first
+FORMS = {
+    "one token, one split": (2, 70, 4, 1, 128, 64, 64, 9, 16, {}, None),
+    "one token, cluster": (1, 2, 4, 1, 128, 960, 1024, 40, 64, {}, None),
+    "one token, workspace": (1, 2, 4, 1, 128, 9024, 9088, 40, 64, {}, None),
+    "eight rows, two bits": (1, 2, 4, 2, 64, 448, 512, 1, 64, dict(bits=2, kind="sym", gv=32), None),
+    "sixteen rows, padded": (3, 1, 4, 4, 128, 512, 576, 2, 64, {}, [0, 100, 511]),
+    "twelve rows, cluster": (1, 1, 3, 4, 128, 1024, 1024, 2, 64, dict(kind="signed", gv=128), None),
+    "32 rows, split": (1, 1, 8, 4, 128, 4096, 4096, 2, 64, dict(gv=32), None),
+    "32 rows, symmetric": (1, 2, 8, 4, 64, 512, 512, 3, 64, dict(kind="sym", gk=128), None),
+    "80 rows": (2, 1, 4, 20, 128, 512, 576, 7, 64, {}, [0, 130]),
+    "160 rows, split": (1, 1, 8, 20, 128, 4096, 4096, 7, 192, {}, None),
+    "240 rows, two bits": (1, 2, 8, 30, 64, 512, 576, 7, 64, dict(bits=2, gv=32), None),
+    "520 rows": (1, 2, 4, 130, 64, 256, 256, 30, 64, dict(kind="sym"), None),
+    "520 rows, split": (2, 1, 4, 130, 128, 2048, 2112, 45, 192, {}, [0, 300]),
+    "520 rows, two bits": (1, 1, 4, 130, 128, 448, 448, 30, 64, dict(bits=2, gv=128), None),
+}
+
+
+def rows_of(c, oq, tq, nres):
+    """The rows that raw buffers (codes, scale, zero, resid) stand for, binary64 [outer, T, C]."""
+    import torch
+    codes, sc, ze, r = c
+    per = 8 // oq.bits
+    C = r.shape[-1]
+    x = np.stack([(codes[:, :tq] >> (oq.bits * k)) & ((1 << oq.bits) - 1) for k in range(per)], -1).astype(np.int32)
+    x = x.reshape(codes.shape[0], tq, C)
+    if oq.mode == O.SYM or oq.qmin < 0:
+        x = (x ^ (1 << (oq.bits - 1))) - (1 << (oq.bits - 1))
+    x = x.astype(np.float32)
+
+    def spread(m):
+        m = S.bf16_to_f64(m).astype(np.float32)
+        if oq.axis == O.ALONG_T:
+            return m[:, np.arange(tq) // oq.group]
+        return m[:, :tq][:, :, np.arange(C) // (oq.group or C)]
+    with np.errstate(invalid="ignore", over="ignore"):
+        if ze is not None:
+            x = x - spread(ze)
+        x = x * spread(sc)
+    x = torch.from_numpy(x).bfloat16().double().numpy()
+    return np.concatenate([x, S.bf16_to_f64(r[:, :nres])], 1)
+
+
+class Case:
+    def __init__(self, name, what):
+        self.B, self.H, self.G, self.n, self.C, tq, cap, nres, rows, fm, self.first = FORMS[name]
+        rng = np.random.default_rng(zlib.crc32((name + what).encode()))
+        self.hc = S.HostCache(rng, self.B * self.H, self.C, tq, cap, nres, rows, *S.formats(**{"gv": 64, **fm}))
+        self.q = S.W.to_bf16_bits(rng.standard_normal((self.B, self.n, self.H * self.G, self.C)).astype(np.float32))
+        POKE[what](self)
+        hc = self.hc
+        hc.K, hc.V = (rows_of(c, p, hc.tq, hc.nres) for c, p in ((hc.k, hc.kq), (hc.v, hc.vq)))
+        T = hc.T
+        f = np.zeros(hc.outer, np.int64) if self.first is None else np.asarray(self.first)
+        self.seen = (np.arange(T) >= f[:, None, None]) & (np.arange(T) <= T - self.n + np.arange(self.n)[:, None])  # [o, i, t]
+
+    def queries(self):
+        import torch
+        return torch.from_numpy(self.q.view(np.int16).copy()).view(torch.bfloat16).cuda()
+
+
+def key_inf(c, negative):
+    """+inf in channel 3 of buffered keys: logits are the sign of q's channel 3."""
+    c.hc.k[3][:, c.hc.nres - 1, 3] = INF
+    c.hc.k[3][:, 0, 3] = INF
+    if negative:
+        c.q[..., 3] |= 0x8000
+    c.q[..., 3] |= 0x0080                                  # not zero
+
+
+def q_nan(c):
+    c.q[0, c.n // 2, 0, 5] = NAN
+
+
+def q_inf(c):
+    c.q[-1, c.n - 1, -1, 7] = NEG
+
+
+def q_all(c):
+    c.q[...] = NAN
+
+
+def k_row(c):
+    c.hc.k[3][0, c.hc.nres // 2, 1] = NAN
+
+
+def k_group(c):
+    """a key group's scale, so every logit of its tokens; slice 0 only"""
+    c.hc.k[1][0, (c.hc.tq - 1) // c.hc.kq.group, 2] = NAN
+
+
+POKE = {"q nan": q_nan, "q inf": q_inf, "q all nan": q_all, "k row": k_row, "k group": k_group,
+        "k inf": lambda c: key_inf(c, False), "k inf, away": lambda c: key_inf(c, True)}
+LOGITS = ["q nan", "q inf", "q all nan", "k row", "k group", "k inf", "k inf, away"]
+
+
+def solve(c):
+    """x [o, i, j, t], mag, p, lse, poisoned [o, i, j]: rows with a NaN or +inf logit."""
+    hc, q = c.hc, S.bf16_to_f64(c.q)
+    with np.errstate(invalid="ignore"):
+        x, mag = S.logits(q, hc.K, c.first, c.H)
+        bad = (np.isnan(x) | (x == np.inf)).any(-1)
+        x0 = np.where(bad[..., None], 0.0, x)               # such rows are not compared further
+        p, lse = S.softmax(np.where(c.seen[:, :, None], x0, -np.inf))
+    mag = np.where(np.isfinite(mag), mag, 0.0)              # a logit of -inf has no error
+    return x0, mag, p, lse, bad
+
+
+def check_out(c, got, gl):
+    hc = c.hc
+    x, mag, p, lse, bad = solve(c)
+    out, absout = np.einsum("oijt,otc->oijc", p, hc.V), np.einsum("oijt,otc->oijc", p, np.abs(hc.V))
+    out = np.where(bad[..., None], np.nan, out)
+    e = 2 * S.logit_error(mag, np.where(np.isfinite(x), x, 0.0), c.C)
+    want, wl = S.to_rows(out, c.H), S.to_rows(np.where(bad, np.nan, lse), c.H)
+    assert np.array_equal(np.isnan(gl), np.isnan(wl)), "lse: NaN"
+    assert np.array_equal(np.isinf(gl), np.isinf(wl)), "lse: infinities"
+    ok = np.isfinite(wl)
+    tl = S.to_rows(e, c.H) + (hc.T + 64) * 2.0 ** -23 + 4 * 2.0 ** -23 * (np.abs(np.where(ok, wl, 0)) + 1)
+    assert np.all(np.abs(gl[ok] - wl[ok]) <= tl[ok])
+    assert np.array_equal(np.isnan(got), np.isnan(want)), "out: NaN"
+    assert np.array_equal(np.isposinf(got), np.isposinf(want)) and np.array_equal(np.isneginf(got), np.isneginf(want))
+    ok = np.isfinite(want)
+    u = 2.0 ** -8
+    to = S.to_rows((u + e[..., None] + (hc.T + 64) * 2.0 ** -23) * absout, c.H) + u * np.abs(np.where(ok, want, 0)) + 1e-30
+    assert np.all(np.abs(got[ok] - want[ok]) <= to[ok])
+
+
+def host(t):
+    return t.float().cpu().numpy().astype(np.float64)
+
+
+@pytest.mark.parametrize("what", LOGITS)
+@pytest.mark.parametrize("name", FORMS)
+def test_logits_that_are_not_finite(b, name, what):
+    c = Case(name, what)
+    out, lse = b.attend_chunk(c.queries(), c.hc.device(b, c.H, c.first))
+    check_out(c, host(out), host(lse))
