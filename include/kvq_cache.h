@@ -69,7 +69,9 @@ typedef struct {
  * kvq_dequantize returns, s * (code - zero_point) rounded once to bf16, and
  * the buffer's rows as they are.  A query that sees nothing (T = 0, n > T, or
  * padding), or only logits of -inf, gets out = 0 and lse = -inf; one that sees
- * a logit of NaN or +inf gets NaN in all of out and in lse.  n = 0 does nothing.
+ * a logit of NaN or +inf gets NaN in all of out and in lse.
+ * An infinity or NaN in v_t reaches its channel of the queries that see token t,
+ * and no other query.  n = 0 does nothing.
  *  - q: bf16 [outer/kv_heads][n][kv_heads*group][C]; out: bf16, same shape;
  *    lse: float32 [outer/kv_heads][n][kv_heads*group], or NULL.
  *  - Logits, softmax statistics and sums are float32; the probabilities enter

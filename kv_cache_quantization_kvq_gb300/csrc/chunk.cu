@@ -74,6 +74,13 @@ __device__ __forceinline__ void add_values(float (&y)[Rows<ROWS, C>::MT][Rows<RO
     }
 }
 
+// a pair of values, made finite where they are not known to be
+template <int BITS, bool FAST>
+__device__ __forceinline__ uint32_t value_of(uint32_t w, int sh, uint32_t mg, uint32_t s, uint32_t z, float off) {
+    const uint32_t x = value_pair<BITS, FAST>(w, sh, mg, s, z, off);
+    return FAST ? x : make_finite(x);
+}
+
 // P.V of one 32-token batch of the store: this lane's code words of its eight
 // tokens, 16 ks + {2 tig, 2 tig + 1, 8 + 2 tig, 9 + 2 tig}; vm: (scale, zero
 // point) of each token and V group.
@@ -97,10 +104,10 @@ __device__ __forceinline__ void values_of(float (&y)[Rows<ROWS, C>::MT][Rows<ROW
             const uint32_t x1 = __byte_perm(w[4 * ks + 2][h / 2], w[4 * ks + 3][h / 2], sel);
 #pragma unroll
             for (int i = 0; i < FH; i += 2)
-                add_values<ROWS, C>(y, h * FH + i, p[ks], value_pair<BITS, FAST>(x0, BITS * i, mg, s0, z0, off),
-                                    value_pair<BITS, FAST>(x1, BITS * i, mg, s1, z1, off),
-                                    value_pair<BITS, FAST>(x0, BITS * (i + 1), mg, s0, z0, off),
-                                    value_pair<BITS, FAST>(x1, BITS * (i + 1), mg, s1, z1, off));
+                add_values<ROWS, C>(y, h * FH + i, p[ks], value_of<BITS, FAST>(x0, BITS * i, mg, s0, z0, off),
+                                    value_of<BITS, FAST>(x1, BITS * i, mg, s1, z1, off),
+                                    value_of<BITS, FAST>(x0, BITS * (i + 1), mg, s0, z0, off),
+                                    value_of<BITS, FAST>(x1, BITS * (i + 1), mg, s1, z1, off));
         }
     }
 }
@@ -224,12 +231,14 @@ attend_rows_kernel(const ChunkArgs A)
     __shared__ __align__(16) uint4 qf[MT * G::kSteps * 32];
     __shared__ __align__(16) uint4 kcs[kWarps][C / 4];
     __shared__ __align__(16) uint32_t vms[kWarps][4][kBatch];
+    __shared__ __align__(16) int odd[2 * C];     // the first tokens with values that are not finite
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, tig = lane & 3;
     const int split = (int)(blockIdx.x % (uint32_t)A.nsplit);
     const int64_t o = blockIdx.x / (uint32_t)A.nsplit;
     stage_queries<BITS, C, MT>(a, o, 0, qf, tid, kThreads);
+    for (int c = tid; c < 2 * C; c += kThreads) odd[c] = kNever;
 
     // ---- the last token each of this lane's rows sees
     const int base = a.T - a.n;                  // token of query 0
@@ -333,6 +342,7 @@ attend_rows_kernel(const ChunkArgs A)
     }
     __syncthreads();                             // the queries are staged
 
+    int slow = 0;                                // values that may not be finite: 1 in the store, 2 in the buffer
     for (int b = b0; b < bs; ++b) {
         const int t0 = b * kBatch, t1 = min(t0 + kBatch, a.tq);
         if (fetched != staged) {
@@ -340,12 +350,10 @@ attend_rows_kernel(const ChunkArgs A)
             staged = fetched;
         }
         // the V constants of this batch
-        bool vfast = true;
-        if (a.vz) {
-            vfast = zero_exact(bf_hi(vr[0])) && zero_exact(bf_hi(vr[1]));
-            if (a.ngv > 2) vfast = vfast && zero_exact(bf_hi(vr[2])) && zero_exact(bf_hi(vr[3]));
-            vfast = __all_sync(0xFFFFFFFFu, vfast);
-        }
+        auto fits = [&](int k) { return scale_fits(vr[k]) && zero_exact(bf_hi(vr[k])); };
+        bool vfast = fits(0) && fits(1);
+        if (a.ngv > 2) vfast = vfast && fits(2) && fits(3);
+        vfast = __all_sync(0xFFFFFFFFu, vfast);
         __syncwarp();                            // the batch before has been read
         auto stage = [&](int k) {
             vms[warp][k][lane] = vfast ? (vr[k] & 0xFFFFu) | (biased(vr[k], 128.0f + a.voff) & 0xFFFF0000u) : vr[k];
@@ -390,7 +398,10 @@ attend_rows_kernel(const ChunkArgs A)
         const bool whole = t0 >= first && t1 - t0 == kBatch && t1 - 1 <= last_lo;
         softmax_of<C, ROWS>(a, s, y, st, p, whole, t0, t1, first, last, tig);
         if (vfast) values_of<BITS, C, ROWS, true>(y, p, vw, vm, vmg, a.voff, tig);
-        else values_of<BITS, C, ROWS, false>(y, p, vw, vm, vmg, a.voff, tig);
+        else {
+            slow |= 1;
+            values_of<BITS, C, ROWS, false>(y, p, vw, vm, vmg, a.voff, tig);
+        }
         if (b + 1 < bs) load_v(b + 1);
     }
 
@@ -426,6 +437,15 @@ attend_rows_kernel(const ChunkArgs A)
                     r[e][4 * i] = x.x; r[e][4 * i + 1] = x.y; r[e][4 * i + 2] = x.z; r[e][4 * i + 3] = x.w;
                 }
             }
+            uint32_t bad[2] = {0u, 0u};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+#pragma unroll
+                for (int i = 0; i < C / 16; ++i) {
+                    bad[e & 1] = add_if_odd(bad[e & 1], r[e][i]);
+                    r[e][i] = make_finite(r[e][i]);
+                }
+            if (__any_sync(0xFFFFFFFFu, (bad[0] | bad[1]) != 0u)) slow |= 2;
 #pragma unroll
             for (int nt = 0; nt < C / 8; nt += 2)
                 add_values<ROWS, C>(y, nt, p[ks], __byte_perm(r[0][nt / 2], r[1][nt / 2], 0x5410),
@@ -465,6 +485,15 @@ attend_rows_kernel(const ChunkArgs A)
                                         y[m][4 * q4 + 3][2 * h + e]);
                 }
             }
+        if (m == 0 && slow) {
+            if (slow & 1) note_rows<BITS, C>(a, o, max(b0 * kBatch, first), min(bs * kBatch, a.tq), odd, lane);
+            if (slow & 2) {
+                int from, to, skip;
+                batch_at(a, sp, max(b0, sp.nsb), from, skip);
+                batch_at(a, sp, b1 - 1, skip, to);
+                note_rows<BITS, C>(a, o, max(from, first), to, odd, lane);
+            }
+        }
         __syncthreads();
         for (int k = tid; k < R::kOut * (C / 4); k += kThreads) {
             const int row = k / (C / 4), c4 = (k % (C / 4)) * 4, r = 16 * m + row;
@@ -482,6 +511,12 @@ attend_rows_kernel(const ChunkArgs A)
                 v[1] = __fmaf_rn(x.y, f, v[1]);
                 v[2] = __fmaf_rn(x.z, f, v[2]);
                 v[3] = __fmaf_rn(x.w, f, v[3]);
+            }
+            const int4 op = *reinterpret_cast<const int4*>(&odd[c4]), on = *reinterpret_cast<const int4*>(&odd[C + c4]);
+            if ((op.x & op.y & op.z & op.w & on.x & on.y & on.z & on.w) != kNever) {
+                const int row_last = base + r / a.group;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] = __fadd_rn(v[i], odd_value(odd, C, c4 + i, row_last));
             }
             if (A.cluster) {
                 *reinterpret_cast<float4*>(&sy[0][row][c4]) = make_float4(v[0], v[1], v[2], v[3]);   // read by this thread only

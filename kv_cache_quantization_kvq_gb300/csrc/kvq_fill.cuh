@@ -40,12 +40,13 @@ __device__ __forceinline__ uint4 unpack_piece(uint32_t w, uint32_t mg, const uin
 }
 
 // Rows [rb, re) of key tile j token by token: at the padding, the store's end, in
-// the buffer (hidden and missing tokens are zeros), or with far zero points.  Kept
-// out of line: inlined into the loops below it pushed them out of the instruction
+// the buffer (hidden and missing tokens are zeros), or with far zero points or
+// scales.  Values that are not finite are made so and noted in odd[2 C], whose next
+// element then says so.  Kept out of line: inlined into the loops below it pushed them out of the instruction
 // cache (5.7 warps stalled on fetches per issue).
 template <int BITS, int C, bool KEYS>
 __device__ __noinline__ void fill_rows(const View& a, int64_t o, int first, int j, int rb, int re, unsigned char* tile,
-                                       int tid) {
+                                       int tid, int* odd) {
     constexpr int P = C / 8, kStep = 128 / P;
     const int p = tid % P;
     const float off = KEYS ? a.koff : a.voff;
@@ -84,6 +85,20 @@ __device__ __noinline__ void fill_rows(const View& a, int64_t o, int first, int 
                 }
                 y = unpack_piece<BITS, false>(load_piece<BITS>(codes + (int64_t)t * (C * BITS / 8)), mg, s, z, off);
             }
+            if constexpr (!KEYS) {
+                if (is_odd(y)) {
+                    auto note = [&](uint32_t& w, int c) {           // channels c and c + 4 of the piece
+                        note_odd(odd, C, p * 8 + c, w & 0xFFFFu, t);
+                        note_odd(odd, C, p * 8 + c + 4, w >> 16, t);
+                        w = make_finite(w);
+                    };
+                    note(y.x, 0);
+                    note(y.y, 1);
+                    note(y.z, 2);
+                    note(y.w, 3);
+                    odd[2 * C] = 1;
+                }
+            }
             *reinterpret_cast<uint4*>(tile + p / 8 * (kTile * 128) + tc::swizzled(row, p % 8)) = y;
         }
     }
@@ -104,6 +119,7 @@ struct Staged {
     static constexpr int kCodesB = kHalf * kRowB, kConstB = 2 * C * 2;                 // up to two key groups' scales
     static constexpr int kStageB = kCodesB + 2 * (C == 128 ? kConstB : 2 * kConstB);   // V: 4 warps x 4 groups x 16 words
     static constexpr int kBytes = kStages * kStageB;
+    static constexpr int kOddAt = kBytes + 256;  // values: where those that are not finite are noted, from the stages
 
     const View& a;
     const int64_t o;
@@ -129,6 +145,7 @@ struct Staged {
         rem = KEYS ? (int)((int64_t)mine() * kHalf % a.gk) : 0;
     }
 
+    __device__ __forceinline__ int* noted() const { return KEYS ? nullptr : reinterpret_cast<int*>(stage + kOddAt); }
     __device__ __forceinline__ int staged() const { return h1 - h0; }
     __device__ __forceinline__ int mine() const { return h0 + ((h0 ^ sub) & 1); }      // this group's first staged half
     // stages half h (one lane); the stage's last readers are done
@@ -166,20 +183,27 @@ struct Staged {
     __device__ __forceinline__ bool half(int h, unsigned char* tile, const Ready& ready) {
         const int rb = (h & 1) * kHalf;
         if (h < h0 || h >= h1) {
-            fill_rows<BITS, C, KEYS>(a, o, first, h >> 1, rb, rb + kHalf, tile, me);
+            fill_rows<BITS, C, KEYS>(a, o, first, h >> 1, rb, rb + kHalf, tile, me, noted());
             return true;
         }
         const int k = k0 + h - h0, s = k % kStages;
         unsigned char* st = stage + s * kStageB;
         uint32_t* meta = reinterpret_cast<uint32_t*>(st + kCodesB) + (me >> 5) * 64;   // [4 groups][16 rows] of this warp
         bool fast = true;
+        uint32_t mv[2] = {0u, 0u};
+        if constexpr (!KEYS) {                   // while the copy is on its way
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                mv[i] = (vm[i] & 0xFFFFu) | (biased(vm[i], bias) & 0xFFFF0000u);
+                fast = fast && scale_fits(vm[i]) && zero_exact(bf_hi(vm[i]));
+            }
+            fast = __all_sync(0xFFFFFFFFu, fast);
+        }
         // the copy has landed, so the stage's last readers, the other group's among them, are done with it
         if (!ready(&rfull[s], (k / kStages) & 1)) return false;
         if constexpr (!KEYS) {
-            fast = __all_sync(0xFFFFFFFFu, zero_exact(bf_hi(vm[0])) && zero_exact(bf_hi(vm[1])));
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-                meta[(((me >> 4) & 1) + 2 * i) * 16 + (me & 15)] = (vm[i] & 0xFFFFu) | (biased(vm[i], bias) & 0xFFFF0000u);
+            for (int i = 0; i < 2; ++i) meta[(((me >> 4) & 1) + 2 * i) * 16 + (me & 15)] = mv[i];
             if (h + 2 < h1) load_meta(h + 2);
             __syncwarp();
         }
@@ -222,7 +246,7 @@ struct Staged {
                 *reinterpret_cast<uint4*>(dst + i * kStep * 128) = unpack_piece<BITS, true>(w, mg, sk, zk, 0.0f);
             }
         }
-        if (!okq[0] || !okq[1]) fill_rows<BITS, C, KEYS>(a, o, first, h >> 1, rb, rb + kHalf, tile, me);
+        if (!okq[0] || !okq[1]) fill_rows<BITS, C, KEYS>(a, o, first, h >> 1, rb, rb + kHalf, tile, me, noted());
         if constexpr (KEYS) {
             rem += 2 * kHalf;
             while (rem >= a.gk) rem -= a.gk;

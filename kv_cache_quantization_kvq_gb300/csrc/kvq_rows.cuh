@@ -140,6 +140,81 @@ __device__ __forceinline__ uint32_t value_pair(uint32_t w, int sh, uint32_t mg, 
     return pack_bf16x2(__fmul_rn(lo, bf_lo(s)), __fmul_rn(hi, bf_hi(s)));
 }
 
+// ---- values that are not finite
+// A token that a row does not see has weight 0 in the row's value product, and 0
+// times NaN or infinity would be NaN there.  So the products read such values as the
+// largest finite one, and a CTA keeps per channel the first of its tokens, padding aside, that holds
+// +inf or NaN (odd[c]) and the first that holds -inf or NaN (odd[C + c]); a row
+// that sees that token has the infinity added to its sum.  Only slow paths look: the
+// fast ones take constants that cannot give such a value.
+constexpr int kNever = 0x7FFFFFFF;               // no token: positions are smaller
+
+// whether a scale may take the bf16 route for values: with |code - zp| < 256 its products are finite
+// (and so does every one of the scales whose bit patterns, sign aside, are at most this)
+constexpr uint32_t kScaleFits = 0x7A00u;         // bf16 1.66e35
+__device__ __forceinline__ bool scale_fits(uint32_t sz) { return (sz & 0x7FFFu) <= kScaleFits; }
+// whether a scale and zero point can give a value that is not finite
+__device__ __forceinline__ bool may_be_odd(float s, float z) { return !(fabsf(s) * (fabsf(z) + 16.0f) < 3.3e38f); }
+// 0 as long as every w added is finite (0 times NaN or infinity is NaN): one instruction a pair
+__device__ __forceinline__ uint32_t add_if_odd(uint32_t acc, uint32_t w) {
+    uint32_t d;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(w), "r"(0u), "r"(acc));
+    return d;
+}
+__device__ __forceinline__ bool is_odd(const uint4& x) {
+    return add_if_odd(add_if_odd(0u, x.x), x.y) != 0u || add_if_odd(add_if_odd(0u, x.z), x.w) != 0u;
+}
+// a pair of bf16 with the largest finite ones in place of infinities and NaN: 0 times it is 0
+__device__ __forceinline__ uint32_t make_finite(uint32_t w) {
+    asm("max.bf16x2 %0, %0, %1;" : "+r"(w) : "r"(0xFF7FFF7Fu));
+    asm("min.bf16x2 %0, %0, %1;" : "+r"(w) : "r"(0x7F7F7F7Fu));
+    return w;
+}
+// notes bf16 value v of channel c and token t
+__device__ __forceinline__ void note_odd(int* odd, int C, int c, uint32_t v, int t) {
+    if ((v & 0x7F80u) != 0x7F80u) return;
+    const bool nan = v & 0x7Fu, neg = v & 0x8000u;
+    if (nan || !neg) atomicMin(&odd[c], t);
+    if (nan || neg) atomicMin(&odd[C + c], t);
+}
+// what a row whose last token is `last` adds to channel c
+__device__ __forceinline__ float odd_value(const int* odd, int C, int c, int last) {
+    return __fadd_rn(odd[c] <= last ? INFINITY : 0.0f, odd[C + c] <= last ? -INFINITY : 0.0f);
+}
+// notes a whole row of values, token t of slice o, one element at a time
+template <int BITS, int C>
+__device__ __forceinline__ void note_row(const View& a, int64_t o, int t, int* odd) {
+    const uint8_t* codes = a.vc + ((uint64_t)o * a.cap + t) * (C * BITS / 8);
+    const int64_t meta = (o * a.cap + t) * a.ngv;
+#pragma unroll 1
+    for (int c = 0; c < C; ++c) {
+        uint32_t v;
+        if (t >= a.tq) {
+            v = bits_of(a.vr + ((uint64_t)o * a.rrows + (t - a.tq)) * C + c);
+        } else {
+            const uint32_t f = ((codes[c * BITS / 8] ^ (a.vflip & 0xFFu)) >> (c * BITS % 8)) & ((1u << BITS) - 1);
+            const float z = a.vz ? bf_lo(bits_of(a.vz + meta + c / a.gv)) : 0.0f;
+            const float x = __fmul_rn(__fsub_rn(__fsub_rn((float)f, a.voff), z), bf_lo(bits_of(a.vs + meta + c / a.gv)));
+            v = pack_bf16x2(x, 0.0f) & 0xFFFFu;
+        }
+        note_odd(odd, C, c, v, t);
+    }
+}
+
+// notes the values of tokens [t0, t1) of slice o, by one warp
+template <int BITS, int C>
+__device__ __noinline__ void note_rows(const View& a, int64_t o, int t0, int t1, int* odd, int lane) {
+#pragma unroll 1
+    for (int64_t t = (int64_t)t0 + lane; t < t1; t += 32) {
+        bool look = t >= a.tq;
+        for (int k = 0; !look && k < a.ngv; ++k) {
+            const int64_t at = (o * a.cap + t) * a.ngv + k;
+            look = may_be_odd(bf_lo(bits_of(a.vs + at)), a.vz ? bf_lo(bits_of(a.vz + at)) : 0.0f);
+        }
+        if (look) note_row<BITS, C>(a, o, (int)t, odd);
+    }
+}
+
 // Channel pairs (c, c + F/2) of this lane's quarter of a bf16 row, from the
 // quarter's first element: the order of the code words' fields.
 template <int BITS, int C>

@@ -50,10 +50,11 @@ constexpr float kSlack = 8.0f;                   // base-2 growth of the maximum
 
 // ---------------------------------------------------------------- expansion
 // A thread takes one piece of 8 channels of 8 consecutive tokens: of K (its
-// group's scales and zero points read once) or of V.
+// group's scales and zero points read once) or of V.  odd[slice][Tp / 8] says which
+// 8 tokens hold values that are not finite; those are made finite.
 template <int BITS, int C>
 __global__ void __launch_bounds__(256)
-expand_kernel(const View a, int64_t o0, int64_t slices, int64_t Tp, __nv_bfloat16* kx, __nv_bfloat16* vx)
+expand_kernel(const View a, int64_t o0, int64_t slices, int64_t Tp, __nv_bfloat16* kx, __nv_bfloat16* vx, uint8_t* odd)
 {
     using W = typename CodeWord<BITS>::T;
     constexpr int P = C / 8;
@@ -72,6 +73,7 @@ expand_kernel(const View a, int64_t o0, int64_t slices, int64_t Tp, __nv_bfloat1
     const uint32_t flip = keys ? a.kflip : a.vflip;
     __nv_bfloat16* dst = (keys ? kx : vx) + (so * Tp + t0) * C + p * 8;
     float s[8], z[8];
+    bool bad = false;
     if (keys && t0 < a.tq) {
         const int64_t at = (o * a.ngk + t0 / a.gk) * C + p * 8;     // 8 tokens lie in one group
         Raw8<__nv_bfloat16> r;
@@ -86,13 +88,16 @@ expand_kernel(const View a, int64_t o0, int64_t slices, int64_t Tp, __nv_bfloat1
     for (int i = 0; i < 8; ++i) {
         const int t = t0 + i;
         uint4 x = make_uint4(0, 0, 0, 0);
+        bool look = false;                       // values that may not be finite
         if (t >= first && t < a.T) {
             if (t >= a.tq) {
+                look = !keys;
                 x = *reinterpret_cast<const uint4*>((keys ? a.kr : a.vr) + ((uint64_t)o * a.rrows + (t - a.tq)) * C + p * 8);
             } else {
                 if (!keys) {
                     const int64_t at = (o * a.cap + t) * a.ngv + p * 8 / a.gv;
                     const float sv = __bfloat162float(sc[at]), zv = ze ? __bfloat162float(ze[at]) : 0.0f;
+                    look = may_be_odd(sv, zv);
 #pragma unroll
                     for (int k = 0; k < 8; ++k) { s[k] = sv; z[k] = zv; }
                 }
@@ -107,7 +112,15 @@ expand_kernel(const View a, int64_t o0, int64_t slices, int64_t Tp, __nv_bfloat1
                 store8(reinterpret_cast<__nv_bfloat16*>(&x), v);
             }
         }
+        if (look && is_odd(x)) {
+            bad = true;
+            x = make_uint4(make_finite(x.x), make_finite(x.y), make_finite(x.z), make_finite(x.w));
+        }
         *reinterpret_cast<uint4*>(dst + (int64_t)i * C) = x;
+    }
+    if (!keys) {                                 // whole warps are here: Tp / 8 P is a multiple of 128
+        const uint32_t any = __ballot_sync(0xFFFFFFFFu, bad) >> (threadIdx.x & 31 & ~(P - 1)) & ((1u << P) - 1);
+        if (p == 0) odd[id / P] = any ? 1 : 0;
     }
 }
 
@@ -115,8 +128,8 @@ expand_kernel(const View a, int64_t o0, int64_t slices, int64_t Tp, __nv_bfloat1
 template <int C>
 struct Smem {
     static constexpr int kTileB = kTile * C * 2; // one Q, K or V tile
-    static constexpr int kQ = 0, kRing = 2 * kTileB, kBars = kRing + kSlots * kTileB;
-    static constexpr int kBytes = kBars + 256 + 1024;               // and room to align to 1024
+    static constexpr int kQ = 0, kRing = 2 * kTileB, kBars = kRing + kSlots * kTileB, kOdd = kBars + 256;
+    static constexpr int kSums = kOdd + (2 * C + 4) * 4, kBytes = kSums + 2 * kTile * 4 + 1024;    // and room to align to 1024
 };
 
 struct TcArgs {
@@ -124,6 +137,8 @@ struct TcArgs {
     int64_t o0, slices, Tp;
     int32_t nwhole;                              // query tiles taken whole; the others are split
     int32_t trows;                               // rows of a tile that partial results are kept for
+    int32_t bits;
+    const uint8_t* odd;                          // [slices][Tp / 8], as expand_kernel writes it
 };
 
 // The query tile and split of a CTA.
@@ -166,6 +181,26 @@ struct TileOf {
     }
 };
 
+// Adds the values that are not finite to the rows that the CTA has written: a thread
+// per row, after everything else (in the softmax warps' epilogue it cost the fused
+// form 6 us of 93).  sums: the rows' sums of weights.
+template <int C>
+__device__ __noinline__ void add_odd(const TcArgs& X, const TileOf& w, const int* odd, const float* sums, int tid, int threads) {
+    const View& a = X.A.v;
+    for (int i = tid; i < w.nrows; i += threads) {
+        const int r = w.r0 + i, last = a.T - a.n + r / a.group;
+        float* part = w.part(X, r, C);
+        __nv_bfloat16* out = X.A.out + row_index(a, w.o, r) * C;
+#pragma unroll 1
+        for (int c = 0; c < C; ++c) {
+            const float x = odd_value(odd, C, c, last);
+            if (x == 0.0f) continue;
+            if (w.nsplit > 1) part[c] = __fadd_rn(part[c], x);
+            else if (sums[i] != 0.0f) out[c] = __float2bfloat16(__fadd_rn(__bfloat162float(out[c]), x));
+        }
+    }
+}
+
 template <int C>
 __global__ void __launch_bounds__(kThreadsTc, 1)
 attend_tc_kernel(const TcArgs X, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap)
@@ -181,6 +216,8 @@ attend_tc_kernel(const TcArgs X, const __grid_constant__ CUtensorMap kmap, const
     uint64_t* odone = pfull + 2;                 // [2] its output is complete
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(odone + 2);
     volatile int* gone = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    int* odd = reinterpret_cast<int*>(sm + S::kOdd);               // [2 C], and whether any is noted
+    float* sums = reinterpret_cast<float*>(sm + S::kSums);         // [256] the rows' sums of weights
 
     const ChunkArgs& A = X.A;
     const View& a = A.v;
@@ -213,11 +250,29 @@ attend_tc_kernel(const TcArgs X, const __grid_constant__ CUtensorMap kmap, const
         *reinterpret_cast<uint4*>(sm + S::kQ + (r / kTile) * S::kTileB + (c / 8) * (kTile * 128) +
                                   tc::swizzled(r % kTile, c % 8)) = x;
     }
+    // a key tile's flags are 16 bytes; what they point to is looked up in the cache itself
+    const uint4* flags = reinterpret_cast<const uint4*>(X.odd + so * (X.Tp / 8)) + j0;
+    uint32_t mine = 0;
+    for (int j = tid; j < n; j += kThreadsTc) {
+        const uint4 f = flags[j];
+        mine |= f.x | f.y | f.z | f.w;
+    }
+    for (int c = tid; c < 2 * C; c += kThreadsTc) odd[c] = kNever;
     tc::async_fence();
     tc::before_sync();
-    __syncthreads();
+    const bool any_odd = __syncthreads_or(mine != 0);
     tc::after_sync();
     const uint32_t tmem = *tmem_slot;
+    if (tid == 0) odd[2 * C] = any_odd;
+    if (any_odd) {
+        for (int t = tid; t < n * kTile; t += kThreadsTc) {
+            const int tok = j0 * kTile + t;
+            if (reinterpret_cast<const uint8_t*>(flags)[t / 8] == 0 || tok < first || tok >= a.T) continue;
+            if (X.bits == 4) note_row<4, C>(a, o, tok, odd);
+            else note_row<2, C>(a, o, tok, odd);
+        }
+        __syncthreads();
+    }
 
     if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
@@ -411,6 +466,7 @@ attend_tc_kernel(const TcArgs X, const __grid_constant__ CUtensorMap kmap, const
             }
             __syncwarp();                        // the next load wants the whole warp
         }
+        if (write) sums[r - r0] = l;
         if (write && nsplit > 1) *reinterpret_cast<float2*>(part + C) = make_float2(m, l);
         if (write && nsplit == 1 && A.lse)
             A.lse[at] = row_lse(m, l);
@@ -421,6 +477,7 @@ attend_tc_kernel(const TcArgs X, const __grid_constant__ CUtensorMap kmap, const
     __syncthreads();
     tc::after_sync();
     if (warp == 9) tc::dealloc(tmem, 512);
+    if (odd[2 * C] && !*gone) add_odd<C>(X, w, odd, sums, tid, kThreadsTc);
 }
 
 // ---------------------------------------------------------------- fused form
@@ -441,7 +498,9 @@ struct SmemF {
     static constexpr int kTileB = kTile * C * 2;
     static constexpr int kQ = 0, kK = 2 * kTileB, kV = kK + 2 * kTileB, kRawK = kV + 2 * kTileB;    // two K, two V tiles,
     static constexpr int kRawV = kRawK + Staged<BITS, C, true>::kBytes;                 // and their staged codes
-    static constexpr int kBars = kRawV + Staged<BITS, C, false>::kBytes, kBytes = kBars + 256 + 1024;
+    static constexpr int kBars = kRawV + Staged<BITS, C, false>::kBytes, kOdd = kRawV + Staged<BITS, C, false>::kOddAt;
+    static_assert(kOdd == kBars + 256, "behind the barriers");
+    static constexpr int kSums = kOdd + (2 * C + 4) * 4, kBytes = kSums + 2 * kTile * 4 + 1024;
 };
 
 template <int BITS, int C>
@@ -461,6 +520,8 @@ attend_fused_kernel(const __grid_constant__ TcArgs X)
     uint64_t* raw_bars = odone + 2;              // [K full, K free, V full, V free][3]
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(raw_bars + 12);
     volatile int* gone = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    int* odd = reinterpret_cast<int*>(sm + S::kOdd);               // [2 C], and whether any is noted
+    float* sums = reinterpret_cast<float*>(sm + S::kSums);         // [256] the rows' sums of weights
 
     const ChunkArgs& A = X.A;
     const View& a = A.v;
@@ -486,6 +547,7 @@ attend_fused_kernel(const __grid_constant__ TcArgs X)
         mbar_init_fence();
     }
     if (warp == 8) tc::alloc(tmem_slot, 512);
+    for (int c = tid; c <= 2 * C; c += kFusedThreads) odd[c] = c < 2 * C ? kNever : 0;
     if (warp < 12)
         for (int k = tid; k < nt * kTile * (C / 8); k += 384) {
             const int r = k / (C / 8), c = k % (C / 8);
@@ -681,6 +743,7 @@ attend_fused_kernel(const __grid_constant__ TcArgs X)
             }
             __syncwarp();
         }
+        if (write) sums[r - r0] = l;
         if (write && w.nsplit > 1) *reinterpret_cast<float2*>(part + C) = make_float2(m, l);
         if (write && w.nsplit == 1 && A.lse)
             A.lse[at] = row_lse(m, l);
@@ -690,6 +753,7 @@ attend_fused_kernel(const __grid_constant__ TcArgs X)
     __syncthreads();
     tc::after_sync();
     if (warp == 8) tc::dealloc(tmem, 512);
+    if (odd[2 * C] && !*gone) add_odd<C>(X, w, odd, sums, tid, kFusedThreads);
 }
 
 // One warp per row of the split query tiles joins their partial results.
@@ -764,7 +828,10 @@ cudaError_t launch_tc(const ChunkArgs& A0, int64_t outer, void* ws, cudaStream_t
     X.trows = (int32_t)std::min<int64_t>(A0.v.rows, 2 * kTile);
     __nv_bfloat16* kx = static_cast<__nv_bfloat16*>(ws);
     __nv_bfloat16* vx = kx + p.slices * p.Tp * C;
-    X.A.part = fused ? static_cast<float*>(ws) : reinterpret_cast<float*>(vx + p.slices * p.Tp * C);
+    X.bits = BITS;
+    uint8_t* odd = reinterpret_cast<uint8_t*>(vx + p.slices * p.Tp * C);
+    X.odd = odd;
+    X.A.part = fused ? static_cast<float*>(ws) : reinterpret_cast<float*>(odd + p.slices * (p.Tp / 8));
     if ((!fused && p.slices * p.Tp > 0x7FFFFFFF) || p.slices * p.ntiles > 0x7FFFFFFF - kMaxSplitCtas)
         return cudaErrorInvalidConfiguration;
     CUtensorMap km, vm;
@@ -785,7 +852,7 @@ cudaError_t launch_tc(const ChunkArgs& A0, int64_t outer, void* ws, cudaStream_t
             attend_fused_kernel<BITS, C><<<grid, kFusedThreads, (SmemF<BITS, C>::kBytes), st>>>(X);
         } else {
             const int64_t items = X.slices * (p.Tp / 8) * (C / 8);
-            expand_kernel<BITS, C><<<dim3((unsigned)((items + 255) / 256), 2), 256, 0, st>>>(X.A.v, o0, X.slices, p.Tp, kx, vx);
+            expand_kernel<BITS, C><<<dim3((unsigned)((items + 255) / 256), 2), 256, 0, st>>>(X.A.v, o0, X.slices, p.Tp, kx, vx, odd);
             attend_tc_kernel<C><<<grid, kThreadsTc, Smem<C>::kBytes, st>>>(X, km, vm);
         }
         if (w.tail) {
@@ -822,6 +889,7 @@ size_t chunk_tc_workspace(int64_t outer, int64_t C, int64_t tmax, int64_t rows)
 {
     const TcPlan p = tc_plan(outer, C, tmax, rows);
     size_t b = fused_form(rows) ? 0 : (size_t)std::min(outer * p.Tp * C * 4, std::max(kExpandBytes, p.Tp * C * 4));
+    b += b / (32 * C);                           // a flag for 8 tokens
     const int64_t trows = std::min<int64_t>(rows, 2 * kTile), tiles = outer * p.ntiles;
     b += (size_t)(std::min(kMaxSplitCtas, tiles * std::max<int64_t>(p.Tp / kTile / 2, 1)) * trows * (C + 4)) * 4;
     return b;

@@ -2,7 +2,9 @@
 
 The definition sums over the tokens a query sees, so:
   * a logit that is NaN or +inf, seen, makes the row's out and lse NaN; a logit
-    of -inf is a weight of 0.
+    of -inf is a weight of 0;
+  * a value that is not finite reaches its channel of every row that sees its
+    token (+inf, -inf, or NaN where both or a NaN are seen), and no other row.
 Whether a number is finite, and which infinity it is, is compared exactly; the
 finite ones with the tolerances of test_stream_attend_gpu.py (u = 2^-8, the
 largest relative error of a rounding to bf16; e twice the logits' error):
@@ -123,9 +125,30 @@ def k_group(c):
     c.hc.k[1][0, (c.hc.tq - 1) // c.hc.kq.group, 2] = NAN
 
 
+def v_buffer(c):
+    v, last = c.hc.v[3], c.hc.nres - 1
+    v[:, last, 1], v[:, last, 2], v[:, last, 33] = INF, NEG, NAN
+    v[0, 0, 5] = INF
+    v[0, last, 5] = NEG                                    # rows that see both: NaN
+
+
+def v_scale(bits):
+    def poke(c):
+        c.hc.v[1][0, c.hc.tq - 1, 0] = bits                # the newest store token, one group of channels
+    return poke
+
+
+def v_zero(c):
+    if c.hc.v[2] is None:
+        return v_scale(INF)(c)
+    c.hc.v[2][0, c.hc.tq - 1, -1] = NEG
+
+
 POKE = {"q nan": q_nan, "q inf": q_inf, "q all nan": q_all, "k row": k_row, "k group": k_group,
-        "k inf": lambda c: key_inf(c, False), "k inf, away": lambda c: key_inf(c, True)}
+        "k inf": lambda c: key_inf(c, False), "k inf, away": lambda c: key_inf(c, True),
+        "v buffer": v_buffer, "v scale inf": v_scale(INF), "v scale nan": v_scale(NAN), "v zero": v_zero}
 LOGITS = ["q nan", "q inf", "q all nan", "k row", "k group", "k inf", "k inf, away"]
+VALUES = ["v buffer", "v scale inf", "v scale nan", "v zero"]
 
 
 def solve(c):
@@ -143,7 +166,13 @@ def solve(c):
 def check_out(c, got, gl):
     hc = c.hc
     x, mag, p, lse, bad = solve(c)
-    out, absout = np.einsum("oijt,otc->oijc", p, hc.V), np.einsum("oijt,otc->oijc", p, np.abs(hc.V))
+    V = np.where(np.isfinite(hc.V), hc.V, 0.0)
+    out, absout = np.einsum("oijt,otc->oijc", p, V), np.einsum("oijt,otc->oijc", p, np.abs(V))
+    seen = c.seen.astype(np.float64)
+    plus = np.einsum("oit,otc->oic", seen, ((hc.V == np.inf) | np.isnan(hc.V)).astype(np.float64)) > 0
+    minus = np.einsum("oit,otc->oic", seen, ((hc.V == -np.inf) | np.isnan(hc.V)).astype(np.float64)) > 0
+    with np.errstate(invalid="ignore"):
+        out = out + np.where(plus, np.inf, 0.0)[:, :, None] + np.where(minus, -np.inf, 0.0)[:, :, None]
     out = np.where(bad[..., None], np.nan, out)
     e = 2 * S.logit_error(mag, np.where(np.isfinite(x), x, 0.0), c.C)
     want, wl = S.to_rows(out, c.H), S.to_rows(np.where(bad, np.nan, lse), c.H)
@@ -168,5 +197,14 @@ def host(t):
 @pytest.mark.parametrize("name", FORMS)
 def test_logits_that_are_not_finite(b, name, what):
     c = Case(name, what)
+    out, lse = b.attend_chunk(c.queries(), c.hc.device(b, c.H, c.first))
+    check_out(c, host(out), host(lse))
+
+
+@pytest.mark.parametrize("what", VALUES)
+@pytest.mark.parametrize("name", FORMS)
+def test_values_that_are_not_finite(b, name, what):
+    c = Case(name, what)
+    assert not np.isfinite(c.hc.V).all()
     out, lse = b.attend_chunk(c.queries(), c.hc.device(b, c.H, c.first))
     check_out(c, host(out), host(lse))
