@@ -99,7 +99,8 @@ KVQ_API kvq_status kvq_attend_chunk(const void* q, int64_t n, int64_t group, int
  *                      + sum_{i < n, j < group, t in seen(o, i)} exp(q . k_t / sqrt(C) - lse[b][i][h*group+j])
  * for t < T; scores of other columns are left as they are.
  *  - q, lse: as kvq_attend_chunk takes and writes them.  A row whose lse is
- *    -inf gives nothing.  Only the K side of the cache is read (its v_* and
+ *    -inf gives nothing, whatever its q holds; one whose lse is NaN makes NaN of
+ *    the score of every token it sees.  Only the K side of the cache is read (its v_* and
  *    v_params are not).
  *  - scores_in, scores_out: float32 [outer][score_stride], score_stride >= T;
  *    scores_in may be NULL (zeros) or scores_out itself; otherwise they must

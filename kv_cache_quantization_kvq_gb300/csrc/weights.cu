@@ -110,12 +110,15 @@ weights_rows_kernel(const WeightArgs A)
             const float la = nlse[16 * t + g], lb = nlse[16 * t + g + 8];
             const int ra = lasts[16 * t + g], rb = lasts[16 * t + g + 8];
             const bool whole = t0 >= first && t1 - t0 == kBatch && t1 - 1 <= lasts[16 * t];
+            // rows that do not exist, or give nothing: selected, since their scores may be NaN all the same
+            const bool da = la == -INFINITY, db = lb == -INFINITY;
             const bool two = 16 * t + 8 < a.rows;                   // rows g + 8 exist
 #pragma unroll
             for (int j = 0; j < 4; ++j)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    float wa = ex2(__fmaf_rn(s[0][j][e], a.scale2, la)), wb = two ? ex2(__fmaf_rn(s[0][j][2 + e], a.scale2, lb)) : 0.0f;
+                    float wa = da ? 0.0f : ex2(__fmaf_rn(s[0][j][e], a.scale2, la));
+                    float wb = two && !db ? ex2(__fmaf_rn(s[0][j][2 + e], a.scale2, lb)) : 0.0f;
                     if (!whole) {                // selected: a hidden token's score may be NaN
                         const int tok = t0 + 8 * j + 2 * tig + e;
                         const bool live = tok >= first && tok < t1;

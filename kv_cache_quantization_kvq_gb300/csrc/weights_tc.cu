@@ -5,9 +5,11 @@
 // transposed: S^T = K Q^T puts a token in each lane of tensor memory and the
 // query rows in its columns, so a token's sum over the rows is a sum over one
 // thread's registers: no shuffles, no atomics, a fixed order.
-//  1. pack_rows_kernel writes the query rows of every slice densely (rows
-//     padded to 128 with zeros), with -lse in base 2 (-inf where a row gives
-//     nothing, so that 2^(x - inf) = 0) and the last token a row sees;
+//  1. pack_rows_kernel writes the query rows of every slice densely, with -lse in
+//     base 2 and the last token a row sees (-1 where it gives nothing: a tile with
+//     such a row takes the masked sums, for its scores may be NaN).  The last row is
+//     repeated to a multiple of 128 rows, with -lse = -inf: zeros there would make
+//     NaN of an infinite key that gives every real row a weight of 0;
 //  2. weights_tc_kernel, one CTA a SM, walks jobs of 256 tokens (and a split of
 //     the rows): eight fill warps unpack the next job's keys into two swizzled
 //     M = 128 tiles (kvq_fill.cuh) while the current ones are in use; one warp loads tiles of 128
@@ -63,23 +65,22 @@ pack_rows_kernel(const View a, const float* lse, int64_t R, int C, int64_t total
     const int p = (int)(id - row * P);
     const int64_t o = row / R;
     const int r = (int)(row - o * R);
-    uint4 x = make_uint4(0, 0, 0, 0);
-    float l = -INFINITY;                         // 2^(x - inf) = 0: no weight
-    int last = -1;
-    if (r < a.rows) {
-        const int64_t at = row_index(a, o, r);
-        x = interleave(*reinterpret_cast<const uint4*>(a.q + at * C + p * 8));
-        if (p == 0) {
-            l = lse[at];
-            l = l == -INFINITY ? -INFINITY : -__fmul_rn(l, kLog2e);
-            last = a.T - a.n + r / a.group;
-        }
+    const int real = min(r, a.rows - 1);
+    const int64_t at = row_index(a, o, real);
+    const uint4 x = interleave(*reinterpret_cast<const uint4*>(a.q + at * C + p * 8));
+    float l = -INFINITY;
+    int last = -1;                               // gives nothing
+    if (p == 0) {
+        l = lse[at];
+        l = l == -INFINITY ? -INFINITY : -__fmul_rn(l, kLog2e);
+        if (l != -INFINITY) last = a.T - a.n + real / a.group;
+        if (r > real) l = -INFINITY;
     }
     reinterpret_cast<uint4*>(qx)[id] = x;
     if (p == 0) {
-        float* at = rows2 + row / kTile * (2 * kTile) + row % kTile;
-        at[0] = l;
-        at[kTile] = __int_as_float(last);
+        float* to = rows2 + row / kTile * (2 * kTile) + row % kTile;
+        to[0] = l;
+        to[kTile] = __int_as_float(last);
     }
 }
 
@@ -290,7 +291,6 @@ weights_tc_kernel(const __grid_constant__ WtArgs A, const __grid_constant__ CUte
         const int t = (warp >> 2) & 1, b = warp >> 3, me = (warp & 3) * 32 + lane;
         const uint32_t d_at = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (2 * t + b) * kTile;
         const u64 sc2 = pk(a.scale2, a.scale2);
-        const int base = a.T - a.n;
         int it = 0, k = 0;
         bool ok = true;
         Job J(A, job0);
@@ -303,9 +303,11 @@ weights_tc_kernel(const __grid_constant__ WtArgs A, const __grid_constant__ CUte
                 ok = ready(&rfull[s], (it / S::kRowSlots) & 1) && ready(&dfull[2 * t + b], (it >> 1) & 1);
                 if (!ok) break;
                 tc::after_sync();
-                const int row0 = (J.n0 + i) * kTile;
-                const bool cut = tile_hi > base + row0 / a.group;   // some row does not see some token
                 const float4* rp = srow + s * (kTile / 2);
+                const float4 z4 = rp[kTile / 4 + lane];
+                const int fewest = __reduce_min_sync(0xFFFFFFFFu, min(min(__float_as_int(z4.x), __float_as_int(z4.y)),
+                                                                     min(__float_as_int(z4.z), __float_as_int(z4.w))));
+                const bool cut = tile_hi > fewest;                  // some row does not see some token, or gives nothing
                 u64 acc0 = 0, acc1 = 0;
                 if (!cut) {
 #pragma unroll 1

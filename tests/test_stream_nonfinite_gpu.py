@@ -1,15 +1,17 @@
-"""kvq_attend_chunk where tokens hold NaN or infinities.
+"""kvq_attend_chunk and kvq_attend_weights where tokens hold NaN or infinities.
 
 The definition sums over the tokens a query sees, so:
-  * a logit that is NaN or +inf, seen, makes the row's out and lse NaN; a logit
-    of -inf is a weight of 0;
+  * a logit that is NaN or +inf, seen, makes the row's out and lse NaN, and the
+    weights of every token that the row sees; a logit of -inf is a weight of 0;
   * a value that is not finite reaches its channel of every row that sees its
-    token (+inf, -inf, or NaN where both or a NaN are seen), and no other row.
+    token (+inf, -inf, or NaN where both or a NaN are seen), and no other row;
+  * rows that give nothing (lse = -inf) and rows that do not exist add nothing.
 Whether a number is finite, and which infinity it is, is compared exactly; the
 finite ones with the tolerances of test_stream_attend_gpu.py (u = 2^-8, the
 largest relative error of a rounding to bf16; e twice the logits' error):
   lse: e + (T + 64) 2^-23 + 4 2^-23 (|lse| + 1)
   out: (u + e + (T + 64) 2^-23) sum_t p_t |v_t| + u |out|
+  weights: (e + (rows + 64) 2^-23 + 8 2^-23 |lse|) sum w + 2^-23 sum w
 """
 import zlib
 
@@ -208,3 +210,36 @@ def test_values_that_are_not_finite(b, name, what):
     assert not np.isfinite(c.hc.V).all()
     out, lse = b.attend_chunk(c.queries(), c.hc.device(b, c.H, c.first))
     check_out(c, host(out), host(lse))
+
+
+@pytest.mark.parametrize("what", LOGITS)
+@pytest.mark.parametrize("name", FORMS)
+def test_weights_of_logits_that_are_not_finite(b, name, what):
+    """attend's lse into the weights: a poisoned row is not dropped, and nothing else is touched."""
+    c = Case(name, what)
+    cache, q = c.hc.device(b, c.H, c.first), c.queries()
+    _, lse = b.attend_chunk(q, cache)
+    got = host(b.attend_weights(q, lse, cache))
+    x, mag, p, l64, bad = solve(c)
+    nan = (bad.any(2)[:, :, None] & c.seen).any(1)           # [o, t]
+    assert np.array_equal(np.isnan(got), nan)
+    p = np.where(bad[..., None], 0.0, p)
+    # lse is the kernel's own: off by at most e and its rounding, once more
+    e = 2 * S.logit_error(mag, np.where(np.isfinite(x), x, 0.0), c.C)
+    big = np.where(np.isfinite(l64), np.abs(l64), 0.0)
+    tol = np.einsum("oijt,oij->ot", p, 2 * e + (c.n * c.G + c.hc.T + 128) * 2.0 ** -23 + 16 * 2.0 ** -23 * (big + 1)) + 1e-30
+    w = p.sum((1, 2))
+    assert np.all(np.abs(got - w)[~nan] <= tol[~nan])
+
+
+@pytest.mark.parametrize("name", FORMS)
+def test_rows_without_lse_give_nothing(b, name):
+    """lse = -inf drops a row, whatever its query holds."""
+    c = Case(name, "q nan")
+    q, cache = c.queries(), c.hc.device(b, c.H, c.first)
+    zero = q.clone()
+    zero[0, c.n // 2, 0] = 0
+    _, lse = b.attend_chunk(zero, cache)
+    lse[0, c.n // 2, 0] = -float("inf")
+    got, want = b.attend_weights(q, lse, cache), b.attend_weights(zero, lse, cache)
+    assert bool(got.isfinite().all()) and np.array_equal(host(got), host(want))
