@@ -135,8 +135,9 @@ KVQ_API kvq_status kvq_attend_weights(const void* q, const float* lse, int64_t n
  *    share any of its buffers (in place); buffers that are not shared must not
  *    overlap.  The bf16 buffers are neither read nor written.  src->tq must be
  *    a multiple of block.  On success dst->tq = k * block, dst->nres = src->nres
- *    (host counters).  dst->first is written unless NULL (src->first NULL counts
- *    as zeros).  What dst holds behind its k blocks is left as it is.
+ *    (host counters).  dst->resid_rows must be at least src->nres.
+ *    dst->first is written unless NULL, which only a source without first allows
+ *    (src->first NULL counts as zeros).  What dst holds behind its k blocks is left as it is.
  *  - block: a multiple of k_params->group when keys are grouped along T, and of
  *    v_params->group when values are; >= 1.
  *  - scores_in: float32 [outer][score_stride], score_stride >= tq + nres, read;

@@ -252,6 +252,10 @@ kvq_status kvq_evict_blocks(const kvq_cache* src, kvq_cache* dst, const kvq_qpar
                      (long long)block, (long long)ps[i]->group);
     }
     if ((s = counters(src, shape))) return s;
+    // what dst must hold whatever moves: the buffered tokens' rows, and what is left of the padding
+    if (dst->resid_rows < src->nres)
+        KVQ_FAIL(KVQ_EINVAL, "dst's resid_rows (%lld) must hold the %lld buffered tokens", (long long)dst->resid_rows, (long long)src->nres);
+    if (src->first && !dst->first) KVQ_FAIL(KVQ_EINVAL, "dst needs first: the source is padded");
     if (src->tq % block != 0) KVQ_FAIL(KVQ_EINVAL, "tq (%lld) must be a multiple of block (%lld)", (long long)src->tq, (long long)block);
     if (budget < 1) KVQ_FAIL(KVQ_EINVAL, "budget must be >= 1");
     if (window < 0 || window > budget) KVQ_FAIL(KVQ_EINVAL, "window must be in [0, budget]");

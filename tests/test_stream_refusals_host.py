@@ -1,0 +1,49 @@
+"""What the streaming cache's calls refuse about pairs of caches and buffers (no
+GPU needed, no kernel launched)."""
+import pytest
+
+FAKE = 1 << 20                       # never dereferenced: validation fails first
+
+
+@pytest.fixture(scope="module")
+def kb():
+    from kv_cache_quantization_kvq_gb300 import build
+    build()
+    from kv_cache_quantization_kvq_gb300 import binding
+    return binding
+
+
+def formats(kb):
+    kw = dict(group=64, scale_dtype=kb.BF16, zero_dtype=kb.BF16)
+    return [kb.QParams.asym(4, 0, 15, axis=a, **kw) for a in (kb.ALONG_T, kb.ALONG_C)]
+
+
+def cache(kb, **kw):
+    f = dict.fromkeys(("k_codes", "k_scale", "k_zero", "k_resid", "v_codes", "v_scale", "v_zero", "v_resid"), FAKE)
+    return kb.kvq_cache(**{**f, "tq": 128, "nres": 10, "resid_rows": 64, "first": None, **kw})
+
+
+def evict(kb, src, dst, block=64, shape=(4, 128, 128)):
+    kb.kvq_evict_blocks(src, dst, *formats(kb), shape, block, 1, 0, FAKE, FAKE, 200, FAKE, FAKE, 1 << 40, 0)
+
+
+def refused(kb, status, call, *a, **kw):
+    with pytest.raises(kb.KvqError) as e:
+        call(kb, *a, **kw)
+    assert e.value.status == status, str(e.value)
+
+
+def test_a_destination_that_cannot_hold_the_result(kb):
+    """No first for a padded source; fewer buffer rows than tokens in the buffer."""
+    for dst in (cache(kb), cache(kb, first=FAKE, resid_rows=9, nres=0)):
+        refused(kb, kb.EINVAL, evict, cache(kb, first=FAKE), dst)
+        assert dst.tq == 128
+    refused(kb, kb.EINVAL, evict, cache(kb), cache(kb, resid_rows=9, nres=0))
+    refused(kb, kb.EINVAL, evict, cache(kb, nres=0), cache(kb, resid_rows=-1, nres=0))
+
+
+def objects(kb, **kw):
+    import torch
+    shape, rows = (2, 128, 128), 64
+    bufs = [tuple(torch.zeros(n, dtype=torch.uint8) for n in kb._store_sizes(shape, q, rows)) for q in formats(kb)]
+    return kb.KVCache(*bufs, shape, *formats(kb), **{**dict(tq=64, nres=3, resid_rows=rows, kv_heads=2), **kw})
