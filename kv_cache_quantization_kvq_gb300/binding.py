@@ -814,19 +814,21 @@ def evict_blocks(cache: KVCache, scores, budget: int, window: int, block: int, d
     """Keep `budget` blocks of `block` store tokens (the newest `window` and the
     best scored others) -> (dst, scores_out, keep int32 [outer, kept]).  By
     default the cache, its first and scores (CUDA float32 [outer, S >= T]) are
-    compacted in place; dst.tq and dst.nres are updated."""
+    compacted in place.  With another cache as dst (its buffered rows are the
+    caller's to copy) the source stays as it is: scores_out is then a new tensor
+    by default, and dst.first is made where the source is padded and dst has
+    none.  dst.tq and dst.nres are updated."""
     import torch
     dst = cache if dst is None else dst
-    scores_out = scores if scores_out is None else scores_out
     dev, ref, outer = scores.device, ctypes.byref, cache.shape[0]
     _want(scores, "scores", torch.float32, (outer, scores.shape[-1]), dev)
-    if scores_out is not scores:
+    if scores_out is not None and scores_out is not scores:
         _want(scores_out, "scores_out", torch.float32, tuple(scores.shape), dev)
+    if dst is not cache and (dst.shape != cache.shape or dst.kqp != cache.kqp or dst.vqp != cache.vqp or
+                             dst.kv_heads != cache.kv_heads or dst.device != cache.device):
+        raise ValueError("dst must have the cache's shape, formats, heads and device")
     if not scores.is_cuda or cache.device != dev:
         raise ValueError("scores must be a CUDA tensor on the cache's device")
-    if dst is not cache and (dst.shape != cache.shape or dst.kqp != cache.kqp or dst.vqp != cache.vqp or
-                             dst.device != dev):
-        raise ValueError("dst must have the cache's shape, formats and device")
     kept = max(0, min(int(budget), cache.tq // max(int(block), 1)))
     if keep is not None:
         _want(keep, "keep", torch.int32, (outer, kept), dev)
@@ -836,9 +838,15 @@ def evict_blocks(cache: KVCache, scores, budget: int, window: int, block: int, d
         if workspace is None:
             workspace = _temporary(_evict_ws(cache.shape, block), dev)
         ws, ws_B = _scratch(workspace, dev)
+        if scores_out is None:
+            scores_out = scores if dst is cache else torch.zeros_like(scores)
+        first = dst.first
+        if first is None and cache.first is not None:
+            first = torch.empty_like(cache.first)
         to = dst.c()
+        to.first = None if first is None else first.data_ptr()
         _check(LIB.kvq_evict_blocks(ref(cache.c()), ref(to), ref(cache.kqp._c), ref(cache.vqp._c),
                                     ref(_shape_of(cache.shape)), block, budget, window, scores.data_ptr(),
                                     scores_out.data_ptr(), scores.shape[1], keep.data_ptr(), ws, ws_B, handle))
-    dst.tq, dst.nres = to.tq, to.nres
+    dst.tq, dst.nres, dst.first = to.tq, to.nres, first
     return dst, scores_out, keep

@@ -47,3 +47,9 @@ def objects(kb, **kw):
     shape, rows = (2, 128, 128), 64
     bufs = [tuple(torch.zeros(n, dtype=torch.uint8) for n in kb._store_sizes(shape, q, rows)) for q in formats(kb)]
     return kb.KVCache(*bufs, shape, *formats(kb), **{**dict(tq=64, nres=3, resid_rows=rows, kv_heads=2), **kw})
+
+
+def test_python_refuses_a_destination_of_other_heads(kb):
+    import torch
+    with pytest.raises(ValueError, match="dst"):
+        kb.evict_blocks(objects(kb), torch.zeros((2, 200)), 1, 0, 64, dst=objects(kb, kv_heads=1))
