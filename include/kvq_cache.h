@@ -144,9 +144,11 @@ KVQ_API kvq_status kvq_attend_weights(const void* q, const float* lse, int64_t n
  *    scores_out: same shape, may be scores_in; must not overlap it otherwise.
  *  - keep: device int32 [outer][k], the kept blocks' indices in src.
  *  - budget >= 1, 0 <= window <= budget; scores must not be NULL.
- *  - formats: any that kvq_append takes, no shape limits.
+ *  - formats: any that kvq_append takes; no shape limits but 2^31 tokens or slices,
+ *    and that a grid holds a thread for every piece of 1 to 16 bytes of a block
+ *    (KVQ_EUNSUPPORTED otherwise).
  *  - workspace: at least kvq_evict_blocks_workspace bytes, 16-byte aligned.
- *  - Errors: KVQ_EINVAL, KVQ_EWORKSPACE, KVQ_ECUDA. */
+ *  - Errors: KVQ_EINVAL, KVQ_EUNSUPPORTED, KVQ_EWORKSPACE, KVQ_ECUDA. */
 KVQ_API kvq_status kvq_evict_blocks_workspace(const kvq_shape* shape, int64_t block, size_t* workspace_B);
 KVQ_API kvq_status kvq_evict_blocks(const kvq_cache* src, kvq_cache* dst, const kvq_qparams* k_params,
                                     const kvq_qparams* v_params, const kvq_shape* shape, int64_t block, int64_t budget,

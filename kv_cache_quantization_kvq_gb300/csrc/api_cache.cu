@@ -312,6 +312,7 @@ kvq_status kvq_evict_blocks(const kvq_cache* src, kvq_cache* dst, const kvq_qpar
     a.first_out = dst->first;
     a.keep = keep;
     a.ws = workspace;
+    if (!kvq::evict_fits(a)) KVQ_FAIL(KVQ_EUNSUPPORTED, "blocks of %lld tokens over %lld slices are more than a grid holds", (long long)block, (long long)outer);
     s = cuda_result(kvq::launch_evict(a, (cudaStream_t)stream), "kvq_evict_blocks launch");
     if (s != KVQ_OK) return s;
     dst->nres = src->nres;

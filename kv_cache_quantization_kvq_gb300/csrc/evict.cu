@@ -104,7 +104,7 @@ select_blocks_kernel(const EvictArgs A)
     int shift = 64;                              // key bits below `shift` are still open
     if (need > 0 && need < cand) {
         // ---- block scores: a warp takes kSumAhead blocks at a time, 32 tokens of each a step
-        for (int b0 = warp * kSumAhead; b0 < cand; b0 += kSelThreads / 32 * kSumAhead) {
+        for (uint32_t b0 = warp * kSumAhead; b0 < (uint32_t)cand; b0 += kSelThreads / 32 * kSumAhead) {
             const float* p = A.scores_in + o * A.stride + (int64_t)b0 * A.block;
             float hi[kSumAhead], lo[kSumAhead];
 #pragma unroll
@@ -114,8 +114,8 @@ select_blocks_kernel(const EvictArgs A)
 #pragma unroll
                 for (int i = 0; i < kSumAhead; ++i) {
                     const float* at = p + i * A.block + t;
-                    x[i][0] = b0 + i < cand ? at[0] : 0.0f;
-                    x[i][1] = b0 + i < cand && t + 32 < A.block ? at[32] : 0.0f;
+                    x[i][0] = b0 + i < (uint32_t)cand ? at[0] : 0.0f;
+                    x[i][1] = b0 + i < (uint32_t)cand && t + 32 < A.block ? at[32] : 0.0f;
                 }
 #pragma unroll
                 for (int i = 0; i < kSumAhead; ++i) {
@@ -130,7 +130,7 @@ select_blocks_kernel(const EvictArgs A)
                     join_to(hi[i], lo[i], __shfl_down_sync(0xFFFFFFFFu, hi[i], x), __shfl_down_sync(0xFFFFFFFFu, lo[i], x));
                 const float s = __fadd_rn(hi[i], lo[i]);             // renormalised: lo is what hi misses
                 lo[i] = __fsub_rn(lo[i], __fsub_rn(s, hi[i]));
-                if (lane == 0 && b0 + i < cand) key[b0 + i] = key_of(fabsf(hi[i]) == INFINITY || hi[i] != hi[i] ? hi[i] : s, lo[i]);
+                if (lane == 0 && b0 + i < (uint32_t)cand) key[b0 + i] = key_of(fabsf(hi[i]) == INFINITY || hi[i] != hi[i] ? hi[i] : s, lo[i]);
             }
         }
         // ---- radix search, most significant digit first
@@ -138,7 +138,7 @@ select_blocks_kernel(const EvictArgs A)
             for (int i = tid; i < 256; i += kSelThreads) hist[i] = 0;
             __syncthreads();
             const int lo = shift - 8;
-            for (int b = tid; b < cand; b += kSelThreads) {
+            for (uint32_t b = tid; b < (uint32_t)cand; b += kSelThreads) {
                 const unsigned long long k = key[b];
                 if (shift == 64 || (k >> shift) == (prefix >> shift)) atomicAdd(&hist[(int)(k >> lo) & 255], 1);
             }
@@ -182,11 +182,11 @@ select_blocks_kernel(const EvictArgs A)
     const long long pad = A.first_in ? max(A.first_in[o], 0) : 0;
     if (tid == 0) s_first = 0;
     __syncthreads();
-    for (int b0 = 0; b0 < nb; b0 += kSelThreads) {
-        const int b = b0 + tid;
+    for (uint32_t b0 = 0; b0 < (uint32_t)nb; b0 += kSelThreads) {  // past 2^31 near the most blocks there may be
+        const uint32_t b = b0 + tid;
         int above = 0, equal = 0;
-        if (b < nb) {
-            if (b >= cand || all) above = 1;
+        if (b < (uint32_t)nb) {
+            if (b >= (uint32_t)cand || all) above = 1;
             else if (!none) {
                 const unsigned long long k = key[b];
                 const unsigned long long kh = shift == 64 ? 0ull : k >> shift, ph = shift == 64 ? 0ull : prefix >> shift;
@@ -201,7 +201,7 @@ select_blocks_kernel(const EvictArgs A)
         const int at = base + cta_scan(flag, warp_sums, &total);
         base += total;
         if (flag) {
-            keep[at] = b;
+            keep[at] = (int32_t)b;
             left += (unsigned long long)min(max(pad - (long long)b * A.block, 0ll), (long long)A.block);
         }
     }
@@ -221,7 +221,7 @@ __device__ __forceinline__ void move_pieces(const char* src, char* dst, int64_t 
     if (same && part > 0) return;                // in place: one thread, in order
     const int from = same ? 0 : (int)((int64_t)kept * part / parts);
     if (!same) kept = (int)((int64_t)kept * (part + 1) / parts);
-    for (int j0 = from; j0 < kept; j0 += kAhead) {
+    for (int j0 = from; j0 < kept; j0 += kAhead) {                 // kept is at most 2^31 - 256
         V x[kAhead];
         int k[kAhead];
 #pragma unroll
@@ -289,11 +289,9 @@ move_blocks_kernel(const EvictArgs A, const MovePlan P, int64_t total)
 
 size_t evict_workspace(int64_t outer, int64_t nb_max) { return nb_max > kSharedKeys ? (size_t)(outer * nb_max) * 8 : 0; }
 
-cudaError_t launch_evict(const EvictArgs& a, cudaStream_t st)
+// The move's threads, and the CTAs that hold them; false: more than a grid does.
+static bool plan_move(const EvictArgs& a, MovePlan& P, int64_t& total, int64_t& grid)
 {
-    if (a.outer == 0) return cudaSuccess;
-    select_blocks_kernel<<<(unsigned)a.outer, kSelThreads, 0, st>>>(a);
-    MovePlan P = {};
     int64_t n = 0;
     for (int i = 0; i < kEvictBufs; ++i) {
         P.first[i] = (int32_t)n;
@@ -303,15 +301,34 @@ cudaError_t launch_evict(const EvictArgs& a, cudaStream_t st)
         const uint64_t bits = (uint64_t)(uintptr_t)b.src | (uint64_t)(uintptr_t)b.dst | (uint64_t)b.slice_B | (uint64_t)b.block_B;
         P.width[i] = bits % 16 == 0 ? 16 : bits % 4 == 0 ? 4 : bits % 2 == 0 ? 2 : 1;
         n += b.block_B / P.width[i];
+        if (n > 0x7FFFFFFF) return false;
     }
     P.first[kEvictBufs] = (int32_t)n;
-    n += a.block;
-    if (n > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+    // a thread per score column of a block; a block may be longer than an empty store's buffer
+    n += std::min(a.block, std::max<int64_t>(a.nb * a.block + a.nres, 1));
+    if (n > 0x7FFFFFFF) return false;
     P.threads = (int32_t)n;
-    const int64_t total = a.outer * n, grid = (total + kMoveThreads - 1) / kMoveThreads;
-    if (grid > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+    total = a.outer * n;
+    grid = (total + kMoveThreads - 1) / kMoveThreads;
+    return grid <= 0x7FFFFFFF;
+}
+
+bool evict_fits(const EvictArgs& a)
+{
+    MovePlan P = {};
+    int64_t total, grid;
+    return plan_move(a, P, total, grid);
+}
+
+cudaError_t launch_evict(const EvictArgs& a, cudaStream_t st)
+{
+    if (a.outer == 0) return cudaSuccess;
+    MovePlan P = {};
+    int64_t total, grid;
+    if (!plan_move(a, P, total, grid)) return cudaErrorInvalidConfiguration;
+    select_blocks_kernel<<<(unsigned)a.outer, kSelThreads, 0, st>>>(a);
     // a full GPU of threads, each with eight blocks at least (64 slices, 112 of 128 blocks: 30 us in one part)
-    const int64_t parts = std::max<int64_t>(1, std::min<int64_t>(152 * 2048 / total, a.kept / kAhead));
+    const int64_t parts = std::max<int64_t>(1, std::min<int64_t>({152 * 2048 / total, a.kept / kAhead, 65535}));
     move_blocks_kernel<<<dim3((unsigned)grid, (unsigned)parts), kMoveThreads, 0, st>>>(a, P, total);
     return cudaGetLastError();
 }

@@ -181,6 +181,7 @@ struct EvictArgs {
     void* ws;
 };
 size_t evict_workspace(int64_t outer, int64_t nb_max);
+bool evict_fits(const EvictArgs& a);                // whether a grid holds the move's threads
 cudaError_t launch_evict(const EvictArgs& a, cudaStream_t st);
 
 // make_spec of api.cu for the other API files: validates a format over a shape

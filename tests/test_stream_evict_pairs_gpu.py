@@ -1,5 +1,5 @@
 """kvq_evict_blocks between two caches: what an out-of-place call leaves alone, and
-caches that share some of their buffers."""
+caches that share some of their buffers; and shapes at the edge of the launch."""
 import numpy as np
 import pytest
 
@@ -69,3 +69,31 @@ def test_caches_that_share_some_buffers(b, which, shared):
     assert torch.equal(got[2], keep) and torch.equal(so[:, :hc.T], ws[:, :hc.T])
     for x, y in zip((*dst.k[:3], *dst.v[:3]), (*want.k[:3], *want.v[:3])):
         assert torch.equal(x, y)
+
+
+def test_a_store_without_channels(b):
+    """C = 0: only the scores move, in more parts than a grid's second dimension holds."""
+    import torch
+    T, keep = 1 << 20, (1 << 20) - 3
+    qp = b.QParams.sym(8, axis=b.ALONG_C, group=0, scale_dtype=b.F32)
+    none = (torch.zeros(0, dtype=torch.uint8, device="cuda"),) + (None,) * 3
+    cache = b.KVCache(k=none, v=none, shape=(1, T, 0), kqp=qp, vqp=qp, tq=T, nres=0, resid_rows=0)
+    dst = b.KVCache(k=none, v=none, shape=(1, T, 0), kqp=qp, vqp=qp, tq=T, nres=0, resid_rows=0)
+    sc = torch.arange(T, device="cuda", dtype=torch.float32)[None]
+    _, out, ids = b.evict_blocks(cache, sc, keep, 0, 1, dst=dst, scores_out=torch.zeros_like(sc))
+    assert torch.equal(ids[0].cpu(), torch.arange(3, T, dtype=torch.int32))
+    assert torch.equal(out[0, :keep], sc[0, 3:]) and not out[0, keep:].any()
+
+
+def test_an_empty_store_takes_any_block(b):
+    """No block at all: the buffered tokens' scores stay, whatever the block's length."""
+    import torch
+    rng = np.random.default_rng(9)
+    hc = S.HostCache(rng, 2, 128, 0, 128, 5, 64, *S.formats())
+    for block in (64, 64 << 20, 64 << 34):
+        cache = hc.device(b, 1, [0, 3])
+        sc = torch.rand((2, 9), device="cuda")
+        want = sc.clone()
+        _, out, keep = b.evict_blocks(cache, sc, 4, 1, block)
+        assert keep.shape == (2, 0) and (cache.tq, cache.nres) == (0, 5)
+        assert torch.equal(out, want) and cache.first.tolist() == [0, 3]

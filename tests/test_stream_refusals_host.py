@@ -42,6 +42,17 @@ def test_a_destination_that_cannot_hold_the_result(kb):
     refused(kb, kb.EINVAL, evict, cache(kb, nres=0), cache(kb, resid_rows=-1, nres=0))
 
 
+def test_a_block_of_more_pieces_than_a_grid_holds(kb):
+    """Refused before anything runs: the selection must not have been launched by then."""
+    T = 1 << 30
+    big = dict(tq=T, nres=0)
+    dst = cache(kb, **big)
+    with pytest.raises(kb.KvqError) as e:
+        kb.kvq_evict_blocks(cache(kb, **big), dst, *formats(kb), (1, T, 128), T, 1, 0, FAKE, FAKE, T, FAKE, FAKE, 1 << 40, 0)
+    assert e.value.status == kb.EUNSUPPORTED, str(e.value)
+    assert dst.tq == T
+
+
 def objects(kb, **kw):
     import torch
     shape, rows = (2, 128, 128), 64
