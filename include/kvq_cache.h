@@ -119,10 +119,13 @@ KVQ_API kvq_status kvq_attend_weights(const void* q, const float* lse, int64_t n
  * scales, so a block of whole groups is the smallest piece that can leave
  * without being quantized again.  With nb = tq / block, W' = min(window, nb)
  * and k = min(budget, nb), per slice:
- *     block score = sum of its tokens' scores, held as a pair of float32 whose
- *                   additions are error-free to the pair's precision (relative
- *                   error about 2^-45 of the sum of magnitudes), so exact sums
- *                   tie exactly; a sum beyond float32 is an infinity
+ *     block score = sum of its tokens' scores, held as three float32 whose
+ *                   additions are error-free, so it is exact as long as the sum
+ *                   of magnitudes is less than 2^63 of the numbers' last place
+ *                   (else off by less than block 2^-63 of it), then rounded to a
+ *                   pair of float32 (48 bits at least): equal sums
+ *                   tie, in whatever order their numbers come; a sum beyond
+ *                   float32 is an infinity
  *     keep        = the newest W' blocks and the k - W' best of the others by
  *                   (score descending, index ascending), ascending
  * (a NaN score ranks below every other).  The kept blocks become blocks

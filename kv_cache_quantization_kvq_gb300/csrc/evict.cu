@@ -5,10 +5,10 @@
 // window; "KV cache 压缩：把历史装得更小" §"少存 token：合并，或淘汰": the dropped
 // entries' K and V are freed.
 //
-// select_blocks_kernel, a CTA per slice: block scores as unevaluated sums of two
-// float32 (error-free additions: 46 bits or so; in binary64, whose units are
-// few here, the sums took 90 of 110 us for 128 slices of 32768 tokens), an
-// order-preserving 64-bit key each, a radix search for the key of the last kept
+// select_blocks_kernel, a CTA per slice: block scores as unevaluated sums of three
+// float32 (error-free additions: 63 bits at least; in binary64, whose units are
+// few here, the sums took 90 of 110 us for 128 slices of 32768 tokens), rounded to
+// a pair, an order-preserving 64-bit key each, a radix search for the key of the last kept
 // block (8 bits a pass, until the remaining bin is taken whole), ties by index,
 // and an ordered scan that writes the ascending keep list; it also counts what
 // is left of the padding.
@@ -38,26 +38,61 @@ constexpr int kSharedKeys = 2048;                // block keys held in shared me
 constexpr int kMoveThreads = 256;
 constexpr int kAhead = 8;                        // loads in flight per thread
 
-// ascending order of keys = ascending order of scores hi + lo (|lo| <= ulp(hi) / 2),
-// NaN lowest, -0 = +0
+// order_of: ascending unsigned order = ascending order of floats, -0 = +0
 __device__ __forceinline__ uint32_t order_of(float x) {
     const int b = __float_as_int(__fadd_rn(x, 0.0f));
     return b < 0 ? ~(uint32_t)b : (uint32_t)b | 0x80000000u;
 }
-__device__ __forceinline__ unsigned long long key_of(float hi, float lo) {
-    if (hi != hi) return 0ull;
-    // the sum of an infinite or overflowed block has no low part
-    return ((unsigned long long)order_of(hi) << 32) | order_of(fabsf(hi) == INFINITY ? 0.0f : lo);
+
+// ---- block scores.  A sum is hi + mid + lo, each addition error-free (Knuth's
+// two-sum) down to lo.  A lane's mid is within 17 2^-24 of the sum S of magnitudes when
+// it is renormalised every 16 numbers, what mid misses within 17 2^-48, so lo is within
+// 2^-39 and is exact as long as S is less than 2^63 of the numbers' last place; else
+// each addition is off by 2^-63 S at most.  (An infinity, a NaN or a partial sum beyond
+// the range makes NaN of mid and lo: such blocks are added again, plainly.)
+struct Sum { float hi, mid, lo; };
+
+// a = RN(a + b), b = what that misses
+__device__ __forceinline__ void two_sum(float& a, float& b) {
+    const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
+    b = __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t));
+    a = s;
 }
-// (hi, lo) += x, and (hi, lo) += (h, l): error-free sums (Knuth), the low parts rounded
-__device__ __forceinline__ void add_to(float& hi, float& lo, float x) {
-    const float s = __fadd_rn(hi, x), t = __fsub_rn(s, hi);
-    lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(hi, __fsub_rn(s, t)), __fsub_rn(x, t)));
-    hi = s;
+__device__ __forceinline__ void add_to(Sum& s, float x) {
+    two_sum(s.hi, x);
+    two_sum(s.mid, x);
+    s.lo = __fadd_rn(s.lo, x);
 }
-__device__ __forceinline__ void join_to(float& hi, float& lo, float h, float l) {
-    add_to(hi, lo, h);
-    lo = __fadd_rn(lo, l);
+__device__ __forceinline__ void normalise(Sum& s) {
+    two_sum(s.hi, s.mid);
+    two_sum(s.mid, s.lo);
+}
+__device__ __forceinline__ void join_to(Sum& s, Sum r) {
+    two_sum(s.hi, r.hi);
+    two_sum(s.mid, r.hi);
+    two_sum(s.mid, r.mid);
+    s.lo = __fadd_rn(s.lo, __fadd_rn(__fadd_rn(r.hi, r.mid), r.lo));
+}
+__device__ __forceinline__ Sum shuffled(const Sum& s, int x) {
+    return {__shfl_xor_sync(0xFFFFFFFFu, s.hi, x), __shfl_xor_sync(0xFFFFFFFFu, s.mid, x),
+            __shfl_xor_sync(0xFFFFFFFFu, s.lo, x)};
+}
+// a + b + c rounded once: the low parts are added rounding to odd, after which the
+// last rounding is right (Boldo and Melquiond).  What the first two steps leave, for a
+// second call: a + b + c = th + b + c with the new b and c.
+__device__ __forceinline__ float sum3(float& a, float& b, float& c) {
+    two_sum(b, c);
+    two_sum(a, b);
+    float u = b, v = c;
+    two_sum(u, v);
+    const uint32_t w = __float_as_uint(u);
+    if (v != 0.0f && !(w & 1u)) u = __uint_as_float((v > 0.0f) == (u > 0.0f) ? w + 1 : w - 1);
+    return __fadd_rn(a, u);
+}
+// Ascending order of keys = ascending order of scores: the sum rounded to a pair of
+// floats, RN(sum) and RN(what that misses), so equal sums have equal keys.  NaN lowest.
+__device__ __forceinline__ unsigned long long key_of(float h, float m) {
+    return h != h ? 0ull : ((unsigned long long)order_of(h) << 32) | order_of(m);
 }
 
 // exclusive prefix sum of one flag word per thread over the CTA; total in *sum
@@ -106,32 +141,58 @@ select_blocks_kernel(const EvictArgs A)
         // ---- block scores: a warp takes kSumAhead blocks at a time, 32 tokens of each a step
         for (uint32_t b0 = warp * kSumAhead; b0 < (uint32_t)cand; b0 += kSelThreads / 32 * kSumAhead) {
             const float* p = A.scores_in + o * A.stride + (int64_t)b0 * A.block;
-            float hi[kSumAhead], lo[kSumAhead];
-#pragma unroll
-            for (int i = 0; i < kSumAhead; ++i) hi[i] = lo[i] = 0.0f;
-            for (int64_t t = lane; t < A.block; t += 64) {
+            Sum sum[kSumAhead];
+            for (int64_t t = lane; t < A.block || t < 32; t += 64) {
                 float x[kSumAhead][2];
 #pragma unroll
                 for (int i = 0; i < kSumAhead; ++i) {
                     const float* at = p + i * A.block + t;
-                    x[i][0] = b0 + i < (uint32_t)cand ? at[0] : 0.0f;
+                    x[i][0] = b0 + i < (uint32_t)cand && t < A.block ? at[0] : 0.0f;
                     x[i][1] = b0 + i < (uint32_t)cand && t + 32 < A.block ? at[32] : 0.0f;
                 }
 #pragma unroll
                 for (int i = 0; i < kSumAhead; ++i) {
-                    add_to(hi[i], lo[i], x[i][0]);
-                    add_to(hi[i], lo[i], x[i][1]);
+                    if (t < 64) {                // the first two numbers of a lane
+                        sum[i] = {x[i][0], x[i][1], 0.0f};
+                        two_sum(sum[i].hi, sum[i].mid);
+                    } else {
+                        add_to(sum[i], x[i][0]);
+                        add_to(sum[i], x[i][1]);
+                        if ((t & 511) < 64) normalise(sum[i]);
+                    }
                 }
             }
+            // the lanes' sums: every step halves the blocks that a lane goes on with, so four blocks take six
+            // joins; eight lanes end with one of them each
+            static_assert(kSumAhead == 4, "two halvings");
+            const bool up = lane & 16, odd = lane & 8;
+            Sum two[2];
 #pragma unroll
-            for (int i = 0; i < kSumAhead; ++i) {
-#pragma unroll
-                for (int x = 16; x > 0; x >>= 1)
-                    join_to(hi[i], lo[i], __shfl_down_sync(0xFFFFFFFFu, hi[i], x), __shfl_down_sync(0xFFFFFFFFu, lo[i], x));
-                const float s = __fadd_rn(hi[i], lo[i]);             // renormalised: lo is what hi misses
-                lo[i] = __fsub_rn(lo[i], __fsub_rn(s, hi[i]));
-                if (lane == 0 && b0 + i < (uint32_t)cand) key[b0 + i] = key_of(fabsf(hi[i]) == INFINITY || hi[i] != hi[i] ? hi[i] : s, lo[i]);
+            for (int i = 0; i < 2; ++i) {
+                two[i] = up ? sum[i + 2] : sum[i];
+                join_to(two[i], shuffled(up ? sum[i] : sum[i + 2], 16));
             }
+            Sum one = odd ? two[1] : two[0];
+            join_to(one, shuffled(odd ? two[0] : two[1], 8));
+#pragma unroll
+            for (int x = 4; x > 0; x >>= 1) join_to(one, shuffled(one, x));
+            const int mine = (up ? 2 : 0) + (odd ? 1 : 0);
+            float h = sum3(one.hi, one.mid, one.lo), rest = __fsub_rn(one.hi, h), m = sum3(rest, one.mid, one.lo);
+            const bool fits = fabsf(h) < INFINITY && fabsf(m) < INFINITY;
+            if (!__all_sync(0xFFFFFFFFu, fits)) {
+#pragma unroll 1
+                for (int i = 0; i < kSumAhead && b0 + i < (uint32_t)cand; ++i) {
+                    float plain = 0.0f;
+                    for (int64_t t = lane; t < A.block; t += 32) plain = __fadd_rn(plain, p[i * A.block + t]);
+#pragma unroll
+                    for (int x = 16; x > 0; x >>= 1) plain = __fadd_rn(plain, __shfl_xor_sync(0xFFFFFFFFu, plain, x));
+                    if (mine == i && !fits) {
+                        h = plain;
+                        m = 0.0f;
+                    }
+                }
+            }
+            if ((lane & 7) == 0 && b0 + mine < (uint32_t)cand) key[b0 + mine] = key_of(h, m);
         }
         // ---- radix search, most significant digit first
         for (bool done = false; !done && shift > 0;) {
