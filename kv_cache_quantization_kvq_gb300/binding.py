@@ -666,6 +666,8 @@ class KVCache:
         R = min(qk.qp.residual, T)
         if tuple(qv.shape) != tuple(qk.shape) or min(qv.qp.residual, T) != R:
             raise ValueError("the key and the value cache need the same shape and residual window")
+        if R and not (qk.x_dtype == qv.x_dtype == BF16):
+            raise ValueError("the buffer of a cache holds bf16 rows: the residual window must have been kept from bf16 tensors")
         return KVCache((qk.codes, qk.scale, qk.zero, qk.resid), (qv.codes, qv.scale, qv.zero, qv.resid),
                        (outer, T - R, C), qk.qp, qv.qp, T - R, R, R, kv_heads, first)
 

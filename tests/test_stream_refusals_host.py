@@ -64,3 +64,21 @@ def test_python_refuses_a_destination_of_other_heads(kb):
     import torch
     with pytest.raises(ValueError, match="dst"):
         kb.evict_blocks(objects(kb), torch.zeros((2, 200)), 1, 0, 64, dst=objects(kb, kv_heads=1))
+
+
+def test_from_quantized_wants_a_bf16_window(kb):
+    """The buffer of a cache is bf16: a float32 window is not one, without a window the codes are all there is."""
+    import torch
+
+    def quantized(residual, x_dtype):
+        qs = [kb.QParams(p.bits, p.mode, p.qmin, p.qmax, p.axis, p.group, residual, p.scale_dtype, p.zero_dtype)
+              for p in formats(kb)]
+        return [kb.Quantized(*(torch.zeros(n, dtype=torch.uint8) for n in kb.kvq_quantized_sizes((2, 192, 128), x_dtype, p)[:4]),
+                             (2, 192, 128), p, x_dtype) for p in qs]
+    assert kb.KVCache.from_quantized(*quantized(64, kb.BF16)).T == 192
+    assert kb.KVCache.from_quantized(*quantized(0, kb.F32)).T == 192
+    with pytest.raises(ValueError, match="bf16"):
+        kb.KVCache.from_quantized(*quantized(64, kb.F32))
+    k, v = quantized(64, kb.BF16)[0], quantized(64, kb.F32)[1]
+    with pytest.raises(ValueError, match="bf16"):
+        kb.KVCache.from_quantized(k, v)
