@@ -72,8 +72,9 @@ typedef struct {
  * a logit of NaN or +inf gets NaN in all of out and in lse.
  * An infinity or NaN in v_t reaches its channel of the queries that see token t,
  * and no other query.  n = 0 does nothing.
- *  - q: bf16 [outer/kv_heads][n][kv_heads*group][C]; out: bf16, same shape;
- *    lse: float32 [outer/kv_heads][n][kv_heads*group], or NULL.
+ *  - q: bf16 [outer/kv_heads][n][kv_heads*group][C]; out: bf16, same shape, may
+ *    be q itself and must not overlap it otherwise; lse: float32
+ *    [outer/kv_heads][n][kv_heads*group], or NULL.
  *  - Logits, softmax statistics and sums are float32; the probabilities enter
  *    the value product in bf16 (relative error 2^-8 at most), out is rounded
  *    once more.  Equal calls give equal bits (no atomics).

@@ -188,6 +188,9 @@ kvq_status kvq_attend_chunk(const void* q, int64_t n, int64_t group, int64_t kv_
     kvq_status s = attend_args(q, n, group, kv_heads, cache, k_params, v_params, true, shape, a);
     if (s != KVQ_OK) return s;
     if ((s = need(out, shape->outer > 0 && n > 0, 16, "out")) || (s = need(lse, lse != nullptr, 4, "lse"))) return s;
+    // in place each row is read before it is written; shifted, another row's query would be gone
+    if (a.outer > 0 && n > 0 && partly_overlap(q, out, (size_t)(a.outer * n * group * a.C) * 2))
+        KVQ_FAIL(KVQ_EINVAL, "q and out overlap without being the same buffer");
     const size_t want = kvq::chunk_workspace(a.outer, a.C, a.cap + a.rrows, n, group);
     if ((s = check_workspace(workspace, workspace_B, want, 256, "kvq_attend_chunk"))) return s;
     return cuda_result(kvq::launch_attend_chunk(a, out, lse, workspace, (cudaStream_t)stream), "kvq_attend_chunk launch");
@@ -295,6 +298,8 @@ kvq_status kvq_evict_blocks(const kvq_cache* src, kvq_cache* dst, const kvq_qpar
         (s = need(keep, any, 4, "keep")) || (s = need(src->first, src->first != nullptr, 4, "first")) ||
         (s = need(dst->first, dst->first != nullptr, 4, "first")))
         return s;
+    if (src->first && partly_overlap(src->first, dst->first, (size_t)outer * sizeof(int32_t)))
+        KVQ_FAIL(KVQ_EINVAL, "first of src and dst overlap without being the same buffer");
     if (sc && partly_overlap(scores_in, scores_out, ((outer - 1) * score_stride + T) * sizeof(float)))
         KVQ_FAIL(KVQ_EINVAL, "scores_in and scores_out overlap without being the same buffer");
     const size_t want = kvq::evict_workspace(outer, shape->T / block);

@@ -282,3 +282,17 @@ def test_keys_and_values_of_different_kinds(b, kinds, n, bits):
     check_attend(cache, q, K, V, out, lse)
     zero = torch.zeros((B * H, hc.T), device="cuda")
     check_weights(cache, q, K, V, lse, zero, b.attend_weights(q, lse, cache))
+
+
+# a case for each form: one split, a cluster, the workspace, fused, expanded, whole tiles and a split tail
+IN_PLACE = [(2, 70, 4, 1, 128, 100), (1, 2, 4, 2, 128, 1000), (1, 2, 8, 4, 64, 9000), (1, 2, 4, 20, 128, 500),
+            (1, 2, 4, 130, 128, 400), *(c[0] for c in BOTH[:3])]
+
+
+@pytest.mark.parametrize("case", range(len(IN_PLACE)))
+def test_out_in_place_of_the_queries(b, case):
+    import torch
+    cache, q, _, _ = make(b, case, *IN_PLACE[case])
+    want, wl = b.attend_chunk(q, cache)
+    got, lse = b.attend_chunk(q, cache, out=q)
+    assert got is q and torch.equal(q.view(torch.int16), want.view(torch.int16)) and torch.equal(lse, wl)

@@ -53,6 +53,20 @@ def test_a_block_of_more_pieces_than_a_grid_holds(kb):
     assert dst.tq == T
 
 
+def test_outputs_that_overlap_the_queries(kb):
+    k, v = formats(kb)
+
+    def attend(kb, out):
+        kb.kvq_attend_chunk(FAKE, 2, 4, 2, cache(kb), k, v, (4, 128, 128), out, None, FAKE, 1 << 40, 0)
+    for out in (FAKE + 16, FAKE - 16, FAKE + 2 * 2 * 8 * 128 * 2 - 16):
+        refused(kb, kb.EINVAL, attend, out)
+
+
+def test_paddings_that_overlap(kb):
+    for at in (FAKE + 4, FAKE - 12):
+        refused(kb, kb.EINVAL, evict, cache(kb, first=FAKE), cache(kb, first=at))
+
+
 def objects(kb, **kw):
     import torch
     shape, rows = (2, 128, 128), 64
