@@ -25,9 +25,12 @@
 // its partial (m, l, y) through distributed shared memory (one launch); more go
 // through the workspace and merge_rows_kernel.  Both join in split order.
 //
-// Measured on one GB300, 4-bit codes: 64 slices x 8 heads over 8192 tokens 37 us
-// (79 MB: 2.1 TB/s), 8 x 4 over 131263 tokens 75 us; bound by the issue of the
-// unpacking (half of the slots busy), not by bytes.
+// Measured on one GB300, 4-bit codes: 64 slices x 8 heads over 8192 tokens 35.4 us
+// (79 MB: 2.2 TB/s), 8 x 4 over 131263 tokens 67 us.  At 16 warps a SM (128
+// registers) 49 % of the issue slots, 28 % of DRAM and 17 % of the tensor pipe are
+// busy: each warp waits on its chain codes -> unpacking -> scores -> weights -> values.
+// At head_dim 128 the kernels spill: 4 bits 4, 4 and 46 bytes (8, 16, 32 rows), 2 bits
+// 76, 72 and 124; at 64 none.
 #include <algorithm>
 
 #include "kvq_chunk.cuh"
@@ -74,11 +77,11 @@ __device__ __forceinline__ void add_values(float (&y)[Rows<ROWS, C>::MT][Rows<RO
     }
 }
 
-// a pair of values, made finite where they are not known to be
+// a pair of values; where they are not known to be finite, 0 in place of those that are not
 template <int BITS, bool FAST>
-__device__ __forceinline__ uint32_t value_of(uint32_t w, int sh, uint32_t mg, uint32_t s, uint32_t z, float off) {
-    const uint32_t x = value_pair<BITS, FAST>(w, sh, mg, s, z, off);
-    return FAST ? x : make_finite(x);
+__device__ __forceinline__ uint32_t value_of(uint32_t w, int sh, uint32_t mg, uint32_t s, uint32_t z, float bias) {
+    const uint32_t x = value_pair<BITS, FAST>(w, sh, mg, s, z, bias);
+    return FAST ? x : finite_or_zero(x);
 }
 
 // P.V of one 32-token batch of the store: this lane's code words of its eight
@@ -88,7 +91,7 @@ template <int BITS, int C, int ROWS, bool FAST>
 __device__ __forceinline__ void values_of(float (&y)[Rows<ROWS, C>::MT][Rows<ROWS, C>::NT][4],
                                           const uint4 (&p)[2][Rows<ROWS, C>::MT],
                                           const uint32_t (&w)[8][Geo<BITS, C>::kVW], const uint32_t* vm, uint32_t mg,
-                                          float off, int tig) {
+                                          float bias, int tig) {
     using G = Geo<BITS, C>;
     constexpr int FH = 16 / BITS;                // fields of a half word: n-tiles per half
 #pragma unroll
@@ -104,10 +107,10 @@ __device__ __forceinline__ void values_of(float (&y)[Rows<ROWS, C>::MT][Rows<ROW
             const uint32_t x1 = __byte_perm(w[4 * ks + 2][h / 2], w[4 * ks + 3][h / 2], sel);
 #pragma unroll
             for (int i = 0; i < FH; i += 2)
-                add_values<ROWS, C>(y, h * FH + i, p[ks], value_of<BITS, FAST>(x0, BITS * i, mg, s0, z0, off),
-                                    value_of<BITS, FAST>(x1, BITS * i, mg, s1, z1, off),
-                                    value_of<BITS, FAST>(x0, BITS * (i + 1), mg, s0, z0, off),
-                                    value_of<BITS, FAST>(x1, BITS * (i + 1), mg, s1, z1, off));
+                add_values<ROWS, C>(y, h * FH + i, p[ks], value_of<BITS, FAST>(x0, BITS * i, mg, s0, z0, bias),
+                                    value_of<BITS, FAST>(x1, BITS * i, mg, s1, z1, bias),
+                                    value_of<BITS, FAST>(x0, BITS * (i + 1), mg, s0, z0, bias),
+                                    value_of<BITS, FAST>(x1, BITS * (i + 1), mg, s1, z1, bias));
         }
     }
 }
@@ -210,6 +213,8 @@ __device__ __forceinline__ void softmax_of(const View& a, float (&s)[R::MT][4][4
                 const float e0 = ex2(__fmaf_rn(s[m][j][2 * h], a.scale2, neg));
                 const float e1 = ex2(__fmaf_rn(s[m][j][2 * h + 1], a.scale2, neg));
                 st.l[m][h] = __fadd_rn(st.l[m][h], __fadd_rn(e0, e1));
+                // one bf16 for the value product, whose operands are of one type: hi + lo would be a second product
+                // a fragment, for an error (2^-8 of each weight at most) of the size of out's own rounding
                 w[j][h] = pack_bf16x2(e0, e1);
             }
         }
@@ -346,7 +351,7 @@ attend_rows_kernel(const ChunkArgs A)
     for (int b = b0; b < bs; ++b) {
         const int t0 = b * kBatch, t1 = min(t0 + kBatch, a.tq);
         if (fetched != staged) {
-            kfast = stage_k_group(kr, a.koff, a.kz != nullptr, kcs[warp], lane, C / 4);
+            kfast = stage_k_group(kr, a.kbias, a.kz != nullptr, kcs[warp], lane, C / 4);
             staged = fetched;
         }
         // the V constants of this batch
@@ -354,9 +359,13 @@ attend_rows_kernel(const ChunkArgs A)
         bool vfast = fits(0) && fits(1);
         if (a.ngv > 2) vfast = vfast && fits(2) && fits(3);
         vfast = __all_sync(0xFFFFFFFFu, vfast);
+        if (!vfast) {                            // far zero points alone give finite values
+            auto bad = [&](int k) { return may_be_odd(bf_lo(vr[k]), bf_hi(vr[k])); };
+            if (__any_sync(0xFFFFFFFFu, bad(0) || bad(1) || bad(2) || bad(3))) slow |= 1;
+        }
         __syncwarp();                            // the batch before has been read
         auto stage = [&](int k) {
-            vms[warp][k][lane] = vfast ? (vr[k] & 0xFFFFu) | (biased(vr[k], 128.0f + a.voff) & 0xFFFF0000u) : vr[k];
+            vms[warp][k][lane] = vfast ? (vr[k] & 0xFFFFu) | (biased(vr[k], a.vbias) & 0xFFFF0000u) : vr[k];
         };
         stage(0);
         if (a.ngv > 1) stage(1);
@@ -371,8 +380,8 @@ attend_rows_kernel(const ChunkArgs A)
         for (int m = 0; m < MT; ++m)
 #pragma unroll
             for (int j = 0; j < 4; ++j) s[m][j][0] = s[m][j][1] = s[m][j][2] = s[m][j][3] = 0.0f;
-        if (kfast) scores_of<BITS, C, MT, true>(s, kw, qf, kcs[warp], kmg, a.koff, lane);
-        else scores_of<BITS, C, MT, false>(s, kw, qf, kcs[warp], kmg, a.koff, lane);
+        if (kfast) scores_of<BITS, C, MT, true>(s, kw, qf, kcs[warp], kmg, a.kbias, lane);
+        else scores_of<BITS, C, MT, false>(s, kw, qf, kcs[warp], kmg, a.kbias, lane);
         if (b + 1 < bs) {
             const int ba = b + kAhead;           // into L2 a few batches ahead: codes, V constants, K group constants
             if (lane < 8 && ba < bs && (ba + 1) * kBatch <= a.tq) {
@@ -397,11 +406,8 @@ attend_rows_kernel(const ChunkArgs A)
         uint4 p[2][MT];
         const bool whole = t0 >= first && t1 - t0 == kBatch && t1 - 1 <= last_lo;
         softmax_of<C, ROWS>(a, s, y, st, p, whole, t0, t1, first, last, tig);
-        if (vfast) values_of<BITS, C, ROWS, true>(y, p, vw, vm, vmg, a.voff, tig);
-        else {
-            slow |= 1;
-            values_of<BITS, C, ROWS, false>(y, p, vw, vm, vmg, a.voff, tig);
-        }
+        if (vfast) values_of<BITS, C, ROWS, true>(y, p, vw, vm, vmg, a.vbias, tig);
+        else values_of<BITS, C, ROWS, false>(y, p, vw, vm, vmg, a.vbias, tig);
         if (b + 1 < bs) load_v(b + 1);
     }
 
@@ -443,7 +449,7 @@ attend_rows_kernel(const ChunkArgs A)
 #pragma unroll
                 for (int i = 0; i < C / 16; ++i) {
                     bad[e & 1] = add_if_odd(bad[e & 1], r[e][i]);
-                    r[e][i] = make_finite(r[e][i]);
+                    r[e][i] = finite_or_zero(r[e][i]);
                 }
             if (__any_sync(0xFFFFFFFFu, (bad[0] | bad[1]) != 0u)) slow |= 2;
 #pragma unroll
@@ -673,8 +679,8 @@ rows::View cache_view(const CacheArgs& x)
     const uint32_t flip = x.bits == 4 ? 0x88888888u : 0xAAAAAAAAu;
     v.kflip = x.k_signed ? flip : 0u;
     v.vflip = x.v_signed ? flip : 0u;
-    v.koff = x.k_signed ? (float)(1 << (x.bits - 1)) : 0.0f;
-    v.voff = x.v_signed ? (float)(1 << (x.bits - 1)) : 0.0f;
+    v.kbias = 128.0f + (x.k_signed ? (float)(1 << (x.bits - 1)) : 0.0f);
+    v.vbias = 128.0f + (x.v_signed ? (float)(1 << (x.bits - 1)) : 0.0f);
     v.scale2 = (float)(1.4426950408889634 / (x.C == 128 ? 11.313708498984761 : 8.0));
     return v;
 }

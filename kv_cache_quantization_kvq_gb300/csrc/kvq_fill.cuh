@@ -32,16 +32,16 @@ __device__ __forceinline__ uint32_t load_piece(const uint8_t* p) {
 // one piece: values of fields (i, i + 4), i = 0 .. 3, with their scale and zero pairs
 template <int BITS, bool FAST>
 __device__ __forceinline__ uint4 unpack_piece(uint32_t w, uint32_t mg, const uint32_t (&s)[4], const uint32_t (&z)[4],
-                                              float off) {
+                                              float bias) {
     uint32_t r[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) r[i] = value_pair<BITS, FAST>(w, BITS * i, mg, s[i], z[i], off);
+    for (int i = 0; i < 4; ++i) r[i] = value_pair<BITS, FAST>(w, BITS * i, mg, s[i], z[i], bias);
     return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
 // Rows [rb, re) of key tile j token by token: at the padding, the store's end, in
 // the buffer (hidden and missing tokens are zeros), or with far zero points or
-// scales.  Values that are not finite are made so and noted in odd[2 C], whose next
+// scales.  Values that are not finite become 0 and are noted in odd[2 C], whose next
 // element then says so.  Kept out of line: inlined into the loops below it pushed them out of the instruction
 // cache (5.7 warps stalled on fetches per issue).
 template <int BITS, int C, bool KEYS>
@@ -49,7 +49,7 @@ __device__ __noinline__ void fill_rows(const View& a, int64_t o, int first, int 
                                        int tid, int* odd) {
     constexpr int P = C / 8, kStep = 128 / P;
     const int p = tid % P;
-    const float off = KEYS ? a.koff : a.voff;
+    const float bias = KEYS ? a.kbias : a.vbias;
     const uint32_t mg = magic<BITS>(KEYS ? a.kflip : a.vflip);
     const uint8_t* codes = (KEYS ? a.kc : a.vc) + (uint64_t)o * a.cap * (C * BITS / 8) + p * BITS;
     constexpr int kAhead = 4;                    // buffer rows in flight
@@ -83,14 +83,14 @@ __device__ __noinline__ void fill_rows(const View& a, int64_t o, int first, int 
                     s[0] = s[1] = s[2] = s[3] = bits_of(a.vs + at) * 0x10001u;
                     z[0] = z[1] = z[2] = z[3] = a.vz ? bits_of(a.vz + at) * 0x10001u : 0u;
                 }
-                y = unpack_piece<BITS, false>(load_piece<BITS>(codes + (int64_t)t * (C * BITS / 8)), mg, s, z, off);
+                y = unpack_piece<BITS, false>(load_piece<BITS>(codes + (int64_t)t * (C * BITS / 8)), mg, s, z, bias);
             }
             if constexpr (!KEYS) {
                 if (is_odd(y)) {
                     auto note = [&](uint32_t& w, int c) {           // channels c and c + 4 of the piece
                         note_odd(odd, C, p * 8 + c, w & 0xFFFFu, t);
                         note_odd(odd, C, p * 8 + c + 4, w >> 16, t);
-                        w = make_finite(w);
+                        w = finite_or_zero(w);
                     };
                     note(y.x, 0);
                     note(y.y, 1);
@@ -139,7 +139,7 @@ struct Staged {
                                       unsigned char* st, uint64_t* full, uint64_t* free, int before = 0)
         : a(v), o(slice), first(hidden), me(tid), sub(part), p(tid % P), r0(tid / P), stage(st), rfull(full), rfree(free),
           codes((KEYS ? v.kc : v.vc) + (uint64_t)slice * v.cap * kRowB), mg(magic<BITS>(KEYS ? v.kflip : v.vflip)),
-          place(tid % P / 8 * (kTile * 128) + tc::swizzled(tid / P, tid % P % 8)), bias(128.0f + (KEYS ? v.koff : v.voff)), k0(before) {
+          place(tid % P / 8 * (kTile * 128) + tc::swizzled(tid / P, tid % P % 8)), bias(KEYS ? v.kbias : v.vbias), k0(before) {
         h0 = max(2 * j0, (first + kHalf - 1) / kHalf);
         h1 = max(h0, min(2 * (j0 + n), a.tq / kHalf));
         rem = KEYS ? (int)((int64_t)mine() * kHalf % a.gk) : 0;

@@ -21,8 +21,9 @@
 // zp)), what kvq_dequantize stores (its float32 product of an 8-bit and an
 // 8-bit significand is exact).  Groups with other zero points take the
 // float32 route: subtract, multiply and round as kvq_dequantize does.
-// Four instructions a pair make the unpacking half of these kernels' work:
-// they are bound by instruction issue, not by bytes.
+// Unpacking is four instructions a pair.  The kernels are bound neither by it nor by
+// bytes (half of the issue slots and three quarters of DRAM idle) but by the latency of
+// a warp's chain of loads, unpacking and products at the warps that registers allow.
 #pragma once
 
 #include "kvq_device.cuh"
@@ -45,7 +46,7 @@ struct View {
     int32_t group, rows;                         // rows = n * group query rows of a slice
     int32_t kv_heads, gk, ngk, gv, ngv;
     uint32_t kflip, vflip;                       // turns two's complement fields into offset binary
-    float koff, voff;                            // that offset: 2^(bits-1) or 0
+    float kbias, vbias;                          // 128 + that offset, 2^(bits-1) or 0
     float scale2;                                // log2(e) / sqrt(C)
 };
 
@@ -73,9 +74,9 @@ __device__ __forceinline__ float row_value(float y, float scale) { return scale 
 __device__ __forceinline__ float row_lse(float m, float l) {
     return l == 0.0f ? -INFINITY : __fmul_rn(__fadd_rn(m, log2f(l)), 0.6931471805599453f);
 }
-// what a part's sums count in the whole: 2^(part's maximum - the whole's), 1 where both are -inf (or +inf),
-// so that a part's NaN stays
-__device__ __forceinline__ float part_scale(float m, float M) { return m == M ? 1.0f : ex2(__fsub_rn(m, M)); }
+// what a part's sums count in the whole: 2^(part's maximum - the whole's), 1 where both are -inf (or +inf), so
+// that a part's NaN stays, and never quite 0, so that its infinities do not turn into NaN
+__device__ __forceinline__ float part_scale(float m, float M) { return m == M ? 1.0f : fmaxf(ex2(__fsub_rn(m, M)), 0x1p-126f); }
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
@@ -132,18 +133,19 @@ __device__ __forceinline__ uint32_t magic(uint32_t flip) { return kOne28 | (flip
 
 // One pair of rows' values from two fields of w at bit `sh` of its halves.
 template <int BITS, bool FAST>
-__device__ __forceinline__ uint32_t value_pair(uint32_t w, int sh, uint32_t mg, uint32_t s, uint32_t z, float off) {
+__device__ __forceinline__ uint32_t value_pair(uint32_t w, int sh, uint32_t mg, uint32_t s, uint32_t z, float bias) {
     const uint32_t x = ((w >> sh) & Geo<BITS, 64>::kMask) ^ mg;
     if constexpr (FAST) return mul_bf16x2(sub_bf16x2(x, z), s);
-    const float lo = __fsub_rn(__fsub_rn((float)(x & 0xFFu), off), bf_lo(z));
-    const float hi = __fsub_rn(__fsub_rn((float)((x >> 16) & 0xFFu), off), bf_hi(z));
+    // x holds 128 + field: bias = 128 + offset comes off exactly, and nothing is converted from an integer
+    const float lo = __fsub_rn(__fsub_rn(bf_lo(x), bias), bf_lo(z));
+    const float hi = __fsub_rn(__fsub_rn(bf_hi(x), bias), bf_hi(z));
     return pack_bf16x2(__fmul_rn(lo, bf_lo(s)), __fmul_rn(hi, bf_hi(s)));
 }
 
 // ---- values that are not finite
 // A token that a row does not see has weight 0 in the row's value product, and 0
-// times NaN or infinity would be NaN there.  So the products read such values as the
-// largest finite one, and a CTA keeps per channel the first of its tokens, padding aside, that holds
+// times NaN or infinity would be NaN there.  So the products read such values as 0,
+// and a CTA keeps per channel the first of its tokens, padding aside, that holds
 // +inf or NaN (odd[c]) and the first that holds -inf or NaN (odd[C + c]); a row
 // that sees that token has the infinity added to its sum.  Only slow paths look: the
 // fast ones take constants that cannot give such a value.
@@ -164,11 +166,11 @@ __device__ __forceinline__ uint32_t add_if_odd(uint32_t acc, uint32_t w) {
 __device__ __forceinline__ bool is_odd(const uint4& x) {
     return add_if_odd(add_if_odd(0u, x.x), x.y) != 0u || add_if_odd(add_if_odd(0u, x.z), x.w) != 0u;
 }
-// a pair of bf16 with the largest finite ones in place of infinities and NaN: 0 times it is 0
-__device__ __forceinline__ uint32_t make_finite(uint32_t w) {
-    asm("max.bf16x2 %0, %0, %1;" : "+r"(w) : "r"(0xFF7FFF7Fu));
-    asm("min.bf16x2 %0, %0, %1;" : "+r"(w) : "r"(0x7F7F7F7Fu));
-    return w;
+// a pair of bf16 with 0 in place of infinities and NaN
+__device__ __forceinline__ uint32_t finite_or_zero(uint32_t w) {
+    uint32_t keep;
+    asm("set.le.u32.bf16x2 %0, %1, %2;" : "=r"(keep) : "r"(w & 0x7FFF7FFFu), "r"(0x7F7F7F7Fu));
+    return w & keep;
 }
 // notes bf16 value v of channel c and token t
 __device__ __forceinline__ void note_odd(int* odd, int C, int c, uint32_t v, int t) {
@@ -194,7 +196,7 @@ __device__ __forceinline__ void note_row(const View& a, int64_t o, int t, int* o
         } else {
             const uint32_t f = ((codes[c * BITS / 8] ^ (a.vflip & 0xFFu)) >> (c * BITS % 8)) & ((1u << BITS) - 1);
             const float z = a.vz ? bf_lo(bits_of(a.vz + meta + c / a.gv)) : 0.0f;
-            const float x = __fmul_rn(__fsub_rn(__fsub_rn((float)f, a.voff), z), bf_lo(bits_of(a.vs + meta + c / a.gv)));
+            const float x = __fmul_rn(__fsub_rn(__fsub_rn(__fadd_rn(128.0f, (float)f), a.vbias), z), bf_lo(bits_of(a.vs + meta + c / a.gv)));
             v = pack_bf16x2(x, 0.0f) & 0xFFFFu;
         }
         note_odd(odd, C, c, v, t);
@@ -256,7 +258,7 @@ __device__ __forceinline__ KRaw fetch_k_group(const View& a, int64_t o, int gk, 
 }
 // Stages them; returns whether the warp may take the bf16 route (the zero
 // pairs are then 128 + off + zp, else as stored).
-__device__ __forceinline__ bool stage_k_group(const KRaw& r, float koff, bool asym, uint4* kc, int lane, int entries) {
+__device__ __forceinline__ bool stage_k_group(const KRaw& r, float bias, bool asym, uint4* kc, int lane, int entries) {
     const uint32_t s0 = __byte_perm(r.s0, r.s1, 0x5410), s1 = __byte_perm(r.s0, r.s1, 0x7632);
     uint32_t z0 = __byte_perm(r.z0, r.z1, 0x5410), z1 = __byte_perm(r.z0, r.z1, 0x7632);
     bool ok = true;
@@ -264,8 +266,8 @@ __device__ __forceinline__ bool stage_k_group(const KRaw& r, float koff, bool as
         ok = __all_sync(0xFFFFFFFFu, zero_exact(bf_lo(z0)) && zero_exact(bf_hi(z0)) && zero_exact(bf_lo(z1)) &&
                                          zero_exact(bf_hi(z1)));
     if (ok) {
-        z0 = biased(z0, 128.0f + koff);
-        z1 = biased(z1, 128.0f + koff);
+        z0 = biased(z0, bias);
+        z1 = biased(z1, bias);
     }
     __syncwarp();                                // the group before has been read
     if (lane < entries) kc[lane] = make_uint4(s0, s1, z0, z1);
@@ -277,7 +279,7 @@ __device__ __forceinline__ bool stage_k_group(const KRaw& r, float koff, bool as
 // from the lane's code words.  qf: [mt][kk][lane] A fragments.
 template <int BITS, int C, int MT, bool FAST>
 __device__ __forceinline__ void scores_of(float (&s)[MT][4][4], const uint32_t (&w)[4][Geo<BITS, C>::kWpl],
-                                          const uint4* qf, const uint4* kc, uint32_t mg, float off, int lane) {
+                                          const uint4* qf, const uint4* kc, uint32_t mg, float bias, int lane) {
     using G = Geo<BITS, C>;
 #pragma unroll
     for (int kk = 0; kk < G::kSteps; ++kk) {
@@ -288,8 +290,8 @@ __device__ __forceinline__ void scores_of(float (&s)[MT][4][4], const uint32_t (
         const int wi = 2 * kk / (G::F / 2), sh = BITS * (2 * kk % (G::F / 2));
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const uint32_t b0 = value_pair<BITS, FAST>(w[j][wi], sh, mg, k.x, k.z, off);
-            const uint32_t b1 = value_pair<BITS, FAST>(w[j][wi], sh + BITS, mg, k.y, k.w, off);
+            const uint32_t b0 = value_pair<BITS, FAST>(w[j][wi], sh, mg, k.x, k.z, bias);
+            const uint32_t b1 = value_pair<BITS, FAST>(w[j][wi], sh + BITS, mg, k.y, k.w, bias);
 #pragma unroll
             for (int m = 0; m < MT; ++m) mma16816(s[m][j], q[m], b0, b1);
         }

@@ -12,8 +12,10 @@
 // its columns over the rows.  Each token belongs to one warp, so no sum needs an
 // atomic and its order is fixed.  Up to 64 rows; more take weights_tc.cu.
 //
-// Measured on one GB300: 64 slices x 8 heads over 8192 tokens 26 us (42 MB: 1.6
-// TB/s), bound like chunk.cu by the issue of the unpacking.
+// Measured on one GB300: 64 slices x 8 heads over 8192 tokens 21.5 us (42 MB: 1.9
+// TB/s; 26.7 us with cold caches); like chunk.cu bound by the latency of a warp's
+// chain (52 % of the issue slots, 20 % of DRAM busy at 16 warps a SM).  Spills at 2
+// bits: 92 bytes at head_dim 128, 12 at 64; at 4 bits 8 and none.
 #include <algorithm>
 
 #include "kvq_chunk.cuh"
@@ -94,7 +96,7 @@ weights_rows_kernel(const WeightArgs A)
         const bool seen = t1 > first;
         const bool store = b < sp.nsb;
         if (store && fetched != staged) {
-            kfast = stage_k_group(kr, a.koff, a.kz != nullptr, kcs[warp], lane, C / 4);
+            kfast = stage_k_group(kr, a.kbias, a.kz != nullptr, kcs[warp], lane, C / 4);
             staged = fetched;
         }
         float sum[4][2];
@@ -142,9 +144,9 @@ weights_rows_kernel(const WeightArgs A)
                         krow[j] = a.kr + ((uint64_t)o * a.rrows + (min(t0 + 8 * j + g, t1 - 1) - a.tq)) * C + tig * (C / 4);
                     scores_of_rows<BITS, C, 1>(s, krow, qt, lane);
                 } else if (kfast) {
-                    scores_of<BITS, C, 1, true>(s, kw, qt, kcs[warp], kmg, a.koff, lane);
+                    scores_of<BITS, C, 1, true>(s, kw, qt, kcs[warp], kmg, a.kbias, lane);
                 } else {
-                    scores_of<BITS, C, 1, false>(s, kw, qt, kcs[warp], kmg, a.koff, lane);
+                    scores_of<BITS, C, 1, false>(s, kw, qt, kcs[warp], kmg, a.kbias, lane);
                 }
                 add(s, t);
             }

@@ -17,11 +17,12 @@
 //     into two tensor-memory buffers, four groups of four warps, one per buffer,
 //     turn them into sums of 2^(x - lse), a token per thread;
 //  3. with several splits of the rows, join_kernel adds their sums in order.
-// Measured on one GB300: 2048 queries x 4 heads over 16384 tokens and 8 slices 240
-// us (1.07 PFLOP/s; tensor cores half busy, issue slots 61 %: a value costs one
+// Measured on one GB300: 2048 queries x 4 heads over 16384 tokens and 8 slices 238
+// us (1.08 PFLOP/s; tensor cores 52 % busy, issue slots 60 %: a value costs one
 // exponential and two packed operations).  63 queries x 4 heads over 32774 tokens
-// and 16 slices 86 us, bound by the fill; a CTA per job, its keys filled before its
-// products, took 146.
+// and 16 slices 80.5 us, bound by the latency of the fill; a CTA per job, its keys
+// filled before its products, took 146.  At 72 registers the kernel spills 124 to 136
+// bytes.
 #include <algorithm>
 
 #include <cuda.h>

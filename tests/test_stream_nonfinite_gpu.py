@@ -146,11 +146,27 @@ def v_zero(c):
     c.hc.v[2][0, c.hc.tq - 1, -1] = NEG
 
 
+def far(c):
+    """far zero points everywhere, and one value scale that is not finite"""
+    for x in (c.hc.k, c.hc.v):
+        if x[2] is not None:
+            x[2][:, :] = S.W.to_bf16_bits(S.bf16_to_f64(x[2]).astype(np.float32) + 150)
+    v_scale(INF)(c)
+
+
+def far_scale(c):
+    """scales beyond the bf16 route's, with finite values"""
+    if c.hc.v[1] is not None:
+        c.hc.v[1][0, c.hc.tq - 1] = S.W.to_bf16_bits(np.float32([3e35]))[0]
+    v_buffer(c)
+
+
 POKE = {"q nan": q_nan, "q inf": q_inf, "q all nan": q_all, "k row": k_row, "k group": k_group,
         "k inf": lambda c: key_inf(c, False), "k inf, away": lambda c: key_inf(c, True),
-        "v buffer": v_buffer, "v scale inf": v_scale(INF), "v scale nan": v_scale(NAN), "v zero": v_zero}
+        "v buffer": v_buffer, "v scale inf": v_scale(INF), "v scale nan": v_scale(NAN), "v zero": v_zero,
+        "far": far, "far scale": far_scale}
 LOGITS = ["q nan", "q inf", "q all nan", "k row", "k group", "k inf", "k inf, away"]
-VALUES = ["v buffer", "v scale inf", "v scale nan", "v zero"]
+VALUES = ["v buffer", "v scale inf", "v scale nan", "v zero", "far", "far scale"]
 
 
 def solve(c):
