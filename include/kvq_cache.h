@@ -77,7 +77,8 @@ typedef struct {
  *    [outer/kv_heads][n][kv_heads*group], or NULL.
  *  - Logits, softmax statistics and sums are float32; the probabilities enter
  *    the value product in bf16 (relative error 2^-8 at most), out is rounded
- *    once more.  Equal calls give equal bits (no atomics).
+ *    once more.  The sums are divided at the end and may carry 2^8 more than the
+ *    weights, so 2^8 T |v| must stay within float32.  Equal calls give equal bits.
  *  - Formats: K groups along T of a multiple of 32 tokens, V groups along C of
  *    32, 64 or 128 channels, both of 2 or both of 4 bits, bf16 scales,
  *    symmetric or with bf16 zero points; C = 64 or 128; group 1 .. 64
