@@ -116,11 +116,11 @@ def check_attend(cache, q, K, V, out, lse, slices=None):
         assert bool(((got - want).abs() <= to).all()), o
 
 
-def check_weights(cache, q, K, V, lse, scores, got):
+def check_weights(cache, q, K, V, lse, scores, got, slices=None):
     """lse: the float32 values that the call was given"""
     import torch
     T, rows = cache.T, q.shape[1] * q.shape[2] // cache.kv_heads
-    for o in range(cache.shape[0]):
+    for o in slices if slices is not None else range(cache.shape[0]):
         p, wl, e, _, _ = solve(cache, q, K, V, o)
         l32 = slice_rows(lse, o, cache.kv_heads).double()
         none = wl.isinf()
@@ -296,3 +296,36 @@ def test_out_in_place_of_the_queries(b, case):
     want, wl = b.attend_chunk(q, cache)
     got, lse = b.attend_chunk(q, cache, out=q)
     assert got is q and torch.equal(q.view(torch.int16), want.view(torch.int16)) and torch.equal(lse, wl)
+
+
+def test_offsets_past_32_bits(b):
+    """A store of 5.4 billion values each of K and V: every form of the three calls, the first and the last slice
+    checked."""
+    import torch
+    outer, H, T, C, block = 40, 8, 1 << 20, 128, 64
+    assert outer * T * C > 1 << 32 and outer * T * C // 2 > 1 << 31
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    kv, rows = [], []
+    for axis in (b.ALONG_T, b.ALONG_C):
+        qp = b.QParams.asym(4, 0, 15, axis=axis, group=block, scale_dtype=b.BF16, zero_dtype=b.BF16)
+        t = b.quantize(torch.randn((outer, T, C), generator=gen, device="cuda", dtype=torch.bfloat16), qp)
+        x = b.dequantize(t)
+        rows.append({o: x[o].double() for o in (0, outer - 1)})
+        kv.append(t)
+        del x
+    cache = b.KVCache.from_quantized(*kv, kv_heads=H)
+    for n, G in ((1, 4), (3, 4), (4, 8), (20, 4), (75, 4)):
+        q = (3 * torch.randn((outer // H, n, H * G, C), generator=gen, device="cuda")).bfloat16()
+        out, lse = b.attend_chunk(q, cache)
+        check_attend(cache, q, *rows, out, lse, (0, outer - 1))
+        got = b.attend_weights(q, lse, cache)
+        zero = torch.zeros((outer, T), device="cuda")
+        check_weights(cache, q, *rows, lse, zero, got, (0, outer - 1))
+    old = [t.codes.view(outer, T, C // 2)[-1].clone() for t in kv]
+    scores = torch.rand((outer, T), generator=gen, device="cuda")
+    sums = scores[-1].view(-1, block).double().sum(1)
+    keep = b.evict_blocks(cache, scores, 1000, 0, block)[2][-1].long()
+    assert torch.equal(keep, torch.sort(torch.topk(sums, 1000).indices).values)
+    tok = (keep[:, None] * block + torch.arange(block, device="cuda")).flatten()
+    for t, was in zip(kv, old):
+        assert torch.equal(t.codes.view(outer, T, C // 2)[-1, :len(tok)], was[tok])
