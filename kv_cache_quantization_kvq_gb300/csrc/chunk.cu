@@ -29,8 +29,8 @@
 // (79 MB: 2.2 TB/s), 8 x 4 over 131263 tokens 67 us.  At 16 warps a SM (128
 // registers) 49 % of the issue slots, 28 % of DRAM and 17 % of the tensor pipe are
 // busy: each warp waits on its chain codes -> unpacking -> scores -> weights -> values.
-// At head_dim 128 the kernels spill: 4 bits 4, 4 and 46 bytes (8, 16, 32 rows), 2 bits
-// 76, 72 and 124; at 64 none.
+// At head_dim 128 the kernels spill: 4 bits 12, 4 and 42 bytes (8, 16, 32 rows), 2 bits
+// 80, 52 and 124; at 64 none.
 #include <algorithm>
 
 #include "kvq_chunk.cuh"
