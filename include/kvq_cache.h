@@ -1,15 +1,23 @@
 /*
  * kvq_cache.h -- C ABI of the streaming quantized cache: attention over it for
  * any number of new tokens, the attention weight it gives every token, and
- * eviction from it by accumulated weight.
+ * eviction from it by accumulated weight; and what serving a batch of requests
+ * needs beside it: attention over packed prompts, filling a cache from them, and
+ * attention over a prefix that the requests share.
  *
- * The three calls work on the cache that kvq_append_kv fills (kvq.h): a store
+ * The first three calls work on the cache that kvq_append_kv fills (kvq.h): a store
  * of quantized tokens and a bf16 buffer of the newest ones.  A serving loop
  * runs them in this order, per layer and step:
  *     kvq_append_kv        the new tokens' K and V enter the cache;
  *     kvq_attend_chunk     their queries attend to it;
  *     kvq_attend_weights   the weight given to every token is accumulated;
  *     kvq_evict_blocks     now and then, the blocks with the least weight go.
+ * A batch of prompts of different lengths comes before that loop, per layer:
+ *     kvq_attend_prompts   their causal attention, packed, from bf16 K and V;
+ *     kvq_fill_prompts     their K and V become the cache's first tokens.
+ * Where the requests share a prefix (a system prompt, a document), it is a cache
+ * of its own, of kv_heads slices, and kvq_attend_shared takes kvq_attend_chunk's
+ * place in the loop, and follows kvq_attend_prompts, joining its results.
  *
  * Sources, cited by page title and section:
  *  [KVC] "KV cache 压缩：把历史装得更小": §"让 kernel 接住收益" (the attention
@@ -17,7 +25,8 @@
  *        (logit_t = q^T k_t / sqrt(d), y = sum_t a_t v_t), §"少存 token：合并，或淘汰"
  *        (eviction frees the dropped K/V).
  *  [FtC] "KV Compression 公式到源码对照": §3.1 cumulative attention score,
- *        §3.2 recent window union heavy hitters.
+ *        §3.2 recent window union heavy hitters; §1.1 and §1.2 scales, zero points
+ *        and codes.
  *
  * The conventions of kvq.h hold: device buffers owned by the caller, work
  * enqueued on `stream` of the current device, arguments checked on the host
@@ -159,6 +168,91 @@ KVQ_API kvq_status kvq_evict_blocks(const kvq_cache* src, kvq_cache* dst, const 
                                     const kvq_qparams* v_params, const kvq_shape* shape, int64_t block, int64_t budget,
                                     int64_t window, const float* scores_in, float* scores_out, int64_t score_stride,
                                     int32_t* keep, void* workspace, size_t workspace_B, void* stream);
+
+/* Attention of a batch over a prefix that all its requests share and over tokens
+ * of their own ([KVC] as kvq_attend_chunk):
+ *     seen(b, i) = all tokens of the prefix that are not padding, and
+ *                  { t : first[o] <= t <= T - n + i } of `cache`'s slice o = b * kv_heads + h
+ *     lse, out   as kvq_attend_chunk defines them over that union.
+ * The prefix is read once for all batch * n * group query rows of a KV head.
+ *  - prefix, shape: a cache of kv_heads slices (shape->outer = kv_heads).
+ *  - The requests' own tokens, one of:
+ *      cache, cache_shape: their cache, batch * kv_heads slices, whose newest n
+ *        tokens are the queries'; its formats may differ from the prefix's;
+ *      own_out, own_lse: what the same queries saw elsewhere, as kvq_attend_chunk
+ *        or kvq_attend_prompts wrote it (out's and lse's shapes); a row whose
+ *        own_lse is -inf saw nothing, whatever own_out holds;
+ *      neither (all NULL): the prefix alone.
+ *  - q, out: bf16 [batch][n][kv_heads*group][C]; out may be q or own_out itself and
+ *    must not overlap them otherwise; lse: float32 [batch][n][kv_heads*group], or
+ *    NULL, may be own_lse itself.
+ *  - Arithmetic, numbers that are not finite, formats, alignment and errors as
+ *    kvq_attend_chunk.  The own cache's part stays in float32 until it is joined;
+ *    own_out has been rounded to bf16 before.
+ *  - workspace: at least kvq_attend_shared_workspace(shape, resid_rows, cache_shape,
+ *    cache's resid_rows, batch, n, group) bytes, 256-byte aligned (cache_shape NULL
+ *    where there is no cache); enough for every tq and nres. */
+KVQ_API kvq_status kvq_attend_shared_workspace(const kvq_shape* shape, int64_t resid_rows, const kvq_shape* cache_shape,
+                                               int64_t cache_resid_rows, int64_t batch, int64_t n, int64_t group,
+                                               size_t* workspace_B);
+KVQ_API kvq_status kvq_attend_shared(const void* q, int64_t batch, int64_t n, int64_t group, int64_t kv_heads,
+                                     const kvq_cache* prefix, const kvq_qparams* k_params, const kvq_qparams* v_params,
+                                     const kvq_shape* shape, const kvq_cache* cache, const kvq_qparams* cache_k_params,
+                                     const kvq_qparams* cache_v_params, const kvq_shape* cache_shape,
+                                     const void* own_out, const float* own_lse, void* out, float* lse, void* workspace,
+                                     size_t workspace_B, void* stream);
+
+/* Causal attention over packed prompts, from bf16 keys and values ([KVC] as
+ * kvq_attend_chunk, before anything is quantized).  Prompt s is tokens
+ * starts[s] .. starts[s + 1] - 1 of q, k and v; token t of it sees
+ * starts[s] .. t, and query head h * group + j reads KV head h:
+ *     lse[t][h*group+j]    = log sum_u exp(q_t . k_u / sqrt(C))
+ *     out[t][h*group+j][:] = sum_u exp(q_t . k_u / sqrt(C) - lse) v_u
+ *  - q: bf16, token t's kv_heads*group heads of C channels at q + t * q_stride
+ *    (elements); k, v alike with kv_heads heads and their strides, so views of one
+ *    projection's output are taken as they are.  16-byte aligned, strides
+ *    multiples of 8 that hold a token's heads.
+ *  - starts: device int32 [prompts + 1], ascending, 0 <= starts[s] <= total, read on
+ *    the GPU: a captured call replays with the lengths it finds.  A prompt may be empty.
+ *    Whatever starts holds, nothing outside of the tensors is read or written;
+ *    prompts that are not in order or overlap give unspecified results.
+ *  - out: bf16 [total][kv_heads*group][C], may be q itself (of q_stride = kv_heads*group*C)
+ *    and must not overlap q, k or v otherwise; lse: float32 [total][kv_heads*group],
+ *    or NULL.  Rows of tokens in no prompt are left as they are.
+ *  - Arithmetic and numbers that are not finite as kvq_attend_chunk.  Equal calls
+ *    give equal bits.
+ *  - C = 64 or 128, group 1 .. 64 (KVQ_EUNSUPPORTED otherwise).
+ *  - workspace: at least kvq_attend_prompts_workspace bytes, 256-byte aligned.
+ *  - Errors: KVQ_EINVAL, KVQ_EUNSUPPORTED, KVQ_EWORKSPACE, KVQ_ECUDA. */
+KVQ_API kvq_status kvq_attend_prompts_workspace(int64_t prompts, int64_t total, int64_t group, int64_t kv_heads, int64_t C,
+                                                size_t* workspace_B);
+KVQ_API kvq_status kvq_attend_prompts(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                                      int64_t v_stride, const int32_t* starts, int64_t prompts, int64_t total,
+                                      int64_t group, int64_t kv_heads, int64_t C, void* out, float* lse, void* workspace,
+                                      size_t workspace_B, void* stream);
+
+/* Packed prompts' keys and values become the tokens of a streaming cache ([FtC]
+ * §1.1, §1.2; the layout of kvq_append_kv).  With T = tq + nres, the length the
+ * cache then has, and L_s = starts[s + 1] - starts[s], slice o = s * kv_heads + h gets
+ * the newest min(L_s, T) tokens of prompt s at positions T - L_s .. T - 1, and
+ *     first[o] = max(T - L_s, 0).
+ * Groups count the tokens that are there: a key group of which first[o] cuts off a
+ * part has its scale and zero point from the rest.  Codes, scales and zero points
+ * are those of kvq_quantize over each group's tokens.  What lies before first[o]
+ * (whole key groups, value groups, rows of codes, buffer rows) is left as it is, as
+ * is everything behind the cache's T tokens.
+ *  - k, v, strides, starts, total: as kvq_attend_prompts; no workspace.
+ *  - cache: the buffers of shape = {prompts * kv_heads, T_cap, C}; tq (a multiple of
+ *    the key group, at most T_cap) and nres (at most resid_rows) say how long it
+ *    becomes; first must not be NULL, it is written.  No buffer may overlap k or v.
+ *  - A cache that kvq_append_kv goes on with needs tq = block * max(0, (T - R) / block)
+ *    and nres = T - tq.
+ *  - Formats and alignment as kvq_attend_chunk.
+ *  - Errors: KVQ_EINVAL, KVQ_EUNSUPPORTED, KVQ_ECUDA. */
+KVQ_API kvq_status kvq_fill_prompts(const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                                    const int32_t* starts, int64_t prompts, int64_t total, int64_t kv_heads,
+                                    const kvq_cache* cache, const kvq_qparams* k_params, const kvq_qparams* v_params,
+                                    const kvq_shape* shape, void* stream);
 
 #ifdef __cplusplus
 }

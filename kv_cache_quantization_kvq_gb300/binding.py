@@ -95,6 +95,11 @@ def _load() -> ctypes.CDLL:
         "kvq_attend_weights": [vp, vp, i64, i64, i64, K, P, S, vp, vp, i64, vp, sz, vp],
         "kvq_evict_blocks_workspace": [S, i64, psz],
         "kvq_evict_blocks": [K, K, P, P, S, i64, i64, i64, vp, vp, i64, vp, vp, sz, vp],
+        "kvq_attend_shared_workspace": [S, i64, S, i64, i64, i64, i64, psz],
+        "kvq_attend_shared": [vp, i64, i64, i64, i64, K, P, P, S, K, P, P, S, vp, vp, vp, vp, vp, sz, vp],
+        "kvq_attend_prompts_workspace": [i64, i64, i64, i64, i64, psz],
+        "kvq_attend_prompts": [vp, i64, vp, i64, vp, i64, vp, i64, i64, i64, i64, i64, vp, vp, vp, sz, vp],
+        "kvq_fill_prompts": [vp, i64, vp, i64, vp, i64, i64, i64, K, P, P, S, vp],
     }
     for name, args in sig.items():
         f = getattr(lib, name)
@@ -120,7 +125,8 @@ EXPORTS = ("kvq_quantized_sizes", "kvq_quantize", "kvq_dequantize", "kvq_error_s
 
 # every symbol include/kvq_cache.h declares
 CACHE_EXPORTS = ("kvq_attend_chunk_workspace", "kvq_attend_chunk", "kvq_attend_weights_workspace",
-                 "kvq_attend_weights", "kvq_evict_blocks_workspace", "kvq_evict_blocks")
+                 "kvq_attend_weights", "kvq_evict_blocks_workspace", "kvq_evict_blocks", "kvq_attend_shared_workspace",
+                 "kvq_attend_shared", "kvq_attend_prompts_workspace", "kvq_attend_prompts", "kvq_fill_prompts")
 
 # size of the library's fixed scratch array behind kvq_error_stats_noalloc
 NOALLOC_SCRATCH_BYTES = 1 << 20
@@ -437,6 +443,49 @@ def kvq_evict_blocks(src: kvq_cache, dst: kvq_cache, kqp: QParams, vqp: QParams,
                                 _stream(stream)))
 
 
+def kvq_attend_shared_workspace(shape, resid_rows: int, cache_shape, cache_resid_rows: int, batch: int, n: int,
+                                group: int) -> int:
+    s, c, out = _shape(shape), None if cache_shape is None else _shape(cache_shape), ctypes.c_size_t()
+    _check(LIB.kvq_attend_shared_workspace(ctypes.byref(s), int(resid_rows), None if c is None else ctypes.byref(c),
+                                           int(cache_resid_rows), int(batch), int(n), int(group), ctypes.byref(out)))
+    return out.value
+
+
+def kvq_attend_shared(q, batch, n, group, kv_heads, prefix: kvq_cache, kqp: QParams, vqp: QParams, shape,
+                      cache: Optional[kvq_cache], ckqp: Optional[QParams], cvqp: Optional[QParams], cache_shape, own_out,
+                      own_lse, out, lse, workspace, workspace_B, stream=None):
+    def ref(x):
+        return None if x is None else ctypes.byref(x)
+
+    s, pk, pv = _shape(shape), kqp.c(), vqp.c()
+    cs = None if cache_shape is None else _shape(cache_shape)
+    ck, cv = (None if p is None else p.c() for p in (ckqp, cvqp))
+    _check(LIB.kvq_attend_shared(_ptr(q), int(batch), int(n), int(group), int(kv_heads), ctypes.byref(prefix), ref(pk),
+                                 ref(pv), ref(s), ref(cache), ref(ck), ref(cv), ref(cs), _ptr(own_out), _ptr(own_lse),
+                                 _ptr(out), _ptr(lse), _ptr(workspace), int(workspace_B), _stream(stream)))
+
+
+def kvq_attend_prompts_workspace(prompts: int, total: int, group: int, kv_heads: int, C: int) -> int:
+    out = ctypes.c_size_t()
+    _check(LIB.kvq_attend_prompts_workspace(int(prompts), int(total), int(group), int(kv_heads), int(C), ctypes.byref(out)))
+    return out.value
+
+
+def kvq_attend_prompts(q, q_stride, k, k_stride, v, v_stride, starts, prompts, total, group, kv_heads, C, out, lse,
+                       workspace, workspace_B, stream=None):
+    _check(LIB.kvq_attend_prompts(_ptr(q), int(q_stride), _ptr(k), int(k_stride), _ptr(v), int(v_stride), _ptr(starts),
+                                  int(prompts), int(total), int(group), int(kv_heads), int(C), _ptr(out), _ptr(lse),
+                                  _ptr(workspace), int(workspace_B), _stream(stream)))
+
+
+def kvq_fill_prompts(k, k_stride, v, v_stride, starts, prompts, total, kv_heads, cache: kvq_cache, kqp: QParams,
+                     vqp: QParams, shape, stream=None):
+    s, pk, pv = _shape(shape), kqp.c(), vqp.c()
+    _check(LIB.kvq_fill_prompts(_ptr(k), int(k_stride), _ptr(v), int(v_stride), _ptr(starts), int(prompts), int(total),
+                                int(kv_heads), ctypes.byref(cache), ctypes.byref(pk), ctypes.byref(pv), ctypes.byref(s),
+                                _stream(stream)))
+
+
 def kvq_last_error() -> str:
     return LIB.kvq_last_error().decode(errors="replace")
 
@@ -723,6 +772,8 @@ def _shape_of(shape) -> kvq_shape:
 _chunk_ws = functools.lru_cache(maxsize=1024)(kvq_attend_chunk_workspace)
 _weights_ws = functools.lru_cache(maxsize=1024)(kvq_attend_weights_workspace)
 _evict_ws = functools.lru_cache(maxsize=1024)(kvq_evict_blocks_workspace)
+_shared_ws = functools.lru_cache(maxsize=1024)(kvq_attend_shared_workspace)
+_prompts_ws = functools.lru_cache(maxsize=1024)(kvq_attend_prompts_workspace)
 
 
 def _want(t, name, dtype, shape, device):
@@ -852,3 +903,136 @@ def evict_blocks(cache: KVCache, scores, budget: int, window: int, block: int, d
                                     scores_out.data_ptr(), scores.shape[1], keep.data_ptr(), ws, ws_B, handle))
     dst.tq, dst.nres, dst.first = to.tq, to.nres, first
     return dst, scores_out, keep
+
+
+# ---- serving a batch: packed prompts, and a prefix that its requests share --------
+
+def attend_shared(q, prefix: KVCache, cache: Optional[KVCache] = None, own=None, out=None, lse=None, workspace=None,
+                  stream=None):
+    """q: CUDA bf16 [batch, n, kv_heads * group, C] -> (out bf16 like q, lse
+    float32 [batch, n, heads]): attention over a prefix that all requests share
+    (a KVCache of kv_heads slices, all of whose tokens every query sees) and over
+    the requests' own tokens: `cache`, of batch * kv_heads slices, whose newest n
+    tokens are the queries' (as attend_chunk), or own = (out, lse) of the same
+    queries from attend_chunk or attend_prompts, which out and lse may be."""
+    import torch
+    heads, C, dev, ref = prefix.kv_heads, prefix.shape[2], q.device, ctypes.byref
+    s = tuple(q.shape)
+    if len(s) != 4 or heads < 1 or prefix.shape[0] != heads or s[2] % heads or s[3] != C:
+        raise ValueError(f"q must be [batch, n, kv_heads * group, C] and the prefix a cache of kv_heads slices, with "
+                         f"kv_heads = {heads}, C = {C} (got {s} and {prefix.shape})")
+    if q.dtype != torch.bfloat16 or not q.is_contiguous() or not q.is_cuda or prefix.device != dev:
+        raise ValueError("q must be a contiguous bf16 CUDA tensor on the prefix's device")
+    batch, n, group = s[0], s[1], s[2] // heads
+    if cache is not None:
+        if own is not None:
+            raise ValueError("the requests' own tokens come as a cache or as own, not both")
+        if cache.kv_heads != heads or cache.shape[0] != batch * heads or cache.shape[2] != C or cache.device != dev:
+            raise ValueError(f"the cache must have batch * kv_heads = {batch} * {heads} slices of {C} channels on {dev}")
+    for x in (own, (out, lse)):
+        if x is not None and x[0] is not None:
+            _want(x[0], "out", torch.bfloat16, s, dev)
+        if x is not None and x[1] is not None:
+            _want(x[1], "lse", torch.float32, s[:3], dev)
+    if own is not None and (own[0] is None or own[1] is None):
+        raise ValueError("own must be (out, lse)")
+    with _On(q, stream) as handle:
+        if out is None:
+            out = torch.empty_like(q)
+        if lse is None:
+            lse = torch.empty(s[:3], dtype=torch.float32, device=dev)
+        if workspace is None:
+            workspace = _temporary(_shared_ws(prefix.shape, prefix.resid_rows, None if cache is None else cache.shape,
+                                              0 if cache is None else cache.resid_rows, batch, n, group), dev)
+        ws, ws_B = _scratch(workspace, dev)
+        mine = (None,) * 4 if cache is None else (ref(cache.c()), ref(cache.kqp._c), ref(cache.vqp._c),
+                                                  ref(_shape_of(cache.shape)))
+        given = (None, None) if own is None else (own[0].data_ptr(), own[1].data_ptr())
+        _check(LIB.kvq_attend_shared(q.data_ptr(), batch, n, group, heads, ref(prefix.c()), ref(prefix.kqp._c),
+                                     ref(prefix.vqp._c), ref(_shape_of(prefix.shape)), *mine, *given, out.data_ptr(),
+                                     lse.data_ptr(), ws, ws_B, handle))
+    return out, lse
+
+
+def _tokens(t, name, heads, C, dev):
+    """The stride between the tokens of a packed tensor [total, heads, C]."""
+    import torch
+    if t.dtype != torch.bfloat16 or not t.is_cuda or t.device != dev or t.dim() != 3 or tuple(t.shape[1:]) != (heads, C):
+        raise ValueError(f"{name} must be a CUDA bf16 tensor [total, {heads}, {C}] on {dev} (got {t.dtype} {tuple(t.shape)} "
+                         f"on {t.device})")
+    if (C > 1 and t.stride(2) != 1) or (heads > 1 and t.stride(1) != C):
+        raise ValueError(f"{name}'s heads must lie one behind the other in a token (strides {tuple(t.stride())})")
+    return t.stride(0) if t.shape[0] > 1 else heads * C
+
+
+def _prompts(starts, dev):
+    if str(starts.dtype) != "torch.int32" or starts.dim() != 1 or starts.numel() < 1 or not starts.is_contiguous() or \
+            starts.device != dev:
+        raise ValueError(f"starts must be a contiguous int32 tensor [prompts + 1] on {dev}")
+    return starts.numel() - 1
+
+
+def attend_prompts(q, k, v, starts, out=None, lse=None, workspace=None, stream=None):
+    """Causal attention over packed prompts: q CUDA bf16 [total, kv_heads * group,
+    C], k and v [total, kv_heads, C] (views of one projection's output among them),
+    starts CUDA int32 [prompts + 1] -> (out bf16 [total, kv_heads * group, C], lse
+    float32 [total, heads]).  Rows of tokens in no prompt are not written."""
+    import torch
+    dev = q.device
+    if q.dim() != 3 or k.dim() != 3 or k.shape[1] < 1 or q.shape[1] % k.shape[1] or q.shape[0] != k.shape[0] or \
+            k.shape != v.shape:
+        raise ValueError(f"q must be [total, kv_heads * group, C], k and v [total, kv_heads, C] (got {tuple(q.shape)}, "
+                         f"{tuple(k.shape)}, {tuple(v.shape)})")
+    total, heads, C = q.shape
+    kv_heads = k.shape[1]
+    strides = [_tokens(t, name, h, C, dev) for t, name, h in ((q, "q", heads), (k, "k", kv_heads), (v, "v", kv_heads))]
+    prompts, group = _prompts(starts, dev), heads // kv_heads
+    if out is not None:
+        _want(out, "out", torch.bfloat16, (total, heads, C), dev)
+    if lse is not None:
+        _want(lse, "lse", torch.float32, (total, heads), dev)
+    with _On(q, stream) as handle:
+        if out is None:
+            out = torch.empty((total, heads, C), dtype=torch.bfloat16, device=dev)
+        if lse is None:
+            lse = torch.empty((total, heads), dtype=torch.float32, device=dev)
+        if workspace is None:
+            workspace = _temporary(_prompts_ws(prompts, total, group, kv_heads, C), dev)
+        ws, ws_B = _scratch(workspace, dev)
+        _check(LIB.kvq_attend_prompts(q.data_ptr(), strides[0], k.data_ptr(), strides[1], v.data_ptr(), strides[2],
+                                      starts.data_ptr(), prompts, total, group, kv_heads, C, out.data_ptr(), lse.data_ptr(),
+                                      ws, ws_B, handle))
+    return out, lse
+
+
+def fill_prompts(k, v, starts, cache: KVCache, tokens: int, stream=None) -> KVCache:
+    """Packed prompts' keys and values (as attend_prompts takes them) become the
+    cache's tokens: `tokens` of them a slice, of which prompt s fills its newest
+    ones and the rest is padding, which cache.first counts (made if None).  As
+    after as many appends, the newest R (the formats' residual) and what does not
+    fill a block of resid_rows - R tokens stay in the buffer."""
+    import torch
+    dev, ref, heads = k.device, ctypes.byref, cache.kv_heads
+    if k.shape != v.shape or cache.device != dev:
+        raise ValueError("k and v must have one shape and lie on the cache's device")
+    total, C, prompts = k.shape[0], cache.shape[2], _prompts(starts, dev)
+    strides = [_tokens(t, name, heads, C, dev) for t, name in ((k, "k"), (v, "v"))]
+    R, tokens = cache.kqp.residual, int(tokens)
+    block = cache.resid_rows - R
+    if cache.vqp.residual != R or tokens < 0 or block < 0 or (block == 0 and tokens > R):
+        raise ValueError("the formats' residual R must be the same and resid_rows hold it and a block")
+    tq = block * max(0, (tokens - R) // block) if block else 0
+    nres = tokens - tq
+    if tq > cache.shape[1] or nres > cache.resid_rows:
+        raise ValueError(f"the cache holds {cache.shape[1]} store tokens and {cache.resid_rows} buffer rows: {tokens} tokens "
+                         f"need {tq} and {nres}")
+    with _On(k, stream) as handle:
+        first = cache.first
+        if first is None:
+            first = torch.empty(cache.shape[0], dtype=torch.int32, device=dev)
+        to = cache.c()
+        to.tq, to.nres, to.first = tq, nres, first.data_ptr() if first.numel() else None
+        _check(LIB.kvq_fill_prompts(k.data_ptr(), strides[0], v.data_ptr(), strides[1], starts.data_ptr(), prompts, total,
+                                    heads, ref(to), ref(cache.kqp._c), ref(cache.vqp._c), ref(_shape_of(cache.shape)), handle))
+    cache.tq, cache.nres, cache.first = tq, nres, first
+    return cache

@@ -167,6 +167,55 @@ bool partly_overlap(const void* a, const void* b, size_t bytes)
     return x != y && (x < y ? y - x : x - y) < bytes;
 }
 
+bool overlap(const void* a, size_t a_B, const void* b, size_t b_B)
+{
+    const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+    return a_B && b_B && x < y + b_B && y < x + a_B;
+}
+
+// Packed tokens: a tensor of `heads` heads of C channels every `stride` elements.
+size_t packed_bytes(int64_t total, int64_t stride, int64_t heads, int64_t C)
+{
+    return total == 0 ? 0 : ((size_t)(total - 1) * stride + heads * C) * 2;
+}
+kvq_status packed(const void* x, int64_t stride, int64_t total, int64_t heads, int64_t C, const char* name)
+{
+    if (stride < heads * C || stride % 8 != 0)
+        KVQ_FAIL(KVQ_EINVAL, "%s's stride (%lld) must be a multiple of 8 that holds a token's %lld elements", name, (long long)stride,
+                 (long long)(heads * C));
+    if (!mul_ok(total, stride)) KVQ_FAIL(KVQ_EINVAL, "%s too large", name);
+    return need(x, total > 0, 16, name);
+}
+kvq_status prompt_counts(int64_t prompts, int64_t total, int64_t group, int64_t kv_heads, int64_t C)
+{
+    if (prompts < 0 || total < 0) KVQ_FAIL(KVQ_EINVAL, "negative number of prompts or tokens");
+    if (group < 1 || kv_heads < 1) KVQ_FAIL(KVQ_EINVAL, "group and kv_heads must be >= 1");
+    if (C != 64 && C != 128) KVQ_FAIL(KVQ_EUNSUPPORTED, "the attention supports head_dim 64 and 128 (got %lld)", (long long)C);
+    if (group > 64) KVQ_FAIL(KVQ_EUNSUPPORTED, "the attention supports up to 64 query heads per KV head (got %lld)", (long long)group);
+    if (prompts > kMaxTokens || total > kMaxTokens || kv_heads > kMaxTokens)
+        KVQ_FAIL(KVQ_EUNSUPPORTED, "2^31 prompts, tokens or heads or more");
+    if (!mul_ok(total, kv_heads, group * C) || !mul_ok(prompts, kv_heads)) KVQ_FAIL(KVQ_EINVAL, "prompts too large");
+    return KVQ_OK;
+}
+
+// How an attend_shared call's shapes fit together.
+kvq_status shared_shapes(const kvq_shape* shape, const kvq_shape* own, int64_t batch, int64_t n, int64_t group)
+{
+    kvq_status s = queries(shape, n, group);
+    if (s != KVQ_OK) return s;
+    if (batch < 0) KVQ_FAIL(KVQ_EINVAL, "batch must be >= 0 (got %lld)", (long long)batch);
+    if (shape->outer < 1) KVQ_FAIL(KVQ_EINVAL, "the prefix needs a slice for every KV head");
+    if (batch > 0 && n > kMaxTokens / group / batch) KVQ_FAIL(KVQ_EUNSUPPORTED, "too many queries (%lld of %lld requests)", (long long)n, (long long)batch);
+    if ((s = queries(shape, batch * n, group))) return s;
+    if (!own) return KVQ_OK;
+    if ((s = queries(own, n, group))) return s;
+    if (own->C != shape->C) KVQ_FAIL(KVQ_EINVAL, "the prefix and the cache need the same head_dim");
+    if (!mul_ok(batch, shape->outer) || own->outer != batch * shape->outer)
+        KVQ_FAIL(KVQ_EINVAL, "the cache needs batch * kv_heads = %lld * %lld slices (got %lld)", (long long)batch,
+                 (long long)shape->outer, (long long)own->outer);
+    return KVQ_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -323,6 +372,134 @@ kvq_status kvq_evict_blocks(const kvq_cache* src, kvq_cache* dst, const kvq_qpar
     dst->nres = src->nres;
     dst->tq = kept * block;
     return KVQ_OK;
+}
+
+kvq_status kvq_attend_shared_workspace(const kvq_shape* shape, int64_t resid_rows, const kvq_shape* cache_shape,
+                                       int64_t cache_resid_rows, int64_t batch, int64_t n, int64_t group,
+                                       size_t* workspace_B)
+{
+    kvq_status s = shared_shapes(shape, cache_shape, batch, n, group);
+    if (s != KVQ_OK) return s;
+    if ((s = workspace_args(shape, resid_rows, n, group, workspace_B))) return s;
+    if (cache_shape && (s = workspace_args(cache_shape, cache_resid_rows, n, group, workspace_B))) return s;
+    *workspace_B = kvq::shared_workspace(shape->T + resid_rows, cache_shape ? cache_shape->T + cache_resid_rows : 0,
+                                         cache_shape != nullptr, shape->C, batch, n, group, shape->outer);
+    return KVQ_OK;
+}
+
+kvq_status kvq_attend_shared(const void* q, int64_t batch, int64_t n, int64_t group, int64_t kv_heads,
+                             const kvq_cache* prefix, const kvq_qparams* k_params, const kvq_qparams* v_params,
+                             const kvq_shape* shape, const kvq_cache* cache, const kvq_qparams* cache_k_params,
+                             const kvq_qparams* cache_v_params, const kvq_shape* cache_shape, const void* own_out,
+                             const float* own_lse, void* out, float* lse, void* workspace, size_t workspace_B, void* stream)
+{
+    kvq::CacheArgs p, c;
+    if (cache && !cache_shape) KVQ_FAIL(KVQ_EINVAL, "cache_shape must not be NULL");
+    if (!cache) cache_shape = nullptr;
+    kvq_status s = shared_shapes(shape, cache_shape, batch, n, group);
+    if (s != KVQ_OK) return s;
+    if (shape->outer != kv_heads) KVQ_FAIL(KVQ_EINVAL, "the prefix needs kv_heads = %lld slices (got %lld)", (long long)kv_heads, (long long)shape->outer);
+    if (cache && (own_out || own_lse)) KVQ_FAIL(KVQ_EINVAL, "the requests' own tokens come as a cache or as own_out and own_lse, not both");
+    if (!own_out != !own_lse) KVQ_FAIL(KVQ_EINVAL, "own_out and own_lse go together");
+    if ((s = attend_args(q, batch * n, group, kv_heads, prefix, k_params, v_params, true, shape, p))) return s;
+    if (cache && (s = attend_args(q, n, group, kv_heads, cache, cache_k_params, cache_v_params, true, cache_shape, c))) return s;
+    const bool any = batch > 0 && n > 0;
+    if ((s = need(out, any, 16, "out")) || (s = need(lse, lse != nullptr, 4, "lse")) ||
+        (s = need(own_out, own_out != nullptr, 16, "own_out")) || (s = need(own_lse, own_lse != nullptr, 4, "own_lse")))
+        return s;
+    const size_t rows = any ? (size_t)(batch * n * kv_heads * group) : 0;
+    if (any && (partly_overlap(q, out, rows * p.C * 2) || (own_out && partly_overlap(own_out, out, rows * p.C * 2))))
+        KVQ_FAIL(KVQ_EINVAL, "out overlaps q or own_out without being the same buffer");
+    if (any && lse && own_lse && partly_overlap(own_lse, lse, rows * sizeof(float)))
+        KVQ_FAIL(KVQ_EINVAL, "own_lse and lse overlap without being the same buffer");
+    const size_t want = kvq::shared_workspace(p.cap + p.rrows, cache ? c.cap + c.rrows : 0, cache != nullptr, p.C, batch, n,
+                                              group, kv_heads);
+    if ((s = check_workspace(workspace, workspace_B, want, 256, "kvq_attend_shared"))) return s;
+    return cuda_result(kvq::launch_attend_shared(p, cache ? &c : nullptr, own_out, own_lse, batch, n, out, lse, workspace,
+                                                 (cudaStream_t)stream),
+                       "kvq_attend_shared launch");
+}
+
+kvq_status kvq_attend_prompts_workspace(int64_t prompts, int64_t total, int64_t group, int64_t kv_heads, int64_t C,
+                                        size_t* workspace_B)
+{
+    const kvq_status s = prompt_counts(prompts, total, group, kv_heads, C);
+    if (s != KVQ_OK) return s;
+    if (!workspace_B) KVQ_FAIL(KVQ_EINVAL, "workspace_B must not be NULL");
+    *workspace_B = kvq::prompts_workspace(prompts, total, group, kv_heads, C);
+    return KVQ_OK;
+}
+
+kvq_status kvq_attend_prompts(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                              int64_t v_stride, const int32_t* starts, int64_t prompts, int64_t total, int64_t group,
+                              int64_t kv_heads, int64_t C, void* out, float* lse, void* workspace, size_t workspace_B,
+                              void* stream)
+{
+    kvq_status s = prompt_counts(prompts, total, group, kv_heads, C);
+    if (s != KVQ_OK) return s;
+    const int64_t heads = group * kv_heads;
+    if ((s = packed(q, q_stride, total, heads, C, "q")) || (s = packed(k, k_stride, total, kv_heads, C, "k")) ||
+        (s = packed(v, v_stride, total, kv_heads, C, "v")) || (s = need(starts, true, 4, "starts")) ||
+        (s = need(out, total > 0, 16, "out")) || (s = need(lse, lse != nullptr, 4, "lse")))
+        return s;
+    const size_t out_B = (size_t)(total * heads * C) * 2;
+    const bool in_place = out == q && q_stride == heads * C;
+    if ((!in_place && overlap(out, out_B, q, packed_bytes(total, q_stride, heads, C))) ||
+        overlap(out, out_B, k, packed_bytes(total, k_stride, kv_heads, C)) ||
+        overlap(out, out_B, v, packed_bytes(total, v_stride, kv_heads, C)))
+        KVQ_FAIL(KVQ_EINVAL, "out overlaps q, k or v");
+    const size_t want = kvq::prompts_workspace(prompts, total, group, kv_heads, C);
+    if ((s = check_workspace(workspace, workspace_B, want, 256, "kvq_attend_prompts"))) return s;
+    const kvq::PromptArgs a = {q, k, v, q_stride, k_stride, v_stride, starts, prompts, total, group, kv_heads, C, out, lse};
+    return cuda_result(kvq::launch_attend_prompts(a, workspace, (cudaStream_t)stream), "kvq_attend_prompts launch");
+}
+
+kvq_status kvq_fill_prompts(const void* k, int64_t k_stride, const void* v, int64_t v_stride, const int32_t* starts,
+                            int64_t prompts, int64_t total, int64_t kv_heads, const kvq_cache* cache,
+                            const kvq_qparams* k_params, const kvq_qparams* v_params, const kvq_shape* shape, void* stream)
+{
+    if (!cache) KVQ_FAIL(KVQ_EINVAL, "cache must not be NULL");
+    if (!shape) KVQ_FAIL(KVQ_EINVAL, "shape must not be NULL");
+    kvq_status s = prompt_counts(prompts, total, 1, kv_heads, shape->C);
+    if (s != KVQ_OK) return s;
+    if (shape->outer != prompts * kv_heads)
+        KVQ_FAIL(KVQ_EINVAL, "the cache needs prompts * kv_heads = %lld slices (got %lld)", (long long)(prompts * kv_heads),
+                 (long long)shape->outer);
+    if ((s = packed(k, k_stride, total, kv_heads, shape->C, "k")) || (s = packed(v, v_stride, total, kv_heads, shape->C, "v")) ||
+        (s = need(starts, true, 4, "starts")))
+        return s;
+    kvq::CacheArgs c;
+    if ((s = attend_args(nullptr, 0, 1, kv_heads, cache, k_params, v_params, true, shape, c))) return s;
+    if ((s = need(cache->first, true, 4, "first"))) return s;
+    if (cache->tq % k_params->group != 0)
+        KVQ_FAIL(KVQ_EINVAL, "tq (%lld) must be a multiple of the key group (%lld)", (long long)cache->tq, (long long)k_params->group);
+    kvq::FillArgs a = {};
+    a.k = {k, k_stride, cache->k_codes, cache->k_scale, cache->k_zero, cache->k_resid, {}};
+    a.v = {v, v_stride, cache->v_codes, cache->v_scale, cache->v_zero, cache->v_resid, {}};
+    if ((s = store_format(shape, k_params, a.k.q)) || (s = store_format(shape, v_params, a.v.q))) return s;
+    const size_t in_B[2] = {packed_bytes(total, k_stride, kv_heads, c.C), packed_bytes(total, v_stride, kv_heads, c.C)};
+    for (int i = 0; i < 2; ++i) {
+        const kvq::FillStore& f = i ? a.v : a.k;
+        const size_t row_B = (size_t)(c.C * f.q.bits / 8), cells = f.q.axis == KVQ_GROUP_ALONG_T ? (size_t)(f.q.ngroups * c.C)
+                                                                                                : (size_t)(c.cap * f.q.ngroups);
+        const void* to[4] = {f.codes, f.scale, f.q.mode == KVQ_ASYM ? f.zero : nullptr, f.resid};
+        const size_t to_B[4] = {(size_t)c.outer * c.cap * row_B, (size_t)c.outer * cells * 2, (size_t)c.outer * cells * 2,
+                                (size_t)c.outer * c.rrows * c.C * 2};
+        for (int m = 0; m < 4; ++m)
+            if (to[m] && (overlap(to[m], to_B[m], k, in_B[0]) || overlap(to[m], to_B[m], v, in_B[1])))
+                KVQ_FAIL(KVQ_EINVAL, "the cache's buffers overlap k or v");
+    }
+    a.starts = starts;
+    a.first = cache->first;
+    a.prompts = prompts;
+    a.total = total;
+    a.kv_heads = kv_heads;
+    a.C = c.C;
+    a.cap = c.cap;
+    a.tq = cache->tq;
+    a.nres = cache->nres;
+    a.rrows = cache->resid_rows;
+    return cuda_result(kvq::launch_fill_prompts(a, (cudaStream_t)stream), "kvq_fill_prompts launch");
 }
 
 }  // extern "C"

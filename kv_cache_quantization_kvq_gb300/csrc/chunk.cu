@@ -136,10 +136,16 @@ __device__ __forceinline__ float4 remote_f4(const void* p, int rank) {
     return v;
 }
 
-// out (4 channels) and, with the row's first channels, lse
+// out (4 channels) and, with the row's first channels, lse; or the row's sums
 template <int C>
 __device__ __forceinline__ void write_row(const ChunkArgs& A, int64_t o, int r, int c4, float M, float L, const float (&v)[4]) {
     const int64_t at = row_index(A.v, o, r);
+    if (A.sums) {
+        float* dst = A.sums + at * (C + 4);
+        *reinterpret_cast<float4*>(dst + c4) = make_float4(v[0], v[1], v[2], v[3]);
+        if (c4 == 0) *reinterpret_cast<float2*>(dst + C) = make_float2(M, L);
+        return;
+    }
     const float inv = row_scale(L);
     *reinterpret_cast<uint2*>(A.out + at * C + c4) =
         make_uint2(pack_bf16x2(row_value(v[0], inv), row_value(v[1], inv)),
@@ -530,7 +536,7 @@ attend_rows_kernel(const ChunkArgs A)
                     gm[row] = M;
                     gl[row] = L;
                 }
-            } else if (A.nsplit > 1) {
+            } else if (A.parts) {
                 float* dst = A.part + ((o * a.rows + r) * A.nsplit + split) * (C + 4);
                 *reinterpret_cast<float4*>(dst + c4) = make_float4(v[0], v[1], v[2], v[3]);
                 if (c4 == 0) *reinterpret_cast<float2*>(dst + C) = make_float2(M, L);
@@ -591,14 +597,14 @@ bool cluster_ok(int64_t outer, int64_t s, int64_t slots) { return s > 1 && s <= 
 // Up to 2048 tokens of few slices the splits stay within a cluster: no workspace.
 bool short_cache(int64_t outer, int64_t T, int64_t slots) { return T <= 2048 && cluster_ok(outer, kCluster, slots); }
 
-RowsPlan rows_plan(int64_t outer, int64_t T, int64_t rows)
+RowsPlan rows_plan(int64_t outer, int64_t T, int64_t rows, bool shared)
 {
     const int64_t slots = slots_of(rows), nb = (T + kBatch - 1) / kBatch + 1;
     const int64_t most = short_cache(outer, T, slots) ? kCluster : nb;
     RowsPlan p = {1, false};
     int64_t best = INT64_MAX;
     for (int64_t s = 1; s == 1 || (outer * s <= kMaxWaves * slots && s * kWarps <= nb && s <= most); ++s) {
-        const bool cluster = cluster_ok(outer, s, slots);
+        const bool cluster = !shared && cluster_ok(outer, s, slots);
         const int64_t cost = ((outer * s + slots - 1) / slots) * ((nb + s * kWarps - 1) / (s * kWarps) + 3) +
                              (s > 1 && !cluster ? 3 : 0);
         if (cost < best) {
@@ -612,8 +618,9 @@ RowsPlan rows_plan(int64_t outer, int64_t T, int64_t rows)
 template <int BITS, int C>
 cudaError_t launch_rows(ChunkArgs A, int64_t outer, cudaStream_t st)
 {
-    const RowsPlan p = rows_plan(outer, A.v.T, A.v.rows);
+    const RowsPlan p = rows_plan(outer, A.v.T, A.v.rows, A.shared);
     A.nsplit = (int32_t)p.nsplit;
+    A.parts = p.nsplit > 1 || A.shared;
     const int64_t grid = outer * p.nsplit;
     if (grid > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
     A.cluster = p.cluster;
@@ -630,7 +637,7 @@ cudaError_t launch_rows(ChunkArgs A, int64_t outer, cudaStream_t st)
                           : A.v.rows <= 16 ? cudaLaunchKernelEx(&cfg, attend_rows_kernel<BITS, C, 16>, A)
                                            : cudaLaunchKernelEx(&cfg, attend_rows_kernel<BITS, C, 32>, A);
     if (e != cudaSuccess) return e;
-    if (p.nsplit > 1 && !p.cluster) {
+    if (A.parts && !p.cluster) {
         const int64_t total = outer * A.v.rows;
         merge_rows_kernel<C><<<(unsigned)((total + kWarps - 1) / kWarps), kThreads, 0, st>>>(A, total);
     }
@@ -639,15 +646,17 @@ cudaError_t launch_rows(ChunkArgs A, int64_t outer, cudaStream_t st)
 
 }  // namespace
 
-size_t chunk_workspace(int64_t outer, int64_t C, int64_t tmax, int64_t n, int64_t group)
+size_t chunk_workspace(int64_t outer, int64_t C, int64_t tmax, int64_t n, int64_t group, bool shared)
 {
     const int64_t rows = n * group;
     if (outer == 0 || rows == 0) return 0;
-    if (chunk_uses_tc(rows)) return chunk_tc_workspace(outer, C, tmax, rows);
+    if (chunk_uses_tc(rows)) return chunk_tc_workspace(outer, C, tmax, rows, shared);
     // every T up to tmax may choose its splits: at most kMaxWaves of CTAs, or one per four batches
     const int64_t slots = slots_of(rows), most = (tmax + kBatch - 1) / kBatch + 1;
-    if (short_cache(outer, tmax, slots) || most / kWarps <= 1) return 0;
-    return (size_t)(std::min(kMaxWaves * slots, outer * (most / kWarps)) * rows * (C + 4)) * sizeof(float);
+    if (!shared && (short_cache(outer, tmax, slots) || most / kWarps <= 1)) return 0;
+    int64_t ctas = std::min(kMaxWaves * slots, outer * (most / kWarps));
+    if (shared) ctas = std::max(ctas, outer);
+    return (size_t)(ctas * rows * (C + 4)) * sizeof(float);
 }
 
 rows::View cache_view(const CacheArgs& x)
@@ -671,6 +680,8 @@ rows::View cache_view(const CacheArgs& x)
     v.n = (int32_t)x.n;
     v.group = (int32_t)x.group;
     v.rows = (int32_t)(x.n * x.group);
+    v.qn = v.n;
+    v.qgroup = v.group;
     v.kv_heads = (int32_t)x.kv_heads;
     v.gk = x.gk;
     v.ngk = (int32_t)((x.cap + x.gk - 1) / x.gk);
@@ -685,17 +696,22 @@ rows::View cache_view(const CacheArgs& x)
     return v;
 }
 
+cudaError_t launch_chunk(ChunkArgs A, int bits, int64_t C, int64_t outer, void* ws, cudaStream_t st)
+{
+    A.part = static_cast<float*>(ws);
+    if (chunk_uses_tc(A.v.rows)) return launch_attend_tc(A, bits, C, outer, ws, st);
+    if (bits == 4) return C == 128 ? launch_rows<4, 128>(A, outer, st) : launch_rows<4, 64>(A, outer, st);
+    return C == 128 ? launch_rows<2, 128>(A, outer, st) : launch_rows<2, 64>(A, outer, st);
+}
+
 cudaError_t launch_attend_chunk(const CacheArgs& x, void* out, float* lse, void* ws, cudaStream_t st)
 {
     if (x.outer == 0 || x.n == 0) return cudaSuccess;
-    ChunkArgs A;
+    ChunkArgs A = {};
     A.v = cache_view(x);
     A.out = static_cast<__nv_bfloat16*>(out);
     A.lse = lse;
-    A.part = static_cast<float*>(ws);
-    if (chunk_uses_tc(A.v.rows)) return launch_attend_tc(A, x.bits, x.C, x.outer, ws, st);
-    if (x.bits == 4) return x.C == 128 ? launch_rows<4, 128>(A, x.outer, st) : launch_rows<4, 64>(A, x.outer, st);
-    return x.C == 128 ? launch_rows<2, 128>(A, x.outer, st) : launch_rows<2, 64>(A, x.outer, st);
+    return launch_chunk(A, x.bits, x.C, x.outer, ws, st);
 }
 
 }  // namespace kvq

@@ -13,29 +13,39 @@ struct ChunkArgs {
     __nv_bfloat16* out;
     float* lse;              // or nullptr
     float* part;             // [row][split][C + 4]: y, m, l
+    float* sums;             // [row_index][C + 4]: the same of whole rows, in place of out and lse; or nullptr
     int32_t nsplit, ntiles, cluster;
+    int32_t parts;           // whether results go to part and are joined later: nsplit > 1, or shared
+    // shared: a launch over tokens that every row sees, to be joined with what the rows
+    // have seen elsewhere: own_sums as `sums` holds it, or (own_out, own_lse), or nothing
+    int32_t shared;
+    const float* own_sums;
+    const __nv_bfloat16* own_out;
+    const float* own_lse;
 };
 
 rows::View cache_view(const CacheArgs& x);
 
-// One warp joins the splits' (y, m, l) of query row r of slice o, in split order.
+// One warp takes the largest m of a row's splits, and adds up the splits' y
+// (channels N lane + i) and l, scaled to the maximum M of the whole, in split order.
 template <int C>
-__device__ __forceinline__ void merge_row(const ChunkArgs& A, int64_t o, int r, const float* p, int lane) {
-    using namespace rows;
+__device__ __forceinline__ float parts_max(const float* p, int nsplit, int lane) {
     float M = -INFINITY;
-    for (int s = lane; s < A.nsplit; s += 32) M = fmaxf(M, p[(int64_t)s * (C + 4) + C]);
+    for (int s = lane; s < nsplit; s += 32) M = fmaxf(M, p[(int64_t)s * (C + 4) + C]);
 #pragma unroll
     for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, x));
+    return M;
+}
+template <int C>
+__device__ __forceinline__ void add_parts(const float* p, int nsplit, int lane, float M, float& L, float (&v)[C / 32]) {
+    using namespace rows;
     constexpr int N = C / 32;
-    float L = 0.0f, v[N];
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = 0.0f;
     // What each split counts is worked out a split per lane, and the outputs are loaded kJoin splits at a time: as a
     // plain loop over the splits the loads wait for one another (one token of 8 slices x 4 heads over 131263 tokens:
     // 73.3 us with it, 66.6 so).
     constexpr int kJoin = 8;
-    for (int s0 = 0; s0 < A.nsplit; s0 += 32) {
-        const int n = min(32, A.nsplit - s0);
+    for (int s0 = 0; s0 < nsplit; s0 += 32) {
+        const int n = min(32, nsplit - s0);
         const float* ps = p + (int64_t)s0 * (C + 4);
         float l = 0.0f, f = 0.0f;
         if (lane < n) {
@@ -68,20 +78,68 @@ __device__ __forceinline__ void merge_row(const ChunkArgs& A, int64_t o, int r, 
             }
         }
     }
-    const int64_t at = row_index(A.v, o, r);
+}
+// the row with maximum M and sums L and v: out and lse
+template <int C>
+__device__ __forceinline__ void write_joined(__nv_bfloat16* out, float* lse, int64_t at, int lane, float M, float L,
+                                             const float (&v)[C / 32]) {
+    using namespace rows;
+    constexpr int N = C / 32;
     const float inv = row_scale(L);
     uint32_t w[N / 2];
 #pragma unroll
     for (int i = 0; i < N / 2; ++i) w[i] = pack_bf16x2(row_value(v[2 * i], inv), row_value(v[2 * i + 1], inv));
-    if constexpr (N == 4) *reinterpret_cast<uint2*>(A.out + at * C + 4 * lane) = make_uint2(w[0], w[1]);
-    else *reinterpret_cast<uint32_t*>(A.out + at * C + 2 * lane) = w[0];
-    if (A.lse && lane == 0)
-        A.lse[at] = row_lse(M, L);
+    if constexpr (N == 4) *reinterpret_cast<uint2*>(out + at * C + 4 * lane) = make_uint2(w[0], w[1]);
+    else *reinterpret_cast<uint32_t*>(out + at * C + 2 * lane) = w[0];
+    if (lse && lane == 0)
+        lse[at] = row_lse(M, L);
+}
+
+// One warp joins the splits' (y, m, l) of query row r of slice o.
+template <int C>
+__device__ __forceinline__ void merge_row(const ChunkArgs& A, int64_t o, int r, const float* p, int lane) {
+    constexpr int N = C / 32;
+    float M = parts_max<C>(p, A.nsplit, lane), L = 0.0f, v[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = 0.0f;
+    const int64_t at = rows::row_index(A.v, o, r);
+    if (A.own_sums) {
+        const float* own = A.own_sums + at * (C + 4);
+        M = fmaxf(M, own[C]);
+        add_parts<C>(own, 1, lane, M, L, v);
+    } else if (A.own_lse) {
+        // weights that sum to 1 at the maximum lse; -inf: nothing was seen, NaN: nothing else comes out
+        const float lse = A.own_lse[at], m = __fmul_rn(lse, rows::kLog2e);
+        M = fmaxf(M, m);
+        if (lse != -INFINITY) {
+            const float f = rows::part_scale(m, M);
+            L = lse != lse ? lse : f;
+#pragma unroll
+            for (int i = 0; i < N; i += 2) {
+                const uint32_t w = *reinterpret_cast<const uint32_t*>(A.own_out + at * C + N * lane + i);
+                v[i] = __fmul_rn(rows::bf_lo(w), f);
+                v[i + 1] = __fmul_rn(rows::bf_hi(w), f);
+            }
+        }
+    }
+    add_parts<C>(p, A.nsplit, lane, M, L, v);
+    if (A.sums) {
+        float* dst = A.sums + at * (C + 4);
+#pragma unroll
+        for (int i = 0; i < C / 32; i += 2)
+            *reinterpret_cast<float2*>(dst + C / 32 * lane + i) = make_float2(v[i], v[i + 1]);
+        if (lane == 0) *reinterpret_cast<float2*>(dst + C) = make_float2(M, L);
+    } else {
+        write_joined<C>(A.out, A.lse, at, lane, M, L, v);
+    }
 }
 
 bool chunk_uses_tc(int64_t rows);
-size_t chunk_tc_workspace(int64_t outer, int64_t C, int64_t tmax, int64_t rows);
+size_t chunk_tc_workspace(int64_t outer, int64_t C, int64_t tmax, int64_t rows, bool shared);
 cudaError_t launch_attend_tc(const ChunkArgs& A, int bits, int64_t C, int64_t outer, void* ws, cudaStream_t st);
+
+// The attention of kvq_attend_chunk over a cache, its rows into A.out and A.lse or into A.sums.
+cudaError_t launch_chunk(ChunkArgs A, int bits, int64_t C, int64_t outer, void* ws, cudaStream_t st);
 
 // the same for kvq_attend_weights (weights_tc.cu)
 bool weights_use_tc(int64_t rows);

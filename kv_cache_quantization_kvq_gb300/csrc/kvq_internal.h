@@ -155,11 +155,44 @@ struct CacheArgs {
     int32_t k_asym, v_asym;         // bf16 zero points present
     int32_t k_signed, v_signed;     // two's complement codes
 };
-size_t chunk_workspace(int64_t outer, int64_t C, int64_t tmax, int64_t n, int64_t group);
+size_t chunk_workspace(int64_t outer, int64_t C, int64_t tmax, int64_t n, int64_t group, bool shared = false);
 cudaError_t launch_attend_chunk(const CacheArgs& a, void* out, float* lse, void* ws, cudaStream_t st);
 size_t weights_workspace(int64_t outer, int64_t C, int64_t n, int64_t group);
 cudaError_t launch_attend_weights(const CacheArgs& a, const float* lse, const float* scores_in, float* scores_out,
                                   int64_t stride, void* ws, cudaStream_t st);
+
+// ---- serving a batch (kvq_cache.h): a prefix shared by all requests, packed prompts
+// prefix: outer = kv_heads, n = batch * n queries; own: the requests' caches, or nullptr
+size_t shared_workspace(int64_t prefix_tmax, int64_t own_tmax, bool own, int64_t C, int64_t batch, int64_t n, int64_t group,
+                        int64_t kv_heads);
+cudaError_t launch_attend_shared(const CacheArgs& prefix, const CacheArgs* own, const void* own_out, const float* own_lse,
+                                 int64_t batch, int64_t n, void* out, float* lse, void* ws, cudaStream_t st);
+
+struct PromptArgs {
+    const void *q, *k, *v;          // bf16, a token every *_stride elements, its heads contiguous
+    int64_t q_stride, k_stride, v_stride;
+    const int32_t* starts;          // [prompts + 1]
+    int64_t prompts, total, group, kv_heads, C;
+    void* out;                      // bf16 [total][kv_heads * group][C]
+    float* lse;                     // [total][kv_heads * group] or nullptr
+};
+size_t prompts_workspace(int64_t prompts, int64_t total, int64_t group, int64_t kv_heads, int64_t C);
+cudaError_t launch_attend_prompts(const PromptArgs& a, void* ws, cudaStream_t st);
+
+// One of the two stores that prompts fill.
+struct FillStore {
+    const void* x;                  // bf16 [total], a token every `stride` elements
+    int64_t stride;
+    void *codes, *scale, *zero, *resid;
+    QSpec q;                        // over [outer, cap, C]
+};
+struct FillArgs {
+    FillStore k, v;
+    const int32_t* starts;
+    int32_t* first;                 // [outer]
+    int64_t prompts, total, kv_heads, C, cap, tq, nres, rrows;
+};
+cudaError_t launch_fill_prompts(const FillArgs& a, cudaStream_t st);
 
 // One buffer of a store as eviction sees it: block b of slice o is the
 // `block_B` bytes at slice o * slice_B + b * block_B.

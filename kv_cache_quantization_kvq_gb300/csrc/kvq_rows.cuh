@@ -43,7 +43,8 @@ struct View {
     const int32_t* first;
     int64_t cap, rrows;
     int32_t tq, nres, T, n;
-    int32_t group, rows;                         // rows = n * group query rows of a slice
+    int32_t group, rows;                         // rows = n * group query rows of a slice: row r sees tokens up to T - n + r / group
+    int32_t qn, qgroup;                          // where they lie: n and group, but for rows that all see every token (n = 1, group = rows)
     int32_t kv_heads, gk, ngk, gv, ngv;
     uint32_t kflip, vflip;                       // turns two's complement fields into offset binary
     float kbias, vbias;                          // 128 + that offset, 2^(bits-1) or 0
@@ -342,9 +343,9 @@ __device__ __forceinline__ int batch_of(const View& a, const Span& s, int t) {
 
 // query row r of slice o: index of its q row (times C) and of its lse
 __device__ __forceinline__ int64_t row_index(const View& a, int64_t o, int r) {
-    const int i = r / a.group, j = r - i * a.group;
+    const int i = r / a.qgroup, j = r - i * a.qgroup;
     const uint32_t b = (uint32_t)o / (uint32_t)a.kv_heads, h = (uint32_t)o - b * (uint32_t)a.kv_heads;
-    return ((int64_t)b * a.n + i) * ((int64_t)a.kv_heads * a.group) + (int64_t)h * a.group + j;
+    return ((int64_t)b * a.qn + i) * ((int64_t)a.kv_heads * a.qgroup) + (int64_t)h * a.qgroup + j;
 }
 
 // A fragments of query rows [r0, r0 + 16 MT) of slice o, made by the whole CTA

@@ -147,12 +147,14 @@ struct TcArgs {
 // The query tile and split of a CTA.
 struct TileOf {
     int tile, split, nsplit, r0, nrows, nt;      // tile of up to 256 rows from r0; nt row tiles of 128 in use
+    bool parts;                                  // its results are joined with others
     int64_t so, o;                               // slice of this launch, slice
     __device__ __forceinline__ explicit TileOf(const TcArgs& X) {
         tile = blockIdx.x;                       // the longest of a slice first
         split = 0;
         nsplit = 1;
-        if (tile >= X.nwhole) {
+        parts = tile >= X.nwhole;
+        if (parts) {
             nsplit = X.A.nsplit;
             split = (tile - X.nwhole) % nsplit;
             tile = X.nwhole + (tile - X.nwhole) / nsplit;
@@ -179,8 +181,10 @@ struct TileOf {
         j0 += (int)(len * split / nsplit);
         return first;
     }
-    __device__ __forceinline__ float* part(const TcArgs& X, int r, int C) const {
-        return X.A.part + (((int64_t)(tile - X.nwhole) * X.trows + (r - r0)) * nsplit + split) * (C + 4);
+    // where row r's sums go, nullptr: out and lse are written; at: its row_index
+    __device__ __forceinline__ float* sums_of(const TcArgs& X, int r, int64_t at, int C) const {
+        if (parts) return X.A.part + (((int64_t)(tile - X.nwhole) * X.trows + (r - r0)) * nsplit + split) * (C + 4);
+        return X.A.sums ? X.A.sums + at * (C + 4) : nullptr;
     }
 };
 
@@ -192,13 +196,14 @@ __device__ __noinline__ void add_odd(const TcArgs& X, const TileOf& w, const int
     const View& a = X.A.v;
     for (int i = tid; i < w.nrows; i += threads) {
         const int r = w.r0 + i, last = a.T - a.n + r / a.group;
-        float* part = w.part(X, r, C);
-        __nv_bfloat16* out = X.A.out + row_index(a, w.o, r) * C;
+        const int64_t at = row_index(a, w.o, r);
+        float* part = w.sums_of(X, r, at, C);
+        __nv_bfloat16* out = X.A.out + at * C;
 #pragma unroll 1
         for (int c = 0; c < C; ++c) {
             const float x = odd_value(odd, C, c, last);
             if (x == 0.0f) continue;
-            if (w.nsplit > 1) part[c] = __fadd_rn(part[c], x);
+            if (part) part[c] = __fadd_rn(part[c], x);
             else if (sums[i] != 0.0f) out[c] = __float2bfloat16(__fadd_rn(__bfloat162float(out[c]), x));
         }
     }
@@ -227,7 +232,7 @@ attend_tc_kernel(const TcArgs X, const __grid_constant__ CUtensorMap kmap, const
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const TileOf w(X);
     const int64_t so = w.so, o = w.o;
-    const int r0 = w.r0, nrows = w.nrows, nt = w.nt, nsplit = w.nsplit, base = a.T - a.n;
+    const int r0 = w.r0, nrows = w.nrows, nt = w.nt, base = a.T - a.n;
     int j0, n;
     const int first = w.keys(X, j0, n), j1 = j0 + n;
 
@@ -440,7 +445,7 @@ attend_tc_kernel(const TcArgs X, const __grid_constant__ CUtensorMap kmap, const
         }
         const bool write = ok && r < a.rows;
         const int64_t at = write ? row_index(a, o, r) : 0;
-        float* part = w.part(X, r, C);
+        float* part = w.sums_of(X, r, at, C);
         const float inv = row_scale(l);
 #pragma unroll
         for (int c = 0; c < C / 32; ++c) {
@@ -452,7 +457,7 @@ attend_tc_kernel(const TcArgs X, const __grid_constant__ CUtensorMap kmap, const
 #pragma unroll
                 for (int i = 0; i < 32; ++i) y[i] = 0u;
             }
-            if (write && nsplit > 1) {
+            if (write && part) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
                     *reinterpret_cast<uint4*>(part + 32 * c + 4 * i) = make_uint4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
@@ -470,8 +475,8 @@ attend_tc_kernel(const TcArgs X, const __grid_constant__ CUtensorMap kmap, const
             __syncwarp();                        // the next load wants the whole warp
         }
         if (write) sums[r - r0] = l;
-        if (write && nsplit > 1) *reinterpret_cast<float2*>(part + C) = make_float2(m, l);
-        if (write && nsplit == 1 && A.lse)
+        if (write && part) *reinterpret_cast<float2*>(part + C) = make_float2(m, l);
+        if (write && !part && A.lse)
             A.lse[at] = row_lse(m, l);
     }
     }
@@ -714,7 +719,7 @@ attend_fused_kernel(const __grid_constant__ TcArgs X)
         }
         const bool write = ok && r < a.rows;
         const int64_t at = write ? row_index(a, o, r) : 0;
-        float* part = w.part(X, r, C);
+        float* part = w.sums_of(X, r, at, C);
         const float inv = row_scale(l);
 #pragma unroll
         for (int c = 0; c < C / 32; ++c) {
@@ -730,7 +735,7 @@ attend_fused_kernel(const __grid_constant__ TcArgs X)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {    // channels 0 .. 7 sit in columns 0 2 4 6 1 3 5 7
                     const uint32_t* z = y + 8 * i;
-                    if (w.nsplit > 1) {
+                    if (part) {
                         *reinterpret_cast<uint4*>(part + 32 * c + 8 * i) = make_uint4(z[0], z[2], z[4], z[6]);
                         *reinterpret_cast<uint4*>(part + 32 * c + 8 * i + 4) = make_uint4(z[1], z[3], z[5], z[7]);
                     } else {
@@ -747,8 +752,8 @@ attend_fused_kernel(const __grid_constant__ TcArgs X)
             __syncwarp();
         }
         if (write) sums[r - r0] = l;
-        if (write && w.nsplit > 1) *reinterpret_cast<float2*>(part + C) = make_float2(m, l);
-        if (write && w.nsplit == 1 && A.lse)
+        if (write && part) *reinterpret_cast<float2*>(part + C) = make_float2(m, l);
+        if (write && !part && A.lse)
             A.lse[at] = row_lse(m, l);
     }
     __syncwarp();
@@ -801,11 +806,11 @@ constexpr int64_t kMaxSplitCtas = 4 * kSms;      // CTAs of split tiles: bounds 
 
 struct Waves { int64_t whole, tail, nsplit; };
 
-Waves waves_of(int64_t tiles, int64_t Tp)
+Waves waves_of(int64_t tiles, int64_t Tp, bool shared)
 {
     const int64_t keys = Tp / kTile;
-    Waves w = {tiles, 0, 1};
-    int64_t best = (tiles + kSms - 1) / kSms * (keys + 6);
+    Waves w = {shared ? 0 : tiles, shared ? tiles : 0, 1};          // shared: every tile's results are joined
+    int64_t best = (tiles + kSms - 1) / kSms * (keys + 6) + (shared ? 8 : 0);
     for (int64_t s = 2; s * 2 <= keys && tiles * s <= kMaxSplitCtas; ++s) {
         const int64_t cost = (tiles * s + kSms - 1) / kSms * ((keys + s - 1) / s + 6) + 8;
         if (cost < best) {
@@ -814,7 +819,7 @@ Waves waves_of(int64_t tiles, int64_t Tp)
         }
     }
     const int64_t tail = tiles % kSms, s = tail ? std::min<int64_t>(kSms / tail, keys / 2) : 1;
-    if (tiles > kSms && s > 1 && tiles / kSms * (keys + 6) + (keys + s - 1) / s + 14 < best) w = {tiles - tail, tail, s};
+    if (!shared && tiles > kSms && s > 1 && tiles / kSms * (keys + 6) + (keys + s - 1) / s + 14 < best) w = {tiles - tail, tail, s};
     return w;
 }
 
@@ -847,7 +852,7 @@ cudaError_t launch_tc(const ChunkArgs& A0, int64_t outer, void* ws, cudaStream_t
     for (int64_t o0 = 0; o0 < outer; o0 += p.slices) {
         X.o0 = o0;
         X.slices = std::min(p.slices, outer - o0);
-        const Waves w = waves_of(X.slices * p.ntiles, p.Tp);
+        const Waves w = waves_of(X.slices * p.ntiles, p.Tp, X.A.shared);
         X.nwhole = (int32_t)w.whole;
         X.A.nsplit = (int32_t)w.nsplit;
         const unsigned grid = (unsigned)(w.whole + w.tail * w.nsplit);
@@ -888,13 +893,15 @@ bool chunk_uses_tc(int64_t rows) { return rows > 32; }
 
 // Enough for every T up to tmax: a shorter cache may take more slices at once,
 // but never more than the bound on expanded bytes.
-size_t chunk_tc_workspace(int64_t outer, int64_t C, int64_t tmax, int64_t rows)
+size_t chunk_tc_workspace(int64_t outer, int64_t C, int64_t tmax, int64_t rows, bool shared)
 {
     const TcPlan p = tc_plan(outer, C, tmax, rows);
     size_t b = fused_form(rows) ? 0 : (size_t)std::min(outer * p.Tp * C * 4, std::max(kExpandBytes, p.Tp * C * 4));
     b += b / (32 * C);                           // a flag for 8 tokens
     const int64_t trows = std::min<int64_t>(rows, 2 * kTile), tiles = outer * p.ntiles;
-    b += (size_t)(std::min(kMaxSplitCtas, tiles * std::max<int64_t>(p.Tp / kTile / 2, 1)) * trows * (C + 4)) * 4;
+    int64_t ctas = std::min(kMaxSplitCtas, tiles * std::max<int64_t>(p.Tp / kTile / 2, 1));
+    if (shared) ctas = std::max(ctas, tiles);    // whole tiles leave their sums too
+    b += (size_t)(ctas * trows * (C + 4)) * 4;
     return b;
 }
 

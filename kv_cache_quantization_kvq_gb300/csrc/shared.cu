@@ -1,0 +1,74 @@
+// shared.cu -- attention of a batch over a quantized prefix that all its requests
+// share (kvq_attend_shared).
+//
+// "KV cache 压缩：把历史装得更小" §"让 kernel 接住收益" (the attention kernel reads the
+// low-bit cache).  Softmax over the union of two token sets A and B needs each
+// set's maximum m, sum l and weighted values y only (the online softmax): with
+// M = max(m_A, m_B), l = l_A 2^(m_A - M) + l_B 2^(m_B - M), y alike, out = y / l.
+// So the prefix is one launch of the streaming attention (chunk.cu, prefill.cu)
+// in which a KV head's rows are the query rows of all requests, batch x n x group
+// of them, that see every token: its codes are read, and unpacked, once for all.
+// The requests' own tokens are another launch over their caches, which leaves
+// (y, m, l) in float32, and the launch that joins the prefix's splits joins that too.
+#include "kvq_chunk.cuh"
+
+namespace kvq {
+
+namespace {
+
+size_t padded(size_t b) { return (b + 255) / 256 * 256; }
+
+// The workspace: the own rows' sums, then what each launch needs.
+struct SharedPlan { size_t sums, own, prefix; };
+
+SharedPlan shared_plan(int64_t prefix_tmax, int64_t own_tmax, bool own, int64_t C, int64_t batch, int64_t n, int64_t group,
+                       int64_t kv_heads)
+{
+    SharedPlan p = {0, 0, 0};
+    if (own) {
+        p.sums = padded((size_t)(batch * n * kv_heads * group * (C + 4)) * sizeof(float));
+        p.own = padded(chunk_workspace(batch * kv_heads, C, own_tmax, n, group));
+    }
+    p.prefix = chunk_workspace(kv_heads, C, prefix_tmax, batch * n, group, true);
+    return p;
+}
+
+}  // namespace
+
+size_t shared_workspace(int64_t prefix_tmax, int64_t own_tmax, bool own, int64_t C, int64_t batch, int64_t n, int64_t group,
+                        int64_t kv_heads)
+{
+    if (batch == 0 || n == 0) return 0;
+    const SharedPlan p = shared_plan(prefix_tmax, own_tmax, own, C, batch, n, group, kv_heads);
+    return p.sums + p.own + p.prefix;
+}
+
+cudaError_t launch_attend_shared(const CacheArgs& prefix, const CacheArgs* own, const void* own_out, const float* own_lse,
+                                 int64_t batch, int64_t n, void* out, float* lse, void* ws, cudaStream_t st)
+{
+    if (batch == 0 || n == 0) return cudaSuccess;
+    const SharedPlan p = shared_plan(prefix.cap + prefix.rrows, own ? own->cap + own->rrows : 0, own != nullptr, prefix.C,
+                                     batch, n, prefix.group, prefix.kv_heads);
+    unsigned char* w = static_cast<unsigned char*>(ws);
+    ChunkArgs A = {};
+    if (own) {
+        A.v = cache_view(*own);
+        A.sums = reinterpret_cast<float*>(w);
+        const cudaError_t e = launch_chunk(A, own->bits, own->C, own->outer, w + p.sums, st);
+        if (e != cudaSuccess) return e;
+        A.own_sums = A.sums;
+        A.sums = nullptr;
+    } else {
+        A.own_out = static_cast<const __nv_bfloat16*>(own_out);
+        A.own_lse = own_lse;
+    }
+    A.v = cache_view(prefix);
+    A.v.n = 1;                       // every row sees every token
+    A.v.group = A.v.rows;
+    A.out = static_cast<__nv_bfloat16*>(out);
+    A.lse = lse;
+    A.shared = 1;
+    return launch_chunk(A, prefix.bits, prefix.C, prefix.outer, w + p.sums + p.own, st);
+}
+
+}  // namespace kvq
