@@ -137,10 +137,10 @@ __device__ __forceinline__ float4 remote_f4(const void* p, int rank) {
 }
 
 // out (4 channels) and, with the row's first channels, lse; or the row's sums
-template <int C>
+template <int C, bool JOIN>
 __device__ __forceinline__ void write_row(const ChunkArgs& A, int64_t o, int r, int c4, float M, float L, const float (&v)[4]) {
-    const int64_t at = row_index(A.v, o, r);
-    if (A.sums) {
+    const int64_t at = row_index<JOIN>(A.v, o, r);
+    if (JOIN && A.sums) {
         float* dst = A.sums + at * (C + 4);
         *reinterpret_cast<float4*>(dst + c4) = make_float4(v[0], v[1], v[2], v[3]);
         if (c4 == 0) *reinterpret_cast<float2*>(dst + C) = make_float2(M, L);
@@ -229,7 +229,7 @@ __device__ __forceinline__ void softmax_of(const View& a, float (&s)[R::MT][4][4
     }
 }
 
-template <int BITS, int C, int ROWS>
+template <int BITS, int C, int ROWS, bool JOIN>
 __global__ void __launch_bounds__(kThreads, (Rows<ROWS, C>::kCtas))
 attend_rows_kernel(const ChunkArgs A)
 {
@@ -248,7 +248,7 @@ attend_rows_kernel(const ChunkArgs A)
     const int g = lane >> 2, tig = lane & 3;
     const int split = (int)(blockIdx.x % (uint32_t)A.nsplit);
     const int64_t o = blockIdx.x / (uint32_t)A.nsplit;
-    stage_queries<BITS, C, MT>(a, o, 0, qf, tid, kThreads);
+    stage_queries<BITS, C, MT, JOIN>(a, o, 0, qf, tid, kThreads);
     for (int c = tid; c < 2 * C; c += kThreads) odd[c] = kNever;
 
     // ---- the last token each of this lane's rows sees
@@ -536,12 +536,12 @@ attend_rows_kernel(const ChunkArgs A)
                     gm[row] = M;
                     gl[row] = L;
                 }
-            } else if (A.parts) {
+            } else if (JOIN ? A.parts : A.nsplit > 1) {
                 float* dst = A.part + ((o * a.rows + r) * A.nsplit + split) * (C + 4);
                 *reinterpret_cast<float4*>(dst + c4) = make_float4(v[0], v[1], v[2], v[3]);
                 if (c4 == 0) *reinterpret_cast<float2*>(dst + C) = make_float2(M, L);
             } else {
-                write_row<C>(A, o, r, c4, M, L, v);
+                write_row<C, JOIN>(A, o, r, c4, M, L, v);
             }
         }
         if (A.cluster) {                         // block rank = split; each takes its share of the rows' pieces
@@ -561,21 +561,21 @@ attend_rows_kernel(const ChunkArgs A)
                     v[2] = __fmaf_rn(x.z, f, v[2]);
                     v[3] = __fmaf_rn(x.w, f, v[3]);
                 }
-                write_row<C>(A, o, r, c4, M, L, v);
+                write_row<C, JOIN>(A, o, r, c4, M, L, v);
             }
             cluster_sync();                      // nobody leaves, or writes the next tile, before all have read
         }
     }
 }
 
-template <int C>
+template <int C, bool JOIN>
 __global__ void __launch_bounds__(kThreads)
 merge_rows_kernel(const ChunkArgs A, int64_t total)
 {
     const int64_t row = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
     if (row >= total) return;
     const int64_t o = row / A.v.rows;
-    merge_row<C>(A, o, (int)(row - o * A.v.rows), A.part + row * A.nsplit * (C + 4), threadIdx.x & 31);
+    merge_row<C, JOIN>(A, o, (int)(row - o * A.v.rows), A.part + row * A.nsplit * (C + 4), threadIdx.x & 31);
 }
 
 // Up to 8, 16 or 32 rows (four, three, two CTAs a SM); more rows take the
@@ -615,7 +615,7 @@ RowsPlan rows_plan(int64_t outer, int64_t T, int64_t rows, bool shared)
     return p;
 }
 
-template <int BITS, int C>
+template <int BITS, int C, bool JOIN>
 cudaError_t launch_rows(ChunkArgs A, int64_t outer, cudaStream_t st)
 {
     const RowsPlan p = rows_plan(outer, A.v.T, A.v.rows, A.shared);
@@ -633,13 +633,13 @@ cudaError_t launch_rows(ChunkArgs A, int64_t outer, cudaStream_t st)
     cfg.stream = st;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
-    const cudaError_t e = A.v.rows <= 8 ? cudaLaunchKernelEx(&cfg, attend_rows_kernel<BITS, C, 8>, A)
-                          : A.v.rows <= 16 ? cudaLaunchKernelEx(&cfg, attend_rows_kernel<BITS, C, 16>, A)
-                                           : cudaLaunchKernelEx(&cfg, attend_rows_kernel<BITS, C, 32>, A);
+    const cudaError_t e = A.v.rows <= 8 ? cudaLaunchKernelEx(&cfg, attend_rows_kernel<BITS, C, 8, JOIN>, A)
+                          : A.v.rows <= 16 ? cudaLaunchKernelEx(&cfg, attend_rows_kernel<BITS, C, 16, JOIN>, A)
+                                           : cudaLaunchKernelEx(&cfg, attend_rows_kernel<BITS, C, 32, JOIN>, A);
     if (e != cudaSuccess) return e;
     if (A.parts && !p.cluster) {
         const int64_t total = outer * A.v.rows;
-        merge_rows_kernel<C><<<(unsigned)((total + kWarps - 1) / kWarps), kThreads, 0, st>>>(A, total);
+        merge_rows_kernel<C, JOIN><<<(unsigned)((total + kWarps - 1) / kWarps), kThreads, 0, st>>>(A, total);
     }
     return cudaGetLastError();
 }
@@ -696,12 +696,18 @@ rows::View cache_view(const CacheArgs& x)
     return v;
 }
 
+template <bool JOIN>
+static cudaError_t launch_any(const ChunkArgs& A, int bits, int64_t C, int64_t outer, cudaStream_t st)
+{
+    if (bits == 4) return C == 128 ? launch_rows<4, 128, JOIN>(A, outer, st) : launch_rows<4, 64, JOIN>(A, outer, st);
+    return C == 128 ? launch_rows<2, 128, JOIN>(A, outer, st) : launch_rows<2, 64, JOIN>(A, outer, st);
+}
+
 cudaError_t launch_chunk(ChunkArgs A, int bits, int64_t C, int64_t outer, void* ws, cudaStream_t st)
 {
     A.part = static_cast<float*>(ws);
     if (chunk_uses_tc(A.v.rows)) return launch_attend_tc(A, bits, C, outer, ws, st);
-    if (bits == 4) return C == 128 ? launch_rows<4, 128>(A, outer, st) : launch_rows<4, 64>(A, outer, st);
-    return C == 128 ? launch_rows<2, 128>(A, outer, st) : launch_rows<2, 64>(A, outer, st);
+    return A.sums || A.shared ? launch_any<true>(A, bits, C, outer, st) : launch_any<false>(A, bits, C, outer, st);
 }
 
 cudaError_t launch_attend_chunk(const CacheArgs& x, void* out, float* lse, void* ws, cudaStream_t st)

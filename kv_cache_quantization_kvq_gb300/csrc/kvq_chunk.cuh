@@ -8,6 +8,8 @@
 
 namespace kvq {
 
+// JOIN in the kernels' templates: the launch is one of several whose results meet,
+// and only then are `sums`, `shared` and the rows' own places looked at.
 struct ChunkArgs {
     rows::View v;
     __nv_bfloat16* out;
@@ -96,18 +98,18 @@ __device__ __forceinline__ void write_joined(__nv_bfloat16* out, float* lse, int
 }
 
 // One warp joins the splits' (y, m, l) of query row r of slice o.
-template <int C>
+template <int C, bool JOIN>
 __device__ __forceinline__ void merge_row(const ChunkArgs& A, int64_t o, int r, const float* p, int lane) {
     constexpr int N = C / 32;
     float M = parts_max<C>(p, A.nsplit, lane), L = 0.0f, v[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] = 0.0f;
-    const int64_t at = rows::row_index(A.v, o, r);
-    if (A.own_sums) {
+    const int64_t at = rows::row_index<JOIN>(A.v, o, r);
+    if (JOIN && A.own_sums) {
         const float* own = A.own_sums + at * (C + 4);
         M = fmaxf(M, own[C]);
         add_parts<C>(own, 1, lane, M, L, v);
-    } else if (A.own_lse) {
+    } else if (JOIN && A.own_lse) {
         // weights that sum to 1 at the maximum lse; -inf: nothing was seen, NaN: nothing else comes out
         const float lse = A.own_lse[at], m = __fmul_rn(lse, rows::kLog2e);
         M = fmaxf(M, m);
@@ -123,7 +125,7 @@ __device__ __forceinline__ void merge_row(const ChunkArgs& A, int64_t o, int r, 
         }
     }
     add_parts<C>(p, A.nsplit, lane, M, L, v);
-    if (A.sums) {
+    if (JOIN && A.sums) {
         float* dst = A.sums + at * (C + 4);
 #pragma unroll
         for (int i = 0; i < C / 32; i += 2)

@@ -44,11 +44,11 @@ struct View {
     int64_t cap, rrows;
     int32_t tq, nres, T, n;
     int32_t group, rows;                         // rows = n * group query rows of a slice: row r sees tokens up to T - n + r / group
-    int32_t qn, qgroup;                          // where they lie: n and group, but for rows that all see every token (n = 1, group = rows)
     int32_t kv_heads, gk, ngk, gv, ngv;
     uint32_t kflip, vflip;                       // turns two's complement fields into offset binary
     float kbias, vbias;                          // 128 + that offset, 2^(bits-1) or 0
     float scale2;                                // log2(e) / sqrt(C)
+    int32_t qn, qgroup;                          // rows that all see every token (n = 1, group = rows): the n and group they lie by
 };
 
 __device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b) {
@@ -342,16 +342,18 @@ __device__ __forceinline__ int batch_of(const View& a, const Span& s, int t) {
 }
 
 // query row r of slice o: index of its q row (times C) and of its lse
+template <bool ALL = false>                       // ALL: rows that all see every token
 __device__ __forceinline__ int64_t row_index(const View& a, int64_t o, int r) {
-    const int i = r / a.qgroup, j = r - i * a.qgroup;
+    const int group = ALL ? a.qgroup : a.group, n = ALL ? a.qn : a.n;
+    const int i = r / group, j = r - i * group;
     const uint32_t b = (uint32_t)o / (uint32_t)a.kv_heads, h = (uint32_t)o - b * (uint32_t)a.kv_heads;
-    return ((int64_t)b * a.qn + i) * ((int64_t)a.kv_heads * a.qgroup) + (int64_t)h * a.qgroup + j;
+    return ((int64_t)b * n + i) * ((int64_t)a.kv_heads * group) + (int64_t)h * group + j;
 }
 
 // A fragments of query rows [r0, r0 + 16 MT) of slice o, made by the whole CTA
 // (rows past the last are zeros): entry (mt, kk, lane) = rows g and g + 8 of
 // tile mt, channel pairs 2 kk and 2 kk + 1.
-template <int BITS, int C, int MT>
+template <int BITS, int C, int MT, bool ALL = false>
 __device__ __forceinline__ void stage_queries(const View& a, int64_t o, int r0, uint4* qf, int tid, int threads) {
     using G = Geo<BITS, C>;
     for (int e = tid; e < MT * G::kSteps * 32; e += threads) {
@@ -362,7 +364,7 @@ __device__ __forceinline__ void stage_queries(const View& a, int64_t o, int r0, 
         for (int h = 0; h < 2; ++h) {
             const int r = r0 + mt * 16 + (lane >> 2) + 8 * h;
             if (r < a.rows) {
-                const __nv_bfloat16* p = a.q + row_index(a, o, r) * C + c;
+                const __nv_bfloat16* p = a.q + row_index<ALL>(a, o, r) * C + c;
                 const uint32_t x = *reinterpret_cast<const uint32_t*>(p);           // channels c, c + 1
                 const uint32_t y = *reinterpret_cast<const uint32_t*>(p + G::F / 2);
                 w[h] = __byte_perm(x, y, 0x5410);

@@ -147,14 +147,12 @@ struct TcArgs {
 // The query tile and split of a CTA.
 struct TileOf {
     int tile, split, nsplit, r0, nrows, nt;      // tile of up to 256 rows from r0; nt row tiles of 128 in use
-    bool parts;                                  // its results are joined with others
     int64_t so, o;                               // slice of this launch, slice
     __device__ __forceinline__ explicit TileOf(const TcArgs& X) {
         tile = blockIdx.x;                       // the longest of a slice first
         split = 0;
         nsplit = 1;
-        parts = tile >= X.nwhole;
-        if (parts) {
+        if (tile >= X.nwhole) {
             nsplit = X.A.nsplit;
             split = (tile - X.nwhole) % nsplit;
             tile = X.nwhole + (tile - X.nwhole) / nsplit;
@@ -182,22 +180,23 @@ struct TileOf {
         return first;
     }
     // where row r's sums go, nullptr: out and lse are written; at: its row_index
+    template <bool JOIN>
     __device__ __forceinline__ float* sums_of(const TcArgs& X, int r, int64_t at, int C) const {
-        if (parts) return X.A.part + (((int64_t)(tile - X.nwhole) * X.trows + (r - r0)) * nsplit + split) * (C + 4);
-        return X.A.sums ? X.A.sums + at * (C + 4) : nullptr;
+        if (JOIN ? tile >= X.nwhole : nsplit > 1) return X.A.part + (((int64_t)(tile - X.nwhole) * X.trows + (r - r0)) * nsplit + split) * (C + 4);
+        return JOIN && X.A.sums ? X.A.sums + at * (C + 4) : nullptr;
     }
 };
 
 // Adds the values that are not finite to the rows that the CTA has written: a thread
 // per row, after everything else (in the softmax warps' epilogue it cost the fused
 // form 6 us of 93).  sums: the rows' sums of weights.
-template <int C>
+template <int C, bool JOIN>
 __device__ __noinline__ void add_odd(const TcArgs& X, const TileOf& w, const int* odd, const float* sums, int tid, int threads) {
     const View& a = X.A.v;
     for (int i = tid; i < w.nrows; i += threads) {
         const int r = w.r0 + i, last = a.T - a.n + r / a.group;
-        const int64_t at = row_index(a, w.o, r);
-        float* part = w.sums_of(X, r, at, C);
+        const int64_t at = row_index<JOIN>(a, w.o, r);
+        float* part = w.sums_of<JOIN>(X, r, at, C);
         __nv_bfloat16* out = X.A.out + at * C;
 #pragma unroll 1
         for (int c = 0; c < C; ++c) {
@@ -209,7 +208,7 @@ __device__ __noinline__ void add_odd(const TcArgs& X, const TileOf& w, const int
     }
 }
 
-template <int C>
+template <int C, bool JOIN>
 __global__ void __launch_bounds__(kThreadsTc, 1)
 attend_tc_kernel(const TcArgs X, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap)
 {
@@ -254,7 +253,7 @@ attend_tc_kernel(const TcArgs X, const __grid_constant__ CUtensorMap kmap, const
     for (int k = tid; k < nt * kTile * (C / 8); k += kThreadsTc) {
         const int r = k / (C / 8), c = k % (C / 8);
         uint4 x = make_uint4(0, 0, 0, 0);
-        if (r < nrows) x = *reinterpret_cast<const uint4*>(a.q + row_index(a, o, r0 + r) * C + c * 8);
+        if (r < nrows) x = *reinterpret_cast<const uint4*>(a.q + row_index<JOIN>(a, o, r0 + r) * C + c * 8);
         *reinterpret_cast<uint4*>(sm + S::kQ + (r / kTile) * S::kTileB + (c / 8) * (kTile * 128) +
                                   tc::swizzled(r % kTile, c % 8)) = x;
     }
@@ -444,8 +443,8 @@ attend_tc_kernel(const TcArgs X, const __grid_constant__ CUtensorMap kmap, const
             l = __fadd_rn(lo_of(sum), hi_of(sum));
         }
         const bool write = ok && r < a.rows;
-        const int64_t at = write ? row_index(a, o, r) : 0;
-        float* part = w.sums_of(X, r, at, C);
+        const int64_t at = write ? row_index<JOIN>(a, o, r) : 0;
+        float* part = w.sums_of<JOIN>(X, r, at, C);
         const float inv = row_scale(l);
 #pragma unroll
         for (int c = 0; c < C / 32; ++c) {
@@ -485,7 +484,7 @@ attend_tc_kernel(const TcArgs X, const __grid_constant__ CUtensorMap kmap, const
     __syncthreads();
     tc::after_sync();
     if (warp == 9) tc::dealloc(tmem, 512);
-    if (odd[2 * C] && !*gone) add_odd<C>(X, w, odd, sums, tid, kThreadsTc);
+    if (odd[2 * C] && !*gone) add_odd<C, JOIN>(X, w, odd, sums, tid, kThreadsTc);
 }
 
 // ---------------------------------------------------------------- fused form
@@ -511,7 +510,7 @@ struct SmemF {
     static constexpr int kSums = kOdd + (2 * C + 4) * 4, kBytes = kSums + 2 * kTile * 4 + 1024;
 };
 
-template <int BITS, int C>
+template <int BITS, int C, bool JOIN>
 __global__ void __launch_bounds__(kFusedThreads, 1)
 attend_fused_kernel(const __grid_constant__ TcArgs X)
 {
@@ -560,7 +559,7 @@ attend_fused_kernel(const __grid_constant__ TcArgs X)
         for (int k = tid; k < nt * kTile * (C / 8); k += 384) {
             const int r = k / (C / 8), c = k % (C / 8);
             uint4 x = make_uint4(0, 0, 0, 0);
-            if (r < nrows) x = interleave(*reinterpret_cast<const uint4*>(a.q + row_index(a, o, r0 + r) * C + c * 8));
+            if (r < nrows) x = interleave(*reinterpret_cast<const uint4*>(a.q + row_index<JOIN>(a, o, r0 + r) * C + c * 8));
             *reinterpret_cast<uint4*>(sm + S::kQ + (r / kTile) * S::kTileB + (c / 8) * (kTile * 128) +
                                       tc::swizzled(r % kTile, c % 8)) = x;
         }
@@ -718,8 +717,8 @@ attend_fused_kernel(const __grid_constant__ TcArgs X)
             l = __fadd_rn(lo_of(sum), hi_of(sum));
         }
         const bool write = ok && r < a.rows;
-        const int64_t at = write ? row_index(a, o, r) : 0;
-        float* part = w.sums_of(X, r, at, C);
+        const int64_t at = write ? row_index<JOIN>(a, o, r) : 0;
+        float* part = w.sums_of<JOIN>(X, r, at, C);
         const float inv = row_scale(l);
 #pragma unroll
         for (int c = 0; c < C / 32; ++c) {
@@ -761,11 +760,11 @@ attend_fused_kernel(const __grid_constant__ TcArgs X)
     __syncthreads();
     tc::after_sync();
     if (warp == 8) tc::dealloc(tmem, 512);
-    if (odd[2 * C] && !*gone) add_odd<C>(X, w, odd, sums, tid, kFusedThreads);
+    if (odd[2 * C] && !*gone) add_odd<C, JOIN>(X, w, odd, sums, tid, kFusedThreads);
 }
 
 // One warp per row of the split query tiles joins their partial results.
-template <int C>
+template <int C, bool JOIN>
 __global__ void __launch_bounds__(256)
 merge_tiles_kernel(const TcArgs X, int64_t total)
 {
@@ -775,7 +774,7 @@ merge_tiles_kernel(const TcArgs X, int64_t total)
     const int tile = X.nwhole + (int)(at / X.trows);
     const int r = (A.ntiles - 1 - tile % A.ntiles) * 2 * kTile + (int)(at % X.trows);
     if (r < A.v.rows)
-        merge_row<C>(A, X.o0 + tile / A.ntiles, r, A.part + at * A.nsplit * (C + 4), threadIdx.x & 31);
+        merge_row<C, JOIN>(A, X.o0 + tile / A.ntiles, r, A.part + at * A.nsplit * (C + 4), threadIdx.x & 31);
 }
 
 constexpr int64_t kExpandBytes = int64_t(1) << 30;                  // expanded K and V held at once
@@ -823,7 +822,7 @@ Waves waves_of(int64_t tiles, int64_t Tp, bool shared)
     return w;
 }
 
-template <int BITS, int C>
+template <int BITS, int C, bool JOIN>
 cudaError_t launch_tc(const ChunkArgs& A0, int64_t outer, void* ws, cudaStream_t st)
 {
     const bool fused = fused_form(A0.v.rows) || A0.v.T == 0;        // an empty cache has nothing to expand
@@ -846,8 +845,8 @@ cudaError_t launch_tc(const ChunkArgs& A0, int64_t outer, void* ws, cudaStream_t
     if (!fused && (!encode_rows_tile_map(kx, p.slices * p.Tp, C, &km) || !encode_rows_tile_map(vx, p.slices * p.Tp, C, &vm)))
         return cudaErrorNotSupported;
     const cudaError_t e = fused
-        ? ensure_kernel_attrs(reinterpret_cast<const void*>(attend_fused_kernel<BITS, C>), (SmemF<BITS, C>::kBytes))
-        : ensure_kernel_attrs(reinterpret_cast<const void*>(attend_tc_kernel<C>), Smem<C>::kBytes);
+        ? ensure_kernel_attrs(reinterpret_cast<const void*>(attend_fused_kernel<BITS, C, JOIN>), (SmemF<BITS, C>::kBytes))
+        : ensure_kernel_attrs(reinterpret_cast<const void*>(attend_tc_kernel<C, JOIN>), Smem<C>::kBytes);
     if (e != cudaSuccess) return e;
     for (int64_t o0 = 0; o0 < outer; o0 += p.slices) {
         X.o0 = o0;
@@ -857,15 +856,15 @@ cudaError_t launch_tc(const ChunkArgs& A0, int64_t outer, void* ws, cudaStream_t
         X.A.nsplit = (int32_t)w.nsplit;
         const unsigned grid = (unsigned)(w.whole + w.tail * w.nsplit);
         if (fused) {
-            attend_fused_kernel<BITS, C><<<grid, kFusedThreads, (SmemF<BITS, C>::kBytes), st>>>(X);
+            attend_fused_kernel<BITS, C, JOIN><<<grid, kFusedThreads, (SmemF<BITS, C>::kBytes), st>>>(X);
         } else {
             const int64_t items = X.slices * (p.Tp / 8) * (C / 8);
             expand_kernel<BITS, C><<<dim3((unsigned)((items + 255) / 256), 2), 256, 0, st>>>(X.A.v, o0, X.slices, p.Tp, kx, vx, odd);
-            attend_tc_kernel<C><<<grid, kThreadsTc, Smem<C>::kBytes, st>>>(X, km, vm);
+            attend_tc_kernel<C, JOIN><<<grid, kThreadsTc, Smem<C>::kBytes, st>>>(X, km, vm);
         }
         if (w.tail) {
             const int64_t total = w.tail * X.trows;
-            merge_tiles_kernel<C><<<(unsigned)((total + 7) / 8), 256, 0, st>>>(X, total);
+            merge_tiles_kernel<C, JOIN><<<(unsigned)((total + 7) / 8), 256, 0, st>>>(X, total);
         }
     }
     return cudaGetLastError();
@@ -905,10 +904,16 @@ size_t chunk_tc_workspace(int64_t outer, int64_t C, int64_t tmax, int64_t rows, 
     return b;
 }
 
+template <bool JOIN>
+static cudaError_t launch_any(const ChunkArgs& A, int bits, int64_t C, int64_t outer, void* ws, cudaStream_t st)
+{
+    if (bits == 4) return C == 128 ? launch_tc<4, 128, JOIN>(A, outer, ws, st) : launch_tc<4, 64, JOIN>(A, outer, ws, st);
+    return C == 128 ? launch_tc<2, 128, JOIN>(A, outer, ws, st) : launch_tc<2, 64, JOIN>(A, outer, ws, st);
+}
+
 cudaError_t launch_attend_tc(const ChunkArgs& A, int bits, int64_t C, int64_t outer, void* ws, cudaStream_t st)
 {
-    if (bits == 4) return C == 128 ? launch_tc<4, 128>(A, outer, ws, st) : launch_tc<4, 64>(A, outer, ws, st);
-    return C == 128 ? launch_tc<2, 128>(A, outer, ws, st) : launch_tc<2, 64>(A, outer, ws, st);
+    return A.sums || A.shared ? launch_any<true>(A, bits, C, outer, ws, st) : launch_any<false>(A, bits, C, outer, ws, st);
 }
 
 }  // namespace kvq
