@@ -703,6 +703,15 @@ static cudaError_t launch_any(const ChunkArgs& A, int bits, int64_t C, int64_t o
     return C == 128 ? launch_rows<2, 128, JOIN>(A, outer, st) : launch_rows<2, 64, JOIN>(A, outer, st);
 }
 
+cudaError_t launch_merge_rows(const ChunkArgs& A, int64_t C, int64_t outer, cudaStream_t st)
+{
+    const int64_t total = outer * A.v.rows, ctas = (total + kWarps - 1) / kWarps;
+    if (ctas > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+    if (C == 128) merge_rows_kernel<128, true><<<(unsigned)ctas, kThreads, 0, st>>>(A, total);
+    else merge_rows_kernel<64, true><<<(unsigned)ctas, kThreads, 0, st>>>(A, total);
+    return cudaGetLastError();
+}
+
 cudaError_t launch_chunk(ChunkArgs A, int bits, int64_t C, int64_t outer, void* ws, cudaStream_t st)
 {
     A.part = static_cast<float*>(ws);

@@ -143,6 +143,13 @@ cudaError_t launch_attend_tc(const ChunkArgs& A, int bits, int64_t C, int64_t ou
 // The attention of kvq_attend_chunk over a cache, its rows into A.out and A.lse or into A.sums.
 cudaError_t launch_chunk(ChunkArgs A, int bits, int64_t C, int64_t outer, void* ws, cudaStream_t st);
 
+// Rows that all see every token on pairs of SMs (prefix.cu), and the launch that
+// joins the splits of part [slice][row][split] (chunk.cu).
+bool prefix_uses_pairs(int64_t C, int64_t rows);
+size_t prefix_workspace(int64_t outer, int64_t tmax, int64_t rows);
+cudaError_t launch_attend_prefix(ChunkArgs A, int bits, int64_t outer, void* ws, cudaStream_t st);
+cudaError_t launch_merge_rows(const ChunkArgs& A, int64_t C, int64_t outer, cudaStream_t st);
+
 // the same for kvq_attend_weights (weights_tc.cu)
 bool weights_use_tc(int64_t rows);
 size_t weights_tc_workspace(int64_t outer, int64_t C, int64_t rows);

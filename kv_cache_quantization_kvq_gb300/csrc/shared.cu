@@ -29,7 +29,8 @@ SharedPlan shared_plan(int64_t prefix_tmax, int64_t own_tmax, bool own, int64_t 
         p.sums = padded((size_t)(batch * n * kv_heads * group * (C + 4)) * sizeof(float));
         p.own = padded(chunk_workspace(batch * kv_heads, C, own_tmax, n, group));
     }
-    p.prefix = chunk_workspace(kv_heads, C, prefix_tmax, batch * n, group, true);
+    p.prefix = prefix_uses_pairs(C, batch * n * group) ? prefix_workspace(kv_heads, prefix_tmax, batch * n * group)
+                                                       : chunk_workspace(kv_heads, C, prefix_tmax, batch * n, group, true);
     return p;
 }
 
@@ -68,7 +69,9 @@ cudaError_t launch_attend_shared(const CacheArgs& prefix, const CacheArgs* own, 
     A.out = static_cast<__nv_bfloat16*>(out);
     A.lse = lse;
     A.shared = 1;
-    return launch_chunk(A, prefix.bits, prefix.C, prefix.outer, w + p.sums + p.own, st);
+    w += p.sums + p.own;
+    if (prefix_uses_pairs(prefix.C, A.v.rows)) return launch_attend_prefix(A, prefix.bits, prefix.outer, w, st);
+    return launch_chunk(A, prefix.bits, prefix.C, prefix.outer, w, st);
 }
 
 }  // namespace kvq
