@@ -136,16 +136,10 @@ __device__ __forceinline__ float4 remote_f4(const void* p, int rank) {
     return v;
 }
 
-// out (4 channels) and, with the row's first channels, lse; or the row's sums
+// out (4 channels) and, with the row's first channels, lse
 template <int C, bool JOIN>
 __device__ __forceinline__ void write_row(const ChunkArgs& A, int64_t o, int r, int c4, float M, float L, const float (&v)[4]) {
     const int64_t at = row_index<JOIN>(A.v, o, r);
-    if (JOIN && A.sums) {
-        float* dst = A.sums + at * (C + 4);
-        *reinterpret_cast<float4*>(dst + c4) = make_float4(v[0], v[1], v[2], v[3]);
-        if (c4 == 0) *reinterpret_cast<float2*>(dst + C) = make_float2(M, L);
-        return;
-    }
     const float inv = row_scale(L);
     *reinterpret_cast<uint2*>(A.out + at * C + c4) =
         make_uint2(pack_bf16x2(row_value(v[0], inv), row_value(v[1], inv)),
@@ -248,6 +242,15 @@ attend_rows_kernel(const ChunkArgs A)
     const int g = lane >> 2, tig = lane & 3;
     const int split = (int)(blockIdx.x % (uint32_t)A.nsplit);
     const int64_t o = blockIdx.x / (uint32_t)A.nsplit;
+    int nsplit = A.nsplit;
+    if constexpr (JOIN) {
+        asm volatile("griddepcontrol.launch_dependents;");
+        if (A.share) {
+            int from, len;
+            nsplit = splits_seen(a, o, A.share, from, len);
+            if (split >= nsplit) return;         // a shorter slice has fewer splits
+        }
+    }
     stage_queries<BITS, C, MT, JOIN>(a, o, 0, qf, tid, kThreads);
     for (int c = tid; c < 2 * C; c += kThreads) odd[c] = kNever;
 
@@ -270,7 +273,7 @@ attend_rows_kernel(const ChunkArgs A)
     }
     {
         const int64_t len = b1 - b0;
-        const int k = split * kWarps + warp, of = A.nsplit * kWarps;
+        const int k = split * kWarps + warp, of = nsplit * kWarps;
         b1 = b0 + (int)(len * (k + 1) / of);
         b0 += (int)(len * k / of);
     }
@@ -701,6 +704,51 @@ static cudaError_t launch_any(const ChunkArgs& A, int bits, int64_t C, int64_t o
 {
     if (bits == 4) return C == 128 ? launch_rows<4, 128, JOIN>(A, outer, st) : launch_rows<4, 64, JOIN>(A, outer, st);
     return C == 128 ? launch_rows<2, 128, JOIN>(A, outer, st) : launch_rows<2, 64, JOIN>(A, outer, st);
+}
+
+// Splits of slices that need not be equally long: as many as cost a quarter more than the
+// best at most where all are, so that a longer slice does not keep the others waiting
+// (64 requests of 50 to 1500 tokens, 8 KV heads: one split 41 us).
+struct Shares { int64_t nsplit, share; };
+
+static Shares shares_of(int64_t outer, int64_t T, int64_t rows)
+{
+    const int64_t slots = slots_of(rows), nb = (T + kBatch - 1) / kBatch + 1;
+    auto cost = [&](int64_t s) { return ((outer * s + slots - 1) / slots) * ((nb + s * kWarps - 1) / (s * kWarps) + 3); };
+    const int64_t most = std::max<int64_t>(1, nb / kWarps);
+    int64_t best = INT64_MAX, s = 1;
+    for (int64_t k = 1; k <= most && (k == 1 || outer * k <= kMaxWaves * 2 * slots); ++k) best = std::min(best, cost(k));
+    for (int64_t k = 1; k <= most && (k == 1 || outer * k <= kMaxWaves * 2 * slots); ++k)
+        if (4 * cost(k) <= 5 * best) s = k;
+    const int64_t share = (nb + s - 1) / s;
+    return {(nb + share - 1) / share, share};
+}
+
+size_t rows_parts_workspace(int64_t outer, int64_t C, int64_t tmax, int64_t rows)
+{
+    const int64_t most = std::max<int64_t>(1, ((tmax + kBatch - 1) / kBatch + 1) / kWarps);
+    return (size_t)(std::max(outer, std::min(kMaxWaves * 2 * slots_of(rows), outer * most)) * rows * (C + 4)) * sizeof(float);
+}
+
+template <int BITS, int C>
+static cudaError_t launch_parts(const ChunkArgs& A, int64_t outer, cudaStream_t st)
+{
+    const int64_t grid = outer * A.nsplit;
+    if (grid > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+    if (A.v.rows <= 8) attend_rows_kernel<BITS, C, 8, true><<<(unsigned)grid, kThreads, 0, st>>>(A);
+    else if (A.v.rows <= 16) attend_rows_kernel<BITS, C, 16, true><<<(unsigned)grid, kThreads, 0, st>>>(A);
+    else attend_rows_kernel<BITS, C, 32, true><<<(unsigned)grid, kThreads, 0, st>>>(A);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_rows_parts(ChunkArgs& A, int bits, int64_t C, int64_t outer, cudaStream_t st)
+{
+    const Shares p = shares_of(outer, A.v.T, A.v.rows);
+    A.nsplit = (int32_t)p.nsplit;
+    A.share = (int32_t)p.share;
+    A.parts = 1;
+    if (bits == 4) return C == 128 ? launch_parts<4, 128>(A, outer, st) : launch_parts<4, 64>(A, outer, st);
+    return C == 128 ? launch_parts<2, 128>(A, outer, st) : launch_parts<2, 64>(A, outer, st);
 }
 
 cudaError_t launch_merge_rows(const ChunkArgs& A, int64_t C, int64_t outer, cudaStream_t st)

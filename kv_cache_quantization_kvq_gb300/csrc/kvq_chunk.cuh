@@ -18,15 +18,32 @@ struct ChunkArgs {
     float* sums;             // [row_index][C + 4]: the same of whole rows, in place of out and lse; or nullptr
     int32_t nsplit, ntiles, cluster;
     int32_t parts;           // whether results go to part and are joined later: nsplit > 1, or shared
+    int32_t share;           // batches of a split, or 0: a slice has as many splits as its tokens need, of at most nsplit
     // shared: a launch over tokens that every row sees, to be joined with what the rows
-    // have seen elsewhere: own_sums as `sums` holds it, or (own_out, own_lse), or nothing
+    // have seen elsewhere: own_sums as `sums` holds it, own_part as `part` does (of the rows
+    // kernel over `own`, own_nsplit and own_share), or (own_out, own_lse), or nothing
     int32_t shared;
     const float* own_sums;
+    const float* own_part;
+    rows::View own;
+    int32_t own_nsplit, own_share;
     const __nv_bfloat16* own_out;
     const float* own_lse;
 };
 
 rows::View cache_view(const CacheArgs& x);
+
+// The visible batches [b0, b0 + len) of slice o, and how many splits of `share` batches they are.
+__device__ __forceinline__ int splits_seen(const rows::View& a, int64_t o, int share, int& b0, int& len) {
+    const int first = rows::padding(a, o), last = a.T - 1;
+    b0 = len = 0;
+    if (first <= last) {
+        const rows::Span sp = rows::span_of(a);
+        b0 = rows::batch_of(a, sp, first);
+        len = rows::batch_of(a, sp, last) + 1 - b0;
+    }
+    return share ? max(1, (len + share - 1) / share) : 1;
+}
 
 // One warp takes the largest m of a row's splits, and adds up the splits' y
 // (channels N lane + i) and l, scaled to the maximum M of the whole, in split order.
@@ -109,6 +126,15 @@ __device__ __forceinline__ void merge_row(const ChunkArgs& A, int64_t o, int r, 
         const float* own = A.own_sums + at * (C + 4);
         M = fmaxf(M, own[C]);
         add_parts<C>(own, 1, lane, M, L, v);
+    } else if (JOIN && A.own_part) {
+        // row r of KV head o is row r % own.rows of a request's slice
+        const int b = r / A.own.rows;
+        const int64_t so = (int64_t)b * A.own.kv_heads + o;
+        int b0, len;
+        const int n = splits_seen(A.own, so, A.own_share, b0, len);
+        const float* own = A.own_part + ((so * A.own.rows + (r - b * A.own.rows)) * A.own_nsplit) * (C + 4);
+        M = fmaxf(M, parts_max<C>(own, n, lane));
+        add_parts<C>(own, n, lane, M, L, v);
     } else if (JOIN && A.own_lse) {
         // weights that sum to 1 at the maximum lse; -inf: nothing was seen, NaN: nothing else comes out
         const float lse = A.own_lse[at], m = __fmul_rn(lse, rows::kLog2e);
@@ -140,7 +166,11 @@ bool chunk_uses_tc(int64_t rows);
 size_t chunk_tc_workspace(int64_t outer, int64_t C, int64_t tmax, int64_t rows, bool shared);
 cudaError_t launch_attend_tc(const ChunkArgs& A, int bits, int64_t C, int64_t outer, void* ws, cudaStream_t st);
 
-// The attention of kvq_attend_chunk over a cache, its rows into A.out and A.lse or into A.sums.
+// The attention of kvq_attend_chunk over a cache, its rows into A.out and A.lse, or
+// into A.sums; with A.parts the rows kernel's, which are left in part: nsplit and
+// share are returned in A.
+size_t rows_parts_workspace(int64_t outer, int64_t C, int64_t tmax, int64_t rows);
+cudaError_t launch_rows_parts(ChunkArgs& A, int bits, int64_t C, int64_t outer, cudaStream_t st);
 cudaError_t launch_chunk(ChunkArgs A, int bits, int64_t C, int64_t outer, void* ws, cudaStream_t st);
 
 // Rows that all see every token on pairs of SMs (prefix.cu), and the launch that

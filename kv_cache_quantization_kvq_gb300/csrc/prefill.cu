@@ -445,6 +445,32 @@ attend_tc_kernel(const TcArgs X, const __grid_constant__ CUtensorMap kmap, const
         const bool write = ok && r < a.rows;
         const int64_t at = write ? row_index<JOIN>(a, o, r) : 0;
         float* part = w.sums_of<JOIN>(X, r, at, C);
+        // a whole tile of a launch to be joined: what the row has seen elsewhere is added here
+        float fm = 1.0f, fo = 0.0f;
+        const float* own_sums = nullptr;
+        const __nv_bfloat16* own_out = nullptr;
+        if constexpr (JOIN) {
+            if (write && !part && A.shared) {
+                float mo = -INFINITY, lo = 0.0f;
+                if (A.own_sums) {
+                    own_sums = A.own_sums + at * (C + 4);
+                    mo = own_sums[C];
+                    lo = own_sums[C + 1];
+                } else if (A.own_lse) {
+                    const float z = A.own_lse[at];
+                    if (z != -INFINITY) {
+                        own_out = A.own_out + at * C;
+                        mo = __fmul_rn(z, kLog2e);
+                        lo = z != z ? z : 1.0f;
+                    }
+                }
+                const float M = fmaxf(m, mo);
+                fm = part_scale(m, M);
+                fo = part_scale(mo, M);
+                l = __fmaf_rn(l, fm, __fmul_rn(lo, fo));
+                m = M;
+            }
+        }
         const float inv = row_scale(l);
 #pragma unroll
         for (int c = 0; c < C / 32; ++c) {
@@ -455,6 +481,30 @@ attend_tc_kernel(const TcArgs X, const __grid_constant__ CUtensorMap kmap, const
             } else {
 #pragma unroll
                 for (int i = 0; i < 32; ++i) y[i] = 0u;
+            }
+            if constexpr (JOIN) {
+                if (own_sums) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float4 x = *reinterpret_cast<const float4*>(own_sums + 32 * c + 4 * i);
+                        const float v[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            y[4 * i + k] = __float_as_uint(__fmaf_rn(__uint_as_float(y[4 * i + k]), fm, __fmul_rn(v[k], fo)));
+                    }
+                } else if (own_out) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint4 x = *reinterpret_cast<const uint4*>(own_out + 32 * c + 8 * i);
+                        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            uint32_t* z = y + 8 * i + 2 * k;
+                            z[0] = __float_as_uint(__fmaf_rn(__uint_as_float(z[0]), fm, __fmul_rn(bf_lo(w[k]), fo)));
+                            z[1] = __float_as_uint(__fmaf_rn(__uint_as_float(z[1]), fm, __fmul_rn(bf_hi(w[k]), fo)));
+                        }
+                    }
+                }
             }
             if (write && part) {
 #pragma unroll
@@ -805,11 +855,11 @@ constexpr int64_t kMaxSplitCtas = 4 * kSms;      // CTAs of split tiles: bounds 
 
 struct Waves { int64_t whole, tail, nsplit; };
 
-Waves waves_of(int64_t tiles, int64_t Tp, bool shared)
+Waves waves_of(int64_t tiles, int64_t Tp, bool parts)
 {
     const int64_t keys = Tp / kTile;
-    Waves w = {shared ? 0 : tiles, shared ? tiles : 0, 1};          // shared: every tile's results are joined
-    int64_t best = (tiles + kSms - 1) / kSms * (keys + 6) + (shared ? 8 : 0);
+    Waves w = {parts ? 0 : tiles, parts ? tiles : 0, 1};            // parts: every tile's results are joined later
+    int64_t best = (tiles + kSms - 1) / kSms * (keys + 6) + (parts ? 8 : 0);
     for (int64_t s = 2; s * 2 <= keys && tiles * s <= kMaxSplitCtas; ++s) {
         const int64_t cost = (tiles * s + kSms - 1) / kSms * ((keys + s - 1) / s + 6) + 8;
         if (cost < best) {
@@ -818,7 +868,7 @@ Waves waves_of(int64_t tiles, int64_t Tp, bool shared)
         }
     }
     const int64_t tail = tiles % kSms, s = tail ? std::min<int64_t>(kSms / tail, keys / 2) : 1;
-    if (!shared && tiles > kSms && s > 1 && tiles / kSms * (keys + 6) + (keys + s - 1) / s + 14 < best) w = {tiles - tail, tail, s};
+    if (!parts && tiles > kSms && s > 1 && tiles / kSms * (keys + 6) + (keys + s - 1) / s + 14 < best) w = {tiles - tail, tail, s};
     return w;
 }
 
@@ -851,7 +901,7 @@ cudaError_t launch_tc(const ChunkArgs& A0, int64_t outer, void* ws, cudaStream_t
     for (int64_t o0 = 0; o0 < outer; o0 += p.slices) {
         X.o0 = o0;
         X.slices = std::min(p.slices, outer - o0);
-        const Waves w = waves_of(X.slices * p.ntiles, p.Tp, X.A.shared);
+        const Waves w = waves_of(X.slices * p.ntiles, p.Tp, X.A.shared && (fused || X.A.own_part));
         X.nwhole = (int32_t)w.whole;
         X.A.nsplit = (int32_t)w.nsplit;
         const unsigned grid = (unsigned)(w.whole + w.tail * w.nsplit);

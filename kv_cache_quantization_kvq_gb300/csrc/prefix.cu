@@ -323,7 +323,7 @@ struct Half {
 };
 
 template <int BITS>
-__global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
+__global__ void __launch_bounds__(kThreads, 1)
 attend_prefix_kernel(const __grid_constant__ PrefixArgs X)
 {
     using S = Smem<BITS>;
@@ -597,6 +597,7 @@ attend_prefix_kernel(const __grid_constant__ PrefixArgs X)
         }
     }
     cluster_sync();                              // the other has read what this one noted
+    asm volatile("griddepcontrol.wait;" ::: "memory");              // so that what follows this launch follows the one before, too
 }
 
 constexpr int64_t kPairs = 76;                   // of SMs
@@ -623,8 +624,20 @@ cudaError_t launch(PrefixArgs X, int64_t outer, cudaStream_t st)
     if (e != cudaSuccess) return e;
     const int64_t grid = 2 * outer * X.ntiles * X.A.nsplit;
     if (grid > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
-    attend_prefix_kernel<BITS><<<(unsigned)grid, kThreads, Smem<BITS>::kBytes, st>>>(X);
-    return cudaGetLastError();
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim = {2, 1, 1};
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = Smem<BITS>::kBytes;
+    cfg.stream = st;
+    cfg.attrs = at;
+    cfg.numAttrs = X.A.own_part ? 2 : 1;         // the launch before is the rows kernel of this call
+    const cudaError_t l = cudaLaunchKernelEx(&cfg, attend_prefix_kernel<BITS>, X);
+    return l != cudaSuccess ? l : cudaGetLastError();
 }
 
 }  // namespace

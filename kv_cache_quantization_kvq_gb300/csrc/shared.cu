@@ -10,6 +10,7 @@
 // of them, that see every token: its codes are read, and unpacked, once for all.
 // The requests' own tokens are another launch over their caches, which leaves
 // (y, m, l) in float32, and the launch that joins the prefix's splits joins that too.
+// The prefix's launch starts while the last CTAs of that one run: it reads nothing of theirs.
 #include "kvq_chunk.cuh"
 
 namespace kvq {
@@ -26,8 +27,13 @@ SharedPlan shared_plan(int64_t prefix_tmax, int64_t own_tmax, bool own, int64_t 
 {
     SharedPlan p = {0, 0, 0};
     if (own) {
-        p.sums = padded((size_t)(batch * n * kv_heads * group * (C + 4)) * sizeof(float));
-        p.own = padded(chunk_workspace(batch * kv_heads, C, own_tmax, n, group));
+        const int64_t outer = batch * kv_heads, rows = n * group;
+        if (chunk_uses_tc(rows)) {
+            p.sums = padded((size_t)(outer * rows * (C + 4)) * sizeof(float));
+            p.own = padded(chunk_workspace(outer, C, own_tmax, n, group));
+        } else {
+            p.own = padded(rows_parts_workspace(outer, C, own_tmax, rows));
+        }
     }
     p.prefix = prefix_uses_pairs(C, batch * n * group) ? prefix_workspace(kv_heads, prefix_tmax, batch * n * group)
                                                        : chunk_workspace(kv_heads, C, prefix_tmax, batch * n, group, true);
@@ -53,12 +59,21 @@ cudaError_t launch_attend_shared(const CacheArgs& prefix, const CacheArgs* own, 
     unsigned char* w = static_cast<unsigned char*>(ws);
     ChunkArgs A = {};
     if (own) {
-        A.v = cache_view(*own);
-        A.sums = reinterpret_cast<float*>(w);
-        const cudaError_t e = launch_chunk(A, own->bits, own->C, own->outer, w + p.sums, st);
+        ChunkArgs B = {};
+        B.v = A.own = cache_view(*own);
+        cudaError_t e;
+        if (chunk_uses_tc(B.v.rows)) {
+            B.sums = reinterpret_cast<float*>(w);
+            e = launch_chunk(B, own->bits, own->C, own->outer, w + p.sums, st);
+            A.own_sums = B.sums;
+        } else {
+            B.part = reinterpret_cast<float*>(w);
+            e = launch_rows_parts(B, own->bits, own->C, own->outer, st);
+            A.own_part = B.part;
+            A.own_nsplit = B.nsplit;
+            A.own_share = B.share;
+        }
         if (e != cudaSuccess) return e;
-        A.own_sums = A.sums;
-        A.sums = nullptr;
     } else {
         A.own_out = static_cast<const __nv_bfloat16*>(own_out);
         A.own_lse = own_lse;
