@@ -7,18 +7,21 @@
 // T - L_b .. T - 1, T = tq + nres; what lies before is padding, which no group counts
 // and nothing writes.
 //
-// One launch, bound by memory (4 C bytes in and about C out a token and KV head).  A
-// warp takes a few units of one slice, of those that hold tokens, so that padding
-// costs nothing:
+// One launch, bound by memory (4 C bytes in and about C out a token and KV head) and
+// by the instructions that make the codes.  A warp takes a few units of one slice, of
+// those that hold tokens, so that padding costs nothing:
 //  * keys: a group of 64 channels.  Lane (lr, lc) = (lane / 8, lane % 8) has eight
-//    channels of every fourth token, up to 64 tokens in registers (longer groups are
-//    read twice, the second time from L2); the extremes meet in two shuffles, each lane
+//    channels of every fourth token; the extremes meet in two shuffles, each lane
 //    derives two channels' constants and writes them;
-//  * values: the rows of 16 KB / 4 C tokens.  A lane has eight channels of eight tokens;
-//    the lanes of a group each derive one token's constants;
+//  * values: eight tokens a lane, eight channels of each; the lanes of a group each
+//    derive a token's constants;
 //  * buffered tokens: the same rows, copied.
+// A unit is read twice, for the extremes and for the codes, the second time from L1:
+// with the rows kept in registers the loops had to be unrolled over all of them, and
+// missed the instruction cache at 16 warps a SM (64 prompts of 26422 tokens: 55 us).
 // The arithmetic is that of the quantize kernels (kvq_elem.cuh), bit for bit.
 #include <algorithm>
+#include <type_traits>
 
 #include "kvq_elem.cuh"
 
@@ -29,8 +32,7 @@ namespace {
 using namespace elem;
 
 constexpr int kWarps = 4;
-constexpr int kRows = 16;                        // rows of a lane that are in flight, keys
-constexpr int kRowsV = 8;                        // values and buffer
+constexpr int kRows = 8;                         // rows of a lane that are in flight
 
 struct Place { int first, shift; };              // position t of the slice holds row t + shift, from t = first on
 
@@ -56,18 +58,17 @@ __device__ __forceinline__ void store_meta16(void* buf, int64_t i, float v) {
     static_cast<__nv_bfloat16*>(buf)[i] = __float2bfloat16_rn(v);
 }
 
+// The codes of eight channels by the IEEE division, out of line: the groups that need it are few.
 template <int BITS, bool ASYM>
-__device__ __forceinline__ typename CodeWord<BITS>::T codes_of(const uint4& w, const QuotK (&kq)[4], const int32_t (&zo)[8],
-                                                               const float (&s)[8], const QSpec& q, int off, bool fast) {
-    uint32_t c[8];
-    if (fast) {
-        codes8_fast<ASYM>(w, kq, zo, q.qmin + off, q.qmax + off, c);
-    } else {
-        float z[8];
+__device__ __noinline__ uint32_t slow_codes(const uint4& w, const float* s, const float* z, const QSpec& q, int off) {
+    float s8[8], z8[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) z[i] = __int_as_float(zo[i]);           // the zero points themselves
-        codes8_slow<ASYM>(w, s, z, q, off, c);
+    for (int i = 0; i < 8; ++i) {
+        s8[i] = s[i];
+        z8[i] = z[i];
     }
+    uint32_t c[8];
+    codes8_slow<ASYM>(w, s8, z8, q, off, c);
     return finish_word<BITS>(c, q.is_signed);
 }
 
@@ -76,39 +77,34 @@ __device__ __forceinline__ void fill_keys(const FillArgs& a, const FillPlan& p, 
 {
     const QSpec& q = a.k.q;
     constexpr int kParts = C / 64;               // groups of 64 channels
+    constexpr int kRowB = C * BITS / 8;
     const int64_t o = warp / p.kwarps, b = o / a.kv_heads, h = o - b * a.kv_heads;
     if (o >= a.prompts * a.kv_heads) return;
     const Place at = place_of(a, b);
     const int g = (int)q.g, lr = lane >> 3, lc = lane & 7, off = q.is_signed ? 1 << (BITS - 1) : 0;
     int64_t u0, u1;
     share(at.first / g * kParts, a.tq / g * kParts, warp - o * p.kwarps, p.kwarps, u0, u1);
-    const int passes = (g + 4 * kRows - 1) / (4 * kRows);
+#pragma unroll 1
     for (int64_t u = u0; u < u1; ++u) {
         const int64_t gi = u / kParts;
         const int c0 = (int)(u - gi * kParts) * 64 + lc * 8;
-        const int t0 = (int)(gi * g), from = max(at.first, t0);
+        const int t0 = (int)(gi * g), from = max(at.first - t0, 0);         // rows from .. g - 1 are there
         const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(a.k.x) + (int64_t)(t0 + at.shift) * a.k.stride + h * C + c0;
-        uint4 w[kRows];
-        auto load = [&](int pass) {
-#pragma unroll
-            for (int j = 0; j < kRows; ++j) {
-                const int r = pass * 4 * kRows + 4 * j + lr;
-                w[j] = make_uint4(0, 0, 0, 0);
-                if (r < g && t0 + r >= from) w[j] = __ldcg(reinterpret_cast<const uint4*>(x + (int64_t)r * a.k.stride));
-            }
-        };
         uint32_t mn[4], mx[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             mn[i] = kBfPosInf2;
             mx[i] = ASYM ? kBfNegInf2 : 0u;
         }
-        for (int pass = 0; pass < passes; ++pass) {
-            load(pass);
+#pragma unroll 1
+        for (int r = lr; r < g; r += 4 * kRows) {
+            uint4 w[kRows];
+#pragma unroll
+            for (int j = 0; j < kRows; ++j)
+                if (r + 4 * j >= from && r + 4 * j < g) w[j] = *reinterpret_cast<const uint4*>(x + (int64_t)(r + 4 * j) * a.k.stride);
 #pragma unroll
             for (int j = 0; j < kRows; ++j) {
-                const int r = pass * 4 * kRows + 4 * j + lr;
-                if (r >= g || t0 + r < from) continue;
+                if (r + 4 * j < from || r + 4 * j >= g) continue;
                 const uint32_t ws[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -117,6 +113,7 @@ __device__ __forceinline__ void fill_keys(const FillArgs& a, const FillPlan& p, 
                 }
             }
         }
+        __syncwarp();
 #pragma unroll
         for (int s = 8; s < 32; s <<= 1)
 #pragma unroll
@@ -137,31 +134,53 @@ __device__ __forceinline__ void fill_keys(const FillArgs& a, const FillPlan& p, 
         const int64_t mi = (o * q.ngroups + gi) * C + c0 + 2 * lr;
         *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.k.scale) + mi) = pack_bf16x2(g0.s, g1.s);
         if (ASYM) *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.k.zero) + mi) = pack_bf16x2(g0.zp, g1.zp);
-        const bool fast = __all_sync(0xFFFFFFFFu, g0.fast && g1.fast);
-        float s8[8];
-        int32_t zo[8];
-        QuotK kq[4];
-        const int32_t z0 = fast ? g0.zoff : __float_as_int(g0.zp), z1 = fast ? g1.zoff : __float_as_int(g1.zp);
+        uint8_t* codes = static_cast<uint8_t*>(a.k.codes) + (o * a.cap + t0) * kRowB + c0 / 8 * BITS;
+        if (__all_sync(0xFFFFFFFFu, g0.fast && g1.fast)) {
+            int32_t zo[8];
+            QuotK kq[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int src = 8 * i + lc;
-            s8[2 * i] = __shfl_sync(0xFFFFFFFFu, g0.s, src);
-            s8[2 * i + 1] = __shfl_sync(0xFFFFFFFFu, g1.s, src);
-            zo[2 * i] = __shfl_sync(0xFFFFFFFFu, z0, src);
-            zo[2 * i + 1] = __shfl_sync(0xFFFFFFFFu, z1, src);
-            kq[i].ns = pk(-s8[2 * i], -s8[2 * i + 1]);
-            kq[i].inv = pk(__shfl_sync(0xFFFFFFFFu, g0.inv, src), __shfl_sync(0xFFFFFFFFu, g1.inv, src));
-        }
-        uint8_t* codes = static_cast<uint8_t*>(a.k.codes) + (o * a.cap + t0) * (C * BITS / 8) + c0 / 8 * BITS;
-        for (int pass = 0; pass < passes; ++pass) {
-            if (passes > 1) load(pass);
-#pragma unroll
-            for (int j = 0; j < kRows; ++j) {
-                const int r = pass * 4 * kRows + 4 * j + lr;
-                if (r < g && t0 + r >= from)
-                    store_codes<BITS>(codes + (int64_t)r * (C * BITS / 8), codes_of<BITS, ASYM>(w[j], kq, zo, s8, q, off, fast));
+            for (int i = 0; i < 4; ++i) {
+                const int src = 8 * i + lc;
+                zo[2 * i] = __shfl_sync(0xFFFFFFFFu, g0.zoff, src);
+                zo[2 * i + 1] = __shfl_sync(0xFFFFFFFFu, g1.zoff, src);
+                kq[i].ns = pk(-__shfl_sync(0xFFFFFFFFu, g0.s, src), -__shfl_sync(0xFFFFFFFFu, g1.s, src));
+                kq[i].inv = pk(__shfl_sync(0xFFFFFFFFu, g0.inv, src), __shfl_sync(0xFFFFFFFFu, g1.inv, src));
             }
+            const int lo = q.qmin + off, hi = q.qmax + off;
+            const uint4* px = reinterpret_cast<const uint4*>(x + (int64_t)lr * a.k.stride);
+            const int64_t step = a.k.stride / 2;                    // four rows, in pieces of eight channels
+            uint8_t* pc = codes + lr * kRowB;
+            auto rows = [&](auto clip) {
+#pragma unroll 2
+                for (int r = lr; r < g; r += 4) {
+                    if (r >= from) {
+                        uint32_t c[8];
+                        codes8_fast<ASYM, decltype(clip)::value>(*px, kq, zo, lo, hi, c);
+                        store_codes<BITS>(pc, finish_word<BITS>(c, q.is_signed));
+                    }
+                    px += step;
+                    pc += 4 * kRowB;
+                }
+            };
+            if (__all_sync(0xFFFFFFFFu, g0.lo_ok && g1.lo_ok)) rows(std::false_type{});
+            else rows(std::true_type{});
+        } else {
+            float s8[8], z8[8];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int src = 8 * i + lc;
+                s8[2 * i] = __shfl_sync(0xFFFFFFFFu, g0.s, src);
+                s8[2 * i + 1] = __shfl_sync(0xFFFFFFFFu, g1.s, src);
+                z8[2 * i] = __shfl_sync(0xFFFFFFFFu, g0.zp, src);
+                z8[2 * i + 1] = __shfl_sync(0xFFFFFFFFu, g1.zp, src);
+            }
+#pragma unroll 1
+            for (int r = lr; r < g; r += 4)
+                if (r >= from)
+                    store_codes<BITS>(codes + (int64_t)r * kRowB, (typename CodeWord<BITS>::T)slow_codes<BITS, ASYM>(
+                                          *reinterpret_cast<const uint4*>(x + (int64_t)r * a.k.stride), s8, z8, q, off));
         }
+        __syncwarp();
     }
 }
 
@@ -169,7 +188,8 @@ template <int BITS, int C, bool ASYM>
 __device__ __forceinline__ void fill_values(const FillArgs& a, const FillPlan& p, int64_t warp, int lane)
 {
     const QSpec& q = a.v.q;
-    constexpr int kLanes = C / 8, kAcross = 32 / kLanes, kUnit = kRowsV * kAcross;    // lanes of a row, rows of a load
+    constexpr int kLanes = C / 8, kAcross = 32 / kLanes, kUnit = kRows * kAcross;     // lanes of a row, rows of a load
+    constexpr int kRowB = C * BITS / 8;
     const int64_t o = warp / p.vwarps, b = o / a.kv_heads, h = o - b * a.kv_heads;
     if (o >= a.prompts * a.kv_heads) return;
     const Place at = place_of(a, b);
@@ -177,84 +197,114 @@ __device__ __forceinline__ void fill_values(const FillArgs& a, const FillPlan& p
     const int gl = (int)q.g / 8, mine = lc & (gl - 1);              // 4, 8 or 16 lanes a group
     int64_t u0, u1;
     share(at.first / kUnit, (a.tq + kUnit - 1) / kUnit, warp - o * p.vwarps, p.vwarps, u0, u1);
+#pragma unroll 1
     for (int64_t u = u0; u < u1; ++u) {
         const int t0 = (int)u * kUnit + lr;      // the lane's rows: t0 + k kAcross
         const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(a.v.x) + (int64_t)(t0 + at.shift) * a.v.stride + h * C + lc * 8;
         auto live = [&](int k) { return t0 + k * kAcross >= at.first && t0 + k * kAcross < a.tq; };
-        uint4 w[kRowsV];
-#pragma unroll
-        for (int k = 0; k < kRowsV; ++k) {
-            w[k] = make_uint4(0, 0, 0, 0);
-            if (live(k)) w[k] = __ldcs(reinterpret_cast<const uint4*>(x + (int64_t)k * kAcross * a.v.stride));
-        }
         // a group's (min, -max), or (0, -max |x|), as one pair: they meet in log2(gl) shuffles
-        uint32_t ext[kRowsV];
+        uint32_t ext[kRows];
+        {
+            uint4 w[kRows];
 #pragma unroll
-        for (int k = 0; k < kRowsV; ++k) {
-            uint32_t mn = kBfPosInf2, mx = ASYM ? kBfNegInf2 : 0u;
-            if (ASYM) fold_minmax(w[k], mn, mx);
-            else fold_absmax(w[k], mx);
-            mn = bmin2(mn, __byte_perm(mn, mn, 0x1032));
-            mx = bmax2(mx, __byte_perm(mx, mx, 0x1032)) ^ 0x80008000u;
-            ext[k] = __byte_perm(mn, mx, 0x5410);
+            for (int k = 0; k < kRows; ++k) {
+                w[k] = make_uint4(0, 0, 0, 0);
+                if (live(k)) w[k] = *reinterpret_cast<const uint4*>(x + (int64_t)k * kAcross * a.v.stride);
+            }
+#pragma unroll
+            for (int k = 0; k < kRows; ++k) {
+                uint32_t mn = kBfPosInf2, mx = ASYM ? kBfNegInf2 : 0u;
+                if (ASYM) fold_minmax(w[k], mn, mx);
+                else fold_absmax(w[k], mx);
+                mn = bmin2(mn, __byte_perm(mn, mn, 0x1032));
+                mx = bmax2(mx, __byte_perm(mx, mx, 0x1032)) ^ 0x80008000u;
+                ext[k] = __byte_perm(mn, mx, 0x5410);
+            }
         }
+#pragma unroll 1
         for (int s = 1; s < gl; s <<= 1)
 #pragma unroll
-            for (int k = 0; k < kRowsV; ++k) ext[k] = bmin2(ext[k], __shfl_xor_sync(0xFFFFFFFFu, ext[k], s));
+            for (int k = 0; k < kRows; ++k) ext[k] = bmin2(ext[k], __shfl_xor_sync(0xFFFFFFFFu, ext[k], s));
         // lane `mine` of a group derives the constants of rows mine and, where a group has four lanes, mine + 4
-        GroupC gc[2];
-        bool fast = true;
+        float gs[2], gi[2], gz[2];
+        int32_t zoff[2];
+        bool fast = true, lo_ok = true;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const int row = i == 0 ? mine & 7 : (mine & 3) + 4;
+            gs[i] = gs[0];
+            gi[i] = gi[0];
+            gz[i] = gz[0];
+            zoff[i] = zoff[0];
+            if (i == 1 && gl != 4) break;
+            const int row = i == 0 ? mine & 7 : mine + 4;
             uint32_t e = ext[0];
 #pragma unroll
-            for (int k = 1; k < kRowsV; ++k)
+            for (int k = 1; k < kRows; ++k)
                 if (row == k) e = ext[k];
-            if (i == 0 || gl == 4) {
-                gc[i] = make_group<ASYM>(lo_f(e), -hi_f(e), q, off);
-                fast = fast && gc[i].fast;
-                const int t = t0 + row * kAcross;
-                if (mine < 8 && t >= at.first && t < a.tq) {
-                    const int64_t mi = (o * a.cap + t) * q.ngroups + lc / gl;
-                    store_meta16(a.v.scale, mi, gc[i].s);
-                    if (ASYM) store_meta16(a.v.zero, mi, gc[i].zp);
-                }
-            } else {
-                gc[i] = gc[0];
+            const GroupC gc = make_group<ASYM>(lo_f(e), -hi_f(e), q, off);
+            gs[i] = gc.s;
+            gi[i] = gc.inv;
+            gz[i] = gc.zp;
+            zoff[i] = gc.zoff;
+            fast = fast && gc.fast;
+            lo_ok = lo_ok && gc.lo_ok;
+            const int t = t0 + row * kAcross;
+            if (mine < 8 && t >= at.first && t < a.tq) {
+                const int64_t mi = (o * a.cap + t) * q.ngroups + lc / gl;
+                store_meta16(a.v.scale, mi, gc.s);
+                if (ASYM) store_meta16(a.v.zero, mi, gc.zp);
             }
         }
-        fast = __all_sync(0xFFFFFFFFu, fast);
         const int lane0 = lane - mine;
-        uint8_t* codes = static_cast<uint8_t*>(a.v.codes) + (o * a.cap + t0) * (C * BITS / 8) + lc * BITS;
-#pragma unroll
-        for (int k = 0; k < kRowsV; ++k) {
-            const int src = lane0 + (gl == 4 ? k & 3 : k);
-            const bool second = k >= 4 && gl == 4;
-            const float s = __shfl_sync(0xFFFFFFFFu, second ? gc[1].s : gc[0].s, src);
-            const float inv = __shfl_sync(0xFFFFFFFFu, second ? gc[1].inv : gc[0].inv, src);
-            const GroupC& gk = second ? gc[1] : gc[0];
-            const int32_t z = __shfl_sync(0xFFFFFFFFu, fast ? gk.zoff : __float_as_int(gk.zp), src);
-            float s8[8];
-            int32_t zo[8];
-            QuotK kq[4];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                s8[i] = s;
-                zo[i] = z;
-                kq[i / 2].ns = pk(-s, -s);
-                kq[i / 2].inv = pk(inv, inv);
+        uint8_t* codes = static_cast<uint8_t*>(a.v.codes) + (o * a.cap + t0) * kRowB + lc * BITS;
+        if (__all_sync(0xFFFFFFFFu, fast)) {
+            const int lo = q.qmin + off, hi = q.qmax + off;
+            const uint4* px = reinterpret_cast<const uint4*>(x);
+            const int64_t step = kAcross * a.v.stride / 8;
+            uint8_t* pc = codes;
+            auto rows = [&](auto clip) {
+#pragma unroll 2
+                for (int k = 0; k < kRows; ++k) {
+                    const bool second = k >= 4 && gl == 4;
+                    const int src = lane0 + (second ? k - 4 : k);
+                    const float s = __shfl_sync(0xFFFFFFFFu, second ? gs[1] : gs[0], src);
+                    const float inv = __shfl_sync(0xFFFFFFFFu, second ? gi[1] : gi[0], src);
+                    const int32_t z = __shfl_sync(0xFFFFFFFFu, second ? zoff[1] : zoff[0], src);
+                    if (live(k)) {
+                        const int32_t zo[8] = {z, z, z, z, z, z, z, z};
+                        const QuotK one = {pk(-s, -s), pk(inv, inv)};
+                        const QuotK kq[4] = {one, one, one, one};
+                        uint32_t c[8];
+                        codes8_fast<ASYM, decltype(clip)::value>(*px, kq, zo, lo, hi, c);
+                        store_codes<BITS>(pc, finish_word<BITS>(c, q.is_signed));
+                    }
+                    px += step;
+                    pc += kAcross * kRowB;
+                }
+            };
+            if (__all_sync(0xFFFFFFFFu, lo_ok)) rows(std::false_type{});
+            else rows(std::true_type{});
+        } else {
+#pragma unroll 1
+            for (int k = 0; k < kRows; ++k) {
+                const bool second = k >= 4 && gl == 4;
+                const int src = lane0 + (second ? k - 4 : k);
+                const float s = __shfl_sync(0xFFFFFFFFu, second ? gs[1] : gs[0], src);
+                const float z = __shfl_sync(0xFFFFFFFFu, second ? gz[1] : gz[0], src);
+                if (!live(k)) continue;
+                const float s8[8] = {s, s, s, s, s, s, s, s}, z8[8] = {z, z, z, z, z, z, z, z};
+                store_codes<BITS>(codes + (int64_t)k * kAcross * kRowB, (typename CodeWord<BITS>::T)slow_codes<BITS, ASYM>(
+                                      *reinterpret_cast<const uint4*>(x + (int64_t)k * kAcross * a.v.stride), s8, z8, q, off));
             }
-            const auto word = codes_of<BITS, ASYM>(w[k], kq, zo, s8, q, off, fast);
-            if (live(k)) store_codes<BITS>(codes + (int64_t)k * kAcross * (C * BITS / 8), word);
         }
+        __syncwarp();
     }
 }
 
 template <int C>
 __device__ __forceinline__ void fill_buffers(const FillArgs& a, const FillPlan& p, int64_t warp, int lane)
 {
-    constexpr int kLanes = C / 8, kAcross = 32 / kLanes, kUnit = kRowsV * kAcross;
+    constexpr int kLanes = C / 8, kAcross = 32 / kLanes, kUnit = kRows * kAcross;
     const int64_t o = warp / p.rwarps, b = o / a.kv_heads, h = o - b * a.kv_heads, part = warp - o * p.rwarps;
     if (o >= a.prompts * a.kv_heads) return;
     const Place at = place_of(a, b);
@@ -270,18 +320,18 @@ __device__ __forceinline__ void fill_buffers(const FillArgs& a, const FillPlan& 
         const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(s.x) + (a.tq + r0 + at.shift) * s.stride + h * C + lc * 8;
         __nv_bfloat16* y = static_cast<__nv_bfloat16*>(s.resid) + (o * a.rrows + r0) * C + lc * 8;
         auto live = [&](int k) { return a.tq + r0 + k * kAcross >= at.first && r0 + k * kAcross < a.nres; };
-        uint4 w[kRowsV];
+        uint4 w[kRows];
 #pragma unroll
-        for (int k = 0; k < kRowsV; ++k)
+        for (int k = 0; k < kRows; ++k)
             if (live(k)) w[k] = __ldcs(reinterpret_cast<const uint4*>(x + (int64_t)k * kAcross * s.stride));
 #pragma unroll
-        for (int k = 0; k < kRowsV; ++k)
+        for (int k = 0; k < kRows; ++k)
             if (live(k)) *reinterpret_cast<uint4*>(y + (int64_t)k * kAcross * C) = w[k];
     }
 }
 
 template <int BITS, int C>
-__global__ void __launch_bounds__(kWarps * 32, 4)
+__global__ void __launch_bounds__(kWarps * 32, 6)
 fill_kernel(const FillArgs a, const FillPlan p)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -303,14 +353,14 @@ fill_kernel(const FillArgs a, const FillPlan p)
 // Units for a warp: enough warps to fill the GPU twice, but at most eight units.
 int64_t warps_of(int64_t units, int64_t outer)
 {
-    const int64_t each = std::min<int64_t>(8, std::max<int64_t>(1, units * outer / (2 * 152 * 16)));
+    const int64_t each = std::min<int64_t>(8, std::max<int64_t>(1, units * outer / (2 * 152 * 28)));
     return (units + each - 1) / each;
 }
 
 template <int BITS, int C>
 cudaError_t launch(const FillArgs& a, int64_t outer, cudaStream_t st)
 {
-    constexpr int kUnit = kRowsV * 32 / (C / 8);
+    constexpr int kUnit = kRows * 32 / (C / 8);
     FillPlan p;
     p.kwarps = a.tq ? warps_of(a.tq / a.k.q.g * (C / 64), outer) : 0;
     p.vwarps = a.tq ? warps_of((a.tq + kUnit - 1) / kUnit, outer) : 0;
