@@ -228,7 +228,7 @@ attend_tc_kernel(const TcArgs X, const __grid_constant__ CUtensorMap kmap, const
 
     const ChunkArgs& A = X.A;
     const View& a = A.v;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), lane = tid & 31;
     const TileOf w(X);
     const int64_t so = w.so, o = w.o;
     const int r0 = w.r0, nrows = w.nrows, nt = w.nt, base = a.T - a.n;
@@ -582,7 +582,7 @@ attend_fused_kernel(const __grid_constant__ TcArgs X)
 
     const ChunkArgs& A = X.A;
     const View& a = A.v;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), lane = tid & 31;
     const TileOf w(X);
     const int64_t o = w.o;
     const int r0 = w.r0, nrows = w.nrows, nt = w.nt, base = a.T - a.n;

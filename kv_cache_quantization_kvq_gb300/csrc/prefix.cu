@@ -346,7 +346,8 @@ attend_prefix_kernel(const __grid_constant__ PrefixArgs X)
 
     const ChunkArgs& A = X.A;
     const View& a = A.v;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // the shuffle tells the compiler that a warp's number is uniform: the products' operands then are, too
+    const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), lane = tid & 31;
     const int rank = (int)cta_rank();
     const int pair = blockIdx.x >> 1, split = pair % A.nsplit, tile = pair / A.nsplit % X.ntiles;
     const int64_t o = pair / A.nsplit / X.ntiles;

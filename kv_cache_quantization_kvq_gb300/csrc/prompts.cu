@@ -151,24 +151,35 @@ struct Args {
     float scale2;                                // log2(e) / sqrt(C)
 };
 
-// The pairs of a CTA, and what a role needs of the current one.
+// The pairs of a CTA, and what a role needs of the current one.  The next one is
+// read ahead: where a pair ends, nobody waits for that.
 struct Walk {
     const Item* items;
     int64_t pairs;
     int kv_heads, round;
     Item x;
     int h;
+    int4 next_x;
+    int next_h;                                  // -1: there is none
     __device__ __forceinline__ explicit Walk(const Args& a)
-        : items(reinterpret_cast<const Item*>(a.plan + 1)), pairs((int64_t)a.plan->count * a.kv_heads), kv_heads(a.kv_heads), round(0) {}
-    __device__ __forceinline__ bool next() {
+        : items(reinterpret_cast<const Item*>(a.plan + 1)), pairs((int64_t)a.plan->count * a.kv_heads), kv_heads(a.kv_heads), round(0) {
+        ahead();
+    }
+    __device__ __forceinline__ void ahead() {
         const int c = round & 1 ? (int)gridDim.x - 1 - (int)blockIdx.x : (int)blockIdx.x;
         const int64_t i = (int64_t)round * gridDim.x + c;
-        if (i >= pairs) return false;
         ++round;
+        next_h = -1;
+        if (i >= pairs) return;
         const int64_t e = i / kv_heads;
-        h = (int)(i - e * kv_heads);
-        const int4 w = *reinterpret_cast<const int4*>(items + e);
-        x = {w.x, w.y, w.z, w.w};
+        next_h = (int)(i - e * kv_heads);
+        next_x = *reinterpret_cast<const int4*>(items + e);
+    }
+    __device__ __forceinline__ bool next() {
+        if (next_h < 0) return false;
+        h = next_h;
+        x = {next_x.x, next_x.y, next_x.z, next_x.w};
+        ahead();
         return true;
     }
     // the key tiles that row tile t sees, 0: it has no rows
@@ -231,7 +242,8 @@ prompts_kernel(const Args a, const __grid_constant__ CUtensorMap qmap, const __g
     volatile int* gone = reinterpret_cast<volatile int*>(tmem_slot + 1);
     int* odds = reinterpret_cast<int*>(sm + S::kOdd);              // [2][2 C + 4]: first tokens, and whether any is noted
 
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // the shuffle tells the compiler that a warp's number is uniform: the products' operands then are, too
+    const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), lane = tid & 31;
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(&qfull[i], 1);
@@ -400,6 +412,17 @@ prompts_kernel(const Args a, const __grid_constant__ CUtensorMap qmap, const __g
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t s_at = tmem + lanes + t * kTile, o_at = tmem + lanes + 256 + t * C;
     unsigned char* stage = sm + S::kOut + warp * S::kOutB;
+    // the rows that this lane writes a quarter of, four at a time: their tokens and their distance from row 0
+    const int64_t heads = (int64_t)a.kv_heads * a.group;
+    int to_token[4];
+    int64_t to_row[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int R = (warp & 3) * 32 + 8 * i + lane / 4;
+        to_token[i] = R / a.group;
+        to_row[i] = to_token[i] * heads + (R - to_token[i] * a.group);
+        if (to_token[i] >= a.tpt) to_token[i] = kNever;
+    }
     int ns = 0, no = 0, pair = 0;                // score tiles, row tiles and pairs so far
     bool ok = true;
     while (ok && w.next()) {
@@ -476,39 +499,46 @@ prompts_kernel(const Args a, const __grid_constant__ CUtensorMap qmap, const __g
             if (!ok) break;
             tc::after_sync();
             const float l = __fadd_rn(lo_of(sum), hi_of(sum)), inv = row_scale(l);
-            const int64_t heads = (int64_t)a.kv_heads * a.group;
             const int64_t base = (int64_t)(w.x.begin + tok) * heads + w.h * a.group;          // of row 0
             const int* odd = odds + (pair & 1) * (2 * C + 4);
             const bool any_odd = odd[2 * C] != 0;
             if (live && a.lse) a.lse[base + token * heads + (row - token * a.group)] = row_lse(m, l);
+            // a row that saw nothing has sums of 0, and inv = 0
+            const u64 inv2 = pk(inv, inv);
 #pragma unroll
-            for (int c = 0; c < C / 32; ++c) {
-                uint32_t y[32];
+            for (int c = 0; c < C / 32; c += 2) {
+                uint32_t y[64];
                 tc::ld32(o_at + 32 * c, y);
+                tc::ld32(o_at + 32 * c + 32, y + 32);
                 tc::wait_ld();
+                if (any_odd) {
 #pragma unroll
-                for (int i = 0; i < 32; ++i) y[i] = __float_as_uint(row_value(__uint_as_float(y[i]), inv));
-                if (any_odd && l != 0.0f) {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        y[i] = __float_as_uint(__fadd_rn(__uint_as_float(y[i]), odd_value(odd, C, 32 * c + i, last)));
+                    for (int i = 0; i < 64; ++i)
+                        if (l != 0.0f)
+                            y[i] = __float_as_uint(__fadd_rn(__uint_as_float(y[i]), odd_value(odd, C, 32 * c + i, last)));
                 }
-                if (c > 0) __syncwarp();         // the piece before has been read
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    uint32_t p[4];
+                for (int b = 0; b < 2; ++b) {
+                    if (c + b > 0) __syncwarp(); // the piece before has been read
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        p[k] = pack_bf16x2(__uint_as_float(y[8 * i + 2 * k]), __uint_as_float(y[8 * i + 2 * k + 1]));
-                    *reinterpret_cast<uint4*>(stage + lane * 64 + ((i ^ (lane >> 1)) & 3) * 16) = make_uint4(p[0], p[1], p[2], p[3]);
-                }
-                __syncwarp();
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t p[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {    // four lanes a row
-                    const int r = 8 * i + lane / 4, q = lane & 3, R = (warp & 3) * 32 + r, tk = R / a.group;
-                    const uint4 x = *reinterpret_cast<const uint4*>(stage + r * 64 + ((q ^ (r >> 1)) & 3) * 16);
-                    if (tk < a.tpt && tok + tk < w.x.len)
-                        *reinterpret_cast<uint4*>(a.out + (base + tk * heads + (R - tk * a.group)) * C + 32 * c + 8 * q) = x;
+                        for (int k = 0; k < 4; ++k) {
+                            const uint32_t* z = y + 32 * b + 8 * i + 2 * k;
+                            const u64 v = mul2(pk(__uint_as_float(z[0]), __uint_as_float(z[1])), inv2);
+                            p[k] = pack_bf16x2(lo_of(v), hi_of(v));
+                        }
+                        *reinterpret_cast<uint4*>(stage + lane * 64 + ((i ^ (lane >> 1)) & 3) * 16) = make_uint4(p[0], p[1], p[2], p[3]);
+                    }
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {                  // four lanes a row
+                        const int r = 8 * i + lane / 4, q = lane & 3;
+                        const uint4 x = *reinterpret_cast<const uint4*>(stage + r * 64 + ((q ^ (r >> 1)) & 3) * 16);
+                        if (to_token[i] < w.x.len - tok)
+                            *reinterpret_cast<uint4*>(a.out + (base + to_row[i]) * C + 32 * (c + b) + 8 * q) = x;
+                    }
                 }
             }
             __syncwarp();
