@@ -569,12 +569,15 @@ attend_rows_kernel(const ChunkArgs A)
             cluster_sync();                      // nobody leaves, or writes the next tile, before all have read
         }
     }
+    // what follows this launch follows the one before, too
+    if constexpr (JOIN) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 template <int C, bool JOIN>
 __global__ void __launch_bounds__(kThreads)
 merge_rows_kernel(const ChunkArgs A, int64_t total)
 {
+    if constexpr (JOIN) asm volatile("griddepcontrol.wait;" ::: "memory");           // the parts
     const int64_t row = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
     if (row >= total) return;
     const int64_t o = row / A.v.rows;
@@ -626,25 +629,33 @@ cudaError_t launch_rows(ChunkArgs A, int64_t outer, cudaStream_t st)
     A.parts = p.nsplit > 1 || A.shared;
     const int64_t grid = outer * p.nsplit;
     if (grid > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
-    A.cluster = p.cluster;
-    cudaLaunchAttribute at;
-    at.id = cudaLaunchAttributeClusterDimension;
-    at.val.clusterDim = {(unsigned)(A.cluster ? p.nsplit : 1), 1, 1};
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)grid);
-    cfg.blockDim = dim3(kThreads);
-    cfg.stream = st;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
-    const cudaError_t e = A.v.rows <= 8 ? cudaLaunchKernelEx(&cfg, attend_rows_kernel<BITS, C, 8, JOIN>, A)
-                          : A.v.rows <= 16 ? cudaLaunchKernelEx(&cfg, attend_rows_kernel<BITS, C, 16, JOIN>, A)
-                                           : cudaLaunchKernelEx(&cfg, attend_rows_kernel<BITS, C, 32, JOIN>, A);
-    if (e != cudaSuccess) return e;
-    if (A.parts && !p.cluster) {
-        const int64_t total = outer * A.v.rows;
-        merge_rows_kernel<C, JOIN><<<(unsigned)((total + kWarps - 1) / kWarps), kThreads, 0, st>>>(A, total);
+    if constexpr (JOIN) {                        // parts, without a cluster
+        const bool early = A.own_part != nullptr;                   // the launch before is the rows kernel of this call
+        const cudaError_t e = A.v.rows <= 8 ? launch_early(attend_rows_kernel<BITS, C, 8, true>, (unsigned)grid, kThreads, st, early, A)
+                              : A.v.rows <= 16 ? launch_early(attend_rows_kernel<BITS, C, 16, true>, (unsigned)grid, kThreads, st, early, A)
+                                               : launch_early(attend_rows_kernel<BITS, C, 32, true>, (unsigned)grid, kThreads, st, early, A);
+        return e != cudaSuccess ? e : launch_merge_rows(A, C, outer, st);
+    } else {
+        A.cluster = p.cluster;
+        cudaLaunchAttribute at;
+        at.id = cudaLaunchAttributeClusterDimension;
+        at.val.clusterDim = {(unsigned)(A.cluster ? p.nsplit : 1), 1, 1};
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)grid);
+        cfg.blockDim = dim3(kThreads);
+        cfg.stream = st;
+        cfg.attrs = &at;
+        cfg.numAttrs = 1;
+        const cudaError_t e = A.v.rows <= 8 ? cudaLaunchKernelEx(&cfg, attend_rows_kernel<BITS, C, 8, false>, A)
+                              : A.v.rows <= 16 ? cudaLaunchKernelEx(&cfg, attend_rows_kernel<BITS, C, 16, false>, A)
+                                               : cudaLaunchKernelEx(&cfg, attend_rows_kernel<BITS, C, 32, false>, A);
+        if (e != cudaSuccess) return e;
+        if (p.nsplit > 1 && !p.cluster) {
+            const int64_t total = outer * A.v.rows;
+            merge_rows_kernel<C, false><<<(unsigned)((total + kWarps - 1) / kWarps), kThreads, 0, st>>>(A, total);
+        }
+        return cudaGetLastError();
     }
-    return cudaGetLastError();
 }
 
 }  // namespace
@@ -755,9 +766,8 @@ cudaError_t launch_merge_rows(const ChunkArgs& A, int64_t C, int64_t outer, cuda
 {
     const int64_t total = outer * A.v.rows, ctas = (total + kWarps - 1) / kWarps;
     if (ctas > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
-    if (C == 128) merge_rows_kernel<128, true><<<(unsigned)ctas, kThreads, 0, st>>>(A, total);
-    else merge_rows_kernel<64, true><<<(unsigned)ctas, kThreads, 0, st>>>(A, total);
-    return cudaGetLastError();
+    return C == 128 ? launch_early(merge_rows_kernel<128, true>, (unsigned)ctas, kThreads, st, true, A, total)
+                    : launch_early(merge_rows_kernel<64, true>, (unsigned)ctas, kThreads, st, true, A, total);
 }
 
 cudaError_t launch_chunk(ChunkArgs A, int bits, int64_t C, int64_t outer, void* ws, cudaStream_t st)

@@ -169,6 +169,22 @@ cudaError_t launch_attend_tc(const ChunkArgs& A, int bits, int64_t C, int64_t ou
 // The attention of kvq_attend_chunk over a cache, its rows into A.out and A.lse, or
 // into A.sums; with A.parts the rows kernel's, which are left in part: nsplit and
 // share are returned in A.
+// A launch that starts while the one before it ends; its kernel waits for that one
+// itself (griddepcontrol.wait).
+template <class... P, class... A>
+cudaError_t launch_early(void (*kernel)(P...), unsigned grid, unsigned threads, cudaStream_t st, bool early, const A&... args) {
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.stream = st;
+    cfg.attrs = &at;
+    cfg.numAttrs = early ? 1 : 0;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
 size_t rows_parts_workspace(int64_t outer, int64_t C, int64_t tmax, int64_t rows);
 cudaError_t launch_rows_parts(ChunkArgs& A, int bits, int64_t C, int64_t outer, cudaStream_t st);
 cudaError_t launch_chunk(ChunkArgs A, int bits, int64_t C, int64_t outer, void* ws, cudaStream_t st);

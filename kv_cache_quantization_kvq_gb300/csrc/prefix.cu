@@ -541,6 +541,7 @@ attend_prefix_kernel(const __grid_constant__ PrefixArgs X)
             if (lane == 0) arrive_first(&pfull[2 * t + (u & 1)]);
         }
         // ---- the row's sums
+        asm volatile("griddepcontrol.launch_dependents;");
         float l = 0.0f;
         if (ok && n > 0) {
             ok = ready(&odone[2 * t + 1], n - 1);

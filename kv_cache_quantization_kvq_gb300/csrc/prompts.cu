@@ -61,6 +61,17 @@ struct Item { int begin, len, tok0, keys; };     // keys: key tiles that its las
 
 struct Plan { int count, pad[63]; };             // and the items behind it
 
+// prompt s, whatever starts holds; its items, and the i-th of them
+__device__ __forceinline__ void prompt_range(const int32_t* starts, int64_t s, int64_t total, int& begin, int& len) {
+    begin = min(max(starts[s], 0), (int)total);
+    len = min(max(starts[s + 1], begin), (int)total) - begin;
+}
+__device__ __forceinline__ int items_of(int len, int tpt) { return (int)(((int64_t)len + 2 * tpt - 1) / (2 * tpt)); }
+__device__ __forceinline__ Item item_at(int begin, int len, int i, int tpt) {
+    const int tok0 = i * 2 * tpt;
+    return Item{begin, len, tok0, (min(tok0 + 2 * tpt, len) + kTile - 1) / kTile};
+}
+
 constexpr int kPlanThreads = 1024;
 constexpr int kBuckets = 64 + 19 * 16;           // of numbers of key tiles: exact below 64, in sixteenths of powers of 2 above
 constexpr int kAlone = 8;                        // items of a prompt that its thread makes; a warp shares the others
@@ -86,21 +97,14 @@ plan_kernel(const int32_t* starts, int64_t prompts, int64_t total, int tpt, int 
         for (int64_t s0 = 0; s0 < prompts; s0 += kPlanThreads) {
             const int64_t s = s0 + tid;
             int begin = 0, len = 0;
-            if (s < prompts) {
-                begin = min(max(starts[s], 0), (int)total);
-                len = min(max(starts[s + 1], begin), (int)total) - begin;
-            }
-            auto item = [&](int b, int n, int i) {
-                const int tok0 = i * 2 * tpt;
-                use(Item{b, n, tok0, (min(tok0 + 2 * tpt, n) + kTile - 1) / kTile});
-            };
-            const int n = (int)(((int64_t)len + 2 * tpt - 1) / (2 * tpt));
-            for (int i = 0; i < min(n, kAlone); ++i) item(begin, len, i);
+            if (s < prompts) prompt_range(starts, s, total, begin, len);
+            const int n = items_of(len, tpt);
+            for (int i = 0; i < min(n, kAlone); ++i) use(item_at(begin, len, i, tpt));
             for (uint32_t more = __ballot_sync(0xFFFFFFFFu, n > kAlone); more; more &= more - 1) {
                 const int from = __ffs(more) - 1;
                 const int b = __shfl_sync(0xFFFFFFFFu, begin, from), l = __shfl_sync(0xFFFFFFFFu, len, from);
                 const int m = __shfl_sync(0xFFFFFFFFu, n, from);
-                for (int i = kAlone + lane; i < m; i += 32) item(b, l, i);
+                for (int i = kAlone + lane; i < m; i += 32) use(item_at(b, l, i, tpt));
             }
         }
     };
@@ -146,7 +150,9 @@ struct Smem {
 struct Args {
     __nv_bfloat16* out;
     float* lse;                                  // or nullptr
-    const Plan* plan;
+    const Plan* plan;                            // or nullptr: a CTA has at most one pair, and finds it itself
+    const int32_t* starts;
+    int64_t prompts, total;
     int32_t group, kv_heads, tpt;
     float scale2;                                // log2(e) / sqrt(C)
 };
@@ -161,9 +167,14 @@ struct Walk {
     int h;
     int4 next_x;
     int next_h;                                  // -1: there is none
-    __device__ __forceinline__ explicit Walk(const Args& a)
-        : items(reinterpret_cast<const Item*>(a.plan + 1)), pairs((int64_t)a.plan->count * a.kv_heads), kv_heads(a.kv_heads), round(0) {
-        ahead();
+    __device__ __forceinline__ explicit Walk(const Args& a) : items(reinterpret_cast<const Item*>(a.plan + 1)), kv_heads(a.kv_heads), round(0) {
+        if (a.plan) {
+            pairs = (int64_t)a.plan->count * a.kv_heads;
+            ahead();
+        } else {
+            pairs = 0;
+            find(a);
+        }
     }
     __device__ __forceinline__ void ahead() {
         const int c = round & 1 ? (int)gridDim.x - 1 - (int)blockIdx.x : (int)blockIdx.x;
@@ -175,11 +186,39 @@ struct Walk {
         next_h = (int)(i - e * kv_heads);
         next_x = *reinterpret_cast<const int4*>(items + e);
     }
+    // the item blockIdx.x / kv_heads of the prompts in their order, by a whole warp
+    __device__ __forceinline__ void find(const Args& a) {
+        const int lane = threadIdx.x & 31;
+        int64_t e = blockIdx.x / kv_heads;
+        next_h = -1;
+        for (int64_t s0 = 0; s0 < a.prompts; s0 += 32) {
+            int begin = 0, len = 0;
+            if (s0 + lane < a.prompts) prompt_range(a.starts, s0 + lane, a.total, begin, len);
+            const int n = items_of(len, a.tpt);
+            int64_t upto = n;
+#pragma unroll
+            for (int d = 1; d < 32; d *= 2) {
+                const int64_t v = __shfl_up_sync(0xFFFFFFFFu, upto, d);
+                if (lane >= d) upto += v;
+            }
+            const uint32_t beyond = __ballot_sync(0xFFFFFFFFu, upto > e);
+            if (beyond) {
+                const int at = __ffs(beyond) - 1;
+                begin = __shfl_sync(0xFFFFFFFFu, begin, at);
+                len = __shfl_sync(0xFFFFFFFFu, len, at);
+                const Item it = item_at(begin, len, (int)(e - __shfl_sync(0xFFFFFFFFu, upto - n, at)), a.tpt);
+                next_x = make_int4(it.begin, it.len, it.tok0, it.keys);
+                next_h = (int)blockIdx.x % kv_heads;
+                return;
+            }
+            e -= __shfl_sync(0xFFFFFFFFu, upto, 31);
+        }
+    }
     __device__ __forceinline__ bool next() {
         if (next_h < 0) return false;
         h = next_h;
         x = {next_x.x, next_x.y, next_x.z, next_x.w};
-        ahead();
+        ahead();                                 // without a plan pairs is 0
         return true;
     }
     // the key tiles that row tile t sees, 0: it has no rows
@@ -588,11 +627,16 @@ cudaError_t launch(const PromptArgs& p, Plan* plan, cudaStream_t st)
     if (e != cudaSuccess) return e;
     const int64_t cap = most_items(p.prompts, p.total, p.group);
     if (cap > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
-    plan_kernel<<<1, kPlanThreads, 0, st>>>(p.starts, p.prompts, p.total, tpt, (int)cap, plan);
+    const int64_t grid = std::min<int64_t>(sm_count(), cap * p.kv_heads);
+    const bool planned = cap * p.kv_heads > grid || p.prompts > 1024;                 // else one launch (17 tokens 9.0 -> 6.4 us in a graph)
+    if (planned) plan_kernel<<<1, kPlanThreads, 0, st>>>(p.starts, p.prompts, p.total, tpt, (int)cap, plan);
     Args a;
     a.out = static_cast<__nv_bfloat16*>(p.out);
     a.lse = p.lse;
-    a.plan = plan;
+    a.plan = planned ? plan : nullptr;
+    a.starts = p.starts;
+    a.prompts = p.prompts;
+    a.total = p.total;
     a.group = (int32_t)p.group;
     a.kv_heads = (int32_t)p.kv_heads;
     a.tpt = tpt;
@@ -602,12 +646,12 @@ cudaError_t launch(const PromptArgs& p, Plan* plan, cudaStream_t st)
     at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)std::min<int64_t>(sm_count(), cap * p.kv_heads));
+    cfg.gridDim = dim3((unsigned)grid);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = Smem<C>::kBytes;
     cfg.stream = st;
     cfg.attrs = &at;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = planned ? 1 : 0;
     e = cudaLaunchKernelEx(&cfg, prompts_kernel<C>, a, qm, km, vm);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
