@@ -161,30 +161,32 @@ struct Half {
         return KEYS ? p / 8 * (64 * 128) + tc::swizzled(row, p % 8) : tc::swizzled(row, p % 8);
     }
 
-    // the copies, by one warp
+    // the copies, by one warp: tile j's into its stage
+    __device__ __forceinline__ void issue(int j, unsigned char* raw, uint64_t* full) const {
+        const int s = (j - ja) % kStages;
+        unsigned char* dst = raw + s * kRaw;
+        if constexpr (KEYS) {                    // 32 tokens are of one group
+            mbar_expect_tx(&full[s], 64 * kRowB + (a.kz ? 4 : 2) * C * 2);
+            for (int q = 0; q < 2; ++q) {
+                const int64_t t = token(j, 32 * q), g = (o * a.ngk + t / a.gk) * C;
+                bulk_g2s(dst + 32 * q * kRowB, codes + t * kRowB, 32 * kRowB, &full[s]);
+                bulk_g2s(dst + 64 * kRowB + q * C * 2, a.ks + g, C * 2, &full[s]);
+                if (a.kz) bulk_g2s(dst + 64 * kRowB + (2 + q) * C * 2, a.kz + g, C * 2, &full[s]);
+            }
+        } else {
+            mbar_expect_tx(&full[s], kTile * kRowB);
+            bulk_g2s(dst, codes + (int64_t)j * kTile * kRowB, kTile * kRowB, &full[s]);
+        }
+        // into L2 some tiles ahead: the first CTA fetches keys, the second values
+        if (j + 8 < jb && c == (KEYS ? 0 : 1)) bulk_prefetch_l2(codes + (int64_t)(j + 8) * kTile * kRowB, kTile * kRowB);
+    }
     template <class Ready>
     __device__ __forceinline__ void copy(unsigned char* raw, uint64_t* full, uint64_t* free, const Ready& ready) const {
         int j = ja;
         for (; j < jb; ++j) {
-            const int k = j - ja, s = k % kStages;
-            if (k >= kStages && !ready(&free[s], (k / kStages - 1) & 1)) break;
-            if (tc::elect()) {
-                unsigned char* dst = raw + s * kRaw;
-                if constexpr (KEYS) {            // 32 tokens are of one group
-                    mbar_expect_tx(&full[s], 64 * kRowB + (a.kz ? 4 : 2) * C * 2);
-                    for (int q = 0; q < 2; ++q) {
-                        const int64_t t = token(j, 32 * q), g = (o * a.ngk + t / a.gk) * C;
-                        bulk_g2s(dst + 32 * q * kRowB, codes + t * kRowB, 32 * kRowB, &full[s]);
-                        bulk_g2s(dst + 64 * kRowB + q * C * 2, a.ks + g, C * 2, &full[s]);
-                        if (a.kz) bulk_g2s(dst + 64 * kRowB + (2 + q) * C * 2, a.kz + g, C * 2, &full[s]);
-                    }
-                } else {
-                    mbar_expect_tx(&full[s], kTile * kRowB);
-                    bulk_g2s(dst, codes + (int64_t)j * kTile * kRowB, kTile * kRowB, &full[s]);
-                }
-                // into L2 some tiles ahead: the first CTA fetches keys, the second values
-                if (j + 8 < jb && c == (KEYS ? 0 : 1)) bulk_prefetch_l2(codes + (int64_t)(j + 8) * kTile * kRowB, kTile * kRowB);
-            }
+            const int k = j - ja;
+            if (k >= kStages && !ready(&free[k % kStages], (k / kStages - 1) & 1)) break;
+            if (tc::elect()) issue(j, raw, full);
             __syncwarp();
         }
         // before the shared memory goes: every copy issued has landed
@@ -382,16 +384,31 @@ attend_prefix_kernel(const __grid_constant__ PrefixArgs X)
         *gone = 0;
         mbar_init_fence();
     }
-    if (warp == 8) alloc_pair(tmem_slot, 512);
     for (int i = tid; i <= 2 * C; i += kThreads) odd[i] = i < 2 * C ? kNever : 0;
-    if (warp < 12)
-        for (int k = tid; k < nt * kTile * (C / 8); k += 384) {
-            const int t = k / (kTile * (C / 8)), row = k / (C / 8) % kTile, p = k % (C / 8);
-            const int r = r0 + t * 256 + rank * kTile + row;
-            uint4 x = make_uint4(0, 0, 0, 0);
-            if (r < a.rows) x = interleave(*reinterpret_cast<const uint4*>(a.q + row_index<true>(a, o, r) * C + p * 8));
-            *reinterpret_cast<uint4*>(sm + S::kQ + t * S::kQB + (p / 8) * (kTile * 128) + tc::swizzled(row, p % 8)) = x;
+    if (warp == 8) alloc_pair(tmem_slot, 512);
+    if (tid == 352 && n > 0 && j0 * kTile < a.tq)                  // the first codes into L2, while the CTAs meet
+        bulk_prefetch_l2((rank ? a.vc : a.kc) + ((uint64_t)o * a.cap + j0 * kTile) * S::kRowB, min(8 * kTile, (a.tq - j0 * kTile)) * S::kRowB);
+    {
+        // the queries, four of a thread's pieces in flight at once
+        constexpr int kEach = 4;
+#pragma unroll 1
+        for (int k0 = tid; k0 < nt * kTile * (C / 8); k0 += kEach * kThreads) {
+            uint4 x[kEach];
+#pragma unroll
+            for (int i = 0; i < kEach; ++i) {
+                const int k = k0 + i * kThreads, t = k / (kTile * (C / 8)), row = k / (C / 8) % kTile, p = k % (C / 8);
+                const int r = r0 + t * 256 + rank * kTile + row;
+                x[i] = make_uint4(0, 0, 0, 0);
+                if (t < nt && r < a.rows) x[i] = *reinterpret_cast<const uint4*>(a.q + row_index<true>(a, o, r) * C + p * 8);
+            }
+#pragma unroll
+            for (int i = 0; i < kEach; ++i) {
+                const int k = k0 + i * kThreads, t = k / (kTile * (C / 8)), row = k / (C / 8) % kTile, p = k % (C / 8);
+                if (t < nt)
+                    *reinterpret_cast<uint4*>(sm + S::kQ + t * S::kQB + (p / 8) * (kTile * 128) + tc::swizzled(row, p % 8)) = interleave(x[i]);
+            }
         }
+    }
     tc::async_fence();
     tc::before_sync();
     __syncthreads();
@@ -548,9 +565,14 @@ attend_prefix_kernel(const __grid_constant__ PrefixArgs X)
             tc::after_sync();
             l = __fadd_rn(lo_of(sum), hi_of(sum));
         }
-        const bool write = ok && r < a.rows;
-        float* part = A.part + ((o * a.rows + r) * A.nsplit + split) * (C + 4);
-#pragma unroll
+        // By way of shared memory, 32 channels at a time, so that a warp writes 128 bytes of a row side by side (a row
+        // per lane took 9 us): the row tile's queries are not needed any more.  Pieces of 16 bytes, in places that a
+        // row's number permutes.
+        unsigned char* stage = sm + S::kQ + t * S::kQB + (warp & 3) * (32 * 128);
+        float* part = A.part + ((o * a.rows + (r - lane)) * A.nsplit + split) * (C + 4);     // of the warp's first row
+        const int64_t pitch = (int64_t)A.nsplit * (C + 4);
+        const int rows = ok ? min(32, a.rows - (r - lane)) : 0;              // that exist
+#pragma unroll 1
         for (int i = 0; i < C / 32; ++i) {
             uint32_t y[32];
             if (ok && n > 0) {
@@ -560,17 +582,23 @@ attend_prefix_kernel(const __grid_constant__ PrefixArgs X)
 #pragma unroll
                 for (int e = 0; e < 32; ++e) y[e] = 0u;
             }
-            if (write) {
+            __syncwarp();                        // the piece before has been read
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {    // channels 0 .. 7 sit in columns 0 2 4 6 1 3 5 7
-                    const uint32_t* z = y + 8 * e;
-                    *reinterpret_cast<uint4*>(part + 32 * i + 8 * e) = make_uint4(z[0], z[2], z[4], z[6]);
-                    *reinterpret_cast<uint4*>(part + 32 * i + 8 * e + 4) = make_uint4(z[1], z[3], z[5], z[7]);
-                }
+            for (int e = 0; e < 4; ++e) {        // channels 0 .. 7 sit in columns 0 2 4 6 1 3 5 7
+                const uint32_t* z = y + 8 * e;
+                *reinterpret_cast<uint4*>(stage + lane * 128 + ((2 * e) ^ (lane & 7)) * 16) = make_uint4(z[0], z[2], z[4], z[6]);
+                *reinterpret_cast<uint4*>(stage + lane * 128 + ((2 * e + 1) ^ (lane & 7)) * 16) = make_uint4(z[1], z[3], z[5], z[7]);
             }
-            __syncwarp();                        // the next load wants the whole warp
+            __syncwarp();
+#pragma unroll 4
+            for (int e = 0; e < 8; ++e) {        // four rows at a time
+                const int row = 4 * e + lane / 8, p = lane & 7;
+                if (row < rows)
+                    *reinterpret_cast<uint4*>(part + row * pitch + 32 * i + 4 * p) =
+                        *reinterpret_cast<const uint4*>(stage + row * 128 + (p ^ (row & 7)) * 16);
+            }
         }
-        if (write) *reinterpret_cast<float2*>(part + C) = make_float2(m, l);
+        if (lane < rows) *reinterpret_cast<float2*>(part + lane * pitch + C) = make_float2(m, l);
     }
     __syncwarp();
     tc::before_sync();
