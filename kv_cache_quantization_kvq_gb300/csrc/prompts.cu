@@ -277,7 +277,8 @@ prompts_kernel(const Args a, const __grid_constant__ CUtensorMap qmap, const __g
     uint64_t* pfull = sfull + 2;                 // [2] its weights are
     uint64_t* odone = pfull + 2;                 // [2] its output is complete
     uint64_t* wrote = odone + 2;                 // [2] the softmax warps are done with a pair (pairs alternate)
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(wrote + 2);
+    uint64_t* clear = wrote + 2;                 // [2] nothing is noted for a pair yet
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(clear + 2);
     volatile int* gone = reinterpret_cast<volatile int*>(tmem_slot + 1);
     int* odds = reinterpret_cast<int*>(sm + S::kOdd);              // [2][2 C + 4]: first tokens, and whether any is noted
 
@@ -296,6 +297,7 @@ prompts_kernel(const Args a, const __grid_constant__ CUtensorMap qmap, const __g
             mbar_init(&pfull[i], 4);
             mbar_init(&odone[i], 2);
             mbar_init(&wrote[i], 8);
+            mbar_init(&clear[i], 1);
         }
         *gone = 0;
         mbar_init_fence();
@@ -422,6 +424,7 @@ prompts_kernel(const Args a, const __grid_constant__ CUtensorMap qmap, const __g
             if (pair >= 2) ok = ready(&wrote[pair & 1], (pair >> 1) - 1);
             for (int c = lane; c <= 2 * C; c += 32) odd[c] = c < 2 * C ? kNever : 0;
             __syncwarp();
+            if (ok && lane == 0) mbar_arrive(&clear[pair & 1]);
             ++pair;
             for (int j = 0; ok && j < w.x.keys; ++j) {
                 ok = ready(&vfull[nv & 1], nv >> 1);
@@ -582,7 +585,10 @@ prompts_kernel(const Args a, const __grid_constant__ CUtensorMap qmap, const __g
             }
             __syncwarp();
         }
-        if (lane == 0) mbar_arrive(&wrote[pair & 1]);
+        // warps of a row tile without rows have waited for nothing: they must not run ahead of the others, and arrive
+        // for a pair whose barrier still counts the one before the last
+        ok = ready(&clear[pair & 1], pair >> 1);
+        if (ok && lane == 0) mbar_arrive(&wrote[pair & 1]);
         ++pair;
     }
     }

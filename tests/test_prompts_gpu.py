@@ -54,6 +54,16 @@ CASES = {
     "long": ([1500], 1, 2, 128, {}),
     "long, C 64": ([1111, 400], 1, 3, 64, {}),
     "many prompts": ([(i * 37) % 50 for i in range(300)], 1, 2, 64, {}),
+    # more pairs than SMs, so that a plan is made: prompts whose items a warp shares, and last items of one row tile
+    "planned": ([1400, 300, 77], 4, 8, 64, {}),
+    "planned, C 128": ([900, 40, 513], 3, 8, 128, dict(fused=True)),
+    "planned, one query head": ([700, 515, 5], 40, 1, 128, {}),
+    "many pairs of one row tile a CTA": ([1 + i % 7 for i in range(900)], 3, 2, 64, {}),
+    "many pairs of two row tiles a CTA": ([129 + i % 7 for i in range(260)], 5, 1, 64, {}),
+    "lone last row tiles": ([1100, 1030, 260], 2, 1, 128, {}),
+    "lone last row tiles, C 64": ([770, 1030], 2, 2, 64, {}),
+    "more prompts than a pass of the plan": ([i % 3 for i in range(1500)], 1, 1, 64, {}),
+    "planned, rows outside": ([333, 0, 500, 1], 8, 8, 64, dict(before=3, behind=50)),
 }
 
 
@@ -105,6 +115,7 @@ def test_attend_prompts(b, name):
     check(name, P.f64(out), gl, x, starts, Hk, G)
     for s in (slice(0, starts[0]), slice(starts[-1], total)):
         assert (bits[s] == SENTINEL).all() and (gl[s] == -7.0).all(), "rows of tokens in no prompt were written"
+    assert b.kvq_wait_timeouts() == 0
 
 
 def test_default_arguments_and_equal_bits(b):

@@ -65,6 +65,23 @@ CASES = {
     "padded prefix": (12, 2, 4, 1, 128, (256, 20, {}), (64, 20, {}), dict(pfirst=[100, 270])),
     "hidden prefix": (12, 2, 4, 1, 128, (256, 20, {}), (64, 20, {}), dict(pfirst=[999, 0])),
     "own tokens split too": (2, 1, 4, 1, 128, (512, 0, {}), (5056, 40, {}), {}),
+    # the forms that pairs of SMs read: groups, kinds and ends of a prefix
+    "pairs, key groups of 32": (10, 1, 8, 1, 128, (672, 9, dict(gk=32, gv=32)), (0, 9, {}), {}),
+    "pairs, key groups of 96": (10, 2, 8, 1, 128, (960, 0, dict(gk=96, gv=128)), (0, 9, {}), {}),
+    "pairs, key groups of 128, symmetric": (10, 1, 8, 1, 128, (896, 70, dict(gk=128, kind="sym")), (64, 9, {}), {}),
+    "pairs, signed": (10, 1, 8, 1, 128, (512, 129, dict(kind="signed", gv=32)), (0, 9, {}), {}),
+    "pairs, two bits": (40, 1, 8, 1, 128, (448, 1, dict(bits=2, gk=64, gv=128)), (64, 9, {}), dict(ragged=True)),
+    "pairs, two bits, symmetric": (70, 1, 8, 1, 128, (704, 33, dict(bits=2, kind="sym", gk=32, gv=32)), (0, 9, {}), {}),
+    "pairs, one tile": (10, 1, 8, 1, 128, (64, 30, {}), (0, 9, {}), {}),
+    "pairs, buffer only": (10, 1, 8, 1, 128, (0, 61, {}), (0, 9, {}), {}),
+    "pairs, padded": (20, 3, 4, 1, 128, (640, 60, {}), (0, 9, {}), dict(pfirst=[64, 130, 655])),
+    "pairs, hidden": (20, 2, 4, 1, 128, (640, 60, {}), (0, 9, {}), dict(pfirst=[700, 699])),
+    "pairs, far zero points": (20, 1, 4, 1, 128, (512, 20, {}), (0, 9, {}), dict(shift=100.0)),
+    "pairs, 257 rows": (257, 1, 1, 1, 128, (256, 20, {}), (0, 3, {}), {}),
+    "pairs, 2000 rows, split": (250, 1, 8, 1, 128, (2048, 100, {}), (0, 9, {}), dict(ragged=True)),
+    "2100 rows": (300, 1, 7, 1, 128, (512, 100, {}), (0, 9, {}), {}),
+    "2100 rows of chunks": (6, 1, 7, 50, 128, (512, 100, {}), (64, 20, {}), dict(first=[0, 80, 33, 1, 84, 20])),
+    "2100 rows, split": (1, 1, 7, 300, 128, (4096, 100, {}), "joined", {}),
 }
 
 
@@ -182,7 +199,8 @@ def test_in_place_and_default_arguments(b, name):
         assert torch.equal(own[0], want[0]) and torch.equal(own[1], want[1])
 
 
-@pytest.mark.parametrize("name", ["few requests", "32 rows", "200 rows", "600 rows", "chunks", "joined, prompts", "long, split"])
+@pytest.mark.parametrize("name", ["few requests", "32 rows", "200 rows", "600 rows", "chunks", "joined, prompts", "long, split",
+                                  "pairs, two bits", "2100 rows of chunks"])
 def test_captured_and_on_two_streams(b, name):
     """Two captured graphs with a workspace each, replayed on two streams, give the bits of an eager call."""
     import torch
@@ -225,6 +243,43 @@ def test_values_that_are_not_finite(b):
         ok[..., 7] = False
         ok[1, 1, :, 9] = False
         assert torch.isfinite(out[ok]).all()
+
+
+def test_stored_values_that_are_not_finite(b):
+    """Scales of the prefix's values that are infinite or NaN: every channel of their group, in every row, whichever of
+    a pair's SMs has the channels; and NaN in hidden tokens reaches nothing."""
+    import torch
+    for B in (3, 40, 300):
+        rng = np.random.default_rng(B)
+        H, G, C = 1, 8, 128
+        pre = S.HostCache(rng, H, C, 512, 512, 20, 64, *S.formats(gv=32))
+        q = P.upload_bf16(S.W.to_bf16_bits(rng.standard_normal((B, 1, H * G, C)).astype(np.float32)))
+        pre.v[1][0, :100] = 0x7FC0               # padding
+        pre.v[3][0, 20:] = 0x7FC0                # behind the filled rows
+        want = b.attend_shared(q, pre.device(b, H, [100]))
+        assert torch.isfinite(want[0]).all() and torch.isfinite(want[1]).all()
+        pre.v[1][0, 300, 1] = 0x7FC0             # channels 32 .. 63 of a token
+        pre.v[1][0, 433, 3] = 0x7FC0             # channels 96 .. 127 of one in another half tile
+        out, lse = b.attend_shared(q, pre.device(b, H, [100]))
+        assert torch.equal(lse, want[1])
+        nan = torch.zeros(C, dtype=torch.bool, device="cuda")
+        nan[32:64] = nan[96:] = True
+        assert out[..., nan].isnan().all() and torch.equal(out[..., ~nan], want[0][..., ~nan])
+
+
+def test_keys_that_are_nan(b):
+    """A prefix key of NaN makes NaN of the KV head that has it, whatever the own tokens say, and of no other."""
+    import torch
+    for B in (3, 40, 300):
+        rng = np.random.default_rng(B)
+        H, G, C = 2, 8, 128
+        pre = S.HostCache(rng, H, C, 256, 256, 20, 64, *S.formats())
+        own = S.HostCache(rng, B * H, C, 0, 64, 9, 64, *S.formats())
+        pre.k[3][1, 7, 5] = 0x7FC0
+        q = P.upload_bf16(S.W.to_bf16_bits(rng.standard_normal((B, 1, H * G, C)).astype(np.float32)))
+        out, lse = b.attend_shared(q, pre.device(b, H), own.device(b, H))
+        assert torch.isfinite(out[:, :, :G]).all() and torch.isfinite(lse[:, :, :G]).all()
+        assert out[:, :, G:].isnan().all() and lse[:, :, G:].isnan().all()
 
 
 def test_rows_that_are_nan_stay_nan(b):
