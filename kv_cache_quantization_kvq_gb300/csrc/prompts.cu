@@ -182,7 +182,7 @@ struct Walk {
         ++round;
         next_h = -1;
         if (i >= pairs) return;
-        const int64_t e = i / kv_heads;
+        const int64_t e = i >> 32 ? i / kv_heads : (int64_t)((uint32_t)i / (uint32_t)kv_heads);
         next_h = (int)(i - e * kv_heads);
         next_x = *reinterpret_cast<const int4*>(items + e);
     }
@@ -547,40 +547,37 @@ prompts_kernel(const Args a, const __grid_constant__ CUtensorMap qmap, const __g
             if (live && a.lse) a.lse[base + token * heads + (row - token * a.group)] = row_lse(m, l);
             // a row that saw nothing has sums of 0, and inv = 0
             const u64 inv2 = pk(inv, inv);
-#pragma unroll
-            for (int c = 0; c < C / 32; c += 2) {
-                uint32_t y[64];
+            // rolled: unrolled it is as much code again as the loop above, and fetched anew for every pair
+#pragma unroll 1
+            for (int c = 0; c < C / 32; ++c) {
+                uint32_t y[32];
                 tc::ld32(o_at + 32 * c, y);
-                tc::ld32(o_at + 32 * c + 32, y + 32);
                 tc::wait_ld();
-                if (any_odd) {
+                __syncwarp();                    // the piece before has been read
 #pragma unroll
-                    for (int i = 0; i < 64; ++i)
-                        if (l != 0.0f)
-                            y[i] = __float_as_uint(__fadd_rn(__uint_as_float(y[i]), odd_value(odd, C, 32 * c + i, last)));
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t p[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const u64 v = mul2(pk(__uint_as_float(y[8 * i + 2 * k]), __uint_as_float(y[8 * i + 2 * k + 1])), inv2);
+                        p[k] = pack_bf16x2(lo_of(v), hi_of(v));
+                    }
+                    *reinterpret_cast<uint4*>(stage + lane * 64 + ((i ^ (lane >> 1)) & 3) * 16) = make_uint4(p[0], p[1], p[2], p[3]);
                 }
-#pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    if (c + b > 0) __syncwarp(); // the piece before has been read
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        uint32_t p[4];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const uint32_t* z = y + 32 * b + 8 * i + 2 * k;
-                            const u64 v = mul2(pk(__uint_as_float(z[0]), __uint_as_float(z[1])), inv2);
-                            p[k] = pack_bf16x2(lo_of(v), hi_of(v));
-                        }
-                        *reinterpret_cast<uint4*>(stage + lane * 64 + ((i ^ (lane >> 1)) & 3) * 16) = make_uint4(p[0], p[1], p[2], p[3]);
+                if (any_odd && l != 0.0f) {      // what the row sees of values that are not finite
+#pragma unroll 1
+                    for (int i = 0; i < 32; ++i) {
+                        const float x = odd_value(odd, C, 32 * c + i, last);
+                        __nv_bfloat16* v = reinterpret_cast<__nv_bfloat16*>(stage + lane * 64 + ((i / 8 ^ (lane >> 1)) & 3) * 16) + i % 8;
+                        if (x != 0.0f) *v = __float2bfloat16_rn(__fadd_rn(__bfloat162float(*v), x));
                     }
-                    __syncwarp();
+                }
+                __syncwarp();
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {                  // four lanes a row
-                        const int r = 8 * i + lane / 4, q = lane & 3;
-                        const uint4 x = *reinterpret_cast<const uint4*>(stage + r * 64 + ((q ^ (r >> 1)) & 3) * 16);
-                        if (to_token[i] < w.x.len - tok)
-                            *reinterpret_cast<uint4*>(a.out + (base + to_row[i]) * C + 32 * (c + b) + 8 * q) = x;
-                    }
+                for (int i = 0; i < 4; ++i) {    // four lanes a row
+                    const int r = 8 * i + lane / 4, q = lane & 3;
+                    const uint4 x = *reinterpret_cast<const uint4*>(stage + r * 64 + ((q ^ (r >> 1)) & 3) * 16);
+                    if (to_token[i] < w.x.len - tok) *reinterpret_cast<uint4*>(a.out + (base + to_row[i]) * C + 32 * c + 8 * q) = x;
                 }
             }
             __syncwarp();
