@@ -17,6 +17,10 @@
 // 11 copy the codes by bulk copies; warps 12-15 unpack keys and 16-19 values.  Every row sees every token that
 // exists, so only the first and the last tile are masked.  Each split leaves (y, m, l) per row,
 // joined in merge_rows_kernel (chunk.cu).
+//
+// Measured on one GB300: 128 requests x 4 heads, 4 bits, over a prefix of 131072 tokens of 8 KV heads 220 us
+// (1.25 PFLOP/s of products; the call, with its own tokens and the joining, 245).  What bounds it is the chain
+// scores -> weights -> value product of a row tile, of which an SM has two.
 #include <algorithm>
 
 #include "kvq_chunk.cuh"
@@ -672,7 +676,11 @@ cudaError_t launch(PrefixArgs X, int64_t outer, cudaStream_t st)
 
 }  // namespace
 
-bool prefix_uses_pairs(int64_t dim, int64_t rows) { return dim == C && rows > 32 && rows <= 2048; }
+// Below, an SM's tensor memory holds the rows of a tile by itself; above, one expansion costs less than unpacking for
+// every 512 rows.  8 slices of 8192 | 32768 tokens and 2 of 65536, in us, pairs against the other forms (chunk.cu, prefill.cu):
+// 64 rows 26 : 24 | 60 : 50 | 37 : 37, 128 rows 27 : 27 | 61 : 52 | 38 : 39, 256 rows 28 : 35 | 61 : 65 | 39 : 48,
+// 2048 rows 77 : 88 | 238 : 265 | 112 : 129, 3000 rows 115 : 130 | 323 : 326 | 160 : 165, 4096 rows 135 : 112 | 441 : 397 | 219 : 226.
+bool prefix_uses_pairs(int64_t dim, int64_t rows) { return dim == C && rows > 128 && rows <= 2048; }
 
 size_t prefix_workspace(int64_t outer, int64_t tmax, int64_t rows)
 {

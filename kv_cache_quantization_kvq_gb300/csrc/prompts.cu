@@ -33,6 +33,10 @@
 // added when it is written.
 // The weights enter the value product as one bf16 (its operands are of one type): an
 // error of 2^-8 of each weight at most, the size of out's own rounding.
+//
+// Measured on one GB300 (C = 128, 8 KV heads x 4): one prompt of 32768 tokens 5.6 ms (1.57 PFLOP/s, tensor cores
+// bound), 64 prompts of 16 to 2000 tokens 270 us, one of 17 tokens 7.2 us (a launch's way through one tile).
+// Key tiles of 64 tokens: 6.6 ms | 262 us; the scores' halves handed over one by one: 6.06 ms.
 #include <algorithm>
 
 #include <cuda.h>
@@ -631,7 +635,9 @@ cudaError_t launch(const PromptArgs& p, Plan* plan, cudaStream_t st)
     const int64_t cap = most_items(p.prompts, p.total, p.group);
     if (cap > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
     const int64_t grid = std::min<int64_t>(sm_count(), cap * p.kv_heads);
-    const bool planned = cap * p.kv_heads > grid || p.prompts > 1024;                 // else one launch (17 tokens 9.0 -> 6.4 us in a graph)
+    // else every CTA finds its pair by itself, one launch: a prompt of 17 | 600 | 2400 tokens 9.7 -> 7.1, 19.4 -> 16.4,
+    // 39.6 -> 37.2 us in a graph; with more prompts, all but a few of them empty, it would look through them for longer
+    const bool planned = cap * p.kv_heads > grid || p.prompts > 1024;
     if (planned) plan_kernel<<<1, kPlanThreads, 0, st>>>(p.starts, p.prompts, p.total, tpt, (int)cap, plan);
     Args a;
     a.out = static_cast<__nv_bfloat16*>(p.out);

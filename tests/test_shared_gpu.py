@@ -66,19 +66,25 @@ CASES = {
     "hidden prefix": (12, 2, 4, 1, 128, (256, 20, {}), (64, 20, {}), dict(pfirst=[999, 0])),
     "own tokens split too": (2, 1, 4, 1, 128, (512, 0, {}), (5056, 40, {}), {}),
     # the forms that pairs of SMs read: groups, kinds and ends of a prefix
-    "pairs, key groups of 32": (10, 1, 8, 1, 128, (672, 9, dict(gk=32, gv=32)), (0, 9, {}), {}),
-    "pairs, key groups of 96": (10, 2, 8, 1, 128, (960, 0, dict(gk=96, gv=128)), (0, 9, {}), {}),
-    "pairs, key groups of 128, symmetric": (10, 1, 8, 1, 128, (896, 70, dict(gk=128, kind="sym")), (64, 9, {}), {}),
-    "pairs, signed": (10, 1, 8, 1, 128, (512, 129, dict(kind="signed", gv=32)), (0, 9, {}), {}),
+    "pairs, key groups of 32": (20, 1, 8, 1, 128, (672, 9, dict(gk=32, gv=32)), (0, 9, {}), {}),
+    "pairs, key groups of 96": (20, 2, 8, 1, 128, (960, 0, dict(gk=96, gv=128)), (0, 9, {}), {}),
+    "pairs, key groups of 128, symmetric": (20, 1, 8, 1, 128, (896, 70, dict(gk=128, kind="sym")), (64, 9, {}), {}),
+    "pairs, signed": (20, 1, 8, 1, 128, (512, 129, dict(kind="signed", gv=32)), (0, 9, {}), {}),
     "pairs, two bits": (40, 1, 8, 1, 128, (448, 1, dict(bits=2, gk=64, gv=128)), (64, 9, {}), dict(ragged=True)),
     "pairs, two bits, symmetric": (70, 1, 8, 1, 128, (704, 33, dict(bits=2, kind="sym", gk=32, gv=32)), (0, 9, {}), {}),
-    "pairs, one tile": (10, 1, 8, 1, 128, (64, 30, {}), (0, 9, {}), {}),
-    "pairs, buffer only": (10, 1, 8, 1, 128, (0, 61, {}), (0, 9, {}), {}),
+    "pairs, one tile": (20, 1, 8, 1, 128, (64, 30, {}), (0, 9, {}), {}),
+    "pairs, buffer only": (20, 1, 8, 1, 128, (0, 61, {}), (0, 9, {}), {}),
     "pairs, padded": (20, 3, 4, 1, 128, (640, 60, {}), (0, 9, {}), dict(pfirst=[64, 130, 655])),
-    "pairs, hidden": (20, 2, 4, 1, 128, (640, 60, {}), (0, 9, {}), dict(pfirst=[700, 699])),
-    "pairs, far zero points": (20, 1, 4, 1, 128, (512, 20, {}), (0, 9, {}), dict(shift=100.0)),
+    "pairs, hidden": (40, 2, 4, 1, 128, (640, 60, {}), (0, 9, {}), dict(pfirst=[700, 699])),
+    "pairs, far zero points": (40, 1, 4, 1, 128, (512, 20, {}), (0, 9, {}), dict(shift=100.0)),
     "pairs, 257 rows": (257, 1, 1, 1, 128, (256, 20, {}), (0, 3, {}), {}),
     "pairs, 2000 rows, split": (250, 1, 8, 1, 128, (2048, 100, {}), (0, 9, {}), dict(ragged=True)),
+    # 33 to 128 rows
+    "one tile, 33 rows": (11, 1, 3, 1, 128, (64, 30, {}), (0, 9, {}), {}),
+    "two bits, 80 rows": (10, 1, 8, 1, 128, (448, 1, dict(bits=2, gk=64, gv=128)), (64, 9, {}), dict(ragged=True)),
+    "key groups of 96, 128 rows": (16, 2, 8, 1, 128, (960, 0, dict(gk=96, gv=128)), (0, 9, {}), {}),
+    "129 rows": (129, 1, 1, 1, 128, (512, 129, dict(kind="signed", gv=32)), (0, 9, {}), {}),
+    "joined, 100 rows": (1, 2, 4, 25, 128, (512, 40, {}), "joined", {}),
     "2100 rows": (300, 1, 7, 1, 128, (512, 100, {}), (0, 9, {}), {}),
     "2100 rows of chunks": (6, 1, 7, 50, 128, (512, 100, {}), (64, 20, {}), dict(first=[0, 80, 33, 1, 84, 20])),
     "2100 rows, split": (1, 1, 7, 300, 128, (4096, 100, {}), "joined", {}),
