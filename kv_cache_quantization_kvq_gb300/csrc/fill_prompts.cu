@@ -21,8 +21,8 @@
 // missed the instruction cache at 16 warps a SM (64 prompts of 26422 tokens: 55 us).
 // The arithmetic is that of the quantize kernels (kvq_elem.cuh), bit for bit.
 //
-// Measured on one GB300, 8 KV heads of 128 channels: 64 prompts of 16 to 2000 tokens at 4 bits 52 us (3.0 TB/s), 4 of
-// 9000 to 32768 at 2 bits 141 us (3.2 TB/s): 54 % of the issue slots, 31 to 39 % of DRAM busy.
+// Measured on one GB300, 8 KV heads of 128 channels: 64 prompts of 16 to 2000 tokens at 4 bits 49 us (3.2 TB/s), 4 of
+// 9000 to 32768 at 2 bits 137 us (3.3 TB/s): 54 % of the issue slots, 31 to 39 % of DRAM busy.
 #include <algorithm>
 #include <type_traits>
 
@@ -61,6 +61,9 @@ __device__ __forceinline__ void store_meta16(void* buf, int64_t i, float v) {
     static_cast<__nv_bfloat16*>(buf)[i] = __float2bfloat16_rn(v);
 }
 
+// The line that p lies in, into L2 (64 ragged prompts 49.7 -> 48.5 us, long ones 141.6 -> 136.9).
+__device__ __forceinline__ void fetch(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
 // The codes of eight channels by the IEEE division, out of line: the groups that need it are few.
 template <int BITS, bool ASYM>
 __device__ __noinline__ uint32_t slow_codes(const uint4& w, const float* s, const float* z, const QSpec& q, int off) {
@@ -93,6 +96,15 @@ __device__ __forceinline__ void fill_keys(const FillArgs& a, const FillPlan& p, 
         const int c0 = (int)(u - gi * kParts) * 64 + lc * 8;
         const int t0 = (int)(gi * g), from = max(at.first - t0, 0);         // rows from .. g - 1 are there
         const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(a.k.x) + (int64_t)(t0 + at.shift) * a.k.stride + h * C + c0;
+        if (u + 1 < u1) {                        // the next unit's rows, a 128-byte line a lane
+            const int64_t gn = (u + 1) / kParts;
+            const int tn = (int)(gn * g);
+            const __nv_bfloat16* xn = static_cast<const __nv_bfloat16*>(a.k.x) + (int64_t)(tn + at.shift) * a.k.stride + h * C +
+                                      (u + 1 - gn * kParts) * 64;
+#pragma unroll 1
+            for (int r = lane; r < g; r += 32)
+                if (tn + r >= at.first) fetch(xn + (int64_t)r * a.k.stride);
+        }
         uint32_t mn[4], mx[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -205,6 +217,11 @@ __device__ __forceinline__ void fill_values(const FillArgs& a, const FillPlan& p
         const int t0 = (int)u * kUnit + lr;      // the lane's rows: t0 + k kAcross
         const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(a.v.x) + (int64_t)(t0 + at.shift) * a.v.stride + h * C + lc * 8;
         auto live = [&](int k) { return t0 + k * kAcross >= at.first && t0 + k * kAcross < a.tq; };
+        if (u + 1 < u1) {
+            const int tn = (int)(u + 1) * kUnit + lane / (C / 64);
+            if (tn >= at.first && tn < a.tq)
+                fetch(static_cast<const __nv_bfloat16*>(a.v.x) + (int64_t)(tn + at.shift) * a.v.stride + h * C + lane % (C / 64) * 64);
+        }
         // a group's (min, -max), or (0, -max |x|), as one pair: they meet in log2(gl) shuffles
         uint32_t ext[kRows];
         {
