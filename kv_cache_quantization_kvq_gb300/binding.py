@@ -957,19 +957,21 @@ def attend_shared(q, prefix: KVCache, cache: Optional[KVCache] = None, own=None,
 def _tokens(t, name, heads, C, dev):
     """The stride between the tokens of a packed tensor [total, heads, C]."""
     import torch
-    if t.dtype != torch.bfloat16 or not t.is_cuda or t.device != dev or t.dim() != 3 or tuple(t.shape[1:]) != (heads, C):
-        raise ValueError(f"{name} must be a CUDA bf16 tensor [total, {heads}, {C}] on {dev} (got {t.dtype} {tuple(t.shape)} "
+    s, stride = t.shape, t.stride()
+    if t.dtype != torch.bfloat16 or not t.is_cuda or t.device != dev or len(s) != 3 or s[1] != heads or s[2] != C:
+        raise ValueError(f"{name} must be a CUDA bf16 tensor [total, {heads}, {C}] on {dev} (got {t.dtype} {tuple(s)} "
                          f"on {t.device})")
-    if (C > 1 and t.stride(2) != 1) or (heads > 1 and t.stride(1) != C):
-        raise ValueError(f"{name}'s heads must lie one behind the other in a token (strides {tuple(t.stride())})")
-    return t.stride(0) if t.shape[0] > 1 else heads * C
+    if (C > 1 and stride[2] != 1) or (heads > 1 and stride[1] != C):
+        raise ValueError(f"{name}'s heads must lie one behind the other in a token (strides {stride})")
+    return stride[0] if s[0] > 1 else heads * C
 
 
 def _prompts(starts, dev):
-    if str(starts.dtype) != "torch.int32" or starts.dim() != 1 or starts.numel() < 1 or not starts.is_contiguous() or \
-            starts.device != dev:
+    import torch
+    n = starts.numel()
+    if starts.dtype != torch.int32 or starts.dim() != 1 or n < 1 or not starts.is_contiguous() or starts.device != dev:
         raise ValueError(f"starts must be a contiguous int32 tensor [prompts + 1] on {dev}")
-    return starts.numel() - 1
+    return n - 1
 
 
 def attend_prompts(q, k, v, starts, out=None, lse=None, workspace=None, stream=None):
@@ -979,12 +981,12 @@ def attend_prompts(q, k, v, starts, out=None, lse=None, workspace=None, stream=N
     float32 [total, heads]).  Rows of tokens in no prompt are not written."""
     import torch
     dev = q.device
-    if q.dim() != 3 or k.dim() != 3 or k.shape[1] < 1 or q.shape[1] % k.shape[1] or q.shape[0] != k.shape[0] or \
-            k.shape != v.shape:
-        raise ValueError(f"q must be [total, kv_heads * group, C], k and v [total, kv_heads, C] (got {tuple(q.shape)}, "
-                         f"{tuple(k.shape)}, {tuple(v.shape)})")
-    total, heads, C = q.shape
-    kv_heads = k.shape[1]
+    qs, ks = q.shape, k.shape
+    if len(qs) != 3 or len(ks) != 3 or ks[1] < 1 or qs[1] % ks[1] or qs[0] != ks[0] or ks != v.shape:
+        raise ValueError(f"q must be [total, kv_heads * group, C], k and v [total, kv_heads, C] (got {tuple(qs)}, "
+                         f"{tuple(ks)}, {tuple(v.shape)})")
+    total, heads, C = qs
+    kv_heads = ks[1]
     strides = [_tokens(t, name, h, C, dev) for t, name, h in ((q, "q", heads), (k, "k", kv_heads), (v, "v", kv_heads))]
     prompts, group = _prompts(starts, dev), heads // kv_heads
     if out is not None:
