@@ -961,7 +961,7 @@ def _tokens(t, name, heads, C, dev):
     if t.dtype != torch.bfloat16 or not t.is_cuda or t.device != dev or len(s) != 3 or s[1] != heads or s[2] != C:
         raise ValueError(f"{name} must be a CUDA bf16 tensor [total, {heads}, {C}] on {dev} (got {t.dtype} {tuple(s)} "
                          f"on {t.device})")
-    if (C > 1 and stride[2] != 1) or (heads > 1 and stride[1] != C):
+    if s[0] > 0 and ((C > 1 and stride[2] != 1) or (heads > 1 and stride[1] != C)):
         raise ValueError(f"{name}'s heads must lie one behind the other in a token (strides {stride})")
     return stride[0] if s[0] > 1 else heads * C
 

@@ -163,6 +163,20 @@ def test_a_cache_filled_from_one_length_equals_appends(b):
         assert torch.equal(a, c)
 
 
+def test_prompts_of_no_tokens(b):
+    """Tensors without tokens, whatever their strides: a cache of padding alone."""
+    import torch
+    kw = dict(scale_dtype=b.BF16, zero_dtype=b.BF16, residual=64)
+    kqp, vqp = (b.QParams.asym(4, 0, 15, axis=a, group=64, **kw) for a in (b.ALONG_T, b.ALONG_C))
+    bufs = [tuple(torch.full((s,), 0xA5, dtype=torch.uint8, device="cuda") for s in b._store_sizes((2, 128, 64), p, 128))
+            for p in (kqp, vqp)]
+    cache = b.KVCache(*bufs, shape=(2, 128, 64), kqp=kqp, vqp=vqp, tq=0, nres=0, resid_rows=128, kv_heads=1)
+    none = torch.empty(1, dtype=torch.bfloat16, device="cuda").as_strided((0, 1, 64), (0, 0, 0))
+    b.fill_prompts(none, none, torch.zeros(3, dtype=torch.int32, device="cuda"), cache, 150)
+    assert (cache.tq, cache.nres) == (64, 86) and (cache.first == 150).all()
+    assert all((t == 0xA5).all() for t in (*cache.k, *cache.v))
+
+
 def test_captured_fill_replays_with_other_lengths_and_streams(b):
     import torch
     name = "ragged"

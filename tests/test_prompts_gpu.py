@@ -41,6 +41,7 @@ CASES = {
     "ragged, C 64": ([300, 1, 129, 31], 3, 2, 64, dict(fused=True)),
     "empty prompts": ([0, 5, 0, 0, 130, 0], 1, 8, 128, {}),
     "all empty": ([0, 0], 1, 4, 128, dict(behind=3)),
+    "no tokens": ([0, 0], 2, 4, 128, {}),
     "rows outside": ([40, 150], 2, 4, 128, dict(before=7, behind=140)),
     "group of 3": ([100, 43, 200], 2, 3, 128, {}),
     "group of 5": ([100, 27], 1, 5, 64, {}),
