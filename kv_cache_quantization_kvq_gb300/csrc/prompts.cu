@@ -43,6 +43,7 @@
 #include <cudaTypedefs.h>
 
 #include "kvq_fast.cuh"
+#include "kvq_plan.cuh"
 #include "kvq_rows.cuh"
 #include "kvq_tc.cuh"
 
@@ -51,8 +52,8 @@ namespace kvq {
 namespace {
 
 using namespace rows;
+using namespace plan;
 
-constexpr int kTile = 128;                       // rows of a row tile, keys of a key tile
 constexpr int kThreads = 384;                    // 12 warps, 168 registers each at launch (64512 in all):
 constexpr int kRegsSoftmax = 216;                // 8 softmax warps take 216 and the other four keep 56
 constexpr int kRegsOther = 56;                   // (62464), so a row of 128 scores stays in registers
@@ -60,22 +61,6 @@ static_assert(256 * kRegsSoftmax + 128 * kRegsOther <= kThreads * 168, "register
 constexpr float kSlack = 8.0f;                   // base-2 growth of the maximum that is let pass
 
 // ---------------------------------------------------------------- plan
-// Two row tiles of a prompt: tokens tok0 .. of the prompt at [begin, begin + len).
-struct Item { int begin, len, tok0, keys; };     // keys: key tiles that its last row sees
-
-struct Plan { int count, pad[63]; };             // and the items behind it
-
-// prompt s, whatever starts holds; its items, and the i-th of them
-__device__ __forceinline__ void prompt_range(const int32_t* starts, int64_t s, int64_t total, int& begin, int& len) {
-    begin = min(max(starts[s], 0), (int)total);
-    len = min(max(starts[s + 1], begin), (int)total) - begin;
-}
-__device__ __forceinline__ int items_of(int len, int tpt) { return (int)(((int64_t)len + 2 * tpt - 1) / (2 * tpt)); }
-__device__ __forceinline__ Item item_at(int begin, int len, int i, int tpt) {
-    const int tok0 = i * 2 * tpt;
-    return Item{begin, len, tok0, (min(tok0 + 2 * tpt, len) + kTile - 1) / kTile};
-}
-
 constexpr int kPlanThreads = 1024;
 constexpr int kBuckets = 64 + 19 * 16;           // of numbers of key tiles: exact below 64, in sixteenths of powers of 2 above
 constexpr int kAlone = 8;                        // items of a prompt that its thread makes; a warp shares the others
@@ -89,20 +74,44 @@ __device__ __forceinline__ int bucket_of(int keys) {                // larger nu
     return kBuckets - 1 - min(b, kBuckets - 1);
 }
 
-// The order of items in a bucket is not fixed, and nothing depends on it.
+// The order of items in a bucket is not fixed, and nothing depends on it.  Starts in order make `cap` items at most.
+// Others may ask for any number: of those the first `cap` are made, in the prompts' order, so that neither the counts
+// nor the work grow beyond what a well-formed call has.
 __global__ void __launch_bounds__(kPlanThreads)
 plan_kernel(const int32_t* starts, int64_t prompts, int64_t total, int tpt, int cap, Plan* plan)
 {
     __shared__ int at[kBuckets];
+    __shared__ int64_t asked[kPlanThreads / 32];
     asm volatile("griddepcontrol.launch_dependents;");
     const int tid = threadIdx.x, lane = tid & 31;
     Item* items = reinterpret_cast<Item*>(plan + 1);
+    bool wild = false;
+#pragma unroll 4
+    for (int64_t s = tid; s < prompts; s += kPlanThreads) wild |= starts[s + 1] < starts[s];
     auto each = [&](auto use) {                  // use(item) for every item
+        int64_t before = 0;                      // wild: what the prompts before s0 ask for
         for (int64_t s0 = 0; s0 < prompts; s0 += kPlanThreads) {
             const int64_t s = s0 + tid;
             int begin = 0, len = 0;
             if (s < prompts) prompt_range(starts, s, total, begin, len);
-            const int n = items_of(len, tpt);
+            int n = items_of(len, tpt);
+            if (__builtin_expect(wild, 0)) {
+                int64_t upto = n;
+#pragma unroll
+                for (int d = 1; d < 32; d *= 2) {
+                    const int64_t x = __shfl_up_sync(0xFFFFFFFFu, upto, d);
+                    if (lane >= d) upto += x;
+                }
+                if (lane == 31) asked[tid >> 5] = upto;
+                __syncthreads();
+                int64_t at_warp = before;
+                for (int w = 0; w < kPlanThreads / 32; ++w) {
+                    if (w < tid >> 5) at_warp += asked[w];
+                    before += asked[w];
+                }
+                __syncthreads();
+                n = items_left(at_warp + upto - n, n, cap);
+            }
             for (int i = 0; i < min(n, kAlone); ++i) use(item_at(begin, len, i, tpt));
             for (uint32_t more = __ballot_sync(0xFFFFFFFFu, n > kAlone); more; more &= more - 1) {
                 const int from = __ffs(more) - 1;
@@ -110,10 +119,11 @@ plan_kernel(const int32_t* starts, int64_t prompts, int64_t total, int tpt, int 
                 const int m = __shfl_sync(0xFFFFFFFFu, n, from);
                 for (int i = kAlone + lane; i < m; i += 32) use(item_at(b, l, i, tpt));
             }
+            if (before >= cap) break;
         }
     };
     for (int i = tid; i < kBuckets; i += kPlanThreads) at[i] = 0;
-    __syncthreads();
+    wild = __syncthreads_or(wild);
     each([&](const Item& x) { atomicAdd(&at[bucket_of(x.keys)], 1); });
     __syncthreads();
     if (tid < 32) {                              // exclusive sums
@@ -137,7 +147,7 @@ plan_kernel(const int32_t* starts, int64_t prompts, int64_t total, int tpt, int 
     __syncthreads();
     each([&](const Item& x) {
         const int i = atomicAdd(&at[bucket_of(x.keys)], 1);
-        if (i < cap) items[i] = x;               // starts that are not in order may make more
+        if ((uint32_t)i < (uint32_t)cap) items[i] = x;              // also where starts change meanwhile
     });
 }
 
@@ -612,13 +622,6 @@ bool encode_map(const void* x, int64_t total, int64_t stride, int64_t heads, int
     return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(x), dims, strides, box, estr,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// Items of prompts that do not overlap, at most.
-int64_t most_items(int64_t prompts, int64_t total, int64_t group)
-{
-    const int64_t tokens = 2 * (kTile / group);
-    return total / tokens + std::min(prompts, total);
 }
 
 template <int C>
