@@ -64,25 +64,6 @@ __device__ __forceinline__ uint32_t at_rank(const void* p, uint32_t rank) {
 __device__ __forceinline__ void arrive_first(uint64_t* bar) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(at_rank(bar, 0)) : "memory");
 }
-// tc::wait for a barrier that both CTAs arrive on
-constexpr uint32_t kPollsPair = 1u << 24;
-__device__ __forceinline__ bool wait_pair(uint64_t* bar, uint32_t parity, volatile int* gone) {
-    for (uint32_t i = 0; i < kPollsPair; ++i) {
-        uint32_t ok;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(ok)
-            : "r"(smem_u32(bar)), "r"(parity)
-            : "memory");
-        if (ok) return true;
-        if (*gone) return false;
-    }
-    *gone = 1;
-    atomicAdd(&g_kvq_wait_timeouts, 1u);
-    return false;
-}
 __device__ __forceinline__ void alloc_pair(uint32_t* slot, uint32_t cols) {      // one warp of each CTA
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)), "r"(cols)
                  : "memory");
@@ -419,8 +400,7 @@ attend_prefix_kernel(const __grid_constant__ PrefixArgs X)
     cluster_sync();                              // both CTAs' barriers, queries and tensor memory are there
     tc::after_sync();
     const uint32_t tmem = *tmem_slot;
-    auto ready = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xFFFFFFFFu, wait_pair(bar, parity & 1, gone)) != 0; };
-    auto ready_pair = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xFFFFFFFFu, wait_pair(bar, parity & 1, gone)) != 0; };
+    auto ready = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xFFFFFFFFu, tc::wait(bar, parity & 1, gone)) != 0; };
 
     if (warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
     else asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
@@ -458,7 +438,7 @@ attend_prefix_kernel(const __grid_constant__ PrefixArgs X)
                 commit_pair(&sfull[2 * t + (u & 1)]);
                 if (u & 1) commit_pair(&kfree[(u >> 1) % kSlots]);
             };
-            bool ok = ready_pair(&kfull[0], 0);
+            bool ok = ready(&kfull[0], 0);
             tc::after_sync();
             if (ok && tc::elect()) {
                 scores(0);
@@ -468,10 +448,10 @@ attend_prefix_kernel(const __grid_constant__ PrefixArgs X)
             for (int u = 0; ok && u < 2 * n; ++u) {
                 const int j = u >> 1, s = j % kSlots;
                 if (!(u & 1)) {
-                    ok = ready_pair(&vfull[s], j / kSlots);
-                    if (j + 1 < n) ok = ok && ready_pair(&kfull[(j + 1) % kSlots], (j + 1) / kSlots);
+                    ok = ready(&vfull[s], j / kSlots);
+                    if (j + 1 < n) ok = ok && ready(&kfull[(j + 1) % kSlots], (j + 1) / kSlots);
                 }
-                ok = ok && ready_pair(&pfull[2 * t + (u & 1)], j);
+                ok = ok && ready(&pfull[2 * t + (u & 1)], j);
                 if (!ok) break;
                 tc::after_sync();
                 if (tc::elect()) {
