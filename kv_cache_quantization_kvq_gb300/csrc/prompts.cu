@@ -74,6 +74,29 @@ __device__ __forceinline__ int bucket_of(int keys) {                // larger nu
     return kBuckets - 1 - min(b, kBuckets - 1);
 }
 
+// What the prompts before this thread's ask for in this pass of the prompts, and in `all` what all of the pass do; n: its
+// own.  Out of line: prompts in order never come here.
+struct Asked { int64_t before, all; };
+__device__ __noinline__ Asked asked_in_pass(int n, int64_t* sums) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int64_t upto = n;
+#pragma unroll 1
+    for (int d = 1; d < 32; d *= 2) {
+        const int64_t x = __shfl_up_sync(0xFFFFFFFFu, upto, d);
+        if (lane >= d) upto += x;
+    }
+    if (lane == 31) sums[warp] = upto;
+    __syncthreads();
+    Asked r = {upto - n, 0};
+#pragma unroll 1
+    for (int w = 0; w < kPlanThreads / 32; ++w) {
+        if (w < warp) r.before += sums[w];
+        r.all += sums[w];
+    }
+    __syncthreads();
+    return r;
+}
+
 // The order of items in a bucket is not fixed, and nothing depends on it.  Starts in order make `cap` items at most.
 // Others may ask for any number: of those the first `cap` are made, in the prompts' order, so that neither the counts
 // nor the work grow beyond what a well-formed call has.
@@ -81,36 +104,32 @@ __global__ void __launch_bounds__(kPlanThreads)
 plan_kernel(const int32_t* starts, int64_t prompts, int64_t total, int tpt, int cap, Plan* plan)
 {
     __shared__ int at[kBuckets];
-    __shared__ int64_t asked[kPlanThreads / 32];
+    __shared__ int64_t sums[kPlanThreads / 32];
     asm volatile("griddepcontrol.launch_dependents;");
     const int tid = threadIdx.x, lane = tid & 31;
     Item* items = reinterpret_cast<Item*>(plan + 1);
+    int begin0 = 0, len0 = 0;                    // the thread's prompt of the first pass
     bool wild = false;
+    if (tid < prompts) {
+        prompt_range(starts, tid, total, begin0, len0);
+        wild = starts[tid + 1] < starts[tid];
+    }
 #pragma unroll 4
-    for (int64_t s = tid; s < prompts; s += kPlanThreads) wild |= starts[s + 1] < starts[s];
+    for (int64_t s = tid + kPlanThreads; s < prompts; s += kPlanThreads) wild |= starts[s + 1] < starts[s];
     auto each = [&](auto use) {                  // use(item) for every item
         int64_t before = 0;                      // wild: what the prompts before s0 ask for
         for (int64_t s0 = 0; s0 < prompts; s0 += kPlanThreads) {
             const int64_t s = s0 + tid;
-            int begin = 0, len = 0;
-            if (s < prompts) prompt_range(starts, s, total, begin, len);
+            int begin = begin0, len = len0;
+            if (s0 > 0) {
+                begin = len = 0;
+                if (s < prompts) prompt_range(starts, s, total, begin, len);
+            }
             int n = items_of(len, tpt);
             if (__builtin_expect(wild, 0)) {
-                int64_t upto = n;
-#pragma unroll
-                for (int d = 1; d < 32; d *= 2) {
-                    const int64_t x = __shfl_up_sync(0xFFFFFFFFu, upto, d);
-                    if (lane >= d) upto += x;
-                }
-                if (lane == 31) asked[tid >> 5] = upto;
-                __syncthreads();
-                int64_t at_warp = before;
-                for (int w = 0; w < kPlanThreads / 32; ++w) {
-                    if (w < tid >> 5) at_warp += asked[w];
-                    before += asked[w];
-                }
-                __syncthreads();
-                n = items_left(at_warp + upto - n, n, cap);
+                const Asked x = asked_in_pass(n, sums);
+                n = items_left(before + x.before, n, cap);
+                before += x.all;
             }
             for (int i = 0; i < min(n, kAlone); ++i) use(item_at(begin, len, i, tpt));
             for (uint32_t more = __ballot_sync(0xFFFFFFFFu, n > kAlone); more; more &= more - 1) {
