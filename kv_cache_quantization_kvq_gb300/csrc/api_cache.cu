@@ -470,7 +470,7 @@ kvq_status kvq_fill_prompts(const void* k, int64_t k_stride, const void* v, int6
         return s;
     kvq::CacheArgs c;
     if ((s = attend_args(nullptr, 0, 1, kv_heads, cache, k_params, v_params, true, shape, c))) return s;
-    if ((s = need(cache->first, true, 4, "first"))) return s;
+    if ((s = need(cache->first, shape->outer > 0, 4, "first"))) return s;
     if (cache->tq % k_params->group != 0)
         KVQ_FAIL(KVQ_EINVAL, "tq (%lld) must be a multiple of the key group (%lld)", (long long)cache->tq, (long long)k_params->group);
     kvq::FillArgs a = {};
