@@ -245,7 +245,7 @@ KVQ_API kvq_status kvq_attend_prompts(const void* q, int64_t q_stride, const voi
  *  - cache: the buffers of shape = {prompts * kv_heads, T_cap, C}; tq (a multiple of
  *    the key group, at most T_cap) and nres (at most resid_rows) say how long it
  *    becomes; first must not be NULL (but where there are no prompts), it is written.
- *    No buffer may overlap k or v.
+ *    Neither it nor a buffer may overlap k, v or starts.
  *  - A cache that kvq_append_kv goes on with needs tq = block * max(0, (T - R) / block)
  *    and nres = T - tq.
  *  - Formats and alignment as kvq_attend_chunk.

@@ -477,7 +477,15 @@ kvq_status kvq_fill_prompts(const void* k, int64_t k_stride, const void* v, int6
     a.k = {k, k_stride, cache->k_codes, cache->k_scale, cache->k_zero, cache->k_resid, {}};
     a.v = {v, v_stride, cache->v_codes, cache->v_scale, cache->v_zero, cache->v_resid, {}};
     if ((s = store_format(shape, k_params, a.k.q)) || (s = store_format(shape, v_params, a.v.q))) return s;
-    const size_t in_B[2] = {packed_bytes(total, k_stride, kv_heads, c.C), packed_bytes(total, v_stride, kv_heads, c.C)};
+    const void* in[3] = {k, v, starts};
+    const size_t in_B[3] = {packed_bytes(total, k_stride, kv_heads, c.C), packed_bytes(total, v_stride, kv_heads, c.C),
+                            (size_t)(prompts + 1) * sizeof(int32_t)};
+    auto over_inputs = [&](const void* to, size_t to_B) {
+        for (int i = 0; i < 3; ++i)
+            if (to && overlap(to, to_B, in[i], in_B[i])) return true;
+        return false;
+    };
+    if (over_inputs(cache->first, (size_t)c.outer * sizeof(int32_t))) KVQ_FAIL(KVQ_EINVAL, "first overlaps k, v or starts");
     for (int i = 0; i < 2; ++i) {
         const kvq::FillStore& f = i ? a.v : a.k;
         const size_t row_B = (size_t)(c.C * f.q.bits / 8), cells = f.q.axis == KVQ_GROUP_ALONG_T ? (size_t)(f.q.ngroups * c.C)
@@ -486,8 +494,7 @@ kvq_status kvq_fill_prompts(const void* k, int64_t k_stride, const void* v, int6
         const size_t to_B[4] = {(size_t)c.outer * c.cap * row_B, (size_t)c.outer * cells * 2, (size_t)c.outer * cells * 2,
                                 (size_t)c.outer * c.rrows * c.C * 2};
         for (int m = 0; m < 4; ++m)
-            if (to[m] && (overlap(to[m], to_B[m], k, in_B[0]) || overlap(to[m], to_B[m], v, in_B[1])))
-                KVQ_FAIL(KVQ_EINVAL, "the cache's buffers overlap k or v");
+            if (over_inputs(to[m], to_B[m])) KVQ_FAIL(KVQ_EINVAL, "the cache's buffers overlap k, v or starts");
     }
     a.starts = starts;
     a.first = cache->first;
