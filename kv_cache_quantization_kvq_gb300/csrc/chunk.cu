@@ -30,7 +30,8 @@
 // registers) 49 % of the issue slots, 28 % of DRAM and 17 % of the tensor pipe are
 // busy: each warp waits on its chain codes -> unpacking -> scores -> weights -> values.
 // At head_dim 128 the kernels spill: 4 bits 12, 4 and 42 bytes (8, 16, 32 rows), 2 bits
-// 80, 52 and 124; at 64 none.
+// 80, 52 and 124; those of launches to be joined 32, 24 and 62, and 104, 136 and 180.  At
+// 64 none does, but for 8 bytes of a joined one (4 bits, 8 rows).
 #include <algorithm>
 
 #include "kvq_chunk.cuh"
@@ -137,9 +138,9 @@ __device__ __forceinline__ float4 remote_f4(const void* p, int rank) {
 }
 
 // out (4 channels) and, with the row's first channels, lse
-template <int C, bool JOIN>
+template <int C>
 __device__ __forceinline__ void write_row(const ChunkArgs& A, int64_t o, int r, int c4, float M, float L, const float (&v)[4]) {
-    const int64_t at = row_index<JOIN>(A.v, o, r);
+    const int64_t at = row_index(A.v, o, r);
     const float inv = row_scale(L);
     *reinterpret_cast<uint2*>(A.out + at * C + c4) =
         make_uint2(pack_bf16x2(row_value(v[0], inv), row_value(v[1], inv)),
@@ -533,21 +534,21 @@ attend_rows_kernel(const ChunkArgs A)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) v[i] = __fadd_rn(v[i], odd_value(odd, C, c4 + i, row_last));
             }
-            if (A.cluster) {
+            if (!JOIN && A.cluster) {
                 *reinterpret_cast<float4*>(&sy[0][row][c4]) = make_float4(v[0], v[1], v[2], v[3]);   // read by this thread only
                 if (c4 == 0) {
                     gm[row] = M;
                     gl[row] = L;
                 }
-            } else if (JOIN ? A.parts : A.nsplit > 1) {
+            } else if (JOIN || A.nsplit > 1) {              // joined by a later launch
                 float* dst = A.part + ((o * a.rows + r) * A.nsplit + split) * (C + 4);
                 *reinterpret_cast<float4*>(dst + c4) = make_float4(v[0], v[1], v[2], v[3]);
                 if (c4 == 0) *reinterpret_cast<float2*>(dst + C) = make_float2(M, L);
             } else {
-                write_row<C, JOIN>(A, o, r, c4, M, L, v);
+                write_row<C>(A, o, r, c4, M, L, v);
             }
         }
-        if (A.cluster) {                         // block rank = split; each takes its share of the rows' pieces
+        if (!JOIN && A.cluster) {                // block rank = split; each takes its share of the rows' pieces
             cluster_sync();
             for (int k = split * kThreads + tid; k < R::kOut * (C / 4); k += A.nsplit * kThreads) {
                 const int row = k / (C / 4), c4 = (k % (C / 4)) * 4, r = 16 * m + row;
@@ -564,7 +565,7 @@ attend_rows_kernel(const ChunkArgs A)
                     v[2] = __fmaf_rn(x.z, f, v[2]);
                     v[3] = __fmaf_rn(x.w, f, v[3]);
                 }
-                write_row<C, JOIN>(A, o, r, c4, M, L, v);
+                write_row<C>(A, o, r, c4, M, L, v);
             }
             cluster_sync();                      // nobody leaves, or writes the next tile, before all have read
         }
@@ -626,7 +627,6 @@ cudaError_t launch_rows(ChunkArgs A, int64_t outer, cudaStream_t st)
 {
     const RowsPlan p = rows_plan(outer, A.v.T, A.v.rows, A.shared);
     A.nsplit = (int32_t)p.nsplit;
-    A.parts = p.nsplit > 1 || A.shared;
     const int64_t grid = outer * p.nsplit;
     if (grid > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
     if constexpr (JOIN) {                        // parts, without a cluster
@@ -757,7 +757,6 @@ cudaError_t launch_rows_parts(ChunkArgs& A, int bits, int64_t C, int64_t outer, 
     const Shares p = shares_of(outer, A.v.T, A.v.rows);
     A.nsplit = (int32_t)p.nsplit;
     A.share = (int32_t)p.share;
-    A.parts = 1;
     if (bits == 4) return C == 128 ? launch_parts<4, 128>(A, outer, st) : launch_parts<4, 64>(A, outer, st);
     return C == 128 ? launch_parts<2, 128>(A, outer, st) : launch_parts<2, 64>(A, outer, st);
 }
@@ -774,7 +773,7 @@ cudaError_t launch_chunk(ChunkArgs A, int bits, int64_t C, int64_t outer, void* 
 {
     A.part = static_cast<float*>(ws);
     if (chunk_uses_tc(A.v.rows)) return launch_attend_tc(A, bits, C, outer, ws, st);
-    return A.sums || A.shared ? launch_any<true>(A, bits, C, outer, st) : launch_any<false>(A, bits, C, outer, st);
+    return A.shared ? launch_any<true>(A, bits, C, outer, st) : launch_any<false>(A, bits, C, outer, st);
 }
 
 cudaError_t launch_attend_chunk(const CacheArgs& x, void* out, float* lse, void* ws, cudaStream_t st)

@@ -17,7 +17,6 @@ struct ChunkArgs {
     float* part;             // [row][split][C + 4]: y, m, l
     float* sums;             // [row_index][C + 4]: the same of whole rows, in place of out and lse; or nullptr
     int32_t nsplit, ntiles, cluster;
-    int32_t parts;           // whether results go to part and are joined later: nsplit > 1, or shared
     int32_t share;           // batches of a split, or 0: a slice has as many splits as its tokens need, of at most nsplit
     // shared: a launch over tokens that every row sees, to be joined with what the rows
     // have seen elsewhere: own_sums as `sums` holds it, own_part as `part` does (of the rows
@@ -166,9 +165,6 @@ bool chunk_uses_tc(int64_t rows);
 size_t chunk_tc_workspace(int64_t outer, int64_t C, int64_t tmax, int64_t rows, bool shared);
 cudaError_t launch_attend_tc(const ChunkArgs& A, int bits, int64_t C, int64_t outer, void* ws, cudaStream_t st);
 
-// The attention of kvq_attend_chunk over a cache, its rows into A.out and A.lse, or
-// into A.sums; with A.parts the rows kernel's, which are left in part: nsplit and
-// share are returned in A.
 // A launch that starts while the one before it ends; its kernel waits for that one
 // itself (griddepcontrol.wait).
 template <class... P, class... A>
@@ -185,8 +181,13 @@ cudaError_t launch_early(void (*kernel)(P...), unsigned grid, unsigned threads, 
     const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
+
+// The rows kernel (at most 32 rows a slice) over slices that need not be equally long. Its
+// results are left in A.part; nsplit and share are returned in A.
 size_t rows_parts_workspace(int64_t outer, int64_t C, int64_t tmax, int64_t rows);
 cudaError_t launch_rows_parts(ChunkArgs& A, int bits, int64_t C, int64_t outer, cudaStream_t st);
+// The attention of kvq_attend_chunk over a cache: its rows into A.out and A.lse, joined with what they
+// have seen elsewhere (A.shared), or into A.sums (tensor-core forms alone).
 cudaError_t launch_chunk(ChunkArgs A, int bits, int64_t C, int64_t outer, void* ws, cudaStream_t st);
 
 // Rows that all see every token on pairs of SMs (prefix.cu), and the launch that

@@ -675,7 +675,6 @@ cudaError_t launch_attend_prefix(ChunkArgs A, int bits, int64_t outer, void* ws,
     X.ntiles = (A.v.rows + 511) / 512;
     A.part = static_cast<float*>(ws);
     A.nsplit = (int32_t)splits_of(outer * X.ntiles, (A.v.T + kTile - 1) / kTile);
-    A.parts = 1;
     X.A = A;
     const cudaError_t e = bits == 4 ? launch<4>(X, outer, st) : launch<2>(X, outer, st);
     return e != cudaSuccess ? e : launch_merge_rows(A, C, outer, st);
