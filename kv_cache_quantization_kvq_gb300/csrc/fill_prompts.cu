@@ -251,11 +251,11 @@ __device__ __forceinline__ void fill_values(const FillArgs& a, const FillPlan& p
         bool fast = true, lo_ok = true;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            gs[i] = gs[0];
-            gi[i] = gi[0];
-            gz[i] = gz[0];
-            zoff[i] = zoff[0];
-            if (i == 1 && gl != 4) break;
+            if (i == 1 && gl != 4) {             // not looked at
+                gs[1] = gi[1] = gz[1] = 0.0f;
+                zoff[1] = 0;
+                break;
+            }
             const int row = i == 0 ? mine & 7 : mine + 4;
             uint32_t e = ext[0];
 #pragma unroll
