@@ -658,8 +658,10 @@ cudaError_t launch(const PromptArgs& p, Plan* plan, cudaStream_t st)
     if (cap > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
     const int64_t grid = std::min<int64_t>(sm_count(), cap * p.kv_heads);
     // else every CTA finds its pair by itself, one launch: a prompt of 17 | 600 | 2400 tokens 9.7 -> 7.1, 19.4 -> 16.4,
-    // 39.6 -> 37.2 us in a graph; with more prompts, all but a few of them empty, it would look through them for longer
-    const bool planned = cap * p.kv_heads > grid || p.prompts > 1024;
+    // 39.6 -> 37.2 us in a graph.  It looks through the prompts for that, which takes longer than the launch from about 200
+    // of them on: 1 | 64 | 128 | 256 | 1024 prompts, all but the last empty, 8.5 | 9.1 | 9.8 | 11.5 | 21.6 us for 100 tokens and
+    // 7.0 | 7.3 | 8.1 | 9.7 | 19.8 us for 18 (of 1 and 8 KV heads), with the launch 10.7 to 10.9 and 9.7 to 9.9 us
+    const bool planned = cap * p.kv_heads > grid || p.prompts > 192;
     if (planned) plan_kernel<<<1, kPlanThreads, 0, st>>>(p.starts, p.prompts, p.total, tpt, (int)cap, plan);
     Args a;
     a.out = static_cast<__nv_bfloat16*>(p.out);
