@@ -22,7 +22,10 @@
 // The arithmetic is that of the quantize kernels (kvq_elem.cuh), bit for bit.
 //
 // Measured on one GB300, 8 KV heads of 128 channels: 64 prompts of 16 to 2000 tokens at 4 bits 49 us (3.2 TB/s), 4 of
-// 9000 to 32768 at 2 bits 137 us (3.3 TB/s): 54 % of the issue slots, 31 to 39 % of DRAM busy.
+// 9000 to 32768 at 2 bits 138 us (3.3 TB/s): 54 % of the issue slots, 31 to 39 % of DRAM busy, so that neither bounds it
+// but a warp's way from loads to extremes, constants, loads again and codes.
+// Six CTAs an SM leave a thread 80 registers, which spill (132 bytes at C = 128, 156 at 64); five, at 96 without a spill, are
+// slower: 69892 tokens in 64 prompts 105.4 and 108.7 us at 4 bits, at C = 64 60.5 and 64.3; 83768 in 4 at 2 bits 127.4 and 134.0.
 #include <algorithm>
 #include <type_traits>
 

@@ -18,9 +18,9 @@
 // exists, so only the first and the last tile are masked.  Each split leaves (y, m, l) per row,
 // joined in merge_rows_kernel (chunk.cu).
 //
-// Measured on one GB300: 128 requests x 4 heads, 4 bits, over a prefix of 131072 tokens of 8 KV heads 220 us
-// (1.25 PFLOP/s of products; the call, with its own tokens and the joining, 245).  What bounds it is the chain
-// scores -> weights -> value product of a row tile, of which an SM has two.
+// Measured on one GB300: 128 requests x 4 heads, 4 bits, over a prefix of 131072 tokens of 8 KV heads 205 us
+// (1.34 PFLOP/s of products; the call, with its own tokens and the joining, 230).  What bounds it is the chain
+// scores -> weights -> value product of a row tile, of which an SM has two: tensor pipe 62 %, issue slots 60 %.
 #include <algorithm>
 
 #include "kvq_chunk.cuh"
@@ -60,7 +60,9 @@ __device__ __forceinline__ uint32_t at_rank(const void* p, uint32_t rank) {
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
     return a;
 }
-// one arrival on the first CTA's barrier
+// One arrival on the first CTA's barrier.  What it hands on lies in this SM's shared and tensor memory, which the
+// tensor cores of both read, and has been fenced for them before; with a release at cluster scope every arrival waited for
+// all of the SM's stores (445 us where 405 are without).
 __device__ __forceinline__ void arrive_first(uint64_t* bar) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(at_rank(bar, 0)) : "memory");
 }
@@ -656,10 +658,15 @@ cudaError_t launch(PrefixArgs X, int64_t outer, cudaStream_t st)
 
 }  // namespace
 
-// Below, an SM's tensor memory holds the rows of a tile by itself; above, one expansion costs less than unpacking for
-// every 512 rows.  8 slices of 8192 | 32768 tokens and 2 of 65536, in us, pairs against the other forms (chunk.cu, prefill.cu):
-// 64 rows 26 : 24 | 60 : 50 | 37 : 37, 128 rows 27 : 27 | 61 : 52 | 38 : 39, 256 rows 28 : 35 | 61 : 65 | 39 : 48,
-// 2048 rows 77 : 88 | 238 : 265 | 112 : 129, 3000 rows 115 : 130 | 323 : 326 | 160 : 165, 4096 rows 135 : 112 | 441 : 397 | 219 : 226.
+// Below, an SM's tensor memory holds the rows of a tile by itself; far above, one expansion costs less than unpacking for
+// every 512 rows.  In us, pairs against the other forms (chunk.cu, prefill.cu), at 4 bits (2 bits alike):
+//   rows                            64        128        160        256       2048       2560       3000       4096
+//   8 slices of  1000 tokens   22 :  21   23 :  24   23 :  27   23 :  31   37 :  33   43 :  33   45 :  33   50 :  33
+//   8 slices of  8192 tokens   25 :  24   27 :  27   27 :  31   28 :  35   76 :  87  107 : 128  114 : 130  133 : 112
+//   8 slices of 32768 tokens   52 :  49   53 :  52   53 :  62   53 :  65  228 : 264  301 : 332  312 : 325  435 : 395
+//   2 slices of 65536 tokens   36 :  36   36 :  39   37 :  44   37 :  48  110 : 129  136 : 151  158 : 167  214 : 226
+// So the upper end is too low for long prefixes and too high for one of 1000 tokens, where pairs pay up to 1024 rows (30 : 33);
+// the rule does not look at the prefix's length.
 bool prefix_uses_pairs(int64_t dim, int64_t rows) { return dim == C && rows > 128 && rows <= 2048; }
 
 size_t prefix_workspace(int64_t outer, int64_t tmax, int64_t rows)

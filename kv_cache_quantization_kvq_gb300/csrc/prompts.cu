@@ -35,7 +35,9 @@
 // error of 2^-8 of each weight at most, the size of out's own rounding.
 //
 // Measured on one GB300 (C = 128, 8 KV heads x 4): one prompt of 32768 tokens 5.6 ms (1.57 PFLOP/s, tensor cores
-// bound), 64 prompts of 16 to 2000 tokens 270 us, one of 17 tokens 7.2 us (a launch's way through one tile).
+// bound), 64 prompts of 16 to 2000 tokens 263 us, one of 17 tokens 7.1 us (a launch's way through one tile).  At C = 64 no
+// unit is half busy (5 prompts of 1501 to 4001 tokens x 12 heads 105 us: tensor pipe 34 %, issue slots 39 %, exponentials 34
+// %): a row tile's chain scores -> weights -> values bounds it.
 // Key tiles of 64 tokens: 6.6 ms | 262 us; the scores' halves handed over one by one: 6.06 ms.
 #include <algorithm>
 

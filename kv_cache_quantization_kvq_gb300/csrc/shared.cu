@@ -12,7 +12,7 @@
 // (y, m, l) in float32, and the launch that joins the prefix's splits joins that too.
 // The prefix's launch starts while the last CTAs of that one run: it reads nothing of theirs.
 //
-// Measured on one GB300: 64 requests of 50 to 1500 tokens, 8 KV heads x 8, behind a prefix of 8192 tokens 64 us, of which
+// Measured on one GB300: 64 requests of 50 to 1500 tokens, 8 KV heads x 8, behind a prefix of 8192 tokens 63 us, of which
 // 28 are their own tokens'; reading the prefix once for each request, as kvq_attend_chunk would, has 64 times its bytes.
 #include "kvq_chunk.cuh"
 
