@@ -11,8 +11,9 @@ def source(name):
 
 
 def test_waits_are_bounded_in_time():
-    """Barriers are polled in two places.  kvq_bulk.cuh's waits are for copies, which land by themselves; those between
-    warps and CTAs are kvq_tc.cuh's, whose polls last 1 us at most and which run out after some seconds."""
+    """Barriers are polled in two places.  kvq_bulk.cuh's waits, of the quantizers' rings, are for the CTA's own copies and for
+    the warps that use them; those of the tensor-core kernels, whose CTAs wait for one another too, are kvq_tc.cuh's: a
+    poll lasts 1 us at most, and they run out after some seconds."""
     polled = {f for f in os.listdir(builder.CSRC) if re.search(r"mbarrier\.(try|test)_wait", source(f))}
     assert polled == {"kvq_bulk.cuh", "kvq_tc.cuh"}
     tc = source("kvq_tc.cuh")
